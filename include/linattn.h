@@ -83,6 +83,12 @@ typedef enum {
     LA_PHI_IDENTITY = 1       /* phi(x) = x (bilinear attention)               */
 } la_phi;
 
+/* How the heads lie in q, k, v and y of the delta-rule calls. */
+typedef enum {
+    LA_LAYOUT_BHND = 0,       /* [B][heads][N][width], as everywhere else here */
+    LA_LAYOUT_BNHD = 1        /* [B][N][heads][width]: heads inside tokens     */
+} la_layout;
+
 /* Human-readable name of a status code (static string, never NULL). */
 LA_API const char *la_status_string(la_status s);
 
@@ -411,6 +417,125 @@ LA_API la_status la_forward_noncausal_noalloc(const void *q, const void *k, cons
  * no-allocation entry point hold no pointer to its scratch.  Allocates nothing.
  */
 LA_API la_status la_noalloc_status(void *stream);
+
+/*
+ * Workspace size in bytes for la_forward_delta with these sizes: 0 where the
+ * call needs none, and for unsupported arguments.
+ */
+LA_API size_t la_delta_workspace_bytes(int B, int H, int Hk, int N, int d, int dv, la_dtype dt);
+
+/*
+ * The gated delta rule, causal forward ("Linear Attention/es" and "Linear
+ * attention" name DeltaNet and its gated form among the variants; the pages
+ * print no equation, and this is the published one):
+ *     S_t = a_t (I - b_t k_t k_t^T) S_{t-1} + b_t k_t v_t^T,   y_t = S_t^T q_t,
+ * that is, with the decayed state a_t S_{t-1}, the value stored under k_t is
+ * moved towards v_t by the fraction b_t.  a_t = exp(log_gate_t).  There is no
+ * feature map, no scale and no denominator: q and k are used as given (keys
+ * of unit length with b in [0, 1] keep the state bounded; the values of b and
+ * of the gates are not checked), and y is usually layer-normed
+ * (la_layer_norm).
+ *   q, k     dtype dt, Hk heads of width d.  H must be a multiple of Hk: head h
+ *            of v reads key head h / (H / Hk).
+ *   v, y     dtype dt, H heads of width dv.  y is rounded once, to dt, from
+ *            float32: unlike a normalised output it has no reader before its
+ *            norm, which takes float32 statistics of what it is given.
+ *   beta     float32 [B][H][N] (LA_LAYOUT_BHND) or [B][N][H] (LA_LAYOUT_BNHD).
+ *   log_gate as beta, natural logarithms of the gates, <= 0 (-inf closes a
+ *            gate: the state restarts); NULL means no gate (a_t = 1).
+ *   S_in     float32 [B][H][d][dv] or NULL (zero); S_out the final state or
+ *            NULL; S_out may equal S_in.
+ * A padding token with beta = 0 and log_gate = 0 leaves the state as it was.
+ * d, dv in {32, 64, 128}; B, H, Hk >= 1; N >= 0 (N = 0 writes S_out only);
+ * B*H*N*max(d, dv) < 2^31 and B*H*d*dv < 2^31.  q, k, v, y, S_in and S_out
+ * 16-byte aligned, beta and log_gate 4-byte aligned.  y must overlap no other
+ * buffer, S_out no other than an identical S_in.
+ * States and all sums are kept in 32 bits or more for both dtypes.
+ */
+LA_API la_status la_forward_delta(const void *q, const void *k, const void *v, void *y,
+                                  const float *beta, const float *log_gate, int B, int H, int Hk,
+                                  int N, int d, int dv, la_dtype dt, la_layout layout,
+                                  const float *S_in, float *S_out, void *workspace,
+                                  size_t workspace_bytes, void *stream);
+
+/*
+ * Workspace size in bytes for la_backward_delta (0 for N == 0 and for
+ * unsupported arguments): a status header, the states and their gradients at
+ * every 64th token, and two float32 rows of dv per token.
+ */
+LA_API size_t la_delta_backward_workspace_bytes(int B, int H, int Hk, int N, int d, int dv,
+                                                la_dtype dt);
+
+/*
+ * Gradients of la_forward_delta for dy = dL/dy (dtype dt, layout and shape of
+ * y) and, optionally, grad_S_out = dL/dS_N (float32; NULL: zero).  With
+ *     e_t = v_t - a_t S_{t-1}^T k_t,
+ *     G_t = q_t dy_t^T + a_{t+1} (I - b_{t+1} k_{t+1} k_{t+1}^T) G_{t+1}   (G_N + grad_S_out),
+ *     du_t = G_t^T k_t:
+ *   grad_q_t = S_t dy_t,   grad_v_t = b_t du_t,   grad_beta_t = du_t . e_t,
+ *   grad_k_t = G_t (b_t e_t) - a_t S_{t-1} (b_t du_t),
+ *   grad_log_gate_t = <G_t - k_t (b_t du_t)^T, a_t S_{t-1}>,
+ *   grad_S_in = a_1 (I - b_1 k_1 k_1^T) G_1.
+ * grad_q, grad_k, grad_v have the dtype and layout of q, k, v (the gradients
+ * of a shared key head are summed over its value heads in float32, then
+ * rounded); grad_beta and grad_log_gate are float32 in beta's layout.
+ * grad_log_gate and log_gate are both given or both NULL; grad_S_in may be
+ * NULL.  No output may overlap another buffer.  Same inputs as the forward;
+ * the states are recomputed.
+ */
+LA_API la_status la_backward_delta(const void *q, const void *k, const void *v, const void *dy,
+                                   const float *beta, const float *log_gate, void *grad_q,
+                                   void *grad_k, void *grad_v, float *grad_beta,
+                                   float *grad_log_gate, int B, int H, int Hk, int N, int d, int dv,
+                                   la_dtype dt, la_layout layout, const float *S_in,
+                                   const float *grad_S_out, float *grad_S_in, void *workspace,
+                                   size_t workspace_bytes, void *stream);
+
+/*
+ * One token of the gated delta rule per (b, h): S_out from S_in (both
+ * float32 [B][H][d][dv]; S_out may equal S_in: in place) and y = S_out^T q.
+ * q, k: [B][Hk][d], v, y: [B][H][dv] of dtype dt; beta, log_gate: float32
+ * [B][H] (log_gate NULL: no gate).  Sizes and alignment as in
+ * la_forward_delta.
+ */
+LA_API la_status la_decode_step_delta(const void *q, const void *k, const void *v, void *y,
+                                      const float *beta, const float *log_gate, const float *S_in,
+                                      float *S_out, int B, int H, int Hk, int d, int dv,
+                                      la_dtype dt, void *stream);
+
+/*
+ * Layer norm over rows of D values ("Linear attention" relies on it where the
+ * denominator of the attention is left out): x and y [rows][D] of dtype dt,
+ *     y = (x - mean) * rstd * weight + bias,   rstd = 1 / sqrt(var + eps),
+ * mean and var (divided by D) of the row in float32.  weight and bias:
+ * float32 [D], each may be NULL (ones, zeros).  mean and rstd: float32 [rows]
+ * outputs, both or neither (NULL).  y may equal x.  rows >= 0,
+ * 1 <= D <= 16384, eps finite and > 0; x and y aligned to their element size,
+ * float32 pointers to 4 bytes.
+ */
+LA_API la_status la_layer_norm(const void *x, void *y, const float *weight, const float *bias,
+                               float *mean, float *rstd, long long rows, int D, la_dtype dt,
+                               float eps, void *stream);
+
+/* Workspace size in bytes for la_layer_norm_backward (0 for unsupported
+ * arguments): per-CTA sums of grad_weight and grad_bias. */
+LA_API size_t la_layer_norm_backward_workspace_bytes(long long rows, int D, la_dtype dt);
+
+/*
+ * Gradients of la_layer_norm for dy of dtype dt, with the forward's mean and
+ * rstd: with xh = (x - mean) rstd and g = dy * weight,
+ *     grad_x = rstd (g - mean(g) - xh mean(g xh)),
+ *     grad_weight = sum over rows of dy xh,   grad_bias = sum over rows of dy.
+ * grad_weight and grad_bias: float32 [D], each may be NULL; rows are summed in
+ * a fixed order (the result does not vary between runs on one device).
+ * weight NULL: ones.  grad_x may equal dy or x.  The workspace may be NULL
+ * when neither sum is asked for.
+ */
+LA_API la_status la_layer_norm_backward(const void *dy, const void *x, const float *mean,
+                                        const float *rstd, const float *weight, void *grad_x,
+                                        float *grad_weight, float *grad_bias, long long rows, int D,
+                                        la_dtype dt, void *workspace, size_t workspace_bytes,
+                                        void *stream);
 
 /*
  * Synchronise `stream` and report the run-time status recorded in a

@@ -479,6 +479,241 @@ la_status la_backward_causal_decay(const void *q, const void *k, const void *v,
 }
 
 
+// ---- gated delta rule, layer norm ------------------------------------------
+}  // extern "C"
+
+namespace la {
+namespace {
+
+struct Buf {
+    const void *p;
+    size_t n;
+};
+bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// Does any output overlap an input or another output?
+template <int NI, int NO> bool clash(const Buf (&in)[NI], const Buf (&out)[NO]) {
+    for (int i = 0; i < NO; ++i) {
+        for (int j = 0; j < NI; ++j)
+            if (overlap(out[i].p, out[i].n, in[j].p, in[j].n)) return true;
+        for (int j = i + 1; j < NO; ++j)
+            if (overlap(out[i].p, out[i].n, out[j].p, out[j].n)) return true;
+    }
+    return false;
+}
+
+la_status check_delta(int B, int H, int Hk, long long N, int d, int dv, la_dtype dt) {
+    if (dt != LA_DTYPE_F32 && dt != LA_DTYPE_BF16) return LA_ERR_UNSUPPORTED;
+    if (B < 1 || H < 1 || Hk < 1 || N < 0 || H % Hk != 0) return LA_ERR_INVALID_ARG;
+    if (!dim_ok(d) || !dim_ok(dv)) return LA_ERR_UNSUPPORTED;
+    const long long BH = (long long)B * H, most = 1LL << 31;   // B*H below 2^62
+    if (BH >= most || BH * d * dv >= most) return LA_ERR_INVALID_ARG;
+    if (N > 0 && BH * (d > dv ? d : dv) >= (most + N - 1) / N) return LA_ERR_INVALID_ARG;
+    return LA_OK;
+}
+
+DeltaArgs delta_args(const void *q, const void *k, const void *v, const float *beta,
+                     const float *log_gate, int B, int H, int Hk, int N, int d, int dv, la_dtype dt,
+                     la_layout layout, const float *S_in, void *ws, void *stream) {
+    DeltaArgs a{};
+    a.q = q; a.k = k; a.v = v; a.beta = beta; a.log_gate = log_gate;
+    a.B = B; a.H = H; a.Hk = Hk; a.N = N; a.d = d; a.dv = dv; a.dt = dt; a.layout = layout;
+    a.S_in = S_in; a.ws = ws; a.stream = static_cast<cudaStream_t>(stream);
+    return a;
+}
+
+size_t delta_bwd_ws_bytes(int B, int H, int Hk, int N, int d, int dv, la_dtype dt) {
+    if (check_delta(B, H, Hk, N, d, dv, dt) != LA_OK || N == 0) return 0;
+    return delta_backward_workspace(delta_args(nullptr, nullptr, nullptr, nullptr, nullptr, B, H, Hk, N,
+                                               d, dv, dt, LA_LAYOUT_BHND, nullptr, nullptr, nullptr));
+}
+
+// dst = src, or zero without one.
+cudaError_t copy_state(float *dst, const float *src, size_t bytes, cudaStream_t s) {
+    if (!dst || dst == src) return cudaSuccess;
+    if (!src) return cudaMemsetAsync(dst, 0, bytes, s);
+    return cudaMemcpyAsync(dst, src, bytes, cudaMemcpyDeviceToDevice, s);
+}
+
+la_status check_norm(const void *x, const void *y, long long rows, int D, la_dtype dt) {
+    if (dt != LA_DTYPE_F32 && dt != LA_DTYPE_BF16) return LA_ERR_UNSUPPORTED;
+    if (rows < 0 || D < 1 || rows > (1LL << 62) / ((long long)D * 4)) return LA_ERR_INVALID_ARG;
+    if (D > 16384) return LA_ERR_UNSUPPORTED;
+    if (rows > 0 && (!x || !y)) return LA_ERR_INVALID_ARG;
+    const uintptr_t m = esize(dt) - 1;
+    if ((reinterpret_cast<uintptr_t>(x) & m) || (reinterpret_cast<uintptr_t>(y) & m))
+        return LA_ERR_INVALID_ARG;
+    return LA_OK;
+}
+
+}  // namespace
+}  // namespace la
+
+extern "C" {
+
+size_t la_delta_workspace_bytes(int B, int H, int Hk, int N, int d, int dv, la_dtype dt) {
+    (void)B; (void)H; (void)Hk; (void)N; (void)d; (void)dv; (void)dt;
+    return 0;
+}
+
+la_status la_forward_delta(const void *q, const void *k, const void *v, void *y, const float *beta,
+                           const float *log_gate, int B, int H, int Hk, int N, int d, int dv,
+                           la_dtype dt, la_layout layout, const float *S_in, float *S_out,
+                           void *workspace, size_t workspace_bytes, void *stream) {
+    la_status st = check_delta(B, H, Hk, N, d, dv, dt);
+    if (st != LA_OK) return st;
+    if (layout != LA_LAYOUT_BHND && layout != LA_LAYOUT_BNHD) return LA_ERR_UNSUPPORTED;
+    const size_t es = esize(dt), TH = (size_t)B * H * N, TK = (size_t)B * Hk * N;
+    const size_t sb = (size_t)B * H * d * dv * 4;
+    if (!aligned16(S_in) || !aligned16(S_out)) return LA_ERR_INVALID_ARG;
+    if (S_in != S_out && overlap(S_in, sb, S_out, sb)) return LA_ERR_INVALID_ARG;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (N == 0) return from_cuda(copy_state(S_out, S_in, sb, s));   // no tokens: q .. beta may be NULL
+    if (!q || !k || !v || !y || !beta) return LA_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(y) || !aligned4(beta) ||
+        !aligned4(log_gate))
+        return LA_ERR_INVALID_ARG;
+    const size_t need = la_delta_workspace_bytes(B, H, Hk, N, d, dv, dt);
+    if ((st = check_ws(workspace, workspace_bytes, need)) != LA_OK) return st;
+    const Buf in[] = {{q, TK * d * es}, {k, TK * d * es}, {v, TH * dv * es}, {beta, TH * 4},
+                      {log_gate, TH * 4}, {S_in != S_out ? S_in : nullptr, sb}};
+    const Buf out[] = {{y, TH * dv * es}, {S_out, sb}, {need ? workspace : nullptr, need}};
+    if (clash(in, out)) return LA_ERR_INVALID_ARG;
+    DeltaArgs a = delta_args(q, k, v, beta, log_gate, B, H, Hk, N, d, dv, dt, layout, S_in, workspace,
+                             stream);
+    a.y = y;
+    a.S_out = S_out;
+    return from_cuda(launch_delta_forward_simt(a));
+}
+
+size_t la_delta_backward_workspace_bytes(int B, int H, int Hk, int N, int d, int dv, la_dtype dt) {
+    return delta_bwd_ws_bytes(B, H, Hk, N, d, dv, dt);
+}
+
+la_status la_backward_delta(const void *q, const void *k, const void *v, const void *dy,
+                            const float *beta, const float *log_gate, void *grad_q, void *grad_k,
+                            void *grad_v, float *grad_beta, float *grad_log_gate, int B, int H, int Hk,
+                            int N, int d, int dv, la_dtype dt, la_layout layout, const float *S_in,
+                            const float *grad_S_out, float *grad_S_in, void *workspace,
+                            size_t workspace_bytes, void *stream) {
+    la_status st = check_delta(B, H, Hk, N, d, dv, dt);
+    if (st != LA_OK) return st;
+    if (layout != LA_LAYOUT_BHND && layout != LA_LAYOUT_BNHD) return LA_ERR_UNSUPPORTED;
+    const size_t es = esize(dt), TH = (size_t)B * H * N, TK = (size_t)B * Hk * N;
+    const size_t sb = (size_t)B * H * d * dv * 4;
+    if (!aligned16(S_in) || !aligned16(grad_S_out) || !aligned16(grad_S_in)) return LA_ERR_INVALID_ARG;
+    if (overlap(grad_S_in, sb, S_in, sb) || overlap(grad_S_in, sb, grad_S_out, sb))
+        return LA_ERR_INVALID_ARG;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (N == 0) return from_cuda(copy_state(grad_S_in, grad_S_out, sb, s));
+    const void *need16[] = {q, k, v, dy, grad_q, grad_k, grad_v};
+    for (const void *p : need16)
+        if (!p || !aligned16(p)) return LA_ERR_INVALID_ARG;
+    if (!beta || !grad_beta || (log_gate == nullptr) != (grad_log_gate == nullptr)) return LA_ERR_INVALID_ARG;
+    if (!aligned4(beta) || !aligned4(log_gate) || !aligned4(grad_beta) || !aligned4(grad_log_gate))
+        return LA_ERR_INVALID_ARG;
+    const size_t need = delta_bwd_ws_bytes(B, H, Hk, N, d, dv, dt);
+    if ((st = check_ws(workspace, workspace_bytes, need)) != LA_OK) return st;
+    const Buf in[] = {{q, TK * d * es}, {k, TK * d * es}, {v, TH * dv * es}, {dy, TH * dv * es},
+                      {beta, TH * 4}, {log_gate, TH * 4}, {S_in, sb}, {grad_S_out, sb}};
+    const Buf out[] = {{grad_q, TK * d * es}, {grad_k, TK * d * es}, {grad_v, TH * dv * es},
+                       {grad_beta, TH * 4}, {grad_log_gate, TH * 4}, {grad_S_in, sb},
+                       {workspace, need}};
+    if (clash(in, out)) return LA_ERR_INVALID_ARG;
+    if (cudaMemsetAsync(workspace, 0, sizeof(WsHeader), s) != cudaSuccess) return LA_ERR_CUDA;
+    DeltaArgs a = delta_args(q, k, v, beta, log_gate, B, H, Hk, N, d, dv, dt, layout, S_in, workspace,
+                             stream);
+    a.dy = dy;
+    a.dq = grad_q; a.dk = grad_k; a.dv_grad = grad_v;
+    a.dbeta = grad_beta; a.dlog_gate = grad_log_gate;
+    a.dS_out = grad_S_out; a.dS_in = grad_S_in;
+    return from_cuda(launch_delta_backward(a));
+}
+
+la_status la_decode_step_delta(const void *q, const void *k, const void *v, void *y, const float *beta,
+                               const float *log_gate, const float *S_in, float *S_out, int B, int H,
+                               int Hk, int d, int dv, la_dtype dt, void *stream) {
+    la_status st = check_delta(B, H, Hk, 1, d, dv, dt);
+    if (st != LA_OK) return st;
+    const void *need16[] = {q, k, v, y, S_in, S_out};
+    for (const void *p : need16)
+        if (!p || !aligned16(p)) return LA_ERR_INVALID_ARG;
+    if (!beta || !aligned4(beta) || !aligned4(log_gate)) return LA_ERR_INVALID_ARG;
+    const size_t es = esize(dt), TH = (size_t)B * H, TK = (size_t)B * Hk, sb = TH * d * dv * 4;
+    const Buf in[] = {{q, TK * d * es}, {k, TK * d * es}, {v, TH * dv * es}, {beta, TH * 4},
+                      {log_gate, TH * 4}, {S_in != S_out ? S_in : nullptr, sb}};
+    const Buf out[] = {{y, TH * dv * es}, {S_out, sb}};
+    if (clash(in, out)) return LA_ERR_INVALID_ARG;
+    DeltaArgs a = delta_args(q, k, v, beta, log_gate, B, H, Hk, 1, d, dv, dt, LA_LAYOUT_BHND, S_in,
+                             nullptr, stream);
+    a.y = y;
+    a.S_out = S_out;
+    return from_cuda(launch_delta_step(a));
+}
+
+la_status la_layer_norm(const void *x, void *y, const float *weight, const float *bias, float *mean,
+                        float *rstd, long long rows, int D, la_dtype dt, float eps, void *stream) {
+    la_status st = check_norm(x, y, rows, D, dt);
+    if (st != LA_OK) return st;
+    if (!(eps > 0.f) || !std::isfinite(eps)) return LA_ERR_INVALID_ARG;
+    if ((mean == nullptr) != (rstd == nullptr)) return LA_ERR_INVALID_ARG;
+    if (!aligned4(weight) || !aligned4(bias) || !aligned4(mean) || !aligned4(rstd))
+        return LA_ERR_INVALID_ARG;
+    if (rows == 0) return LA_OK;
+    const size_t n = (size_t)rows * D * esize(dt);
+    const Buf in[] = {{x != y ? x : nullptr, n}, {weight, (size_t)D * 4}, {bias, (size_t)D * 4}};
+    const Buf out[] = {{y, n}, {mean, (size_t)rows * 4}, {rstd, (size_t)rows * 4}};
+    const Buf same[] = {{x, n}};
+    const Buf stats[] = {{mean, (size_t)rows * 4}, {rstd, (size_t)rows * 4}};
+    if (clash(in, out) || clash(same, stats)) return LA_ERR_INVALID_ARG;
+    LayerNormArgs a{};
+    a.x = x; a.y = y; a.weight = weight; a.bias = bias; a.mean = mean; a.rstd = rstd;
+    a.rows = rows; a.D = D; a.dt = dt; a.eps = eps; a.stream = static_cast<cudaStream_t>(stream);
+    return from_cuda(launch_layer_norm(a));
+}
+
+size_t la_layer_norm_backward_workspace_bytes(long long rows, int D, la_dtype dt) {
+    if (rows < 1 || check_norm(&dt, &dt, rows, D, dt) != LA_OK) return 0;
+    return sizeof(WsHeader) + layer_norm_partials(rows, D, dt) * 4;
+}
+
+la_status la_layer_norm_backward(const void *dy, const void *x, const float *mean, const float *rstd,
+                                 const float *weight, void *grad_x, float *grad_weight,
+                                 float *grad_bias, long long rows, int D, la_dtype dt, void *workspace,
+                                 size_t workspace_bytes, void *stream) {
+    la_status st = check_norm(x, grad_x, rows, D, dt);
+    if (st == LA_OK) st = check_norm(dy, dy, rows, D, dt);
+    if (st != LA_OK) return st;
+    if (!aligned4(weight) || !aligned4(mean) || !aligned4(rstd) || !aligned4(grad_weight) ||
+        !aligned4(grad_bias))
+        return LA_ERR_INVALID_ARG;
+    const size_t n = (size_t)rows * D * esize(dt), nr = (size_t)rows * 4, nd = (size_t)D * 4;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (rows == 0) {   // empty sums
+        cudaError_t e = grad_weight ? cudaMemsetAsync(grad_weight, 0, nd, s) : cudaSuccess;
+        if (e == cudaSuccess && grad_bias) e = cudaMemsetAsync(grad_bias, 0, nd, s);
+        return from_cuda(e);
+    }
+    if (!mean || !rstd) return LA_ERR_INVALID_ARG;
+    const bool sums = grad_weight || grad_bias;
+    const size_t need = sums ? la_layer_norm_backward_workspace_bytes(rows, D, dt) : 0;
+    if ((st = check_ws(workspace, workspace_bytes, need)) != LA_OK) return st;
+    const Buf in[] = {{x != grad_x ? x : nullptr, n}, {dy != grad_x ? dy : nullptr, n},
+                      {mean, nr}, {rstd, nr}, {weight, nd}};
+    const Buf out[] = {{grad_x, n}, {grad_weight, nd}, {grad_bias, nd}, {sums ? workspace : nullptr, need}};
+    const Buf whole[] = {{x, n}, {dy, n}};
+    const Buf rest[] = {{grad_weight, nd}, {grad_bias, nd}, {sums ? workspace : nullptr, need}};
+    if (clash(in, out) || clash(whole, rest)) return LA_ERR_INVALID_ARG;
+    if (sums && cudaMemsetAsync(workspace, 0, sizeof(WsHeader), s) != cudaSuccess) return LA_ERR_CUDA;
+    LayerNormArgs a{};
+    a.x = x; a.dy = dy; a.dx = grad_x; a.weight = weight;
+    a.mean = const_cast<float *>(mean); a.rstd = const_cast<float *>(rstd);
+    a.dweight = grad_weight; a.dbias = grad_bias;
+    a.partials = sums ? reinterpret_cast<float *>(static_cast<char *>(workspace) + sizeof(WsHeader)) : nullptr;
+    a.rows = rows; a.D = D; a.dt = dt; a.stream = s;
+    return from_cuda(launch_layer_norm_backward(a));
+}
+
 la_status la_workspace_status(const void *workspace, size_t workspace_bytes, void *stream) {
     if (!workspace || workspace_bytes < sizeof(WsHeader)) return LA_ERR_WORKSPACE;
     cudaStream_t s = static_cast<cudaStream_t>(stream);

@@ -1,0 +1,74 @@
+// delta_common.cuh -- what the kernels of the gated delta rule share.
+//
+// The recurrence, per head, with the state S [d, dv] in float32:
+//   e_t = v_t - a_t S_{t-1}^T k_t,   S_t = a_t S_{t-1} + k_t (b_t e_t)^T,   y_t = S_t^T q_t
+// (a_t = exp(log_gate_t); the same update as a_t (I - b_t k_t k_t^T) S_{t-1} + b_t k_t v_t^T).
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "la_device.cuh"
+#include "la_internal.h"
+
+namespace la {
+
+constexpr int kDeltaC = 64;   // tokens of a block: the distance of the states the backward keeps
+
+// Token rows of one head: row t starts at base + t * step (elements).
+struct TokenRows {
+    size_t base, step;
+    __device__ __forceinline__ size_t at(int t) const { return base + (size_t)t * step; }
+};
+__host__ __device__ __forceinline__ TokenRows token_rows(int layout, int b, int h, int heads, int N,
+                                                         int w) {
+    if (layout == LA_LAYOUT_BNHD)
+        return {((size_t)b * N * heads + h) * w, (size_t)heads * w};
+    return {((size_t)b * heads + h) * N * w, (size_t)w};
+}
+
+template <typename T> __device__ __forceinline__ T from_f(float x);
+template <> __device__ __forceinline__ float from_f<float>(float x) { return x; }
+template <> __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float x) {
+    return __float2bfloat16_rn(x);
+}
+
+// N consecutive values (N * sizeof(T) a multiple of 16, p 16-byte aligned) as floats.
+template <int N> __device__ __forceinline__ void load_vec(const float *p, float (&x)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; i += 4) {
+        const float4 f = __ldg(reinterpret_cast<const float4 *>(p + i));
+        x[i] = f.x; x[i + 1] = f.y; x[i + 2] = f.z; x[i + 3] = f.w;
+    }
+}
+template <int N> __device__ __forceinline__ void load_vec(const __nv_bfloat16 *p, float (&x)[N]) {
+    static_assert(N % 8 == 0, "16-byte vectors");
+#pragma unroll
+    for (int i = 0; i < N; i += 8) {
+        const uint4 w = __ldg(reinterpret_cast<const uint4 *>(p + i));
+        const unsigned u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            x[i + 2 * j] = __uint_as_float(u[j] << 16);
+            x[i + 2 * j + 1] = __uint_as_float(u[j] & 0xFFFF0000u);
+        }
+    }
+}
+
+// Workspace of the gradients, in floats behind the status header: the states before each block and
+// the final one, their gradients after each block, e and du of every token (head-major).
+struct DeltaBwdWs {
+    float *S, *G, *e, *du;
+};
+__host__ __device__ __forceinline__ int delta_blocks(int N) { return (N + kDeltaC - 1) / kDeltaC; }
+inline DeltaBwdWs delta_bwd_ws(const DeltaArgs &a) {
+    const size_t BH = (size_t)a.B * a.H, nc = delta_blocks(a.N), st = (size_t)a.d * a.dv;
+    DeltaBwdWs w;
+    w.S = reinterpret_cast<float *>(static_cast<char *>(a.ws) + sizeof(WsHeader));
+    w.G = w.S + BH * (nc + 1) * st;
+    w.e = w.G + BH * nc * st;
+    w.du = w.e + BH * a.N * a.dv;
+    return w;
+}
+
+}  // namespace la

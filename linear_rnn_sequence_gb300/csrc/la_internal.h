@@ -73,6 +73,43 @@ struct BwdArgs {
     const float *gamma = nullptr;  // per-head decay [H] (device), null: none
 };
 
+// The gated delta rule; pointers are device pointers.  A head h of v, y, beta
+// and log_gate reads key head h / (H / Hk) of q and k.
+struct DeltaArgs {
+    const void *q, *k, *v;
+    void *y;                        // forward
+    const float *beta, *log_gate;   // log_gate nullable (no decay)
+    int B, H, Hk, N, d, dv;
+    la_dtype dt;
+    la_layout layout;
+    const float *S_in;              // nullable (zero initial state)
+    float *S_out;                   // nullable
+    void *ws;
+    cudaStream_t stream;
+    // gradients
+    const void *dy = nullptr;
+    void *dq = nullptr, *dk = nullptr, *dv_grad = nullptr;
+    float *dbeta = nullptr, *dlog_gate = nullptr;   // dlog_gate null without gates
+    const float *dS_out = nullptr;                  // nullable (zero)
+    float *dS_in = nullptr;                         // nullable
+};
+
+struct LayerNormArgs {
+    const void *x;
+    void *y;
+    const float *weight, *bias;   // nullable
+    float *mean, *rstd;           // forward: nullable; backward: inputs
+    long long rows;
+    int D;
+    la_dtype dt;
+    float eps;
+    cudaStream_t stream;
+    const void *dy = nullptr;     // backward
+    void *dx = nullptr;
+    float *dweight = nullptr, *dbias = nullptr;   // nullable
+    float *partials = nullptr;
+};
+
 // Workspace header written at the start of every workspace (256 bytes).
 struct WsHeader {
     unsigned int error;         // 0 = ok, else an la_status value (LA_ERR_TIMEOUT)
@@ -127,5 +164,16 @@ cudaError_t launch_random_features(const void *x, float *out, long long rows, in
 // gradients of the causal form (CUDA cores, fp32)
 size_t causal_backward_workspace(int BH, int N, int d, int dv);
 cudaError_t launch_causal_backward(const BwdArgs &a);
+
+// gated delta rule (CUDA cores, fp32) and layer norm
+cudaError_t launch_delta_forward_simt(const DeltaArgs &a);
+cudaError_t launch_delta_states_simt(const DeltaArgs &a);    // the backward's first pass
+cudaError_t launch_delta_reverse_simt(const DeltaArgs &a);   // and its second
+size_t delta_backward_workspace(const DeltaArgs &a);
+cudaError_t launch_delta_backward(const DeltaArgs &a);
+cudaError_t launch_delta_step(const DeltaArgs &a);
+cudaError_t launch_layer_norm(const LayerNormArgs &a);
+size_t layer_norm_partials(long long rows, int D, la_dtype dt);   // floats of `partials`
+cudaError_t launch_layer_norm_backward(const LayerNormArgs &a);
 
 }  // namespace la

@@ -12,10 +12,13 @@ Names follow the C ABI:
 * ``decode_step``       -> ``la_decode_step``
 * ``forward_causal_gated``, ``decode_step_gated``, ``forward_noncausal_phi``,
   ``random_features`` -> the gated and feature-map entry points
+* ``forward_delta``, ``backward_delta``, ``decode_step_delta`` -> the gated delta rule
+* ``layer_norm``, ``layer_norm_backward`` -> the norm that follows it
 """
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -26,6 +29,7 @@ from . import _build
 LA_OK, LA_ERR_INVALID_ARG, LA_ERR_UNSUPPORTED, LA_ERR_CUDA, LA_ERR_TIMEOUT, LA_ERR_WORKSPACE = range(6)
 LA_DTYPE_F32, LA_DTYPE_BF16 = 0, 1
 PHI = {"elu1": 0, "identity": 1}   # la_phi
+LAYOUT = {"bhnd": 0, "bnhd": 1}    # la_layout
 
 _lock = threading.Lock()
 _lib = None
@@ -112,6 +116,23 @@ def lib():
             L.la_forward_noncausal_phi.restype = i
             L.la_random_features.argtypes = [vp, vp, ctypes.c_longlong, i, i, i, vp, vp]
             L.la_random_features.restype = i
+            L.la_delta_workspace_bytes.argtypes = [i, i, i, i, i, i, i]
+            L.la_delta_workspace_bytes.restype = sz
+            L.la_forward_delta.argtypes = [vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, i, i, vp, vp,
+                                           vp, sz, vp]
+            L.la_forward_delta.restype = i
+            L.la_delta_backward_workspace_bytes.argtypes = [i, i, i, i, i, i, i]
+            L.la_delta_backward_workspace_bytes.restype = sz
+            L.la_backward_delta.argtypes = [vp] * 11 + [i] * 8 + [vp, vp, vp, vp, sz, vp]
+            L.la_backward_delta.restype = i
+            L.la_decode_step_delta.argtypes = [vp] * 8 + [i] * 6 + [vp]
+            L.la_decode_step_delta.restype = i
+            L.la_layer_norm.argtypes = [vp] * 6 + [ctypes.c_longlong, i, i, f, vp]
+            L.la_layer_norm.restype = i
+            L.la_layer_norm_backward_workspace_bytes.argtypes = [ctypes.c_longlong, i, i]
+            L.la_layer_norm_backward_workspace_bytes.restype = sz
+            L.la_layer_norm_backward.argtypes = [vp] * 8 + [ctypes.c_longlong, i, i, vp, sz, vp]
+            L.la_layer_norm_backward.restype = i
             _lib = L
     return _lib
 
@@ -527,3 +548,211 @@ def random_features(x, W, out=None, stream=None):
                                   _stream_handle(stream, x.device))
     _raise(st, "la_random_features")
     return y
+
+
+# ---- gated delta rule, layer norm -------------------------------------------
+def _on_device(fn):
+    """Run ``fn`` with its first argument's device and, if given, ``stream`` current, so that what
+    it allocates belongs to the device and stream that use it."""
+    first = fn.__code__.co_varnames[0]
+
+    @functools.wraps(fn)
+    def call(*args, stream=None, **kw):
+        t = args[0] if args else kw[first]
+        if not t.is_cuda:
+            raise ValueError("tensors must be CUDA tensors (no CPU fallback)")
+        if stream is None and t.device.index == torch.cuda.current_device():
+            return fn(*args, **kw)
+        if stream is not None and stream.device != t.device:
+            raise ValueError("the stream is of another device than the tensors")
+        with torch.cuda.device(t.device), torch.cuda.stream(stream):
+            return fn(*args, **kw)
+    return call
+
+
+def _current_stream(t) -> int:
+    return torch.cuda.current_stream(t.device).cuda_stream
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _expect(name, t, shape, dtype, like):
+    """``t`` is None or a contiguous tensor of this shape and dtype on ``like``'s device."""
+    if t is None:
+        return
+    if t.shape != shape or t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype} of shape {tuple(shape)}, not {t.dtype} of {tuple(t.shape)}")
+    if t.device != like.device:
+        raise ValueError(f"{name} is on {t.device}, not on {like.device}")
+    if not t.is_contiguous():
+        raise ValueError("tensors must be contiguous")
+
+
+def _workspace(workspace, need, like):
+    if workspace is None:
+        return torch.empty(need, dtype=torch.uint8, device=like.device) if need else None, need
+    if workspace.device != like.device or not workspace.is_contiguous():
+        raise ValueError("the workspace must be contiguous and on the tensors' device")
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+def _check_run_time(workspace, where):
+    if workspace is not None:
+        err, site = workspace_header(workspace)
+        if err != LA_OK:
+            raise LinAttnError(err, f"{where} (run time, wait site {site})")
+
+
+def _delta_sizes(q, k, v, beta, log_gate, layout):
+    """Checks the inputs of a delta-rule call; returns B, H, Hk, N, d, dv."""
+    if layout not in LAYOUT:
+        raise ValueError(f"layout must be one of {sorted(LAYOUT)}")
+    if q.dim() != 4 or v.dim() != 4:
+        raise ValueError("q, k and v must have four dimensions")
+    n, h = (2, 1) if layout == "bhnd" else (1, 2)
+    B, Hk, N, d = q.shape[0], q.shape[h], q.shape[n], q.shape[3]
+    H, dv = v.shape[h], v.shape[3]
+    _expect("q", q, q.shape, q.dtype, q)
+    _expect("k", k, q.shape, q.dtype, q)
+    _expect("v", v, (B, H, N, dv) if layout == "bhnd" else (B, N, H, dv), q.dtype, q)
+    _expect("beta", beta, v.shape[:3], torch.float32, q)
+    _expect("log_gate", log_gate, v.shape[:3], torch.float32, q)
+    return B, H, Hk, N, d, dv
+
+
+@_on_device
+def forward_delta(q, k, v, beta, log_gate=None, S_in=None, return_state=False, out=None,
+                  S_out=None, layout="bhnd", workspace=None, check_status=False):
+    """The gated delta rule, causal:
+    S_t = a_t (I - b_t k_t k_t^T) S_{t-1} + b_t k_t v_t^T, y_t = S_t^T q_t, a_t = exp(log_gate_t).
+
+    q, k: [B,Hk,N,d]; v: [B,H,N,dv], H a multiple of Hk (bf16 or fp32); beta, log_gate: float32
+    [B,H,N] (log_gate None: no gate); with ``layout="bnhd"`` heads and tokens swap places in all of
+    them.  Returns y in v's shape and dtype (and the final state [B,H,d,dv], float32, when
+    ``return_state``).  S_in: the initial state; S_out may be S_in.
+    """
+    B, H, Hk, N, d, dv = _delta_sizes(q, k, v, beta, log_gate, layout)
+    dt = _dtype_code(q)
+    _expect("S_in", S_in, (B, H, d, dv), torch.float32, q)
+    _expect("S_out", S_out, (B, H, d, dv), torch.float32, q)
+    _expect("out", out, v.shape, v.dtype, q)
+    y = out if out is not None else torch.empty_like(v)
+    if return_state and S_out is None:
+        S_out = torch.empty((B, H, d, dv), dtype=torch.float32, device=q.device)
+    L = lib()
+    workspace, wbytes = _workspace(workspace, L.la_delta_workspace_bytes(B, H, Hk, N, d, dv, dt), q)
+    st = L.la_forward_delta(_addr(q), _addr(k), _addr(v), _addr(y), _addr(beta), _addr(log_gate), B,
+                            H, Hk, N, d, dv, dt, LAYOUT[layout], _addr(S_in), _addr(S_out),
+                            _addr(workspace), wbytes, _current_stream(q))
+    _raise(st, "la_forward_delta")
+    if check_status:
+        _check_run_time(workspace, "la_forward_delta")
+    return (y, S_out) if return_state else y
+
+
+@_on_device
+def backward_delta(q, k, v, beta, dy, log_gate=None, S_in=None, grad_S_out=None, layout="bhnd",
+                   workspace=None, check_status=False):
+    """Gradients of ``forward_delta`` for dy = dL/dy (dtype and shape of v) and grad_S_out = dL/dS
+    of the final state (None: zero).  Returns (grad_q, grad_k, grad_v, grad_beta, grad_log_gate,
+    grad_S_in): the first three in the inputs' dtype, the others float32; grad_log_gate is None
+    without log_gate, grad_S_in is None unless S_in or grad_S_out is given.
+    """
+    B, H, Hk, N, d, dv = _delta_sizes(q, k, v, beta, log_gate, layout)
+    dt = _dtype_code(q)
+    _expect("dy", dy, v.shape, v.dtype, q)
+    _expect("S_in", S_in, (B, H, d, dv), torch.float32, q)
+    _expect("grad_S_out", grad_S_out, (B, H, d, dv), torch.float32, q)
+    gq, gk, gv, gb = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v), torch.empty_like(beta)
+    gl = None if log_gate is None else torch.empty_like(log_gate)
+    gS = None
+    if S_in is not None or grad_S_out is not None:
+        gS = torch.empty((B, H, d, dv), dtype=torch.float32, device=q.device)
+    L = lib()
+    workspace, wbytes = _workspace(workspace, L.la_delta_backward_workspace_bytes(B, H, Hk, N, d, dv, dt), q)
+    st = L.la_backward_delta(_addr(q), _addr(k), _addr(v), _addr(dy), _addr(beta), _addr(log_gate),
+                             _addr(gq), _addr(gk), _addr(gv), _addr(gb), _addr(gl), B, H, Hk, N, d,
+                             dv, dt, LAYOUT[layout], _addr(S_in), _addr(grad_S_out), _addr(gS),
+                             _addr(workspace), wbytes, _current_stream(q))
+    _raise(st, "la_backward_delta")
+    if check_status:
+        _check_run_time(workspace, "la_backward_delta")
+    return gq, gk, gv, gb, gl, gS
+
+
+@_on_device
+def decode_step_delta(q, k, v, beta, S, log_gate=None, S_out=None, out=None):
+    """One token of ``forward_delta``: q, k [B,Hk,d]; v [B,H,dv]; beta, log_gate [B,H] float32;
+    S [B,H,d,dv] float32, updated in place unless ``S_out`` is given.  Returns y [B,H,dv] in v's dtype.
+    """
+    if q.dim() != 3 or v.dim() != 3:
+        raise ValueError("q, k and v must have three dimensions")
+    B, Hk, d = q.shape
+    H, dv = v.shape[1], v.shape[2]
+    dt = _dtype_code(q)
+    _expect("q", q, q.shape, q.dtype, q)
+    _expect("k", k, q.shape, q.dtype, q)
+    _expect("v", v, (B, H, dv), q.dtype, q)
+    _expect("beta", beta, (B, H), torch.float32, q)
+    _expect("log_gate", log_gate, (B, H), torch.float32, q)
+    _expect("S", S, (B, H, d, dv), torch.float32, q)
+    _expect("S_out", S_out, (B, H, d, dv), torch.float32, q)
+    _expect("out", out, v.shape, v.dtype, q)
+    y = out if out is not None else torch.empty_like(v)
+    st = lib().la_decode_step_delta(_addr(q), _addr(k), _addr(v), _addr(y), _addr(beta),
+                                    _addr(log_gate), _addr(S), _addr(S if S_out is None else S_out),
+                                    B, H, Hk, d, dv, dt, _current_stream(q))
+    _raise(st, "la_decode_step_delta")
+    return y
+
+
+@_on_device
+def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, return_stats=False, out=None):
+    """(x - mean) * rstd * weight + bias over the last dimension (at most 16384 values, bf16 or
+    fp32); weight, bias: float32 [D] or None.  Returns y in x's dtype (and mean, rstd, float32 in
+    x's shape without its last dimension, when ``return_stats``).  ``out`` may be x."""
+    D = x.shape[-1]
+    dt = _dtype_code(x)
+    _expect("x", x, x.shape, x.dtype, x)
+    _expect("weight", weight, (D,), torch.float32, x)
+    _expect("bias", bias, (D,), torch.float32, x)
+    _expect("out", out, x.shape, x.dtype, x)
+    y = out if out is not None else torch.empty_like(x)
+    mean = rstd = None
+    if return_stats:
+        mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+        rstd = torch.empty_like(mean)
+    st = lib().la_layer_norm(_addr(x), _addr(y), _addr(weight), _addr(bias), _addr(mean), _addr(rstd),
+                             x.numel() // D if D else 0, D, dt, float(eps), _current_stream(x))
+    _raise(st, "la_layer_norm")
+    return (y, mean, rstd) if return_stats else y
+
+
+@_on_device
+def layer_norm_backward(dy, x, mean, rstd, weight=None, sums=None, workspace=None):
+    """Gradients of ``layer_norm`` from its mean and rstd: (grad_x, grad_weight, grad_bias), the
+    first in x's dtype, the sums float32 [D].  ``sums`` says whether to compute the latter two
+    (default: when weight is given); they are None otherwise."""
+    D = x.shape[-1]
+    dt = _dtype_code(x)
+    _expect("x", x, x.shape, x.dtype, x)
+    _expect("dy", dy, x.shape, x.dtype, x)
+    _expect("mean", mean, x.shape[:-1], torch.float32, x)
+    _expect("rstd", rstd, x.shape[:-1], torch.float32, x)
+    _expect("weight", weight, (D,), torch.float32, x)
+    gx = torch.empty_like(x)
+    rows = x.numel() // D if D else 0
+    gw = gb = None
+    wbytes = 0
+    L = lib()
+    if weight is not None if sums is None else sums:
+        gw = torch.empty(D, dtype=torch.float32, device=x.device)
+        gb = torch.empty_like(gw)
+        workspace, wbytes = _workspace(workspace, L.la_layer_norm_backward_workspace_bytes(rows, D, dt), x)
+    st = L.la_layer_norm_backward(_addr(dy), _addr(x), _addr(mean), _addr(rstd), _addr(weight),
+                                  _addr(gx), _addr(gw), _addr(gb), rows, D, dt, _addr(workspace),
+                                  wbytes, _current_stream(x))
+    _raise(st, "la_layer_norm_backward")
+    return gx, gw, gb

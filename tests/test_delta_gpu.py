@@ -1,0 +1,318 @@
+"""The gated delta rule and layer norm on the GPU against their float64 references, with the bounds
+derived in delta_ref.py."""
+import pytest
+import torch
+
+import delta_ref as R
+from linear_rnn_sequence_gb300 import linattn as la
+
+pytestmark = pytest.mark.gpu
+
+BF16, F32 = torch.bfloat16, torch.float32
+NAMES = ("grad_q", "grad_k", "grad_v", "grad_beta", "grad_log_gate", "grad_S_in")
+
+
+def on_gpu(x):
+    return {n: t if t is None else t.cuda() for n, t in x.items()}
+
+
+def gpu_forward(x, layout="bhnd", **kw):
+    x = on_gpu(x)
+    return la.forward_delta(x["q"], x["k"], x["v"], x["beta"], x["log_gate"], S_in=x["S_in"], layout=layout,
+                            check_status=True, **kw)
+
+
+def gpu_backward(x, dy, dS=None, layout="bhnd"):
+    x = on_gpu(x)
+    return la.backward_delta(x["q"], x["k"], x["v"], x["beta"], dy.cuda(), x["log_gate"], S_in=x["S_in"],
+                             grad_S_out=None if dS is None else dS.cuda(), layout=layout, check_status=True)
+
+
+def upstream(x, dtype, seed=9, scale=1.0):
+    g = torch.Generator().manual_seed(seed)
+    dy = torch.randn(x["v"].shape, generator=g).to(dtype)
+    dS = None if x["S_in"] is None else scale * torch.randn(x["S_in"].shape, generator=g)
+    return dy, dS
+
+
+def check_forward(x, layout="bhnd"):
+    y, S = gpu_forward(x, layout, return_state=True)
+    yr, Sr = R.forward(x, layout)
+    R.check(y, yr, "y")
+    R.check(S, Sr, "S")
+
+
+def check_backward(x, dtype, layout="bhnd"):
+    dy, dS = upstream(x, dtype)
+    got, want = gpu_backward(x, dy, dS, layout), R.backward(x, dy, dS, layout)
+    for n, a, b in zip(NAMES, got, want):
+        if n == "grad_S_in" and dS is None:
+            assert a is None
+        elif a is None:
+            assert n == "grad_log_gate" and x["log_gate"] is None
+        else:
+            R.check(a, b, n, slack=R.log_gate_slack(x, dy, dS, want, layout) if n == "grad_log_gate" else 0.0)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("d", [32, 64, 128])
+@pytest.mark.parametrize("dv", [32, 64, 128])
+def test_every_width(d, dv, dtype):
+    x = R.inputs(1, 4, 2, 150, d, dv, dtype, state=True, seed=d + dv)
+    check_forward(x)
+    check_backward(x, dtype)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("N", [1, 2, 15, 16, 17, 63, 64, 65, 127, 128, 129, 191, 333])
+def test_lengths(N, dtype):
+    x = R.inputs(2, 2, 1, N, 64, 128, dtype, state=N % 2 == 0, layout="bnhd", seed=N)
+    check_forward(x, "bnhd")
+    check_backward(x, dtype, "bnhd")
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("gate", [None, "any"])
+@pytest.mark.parametrize("group", [1, 4])
+def test_gates_and_shared_heads(gate, group, dtype):
+    x = R.inputs(2, 4, 4 // group, 200, 128, 64, dtype, gate=gate, state=True, seed=group)
+    check_forward(x)
+    check_backward(x, dtype)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_equal_keys_and_full_writes(dtype):
+    # the same key again and again with b = 1: the hardest inverse of a block
+    x = R.inputs(1, 2, 2, 140, 64, 64, dtype, gate=None, state=True, seed=4)
+    x["k"][:] = x["k"][:, :, :1]
+    x["beta"][:] = 1.0
+    check_forward(x)
+    check_backward(x, dtype)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("layout", ["bhnd", "bnhd"])
+def test_long_sequence(dtype, layout):
+    x = R.inputs(1, 2, 1, 1000, 128, 128, dtype, layout=layout, seed=6)
+    check_forward(x, layout)
+    check_backward(x, dtype, layout)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_a_sequence_in_parts(dtype):
+    x = on_gpu(R.inputs(2, 2, 2, 300, 64, 64, dtype, state=True, seed=8))
+
+    def part(a, b, S):
+        c = {n: t[:, :, a:b].contiguous() for n, t in x.items() if n != "S_in"}
+        return la.forward_delta(**c, S_in=S, return_state=True)
+
+    y, S = la.forward_delta(**x, return_state=True)
+    S1, ys = x["S_in"], []
+    for a, b in ((0, 100), (100, 101), (101, 101), (101, 300)):
+        y1, S1 = part(a, b, S1)
+        ys.append(y1)
+    # two summation orders of the same sums: twice the bound
+    R.check(torch.cat(ys, 2), y.cpu(), "y", 2 * R.R_F32 + 2 * R.half_step(dtype))
+    R.check(S1, S.cpu(), "S", 2 * R.R_F32)
+
+
+def test_padding_leaves_the_state():
+    x = R.inputs(1, 2, 2, 90, 64, 64, BF16, state=True, seed=11)
+    x["beta"][:, :, 70:] = 0
+    x["log_gate"][:, :, 70:] = 0
+    _, S = gpu_forward(x, return_state=True)
+    cut = {n: t if n == "S_in" else t[:, :, :70].contiguous() for n, t in x.items()}
+    R.check(S, R.forward(cut)[1], "S")
+
+
+def test_final_state_over_the_initial_one():
+    x = R.inputs(1, 2, 2, 130, 64, 128, BF16, state=True, seed=12)
+    want = gpu_forward(x, return_state=True)
+    xg = on_gpu(x)
+    S = xg["S_in"]
+    y, S2 = la.forward_delta(**xg, S_out=S, return_state=True)
+    assert S2 is S and torch.equal(S, want[1]) and torch.equal(y, want[0])
+
+
+def test_no_tokens():
+    x = on_gpu(R.inputs(1, 2, 1, 0, 64, 64, BF16, state=True))
+    y, S = la.forward_delta(**x, return_state=True)
+    assert y.shape == (1, 2, 0, 64) and torch.equal(S, x["S_in"])
+    x0 = {**x, "S_in": None}
+    assert not la.forward_delta(**x0, return_state=True)[1].any()
+    dS = torch.randn_like(x["S_in"])
+    got = la.backward_delta(x["q"], x["k"], x["v"], x["beta"], x["v"], x["log_gate"], S_in=x["S_in"], grad_S_out=dS)
+    assert torch.equal(got[5], dS)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_the_same_bits_again(dtype):
+    x = R.inputs(2, 4, 2, 260, 128, 128, dtype, state=True, seed=13)
+    dy, dS = upstream(x, dtype)
+    a, b = gpu_forward(x, return_state=True), gpu_forward(x, return_state=True)
+    assert all(torch.equal(s, t) for s, t in zip(a, b))
+    a, b = gpu_backward(x, dy, dS), gpu_backward(x, dy, dS)
+    assert all(torch.equal(s, t) for s, t in zip(a, b))
+
+
+def test_nothing_is_written_outside():
+    """Outputs carved out of one buffer: what lies between them stays."""
+    x = on_gpu(R.inputs(1, 2, 2, 77, 64, 64, BF16, state=True, seed=14))
+    n = x["v"].numel()
+    buf = torch.full((3 * n,), 7.0, dtype=BF16, device="cuda")
+    y = buf[n:2 * n].view(x["v"].shape)
+    sbuf = torch.full((3 * x["S_in"].numel(),), 7.0, device="cuda")
+    m = x["S_in"].numel()
+    S = sbuf[m:2 * m].view(x["S_in"].shape)
+    la.forward_delta(**x, out=y, S_out=S, return_state=True)
+    assert (buf[:n] == 7).all() and (buf[2 * n:] == 7).all() and (sbuf[:m] == 7).all() and (sbuf[2 * m:] == 7).all()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("d,dv,group", [(32, 32, 1), (128, 128, 2), (64, 128, 1), (128, 32, 4)])
+@pytest.mark.parametrize("gate", [None, "any"])
+def test_single_steps_are_the_sequence(dtype, d, dv, group, gate):
+    x = R.inputs(3, 4, 4 // group, 6, d, dv, dtype, gate=gate, state=True, seed=d)
+    yr, Sr = R.forward(x)
+    xg = on_gpu(x)
+    S = xg["S_in"].clone()
+    for t in range(6):
+        y = la.decode_step_delta(*(xg[n][:, :, t].contiguous() for n in ("q", "k", "v", "beta")), S,
+                                 None if gate is None else xg["log_gate"][:, :, t].contiguous())
+        R.check(y, yr[:, :, t], f"y {t}")
+    R.check(S, Sr, "S")
+
+
+def test_step_into_another_state():
+    x = on_gpu(R.inputs(2, 2, 2, 1, 64, 64, BF16, state=True, seed=15))
+    args = [x[n][:, :, 0].contiguous() for n in ("q", "k", "v", "beta")]
+    S0, S1 = x["S_in"].clone(), torch.empty_like(x["S_in"])
+    y1 = la.decode_step_delta(*args, S0, x["log_gate"][:, :, 0].contiguous(), S_out=S1)
+    assert torch.equal(S0, x["S_in"])
+    y0 = la.decode_step_delta(*args, S0, x["log_gate"][:, :, 0].contiguous())
+    assert torch.equal(S0, S1) and torch.equal(y0, y1)
+
+
+# ---- layer norm -----------------------------------------------------------------
+# float32 sums of D values: mean and rstd are off by a few 2^-24 (a tree of sums) of the RMS of x,
+# far below r = 1e-5; the column sums of `rows` values by 2^-24 sqrt(rows) or less
+R_NORM = 1e-5
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("rows,D", [(1, 1), (3, 7), (5, 32), (700, 64), (1000, 128), (33, 100), (17, 127), (9, 256),
+                                    (40, 511), (40, 512), (21, 1000), (6, 2048), (5, 4099), (4, 8192), (3, 16384),
+                                    (2, 16383), (20011, 8)])
+@pytest.mark.parametrize("affine", [False, True])
+def test_layer_norm(dtype, rows, D, affine):
+    g = torch.Generator().manual_seed(D)
+    x = (torch.randn(rows, D, generator=g) * 2 + torch.randn(rows, 1, generator=g)).to(dtype)
+    dy = torch.randn(rows, D, generator=g).to(dtype)
+    w, b = (1 + 0.3 * torch.randn(D, generator=g), torch.randn(D, generator=g)) if affine else (None, None)
+    dev = [t if t is None else t.cuda() for t in (x, w, b)]
+    y, mean, rstd = la.layer_norm(*dev, return_stats=True)
+    yr, mr, rr = R.layer_norm(x, w, b)
+    if D == 1:   # x - mean is exactly zero, and so is every gradient of x
+        assert torch.equal(y.cpu().double(), torch.zeros_like(yr) if b is None else b.expand_as(yr).to(dtype).double())
+    else:
+        R.check(y, yr, "y", R_NORM)
+    R.check(mean, mr, "mean", R_NORM)
+    R.check(rstd, rr, "rstd", R_NORM)
+    gx, gw, gb = la.layer_norm_backward(dy.cuda(), dev[0], mr.float().cuda(), rr.float().cuda(), dev[1], sums=True)
+    gxr, gwr, gbr = R.layer_norm_backward(dy, x, mr.float(), rr.float(), w)
+    # of the size of dy rstd, the terms it is the difference of
+    scale = (dy.double() * rr[:, None]).square().mean().sqrt() / gxr.square().mean().sqrt().clamp_min(1e-30)
+    if D > 2:
+        R.check(gx, gxr, "grad_x", R_NORM * max(1.0, scale.item()))
+    R.check(gw, gwr, "grad_weight", 4 * R_NORM)
+    R.check(gb, gbr, "grad_bias", 4 * R_NORM)
+    only = la.layer_norm_backward(dy.cuda(), dev[0], mr.float().cuda(), rr.float().cuda(), dev[1], sums=False)
+    assert only[1] is None and torch.equal(only[0], gx)
+
+
+def test_layer_norm_unaligned_rows_and_in_place():
+    # rows that start 2 bytes off a 16-byte boundary, and y written over x
+    buf = torch.randn(4 * 128 + 1, device="cuda").to(BF16)
+    x = buf[1:].view(4, 128)
+    yr, _, _ = R.layer_norm(x.cpu())
+    R.check(la.layer_norm(x), yr, "y", R_NORM)
+    z = x.clone()
+    la.layer_norm(z, out=z)
+    R.check(z, yr, "y", R_NORM)
+
+
+def test_layer_norm_of_equal_values():
+    x = torch.full((3, 96), 5.0, device="cuda")
+    y, mean, rstd = la.layer_norm(x, return_stats=True)
+    assert not y.any() and (mean == 5).all() and torch.allclose(rstd, torch.full_like(rstd, 1e-5 ** -0.5))
+
+
+def test_layer_norm_no_rows():
+    x = torch.empty(0, 64, device="cuda")
+    assert la.layer_norm(x).shape == (0, 64)
+    s = torch.empty(0, device="cuda")
+    gx, gw, gb = la.layer_norm_backward(x, x, s, s, torch.ones(64, device="cuda"))
+    assert gx.shape == (0, 64) and not gw.any() and not gb.any()
+
+
+# ---- together -------------------------------------------------------------------
+def test_one_layer_and_its_gradients():
+    """The delta rule, its norm, and the gradients back through both, as a training step runs them;
+    against float64 autograd through both.  The values between the two are rounded to bf16 on the
+    way (y, and dy): two half steps of their RMS on top of the bounds."""
+    B, H, N, d, dv = 2, 4, 150, 64, 64
+    x = R.inputs(B, H, 2, N, d, dv, BF16, layout="bnhd", seed=21)
+    g = torch.Generator().manual_seed(22)
+    w, b = 1 + 0.1 * torch.randn(dv, generator=g), 0.1 * torch.randn(dv, generator=g)
+    do = torch.randn(B, N, H, dv, generator=g).to(BF16)
+    xg = on_gpu(x)
+    y = la.forward_delta(**xg, layout="bnhd")
+    o, mean, rstd = la.layer_norm(y, w.cuda(), b.cuda(), return_stats=True)
+    gy, gw, gb = la.layer_norm_backward(do.cuda(), y, mean, rstd, w.cuda())
+    grads = la.backward_delta(xg["q"], xg["k"], xg["v"], xg["beta"], gy, xg["log_gate"], layout="bnhd")
+
+    leaves = {n: t if t is None else t.double().requires_grad_() for n, t in x.items()}
+    wl, bl = w.double().requires_grad_(), b.double().requires_grad_()
+    yr, _ = R.forward(leaves, "bnhd")
+    outr, _, _ = R.layer_norm(yr, wl, bl)
+    names = ["q", "k", "v", "beta", "log_gate"]
+    want = torch.autograd.grad((outr * do.double()).sum(), [leaves[n] for n in names] + [wl, bl])
+    for n, a, r in zip(names + ["weight", "bias"], [*grads[:5], gw, gb], want):
+        err = (a.cpu().double() - r).norm() / r.norm()
+        assert err <= 4 * R.half_step(BF16), (n, err.item())
+    assert (o.cpu().double() - outr).norm() / outr.norm() <= 3 * R.half_step(BF16)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_captured_and_on_another_stream(dtype):
+    x = on_gpu(R.inputs(1, 4, 2, 200, 64, 64, dtype, state=True, seed=31))
+    dy = torch.randn_like(x["v"])
+    w = torch.rand(64, device="cuda")
+
+    def step():
+        y, S = la.forward_delta(**x, return_state=True)
+        o, mean, rstd = la.layer_norm(y, w, return_stats=True)
+        gy, gw, gb = la.layer_norm_backward(dy, y, mean, rstd, w)
+        grads = la.backward_delta(x["q"], x["k"], x["v"], x["beta"], gy, x["log_gate"], S_in=x["S_in"])
+        st = la.decode_step_delta(x["q"][:, :, 0].contiguous(), x["k"][:, :, 0].contiguous(),
+                                  x["v"][:, :, 0].contiguous(), x["beta"][:, :, 0].contiguous(), S)
+        return [y, S, o, gy, gw, gb, *grads, st]
+
+    want = step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    x["v"].mul_(2)
+    want2 = step()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want2))
+    assert not torch.equal(want[0], want2[0])
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    y = la.forward_delta(**x, stream=s)
+    n = la.layer_norm(y, w, stream=s)
+    s.synchronize()
+    assert torch.equal(y, want2[0]) and torch.equal(n, want2[2])
