@@ -528,6 +528,10 @@ size_t delta_bwd_ws_bytes(int B, int H, int Hk, int N, int d, int dv, la_dtype d
                                                d, dv, dt, LA_LAYOUT_BHND, nullptr, nullptr, nullptr));
 }
 
+// The tensor-core kernel takes a block of 64 tokens at a time and has a longer start; below half a
+// block the token-by-token kernel is done sooner.
+bool delta_on_tensor_cores(const DeltaArgs &a) { return a.N >= 32 && delta_tc_supported(a); }
+
 // dst = src, or zero without one.
 cudaError_t copy_state(float *dst, const float *src, size_t bytes, cudaStream_t s) {
     if (!dst || dst == src) return cudaSuccess;
@@ -552,8 +556,10 @@ la_status check_norm(const void *x, const void *y, long long rows, int D, la_dty
 extern "C" {
 
 size_t la_delta_workspace_bytes(int B, int H, int Hk, int N, int d, int dv, la_dtype dt) {
-    (void)B; (void)H; (void)Hk; (void)N; (void)d; (void)dv; (void)dt;
-    return 0;
+    if (check_delta(B, H, Hk, N, d, dv, dt) != LA_OK || N == 0) return 0;
+    return delta_on_tensor_cores(delta_args(nullptr, nullptr, nullptr, nullptr, nullptr, B, H, Hk, N, d,
+                                            dv, dt, LA_LAYOUT_BHND, nullptr, nullptr, nullptr))
+               ? sizeof(WsHeader) : 0;
 }
 
 la_status la_forward_delta(const void *q, const void *k, const void *v, void *y, const float *beta,
@@ -583,7 +589,9 @@ la_status la_forward_delta(const void *q, const void *k, const void *v, void *y,
                              stream);
     a.y = y;
     a.S_out = S_out;
-    return from_cuda(launch_delta_forward_simt(a));
+    if (need == 0) return from_cuda(launch_delta_forward_simt(a));
+    if (cudaMemsetAsync(workspace, 0, sizeof(WsHeader), s) != cudaSuccess) return LA_ERR_CUDA;
+    return from_cuda(launch_delta_forward_tc(a));
 }
 
 size_t la_delta_backward_workspace_bytes(int B, int H, int Hk, int N, int d, int dv, la_dtype dt) {

@@ -1,0 +1,708 @@
+// delta_tc.cu -- the gated delta rule on the tensor cores (bf16 inputs, d and
+// dv in {64, 128}): blocks of C = 64 tokens, one CTA per head.
+//
+// With c_i the product of the block's gates up to token i, D_ij = c_i / c_j
+// and S the state before the block, the errors e of a block's tokens solve
+//     (I + M) e = v - c . (K S),     M_ij = D_ij (k_i . k_j) b_j  (j < i),
+// and with T = (I + M)^-1 (unit lower triangular)
+//     e  = T (v - c . (K S)),
+//     y  = c . (Q S) + P e,          P_ij = D_ij (q_i . k_j) b_j  (j <= i),
+//     S' = c_C S + K^T W,            W_j = D_Cj b_j e_j.
+// Everything that meets the state is held transposed, a TMEM lane for each of
+// the dv columns of S: S^T, e^T and y^T are accumulators whose rows one thread
+// reads, scales and writes back as the next product's TMEM operand, so the
+// chain S -> K S -> e -> S' never leaves TMEM and registers.
+//
+// Precision: states, e and T are float32 values.  A float32 operand enters
+// the MMAs as three bf16 pieces that add up to it exactly (the top, middle and
+// low 8 bits of its significand, by truncation), so K S and K^T W, whose other
+// operand is the bf16 input itself, lose nothing but the accumulator's
+// float32 rounding, and T r drops only the products of pieces below 2^-24.
+// What only y depends on, which is rounded to bf16 anyway, takes two pieces
+// (2^-16): Q S and P e.
+//
+// Roles (16 warps): warps 0-7 carry the chain (two threads a row, each half of
+// the columns; the float32 state lives in their registers); warps 8 and 9 run
+// one to two blocks ahead and turn K K^T into T, warps 10 and 11 Q K^T into P;
+// warps 12-15 write y.  One thread of the chain issues its MMAs and the TMA loads.
+#include "delta_common.cuh"
+#include "tc_common.cuh"
+
+namespace la {
+namespace {
+
+constexpr int kDC = kDeltaC;   // tokens of a block
+constexpr int kStages = 3;     // K and Q tiles in flight
+constexpr int kChain = 256, kInner = 64, kOut = 128;   // threads: chain; T, and P; y
+constexpr int kBarChain = 1, kBarInner = 2;
+
+// TMEM columns.  The state's pieces take SP .. SP + 3 D/2; once K S and Q S
+// are done, their place serves the residual r (SP + 96), W (SP) and, after
+// T r, the pieces of e for P e (SP + 96).
+constexpr uint32_t kColSP = 0, kColR = 96, kColW = 0, kColE = 96;
+constexpr uint32_t kColSD = 192;    // K^T W, D columns
+constexpr uint32_t kColKS = 320;    // K S, then T r, then P e
+constexpr uint32_t kColQS = 384;
+constexpr uint32_t kColKK = 448;    // [K; Q] K^T: lanes 0-63 and 64-127
+
+struct DeltaTc {
+    __nv_bfloat16 *y;
+    const float *beta, *lg;
+    int H, group, N, layout, nblk;
+    const float *S_in;
+    float *S_out;
+    float *S_ck, *e;               // SAVE
+    unsigned int *err, *err_where;
+    unsigned long long limit_ns;
+    int drop_item;
+};
+
+struct Gates {   // of one block
+    float c[kDC], w[kDC], b[kDC], hi[kDC], lo[kDC], cC, pad[3];
+};
+struct DeltaSmall {
+    Gates gates[4];
+    uint64_t kq_full[kStages], v_full[2], kk_full, kk_read, g_ready, t_ready[2], t_free[2], p_ready, ks_done, qs_done,
+        e_done, s_done, pu_done, o_read, drain[2];
+    uint32_t tmem_base;
+    volatile int abort_flag;
+};
+
+template <int D, int DV> struct DeltaLay {
+    static constexpr int kKQ = (D / 64) * 16384;      // per 64 features: K rows, then Q rows
+    static constexpr int kV = (DV / 64) * 8192;
+    static constexpr int kT = 3 * 8192, kP = 2 * 8192, kA = kDC * kDC * 4;
+    static constexpr int oKQ = 0, oV = oKQ + kStages * kKQ, oT = oV + 2 * kV, oP = oT + 2 * kT,
+                         oA = oP + kP, oSmall = oA + kA;
+    static constexpr int total = oSmall + (int)sizeof(DeltaSmall);
+    static constexpr int request = total + 1024;
+};
+
+// Three pieces of a pair: words of the high, middle and low bf16 halves.
+__device__ __forceinline__ void split3(float x0, float x1, uint32_t &h, uint32_t &m, uint32_t &l) {
+    const uint32_t a0 = f2u(x0), a1 = f2u(x1);
+    h = __byte_perm(a0, a1, 0x7632);
+    float r0, r1;
+    f2unpack(f2sub(f2pack(x0, x1), f2pack(u2f(a0 & 0xFFFF0000u), u2f(a1 & 0xFFFF0000u))), r0, r1);
+    const uint32_t b0 = f2u(r0), b1 = f2u(r1);
+    m = __byte_perm(b0, b1, 0x7632);
+    f2unpack(f2sub(f2pack(r0, r1), f2pack(u2f(b0 & 0xFFFF0000u), u2f(b1 & 0xFFFF0000u))), r0, r1);
+    l = __byte_perm(f2u(r0), f2u(r1), 0x7632);
+}
+__device__ __forceinline__ void split2(float x0, float x1, uint32_t &h, uint32_t &m) {
+    const uint32_t a0 = f2u(x0), a1 = f2u(x1);
+    h = __byte_perm(a0, a1, 0x7632);
+    float r0, r1;
+    f2unpack(f2sub(f2pack(x0, x1), f2pack(u2f(a0 & 0xFFFF0000u), u2f(a1 & 0xFFFF0000u))), r0, r1);
+    m = pack_bf16x2(r0, r1);
+}
+__device__ __forceinline__ uint64_t f2fma(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
+// The gates of a block: running log2 sums as pairs hi + lo (differences of two of
+// them keep their precision behind a nearly closed gate), c, w = D_Cj b_j, b.  One warp; two
+// tokens a lane.
+__device__ __forceinline__ void block_gates(Gates &g, const float (&b)[2], const float (&lg)[2], int lane) {
+    double x[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)   // 2^-14427 is 0; keeps -inf out
+        x[i] = 1.4426950408889634 * (double)(lg[i] < -1e4f ? -1e4f : lg[i]);
+    x[1] += x[0];
+    double s = x[1];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const double y = __shfl_up_sync(0xffffffffu, s, o);
+        if (lane >= o) s += y;
+    }
+    const double before = s - x[1], last = __shfl_sync(0xffffffffu, s, 31);
+    x[0] += before;
+    x[1] += before;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int j = 2 * lane + i;
+        const float hi = (float)x[i];
+        g.hi[j] = hi;
+        g.lo[j] = (float)(x[i] - (double)hi);
+        g.c[j] = ex2_ftz(hi);
+        g.w[j] = ex2_ftz((float)(last - x[i])) * b[i];
+        g.b[j] = b[i];
+    }
+    if (lane == 31) g.cC = ex2_ftz((float)last);
+}
+
+// Row `row` of T = (I + A)^-1 for the unit lower triangular I + A, rows below R: back substitution
+// t_j = [j = row] - sum_{m > j} t_m A_mj with A's columns in `at` (at[j * 64 + m] = A_mj, zero for
+// m <= j).  t as packed pairs.
+template <int R> __device__ __forceinline__ void invert_row(const float *at, int row, uint64_t (&t)[32]) {
+#pragma unroll
+    for (int p = 0; p < 32; ++p) t[p] = f2pack(0.f, 0.f);
+#pragma unroll
+    for (int j = R - 1; j >= 0; --j) {
+        uint64_t s0 = f2pack(0.f, 0.f), s1 = s0;
+        const ulonglong2 *col = reinterpret_cast<const ulonglong2 *>(at + j * kDC);
+#pragma unroll
+        for (int p = j / 4 * 2; p < R / 2; p += 2) {
+            const ulonglong2 a = col[p / 2];
+            s0 = f2fma(t[p], a.x, s0);
+            s1 = f2fma(t[p + 1], a.y, s1);
+        }
+        const float v = j == row ? 1.f : -f2sum(f2add(s0, s1));
+        float a, b;
+        f2unpack(t[j / 2], a, b);
+        t[j / 2] = (j & 1) ? f2pack(a, v) : f2pack(v, b);
+    }
+}
+
+__device__ __forceinline__ uint64_t desc_k(uint32_t addr) { return smem_desc(addr, 16, 1024, kSwizzle128B); }
+
+// SAVE: the backward's first pass -- writes e and the state before every block (and the last one)
+// instead of y; warps 10-15 are not launched.
+template <int D, int DV, bool SAVE>
+__global__ void __launch_bounds__(SAVE ? kChain + kInner : kChain + 2 * kInner + kOut, 1)
+delta_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
+                const __grid_constant__ CUtensorMap vmap, const DeltaTc p) {
+    using Lay = DeltaLay<D, DV>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                              ~static_cast<uintptr_t>(1023));
+    DeltaSmall &S = *reinterpret_cast<DeltaSmall *>(sm + Lay::oSmall);
+    uint8_t *sKQ = sm + Lay::oKQ, *sV = sm + Lay::oV, *sT = sm + Lay::oT, *sP = sm + Lay::oP;
+    float *sA = reinterpret_cast<float *>(sm + Lay::oA);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int bh = blockIdx.x, b = bh / p.H, h = bh - b * p.H, hk = h / p.group;
+    const int nblk = p.nblk;
+    const Guard g{&S.abort_flag, p.err, p.err_where, p.limit_ns};
+
+    if (tid == 0) {
+        S.abort_flag = 0;
+        for (int i = 0; i < kStages; ++i) mbar_init(&S.kq_full[i], 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&S.v_full[i], 1);
+            mbar_init(&S.t_ready[i], kInner);
+            mbar_init(&S.t_free[i], 1);
+            mbar_init(&S.drain[i], 1);
+        }
+        mbar_init(&S.kk_full, 1);
+        mbar_init(&S.kk_read, SAVE ? kInner : 2 * kInner);
+        mbar_init(&S.g_ready, 32);
+        mbar_init(&S.p_ready, kInner);
+        mbar_init(&S.ks_done, 1);
+        mbar_init(&S.qs_done, 1);
+        mbar_init(&S.e_done, 1);
+        mbar_init(&S.s_done, 1);
+        mbar_init(&S.pu_done, 2);       // the MMAs, and their issuer's own arrival
+        mbar_init(&S.o_read, kOut);
+        fence_mbar_init();
+        prefetch_tmap(&kmap);
+        prefetch_tmap(&vmap);
+        if (!SAVE) prefetch_tmap(&qmap);
+    }
+    if (warp == 0) {
+        tmem_alloc(&S.tmem_base, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tb = S.tmem_base;
+    const int wq = warp & 3, row = wq * 32 + lane;
+    const uint32_t lb = (uint32_t)(wq * 32) << 16;
+    constexpr uint32_t i64 = idesc_bf16(128, kDC, 0, 0);
+
+    if (warp < 8) {
+        // ------------------------------------------------------------ chain
+        constexpr uint32_t iS = idesc_bf16(128, D, 0, 1);   // B = K, feature-major
+        const int half = warp >> 2;
+        const bool live = row < DV;   // warp-uniform
+        constexpr int SC = D / 2;     // state columns of a thread
+        int kq_issued = 0, v_issued = 0;
+        auto load_kq = [&](int n) {
+            uint64_t *bar = &S.kq_full[n % kStages];
+            mbar_arrive_expect_tx(bar, (SAVE ? 1 : 2) * kDC * D * 2);
+            ++kq_issued;
+            if (n == 0 && bh == p.drop_item) return;   // test hook: announced, never issued
+            uint8_t *dst = sKQ + (n % kStages) * Lay::kKQ;
+#pragma unroll
+            for (int f = 0; f < D / 64; ++f) {
+                tma_load_4d(dst + f * 16384, &kmap, bar, f * 64, n * kDC, hk, b);
+                if (!SAVE) tma_load_4d(dst + f * 16384 + 8192, &qmap, bar, f * 64, n * kDC, hk, b);
+            }
+        };
+        auto load_v = [&](int n) {
+            uint64_t *bar = &S.v_full[n & 1];
+            mbar_arrive_expect_tx(bar, kDC * DV * 2);
+            ++v_issued;
+            uint8_t *dst = sV + (n & 1) * Lay::kV;
+#pragma unroll
+            for (int f = 0; f < DV / 64; ++f)
+                tma_load_4d(dst + f * 8192, &vmap, bar, f * 64, n * kDC, h, b);
+        };
+        if (tid == 0) {
+            for (int n = 0; n < kStages && n < nblk; ++n) {
+                load_kq(n);
+                if (n < 2) load_v(n);
+            }
+        }
+        // the state, its column `row`, rows half * SC ..
+        float st[SC];
+        const size_t sbase = (size_t)bh * D * DV + (size_t)half * SC * DV + row;
+#pragma unroll
+        for (int i = 0; i < SC; ++i)
+            st[i] = live && p.S_in ? p.S_in[sbase + (size_t)i * DV] : 0.f;
+        auto write_state = [&](float *dst) {   // dst: this head's [D][DV], at row half * SC, column row
+#pragma unroll
+            for (int i = 0; i < SC; ++i) dst[(size_t)i * DV] = st[i];
+        };
+        auto put_state = [&](int i0) {   // pieces of 16 columns
+            uint32_t hi[8], mi[8], lo[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                split3(st[i0 + 2 * i], st[i0 + 2 * i + 1], hi[i], mi[i], lo[i]);
+            const uint32_t col = tb + lb + kColSP + (half * SC + i0) / 2;
+            tmem_st8(col, hi);
+            tmem_st8(col + D / 2, mi);
+            tmem_st8(col + D, lo);
+        };
+        if (live) {
+#pragma unroll
+            for (int i = 0; i < SC; i += 16) put_state(i);
+            if (SAVE)
+                write_state(p.S_ck + (size_t)bh * (nblk + 1) * D * DV + (size_t)half * SC * DV + row);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        bool failed = group_any<kBarChain, kChain>(false);
+
+        for (int n = 0; n < nblk && !failed; ++n) {
+            const uint32_t kq = smem_u32(sKQ + (n % kStages) * Lay::kKQ);
+            const Gates &G = S.gates[n & 3];
+            bool ok = true;
+            if (tid == 0) {
+                ok = mbar_wait(&S.kq_full[n % kStages], (n / kStages) & 1, g, 1);
+                if (!SAVE && ok && n > 0) ok = mbar_wait(&S.o_read, (n - 1) & 1, g, 2);
+                if (ok) {
+                    tc_fence_after();
+#pragma unroll
+                    for (int pc = 0; pc < 3; ++pc)
+#pragma unroll
+                        for (int ks = 0; ks < D / 16; ++ks)
+                            mma_ts(tb + kColKS, tb + kColSP + pc * (D / 2) + ks * 8,
+                                   desc_k(kq + (ks >> 2) * 16384 + (ks & 3) * 32), i64, pc + ks > 0);
+                    mma_commit(&S.ks_done);
+                    if (!SAVE) {
+#pragma unroll
+                        for (int pc = 0; pc < 2; ++pc)
+#pragma unroll
+                            for (int ks = 0; ks < D / 16; ++ks)
+                                mma_ts(tb + kColQS, tb + kColSP + pc * (D / 2) + ks * 8,
+                                       desc_k(kq + 8192 + (ks >> 2) * 16384 + (ks & 3) * 32), i64,
+                                       pc + ks > 0);
+                        mma_commit(&S.qs_done);
+                    }
+                }
+            }
+            __syncwarp();
+            // ---- r = v - c . (K S)
+            ok = ok && mbar_wait(&S.v_full[n & 1], (n >> 1) & 1, g, 3);
+            ok = ok && mbar_wait(&S.t_ready[n & 1], (n >> 1) & 1, g, 4);
+            ok = ok && mbar_wait(&S.ks_done, n & 1, g, 5);
+            ok = __all_sync(0xffffffffu, ok);
+            if (ok && live) {
+                tc_fence_after();
+                const uint8_t *tv = sV + (n & 1) * Lay::kV + (row >> 6) * 8192;
+                uint32_t acc[2][16], hi[8], mi[8], lo[8];
+                tmem_ld16(tb + lb + kColKS + half * 32, acc[0]);
+                tmem_ld16(tb + lb + kColKS + half * 32 + 16, acc[1]);
+                tmem_wait_ld();
+                if (!SAVE) ok = __all_sync(0xffffffffu, mbar_wait(&S.qs_done, n & 1, g, 6));
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const int j0 = half * 32 + u * 16;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        float r[2];
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int j = j0 + 2 * i + e;
+                            const float v = __bfloat162float(
+                                *reinterpret_cast<const __nv_bfloat16 *>(tv + sw128_off(j, row & 63)));
+                            r[e] = fmaf(-G.c[j], u2f(acc[u][2 * i + e]), v);
+                        }
+                        split3(r[0], r[1], hi[i], mi[i], lo[i]);
+                    }
+                    const uint32_t col = tb + lb + kColR + j0 / 2;
+                    tmem_st8(col, hi);
+                    tmem_st8(col + 32, mi);
+                    tmem_st8(col + 64, lo);
+                }
+                tmem_wait_st();
+                tc_fence_before();
+            }
+            if ((failed = group_any<kBarChain, kChain>(!ok))) break;
+            // ---- e = T r
+            if (tid == 0) {
+                tc_fence_after();
+                const uint32_t t = smem_u32(sT + (n & 1) * Lay::kT);
+                // pieces (r, T) whose product is above 2^-24 of the whole
+                constexpr int order[6][2] = {{0, 0}, {0, 1}, {1, 0}, {1, 1}, {0, 2}, {2, 0}};
+#pragma unroll
+                for (int o = 0; o < 6; ++o)
+#pragma unroll
+                    for (int ks = 0; ks < kDC / 16; ++ks)
+                        mma_ts(tb + kColKS, tb + kColR + order[o][0] * 32 + ks * 8,
+                               desc_k(t + order[o][1] * 8192 + ks * 32), i64, o + ks > 0);
+                mma_commit(&S.e_done);
+                mma_commit(&S.t_free[n & 1]);
+                if (n + 2 < nblk) load_v(n + 2);   // every thread has read this block's v
+            }
+            __syncwarp();
+            ok = __all_sync(0xffffffffu, mbar_wait(&S.e_done, n & 1, g, 7));
+            if (ok && live) {
+                tc_fence_after();
+                uint32_t acc[2][16], hi[8], mi[8], lo[8];
+                tmem_ld16(tb + lb + kColKS + half * 32, acc[0]);
+                tmem_ld16(tb + lb + kColKS + half * 32 + 16, acc[1]);
+                tmem_wait_ld();
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const int j0 = half * 32 + u * 16;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        split3(G.w[j0 + 2 * i] * u2f(acc[u][2 * i]), G.w[j0 + 2 * i + 1] * u2f(acc[u][2 * i + 1]),
+                               hi[i], mi[i], lo[i]);
+                    const uint32_t col = tb + lb + kColW + j0 / 2;
+                    tmem_st8(col, hi);
+                    tmem_st8(col + 32, mi);
+                    tmem_st8(col + 64, lo);
+                    if (!SAVE) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            split2(u2f(acc[u][2 * i]), u2f(acc[u][2 * i + 1]), hi[i], mi[i]);
+                        const uint32_t ce = tb + lb + kColE + j0 / 2;
+                        tmem_st8(ce, hi);
+                        tmem_st8(ce + 32, mi);
+                    } else {
+                        float *dst = p.e + ((size_t)bh * p.N + (size_t)n * kDC + j0) * DV + row;
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            if (n * kDC + j0 + i < p.N) dst[(size_t)i * DV] = u2f(acc[u][i]);
+                    }
+                }
+                tmem_wait_st();
+                tc_fence_before();
+            }
+            if ((failed = group_any<kBarChain, kChain>(!ok))) break;
+            // ---- S' = c_C S + K^T W, y's second part
+            if (tid == 0) {
+                tc_fence_after();
+#pragma unroll
+                for (int pc = 0; pc < 3; ++pc)
+#pragma unroll
+                    for (int ks = 0; ks < kDC / 16; ++ks)
+                        mma_ts(tb + kColSD, tb + kColW + pc * 32 + ks * 8,
+                               smem_desc(kq + ks * 2048, 16384, 1024, kSwizzle128B), iS, pc + ks > 0);
+                mma_commit(&S.s_done);
+                if (!SAVE) {
+                    ok = mbar_wait(&S.p_ready, n & 1, g, 8);
+                    if (ok) {
+                        tc_fence_after();
+                        const uint32_t sp = smem_u32(sP);
+                        constexpr int order[3][2] = {{0, 0}, {0, 1}, {1, 0}};   // pieces (e, P)
+#pragma unroll
+                        for (int o = 0; o < 3; ++o)
+#pragma unroll
+                            for (int ks = 0; ks < kDC / 16; ++ks)
+                                mma_ts(tb + kColKS, tb + kColE + order[o][0] * 32 + ks * 8,
+                                       desc_k(sp + order[o][1] * 8192 + ks * 32), i64, o + ks > 0);
+                        mma_commit(&S.pu_done);
+                        mbar_arrive(&S.pu_done);
+                    }
+                }
+            }
+            __syncwarp();
+            ok = ok && mbar_wait(&S.s_done, n & 1, g, 9);
+            ok = __all_sync(0xffffffffu, ok);
+            // this block's K and Q have been read: [K; Q] K^T before T was ready, Q S before r
+            if (tid == 0 && ok && n + kStages < nblk) load_kq(n + kStages);
+            if (ok && live) {
+                tc_fence_after();
+                const float cC = G.cC;
+#pragma unroll
+                for (int i = 0; i < SC; i += 16) {
+                    uint32_t acc[16];
+                    tmem_ld16(tb + lb + kColSD + half * SC + i, acc);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) st[i + j] = fmaf(cC, st[i + j], u2f(acc[j]));
+                    // SP is free: W, the last operand there, has been read
+                    if (n + 1 < nblk && SAVE) put_state(i);
+                }
+                if (!SAVE && n + 1 < nblk) {
+                    // the pieces of e lie in SP too: wait for P e
+                    ok = __all_sync(0xffffffffu, mbar_wait(&S.pu_done, n & 1, g, 10));
+                    tc_fence_after();
+                    if (ok) {
+#pragma unroll
+                        for (int i = 0; i < SC; i += 16) put_state(i);
+                    }
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                if (SAVE)
+                    write_state(p.S_ck + ((size_t)bh * (nblk + 1) + n + 1) * D * DV +
+                                (size_t)half * SC * DV + row);
+            }
+            failed = group_any<kBarChain, kChain>(!ok);
+        }
+        if (!failed && live && p.S_out) write_state(p.S_out + sbase);
+        if (tid == 0) {
+            mma_commit(&S.drain[0]);
+            drain_wait(&S.drain[0], 0, g.limit_ns);
+            if (S.abort_flag) {   // let the copies in flight land
+                for (int n = max(0, kq_issued - kStages); n < kq_issued; ++n)
+                    if (!(n == 0 && bh == p.drop_item))
+                        drain_wait(&S.kq_full[n % kStages], (n / kStages) & 1, g.limit_ns);
+                for (int n = max(0, v_issued - 2); n < v_issued; ++n)
+                    drain_wait(&S.v_full[n & 1], (n >> 1) & 1, g.limit_ns);
+            }
+        }
+        __syncwarp();
+    } else if (warp < 10) {
+        // ------------------------------------------------------------ T, ahead of the chain
+        const TokenRows rs = token_rows(p.layout, b, h, p.H, p.N, 1);
+        float bv[2], gv[2];   // warp 8: the next block's beta and log gates
+        auto fetch = [&](int n) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int t = n * kDC + 2 * lane + i;
+                bv[i] = t < p.N ? p.beta[rs.at(t)] : 0.f;
+                gv[i] = t < p.N && p.lg ? p.lg[rs.at(t)] : 0.f;
+            }
+        };
+        if (warp == 8) fetch(0);
+        for (int n = 0; n < nblk; ++n) {
+            // gates[n & 3] was last read for block n - 4, which the chain and the output have left:
+            // T n - 3 has been used, and that block's K S waited for y n - 4 to be read
+            Gates &G = S.gates[n & 3];
+            bool ok = true;
+            if (warp == 8) {
+                if (lane == 0) {
+                    ok = mbar_wait(&S.kq_full[n % kStages], (n / kStages) & 1, g, 20);
+                    if (ok && n > 0) ok = mbar_wait(&S.kk_read, (n - 1) & 1, g, 24);
+                    if (ok) {
+                        tc_fence_after();
+                        const uint32_t kq = smem_u32(sKQ + (n % kStages) * Lay::kKQ);
+#pragma unroll
+                        for (int ks = 0; ks < D / 16; ++ks) {
+                            const uint64_t d = desc_k(kq + (ks >> 2) * 16384 + (ks & 3) * 32);
+                            mma_ss(tb + kColKK, d, d, i64, ks > 0);
+                        }
+                        mma_commit(&S.kk_full);
+                    }
+                }
+                ok = __all_sync(0xffffffffu, ok);
+                if (ok) {
+                    block_gates(G, bv, gv, lane);
+                    mbar_arrive(&S.g_ready);
+                }
+            }
+            ok = ok && mbar_wait(&S.g_ready, n & 1, g, 25);
+            ok = ok && mbar_wait(&S.kk_full, n & 1, g, 21);
+            ok = __all_sync(0xffffffffu, ok);
+            if (ok) {
+                tc_fence_after();
+                // A_ij = D_ij (k_i . k_j) b_j, j < i, by columns
+                const float hi = G.hi[row], lo = G.lo[row];
+#pragma unroll 1
+                for (int j0 = 0; j0 < kDC; j0 += 16) {
+                    uint32_t acc[16];
+                    tmem_ld16(tb + lb + kColKK + j0, acc);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int jj = 0; jj < 16; ++jj) {
+                        const int j = j0 + jj;
+                        const float x = ex2_ftz((hi - G.hi[j]) + (lo - G.lo[j])) * u2f(acc[jj]) * G.b[j];
+                        sA[j * kDC + row] = j < row ? x : 0.f;
+                    }
+                }
+                tc_fence_before();
+                mbar_arrive(&S.kk_read);
+                if (warp == 8 && n + 1 < nblk) fetch(n + 1);
+            }
+            if (group_any<kBarInner, 64>(!ok)) break;   // A complete
+            ok = n < 2 || mbar_wait(&S.t_free[n & 1], ((n >> 1) - 1) & 1, g, 23);
+            ok = __all_sync(0xffffffffu, ok);
+            if (ok) {
+                uint64_t t[32];
+                if (row < 32) invert_row<32>(sA, row, t);
+                else invert_row<64>(sA, row, t);
+                uint8_t *dst = sT + (n & 1) * Lay::kT;
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                    uint32_t hi[4], mi[4], lo[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        float x0, x1;
+                        f2unpack(t[4 * q + e], x0, x1);
+                        split3(x0, x1, hi[e], mi[e], lo[e]);
+                    }
+                    const uint32_t o = sw128_off(row, 8 * q);
+                    *reinterpret_cast<uint4 *>(dst + o) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                    *reinterpret_cast<uint4 *>(dst + 8192 + o) = make_uint4(mi[0], mi[1], mi[2], mi[3]);
+                    *reinterpret_cast<uint4 *>(dst + 16384 + o) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                }
+                fence_proxy_async();
+                mbar_arrive(&S.t_ready[n & 1]);
+            }
+            if (group_any<kBarInner, 64>(!ok)) break;   // A may be written again
+        }
+        if (warp == 8 && lane == 0) {
+            mma_commit(&S.drain[1]);
+            drain_wait(&S.drain[1], 0, g.limit_ns);
+        }
+        __syncwarp();
+    } else if (warp < 12) {
+        // ------------------------------------------------------------ P_ij = D_ij (q_i . k_j) b_j, j <= i
+        const int i = row & 63;
+        for (int n = 0; n < nblk; ++n) {
+            const Gates &G = S.gates[n & 3];
+            bool ok = mbar_wait(&S.g_ready, n & 1, g, 26) && mbar_wait(&S.kk_full, n & 1, g, 27);
+            if (!__all_sync(0xffffffffu, ok)) break;
+            tc_fence_after();
+            uint32_t acc[4][16];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) tmem_ld16(tb + lb + kColKK + 16 * u, acc[u]);
+            tmem_wait_ld();
+            tc_fence_before();
+            mbar_arrive(&S.kk_read);
+            ok = n == 0 || mbar_wait(&S.pu_done, (n - 1) & 1, g, 22);   // the previous P has been used
+            if (!__all_sync(0xffffffffu, ok)) break;
+            const float ghi = G.hi[i], glo = G.lo[i];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                uint32_t hi[8], mi[8];
+#pragma unroll
+                for (int jj = 0; jj < 8; ++jj) {
+                    float x[2];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int j = 16 * u + 2 * jj + e;
+                        const float v = ex2_ftz((ghi - G.hi[j]) + (glo - G.lo[j])) * u2f(acc[u][2 * jj + e]) * G.b[j];
+                        x[e] = j <= i ? v : 0.f;
+                    }
+                    split2(x[0], x[1], hi[jj], mi[jj]);
+                }
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    const uint32_t o = sw128_off(i, 16 * u + 8 * q);
+                    *reinterpret_cast<uint4 *>(sP + o) =
+                        make_uint4(hi[4 * q], hi[4 * q + 1], hi[4 * q + 2], hi[4 * q + 3]);
+                    *reinterpret_cast<uint4 *>(sP + 8192 + o) =
+                        make_uint4(mi[4 * q], mi[4 * q + 1], mi[4 * q + 2], mi[4 * q + 3]);
+                }
+            }
+            fence_proxy_async();
+            mbar_arrive(&S.p_ready);
+        }
+    } else {
+        // ------------------------------------------------------------ y = c . (Q S) + P e
+        const TokenRows rv = token_rows(p.layout, b, h, p.H, p.N, DV);
+        for (int n = 0; n < nblk; ++n) {
+            const Gates &G = S.gates[n & 3];
+            const bool ok = __all_sync(0xffffffffu, mbar_wait(&S.pu_done, n & 1, g, 30));
+            if (!ok) break;
+            tc_fence_after();
+            if (row < DV) {
+#pragma unroll 1
+                for (int j0 = 0; j0 < kDC; j0 += 16) {
+                    uint32_t qs[16], pe[16];
+                    tmem_ld16(tb + lb + kColQS + j0, qs);
+                    tmem_ld16(tb + lb + kColKS + j0, pe);
+                    tmem_wait_ld();
+                    if (j0 == kDC - 16) {
+                        tc_fence_before();
+                        mbar_arrive(&S.o_read);
+                    }
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        const int t = n * kDC + j0 + j;
+                        if (t < p.N)
+                            p.y[rv.at(t) + row] = __float2bfloat16_rn(fmaf(G.c[j0 + j], u2f(qs[j]), u2f(pe[j])));
+                    }
+                }
+            } else {
+                mbar_arrive(&S.o_read);
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 0) {
+        tc_fence_after();
+        tmem_dealloc(tb, 512);
+    }
+}
+
+// Map over a token tensor of `heads` heads of width w: (feature, token, head, batch), boxes of 64
+// features x 64 tokens.
+bool encode_tokens(CUtensorMap *m, const void *base, int layout, int B, int heads, int N, int w) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t tok = layout == LA_LAYOUT_BNHD ? (cuuint64_t)heads * w : w;
+    const cuuint64_t hd = layout == LA_LAYOUT_BNHD ? w : (cuuint64_t)N * w;
+    const cuuint64_t dims[4] = {(cuuint64_t)w, (cuuint64_t)N, (cuuint64_t)heads, (cuuint64_t)B};
+    const cuuint64_t strides[3] = {2 * tok, 2 * hd, 2 * (cuuint64_t)heads * N * w};
+    const cuuint32_t box[4] = {64, kDC, 1, 1}, es[4] = {1, 1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base), dims, strides, box, es,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, int DV, bool SAVE> cudaError_t launch_tc(const DeltaArgs &a) {
+    CUtensorMap qm, km, vm;
+    if (!encode_tokens(&qm, a.q, a.layout, a.B, a.Hk, a.N, D) ||
+        !encode_tokens(&km, a.k, a.layout, a.B, a.Hk, a.N, D) ||
+        !encode_tokens(&vm, a.v, a.layout, a.B, a.H, a.N, DV))
+        return cudaErrorInvalidValue;
+    DeltaTc p{};
+    p.y = static_cast<__nv_bfloat16 *>(a.y);
+    p.beta = a.beta; p.lg = a.log_gate;
+    p.H = a.H; p.group = a.H / a.Hk; p.N = a.N; p.layout = a.layout; p.nblk = delta_blocks(a.N);
+    p.S_in = a.S_in; p.S_out = a.S_out;
+    if (SAVE) {
+        const DeltaBwdWs w = delta_bwd_ws(a);
+        p.S_ck = w.S;
+        p.e = w.e;
+    }
+    WsHeader *hdr = static_cast<WsHeader *>(a.ws);
+    p.err = &hdr->error;
+    p.err_where = &hdr->error_where;
+    const long long lim = debug_fault().wait_limit_ns;
+    p.limit_ns = lim > 0 ? (unsigned long long)lim : 1000000000ull;
+    p.drop_item = debug_fault().drop_load_item;
+    auto kern = delta_tc_kernel<D, DV, SAVE>;
+    constexpr int smem = DeltaLay<D, DV>::request;
+    static_assert(smem <= 232448, "shared memory of a CTA");
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    kern<<<a.B * a.H, SAVE ? kChain + kInner : kChain + 2 * kInner + kOut, smem, a.stream>>>(qm, km, vm, p);
+    return cudaGetLastError();
+}
+
+template <bool SAVE> cudaError_t launch_tc_dims(const DeltaArgs &a) {
+    if (a.d == 64) return a.dv == 64 ? launch_tc<64, 64, SAVE>(a) : launch_tc<64, 128, SAVE>(a);
+    return a.dv == 64 ? launch_tc<128, 64, SAVE>(a) : launch_tc<128, 128, SAVE>(a);
+}
+
+}  // namespace
+
+bool delta_tc_supported(const DeltaArgs &a) {
+    return a.dt == LA_DTYPE_BF16 && (a.d == 64 || a.d == 128) && (a.dv == 64 || a.dv == 128);
+}
+cudaError_t launch_delta_forward_tc(const DeltaArgs &a) { return launch_tc_dims<false>(a); }
+cudaError_t launch_delta_states_tc(const DeltaArgs &a) { return launch_tc_dims<true>(a); }
+
+}  // namespace la

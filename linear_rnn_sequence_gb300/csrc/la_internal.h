@@ -169,6 +169,10 @@ cudaError_t launch_causal_backward(const BwdArgs &a);
 cudaError_t launch_delta_forward_simt(const DeltaArgs &a);
 cudaError_t launch_delta_states_simt(const DeltaArgs &a);    // the backward's first pass
 cudaError_t launch_delta_reverse_simt(const DeltaArgs &a);   // and its second
+// tensor cores (bf16, d and dv in {64, 128}); a.ws starts with a status header
+bool delta_tc_supported(const DeltaArgs &a);
+cudaError_t launch_delta_forward_tc(const DeltaArgs &a);
+cudaError_t launch_delta_states_tc(const DeltaArgs &a);
 size_t delta_backward_workspace(const DeltaArgs &a);
 cudaError_t launch_delta_backward(const DeltaArgs &a);
 cudaError_t launch_delta_step(const DeltaArgs &a);
