@@ -22,9 +22,12 @@
 // (2^-16): Q S and P e.
 //
 // Roles (16 warps): warps 0-7 carry the chain (two threads a row, each half of
-// the columns; the float32 state lives in their registers); warps 8 and 9 run
-// one to two blocks ahead and turn K K^T into T, warps 10 and 11 Q K^T into P;
-// warps 12-15 write y.  One thread of the chain issues its MMAs and the TMA loads.
+// the columns; the float32 state lives in their registers); warps 8-11 run one
+// to two blocks ahead and turn K K^T into T; warps 12-15 turn Q K^T into P (two
+// of them) and write y.  One thread of the chain issues its MMAs and the TMA
+// loads.  Every role runs short loops rather than unrolled code: with each
+// warp's code fetched once a block, straight-line code ran at about 7 cycles
+// an instruction, whatever it did (B8 H16 N8192 d128: 1.81 ms unrolled).
 #include "delta_common.cuh"
 #include "tc_common.cuh"
 
@@ -33,8 +36,9 @@ namespace {
 
 constexpr int kDC = kDeltaC;   // tokens of a block
 constexpr int kStages = 3;     // K and Q tiles in flight
-constexpr int kChain = 256, kInner = 64, kOut = 128;   // threads: chain; T, and P; y
+constexpr int kChain = 256, kInner = 128, kOut = 128;   // threads: chain; T; P and y
 constexpr int kBarChain = 1, kBarInner = 2;
+constexpr int kAP = kDC + 4;   // floats of a row of A: rows four banks apart
 
 // TMEM columns.  The state's pieces take SP .. SP + 3 D/2; once K S and Q S
 // are done, their place serves the residual r (SP + 96), W (SP) and, after
@@ -62,8 +66,7 @@ struct Gates {   // of one block
 };
 struct DeltaSmall {
     Gates gates[4];
-    uint64_t kq_full[kStages], v_full[2], kk_full, kk_read, g_ready, t_ready[2], t_free[2], p_ready, ks_done, qs_done,
-        e_done, s_done, pu_done, o_read, drain[2];
+    uint64_t kq_full[kStages], v_full[2], kk_full, kk_read, g_ready, t_ready[2], t_free[2], p_ready, ks_done, qs_done, e_done, s_done, pu_done, o_read, drain[2];
     uint32_t tmem_base;
     volatile int abort_flag;
 };
@@ -71,7 +74,7 @@ struct DeltaSmall {
 template <int D, int DV> struct DeltaLay {
     static constexpr int kKQ = (D / 64) * 16384;      // per 64 features: K rows, then Q rows
     static constexpr int kV = (DV / 64) * 8192;
-    static constexpr int kT = 3 * 8192, kP = 2 * 8192, kA = kDC * kDC * 4;
+    static constexpr int kT = 3 * 8192, kP = 2 * 8192, kA = kDC * kAP * 4;
     static constexpr int oKQ = 0, oV = oKQ + kStages * kKQ, oT = oV + 2 * kV, oP = oT + 2 * kT,
                          oA = oP + kP, oSmall = oA + kA;
     static constexpr int total = oSmall + (int)sizeof(DeltaSmall);
@@ -96,82 +99,158 @@ __device__ __forceinline__ void split2(float x0, float x1, uint32_t &h, uint32_t
     f2unpack(f2sub(f2pack(x0, x1), f2pack(u2f(a0 & 0xFFFF0000u), u2f(a1 & 0xFFFF0000u))), r0, r1);
     m = pack_bf16x2(r0, r1);
 }
-__device__ __forceinline__ uint64_t f2fma(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
+__device__ __forceinline__ void load16(const float *p, float (&x)[16]) {
+#pragma unroll
+    for (int i = 0; i < 16; i += 4)
+        *reinterpret_cast<float4 *>(x + i) = *reinterpret_cast<const float4 *>(p + i);
+}
+
+// A float32 pair h + l, |l| at most half a step of h: sums keep about 46 bits.
+struct F2 {
+    float h, l;
+};
+__device__ __forceinline__ F2 f2sum2(F2 a, F2 b) {
+    const float s = a.h + b.h, t = s - a.h;
+    const float l = ((a.h - (s - t)) + (b.h - t)) + (a.l + b.l);
+    const float h = s + l;
+    return {h, l - (h - s)};
 }
 
 // The gates of a block: running log2 sums as pairs hi + lo (differences of two of
 // them keep their precision behind a nearly closed gate), c, w = D_Cj b_j, b.  One warp; two
 // tokens a lane.
 __device__ __forceinline__ void block_gates(Gates &g, const float (&b)[2], const float (&lg)[2], int lane) {
-    double x[2];
+    constexpr float kL = 1.44269502f, kLl = 1.92596299e-8f;   // log2(e) in two floats
+    F2 x[2];
 #pragma unroll
-    for (int i = 0; i < 2; ++i)   // 2^-14427 is 0; keeps -inf out
-        x[i] = 1.4426950408889634 * (double)(lg[i] < -1e4f ? -1e4f : lg[i]);
-    x[1] += x[0];
-    double s = x[1];
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const double y = __shfl_up_sync(0xffffffffu, s, o);
-        if (lane >= o) s += y;
+    for (int i = 0; i < 2; ++i) {   // 2^-14427 is 0; keeps -inf out
+        const float v = lg[i] < -1e4f ? -1e4f : lg[i], h = v * kL;
+        x[i] = {h, fmaf(v, kL, -h) + v * kLl};
     }
-    const double before = s - x[1], last = __shfl_sync(0xffffffffu, s, 31);
-    x[0] += before;
-    x[1] += before;
+    x[1] = f2sum2(x[0], x[1]);
+    F2 s = x[1];
+#pragma unroll 1
+    for (int o = 1; o < 32; o <<= 1) {
+        const F2 y = {__shfl_up_sync(0xffffffffu, s.h, o), __shfl_up_sync(0xffffffffu, s.l, o)};
+        if (lane >= o) s = f2sum2(y, s);
+    }
+    F2 before = {__shfl_up_sync(0xffffffffu, s.h, 1), __shfl_up_sync(0xffffffffu, s.l, 1)};
+    if (lane == 0) before = {0.f, 0.f};
+    const F2 last = {__shfl_sync(0xffffffffu, s.h, 31), __shfl_sync(0xffffffffu, s.l, 31)};
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const int j = 2 * lane + i;
-        const float hi = (float)x[i];
-        g.hi[j] = hi;
-        g.lo[j] = (float)(x[i] - (double)hi);
-        g.c[j] = ex2_ftz(hi);
-        g.w[j] = ex2_ftz((float)(last - x[i])) * b[i];
+        const F2 y = f2sum2(before, x[i]);
+        g.hi[j] = y.h;
+        g.lo[j] = y.l;
+        g.c[j] = ex2_ftz(y.h) * fmaf(y.l, 0.693147f, 1.f);
+        g.w[j] = ex2_ftz((last.h - y.h) + (last.l - y.l)) * b[i];
         g.b[j] = b[i];
     }
-    if (lane == 31) g.cC = ex2_ftz((float)last);
+    if (lane == 31) g.cC = ex2_ftz(last.h) * fmaf(last.l, 0.693147f, 1.f);
 }
 
-// Row `row` of T = (I + A)^-1 for the unit lower triangular I + A, rows below R: back substitution
-// t_j = [j = row] - sum_{m > j} t_m A_mj with A's columns in `at` (at[j * 64 + m] = A_mj, zero for
-// m <= j).  t as packed pairs.
-template <int R> __device__ __forceinline__ void invert_row(const float *at, int row, uint64_t (&t)[32]) {
+// T = (I + A)^-1 in place, for A [64][64] strictly lower triangular with zeros above (row pitch
+// kAP), by the kInner threads of the T warps: the four diagonal blocks of 16 by forward
+// substitution, a thread for each column, then twice [[T1, 0], [-T2 A21 T1, T2]].
+template <int SZ> __device__ __forceinline__ void merge_blocks(float *A, int t) {
+    constexpr int RT = SZ / 16, PER = SZ * SZ / 4 / RT;   // rows of a thread (x 4 columns), threads a pair
+    const int pair = t / PER, q = t % PER;
+    const int r = q / (SZ / 4) * RT, c = q % (SZ / 4) * 4;
+    float *T1 = A + pair * 2 * SZ * (kAP + 1), *A21 = T1 + SZ * kAP, *T2 = A21 + SZ;
+#pragma unroll 1
+    for (int step = 0; step < 2; ++step) {   // A21 <- A21 T1, then A21 <- -T2 A21
+        const float *L = step ? T2 : A21, *Rm = step ? A21 : T1;
+        float acc[RT][4];
 #pragma unroll
-    for (int p = 0; p < 32; ++p) t[p] = f2pack(0.f, 0.f);
+        for (int i = 0; i < RT; ++i)
 #pragma unroll
-    for (int j = R - 1; j >= 0; --j) {
-        uint64_t s0 = f2pack(0.f, 0.f), s1 = s0;
-        const ulonglong2 *col = reinterpret_cast<const ulonglong2 *>(at + j * kDC);
+            for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
+#pragma unroll 1
+        for (int m = 0; m < SZ; m += 4) {
+            float l[RT][4];
 #pragma unroll
-        for (int p = j / 4 * 2; p < R / 2; p += 2) {
-            const ulonglong2 a = col[p / 2];
-            s0 = f2fma(t[p], a.x, s0);
-            s1 = f2fma(t[p + 1], a.y, s1);
+            for (int i = 0; i < RT; ++i)
+                *reinterpret_cast<float4 *>(l[i]) = *reinterpret_cast<const float4 *>(L + (r + i) * kAP + m);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float4 x = *reinterpret_cast<const float4 *>(Rm + (m + k) * kAP + c);
+#pragma unroll
+                for (int i = 0; i < RT; ++i) {
+                    acc[i][0] = fmaf(l[i][k], x.x, acc[i][0]);
+                    acc[i][1] = fmaf(l[i][k], x.y, acc[i][1]);
+                    acc[i][2] = fmaf(l[i][k], x.z, acc[i][2]);
+                    acc[i][3] = fmaf(l[i][k], x.w, acc[i][3]);
+                }
+            }
         }
-        const float v = j == row ? 1.f : -f2sum(f2add(s0, s1));
-        float a, b;
-        f2unpack(t[j / 2], a, b);
-        t[j / 2] = (j & 1) ? f2pack(a, v) : f2pack(v, b);
+        named_bar(kBarInner, kInner);
+        const float sg = step ? -1.f : 1.f;
+#pragma unroll
+        for (int i = 0; i < RT; ++i)
+            *reinterpret_cast<float4 *>(A21 + (r + i) * kAP + c) =
+                make_float4(sg * acc[i][0], sg * acc[i][1], sg * acc[i][2], sg * acc[i][3]);
+        named_bar(kBarInner, kInner);
     }
+}
+__device__ __forceinline__ void invert_unit_lower(float *A, int t) {
+    float *blk = A + (t >> 4) * 16 * (kAP + 1);
+    const int c = t & 15;
+    float x[16];
+    if (t < 64) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            float v = i == c ? 1.f : 0.f;
+#pragma unroll
+            for (int j = 0; j < i; j += 4) {
+                const float4 a = *reinterpret_cast<const float4 *>(blk + i * kAP + j);
+                v = fmaf(-a.x, x[j], v);
+                if (j + 1 < i) v = fmaf(-a.y, x[j + 1], v);
+                if (j + 2 < i) v = fmaf(-a.z, x[j + 2], v);
+                if (j + 3 < i) v = fmaf(-a.w, x[j + 3], v);
+            }
+            x[i] = v;
+        }
+    }
+    named_bar(kBarInner, kInner);
+    if (t < 64) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) blk[i * kAP + c] = x[i];
+    }
+    named_bar(kBarInner, kInner);
+    merge_blocks<16>(A, t);
+    merge_blocks<32>(A, t);
 }
 
 __device__ __forceinline__ uint64_t desc_k(uint32_t addr) { return smem_desc(addr, 16, 1024, kSwizzle128B); }
 
+// d (+)= A B^T over K = 16 N values: A in TMEM from column `a` on, B token- or row-major (K
+// contiguous) in 64-value slabs SLAB bytes apart.
+template <int N, int SLAB>
+__device__ __forceinline__ void mma_rows(uint32_t leader, uint32_t d, uint32_t a, uint32_t b, uint32_t idesc,
+                                         bool add) {
+    const uint64_t base = desc_k(b);
+#pragma unroll
+    for (int ks = 0; ks < N; ++ks)
+        mma_ts_if(leader, d, a + ks * 8, base + (uint32_t)(((ks >> 2) * SLAB + (ks & 3) * 32) >> 4), idesc,
+                  add || ks > 0);
+}
+
 // SAVE: the backward's first pass -- writes e and the state before every block (and the last one)
-// instead of y; warps 10-15 are not launched.
+// instead of y; warps 12-15 are not launched.
 template <int D, int DV, bool SAVE>
-__global__ void __launch_bounds__(SAVE ? kChain + kInner : kChain + 2 * kInner + kOut, 1)
+__global__ void __launch_bounds__(SAVE ? kChain + kInner : kChain + kInner + kOut, 1)
 delta_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                 const __grid_constant__ CUtensorMap vmap, const DeltaTc p) {
     using Lay = DeltaLay<D, DV>;
     extern __shared__ uint8_t smem_raw[];
-    uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                              ~static_cast<uintptr_t>(1023));
+    // aligned by an offset, so that the compiler still sees shared memory
+    uint8_t *sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     DeltaSmall &S = *reinterpret_cast<DeltaSmall *>(sm + Lay::oSmall);
     uint8_t *sKQ = sm + Lay::oKQ, *sV = sm + Lay::oV, *sT = sm + Lay::oT, *sP = sm + Lay::oP;
     float *sA = reinterpret_cast<float *>(sm + Lay::oA);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    // warp-uniform to the compiler too
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const int bh = blockIdx.x, b = bh / p.H, h = bh - b * p.H, hk = h / p.group;
     const int nblk = p.nblk;
     const Guard g{&S.abort_flag, p.err, p.err_where, p.limit_ns};
@@ -186,9 +265,9 @@ delta_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
             mbar_init(&S.drain[i], 1);
         }
         mbar_init(&S.kk_full, 1);
-        mbar_init(&S.kk_read, SAVE ? kInner : 2 * kInner);
+        mbar_init(&S.kk_read, SAVE ? 64 : 128);   // a thread for each row of K, and of Q
         mbar_init(&S.g_ready, 32);
-        mbar_init(&S.p_ready, kInner);
+        mbar_init(&S.p_ready, 64);
         mbar_init(&S.ks_done, 1);
         mbar_init(&S.qs_done, 1);
         mbar_init(&S.e_done, 1);
@@ -207,7 +286,7 @@ delta_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tb = S.tmem_base;
+    const uint32_t tb = __shfl_sync(0xffffffffu, S.tmem_base, 0);
     const int wq = warp & 3, row = wq * 32 + lane;
     const uint32_t lb = (uint32_t)(wq * 32) << 16;
     constexpr uint32_t i64 = idesc_bf16(128, kDC, 0, 0);
@@ -240,12 +319,14 @@ delta_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
             for (int f = 0; f < DV / 64; ++f)
                 tma_load_4d(dst + f * 8192, &vmap, bar, f * 64, n * kDC, h, b);
         };
-        if (tid == 0) {
+        const uint32_t leader = warp == 0 ? elect_leader() : 0u;
+        if (leader) {
             for (int n = 0; n < kStages && n < nblk; ++n) {
                 load_kq(n);
                 if (n < 2) load_v(n);
             }
         }
+        __syncwarp();
         // the state, its column `row`, rows half * SC ..
         float st[SC];
         const size_t sbase = (size_t)bh * D * DV + (size_t)half * SC * DV + row;
@@ -274,65 +355,61 @@ delta_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
         }
         tmem_wait_st();
         tc_fence_before();
-        bool failed = group_any<kBarChain, kChain>(false);
+        // the group's agreement, uniform to the compiler as well
+        auto any_failed = [](bool f) { return __any_sync(0xffffffffu, group_any<kBarChain, kChain>(f)) != 0; };
+        bool failed = any_failed(false);
 
         for (int n = 0; n < nblk && !failed; ++n) {
-            const uint32_t kq = smem_u32(sKQ + (n % kStages) * Lay::kKQ);
+            const uint32_t kq = smem_u32(sKQ) + (n % kStages) * Lay::kKQ;
             const Gates &G = S.gates[n & 3];
             bool ok = true;
-            if (tid == 0) {
-                ok = mbar_wait(&S.kq_full[n % kStages], (n / kStages) & 1, g, 1);
-                if (!SAVE && ok && n > 0) ok = mbar_wait(&S.o_read, (n - 1) & 1, g, 2);
+            if (warp == 0) {
+                ok = mbar_wait<1>(&S.kq_full[n % kStages], (n / kStages) & 1, g, 1);
+                if (!SAVE && n > 0) ok = ok && mbar_wait<1>(&S.o_read, (n - 1) & 1, g, 2);
+                ok = __all_sync(0xffffffffu, ok);
                 if (ok) {
                     tc_fence_after();
-#pragma unroll
-                    for (int pc = 0; pc < 3; ++pc)
-#pragma unroll
-                        for (int ks = 0; ks < D / 16; ++ks)
-                            mma_ts(tb + kColKS, tb + kColSP + pc * (D / 2) + ks * 8,
-                                   desc_k(kq + (ks >> 2) * 16384 + (ks & 3) * 32), i64, pc + ks > 0);
-                    mma_commit(&S.ks_done);
+                    // small pieces first: the accumulator truncates, relative to what it holds
+#pragma unroll 1
+                    for (int pc = 2; pc >= 0; --pc)
+                        mma_rows<D / 16, 16384>(leader, tb + kColKS, tb + kColSP + pc * (D / 2), kq, i64, pc < 2);
+                    mma_commit_if(leader, &S.ks_done);
                     if (!SAVE) {
-#pragma unroll
-                        for (int pc = 0; pc < 2; ++pc)
-#pragma unroll
-                            for (int ks = 0; ks < D / 16; ++ks)
-                                mma_ts(tb + kColQS, tb + kColSP + pc * (D / 2) + ks * 8,
-                                       desc_k(kq + 8192 + (ks >> 2) * 16384 + (ks & 3) * 32), i64,
-                                       pc + ks > 0);
-                        mma_commit(&S.qs_done);
+#pragma unroll 1
+                        for (int pc = 1; pc >= 0; --pc)
+                            mma_rows<D / 16, 16384>(leader, tb + kColQS, tb + kColSP + pc * (D / 2), kq + 8192,
+                                                    i64, pc < 1);
+                        mma_commit_if(leader, &S.qs_done);
                     }
                 }
             }
-            __syncwarp();
             // ---- r = v - c . (K S)
-            ok = ok && mbar_wait(&S.v_full[n & 1], (n >> 1) & 1, g, 3);
-            ok = ok && mbar_wait(&S.t_ready[n & 1], (n >> 1) & 1, g, 4);
-            ok = ok && mbar_wait(&S.ks_done, n & 1, g, 5);
+            ok = ok && mbar_wait<1>(&S.v_full[n & 1], (n >> 1) & 1, g, 3);
+            ok = ok && mbar_wait<1>(&S.t_ready[n & 1], (n >> 1) & 1, g, 4);
+            ok = ok && mbar_wait<1>(&S.ks_done, n & 1, g, 5);
             ok = __all_sync(0xffffffffu, ok);
             if (ok && live) {
                 tc_fence_after();
-                const uint8_t *tv = sV + (n & 1) * Lay::kV + (row >> 6) * 8192;
-                uint32_t acc[2][16], hi[8], mi[8], lo[8];
-                tmem_ld16(tb + lb + kColKS + half * 32, acc[0]);
-                tmem_ld16(tb + lb + kColKS + half * 32 + 16, acc[1]);
-                tmem_wait_ld();
-                if (!SAVE) ok = __all_sync(0xffffffffu, mbar_wait(&S.qs_done, n & 1, g, 6));
-#pragma unroll
+                // v of token j: chunk (row / 8) ^ (j % 8) of the token's 128-byte row
+                const uint8_t *tv = sV + (n & 1) * Lay::kV + (row >> 6) * 8192 + half * 32 * 128 + (row & 7) * 2;
+                const uint32_t ch = (uint32_t)(row & 63) >> 3;
+                if (!SAVE) ok = __all_sync(0xffffffffu, mbar_wait<1>(&S.qs_done, n & 1, g, 6));
+#pragma unroll 1
                 for (int u = 0; u < 2; ++u) {
                     const int j0 = half * 32 + u * 16;
+                    uint32_t acc[16], hi[8], mi[8], lo[8];
+                    tmem_ld16(tb + lb + kColKS + j0, acc);
+                    float r[16], c[16];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        float r[2];
+                    for (int j = 0; j < 16; ++j)
+                        r[j] = __uint_as_float((uint32_t)*reinterpret_cast<const uint16_t *>(
+                                   tv + (u * 16 + j) * 128 + ((ch ^ (j & 7)) << 4)) << 16);
+                    load16(&G.c[j0], c);
+                    tmem_wait_ld();
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const int j = j0 + 2 * i + e;
-                            const float v = __bfloat162float(
-                                *reinterpret_cast<const __nv_bfloat16 *>(tv + sw128_off(j, row & 63)));
-                            r[e] = fmaf(-G.c[j], u2f(acc[u][2 * i + e]), v);
-                        }
-                        split3(r[0], r[1], hi[i], mi[i], lo[i]);
-                    }
+                    for (int j = 0; j < 16; ++j) r[j] = fmaf(-c[j], u2f(acc[j]), r[j]);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) split3(r[2 * i], r[2 * i + 1], hi[i], mi[i], lo[i]);
                     const uint32_t col = tb + lb + kColR + j0 / 2;
                     tmem_st8(col, hi);
                     tmem_st8(col + 32, mi);
@@ -341,92 +418,92 @@ delta_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
                 tmem_wait_st();
                 tc_fence_before();
             }
-            if ((failed = group_any<kBarChain, kChain>(!ok))) break;
+            if ((failed = any_failed(!ok))) break;
             // ---- e = T r
-            if (tid == 0) {
+            if (warp == 0) {
                 tc_fence_after();
-                const uint32_t t = smem_u32(sT + (n & 1) * Lay::kT);
-                // pieces (r, T) whose product is above 2^-24 of the whole
-                constexpr int order[6][2] = {{0, 0}, {0, 1}, {1, 0}, {1, 1}, {0, 2}, {2, 0}};
-#pragma unroll
-                for (int o = 0; o < 6; ++o)
-#pragma unroll
-                    for (int ks = 0; ks < kDC / 16; ++ks)
-                        mma_ts(tb + kColKS, tb + kColR + order[o][0] * 32 + ks * 8,
-                               desc_k(t + order[o][1] * 8192 + ks * 32), i64, o + ks > 0);
-                mma_commit(&S.e_done);
-                mma_commit(&S.t_free[n & 1]);
-                if (n + 2 < nblk) load_v(n + 2);   // every thread has read this block's v
+                const uint32_t t = smem_u32(sT) + (n & 1) * Lay::kT;
+                // the pieces (r, T) whose product is above 2^-24 of the whole, small ones first:
+                // (2, 0) (0, 2) (1, 1) (1, 0) (0, 1) (0, 0)
+#pragma unroll 1
+                for (int o = 0; o < 6; ++o) {
+                    const int pr = (0x201100u >> (20 - 4 * o)) & 3, pt = (0x021010u >> (20 - 4 * o)) & 3;
+                    mma_rows<kDC / 16, 0>(leader, tb + kColKS, tb + kColR + pr * 32, t + pt * 8192, i64, o > 0);
+                }
+                mma_commit_if(leader, &S.e_done);
+                mma_commit_if(leader, &S.t_free[n & 1]);
+                if (leader && n + 2 < nblk) load_v(n + 2);   // every thread has read this block's v
+                __syncwarp();
             }
-            __syncwarp();
-            ok = __all_sync(0xffffffffu, mbar_wait(&S.e_done, n & 1, g, 7));
+            ok = __all_sync(0xffffffffu, mbar_wait<1>(&S.e_done, n & 1, g, 7));
             if (ok && live) {
                 tc_fence_after();
-                uint32_t acc[2][16], hi[8], mi[8], lo[8];
-                tmem_ld16(tb + lb + kColKS + half * 32, acc[0]);
-                tmem_ld16(tb + lb + kColKS + half * 32 + 16, acc[1]);
-                tmem_wait_ld();
-#pragma unroll
+#pragma unroll 1
                 for (int u = 0; u < 2; ++u) {
                     const int j0 = half * 32 + u * 16;
+                    uint32_t acc[16], hi[8], mi[8], lo[8];
+                    float w[16];
+                    tmem_ld16(tb + lb + kColKS + j0, acc);
+                    load16(&G.w[j0], w);
+                    tmem_wait_ld();
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
-                        split3(G.w[j0 + 2 * i] * u2f(acc[u][2 * i]), G.w[j0 + 2 * i + 1] * u2f(acc[u][2 * i + 1]),
-                               hi[i], mi[i], lo[i]);
+                        split3(w[2 * i] * u2f(acc[2 * i]), w[2 * i + 1] * u2f(acc[2 * i + 1]), hi[i], mi[i], lo[i]);
                     const uint32_t col = tb + lb + kColW + j0 / 2;
                     tmem_st8(col, hi);
                     tmem_st8(col + 32, mi);
                     tmem_st8(col + 64, lo);
                     if (!SAVE) {
 #pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            split2(u2f(acc[u][2 * i]), u2f(acc[u][2 * i + 1]), hi[i], mi[i]);
+                        for (int i = 0; i < 8; ++i) split2(u2f(acc[2 * i]), u2f(acc[2 * i + 1]), hi[i], mi[i]);
                         const uint32_t ce = tb + lb + kColE + j0 / 2;
                         tmem_st8(ce, hi);
                         tmem_st8(ce + 32, mi);
                     } else {
                         float *dst = p.e + ((size_t)bh * p.N + (size_t)n * kDC + j0) * DV + row;
+                        const int in = p.N - n * kDC - j0;
 #pragma unroll
                         for (int i = 0; i < 16; ++i)
-                            if (n * kDC + j0 + i < p.N) dst[(size_t)i * DV] = u2f(acc[u][i]);
+                            if (i < in) dst[(size_t)i * DV] = u2f(acc[i]);
                     }
                 }
                 tmem_wait_st();
                 tc_fence_before();
             }
-            if ((failed = group_any<kBarChain, kChain>(!ok))) break;
+            if ((failed = any_failed(!ok))) break;
             // ---- S' = c_C S + K^T W, y's second part
-            if (tid == 0) {
+            if (warp == 0) {
                 tc_fence_after();
-#pragma unroll
-                for (int pc = 0; pc < 3; ++pc)
+                const uint64_t kd = smem_desc(kq, 16384, 1024, kSwizzle128B);
+#pragma unroll 1
+                for (int pc = 2; pc >= 0; --pc)
 #pragma unroll
                     for (int ks = 0; ks < kDC / 16; ++ks)
-                        mma_ts(tb + kColSD, tb + kColW + pc * 32 + ks * 8,
-                               smem_desc(kq + ks * 2048, 16384, 1024, kSwizzle128B), iS, pc + ks > 0);
-                mma_commit(&S.s_done);
+                        mma_ts_if(leader, tb + kColSD, tb + kColW + pc * 32 + ks * 8, kd + ks * 128, iS,
+                                  pc < 2 || ks > 0);
+                mma_commit_if(leader, &S.s_done);
                 if (!SAVE) {
-                    ok = mbar_wait(&S.p_ready, n & 1, g, 8);
+                    ok = __all_sync(0xffffffffu, mbar_wait<1>(&S.p_ready, n & 1, g, 8));
                     if (ok) {
                         tc_fence_after();
                         const uint32_t sp = smem_u32(sP);
-                        constexpr int order[3][2] = {{0, 0}, {0, 1}, {1, 0}};   // pieces (e, P)
-#pragma unroll
-                        for (int o = 0; o < 3; ++o)
-#pragma unroll
-                            for (int ks = 0; ks < kDC / 16; ++ks)
-                                mma_ts(tb + kColKS, tb + kColE + order[o][0] * 32 + ks * 8,
-                                       desc_k(sp + order[o][1] * 8192 + ks * 32), i64, o + ks > 0);
-                        mma_commit(&S.pu_done);
-                        mbar_arrive(&S.pu_done);
+#pragma unroll 1
+                        for (int o = 0; o < 3; ++o)   // pieces (e, P): (0, 1) (1, 0) (0, 0)
+                            mma_rows<kDC / 16, 0>(leader, tb + kColKS, tb + kColE + (o == 1) * 32,
+                                                  sp + (o == 0) * 8192, i64, o > 0);
+                        mma_commit_if(leader, &S.pu_done);
+                        if (leader) mbar_arrive(&S.pu_done);
+                        __syncwarp();
                     }
                 }
             }
-            __syncwarp();
-            ok = ok && mbar_wait(&S.s_done, n & 1, g, 9);
+            ok = ok && mbar_wait<1>(&S.s_done, n & 1, g, 9);
             ok = __all_sync(0xffffffffu, ok);
             // this block's K and Q have been read: [K; Q] K^T before T was ready, Q S before r
-            if (tid == 0 && ok && n + kStages < nblk) load_kq(n + kStages);
+            if (warp == 0 && ok && n + kStages < nblk) {
+                if (leader) load_kq(n + kStages);
+                __syncwarp();
+            }
             if (ok && live) {
                 tc_fence_after();
                 const float cC = G.cC;
@@ -442,7 +519,7 @@ delta_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
                 }
                 if (!SAVE && n + 1 < nblk) {
                     // the pieces of e lie in SP too: wait for P e
-                    ok = __all_sync(0xffffffffu, mbar_wait(&S.pu_done, n & 1, g, 10));
+                    ok = __all_sync(0xffffffffu, mbar_wait<1>(&S.pu_done, n & 1, g, 10));
                     tc_fence_after();
                     if (ok) {
 #pragma unroll
@@ -455,10 +532,10 @@ delta_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
                     write_state(p.S_ck + ((size_t)bh * (nblk + 1) + n + 1) * D * DV +
                                 (size_t)half * SC * DV + row);
             }
-            failed = group_any<kBarChain, kChain>(!ok);
+            failed = any_failed(!ok);
         }
         if (!failed && live && p.S_out) write_state(p.S_out + sbase);
-        if (tid == 0) {
+        if (leader) {
             mma_commit(&S.drain[0]);
             drain_wait(&S.drain[0], 0, g.limit_ns);
             if (S.abort_flag) {   // let the copies in flight land
@@ -470,86 +547,96 @@ delta_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
             }
         }
         __syncwarp();
-    } else if (warp < 10) {
+    } else if (warp < 12) {
         // ------------------------------------------------------------ T, ahead of the chain
         const TokenRows rs = token_rows(p.layout, b, h, p.H, p.N, 1);
-        float bv[2], gv[2];   // warp 8: the next block's beta and log gates
+        const int t = tid - kChain;
+        float bv[2], gv[2];   // warp 10: the next block's beta and log gates
         auto fetch = [&](int n) {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const int t = n * kDC + 2 * lane + i;
-                bv[i] = t < p.N ? p.beta[rs.at(t)] : 0.f;
-                gv[i] = t < p.N && p.lg ? p.lg[rs.at(t)] : 0.f;
+                const int tok = n * kDC + 2 * lane + i;
+                bv[i] = tok < p.N ? p.beta[rs.at(tok)] : 0.f;
+                gv[i] = tok < p.N && p.lg ? p.lg[rs.at(tok)] : 0.f;
             }
         };
-        if (warp == 8) fetch(0);
+        if (warp == 10) fetch(0);
+        const uint32_t leader = warp == 8 ? elect_leader() : 0u;
         for (int n = 0; n < nblk; ++n) {
             // gates[n & 3] was last read for block n - 4, which the chain and the output have left:
             // T n - 3 has been used, and that block's K S waited for y n - 4 to be read
             Gates &G = S.gates[n & 3];
             bool ok = true;
             if (warp == 8) {
-                if (lane == 0) {
-                    ok = mbar_wait(&S.kq_full[n % kStages], (n / kStages) & 1, g, 20);
-                    if (ok && n > 0) ok = mbar_wait(&S.kk_read, (n - 1) & 1, g, 24);
-                    if (ok) {
-                        tc_fence_after();
-                        const uint32_t kq = smem_u32(sKQ + (n % kStages) * Lay::kKQ);
+                ok = mbar_wait<1>(&S.kq_full[n % kStages], (n / kStages) & 1, g, 20);
+                if (n > 0) ok = ok && mbar_wait<1>(&S.kk_read, (n - 1) & 1, g, 24);
+                ok = __all_sync(0xffffffffu, ok);
+                if (ok) {
+                    tc_fence_after();
+                    const uint64_t kd = desc_k(smem_u32(sKQ) + (n % kStages) * Lay::kKQ);
 #pragma unroll
-                        for (int ks = 0; ks < D / 16; ++ks) {
-                            const uint64_t d = desc_k(kq + (ks >> 2) * 16384 + (ks & 3) * 32);
-                            mma_ss(tb + kColKK, d, d, i64, ks > 0);
-                        }
-                        mma_commit(&S.kk_full);
+                    for (int ks = 0; ks < D / 16; ++ks) {
+                        const uint64_t d = kd + (uint32_t)(((ks >> 2) * 16384 + (ks & 3) * 32) >> 4);
+                        mma_ss_if(leader, tb + kColKK, d, d, i64, ks > 0);
                     }
+                    mma_commit_if(leader, &S.kk_full);
                 }
+            }
+            if (warp == 10) {
+                // not ahead of a reader of the block before's gates (it arrives at kk_read after them)
+                ok = n == 0 || mbar_wait<1>(&S.kk_read, (n - 1) & 1, g, 28);
                 ok = __all_sync(0xffffffffu, ok);
                 if (ok) {
                     block_gates(G, bv, gv, lane);
                     mbar_arrive(&S.g_ready);
+                    if (n + 1 < nblk) fetch(n + 1);
                 }
             }
-            ok = ok && mbar_wait(&S.g_ready, n & 1, g, 25);
-            ok = ok && mbar_wait(&S.kk_full, n & 1, g, 21);
-            ok = __all_sync(0xffffffffu, ok);
-            if (ok) {
-                tc_fence_after();
-                // A_ij = D_ij (k_i . k_j) b_j, j < i, by columns
-                const float hi = G.hi[row], lo = G.lo[row];
+            if (row < 64) {   // A_ij = D_ij (k_i . k_j) b_j, j < i
+                ok = ok && mbar_wait<1>(&S.g_ready, n & 1, g, 25);
+                ok = ok && mbar_wait<1>(&S.kk_full, n & 1, g, 21);
+                ok = __all_sync(0xffffffffu, ok);
+                if (ok) {
+                    tc_fence_after();
+                    const float hi = G.hi[row], lo = G.lo[row];
 #pragma unroll 1
-                for (int j0 = 0; j0 < kDC; j0 += 16) {
-                    uint32_t acc[16];
-                    tmem_ld16(tb + lb + kColKK + j0, acc);
-                    tmem_wait_ld();
+                    for (int j0 = 0; j0 < kDC; j0 += 16) {
+                        uint32_t acc[16];
+                        float x[16], y[16];
+                        tmem_ld16(tb + lb + kColKK + j0, acc);
+                        load16(&G.hi[j0], x);
+                        load16(&G.lo[j0], y);
 #pragma unroll
-                    for (int jj = 0; jj < 16; ++jj) {
-                        const int j = j0 + jj;
-                        const float x = ex2_ftz((hi - G.hi[j]) + (lo - G.lo[j])) * u2f(acc[jj]) * G.b[j];
-                        sA[j * kDC + row] = j < row ? x : 0.f;
+                        for (int j = 0; j < 16; ++j) x[j] = ex2_ftz((hi - x[j]) + (lo - y[j]));
+                        load16(&G.b[j0], y);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) x[j] = j0 + j < row ? x[j] * y[j] * u2f(acc[j]) : 0.f;
+#pragma unroll
+                        for (int j = 0; j < 16; j += 4)
+                            *reinterpret_cast<float4 *>(sA + row * kAP + j0 + j) =
+                                make_float4(x[j], x[j + 1], x[j + 2], x[j + 3]);
                     }
+                    tc_fence_before();
+                    mbar_arrive(&S.kk_read);
                 }
-                tc_fence_before();
-                mbar_arrive(&S.kk_read);
-                if (warp == 8 && n + 1 < nblk) fetch(n + 1);
             }
-            if (group_any<kBarInner, 64>(!ok)) break;   // A complete
-            ok = n < 2 || mbar_wait(&S.t_free[n & 1], ((n >> 1) - 1) & 1, g, 23);
+            if (__any_sync(0xffffffffu, group_any<kBarInner, kInner>(!ok))) break;   // A complete
+            invert_unit_lower(sA, t);
+            ok = n < 2 || mbar_wait<1>(&S.t_free[n & 1], ((n >> 1) - 1) & 1, g, 23);
             ok = __all_sync(0xffffffffu, ok);
             if (ok) {
-                uint64_t t[32];
-                if (row < 32) invert_row<32>(sA, row, t);
-                else invert_row<64>(sA, row, t);
                 uint8_t *dst = sT + (n & 1) * Lay::kT;
-#pragma unroll
-                for (int q = 0; q < 8; ++q) {
+                const int i = t >> 1;
+#pragma unroll 1
+                for (int q = (t & 1) * 4, e = q + 4; q < e; ++q) {   // 8 columns
+                    float x[8];
+                    *reinterpret_cast<float4 *>(x) = *reinterpret_cast<const float4 *>(sA + i * kAP + 8 * q);
+                    *reinterpret_cast<float4 *>(x + 4) = *reinterpret_cast<const float4 *>(sA + i * kAP + 8 * q + 4);
                     uint32_t hi[4], mi[4], lo[4];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        float x0, x1;
-                        f2unpack(t[4 * q + e], x0, x1);
-                        split3(x0, x1, hi[e], mi[e], lo[e]);
-                    }
-                    const uint32_t o = sw128_off(row, 8 * q);
+                    for (int e2 = 0; e2 < 4; ++e2) split3(x[2 * e2], x[2 * e2 + 1], hi[e2], mi[e2], lo[e2]);
+                    const uint32_t o = sw128_off(i, 8 * q);
                     *reinterpret_cast<uint4 *>(dst + o) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
                     *reinterpret_cast<uint4 *>(dst + 8192 + o) = make_uint4(mi[0], mi[1], mi[2], mi[3]);
                     *reinterpret_cast<uint4 *>(dst + 16384 + o) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
@@ -557,85 +644,78 @@ delta_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
                 fence_proxy_async();
                 mbar_arrive(&S.t_ready[n & 1]);
             }
-            if (group_any<kBarInner, 64>(!ok)) break;   // A may be written again
+            if (__any_sync(0xffffffffu, group_any<kBarInner, kInner>(!ok))) break;   // A may be written again
         }
-        if (warp == 8 && lane == 0) {
+        if (leader) {
             mma_commit(&S.drain[1]);
             drain_wait(&S.drain[1], 0, g.limit_ns);
         }
         __syncwarp();
-    } else if (warp < 12) {
-        // ------------------------------------------------------------ P_ij = D_ij (q_i . k_j) b_j, j <= i
-        const int i = row & 63;
-        for (int n = 0; n < nblk; ++n) {
-            const Gates &G = S.gates[n & 3];
-            bool ok = mbar_wait(&S.g_ready, n & 1, g, 26) && mbar_wait(&S.kk_full, n & 1, g, 27);
-            if (!__all_sync(0xffffffffu, ok)) break;
-            tc_fence_after();
-            uint32_t acc[4][16];
-#pragma unroll
-            for (int u = 0; u < 4; ++u) tmem_ld16(tb + lb + kColKK + 16 * u, acc[u]);
-            tmem_wait_ld();
-            tc_fence_before();
-            mbar_arrive(&S.kk_read);
-            ok = n == 0 || mbar_wait(&S.pu_done, (n - 1) & 1, g, 22);   // the previous P has been used
-            if (!__all_sync(0xffffffffu, ok)) break;
-            const float ghi = G.hi[i], glo = G.lo[i];
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                uint32_t hi[8], mi[8];
-#pragma unroll
-                for (int jj = 0; jj < 8; ++jj) {
-                    float x[2];
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int j = 16 * u + 2 * jj + e;
-                        const float v = ex2_ftz((ghi - G.hi[j]) + (glo - G.lo[j])) * u2f(acc[u][2 * jj + e]) * G.b[j];
-                        x[e] = j <= i ? v : 0.f;
-                    }
-                    split2(x[0], x[1], hi[jj], mi[jj]);
-                }
-#pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    const uint32_t o = sw128_off(i, 16 * u + 8 * q);
-                    *reinterpret_cast<uint4 *>(sP + o) =
-                        make_uint4(hi[4 * q], hi[4 * q + 1], hi[4 * q + 2], hi[4 * q + 3]);
-                    *reinterpret_cast<uint4 *>(sP + 8192 + o) =
-                        make_uint4(mi[4 * q], mi[4 * q + 1], mi[4 * q + 2], mi[4 * q + 3]);
-                }
-            }
-            fence_proxy_async();
-            mbar_arrive(&S.p_ready);
-        }
     } else {
-        // ------------------------------------------------------------ y = c . (Q S) + P e
+        // ------------------------------------------------------------ P and y
         const TokenRows rv = token_rows(p.layout, b, h, p.H, p.N, DV);
         for (int n = 0; n < nblk; ++n) {
             const Gates &G = S.gates[n & 3];
-            const bool ok = __all_sync(0xffffffffu, mbar_wait(&S.pu_done, n & 1, g, 30));
-            if (!ok) break;
+            bool ok = true;
+            if (row >= 64) {   // P_ij = D_ij (q_i . k_j) b_j, j <= i; the previous P was used before y n - 1
+                const int i = row & 63;
+                ok = mbar_wait<1>(&S.g_ready, n & 1, g, 26) && mbar_wait<1>(&S.kk_full, n & 1, g, 27);
+                if (!__all_sync(0xffffffffu, ok)) break;
+                tc_fence_after();
+                const float ghi = G.hi[i], glo = G.lo[i];
+#pragma unroll 1
+                for (int j0 = 0; j0 < kDC; j0 += 16) {
+                    uint32_t acc[16], hi[8], mi[8];
+                    float x[16], y[16];
+                    tmem_ld16(tb + lb + kColKK + j0, acc);
+                    load16(&G.hi[j0], x);
+                    load16(&G.lo[j0], y);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) x[j] = ex2_ftz((ghi - x[j]) + (glo - y[j]));
+                    load16(&G.b[j0], y);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) x[j] = j0 + j <= i ? x[j] * y[j] * u2f(acc[j]) : 0.f;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) split2(x[2 * j], x[2 * j + 1], hi[j], mi[j]);
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        const uint32_t o = sw128_off(i, j0 + 8 * q);
+                        *reinterpret_cast<uint4 *>(sP + o) =
+                            make_uint4(hi[4 * q], hi[4 * q + 1], hi[4 * q + 2], hi[4 * q + 3]);
+                        *reinterpret_cast<uint4 *>(sP + 8192 + o) =
+                            make_uint4(mi[4 * q], mi[4 * q + 1], mi[4 * q + 2], mi[4 * q + 3]);
+                    }
+                }
+                tc_fence_before();
+                mbar_arrive(&S.kk_read);
+                fence_proxy_async();
+                mbar_arrive(&S.p_ready);
+            }
+            ok = mbar_wait<1>(&S.pu_done, n & 1, g, 30);
+            if (!__all_sync(0xffffffffu, ok)) break;
             tc_fence_after();
-            if (row < DV) {
+            if (row < DV) {   // y = c . (Q S) + P e
+                const int n_in = p.N - n * kDC;
+                __nv_bfloat16 *dst = p.y + rv.at(n * kDC) + row;
 #pragma unroll 1
                 for (int j0 = 0; j0 < kDC; j0 += 16) {
                     uint32_t qs[16], pe[16];
+                    float c[16];
                     tmem_ld16(tb + lb + kColQS + j0, qs);
                     tmem_ld16(tb + lb + kColKS + j0, pe);
+                    load16(&G.c[j0], c);
                     tmem_wait_ld();
-                    if (j0 == kDC - 16) {
-                        tc_fence_before();
-                        mbar_arrive(&S.o_read);
-                    }
 #pragma unroll
                     for (int j = 0; j < 16; ++j) {
-                        const int t = n * kDC + j0 + j;
-                        if (t < p.N)
-                            p.y[rv.at(t) + row] = __float2bfloat16_rn(fmaf(G.c[j0 + j], u2f(qs[j]), u2f(pe[j])));
+                        if (j0 + j < n_in)
+                            *dst = __float2bfloat16_rn(fmaf(c[j], u2f(qs[j]), u2f(pe[j])));
+                        dst += rv.step;
                     }
                 }
-            } else {
-                mbar_arrive(&S.o_read);
+                tc_fence_before();
             }
+            mbar_arrive(&S.o_read);
         }
     }
     tc_fence_before();
@@ -688,7 +768,7 @@ template <int D, int DV, bool SAVE> cudaError_t launch_tc(const DeltaArgs &a) {
     static_assert(smem <= 232448, "shared memory of a CTA");
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    kern<<<a.B * a.H, SAVE ? kChain + kInner : kChain + 2 * kInner + kOut, smem, a.stream>>>(qm, km, vm, p);
+    kern<<<a.B * a.H, SAVE ? kChain + kInner : kChain + kInner + kOut, smem, a.stream>>>(qm, km, vm, p);
     return cudaGetLastError();
 }
 
