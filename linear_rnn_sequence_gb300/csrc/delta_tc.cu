@@ -22,12 +22,12 @@
 // (2^-16): Q S and P e.
 //
 // Roles (16 warps): warps 0-7 carry the chain (two threads a row, each half of
-// the columns; the float32 state lives in their registers); warps 8-11 run one
-// to two blocks ahead and turn K K^T into T; warps 12-15 turn Q K^T into P (two
-// of them) and write y.  One thread of the chain issues its MMAs and the TMA
-// loads.  Every role runs short loops rather than unrolled code: with each
-// warp's code fetched once a block, straight-line code ran at about 7 cycles
-// an instruction, whatever it did (B8 H16 N8192 d128: 1.81 ms unrolled).
+// the columns; the float32 state lives in their registers); warps 8 and 9 turn
+// K K^T of the even blocks into T, warps 10 and 11 that of the odd ones, both
+// ahead of the chain; warps 12-15 turn Q K^T into P (two of them) and write y.
+// The rows of [K; Q] K^T are TMEM lanes, which a warp reaches by its number
+// mod 4: so odd blocks hold Q before K.  The chain's first warp issues its
+// MMAs and the TMA loads.
 #include "delta_common.cuh"
 #include "tc_common.cuh"
 
@@ -36,21 +36,20 @@ namespace {
 
 constexpr int kDC = kDeltaC;   // tokens of a block
 constexpr int kStages = 3;     // K and Q tiles in flight
-constexpr int kChain = 256, kInner = 128, kOut = 128;   // threads: chain; T; P and y
-constexpr int kBarChain = 1, kBarInner = 2;
+constexpr int kChain = 256, kInner = 64, kOut = 128;   // threads: chain; each T group; P and y
+constexpr int kBarChain = 1, kBarInner = 2;   // kBarInner + 1: the second T group
 constexpr int kAP = kDC + 4;   // floats of a row of A: rows four banks apart
 
 // TMEM columns.  The state's pieces take SP .. SP + 3 D/2; once K S and Q S
-// are done, their place serves the residual r (SP + 96), W (SP) and, after
-// T r, the pieces of e for P e (SP + 96).
-constexpr uint32_t kColSP = 0, kColR = 96, kColW = 0, kColE = 96;
-constexpr uint32_t kColSD = 192;    // K^T W, D columns
-constexpr uint32_t kColKS = 320;    // K S, then T r, then P e
+// are done, their place serves W (SP) and the pieces of e for P e (SP + 96).
+// The residual r takes the place of K^T W, which comes after it.
+constexpr uint32_t kColSP = 0, kColW = 0, kColE = 96;
+constexpr uint32_t kColSD = 192, kColR = 192;   // K^T W: D columns
+constexpr uint32_t kColKS = 320;                // K S, then T r, then P e
 constexpr uint32_t kColQS = 384;
-constexpr uint32_t kColKK = 448;    // [K; Q] K^T: lanes 0-63 and 64-127
+constexpr uint32_t kColKK = 448;                // [K; Q] K^T or, for odd blocks, [Q; K] K^T
 
 struct DeltaTc {
-    __nv_bfloat16 *y;
     const float *beta, *lg;
     int H, group, N, layout, nblk;
     const float *S_in;
@@ -62,21 +61,23 @@ struct DeltaTc {
 };
 
 struct Gates {   // of one block
-    float c[kDC], w[kDC], b[kDC], hi[kDC], lo[kDC], cC, pad[3];
+    float c[kDC], w[kDC], b[kDC], hi[kDC], lo[kDC];
+    float f[kDC];   // b_j / c_j, for blocks whose c stays above 2^-60 (`fast`)
+    float cC, fast, pad[2];
 };
 struct DeltaSmall {
     Gates gates[4];
-    uint64_t kq_full[kStages], v_full[2], kk_full, kk_read, g_ready, t_ready[2], t_free[2], p_ready, ks_done, qs_done, e_done, s_done, pu_done, o_read, drain[2];
+    uint64_t kq_full[kStages], v_full[2], kk_full, kk_read, g_ready[2], t_ready[2], t_free[2], p_ready, ks_done, qs_done, e_done, s_done, pu_done, o_read, drain[3];
     uint32_t tmem_base;
     volatile int abort_flag;
 };
 
 template <int D, int DV> struct DeltaLay {
-    static constexpr int kKQ = (D / 64) * 16384;      // per 64 features: K rows, then Q rows
+    static constexpr int kKQ = (D / 64) * 16384;      // per 64 features: K and Q rows, odd blocks Q first
     static constexpr int kV = (DV / 64) * 8192;
-    static constexpr int kT = 3 * 8192, kP = 2 * 8192, kA = kDC * kAP * 4;
+    static constexpr int kT = 3 * 8192, kP = 2 * 8192;   // T's place first holds A, [64][kAP] floats
     static constexpr int oKQ = 0, oV = oKQ + kStages * kKQ, oT = oV + 2 * kV, oP = oT + 2 * kT,
-                         oA = oP + kP, oSmall = oA + kA;
+                         oY = oP + kP, oSmall = oY + kV;
     static constexpr int total = oSmall + (int)sizeof(DeltaSmall);
     static constexpr int request = total + 1024;
 };
@@ -98,6 +99,11 @@ __device__ __forceinline__ void split2(float x0, float x1, uint32_t &h, uint32_t
     float r0, r1;
     f2unpack(f2sub(f2pack(x0, x1), f2pack(u2f(a0 & 0xFFFF0000u), u2f(a1 & 0xFFFF0000u))), r0, r1);
     m = pack_bf16x2(r0, r1);
+}
+__device__ __forceinline__ uint64_t f2fma(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
 }
 __device__ __forceinline__ void load16(const float *p, float (&x)[16]) {
 #pragma unroll
@@ -146,35 +152,39 @@ __device__ __forceinline__ void block_gates(Gates &g, const float (&b)[2], const
         g.c[j] = ex2_ftz(y.h) * fmaf(y.l, 0.693147f, 1.f);
         g.w[j] = ex2_ftz((last.h - y.h) + (last.l - y.l)) * b[i];
         g.b[j] = b[i];
+        g.f[j] = b[i] * (ex2_ftz(-y.h) * fmaf(y.l, -0.693147f, 1.f));
     }
+    // sums of logs of gates <= 1 fall; any other order of a block's sums takes the general path
+    const bool fast = __all_sync(0xffffffffu, lg[0] <= 0.f && lg[1] <= 0.f && last.h > -60.f);
+    if (lane == 31) g.fast = fast ? 1.f : 0.f;
     if (lane == 31) g.cC = ex2_ftz(last.h) * fmaf(last.l, 0.693147f, 1.f);
 }
 
 // T = (I + A)^-1 in place, for A [64][64] strictly lower triangular with zeros above (row pitch
-// kAP), by the kInner threads of the T warps: the four diagonal blocks of 16 by forward
-// substitution, a thread for each column, then twice [[T1, 0], [-T2 A21 T1, T2]].
-template <int SZ> __device__ __forceinline__ void merge_blocks(float *A, int t) {
-    constexpr int RT = SZ / 16, PER = SZ * SZ / 4 / RT;   // rows of a thread (x 4 columns), threads a pair
+// kAP), by the 64 threads of a T group: the four diagonal blocks of 16 by forward substitution, a
+// thread for each column, then twice [[T1, 0], [-T2 A21 T1, T2]].
+template <int SZ> __device__ __forceinline__ void merge_blocks(float *A, int t, int bar) {
+    constexpr int RT = SZ / 8, PER = SZ * SZ / 4 / RT;   // rows of a thread (x 4 columns), threads a pair
     const int pair = t / PER, q = t % PER;
     const int r = q / (SZ / 4) * RT, c = q % (SZ / 4) * 4;
     float *T1 = A + pair * 2 * SZ * (kAP + 1), *A21 = T1 + SZ * kAP, *T2 = A21 + SZ;
 #pragma unroll 1
     for (int step = 0; step < 2; ++step) {   // A21 <- A21 T1, then A21 <- -T2 A21
-        const float *L = step ? T2 : A21, *Rm = step ? A21 : T1;
+        const float *L = (step ? T2 : A21) + r * kAP, *Rm = (step ? A21 : T1) + c;
         float acc[RT][4];
 #pragma unroll
         for (int i = 0; i < RT; ++i)
 #pragma unroll
             for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
-#pragma unroll 1
+#pragma unroll 2
         for (int m = 0; m < SZ; m += 4) {
             float l[RT][4];
 #pragma unroll
             for (int i = 0; i < RT; ++i)
-                *reinterpret_cast<float4 *>(l[i]) = *reinterpret_cast<const float4 *>(L + (r + i) * kAP + m);
+                *reinterpret_cast<float4 *>(l[i]) = *reinterpret_cast<const float4 *>(L + i * kAP + m);
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                const float4 x = *reinterpret_cast<const float4 *>(Rm + (m + k) * kAP + c);
+                const float4 x = *reinterpret_cast<const float4 *>(Rm + (m + k) * kAP);
 #pragma unroll
                 for (int i = 0; i < RT; ++i) {
                     acc[i][0] = fmaf(l[i][k], x.x, acc[i][0]);
@@ -184,42 +194,61 @@ template <int SZ> __device__ __forceinline__ void merge_blocks(float *A, int t) 
                 }
             }
         }
-        named_bar(kBarInner, kInner);
+        named_bar(bar, kInner);
         const float sg = step ? -1.f : 1.f;
 #pragma unroll
         for (int i = 0; i < RT; ++i)
             *reinterpret_cast<float4 *>(A21 + (r + i) * kAP + c) =
                 make_float4(sg * acc[i][0], sg * acc[i][1], sg * acc[i][2], sg * acc[i][3]);
-        named_bar(kBarInner, kInner);
+        named_bar(bar, kInner);
     }
 }
-__device__ __forceinline__ void invert_unit_lower(float *A, int t) {
+__device__ __forceinline__ void invert_unit_lower(float *A, int t, int bar) {
     float *blk = A + (t >> 4) * 16 * (kAP + 1);
     const int c = t & 15;
     float x[16];
-    if (t < 64) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            float v = i == c ? 1.f : 0.f;
+    for (int i = 0; i < 16; ++i) {
+        float v = i == c ? 1.f : 0.f, w = 0.f;
 #pragma unroll
-            for (int j = 0; j < i; j += 4) {
-                const float4 a = *reinterpret_cast<const float4 *>(blk + i * kAP + j);
-                v = fmaf(-a.x, x[j], v);
-                if (j + 1 < i) v = fmaf(-a.y, x[j + 1], v);
-                if (j + 2 < i) v = fmaf(-a.z, x[j + 2], v);
-                if (j + 3 < i) v = fmaf(-a.w, x[j + 3], v);
-            }
-            x[i] = v;
+        for (int j = 0; j < i; j += 4) {
+            const float4 a = *reinterpret_cast<const float4 *>(blk + i * kAP + j);
+            v = fmaf(-a.x, x[j], v);
+            if (j + 1 < i) w = fmaf(-a.y, x[j + 1], w);
+            if (j + 2 < i) v = fmaf(-a.z, x[j + 2], v);
+            if (j + 3 < i) w = fmaf(-a.w, x[j + 3], w);
         }
+        x[i] = v + w;
     }
-    named_bar(kBarInner, kInner);
-    if (t < 64) {
+    named_bar(bar, kInner);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) blk[i * kAP + c] = x[i];
+    for (int i = 0; i < 16; ++i) blk[i * kAP + c] = x[i];
+    named_bar(bar, kInner);
+    merge_blocks<16>(A, t, bar);
+    merge_blocks<32>(A, t, bar);
+}
+
+// x_j = D_ij b_j s_j for 16 columns j0.. of row i (s: 16 scores; LD: still in flight from TMEM).
+template <bool LD>
+__device__ __forceinline__ void decayed16(const Gates &G, int i, int j0, const uint32_t (&s)[16], float (&x)[16]) {
+    if (G.fast != 0.f) {   // c_i (b_j / c_j)
+        const float c = G.c[i];
+        load16(&G.f[j0], x);
+        if (LD) tmem_wait_ld();
+#pragma unroll
+        for (int j = 0; j < 16; ++j) x[j] = c * x[j] * u2f(s[j]);
+    } else {
+        const float hi = G.hi[i], lo = G.lo[i];
+        float y[16];
+        load16(&G.hi[j0], x);
+        load16(&G.lo[j0], y);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) x[j] = ex2_ftz((hi - x[j]) + (lo - y[j]));
+        load16(&G.b[j0], y);
+        if (LD) tmem_wait_ld();
+#pragma unroll
+        for (int j = 0; j < 16; ++j) x[j] = x[j] * y[j] * u2f(s[j]);
     }
-    named_bar(kBarInner, kInner);
-    merge_blocks<16>(A, t);
-    merge_blocks<32>(A, t);
 }
 
 __device__ __forceinline__ uint64_t desc_k(uint32_t addr) { return smem_desc(addr, 16, 1024, kSwizzle128B); }
@@ -239,16 +268,17 @@ __device__ __forceinline__ void mma_rows(uint32_t leader, uint32_t d, uint32_t a
 // SAVE: the backward's first pass -- writes e and the state before every block (and the last one)
 // instead of y; warps 12-15 are not launched.
 template <int D, int DV, bool SAVE>
-__global__ void __launch_bounds__(SAVE ? kChain + kInner : kChain + kInner + kOut, 1)
+__global__ void __launch_bounds__(kChain + 2 * kInner + (SAVE ? 0 : kOut), 1)
 delta_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
-                const __grid_constant__ CUtensorMap vmap, const DeltaTc p) {
+                const __grid_constant__ CUtensorMap vmap, const __grid_constant__ CUtensorMap ymap,
+                const DeltaTc p) {
     using Lay = DeltaLay<D, DV>;
     extern __shared__ uint8_t smem_raw[];
     // aligned by an offset, so that the compiler still sees shared memory
     uint8_t *sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     DeltaSmall &S = *reinterpret_cast<DeltaSmall *>(sm + Lay::oSmall);
-    uint8_t *sKQ = sm + Lay::oKQ, *sV = sm + Lay::oV, *sT = sm + Lay::oT, *sP = sm + Lay::oP;
-    float *sA = reinterpret_cast<float *>(sm + Lay::oA);
+    uint8_t *sKQ = sm + Lay::oKQ, *sV = sm + Lay::oV, *sT = sm + Lay::oT, *sP = sm + Lay::oP,
+            *sY = sm + Lay::oY;
     // warp-uniform to the compiler too
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const int bh = blockIdx.x, b = bh / p.H, h = bh - b * p.H, hk = h / p.group;
@@ -261,12 +291,12 @@ delta_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
         for (int i = 0; i < 2; ++i) {
             mbar_init(&S.v_full[i], 1);
             mbar_init(&S.t_ready[i], kInner);
+            mbar_init(&S.g_ready[i], 32);
             mbar_init(&S.t_free[i], 1);
-            mbar_init(&S.drain[i], 1);
         }
+        for (int i = 0; i < 3; ++i) mbar_init(&S.drain[i], 1);
         mbar_init(&S.kk_full, 1);
-        mbar_init(&S.kk_read, SAVE ? 64 : 128);   // a thread for each row of K, and of Q
-        mbar_init(&S.g_ready, 32);
+        mbar_init(&S.kk_read, SAVE ? kInner : 2 * kInner);   // a thread for each row of K, and of Q
         mbar_init(&S.p_ready, 64);
         mbar_init(&S.ks_done, 1);
         mbar_init(&S.qs_done, 1);
@@ -306,8 +336,9 @@ delta_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
             uint8_t *dst = sKQ + (n % kStages) * Lay::kKQ;
 #pragma unroll
             for (int f = 0; f < D / 64; ++f) {
-                tma_load_4d(dst + f * 16384, &kmap, bar, f * 64, n * kDC, hk, b);
-                if (!SAVE) tma_load_4d(dst + f * 16384 + 8192, &qmap, bar, f * 64, n * kDC, hk, b);
+                tma_load_4d(dst + f * 16384 + (n & 1) * 8192, &kmap, bar, f * 64, n * kDC, hk, b);
+                if (!SAVE)
+                    tma_load_4d(dst + f * 16384 + (~n & 1) * 8192, &qmap, bar, f * 64, n * kDC, hk, b);
             }
         };
         auto load_v = [&](int n) {
@@ -319,8 +350,7 @@ delta_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
             for (int f = 0; f < DV / 64; ++f)
                 tma_load_4d(dst + f * 8192, &vmap, bar, f * 64, n * kDC, h, b);
         };
-        const uint32_t leader = warp == 0 ? elect_leader() : 0u;
-        if (leader) {
+        if (warp == 0 && elect_leader()) {   // always the same lane: it keeps the counts
             for (int n = 0; n < kStages && n < nblk; ++n) {
                 load_kq(n);
                 if (n < 2) load_v(n);
@@ -360,7 +390,7 @@ delta_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
         bool failed = any_failed(false);
 
         for (int n = 0; n < nblk && !failed; ++n) {
-            const uint32_t kq = smem_u32(sKQ) + (n % kStages) * Lay::kKQ;
+            const uint32_t kk = smem_u32(sKQ) + (n % kStages) * Lay::kKQ + (n & 1) * 8192;   // K
             const Gates &G = S.gates[n & 3];
             bool ok = true;
             if (warp == 0) {
@@ -368,19 +398,13 @@ delta_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
                 if (!SAVE && n > 0) ok = ok && mbar_wait<1>(&S.o_read, (n - 1) & 1, g, 2);
                 ok = __all_sync(0xffffffffu, ok);
                 if (ok) {
+                    const uint32_t leader = elect_leader();
                     tc_fence_after();
                     // small pieces first: the accumulator truncates, relative to what it holds
 #pragma unroll 1
                     for (int pc = 2; pc >= 0; --pc)
-                        mma_rows<D / 16, 16384>(leader, tb + kColKS, tb + kColSP + pc * (D / 2), kq, i64, pc < 2);
+                        mma_rows<D / 16, 16384>(leader, tb + kColKS, tb + kColSP + pc * (D / 2), kk, i64, pc < 2);
                     mma_commit_if(leader, &S.ks_done);
-                    if (!SAVE) {
-#pragma unroll 1
-                        for (int pc = 1; pc >= 0; --pc)
-                            mma_rows<D / 16, 16384>(leader, tb + kColQS, tb + kColSP + pc * (D / 2), kq + 8192,
-                                                    i64, pc < 1);
-                        mma_commit_if(leader, &S.qs_done);
-                    }
                 }
             }
             // ---- r = v - c . (K S)
@@ -393,7 +417,6 @@ delta_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
                 // v of token j: chunk (row / 8) ^ (j % 8) of the token's 128-byte row
                 const uint8_t *tv = sV + (n & 1) * Lay::kV + (row >> 6) * 8192 + half * 32 * 128 + (row & 7) * 2;
                 const uint32_t ch = (uint32_t)(row & 63) >> 3;
-                if (!SAVE) ok = __all_sync(0xffffffffu, mbar_wait<1>(&S.qs_done, n & 1, g, 6));
 #pragma unroll 1
                 for (int u = 0; u < 2; ++u) {
                     const int j0 = half * 32 + u * 16;
@@ -421,6 +444,7 @@ delta_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
             if ((failed = any_failed(!ok))) break;
             // ---- e = T r
             if (warp == 0) {
+                const uint32_t leader = elect_leader();
                 tc_fence_after();
                 const uint32_t t = smem_u32(sT) + (n & 1) * Lay::kT;
                 // the pieces (r, T) whose product is above 2^-24 of the whole, small ones first:
@@ -432,6 +456,13 @@ delta_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
                 }
                 mma_commit_if(leader, &S.e_done);
                 mma_commit_if(leader, &S.t_free[n & 1]);
+                if (!SAVE) {
+                    const uint32_t qq = smem_u32(sKQ) + (n % kStages) * Lay::kKQ + (~n & 1) * 8192;
+#pragma unroll 1
+                    for (int pc = 1; pc >= 0; --pc)
+                        mma_rows<D / 16, 16384>(leader, tb + kColQS, tb + kColSP + pc * (D / 2), qq, i64, pc < 1);
+                    mma_commit_if(leader, &S.qs_done);
+                }
                 if (leader && n + 2 < nblk) load_v(n + 2);   // every thread has read this block's v
                 __syncwarp();
             }
@@ -449,11 +480,42 @@ delta_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
                         split3(w[2 * i] * u2f(acc[2 * i]), w[2 * i + 1] * u2f(acc[2 * i + 1]), hi[i], mi[i], lo[i]);
+                    if (!SAVE && u == 0) {   // W takes the place of the state's pieces
+                        ok = __all_sync(0xffffffffu, mbar_wait<1>(&S.qs_done, n & 1, g, 6));
+                        if (!ok) break;
+                    }
                     const uint32_t col = tb + lb + kColW + j0 / 2;
                     tmem_st8(col, hi);
                     tmem_st8(col + 32, mi);
                     tmem_st8(col + 64, lo);
+                }
+                tmem_wait_st();
+                tc_fence_before();
+            }
+            if ((failed = any_failed(!ok))) break;
+            // ---- S' = c_C S + K^T W
+            if (warp == 0) {
+                const uint32_t leader = elect_leader();
+                tc_fence_after();
+                const uint64_t kd = smem_desc(kk, 16384, 1024, kSwizzle128B);
+#pragma unroll 1
+                for (int pc = 2; pc >= 0; --pc)
+#pragma unroll
+                    for (int ks = 0; ks < kDC / 16; ++ks)
+                        mma_ts_if(leader, tb + kColSD, tb + kColW + pc * 32 + ks * 8, kd + ks * 128, iS,
+                                  pc < 2 || ks > 0);
+                mma_commit_if(leader, &S.s_done);
+            }
+            // ---- e once more: for y's second part, P e, or to the workspace
+            if (live) {
+#pragma unroll 1
+                for (int u = 0; u < 2; ++u) {
+                    const int j0 = half * 32 + u * 16;
+                    uint32_t acc[16];
+                    tmem_ld16(tb + lb + kColKS + j0, acc);
+                    tmem_wait_ld();
                     if (!SAVE) {
+                        uint32_t hi[8], mi[8];
 #pragma unroll
                         for (int i = 0; i < 8; ++i) split2(u2f(acc[2 * i]), u2f(acc[2 * i + 1]), hi[i], mi[i]);
                         const uint32_t ce = tb + lb + kColE + j0 / 2;
@@ -470,21 +532,12 @@ delta_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
                 tmem_wait_st();
                 tc_fence_before();
             }
-            if ((failed = any_failed(!ok))) break;
-            // ---- S' = c_C S + K^T W, y's second part
-            if (warp == 0) {
-                tc_fence_after();
-                const uint64_t kd = smem_desc(kq, 16384, 1024, kSwizzle128B);
-#pragma unroll 1
-                for (int pc = 2; pc >= 0; --pc)
-#pragma unroll
-                    for (int ks = 0; ks < kDC / 16; ++ks)
-                        mma_ts_if(leader, tb + kColSD, tb + kColW + pc * 32 + ks * 8, kd + ks * 128, iS,
-                                  pc < 2 || ks > 0);
-                mma_commit_if(leader, &S.s_done);
-                if (!SAVE) {
+            if (!SAVE) {
+                if ((failed = any_failed(false))) break;
+                if (warp == 0) {
                     ok = __all_sync(0xffffffffu, mbar_wait<1>(&S.p_ready, n & 1, g, 8));
                     if (ok) {
+                        const uint32_t leader = elect_leader();
                         tc_fence_after();
                         const uint32_t sp = smem_u32(sP);
 #pragma unroll 1
@@ -501,25 +554,27 @@ delta_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
             ok = __all_sync(0xffffffffu, ok);
             // this block's K and Q have been read: [K; Q] K^T before T was ready, Q S before r
             if (warp == 0 && ok && n + kStages < nblk) {
-                if (leader) load_kq(n + kStages);
+                if (elect_leader()) load_kq(n + kStages);
                 __syncwarp();
             }
             if (ok && live) {
                 tc_fence_after();
-                const float cC = G.cC;
+                const uint64_t cC2 = f2pack(G.cC, G.cC);
 #pragma unroll
                 for (int i = 0; i < SC; i += 16) {
                     uint32_t acc[16];
                     tmem_ld16(tb + lb + kColSD + half * SC + i, acc);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) st[i + j] = fmaf(cC, st[i + j], u2f(acc[j]));
+                    for (int j = 0; j < 16; j += 2)
+                        f2unpack(f2fma(cC2, f2pack(st[i + j], st[i + j + 1]), f2pack(u2f(acc[j]), u2f(acc[j + 1]))),
+                                 st[i + j], st[i + j + 1]);
                     // SP is free: W, the last operand there, has been read
                     if (n + 1 < nblk && SAVE) put_state(i);
                 }
                 if (!SAVE && n + 1 < nblk) {
-                    // the pieces of e lie in SP too: wait for P e
-                    ok = __all_sync(0xffffffffu, mbar_wait<1>(&S.pu_done, n & 1, g, 10));
+                    // at D = 128 the pieces of e lie in SP too: wait for P e
+                    if (D > 64) ok = __all_sync(0xffffffffu, mbar_wait<1>(&S.pu_done, n & 1, g, 10));
                     tc_fence_after();
                     if (ok) {
 #pragma unroll
@@ -535,7 +590,7 @@ delta_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
             failed = any_failed(!ok);
         }
         if (!failed && live && p.S_out) write_state(p.S_out + sbase);
-        if (leader) {
+        if (warp == 0 && elect_leader()) {
             mma_commit(&S.drain[0]);
             drain_wait(&S.drain[0], 0, g.limit_ns);
             if (S.abort_flag) {   // let the copies in flight land
@@ -550,8 +605,11 @@ delta_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
     } else if (warp < 12) {
         // ------------------------------------------------------------ T, ahead of the chain
         const TokenRows rs = token_rows(p.layout, b, h, p.H, p.N, 1);
-        const int t = tid - kChain;
-        float bv[2], gv[2];   // warp 10: the next block's beta and log gates
+        const int grp = (warp - 8) >> 1, t = tid - kChain - grp * kInner, bar = kBarInner + grp;
+        uint8_t *sTg = sT + grp * Lay::kT;
+        float *A = reinterpret_cast<float *>(sTg);
+        const bool gates_warp = (warp & 1) != 0;
+        float bv[2], gv[2];   // gates warp: the next block's beta and log gates
         auto fetch = [&](int n) {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
@@ -560,163 +618,196 @@ delta_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
                 gv[i] = tok < p.N && p.lg ? p.lg[rs.at(tok)] : 0.f;
             }
         };
-        if (warp == 10) fetch(0);
-        const uint32_t leader = warp == 8 ? elect_leader() : 0u;
-        for (int n = 0; n < nblk; ++n) {
-            // gates[n & 3] was last read for block n - 4, which the chain and the output have left:
-            // T n - 3 has been used, and that block's K S waited for y n - 4 to be read
+        auto any_out = [&](bool f) {
+            uint32_t r;
+            asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+                         "bar.red.or.pred q, %2, %3, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+                         : "=r"(r) : "r"((uint32_t)f), "r"(bar), "n"(kInner) : "memory");
+            return __any_sync(0xffffffffu, r != 0) != 0;
+        };
+        if (gates_warp) fetch(grp);
+        for (int n = grp; n < nblk; n += 2) {
+            // T n - 2 has been used: its place is free, and so are gates[n & 3], whose last reader
+            // is y n - 4 (block n - 2's K S waited for y n - 3)
             Gates &G = S.gates[n & 3];
-            bool ok = true;
-            if (warp == 8) {
-                ok = mbar_wait<1>(&S.kq_full[n % kStages], (n / kStages) & 1, g, 20);
-                if (n > 0) ok = ok && mbar_wait<1>(&S.kk_read, (n - 1) & 1, g, 24);
+            bool ok = n < 2 || mbar_wait<1>(&S.t_free[grp], ((n >> 1) - 1) & 1, g, 23);
+            // the block before's [K; Q] K^T and gates have been read
+            if (n > 0) ok = ok && mbar_wait<1>(&S.kk_read, (n - 1) & 1, g, 24);
+            if (!gates_warp) {
+                ok = ok && mbar_wait<1>(&S.kq_full[n % kStages], (n / kStages) & 1, g, 20);
                 ok = __all_sync(0xffffffffu, ok);
                 if (ok) {
+                    const uint32_t leader = elect_leader();
                     tc_fence_after();
-                    const uint64_t kd = desc_k(smem_u32(sKQ) + (n % kStages) * Lay::kKQ);
+                    const uint32_t base = smem_u32(sKQ) + (n % kStages) * Lay::kKQ;
+                    const uint64_t ad = desc_k(base), kd = desc_k(base + grp * 8192);
 #pragma unroll
                     for (int ks = 0; ks < D / 16; ++ks) {
-                        const uint64_t d = kd + (uint32_t)(((ks >> 2) * 16384 + (ks & 3) * 32) >> 4);
-                        mma_ss_if(leader, tb + kColKK, d, d, i64, ks > 0);
+                        const uint32_t o = ((ks >> 2) * 16384 + (ks & 3) * 32) >> 4;
+                        mma_ss_if(leader, tb + kColKK, ad + o, kd + o, i64, ks > 0);
                     }
                     mma_commit_if(leader, &S.kk_full);
                 }
-            }
-            if (warp == 10) {
-                // not ahead of a reader of the block before's gates (it arrives at kk_read after them)
-                ok = n == 0 || mbar_wait<1>(&S.kk_read, (n - 1) & 1, g, 28);
+            } else {
                 ok = __all_sync(0xffffffffu, ok);
                 if (ok) {
                     block_gates(G, bv, gv, lane);
-                    mbar_arrive(&S.g_ready);
-                    if (n + 1 < nblk) fetch(n + 1);
+                    mbar_arrive(&S.g_ready[grp]);
+                    if (n + 2 < nblk) fetch(n + 2);
                 }
             }
-            if (row < 64) {   // A_ij = D_ij (k_i . k_j) b_j, j < i
-                ok = ok && mbar_wait<1>(&S.g_ready, n & 1, g, 25);
-                ok = ok && mbar_wait<1>(&S.kk_full, n & 1, g, 21);
-                ok = __all_sync(0xffffffffu, ok);
-                if (ok) {
-                    tc_fence_after();
-                    const float hi = G.hi[row], lo = G.lo[row];
-#pragma unroll 1
-                    for (int j0 = 0; j0 < kDC; j0 += 16) {
-                        uint32_t acc[16];
-                        float x[16], y[16];
-                        tmem_ld16(tb + lb + kColKK + j0, acc);
-                        load16(&G.hi[j0], x);
-                        load16(&G.lo[j0], y);
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) x[j] = ex2_ftz((hi - x[j]) + (lo - y[j]));
-                        load16(&G.b[j0], y);
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) x[j] = j0 + j < row ? x[j] * y[j] * u2f(acc[j]) : 0.f;
-#pragma unroll
-                        for (int j = 0; j < 16; j += 4)
-                            *reinterpret_cast<float4 *>(sA + row * kAP + j0 + j) =
-                                make_float4(x[j], x[j + 1], x[j + 2], x[j + 3]);
-                    }
-                    tc_fence_before();
-                    mbar_arrive(&S.kk_read);
-                }
-            }
-            if (__any_sync(0xffffffffu, group_any<kBarInner, kInner>(!ok))) break;   // A complete
-            invert_unit_lower(sA, t);
-            ok = n < 2 || mbar_wait<1>(&S.t_free[n & 1], ((n >> 1) - 1) & 1, g, 23);
+            ok = ok && mbar_wait<1>(&S.g_ready[grp], (n >> 1) & 1, g, 25);
+            ok = ok && mbar_wait<1>(&S.kk_full, n & 1, g, 21);
             ok = __all_sync(0xffffffffu, ok);
-            if (ok) {
-                uint8_t *dst = sT + (n & 1) * Lay::kT;
-                const int i = t >> 1;
+            if (ok) {   // A_ij = D_ij (k_i . k_j) b_j, j < i
+                tc_fence_after();
 #pragma unroll 1
-                for (int q = (t & 1) * 4, e = q + 4; q < e; ++q) {   // 8 columns
-                    float x[8];
-                    *reinterpret_cast<float4 *>(x) = *reinterpret_cast<const float4 *>(sA + i * kAP + 8 * q);
-                    *reinterpret_cast<float4 *>(x + 4) = *reinterpret_cast<const float4 *>(sA + i * kAP + 8 * q + 4);
-                    uint32_t hi[4], mi[4], lo[4];
+                for (int j0 = 0; j0 < kDC; j0 += 16) {
+                    float x[16];
+                    if (j0 >= (t | 31)) {   // warp-uniform: above the diagonal
 #pragma unroll
-                    for (int e2 = 0; e2 < 4; ++e2) split3(x[2 * e2], x[2 * e2 + 1], hi[e2], mi[e2], lo[e2]);
-                    const uint32_t o = sw128_off(i, 8 * q);
-                    *reinterpret_cast<uint4 *>(dst + o) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                    *reinterpret_cast<uint4 *>(dst + 8192 + o) = make_uint4(mi[0], mi[1], mi[2], mi[3]);
-                    *reinterpret_cast<uint4 *>(dst + 16384 + o) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                        for (int j = 0; j < 16; ++j) x[j] = 0.f;
+                    } else {
+                        uint32_t acc[16];
+                        tmem_ld16(tb + lb + kColKK + j0, acc);
+                        decayed16<true>(G, t, j0, acc, x);
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) x[j] = j0 + j < t ? x[j] : 0.f;
+                    }
+#pragma unroll
+                    for (int j = 0; j < 16; j += 4)
+                        *reinterpret_cast<float4 *>(A + t * kAP + j0 + j) =
+                            make_float4(x[j], x[j + 1], x[j + 2], x[j + 3]);
                 }
-                fence_proxy_async();
-                mbar_arrive(&S.t_ready[n & 1]);
+                tc_fence_before();
+                mbar_arrive(&S.kk_read);
             }
-            if (__any_sync(0xffffffffu, group_any<kBarInner, kInner>(!ok))) break;   // A may be written again
+            if (any_out(!ok)) break;   // A complete
+            invert_unit_lower(A, t, bar);
+            // T's pieces over A: a thread's row is in registers before any is written
+            float x[kDC];
+#pragma unroll
+            for (int j = 0; j < kDC; j += 4)
+                *reinterpret_cast<float4 *>(x + j) = *reinterpret_cast<const float4 *>(A + t * kAP + j);
+            named_bar(bar, kInner);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+                uint32_t hi[4], mi[4], lo[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) split3(x[8 * q + 2 * e], x[8 * q + 2 * e + 1], hi[e], mi[e], lo[e]);
+                const uint32_t o = sw128_off(t, 8 * q);
+                *reinterpret_cast<uint4 *>(sTg + o) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                *reinterpret_cast<uint4 *>(sTg + 8192 + o) = make_uint4(mi[0], mi[1], mi[2], mi[3]);
+                *reinterpret_cast<uint4 *>(sTg + 16384 + o) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            }
+            fence_proxy_async();
+            mbar_arrive(&S.t_ready[grp]);
         }
-        if (leader) {
-            mma_commit(&S.drain[1]);
-            drain_wait(&S.drain[1], 0, g.limit_ns);
+        if (!gates_warp && elect_leader()) {
+            mma_commit(&S.drain[1 + grp]);
+            drain_wait(&S.drain[1 + grp], 0, g.limit_ns);
         }
         __syncwarp();
     } else {
         // ------------------------------------------------------------ P and y
-        const TokenRows rv = token_rows(p.layout, b, h, p.H, p.N, DV);
-        for (int n = 0; n < nblk; ++n) {
-            const Gates &G = S.gates[n & 3];
-            bool ok = true;
-            if (row >= 64) {   // P_ij = D_ij (q_i . k_j) b_j, j <= i; the previous P was used before y n - 1
-                const int i = row & 63;
-                ok = mbar_wait<1>(&S.g_ready, n & 1, g, 26) && mbar_wait<1>(&S.kk_full, n & 1, g, 27);
-                if (!__all_sync(0xffffffffu, ok)) break;
+        constexpr int kBarOut = kBarInner + 2;
+        // P_ij = D_ij (q_i . k_j) b_j, j <= i, by the warps whose lanes hold the rows of Q.  The scores
+        // of the next block are read before the wait for this block's P e, so that [K; Q] K^T can
+        // move on; P itself follows y, its place being free then.
+        uint32_t sc[4][16];
+        auto rows_of_q = [&](int n) { return (row >> 6) != (n & 1); };
+        auto read_scores = [&](int n) {
+            // the gates' phase too before arriving at kk_read, which lets the next block's gates come
+            const bool ok = __all_sync(0xffffffffu, mbar_wait<1>(&S.g_ready[n & 1], (n >> 1) & 1, g, 26) &&
+                                                        mbar_wait<1>(&S.kk_full, n & 1, g, 27));
+            if (ok) {
                 tc_fence_after();
-                const float ghi = G.hi[i], glo = G.lo[i];
-#pragma unroll 1
-                for (int j0 = 0; j0 < kDC; j0 += 16) {
-                    uint32_t acc[16], hi[8], mi[8];
-                    float x[16], y[16];
-                    tmem_ld16(tb + lb + kColKK + j0, acc);
-                    load16(&G.hi[j0], x);
-                    load16(&G.lo[j0], y);
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) x[j] = ex2_ftz((ghi - x[j]) + (glo - y[j]));
-                    load16(&G.b[j0], y);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) x[j] = j0 + j <= i ? x[j] * y[j] * u2f(acc[j]) : 0.f;
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) split2(x[2 * j], x[2 * j + 1], hi[j], mi[j]);
-#pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        const uint32_t o = sw128_off(i, j0 + 8 * q);
-                        *reinterpret_cast<uint4 *>(sP + o) =
-                            make_uint4(hi[4 * q], hi[4 * q + 1], hi[4 * q + 2], hi[4 * q + 3]);
-                        *reinterpret_cast<uint4 *>(sP + 8192 + o) =
-                            make_uint4(mi[4 * q], mi[4 * q + 1], mi[4 * q + 2], mi[4 * q + 3]);
-                    }
-                }
+                for (int u = 0; u < 4; ++u) tmem_ld16(tb + lb + kColKK + 16 * u, sc[u]);
+                tmem_wait_ld();
                 tc_fence_before();
                 mbar_arrive(&S.kk_read);
-                fence_proxy_async();
-                mbar_arrive(&S.p_ready);
             }
-            ok = mbar_wait<1>(&S.pu_done, n & 1, g, 30);
-            if (!__all_sync(0xffffffffu, ok)) break;
+            return ok;
+        };
+        auto make_p = [&](int n) {
+            const Gates &G = S.gates[n & 3];
+            const int i = row & 63;
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                uint32_t hi[8], mi[8];
+                float x[16];
+                decayed16<false>(G, i, 16 * u, sc[u], x);
+#pragma unroll
+                for (int j = 0; j < 16; ++j) x[j] = 16 * u + j <= i ? x[j] : 0.f;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) split2(x[2 * j], x[2 * j + 1], hi[j], mi[j]);
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    const uint32_t o = sw128_off(i, 16 * u + 8 * q);
+                    *reinterpret_cast<uint4 *>(sP + o) =
+                        make_uint4(hi[4 * q], hi[4 * q + 1], hi[4 * q + 2], hi[4 * q + 3]);
+                    *reinterpret_cast<uint4 *>(sP + 8192 + o) =
+                        make_uint4(mi[4 * q], mi[4 * q + 1], mi[4 * q + 2], mi[4 * q + 3]);
+                }
+            }
+            fence_proxy_async();
+            mbar_arrive(&S.p_ready);
+        };
+        bool good = true;
+        if (rows_of_q(0)) {
+            good = read_scores(0);
+            if (good) make_p(0);
+        }
+        for (int n = 0; n < nblk; ++n) {
+            const Gates &G = S.gates[n & 3];
+            bool ok = good;
+            const bool next = n + 1 < nblk && rows_of_q(n + 1);
+            if (next) ok = ok && read_scores(n + 1);
+            ok = ok && mbar_wait<1>(&S.pu_done, n & 1, g, 30);
+            ok = __all_sync(0xffffffffu, ok);
+            if (tid == kChain + 2 * kInner) bulk_wait_read<0>();   // the last y has left its tile
+            if (__any_sync(0xffffffffu, group_any<kBarOut, kOut>(!ok))) break;
             tc_fence_after();
-            if (row < DV) {   // y = c . (Q S) + P e
-                const int n_in = p.N - n * kDC;
-                __nv_bfloat16 *dst = p.y + rv.at(n * kDC) + row;
+            if (row < DV) {   // y = c . (Q S) + P e, 16 rows x 32 tokens at a time, through shared memory
+                const int tq = (lane & 3) * 2;
 #pragma unroll 1
-                for (int j0 = 0; j0 < kDC; j0 += 16) {
-                    uint32_t qs[16], pe[16];
-                    float c[16];
-                    tmem_ld16(tb + lb + kColQS + j0, qs);
-                    tmem_ld16(tb + lb + kColKS + j0, pe);
-                    load16(&G.c[j0], c);
+                for (int it = 0; it < 4; ++it) {
+                    const int j0 = (it & 1) * 32, hl = it >> 1;
+                    const uint32_t ta = tb + lb + ((uint32_t)hl << 20) + j0;
+                    uint32_t qs[16], pe[16], o[8];
+                    tmem_ld_16x256b_x4(ta + kColQS, qs);
+                    tmem_ld_16x256b_x4(ta + kColKS, pe);
+                    float2 c[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) c[k] = *reinterpret_cast<const float2 *>(&G.c[j0 + 8 * k + tq]);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        if (j0 + j < n_in)
-                            *dst = __float2bfloat16_rn(fmaf(c[j], u2f(qs[j]), u2f(pe[j])));
-                        dst += rv.step;
+                    for (int k = 0; k < 8; ++k) {   // rows lane / 4 and + 8, tokens tq and + 1 of group k / 2
+                        const float2 ck = c[k >> 1];
+                        o[k] = pack_bf16x2(fmaf(ck.x, u2f(qs[2 * k]), u2f(pe[2 * k])),
+                                           fmaf(ck.y, u2f(qs[2 * k + 1]), u2f(pe[2 * k + 1])));
                     }
+                    // matrices (group, row half): lane 8 m + i addresses token i of group m / 2, chunk m % 2
+                    const int dv0 = wq * 32 + hl * 16 + ((lane >> 3) & 1) * 8, tok = j0 + (lane >> 4) * 8 + (lane & 7);
+                    const uint32_t at = smem_u32(sY) + (dv0 >> 6) * 8192 + sw128_off(tok, dv0 & 63);
+                    stmatrix_x4_trans(at, o[0], o[1], o[2], o[3]);
+                    stmatrix_x4_trans(at + 16 * 128, o[4], o[5], o[6], o[7]);
                 }
                 tc_fence_before();
             }
             mbar_arrive(&S.o_read);
+            fence_proxy_async();
+            named_bar(kBarOut, kOut);
+            if (tid == kChain + 2 * kInner) {
+#pragma unroll
+                for (int f = 0; f < DV / 64; ++f) tma_store_4d(&ymap, sY + f * 8192, f * 64, n * kDC, h, b);
+                bulk_commit();
+            }
+            if (next) make_p(n + 1);
         }
+        if (tid == kChain + 2 * kInner) bulk_wait<0>();
+        __syncwarp();
     }
     tc_fence_before();
     __syncthreads();
@@ -742,13 +833,13 @@ bool encode_tokens(CUtensorMap *m, const void *base, int layout, int B, int head
 }
 
 template <int D, int DV, bool SAVE> cudaError_t launch_tc(const DeltaArgs &a) {
-    CUtensorMap qm, km, vm;
+    CUtensorMap qm, km, vm, ym{};
     if (!encode_tokens(&qm, a.q, a.layout, a.B, a.Hk, a.N, D) ||
         !encode_tokens(&km, a.k, a.layout, a.B, a.Hk, a.N, D) ||
-        !encode_tokens(&vm, a.v, a.layout, a.B, a.H, a.N, DV))
+        !encode_tokens(&vm, a.v, a.layout, a.B, a.H, a.N, DV) ||
+        (!SAVE && !encode_tokens(&ym, a.y, a.layout, a.B, a.H, a.N, DV)))
         return cudaErrorInvalidValue;
     DeltaTc p{};
-    p.y = static_cast<__nv_bfloat16 *>(a.y);
     p.beta = a.beta; p.lg = a.log_gate;
     p.H = a.H; p.group = a.H / a.Hk; p.N = a.N; p.layout = a.layout; p.nblk = delta_blocks(a.N);
     p.S_in = a.S_in; p.S_out = a.S_out;
@@ -768,7 +859,7 @@ template <int D, int DV, bool SAVE> cudaError_t launch_tc(const DeltaArgs &a) {
     static_assert(smem <= 232448, "shared memory of a CTA");
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    kern<<<a.B * a.H, SAVE ? kChain + kInner : kChain + kInner + kOut, smem, a.stream>>>(qm, km, vm, p);
+    kern<<<a.B * a.H, kChain + 2 * kInner + (SAVE ? 0 : kOut), smem, a.stream>>>(qm, km, vm, ym, p);
     return cudaGetLastError();
 }
 

@@ -177,6 +177,22 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap *m, const void *s
         "r"(smem_u32(src)), "r"(x), "r"(y), "r"(z)
         : "memory");
 }
+__device__ __forceinline__ void tma_store_4d(const CUtensorMap *m, const void *src, int x, int y,
+                                             int z, int w) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4, %5}], [%1];" ::
+            "l"(reinterpret_cast<uint64_t>(m)),
+        "r"(smem_u32(src)), "r"(x), "r"(y), "r"(z), "r"(w)
+        : "memory");
+}
+// Four 8 x 8 matrices of 16-bit values, each stored transposed: lane 8 m + i gives the address of
+// the 16-byte row that column i of matrix m becomes.
+__device__ __forceinline__ void stmatrix_x4_trans(uint32_t addr, uint32_t a, uint32_t b, uint32_t c,
+                                                  uint32_t d) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a),
+                 "r"(b), "r"(c), "r"(d)
+                 : "memory");
+}
 __device__ __forceinline__ void bulk_commit() {
     asm volatile("cp.async.bulk.commit_group;" ::: "memory");
 }
@@ -257,8 +273,9 @@ __device__ __forceinline__ void mma_commit(uint64_t *bar) {
 }
 
 // The same three issued by a whole converged warp, by its one lane with `leader` set: the warp's
-// control flow stays uniform, so addresses and descriptors live in uniform registers (inside a
-// branch of one lane every operand is moved there for every MMA, 80 to 120 cycles each).
+// control flow stays uniform, so addresses and descriptors live in uniform registers.  `leader`
+// has to come from an elect_leader() in the same branch: 30 cycles per M = 128, N = 64 MMA, the rate
+// of the pipe; 61 with the election made earlier and kept, 80 to 120 in a branch of one lane.
 __device__ __forceinline__ uint32_t elect_leader() {
     uint32_t r;
     asm volatile(
