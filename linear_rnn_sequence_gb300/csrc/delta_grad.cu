@@ -7,7 +7,7 @@
 //   dq_i = c_i S dy_i + sum_{j<=i} D_ij (dy_i . u_j) k_j
 //   dk_j = D_Cj G u_j - b_j c_j S du_j + sum_{i>=j} D_ij (dy_i . u_j) q_i
 //          - sum_{i>j} b_i D_ij (du_i . u_j) k_i - sum_{i<j} b_j D_ji (du_j . u_i) k_i
-//   db_j = du_j . e_j
+//   dv_j = b_j du_j,   db_j = du_j . e_j
 //   dlog a_j = <G, S'> + sum_{i>=j} (q_i . dq_i - v_i . dv_i)
 // (S' the state after the block; the last line holds because scaling the
 // state after token j scales what every later token reads of it, and what
@@ -27,7 +27,7 @@ constexpr int kP = kDeltaC + 4;   // padded row of the transposed stages
 struct GradParams {
     const void *q, *k, *v, *dy;
     const float *beta, *lg;
-    void *dq, *dk;
+    void *dq, *dk, *dvg;
     float *dbeta, *dlg;
     const float *S_ck, *G_ck, *e, *du;
     int H, Hk, N, dv, layout;
@@ -119,6 +119,7 @@ __global__ void __launch_bounds__(kThr) delta_grad_kernel(const GradParams p) {
                     du = p.du[(bh * p.N + t0 + t) * p.dv + c0 + c];
                 }
                 s.dyT[c][t] = x; s.eT[c][t] = e; s.duT[c][t] = du;
+                if (t < n) ((T *)p.dvg)[rv.at(t0 + t) + c0 + c] = from_f<T>(s.b[t] * du);
                 float db = e * du;
                 float vd = t < n && p.lg ? s.b[t] * du * to_f(v[rv.at(t0 + t) + c0 + c]) : 0.f;
 #pragma unroll
@@ -259,7 +260,7 @@ __global__ void __launch_bounds__(kThr) delta_grad_kernel(const GradParams p) {
 
 template <int D, typename T> cudaError_t launch_grad(const DeltaArgs &a) {
     const DeltaBwdWs w = delta_bwd_ws(a);
-    const GradParams p{a.q, a.k, a.v, a.dy, a.beta, a.log_gate, a.dq, a.dk, a.dbeta, a.dlog_gate,
+    const GradParams p{a.q, a.k, a.v, a.dy, a.beta, a.log_gate, a.dq, a.dk, a.dv_grad, a.dbeta, a.dlog_gate,
                        w.S, w.G, w.e, w.du, a.H, a.Hk, a.N, a.dv, (int)a.layout};
     const size_t smem = sizeof(GradSmem<D>);
     cudaError_t e = cudaFuncSetAttribute(delta_grad_kernel<D, T>,
@@ -286,7 +287,8 @@ size_t delta_backward_workspace(const DeltaArgs &a) {
 
 cudaError_t launch_delta_backward(const DeltaArgs &a) {
     cudaError_t e = delta_tc_supported(a) ? launch_delta_states_tc(a) : launch_delta_states_simt(a);
-    if (e == cudaSuccess) e = launch_delta_reverse_simt(a);
+    if (e == cudaSuccess)
+        e = delta_tc_supported(a) ? launch_delta_reverse_tc(a) : launch_delta_reverse_simt(a);
     if (e != cudaSuccess) return e;
     return a.dt == LA_DTYPE_BF16 ? launch_grad_t<__nv_bfloat16>(a) : launch_grad_t<float>(a);
 }

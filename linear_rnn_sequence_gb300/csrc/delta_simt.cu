@@ -20,7 +20,7 @@ constexpr int kTile = 16;      // tokens staged in shared memory at a time
 
 struct DeltaSimt {
     const void *q, *k, *v, *dy;
-    void *y, *dv_grad;
+    void *y;
     const float *beta, *lg;
     int H, Hk, N, dv, layout;
     const float *S_in;
@@ -143,7 +143,7 @@ __global__ void __launch_bounds__(kThr) delta_forward_kernel(const DeltaSimt p) 
     if (!SAVE && p.S_out) keep(p.S_out + bh * st);
 }
 
-// Backwards through the tokens: G <- a (I - b k k^T)(G + q dy^T), du = (G + q dy^T)^T k, dv = b du.
+// Backwards through the tokens: G <- a (I - b k k^T)(G + q dy^T), du = (G + q dy^T)^T k.
 template <int D, typename T>
 __global__ void __launch_bounds__(kThr) delta_reverse_kernel(const DeltaSimt p) {
     constexpr int R = D / 8;
@@ -205,9 +205,7 @@ __global__ void __launch_bounds__(kThr) delta_reverse_kernel(const DeltaSimt p) 
         __syncthreads();
         for (int i = tid; i < n * kCols; i += kThr) {
             const int t = i / kCols, c = i % kCols;
-            const float du = os[t][c];
-            p.du[((size_t)bh * p.N + t0 + t) * p.dv + c0 + c] = du;
-            ((T *)p.dv_grad)[rv.at(t0 + t) + c0 + c] = from_f<T>(bs[t] * du);
+            p.du[((size_t)bh * p.N + t0 + t) * p.dv + c0 + c] = os[t][c];
         }
     }
     if (p.dS_in) keep(p.dS_in + bh * st);
@@ -216,7 +214,7 @@ __global__ void __launch_bounds__(kThr) delta_reverse_kernel(const DeltaSimt p) 
 DeltaSimt params(const DeltaArgs &a) {
     DeltaSimt p{};
     p.q = a.q; p.k = a.k; p.v = a.v; p.dy = a.dy;
-    p.y = a.y; p.dv_grad = a.dv_grad;
+    p.y = a.y;
     p.beta = a.beta; p.lg = a.log_gate;
     p.H = a.H; p.Hk = a.Hk; p.N = a.N; p.dv = a.dv; p.layout = a.layout;
     p.S_in = a.S_in; p.S_out = a.S_out;
