@@ -286,9 +286,13 @@ size_t delta_backward_workspace(const DeltaArgs &a) {
 }
 
 cudaError_t launch_delta_backward(const DeltaArgs &a) {
-    cudaError_t e = delta_tc_supported(a) ? launch_delta_states_tc(a) : launch_delta_states_simt(a);
-    if (e == cudaSuccess)
-        e = delta_tc_supported(a) ? launch_delta_reverse_tc(a) : launch_delta_reverse_simt(a);
+    if (delta_tc_supported(a)) {
+        cudaError_t e = launch_delta_states_tc(a);
+        if (e == cudaSuccess) e = launch_delta_reverse_tc(a);
+        return e == cudaSuccess ? launch_delta_grad_tc(a) : e;
+    }
+    cudaError_t e = launch_delta_states_simt(a);
+    if (e == cudaSuccess) e = launch_delta_reverse_simt(a);
     if (e != cudaSuccess) return e;
     return a.dt == LA_DTYPE_BF16 ? launch_grad_t<__nv_bfloat16>(a) : launch_grad_t<float>(a);
 }

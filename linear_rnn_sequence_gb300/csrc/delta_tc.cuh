@@ -31,11 +31,11 @@ __device__ __forceinline__ void split3(float x0, float x1, uint32_t &h, uint32_t
     f2unpack(f2sub(f2pack(r0, r1), f2pack(u2f(b0 & 0xFFFF0000u), u2f(b1 & 0xFFFF0000u))), r0, r1);
     l = __byte_perm(f2u(r0), f2u(r1), 0x7632);
 }
+// Two pieces, each rounded to nearest: 2^-18 of x is left.
 __device__ __forceinline__ void split2(float x0, float x1, uint32_t &h, uint32_t &m) {
-    const uint32_t a0 = f2u(x0), a1 = f2u(x1);
-    h = __byte_perm(a0, a1, 0x7632);
+    h = pack_bf16x2(x0, x1);
     float r0, r1;
-    f2unpack(f2sub(f2pack(x0, x1), f2pack(u2f(a0 & 0xFFFF0000u), u2f(a1 & 0xFFFF0000u))), r0, r1);
+    f2unpack(f2sub(f2pack(x0, x1), f2pack(bf16_lo_f(h), bf16_hi_f(h))), r0, r1);
     m = pack_bf16x2(r0, r1);
 }
 __device__ __forceinline__ uint64_t f2fma(uint64_t a, uint64_t b, uint64_t c) {

@@ -174,6 +174,7 @@ bool delta_tc_supported(const DeltaArgs &a);
 cudaError_t launch_delta_forward_tc(const DeltaArgs &a);
 cudaError_t launch_delta_states_tc(const DeltaArgs &a);
 cudaError_t launch_delta_reverse_tc(const DeltaArgs &a);
+cudaError_t launch_delta_grad_tc(const DeltaArgs &a);
 size_t delta_backward_workspace(const DeltaArgs &a);
 cudaError_t launch_delta_backward(const DeltaArgs &a);
 cudaError_t launch_delta_step(const DeltaArgs &a);
