@@ -682,7 +682,7 @@ la_status la_layer_norm(const void *x, void *y, const float *weight, const float
 
 size_t la_layer_norm_backward_workspace_bytes(long long rows, int D, la_dtype dt) {
     if (rows < 1 || check_norm(&dt, &dt, rows, D, dt) != LA_OK) return 0;
-    return sizeof(WsHeader) + layer_norm_partials(rows, D, dt) * 4;
+    return layer_norm_partials(rows, D, dt) * 4;
 }
 
 la_status la_layer_norm_backward(const void *dy, const void *x, const float *mean, const float *rstd,
@@ -712,12 +712,11 @@ la_status la_layer_norm_backward(const void *dy, const void *x, const float *mea
     const Buf whole[] = {{x, n}, {dy, n}};
     const Buf rest[] = {{grad_weight, nd}, {grad_bias, nd}, {sums ? workspace : nullptr, need}};
     if (clash(in, out) || clash(whole, rest)) return LA_ERR_INVALID_ARG;
-    if (sums && cudaMemsetAsync(workspace, 0, sizeof(WsHeader), s) != cudaSuccess) return LA_ERR_CUDA;
     LayerNormArgs a{};
     a.x = x; a.dy = dy; a.dx = grad_x; a.weight = weight;
     a.mean = const_cast<float *>(mean); a.rstd = const_cast<float *>(rstd);
     a.dweight = grad_weight; a.dbias = grad_bias;
-    a.partials = sums ? reinterpret_cast<float *>(static_cast<char *>(workspace) + sizeof(WsHeader)) : nullptr;
+    a.partials = sums ? static_cast<float *>(workspace) : nullptr;
     a.rows = rows; a.D = D; a.dt = dt; a.stream = s;
     return from_cuda(launch_layer_norm_backward(a));
 }

@@ -19,21 +19,28 @@ namespace {
 // E elements of T moved at once.
 template <typename T, int E> struct Vec;
 template <typename T> struct Vec<T, 1> {
-    static __device__ __forceinline__ void load(const T *p, float (&x)[1]) { x[0] = to_f(*p); }
+    using Raw = T;
+    static __device__ __forceinline__ Raw load(const T *p) { return *p; }
+    static __device__ __forceinline__ Raw zero() { return from_f<T>(0.f); }
+    static __device__ __forceinline__ void unpack(Raw r, float (&x)[1]) { x[0] = to_f(r); }
     static __device__ __forceinline__ void store(T *p, const float (&x)[1]) { *p = from_f<T>(x[0]); }
 };
 template <> struct Vec<float, 4> {
-    static __device__ __forceinline__ void load(const float *p, float (&x)[4]) {
-        const float4 f = *reinterpret_cast<const float4 *>(p);
-        x[0] = f.x; x[1] = f.y; x[2] = f.z; x[3] = f.w;
+    using Raw = float4;
+    static __device__ __forceinline__ Raw load(const float *p) { return *reinterpret_cast<const float4 *>(p); }
+    static __device__ __forceinline__ Raw zero() { return make_float4(0.f, 0.f, 0.f, 0.f); }
+    static __device__ __forceinline__ void unpack(Raw r, float (&x)[4]) {
+        x[0] = r.x; x[1] = r.y; x[2] = r.z; x[3] = r.w;
     }
     static __device__ __forceinline__ void store(float *p, const float (&x)[4]) {
         *reinterpret_cast<float4 *>(p) = make_float4(x[0], x[1], x[2], x[3]);
     }
 };
 template <> struct Vec<__nv_bfloat16, 8> {
-    static __device__ __forceinline__ void load(const __nv_bfloat16 *p, float (&x)[8]) {
-        const uint4 w = *reinterpret_cast<const uint4 *>(p);
+    using Raw = uint4;
+    static __device__ __forceinline__ Raw load(const __nv_bfloat16 *p) { return *reinterpret_cast<const uint4 *>(p); }
+    static __device__ __forceinline__ Raw zero() { return make_uint4(0u, 0u, 0u, 0u); }
+    static __device__ __forceinline__ void unpack(Raw w, float (&x)[8]) {
         const unsigned u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -48,21 +55,27 @@ template <> struct Vec<__nv_bfloat16, 8> {
     }
 };
 
-// Sum over the G threads of a row: shuffles within a warp, then shared memory.
-// A row takes two sums through two `red` arrays in turn, so that the barrier
-// of one also orders the other's reads before its next writes.
-template <int G> __device__ __forceinline__ float row_sum(float x, float *red) {
+// Sums over the G threads of a row, for RW rows at once: shuffles within a
+// warp, then shared memory.  `red` alternates between two places, so that one
+// barrier a sum is enough.
+template <int G, int RW> __device__ __forceinline__ void row_sums(float (&x)[RW], float (*red)[RW]) {
     constexpr int W = G < 32 ? G : 32;
 #pragma unroll
-    for (int o = W / 2; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-    if (G > 32) {
-        if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = x;
-        __syncthreads();
-        x = 0.f;
+    for (int o = W / 2; o > 0; o >>= 1)
 #pragma unroll
-        for (int w = 0; w < G / 32; ++w) x += red[w];
+        for (int i = 0; i < RW; ++i) x[i] += __shfl_xor_sync(0xffffffffu, x[i], o);
+    if (G > 32) {
+        if ((threadIdx.x & 31) == 0)
+#pragma unroll
+            for (int i = 0; i < RW; ++i) red[threadIdx.x >> 5][i] = x[i];
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < RW; ++i) x[i] = 0.f;
+#pragma unroll
+        for (int w = 0; w < G / 32; ++w)
+#pragma unroll
+            for (int i = 0; i < RW; ++i) x[i] += red[w][i];
     }
-    return x;
 }
 
 struct LnParams {
@@ -76,113 +89,178 @@ struct LnParams {
     float eps;
 };
 
-// V vectors of E elements per thread; column of element j of vector i: (i * G + lane) * E + j.
-template <typename T, int E, int V, int G, int THR>
+// G threads share a row and have V vectors of E elements of it; column of element j of vector i:
+// (i * G + lane) * E + j.  RW rows of each group are in flight at once.
+template <typename T, int E, int V, int G, int RW, int THR>
 __global__ void __launch_bounds__(THR) layer_norm_kernel(const LnParams p) {
     constexpr int RPB = THR / G;
-    __shared__ float red[2][32];
-    const int lane = threadIdx.x % G, D = p.D;
+    constexpr bool kKeep = V * E <= 16;   // weight and bias stay in registers
+    __shared__ float red[2][32][RW];
+    const int lane = threadIdx.x % G, grp = threadIdx.x / G, D = p.D;
     const float invD = 1.f / (float)D;
     const T *x = (const T *)p.x;
     T *y = (T *)p.y;
-    for (long long r0 = (long long)blockIdx.x * RPB; r0 < p.rows; r0 += (long long)gridDim.x * RPB) {
-        const long long r = r0 + threadIdx.x / G;
-        const bool in = r < p.rows;
-        float v[V][E];
-        float sum = 0.f;
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const int c = (i * G + lane) * E;
-            if (in && c < D) {
-                Vec<T, E>::load(x + r * D + c, v[i]);
-            } else {
-#pragma unroll
-                for (int j = 0; j < E; ++j) v[i][j] = 0.f;
-            }
-#pragma unroll
-            for (int j = 0; j < E; ++j) sum += v[i][j];
-        }
-        const float mean = row_sum<G>(sum, red[0]) * invD;
-        float sq = 0.f;
+    float w[kKeep ? V : 1][E], bi[kKeep ? V : 1][E];
+    if (kKeep) {
 #pragma unroll
         for (int i = 0; i < V; ++i)
-            if ((i * G + lane) * E < D)
-#pragma unroll
-                for (int j = 0; j < E; ++j) {
-                    const float d = v[i][j] - mean;
-                    sq = fmaf(d, d, sq);
-                }
-        const float var = row_sum<G>(sq, red[1]) * invD;
-        const float rstd = 1.f / sqrtf(var + p.eps);
-        if (in && lane == 0 && p.mean) {
-            p.mean[r] = mean;
-            p.rstd[r] = rstd;
-        }
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const int c = (i * G + lane) * E;
-            if (!in || c >= D) continue;
-            float o[E];
 #pragma unroll
             for (int j = 0; j < E; ++j) {
-                o[j] = (v[i][j] - mean) * rstd;
-                if (p.weight) o[j] *= p.weight[c + j];
-                if (p.bias) o[j] += p.bias[c + j];
+                const int c = (i * G + lane) * E + j;
+                w[i][j] = p.weight && c < D ? p.weight[c] : 1.f;
+                bi[i][j] = p.bias && c < D ? p.bias[c] : 0.f;
             }
-            Vec<T, E>::store(y + r * D + c, o);
+    }
+    for (long long r0 = (long long)blockIdx.x * RPB * RW; r0 < p.rows; r0 += (long long)gridDim.x * RPB * RW) {
+        typename Vec<T, E>::Raw raw[RW][V];
+        float s[RW], mean[RW];
+#pragma unroll
+        for (int k = 0; k < RW; ++k) {
+            const long long r = r0 + k * RPB + grp;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const int c = (i * G + lane) * E;
+                raw[k][i] = r < p.rows && c < D ? Vec<T, E>::load(x + r * D + c) : Vec<T, E>::zero();
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < RW; ++k) {
+            s[k] = 0.f;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                float v[E];
+                Vec<T, E>::unpack(raw[k][i], v);
+#pragma unroll
+                for (int j = 0; j < E; ++j) s[k] += v[j];
+            }
+        }
+        row_sums<G, RW>(s, red[0]);
+#pragma unroll
+        for (int k = 0; k < RW; ++k) {
+            mean[k] = s[k] * invD;
+            s[k] = 0.f;
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                if ((i * G + lane) * E < D) {
+                    float v[E];
+                    Vec<T, E>::unpack(raw[k][i], v);
+#pragma unroll
+                    for (int j = 0; j < E; ++j) s[k] = fmaf(v[j] - mean[k], v[j] - mean[k], s[k]);
+                }
+        }
+        row_sums<G, RW>(s, red[1]);
+#pragma unroll
+        for (int k = 0; k < RW; ++k) {
+            const long long r = r0 + k * RPB + grp;
+            if (r >= p.rows) continue;
+            const float rstd = 1.f / sqrtf(fmaf(s[k], invD, p.eps));
+            if (lane == 0 && p.mean) {
+                p.mean[r] = mean[k];
+                p.rstd[r] = rstd;
+            }
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const int c = (i * G + lane) * E;
+                if (c >= D) continue;
+                float v[E];
+                Vec<T, E>::unpack(raw[k][i], v);
+#pragma unroll
+                for (int j = 0; j < E; ++j) {
+                    v[j] = (v[j] - mean[k]) * rstd;
+                    if (kKeep) {
+                        v[j] = fmaf(v[j], w[i][j], bi[i][j]);
+                    } else {
+                        if (p.weight) v[j] *= p.weight[c + j];
+                        if (p.bias) v[j] += p.bias[c + j];
+                    }
+                }
+                Vec<T, E>::store(y + r * D + c, v);
+            }
         }
     }
 }
 
-template <typename T, int E, int V, int G, int THR>
+template <typename T, int E, int V, int G, int RW, int THR>
 __global__ void __launch_bounds__(THR) layer_norm_backward_kernel(const LnParams p) {
     constexpr int RPB = THR / G;
-    __shared__ float red[2][32];
+    constexpr bool kKeep = V * E <= 16;
+    __shared__ float red[2][32][2 * RW];
     extern __shared__ float cols[];   // RPB > 1: the row groups' column sums, joined at the end
-    const int lane = threadIdx.x % G, D = p.D;
+    const int lane = threadIdx.x % G, grp = threadIdx.x / G, D = p.D;
     const float invD = 1.f / (float)D;
     const T *x = (const T *)p.x, *dy = (const T *)p.dy;
     T *dx = (T *)p.y;
-    float aw[V][E], ab[V][E];
+    float aw[V][E], ab[V][E], w[kKeep ? V : 1][E];
 #pragma unroll
     for (int i = 0; i < V; ++i)
 #pragma unroll
-        for (int j = 0; j < E; ++j) aw[i][j] = ab[i][j] = 0.f;
-    for (long long r0 = (long long)blockIdx.x * RPB; r0 < p.rows; r0 += (long long)gridDim.x * RPB) {
-        const long long r = r0 + threadIdx.x / G;
-        const bool in = r < p.rows;
-        const float mean = in ? p.mean[r] : 0.f, rstd = in ? p.rstd[r] : 0.f;
-        float xh[V][E], g[V][E], s1 = 0.f, s2 = 0.f;
+        for (int j = 0; j < E; ++j) {
+            aw[i][j] = ab[i][j] = 0.f;
+            const int c = (i * G + lane) * E + j;
+            if (kKeep) w[i][j] = p.weight && c < D ? p.weight[c] : 1.f;
+        }
+    int turn = 0;
+    for (long long r0 = (long long)blockIdx.x * RPB * RW; r0 < p.rows; r0 += (long long)gridDim.x * RPB * RW) {
+        typename Vec<T, E>::Raw rx[RW][V], ry[RW][V];
+        float mean[RW], rstd[RW], s[2 * RW];
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
+        for (int k = 0; k < RW; ++k) {
+            const long long r = r0 + k * RPB + grp;
+            const bool in = r < p.rows;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const int c = (i * G + lane) * E;
+                rx[k][i] = in && c < D ? Vec<T, E>::load(x + r * D + c) : Vec<T, E>::zero();
+                ry[k][i] = in && c < D ? Vec<T, E>::load(dy + r * D + c) : Vec<T, E>::zero();
+            }
+            mean[k] = in ? p.mean[r] : 0.f;
+            rstd[k] = in ? p.rstd[r] : 0.f;
+        }
+        // xh and g = dy weight of one vector; what lies behind the row or the last row adds nothing
+        // (dy = 0 there)
+        auto values = [&](int k, int i, float (&xh)[E], float (&g)[E], float (&d)[E]) {
+            Vec<T, E>::unpack(rx[k][i], xh);
+            Vec<T, E>::unpack(ry[k][i], d);
             const int c = (i * G + lane) * E;
-            if (in && c < D) {
-                Vec<T, E>::load(x + r * D + c, xh[i]);
-                Vec<T, E>::load(dy + r * D + c, g[i]);
+#pragma unroll
+            for (int j = 0; j < E; ++j) {
+                xh[j] = (xh[j] - mean[k]) * rstd[k];
+                g[j] = kKeep ? d[j] * w[i][j] : p.weight && c + j < D ? d[j] * p.weight[c + j] : d[j];
+            }
+        };
+#pragma unroll
+        for (int k = 0; k < RW; ++k) {
+            s[2 * k] = s[2 * k + 1] = 0.f;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                float xh[E], g[E], d[E];
+                values(k, i, xh, g, d);
 #pragma unroll
                 for (int j = 0; j < E; ++j) {
-                    xh[i][j] = (xh[i][j] - mean) * rstd;
-                    aw[i][j] = fmaf(g[i][j], xh[i][j], aw[i][j]);
-                    ab[i][j] += g[i][j];
-                    if (p.weight) g[i][j] *= p.weight[c + j];
-                    s1 += g[i][j];
-                    s2 = fmaf(g[i][j], xh[i][j], s2);
+                    s[2 * k] += g[j];
+                    s[2 * k + 1] = fmaf(g[j], xh[j], s[2 * k + 1]);
+                    aw[i][j] = fmaf(d[j], xh[j], aw[i][j]);
+                    ab[i][j] += d[j];
                 }
-            } else {
-#pragma unroll
-                for (int j = 0; j < E; ++j) xh[i][j] = g[i][j] = 0.f;
             }
         }
-        s1 = row_sum<G>(s1, red[0]) * invD;
-        s2 = row_sum<G>(s2, red[1]) * invD;
+        row_sums<G, 2 * RW>(s, red[turn]);
+        turn ^= 1;
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const int c = (i * G + lane) * E;
-            if (!in || c >= D) continue;
-            float o[E];
+        for (int k = 0; k < RW; ++k) {
+            const long long r = r0 + k * RPB + grp;
+            if (r >= p.rows) continue;
+            const float s1 = s[2 * k] * invD, s2 = s[2 * k + 1] * invD;
 #pragma unroll
-            for (int j = 0; j < E; ++j) o[j] = (g[i][j] - s1 - xh[i][j] * s2) * rstd;
-            Vec<T, E>::store(dx + r * D + c, o);
+            for (int i = 0; i < V; ++i) {
+                const int c = (i * G + lane) * E;
+                if (c >= D) continue;
+                float xh[E], g[E], d[E];
+                values(k, i, xh, g, d);
+#pragma unroll
+                for (int j = 0; j < E; ++j) d[j] = (g[j] - s1 - xh[j] * s2) * rstd[k];
+                Vec<T, E>::store(dx + r * D + c, d);
+            }
         }
     }
     if (!p.partials) return;
@@ -199,7 +277,7 @@ __global__ void __launch_bounds__(THR) layer_norm_backward_kernel(const LnParams
     }
     // row groups in their order
     constexpr int WID = V * G * E;
-    float *mine = cols + (size_t)(threadIdx.x / G) * 2 * WID;
+    float *mine = cols + (size_t)grp * 2 * WID;
 #pragma unroll
     for (int i = 0; i < V; ++i)
 #pragma unroll
@@ -255,20 +333,20 @@ int backward_ctas(long long rows, int rows_per_cta) {
 
 bool vec16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-template <typename T, int E, int V, int G, int THR>
+template <typename T, int E, int V, int G, int RW, int THR>
 cudaError_t go(const LayerNormArgs &a, bool backward) {
     LnParams p{a.x, a.dy, backward ? a.dx : a.y, a.weight, a.bias, a.mean, a.rstd, nullptr, a.rows, a.D,
                a.eps};
     constexpr int RPB = THR / G;
     if (!backward) {
-        const long long need = (a.rows + RPB - 1) / RPB, most = 16LL * sm_count();
-        layer_norm_kernel<T, E, V, G, THR><<<(unsigned)(need < most ? need : most), THR, 0, a.stream>>>(p);
+        const long long need = (a.rows + RPB * RW - 1) / (RPB * RW), most = 16LL * sm_count();
+        layer_norm_kernel<T, E, V, G, RW, THR><<<(unsigned)(need < most ? need : most), THR, 0, a.stream>>>(p);
         return cudaGetLastError();
     }
     p.partials = a.dweight || a.dbias ? a.partials : nullptr;
-    const int ctas = backward_ctas(a.rows, RPB);
+    const int ctas = backward_ctas(a.rows, RPB * RW);
     const size_t smem = RPB > 1 && p.partials ? sizeof(float) * RPB * 2 * V * G * E : 0;
-    layer_norm_backward_kernel<T, E, V, G, THR><<<ctas, THR, smem, a.stream>>>(p);
+    layer_norm_backward_kernel<T, E, V, G, RW, THR><<<ctas, THR, smem, a.stream>>>(p);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || !p.partials) return e;
     layer_norm_columns_kernel<<<dim3((a.D + 31) / 32, 2), 256, 0, a.stream>>>(a.partials, ctas, a.D,
@@ -276,24 +354,31 @@ cudaError_t go(const LayerNormArgs &a, bool backward) {
     return cudaGetLastError();
 }
 
-// The threads of a row and the vectors of a thread, by the number n of vectors in a row; f is called
-// with them as template arguments.
+// The threads of a row, the vectors of a thread and the rows in flight, by the number n of vectors in
+// a row.  Few rows want threads rather than rows in flight: one row of each group then (a row's
+// latency is what such a call takes).
+template <typename T, int E, int V, int G, int THR>
+cudaError_t rows_in_flight(const LayerNormArgs &a, bool bwd) {
+    constexpr int RW = V * E <= 8 ? 4 : V * E <= 16 ? 2 : 1;
+    if (RW == 1 || a.rows >= 4LL * RW * sm_count() * (THR / G)) return go<T, E, V, G, RW, THR>(a, bwd);
+    return go<T, E, V, G, 1, THR>(a, bwd);
+}
 template <typename T, int E> cudaError_t shape(const LayerNormArgs &a, bool bwd) {
     const int n = (a.D + E - 1) / E;
     if (E == 1) {
-        if (n <= 128) return go<T, E, 4, 32, 256>(a, bwd);
-        if (n <= 1024) return go<T, E, 4, 256, 256>(a, bwd);
-        if (n <= 4096) return go<T, E, 16, 256, 256>(a, bwd);
-        return go<T, E, 16, 1024, 1024>(a, bwd);
+        if (n <= 128) return rows_in_flight<T, E, 4, 32, 256>(a, bwd);
+        if (n <= 1024) return rows_in_flight<T, E, 4, 256, 256>(a, bwd);
+        if (n <= 4096) return rows_in_flight<T, E, 16, 256, 256>(a, bwd);
+        return rows_in_flight<T, E, 16, 1024, 1024>(a, bwd);
     }
-    if (n <= 16) return go<T, E, 1, 16, 256>(a, bwd);
-    if (n <= 32) return go<T, E, 1, 32, 256>(a, bwd);
-    if (n <= 64) return go<T, E, 2, 32, 256>(a, bwd);
-    if (n <= 256) return go<T, E, 1, 256, 256>(a, bwd);
-    if (n <= 512) return go<T, E, 2, 256, 256>(a, bwd);
-    if (n <= 1024) return go<T, E, 4, 256, 256>(a, bwd);
-    if (n <= 2048) return go<T, E, 2, 1024, 1024>(a, bwd);
-    return go<T, E, 4, 1024, 1024>(a, bwd);
+    if (n <= 16) return rows_in_flight<T, E, 1, 16, 256>(a, bwd);
+    if (n <= 32) return rows_in_flight<T, E, 1, 32, 256>(a, bwd);
+    if (n <= 64) return rows_in_flight<T, E, 2, 32, 256>(a, bwd);
+    if (n <= 256) return rows_in_flight<T, E, 1, 256, 256>(a, bwd);
+    if (n <= 512) return rows_in_flight<T, E, 2, 256, 256>(a, bwd);
+    if (n <= 1024) return rows_in_flight<T, E, 4, 256, 256>(a, bwd);
+    if (n <= 2048) return rows_in_flight<T, E, 2, 1024, 1024>(a, bwd);
+    return rows_in_flight<T, E, 4, 1024, 1024>(a, bwd);
 }
 
 template <typename T> cudaError_t run(const LayerNormArgs &a, bool bwd) {

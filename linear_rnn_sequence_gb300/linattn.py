@@ -48,6 +48,8 @@ def library_path() -> str:
 def lib():
     """Load (building first if the sources are newer) and return the ctypes library."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if _build.is_stale():
@@ -561,7 +563,7 @@ def _on_device(fn):
         t = args[0] if args else kw[first]
         if not t.is_cuda:
             raise ValueError("tensors must be CUDA tensors (no CPU fallback)")
-        if stream is None and t.device.index == torch.cuda.current_device():
+        if stream is None and t.get_device() == _current_device():
             return fn(*args, **kw)
         if stream is not None and stream.device != t.device:
             raise ValueError("the stream is of another device than the tensors")
@@ -570,32 +572,51 @@ def _on_device(fn):
     return call
 
 
-def _current_stream(t) -> int:
-    return torch.cuda.current_stream(t.device).cuda_stream
+# Small calls cost mostly this module's own time, so its checks read each property once.
+_current_device = torch.cuda.current_device
+
+
+def _current_stream(device_index) -> int:
+    return torch.cuda.current_stream(device_index).cuda_stream
 
 
 def _addr(t):
     return None if t is None else t.data_ptr()
 
 
-def _expect(name, t, shape, dtype, like):
-    """``t`` is None or a contiguous tensor of this shape and dtype on ``like``'s device."""
+def _expect(name, t, shape, dtype, device_index):
+    """Address of ``t``, which is None or a contiguous tensor of this shape and dtype on this device."""
     if t is None:
-        return
-    if t.shape != shape or t.dtype != dtype:
+        return None
+    if t.shape != shape or t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype} of shape {tuple(shape)}, not {t.dtype} of {tuple(t.shape)}")
-    if t.device != like.device:
-        raise ValueError(f"{name} is on {t.device}, not on {like.device}")
+    if t.get_device() != device_index:
+        raise ValueError(f"{name} is on {t.device}, not on cuda:{device_index}")
     if not t.is_contiguous():
         raise ValueError("tensors must be contiguous")
+    return t.data_ptr()
 
 
 def _workspace(workspace, need, like):
+    """(tensor, address, bytes) of the workspace; one is allocated when none is given."""
     if workspace is None:
-        return torch.empty(need, dtype=torch.uint8, device=like.device) if need else None, need
+        if not need:
+            return None, None, 0
+        workspace = torch.empty(need, dtype=torch.uint8, device=like.device)
+        return workspace, workspace.data_ptr(), need
     if workspace.device != like.device or not workspace.is_contiguous():
         raise ValueError("the workspace must be contiguous and on the tensors' device")
-    return workspace, workspace.numel() * workspace.element_size()
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+@functools.lru_cache(maxsize=1024)
+def _delta_bytes(*sizes):
+    return int(lib().la_delta_workspace_bytes(*sizes))
+
+
+@functools.lru_cache(maxsize=1024)
+def _delta_backward_bytes(*sizes):
+    return int(lib().la_delta_backward_workspace_bytes(*sizes))
 
 
 def _check_run_time(workspace, where):
@@ -605,21 +626,27 @@ def _check_run_time(workspace, where):
             raise LinAttnError(err, f"{where} (run time, wait site {site})")
 
 
-def _delta_sizes(q, k, v, beta, log_gate, layout):
-    """Checks the inputs of a delta-rule call; returns B, H, Hk, N, d, dv."""
+def _delta_inputs(q, k, v, beta, log_gate, layout):
+    """Checks the inputs of a delta-rule call: its sizes (B, H, Hk, N, d, dv, dtype code), the
+    device's index and the inputs' addresses."""
     if layout not in LAYOUT:
         raise ValueError(f"layout must be one of {sorted(LAYOUT)}")
-    if q.dim() != 4 or v.dim() != 4:
+    shape, vs = q.shape, v.shape
+    if len(shape) != 4 or len(vs) != 4:
         raise ValueError("q, k and v must have four dimensions")
-    n, h = (2, 1) if layout == "bhnd" else (1, 2)
-    B, Hk, N, d = q.shape[0], q.shape[h], q.shape[n], q.shape[3]
-    H, dv = v.shape[h], v.shape[3]
-    _expect("q", q, q.shape, q.dtype, q)
-    _expect("k", k, q.shape, q.dtype, q)
-    _expect("v", v, (B, H, N, dv) if layout == "bhnd" else (B, N, H, dv), q.dtype, q)
-    _expect("beta", beta, v.shape[:3], torch.float32, q)
-    _expect("log_gate", log_gate, v.shape[:3], torch.float32, q)
-    return B, H, Hk, N, d, dv
+    if layout == "bhnd":
+        B, Hk, N, d = shape
+        H, dv = vs[1], vs[3]
+        vshape = (B, H, N, dv)
+    else:
+        B, N, Hk, d = shape
+        H, dv = vs[2], vs[3]
+        vshape = (B, N, H, dv)
+    dev, dt = q.get_device(), q.dtype
+    at = (_expect("q", q, shape, dt, dev), _expect("k", k, shape, dt, dev), _expect("v", v, vshape, dt, dev),
+          _expect("beta", beta, vshape[:3], torch.float32, dev),
+          _expect("log_gate", log_gate, vshape[:3], torch.float32, dev))
+    return (B, H, Hk, N, d, dv, _dtype_code(q)), dev, at
 
 
 @_on_device
@@ -633,23 +660,23 @@ def forward_delta(q, k, v, beta, log_gate=None, S_in=None, return_state=False, o
     them.  Returns y in v's shape and dtype (and the final state [B,H,d,dv], float32, when
     ``return_state``).  S_in: the initial state; S_out may be S_in.
     """
-    B, H, Hk, N, d, dv = _delta_sizes(q, k, v, beta, log_gate, layout)
-    dt = _dtype_code(q)
-    _expect("S_in", S_in, (B, H, d, dv), torch.float32, q)
-    _expect("S_out", S_out, (B, H, d, dv), torch.float32, q)
-    _expect("out", out, v.shape, v.dtype, q)
-    y = out if out is not None else torch.empty_like(v)
+    sizes, dev, (qa, ka, va, ba, la) = _delta_inputs(q, k, v, beta, log_gate, layout)
+    B, H, Hk, N, d, dv, dt = sizes
+    state = (B, H, d, dv)
+    if out is None:
+        out = torch.empty_like(v)
     if return_state and S_out is None:
-        S_out = torch.empty((B, H, d, dv), dtype=torch.float32, device=q.device)
-    L = lib()
-    workspace, wbytes = _workspace(workspace, L.la_delta_workspace_bytes(B, H, Hk, N, d, dv, dt), q)
-    st = L.la_forward_delta(_addr(q), _addr(k), _addr(v), _addr(y), _addr(beta), _addr(log_gate), B,
-                            H, Hk, N, d, dv, dt, LAYOUT[layout], _addr(S_in), _addr(S_out),
-                            _addr(workspace), wbytes, _current_stream(q))
+        S_out = torch.empty(state, dtype=torch.float32, device=q.device)
+    workspace, wa, wbytes = _workspace(workspace, _delta_bytes(*sizes), q)
+    st = lib().la_forward_delta(qa, ka, va, _expect("out", out, v.shape, v.dtype, dev), ba, la, B, H, Hk,
+                                N, d, dv, dt, LAYOUT[layout],
+                                _expect("S_in", S_in, state, torch.float32, dev),
+                                _expect("S_out", S_out, state, torch.float32, dev), wa, wbytes,
+                                _current_stream(dev))
     _raise(st, "la_forward_delta")
     if check_status:
         _check_run_time(workspace, "la_forward_delta")
-    return (y, S_out) if return_state else y
+    return (out, S_out) if return_state else out
 
 
 @_on_device
@@ -660,22 +687,20 @@ def backward_delta(q, k, v, beta, dy, log_gate=None, S_in=None, grad_S_out=None,
     grad_S_in): the first three in the inputs' dtype, the others float32; grad_log_gate is None
     without log_gate, grad_S_in is None unless S_in or grad_S_out is given.
     """
-    B, H, Hk, N, d, dv = _delta_sizes(q, k, v, beta, log_gate, layout)
-    dt = _dtype_code(q)
-    _expect("dy", dy, v.shape, v.dtype, q)
-    _expect("S_in", S_in, (B, H, d, dv), torch.float32, q)
-    _expect("grad_S_out", grad_S_out, (B, H, d, dv), torch.float32, q)
+    sizes, dev, (qa, ka, va, ba, la) = _delta_inputs(q, k, v, beta, log_gate, layout)
+    B, H, Hk, N, d, dv, dt = sizes
+    state = (B, H, d, dv)
     gq, gk, gv, gb = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v), torch.empty_like(beta)
     gl = None if log_gate is None else torch.empty_like(log_gate)
     gS = None
     if S_in is not None or grad_S_out is not None:
-        gS = torch.empty((B, H, d, dv), dtype=torch.float32, device=q.device)
-    L = lib()
-    workspace, wbytes = _workspace(workspace, L.la_delta_backward_workspace_bytes(B, H, Hk, N, d, dv, dt), q)
-    st = L.la_backward_delta(_addr(q), _addr(k), _addr(v), _addr(dy), _addr(beta), _addr(log_gate),
-                             _addr(gq), _addr(gk), _addr(gv), _addr(gb), _addr(gl), B, H, Hk, N, d,
-                             dv, dt, LAYOUT[layout], _addr(S_in), _addr(grad_S_out), _addr(gS),
-                             _addr(workspace), wbytes, _current_stream(q))
+        gS = torch.empty(state, dtype=torch.float32, device=q.device)
+    workspace, wa, wbytes = _workspace(workspace, _delta_backward_bytes(*sizes), q)
+    st = lib().la_backward_delta(qa, ka, va, _expect("dy", dy, v.shape, v.dtype, dev), ba, la, gq.data_ptr(),
+                                 gk.data_ptr(), gv.data_ptr(), gb.data_ptr(), _addr(gl), B, H, Hk, N, d, dv,
+                                 dt, LAYOUT[layout], _expect("S_in", S_in, state, torch.float32, dev),
+                                 _expect("grad_S_out", grad_S_out, state, torch.float32, dev), _addr(gS),
+                                 wa, wbytes, _current_stream(dev))
     _raise(st, "la_backward_delta")
     if check_status:
         _check_run_time(workspace, "la_backward_delta")
@@ -687,25 +712,23 @@ def decode_step_delta(q, k, v, beta, S, log_gate=None, S_out=None, out=None):
     """One token of ``forward_delta``: q, k [B,Hk,d]; v [B,H,dv]; beta, log_gate [B,H] float32;
     S [B,H,d,dv] float32, updated in place unless ``S_out`` is given.  Returns y [B,H,dv] in v's dtype.
     """
-    if q.dim() != 3 or v.dim() != 3:
+    shape, vs = q.shape, v.shape
+    if len(shape) != 3 or len(vs) != 3:
         raise ValueError("q, k and v must have three dimensions")
-    B, Hk, d = q.shape
-    H, dv = v.shape[1], v.shape[2]
-    dt = _dtype_code(q)
-    _expect("q", q, q.shape, q.dtype, q)
-    _expect("k", k, q.shape, q.dtype, q)
-    _expect("v", v, (B, H, dv), q.dtype, q)
-    _expect("beta", beta, (B, H), torch.float32, q)
-    _expect("log_gate", log_gate, (B, H), torch.float32, q)
-    _expect("S", S, (B, H, d, dv), torch.float32, q)
-    _expect("S_out", S_out, (B, H, d, dv), torch.float32, q)
-    _expect("out", out, v.shape, v.dtype, q)
-    y = out if out is not None else torch.empty_like(v)
-    st = lib().la_decode_step_delta(_addr(q), _addr(k), _addr(v), _addr(y), _addr(beta),
-                                    _addr(log_gate), _addr(S), _addr(S if S_out is None else S_out),
-                                    B, H, Hk, d, dv, dt, _current_stream(q))
+    B, Hk, d = shape
+    H, dv = vs[1], vs[2]
+    dev, dt, f32 = q.get_device(), q.dtype, torch.float32
+    if out is None:
+        out = torch.empty_like(v)
+    sa = _expect("S", S, (B, H, d, dv), f32, dev)
+    st = lib().la_decode_step_delta(_expect("q", q, shape, dt, dev), _expect("k", k, shape, dt, dev),
+                                    _expect("v", v, (B, H, dv), dt, dev), _expect("out", out, vs, dt, dev),
+                                    _expect("beta", beta, (B, H), f32, dev),
+                                    _expect("log_gate", log_gate, (B, H), f32, dev), sa,
+                                    sa if S_out is None else _expect("S_out", S_out, (B, H, d, dv), f32, dev),
+                                    B, H, Hk, d, dv, _dtype_code(q), _current_stream(dev))
     _raise(st, "la_decode_step_delta")
-    return y
+    return out
 
 
 @_on_device
@@ -713,21 +736,25 @@ def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, return_stats=False,
     """(x - mean) * rstd * weight + bias over the last dimension (at most 16384 values, bf16 or
     fp32); weight, bias: float32 [D] or None.  Returns y in x's dtype (and mean, rstd, float32 in
     x's shape without its last dimension, when ``return_stats``).  ``out`` may be x."""
-    D = x.shape[-1]
-    dt = _dtype_code(x)
-    _expect("x", x, x.shape, x.dtype, x)
-    _expect("weight", weight, (D,), torch.float32, x)
-    _expect("bias", bias, (D,), torch.float32, x)
-    _expect("out", out, x.shape, x.dtype, x)
-    y = out if out is not None else torch.empty_like(x)
+    shape, dev, f32 = x.shape, x.get_device(), torch.float32
+    D = shape[-1]
+    if out is None:
+        out = torch.empty_like(x)
     mean = rstd = None
     if return_stats:
-        mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+        mean = torch.empty(shape[:-1], dtype=f32, device=x.device)
         rstd = torch.empty_like(mean)
-    st = lib().la_layer_norm(_addr(x), _addr(y), _addr(weight), _addr(bias), _addr(mean), _addr(rstd),
-                             x.numel() // D if D else 0, D, dt, float(eps), _current_stream(x))
+    st = lib().la_layer_norm(_expect("x", x, shape, x.dtype, dev), _expect("out", out, shape, x.dtype, dev),
+                             _expect("weight", weight, (D,), f32, dev), _expect("bias", bias, (D,), f32, dev),
+                             _addr(mean), _addr(rstd), x.numel() // D if D else 0, D, _dtype_code(x),
+                             eps, _current_stream(dev))
     _raise(st, "la_layer_norm")
-    return (y, mean, rstd) if return_stats else y
+    return (out, mean, rstd) if return_stats else out
+
+
+@functools.lru_cache(maxsize=1024)
+def _norm_backward_bytes(rows, D, dt):
+    return int(lib().la_layer_norm_backward_workspace_bytes(rows, D, dt))
 
 
 @_on_device
@@ -735,24 +762,20 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, sums=None, workspace=Non
     """Gradients of ``layer_norm`` from its mean and rstd: (grad_x, grad_weight, grad_bias), the
     first in x's dtype, the sums float32 [D].  ``sums`` says whether to compute the latter two
     (default: when weight is given); they are None otherwise."""
-    D = x.shape[-1]
-    dt = _dtype_code(x)
-    _expect("x", x, x.shape, x.dtype, x)
-    _expect("dy", dy, x.shape, x.dtype, x)
-    _expect("mean", mean, x.shape[:-1], torch.float32, x)
-    _expect("rstd", rstd, x.shape[:-1], torch.float32, x)
-    _expect("weight", weight, (D,), torch.float32, x)
+    shape, dev, f32 = x.shape, x.get_device(), torch.float32
+    D, dt = shape[-1], _dtype_code(x)
     gx = torch.empty_like(x)
     rows = x.numel() // D if D else 0
-    gw = gb = None
+    gw = gb = wa = None
     wbytes = 0
-    L = lib()
     if weight is not None if sums is None else sums:
-        gw = torch.empty(D, dtype=torch.float32, device=x.device)
+        gw = torch.empty(D, dtype=f32, device=x.device)
         gb = torch.empty_like(gw)
-        workspace, wbytes = _workspace(workspace, L.la_layer_norm_backward_workspace_bytes(rows, D, dt), x)
-    st = L.la_layer_norm_backward(_addr(dy), _addr(x), _addr(mean), _addr(rstd), _addr(weight),
-                                  _addr(gx), _addr(gw), _addr(gb), rows, D, dt, _addr(workspace),
-                                  wbytes, _current_stream(x))
+        workspace, wa, wbytes = _workspace(workspace, _norm_backward_bytes(rows, D, dt), x)
+    st = lib().la_layer_norm_backward(_expect("dy", dy, shape, x.dtype, dev), _expect("x", x, shape, x.dtype, dev),
+                                      _expect("mean", mean, shape[:-1], f32, dev),
+                                      _expect("rstd", rstd, shape[:-1], f32, dev),
+                                      _expect("weight", weight, (D,), f32, dev), gx.data_ptr(), _addr(gw),
+                                      _addr(gb), rows, D, dt, wa, wbytes, _current_stream(dev))
     _raise(st, "la_layer_norm_backward")
     return gx, gw, gb
