@@ -557,9 +557,9 @@ extern "C" {
 
 size_t la_delta_workspace_bytes(int B, int H, int Hk, int N, int d, int dv, la_dtype dt) {
     if (check_delta(B, H, Hk, N, d, dv, dt) != LA_OK || N == 0) return 0;
-    return delta_on_tensor_cores(delta_args(nullptr, nullptr, nullptr, nullptr, nullptr, B, H, Hk, N, d,
-                                            dv, dt, LA_LAYOUT_BHND, nullptr, nullptr, nullptr))
-               ? sizeof(WsHeader) : 0;
+    const DeltaArgs a = delta_args(nullptr, nullptr, nullptr, nullptr, nullptr, B, H, Hk, N, d, dv, dt,
+                                   LA_LAYOUT_BHND, nullptr, nullptr, nullptr);
+    return delta_on_tensor_cores(a) ? delta_tc_workspace(a) : 0;
 }
 
 la_status la_forward_delta(const void *q, const void *k, const void *v, void *y, const float *beta,

@@ -45,9 +45,11 @@ constexpr uint32_t kColKK = 448;                // [K; Q] K^T or, for odd blocks
 struct DeltaTc {
     const float *beta, *lg;
     int H, group, N, layout, nblk;
-    const float *S_in;
-    float *S_out;
-    float *S_ck, *e;               // SAVE
+    int nseg, seg_blocks, parts;   // segments of a head, blocks of one, CTAs of one (kSegment)
+    const float *S_in;             // by (head, segment)
+    float *S_out;                  // by head
+    float *S_ck, *e;               // kSave
+    float *S_local, *Phi;          // kSegment, by (head, segment but the last)
     unsigned int *err, *err_where;
     unsigned long long limit_ns;
     int drop_item;
@@ -70,10 +72,18 @@ template <int D, int DV> struct DeltaLay {
     static constexpr int request = total + 1024;
 };
 
-// SAVE: the backward's first pass -- writes e and the state before every block (and the last one)
-// instead of y; warps 12-15 are not launched.
-template <int D, int DV, bool SAVE>
-__global__ void __launch_bounds__(kChain + 2 * kInner + (SAVE ? 0 : kOut), 1)
+// What a launch computes.
+enum DeltaMode {
+    kForward,   // y, from the initial state of each (head, segment)
+    kSave,      // the backward's first pass: e, and the state before every block and after the last
+    kSegment    // segments from an empty state (rows < dv), and the segments' maps of the state:
+                // S_end = Phi S_start + S_local, row dv + a being column a of Phi (from a unit state,
+                // without values); `parts` CTAs of 128 rows each
+};
+
+// Only kForward launches warps 12-15.
+template <int D, int DV, int MODE>
+__global__ void __launch_bounds__(kChain + 2 * kInner + (MODE == kForward ? kOut : 0), 1)
 delta_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                 const __grid_constant__ CUtensorMap vmap, const __grid_constant__ CUtensorMap ymap,
                 const DeltaTc p) {
@@ -86,8 +96,11 @@ delta_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
             *sY = sm + Lay::oY;
     // warp-uniform to the compiler too
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
-    const int bh = blockIdx.x, b = bh / p.H, h = bh - b * p.H, hk = h / p.group;
-    const int nblk = p.nblk;
+    constexpr bool Y = MODE == kForward, SAVE = MODE == kSave, SEG = MODE == kSegment;
+    const int part = SEG ? blockIdx.x % p.parts : 0, item = SEG ? blockIdx.x / p.parts : blockIdx.x;
+    const int segs = SEG ? p.nseg - 1 : p.nseg, bh = item / segs, seg = item - bh * segs;
+    const int b = bh / p.H, h = bh - b * p.H, hk = h / p.group;
+    const int blk0 = seg * p.seg_blocks, nblk = min(p.seg_blocks, p.nblk - blk0);   // blocks of this item
     const Guard g{&S.abort_flag, p.err, p.err_where, p.limit_ns};
 
     if (tid == 0) {
@@ -101,7 +114,7 @@ delta_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
         }
         for (int i = 0; i < 3; ++i) mbar_init(&S.drain[i], 1);
         mbar_init(&S.kk_full, 1);
-        mbar_init(&S.kk_read, SAVE ? kInner : 2 * kInner);   // a thread for each row of K, and of Q
+        mbar_init(&S.kk_read, Y ? 2 * kInner : kInner);   // a thread for each row of K, and of Q
         mbar_init(&S.p_ready, 64);
         mbar_init(&S.ks_done, 1);
         mbar_init(&S.qs_done, 1);
@@ -112,7 +125,7 @@ delta_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
         fence_mbar_init();
         prefetch_tmap(&kmap);
         prefetch_tmap(&vmap);
-        if (!SAVE) prefetch_tmap(&qmap);
+        if (Y) prefetch_tmap(&qmap);
     }
     if (warp == 0) {
         tmem_alloc(&S.tmem_base, 512);
@@ -130,20 +143,22 @@ delta_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
         // ------------------------------------------------------------ chain
         constexpr uint32_t iS = idesc_bf16(128, D, 0, 1);   // B = K, feature-major
         const int half = warp >> 2;
-        const bool live = row < DV;   // warp-uniform
+        // column of S, or (SEG) dv + column of Phi; warp-uniform what it is
+        const int col_of = part * 128 + row;
+        const bool live = col_of < (SEG ? DV + D : DV), values = col_of < DV;
         constexpr int SC = D / 2;     // state columns of a thread
         int kq_issued = 0, v_issued = 0;
         auto load_kq = [&](int n) {
             uint64_t *bar = &S.kq_full[n % kStages];
-            mbar_arrive_expect_tx(bar, (SAVE ? 1 : 2) * kDC * D * 2);
+            mbar_arrive_expect_tx(bar, (Y ? 2 : 1) * kDC * D * 2);
             ++kq_issued;
-            if (n == 0 && bh == p.drop_item) return;   // test hook: announced, never issued
+            if (n == 0 && (int)blockIdx.x == p.drop_item) return;   // test hook: announced, never issued
             uint8_t *dst = sKQ + (n % kStages) * Lay::kKQ;
 #pragma unroll
             for (int f = 0; f < D / 64; ++f) {
-                tma_load_4d(dst + f * 16384 + (n & 1) * 8192, &kmap, bar, f * 64, n * kDC, hk, b);
-                if (!SAVE)
-                    tma_load_4d(dst + f * 16384 + (~n & 1) * 8192, &qmap, bar, f * 64, n * kDC, hk, b);
+                tma_load_4d(dst + f * 16384 + (n & 1) * 8192, &kmap, bar, f * 64, (blk0 + n) * kDC, hk, b);
+                if (Y)
+                    tma_load_4d(dst + f * 16384 + (~n & 1) * 8192, &qmap, bar, f * 64, (blk0 + n) * kDC, hk, b);
             }
         };
         auto load_v = [&](int n) {
@@ -153,7 +168,7 @@ delta_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
             uint8_t *dst = sV + (n & 1) * Lay::kV;
 #pragma unroll
             for (int f = 0; f < DV / 64; ++f)
-                tma_load_4d(dst + f * 8192, &vmap, bar, f * 64, n * kDC, h, b);
+                tma_load_4d(dst + f * 8192, &vmap, bar, f * 64, (blk0 + n) * kDC, h, b);
         };
         if (warp == 0 && elect_leader()) {   // always the same lane: it keeps the counts
             for (int n = 0; n < kStages && n < nblk; ++n) {
@@ -164,14 +179,18 @@ delta_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
         __syncwarp();
         // the state, its column `row`, rows half * SC ..
         float st[SC];
-        const size_t sbase = (size_t)bh * D * DV + (size_t)half * SC * DV + row;
+        const size_t sbase = (size_t)item * D * DV + (size_t)half * SC * DV + row;
 #pragma unroll
         for (int i = 0; i < SC; ++i)
-            st[i] = live && p.S_in ? p.S_in[sbase + (size_t)i * DV] : 0.f;
-        auto write_state = [&](float *dst) {   // dst: this head's [D][DV], at row half * SC, column row
+            st[i] = SEG ? (half * SC + i == col_of - DV ? 1.f : 0.f)
+                        : live && p.S_in ? p.S_in[sbase + (size_t)i * DV] : 0.f;
+        auto write_state = [&](float *dst, int ld) {   // dst: a [D][ld] matrix, at row half * SC, a column
 #pragma unroll
-            for (int i = 0; i < SC; ++i) dst[(size_t)i * DV] = st[i];
+            for (int i = 0; i < SC; ++i) dst[(size_t)i * ld] = st[i];
         };
+        // where the states before this item's blocks go; the next item writes the one behind its last
+        float *sck = SAVE ? p.S_ck + ((size_t)bh * (p.nblk + 1) + blk0) * D * DV + (size_t)half * SC * DV + row
+                          : nullptr;
         auto put_state = [&](int i0) {   // pieces of 16 columns
             uint32_t hi[8], mi[8], lo[8];
 #pragma unroll
@@ -185,8 +204,7 @@ delta_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
         if (live) {
 #pragma unroll
             for (int i = 0; i < SC; i += 16) put_state(i);
-            if (SAVE)
-                write_state(p.S_ck + (size_t)bh * (nblk + 1) * D * DV + (size_t)half * SC * DV + row);
+            if (SAVE) write_state(sck, DV);
         }
         tmem_wait_st();
         tc_fence_before();
@@ -200,7 +218,7 @@ delta_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
             bool ok = true;
             if (warp == 0) {
                 ok = mbar_wait<1>(&S.kq_full[n % kStages], (n / kStages) & 1, g, 1);
-                if (!SAVE && n > 0) ok = ok && mbar_wait<1>(&S.o_read, (n - 1) & 1, g, 2);
+                if (Y && n > 0) ok = ok && mbar_wait<1>(&S.o_read, (n - 1) & 1, g, 2);
                 ok = __all_sync(0xffffffffu, ok);
                 if (ok) {
                     const uint32_t leader = elect_leader();
@@ -228,10 +246,15 @@ delta_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
                     uint32_t acc[16], hi[8], mi[8], lo[8];
                     tmem_ld16(tb + lb + kColKS + j0, acc);
                     float r[16], c[16];
+                    if (!SEG || values) {
 #pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                        r[j] = __uint_as_float((uint32_t)*reinterpret_cast<const uint16_t *>(
-                                   tv + (u * 16 + j) * 128 + ((ch ^ (j & 7)) << 4)) << 16);
+                        for (int j = 0; j < 16; ++j)
+                            r[j] = __uint_as_float((uint32_t)*reinterpret_cast<const uint16_t *>(
+                                       tv + (u * 16 + j) * 128 + ((ch ^ (j & 7)) << 4)) << 16);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) r[j] = 0.f;
+                    }
                     load16(&G.c[j0], c);
                     tmem_wait_ld();
 #pragma unroll
@@ -261,7 +284,7 @@ delta_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
                 }
                 mma_commit_if(leader, &S.e_done);
                 mma_commit_if(leader, &S.t_free[n & 1]);
-                if (!SAVE) {
+                if (Y) {
                     const uint32_t qq = smem_u32(sKQ) + (n % kStages) * Lay::kKQ + (~n & 1) * 8192;
 #pragma unroll 1
                     for (int pc = 1; pc >= 0; --pc)
@@ -285,7 +308,7 @@ delta_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
                         split3(w[2 * i] * u2f(acc[2 * i]), w[2 * i + 1] * u2f(acc[2 * i + 1]), hi[i], mi[i], lo[i]);
-                    if (!SAVE && u == 0) {   // W takes the place of the state's pieces
+                    if (Y && u == 0) {   // W takes the place of the state's pieces
                         ok = __all_sync(0xffffffffu, mbar_wait<1>(&S.qs_done, n & 1, g, 6));
                         if (!ok) break;
                     }
@@ -312,14 +335,14 @@ delta_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
                 mma_commit_if(leader, &S.s_done);
             }
             // ---- e once more: for y's second part, P e, or to the workspace
-            if (live) {
+            if (!SEG && live) {
 #pragma unroll 1
                 for (int u = 0; u < 2; ++u) {
                     const int j0 = half * 32 + u * 16;
                     uint32_t acc[16];
                     tmem_ld16(tb + lb + kColKS + j0, acc);
                     tmem_wait_ld();
-                    if (!SAVE) {
+                    if (Y) {
                         uint32_t hi[8], mi[8];
 #pragma unroll
                         for (int i = 0; i < 8; ++i) split2(u2f(acc[2 * i]), u2f(acc[2 * i + 1]), hi[i], mi[i]);
@@ -327,8 +350,8 @@ delta_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
                         tmem_st8(ce, hi);
                         tmem_st8(ce + 32, mi);
                     } else {
-                        float *dst = p.e + ((size_t)bh * p.N + (size_t)n * kDC + j0) * DV + row;
-                        const int in = p.N - n * kDC - j0;
+                        const int tok = (blk0 + n) * kDC + j0, in = p.N - tok;
+                        float *dst = p.e + ((size_t)bh * p.N + tok) * DV + row;
 #pragma unroll
                         for (int i = 0; i < 16; ++i)
                             if (i < in) dst[(size_t)i * DV] = u2f(acc[i]);
@@ -337,7 +360,7 @@ delta_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
                 tmem_wait_st();
                 tc_fence_before();
             }
-            if (!SAVE) {
+            if (Y) {
                 if ((failed = any_failed(false))) break;
                 if (warp == 0) {
                     ok = __all_sync(0xffffffffu, mbar_wait<1>(&S.p_ready, n & 1, g, 8));
@@ -375,9 +398,9 @@ delta_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
                         f2unpack(f2fma(cC2, f2pack(st[i + j], st[i + j + 1]), f2pack(u2f(acc[j]), u2f(acc[j + 1]))),
                                  st[i + j], st[i + j + 1]);
                     // SP is free: W, the last operand there, has been read
-                    if (n + 1 < nblk && SAVE) put_state(i);
+                    if (n + 1 < nblk && !Y) put_state(i);
                 }
-                if (!SAVE && n + 1 < nblk) {
+                if (Y && n + 1 < nblk) {
                     // at D = 128 the pieces of e lie in SP too: wait for P e
                     if (D > 64) ok = __all_sync(0xffffffffu, mbar_wait<1>(&S.pu_done, n & 1, g, 10));
                     tc_fence_after();
@@ -388,19 +411,25 @@ delta_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
                 }
                 tmem_wait_st();
                 tc_fence_before();
-                if (SAVE)
-                    write_state(p.S_ck + ((size_t)bh * (nblk + 1) + n + 1) * D * DV +
-                                (size_t)half * SC * DV + row);
+                sck += D * DV;
+                if (SAVE && (n + 1 < nblk || seg == segs - 1)) write_state(sck, DV);
             }
             failed = any_failed(!ok);
         }
-        if (!failed && live && p.S_out) write_state(p.S_out + sbase);
+        if (SEG) {
+            if (!failed && live && values)
+                write_state(p.S_local + (size_t)item * D * DV + (size_t)half * SC * DV + col_of, DV);
+            else if (!failed && live)
+                write_state(p.Phi + (size_t)item * D * D + (size_t)half * SC * D + col_of - DV, D);
+        } else if (!failed && live && p.S_out && seg == segs - 1) {
+            write_state(p.S_out + (size_t)bh * D * DV + (size_t)half * SC * DV + row, DV);
+        }
         if (warp == 0 && elect_leader()) {
             mma_commit(&S.drain[0]);
             drain_wait(&S.drain[0], 0, g.limit_ns);
             if (S.abort_flag) {   // let the copies in flight land
                 for (int n = max(0, kq_issued - kStages); n < kq_issued; ++n)
-                    if (!(n == 0 && bh == p.drop_item))
+                    if (!(n == 0 && (int)blockIdx.x == p.drop_item))
                         drain_wait(&S.kq_full[n % kStages], (n / kStages) & 1, g.limit_ns);
                 for (int n = max(0, v_issued - 2); n < v_issued; ++n)
                     drain_wait(&S.v_full[n & 1], (n >> 1) & 1, g.limit_ns);
@@ -418,7 +447,7 @@ delta_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
         auto fetch = [&](int n) {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const int tok = n * kDC + 2 * lane + i;
+                const int tok = (blk0 + n) * kDC + 2 * lane + i;
                 bv[i] = tok < p.N ? p.beta[rs.at(tok)] : 0.f;
                 gv[i] = tok < p.N && p.lg ? p.lg[rs.at(tok)] : 0.f;
             }
@@ -606,7 +635,7 @@ delta_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
             named_bar(kBarOut, kOut);
             if (tid == kChain + 2 * kInner) {
 #pragma unroll
-                for (int f = 0; f < DV / 64; ++f) tma_store_4d(&ymap, sY + f * 8192, f * 64, n * kDC, h, b);
+                for (int f = 0; f < DV / 64; ++f) tma_store_4d(&ymap, sY + f * 8192, f * 64, (blk0 + n) * kDC, h, b);
                 bulk_commit();
             }
             if (next) make_p(n + 1);
@@ -622,40 +651,126 @@ delta_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
     }
 }
 
-template <int D, int DV, bool SAVE> cudaError_t launch_tc(const DeltaArgs &a) {
+// States at the segments' starts: P_0 = S_in (or 0), P_{s+1} = Phi_s P_s + S_local_s.  16 columns a
+// CTA, walking the segments; a float32 product of [D x D] by [D x 16] a step.
+constexpr int kPrefixCols = 16, kPrefixThr = 256;
+template <int D>
+__global__ void __launch_bounds__(kPrefixThr)
+delta_prefix_kernel(const float *__restrict__ Phi, const float *__restrict__ S_local,
+                    const float *__restrict__ S_in, float *__restrict__ P, int nseg, int DV) {
+    constexpr int NC = kPrefixCols * D / kPrefixThr;   // columns of a thread (a row of Phi each)
+    __shared__ float Ps[D][kPrefixCols], F[D][33];
+    const int bh = blockIdx.x, c0 = blockIdx.y * kPrefixCols;
+    const int i = threadIdx.x % D, c = threadIdx.x / D * NC;
+    const size_t st = (size_t)D * DV, at = (size_t)i * DV + c0 + c;
+    float x[NC];
+#pragma unroll
+    for (int j = 0; j < NC; ++j) x[j] = S_in ? S_in[bh * st + at + j] : 0.f;
+    for (int s = 0;; ++s) {
+#pragma unroll
+        for (int j = 0; j < NC; ++j) {
+            Ps[i][c + j] = x[j];
+            P[((size_t)bh * nseg + s) * st + at + j] = x[j];
+        }
+        if (s == nseg - 1) break;
+        const size_t item = (size_t)bh * (nseg - 1) + s;
+#pragma unroll
+        for (int j = 0; j < NC; ++j) x[j] = S_local[item * st + at + j];
+        for (int a0 = 0; a0 < D; a0 += 32) {
+            __syncthreads();
+            for (int k = threadIdx.x; k < D * 32; k += kPrefixThr)
+                F[k / 32][k % 32] = Phi[item * D * D + (size_t)(k / 32) * D + a0 + k % 32];
+            __syncthreads();
+#pragma unroll 8
+            for (int a = 0; a < 32; ++a) {
+                const float f = F[i][a];
+#pragma unroll
+                for (int j = 0; j < NC; ++j) x[j] = fmaf(f, Ps[a0 + a][c + j], x[j]);
+            }
+        }
+        __syncthreads();
+    }
+}
+
+// Segments of a head.  Splitting pays where the heads leave SMs idle: the segments but the last of
+// each head then run once more, ahead, from an empty state (ceil((dv + d) / 128) CTAs each), and
+// their ends are joined.  In units of a block's time (about 5 us): a wave of CTAs takes its
+// segments' length; a second start, the join and their launches take about 8 + nseg / 2 (24 heads of
+// 17 blocks: 94 us whole, 103 us in four; 32 heads of 2048 blocks: 8.4 ms whole, 3.6 ms in four).
+void delta_segments(const DeltaArgs &a, int &nseg, int &seg_blocks) {
+    const int nblk = delta_blocks(a.N), sms = num_sms(), parts = (a.dv + a.d + 127) / 128;
+    const long long BH = (long long)a.B * a.H;
+    auto waves = [&](long long ctas) { return (double)((ctas + sms - 1) / sms); };
+    nseg = 1;
+    seg_blocks = nblk;
+    if (BH >= sms) return;
+    double best = waves(BH) * nblk;
+    for (int s = 2; s <= 64 && 2 * s <= nblk; ++s) {
+        const int len = (nblk + s - 1) / s, n = (nblk + len - 1) / len;
+        if (n != s) continue;
+        const double cost = (waves(BH * (s - 1) * parts) + waves(BH * s)) * len + 8 + 0.5 * s;
+        if (cost < best) {
+            best = cost;
+            nseg = s;
+            seg_blocks = len;
+        }
+    }
+}
+
+template <int D, int DV, int MODE> cudaError_t launch_tc(const DeltaArgs &a, DeltaTc p) {
     CUtensorMap qm, km, vm, ym{};
     if (!encode_tokens(&qm, a.q, a.layout, a.B, a.Hk, a.N, D) ||
         !encode_tokens(&km, a.k, a.layout, a.B, a.Hk, a.N, D) ||
         !encode_tokens(&vm, a.v, a.layout, a.B, a.H, a.N, DV) ||
-        (!SAVE && !encode_tokens(&ym, a.y, a.layout, a.B, a.H, a.N, DV)))
+        (MODE == kForward && !encode_tokens(&ym, a.y, a.layout, a.B, a.H, a.N, DV)))
         return cudaErrorInvalidValue;
+    auto kern = delta_tc_kernel<D, DV, MODE>;
+    constexpr int smem = DeltaLay<D, DV>::request;
+    static_assert(smem <= 232448, "shared memory of a CTA");
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    const int ctas = a.B * a.H * (MODE == kSegment ? (p.nseg - 1) * p.parts : p.nseg);
+    kern<<<ctas, kChain + 2 * kInner + (MODE == kForward ? kOut : 0), smem, a.stream>>>(qm, km, vm, ym, p);
+    return cudaGetLastError();
+}
+
+template <int D, int DV> cudaError_t launch_dims(const DeltaArgs &a, bool save) {
     DeltaTc p{};
     p.beta = a.beta; p.lg = a.log_gate;
     p.H = a.H; p.group = a.H / a.Hk; p.N = a.N; p.layout = a.layout; p.nblk = delta_blocks(a.N);
+    p.nseg = 1; p.seg_blocks = p.nblk; p.parts = (DV + D + 127) / 128;
     p.S_in = a.S_in; p.S_out = a.S_out;
-    if (SAVE) {
-        const DeltaBwdWs w = delta_bwd_ws(a);
-        p.S_ck = w.S;
-        p.e = w.e;
-    }
     WsHeader *hdr = static_cast<WsHeader *>(a.ws);
     p.err = &hdr->error;
     p.err_where = &hdr->error_where;
     const long long lim = debug_fault().wait_limit_ns;
     p.limit_ns = lim > 0 ? (unsigned long long)lim : 1000000000ull;
     p.drop_item = debug_fault().drop_load_item;
-    auto kern = delta_tc_kernel<D, DV, SAVE>;
-    constexpr int smem = DeltaLay<D, DV>::request;
-    static_assert(smem <= 232448, "shared memory of a CTA");
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-    kern<<<a.B * a.H, kChain + 2 * kInner + (SAVE ? 0 : kOut), smem, a.stream>>>(qm, km, vm, ym, p);
-    return cudaGetLastError();
+    if (save) {
+        const DeltaBwdWs w = delta_bwd_ws(a);
+        p.S_ck = w.S;
+        p.e = w.e;
+        return launch_tc<D, DV, kSave>(a, p);
+    }
+    delta_segments(a, p.nseg, p.seg_blocks);
+    if (p.nseg > 1) {
+        const size_t items = (size_t)a.B * a.H * (p.nseg - 1);
+        p.S_local = reinterpret_cast<float *>(static_cast<char *>(a.ws) + sizeof(WsHeader));
+        p.Phi = p.S_local + items * D * DV;
+        float *P = p.Phi + items * D * D;
+        cudaError_t e = launch_tc<D, DV, kSegment>(a, p);
+        if (e != cudaSuccess) return e;
+        delta_prefix_kernel<D><<<dim3(a.B * a.H, DV / kPrefixCols), kPrefixThr, 0, a.stream>>>(
+            p.Phi, p.S_local, a.S_in, P, p.nseg, DV);
+        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        p.S_in = P;
+    }
+    return launch_tc<D, DV, kForward>(a, p);
 }
 
-template <bool SAVE> cudaError_t launch_tc_dims(const DeltaArgs &a) {
-    if (a.d == 64) return a.dv == 64 ? launch_tc<64, 64, SAVE>(a) : launch_tc<64, 128, SAVE>(a);
-    return a.dv == 64 ? launch_tc<128, 64, SAVE>(a) : launch_tc<128, 128, SAVE>(a);
+cudaError_t launch_all(const DeltaArgs &a, bool save) {
+    if (a.d == 64) return a.dv == 64 ? launch_dims<64, 64>(a, save) : launch_dims<64, 128>(a, save);
+    return a.dv == 64 ? launch_dims<128, 64>(a, save) : launch_dims<128, 128>(a, save);
 }
 
 }  // namespace
@@ -663,7 +778,18 @@ template <bool SAVE> cudaError_t launch_tc_dims(const DeltaArgs &a) {
 bool delta_tc_supported(const DeltaArgs &a) {
     return a.dt == LA_DTYPE_BF16 && (a.d == 64 || a.d == 128) && (a.dv == 64 || a.dv == 128);
 }
-cudaError_t launch_delta_forward_tc(const DeltaArgs &a) { return launch_tc_dims<false>(a); }
-cudaError_t launch_delta_states_tc(const DeltaArgs &a) { return launch_tc_dims<true>(a); }
+// header | (split sequences) the segments' ends and maps, the states at their starts
+size_t delta_tc_workspace(const DeltaArgs &a) {
+    int nseg, len;
+    delta_segments(a, nseg, len);
+    size_t floats = 0;
+    if (nseg > 1) {
+        const size_t BH = (size_t)a.B * a.H, st = (size_t)a.d * a.dv;
+        floats = BH * (nseg - 1) * (st + (size_t)a.d * a.d) + BH * nseg * st;
+    }
+    return sizeof(WsHeader) + 4 * floats;
+}
+cudaError_t launch_delta_forward_tc(const DeltaArgs &a) { return launch_all(a, false); }
+cudaError_t launch_delta_states_tc(const DeltaArgs &a) { return launch_all(a, true); }
 
 }  // namespace la

@@ -171,6 +171,7 @@ cudaError_t launch_delta_states_simt(const DeltaArgs &a);    // the backward's f
 cudaError_t launch_delta_reverse_simt(const DeltaArgs &a);   // and its second
 // tensor cores (bf16, d and dv in {64, 128}); a.ws starts with a status header
 bool delta_tc_supported(const DeltaArgs &a);
+size_t delta_tc_workspace(const DeltaArgs &a);   // depends on the current device's SM count
 cudaError_t launch_delta_forward_tc(const DeltaArgs &a);
 cudaError_t launch_delta_states_tc(const DeltaArgs &a);
 cudaError_t launch_delta_reverse_tc(const DeltaArgs &a);

@@ -576,8 +576,9 @@ def _on_device(fn):
 _current_device = torch.cuda.current_device
 
 
-def _current_stream(device_index) -> int:
-    return torch.cuda.current_stream(device_index).cuda_stream
+# the stream's handle without a Stream object around it, where torch offers that
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda device_index: torch.cuda.current_stream(device_index).cuda_stream)
 
 
 def _addr(t):
@@ -610,7 +611,7 @@ def _workspace(workspace, need, like):
 
 
 @functools.lru_cache(maxsize=1024)
-def _delta_bytes(*sizes):
+def _delta_bytes(device_index, *sizes):   # the split depends on the current device
     return int(lib().la_delta_workspace_bytes(*sizes))
 
 
@@ -667,7 +668,7 @@ def forward_delta(q, k, v, beta, log_gate=None, S_in=None, return_state=False, o
         out = torch.empty_like(v)
     if return_state and S_out is None:
         S_out = torch.empty(state, dtype=torch.float32, device=q.device)
-    workspace, wa, wbytes = _workspace(workspace, _delta_bytes(*sizes), q)
+    workspace, wa, wbytes = _workspace(workspace, _delta_bytes(dev, *sizes), q)
     st = lib().la_forward_delta(qa, ka, va, _expect("out", out, v.shape, v.dtype, dev), ba, la, B, H, Hk,
                                 N, d, dv, dt, LAYOUT[layout],
                                 _expect("S_in", S_in, state, torch.float32, dev),
@@ -753,7 +754,7 @@ def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, return_stats=False,
 
 
 @functools.lru_cache(maxsize=1024)
-def _norm_backward_bytes(rows, D, dt):
+def _norm_backward_bytes(device_index, rows, D, dt):   # as many sums as the device has CTAs
     return int(lib().la_layer_norm_backward_workspace_bytes(rows, D, dt))
 
 
@@ -771,7 +772,7 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, sums=None, workspace=Non
     if weight is not None if sums is None else sums:
         gw = torch.empty(D, dtype=f32, device=x.device)
         gb = torch.empty_like(gw)
-        workspace, wa, wbytes = _workspace(workspace, _norm_backward_bytes(rows, D, dt), x)
+        workspace, wa, wbytes = _workspace(workspace, _norm_backward_bytes(dev, rows, D, dt), x)
     st = lib().la_layer_norm_backward(_expect("dy", dy, shape, x.dtype, dev), _expect("x", x, shape, x.dtype, dev),
                                       _expect("mean", mean, shape[:-1], f32, dev),
                                       _expect("rstd", rstd, shape[:-1], f32, dev),

@@ -98,6 +98,19 @@ def test_long_sequence(dtype, layout):
     check_backward(x, dtype, layout)
 
 
+@pytest.mark.parametrize("d,dv", [(64, 64), (128, 128), (64, 128), (128, 64)])
+@pytest.mark.parametrize("gate,N", [(None, 2500), ("open", 4000), ("any", 1900)])
+def test_few_heads_and_many_tokens(d, dv, gate, N):
+    """bf16 sequences long enough to be split over the SMs, from a given state.  Without gates the
+    state is the one of two orders of the same sums (maps of the state, then the state): the bound
+    is that of a sequence of N tokens all the same, sqrt(2 d) tokens being remembered."""
+    x = R.inputs(1, 2, 1, N, d, dv, BF16, gate=gate, state=True, layout="bnhd", seed=N + d)
+    check_forward(x, "bnhd")
+    y, S = gpu_forward(x, "bnhd", return_state=True)
+    y2, S2 = gpu_forward(x, "bnhd", return_state=True)
+    assert torch.equal(y, y2) and torch.equal(S, S2)
+
+
 @pytest.mark.parametrize("dtype", [BF16, F32])
 def test_a_sequence_in_parts(dtype):
     x = on_gpu(R.inputs(2, 2, 2, 300, 64, 64, dtype, state=True, seed=8))
