@@ -1,6 +1,6 @@
 // delta_grad_tc.cu -- delta_grad.cu's products on the tensor cores (bf16 inputs,
-// d and dv in {64, 128}): one CTA per block of 64 tokens and key head, all
-// blocks at once; it sums over the key head's value heads in registers.
+// d and dv in {64, 128}): an item is a block of 64 tokens and a key head, whose
+// value heads (units) are summed in registers.
 //
 // The gradients of q and k are accumulated transposed, a TMEM lane for each of
 // the d features (S, G the state before the block and its gradient after it):
@@ -15,14 +15,18 @@
 // two pieces (2^-16).
 //
 // Bound by HBM: S, G, e and du are read once (S of the next block too, from
-// L2, for <G, S'>), 256 KB a block at d = dv = 128 beside the 112 KB of inputs
-// and outputs.
+// L2, for <G, S'>), 192 KB a block at d = dv = 128 beside the 112 KB of inputs
+// and outputs.  Persistent CTAs, one an SM: 16 warps turn float32 rows into
+// operands and accumulators into gradients; warp 0 also issues the MMAs and
+// copies, and has the next unit's float32 values brought into L2 meanwhile.
+// (A warp of its own for that leaves 96 registers a thread, and spills; so does
+// the next unit's S in registers.)
 #include "delta_tc.cuh"
 
 namespace la {
 namespace {
 
-constexpr int kGThr = 512;
+constexpr int kGThr = 512, kBarG = 1;
 // TMEM columns: pieces of S (3 DV/2); the scores' two accumulators, then the pieces of G (2 DV/2);
 // S dy^T, G e^T, S du^T.  K^T P^T and Q^T P + K^T F take the place of S.
 constexpr uint32_t gS = 0, gPF = 192, gG = 192, gQ = 320, gGe = 384, gSu = 448, gQ2 = 0, gK2 = 64;
@@ -32,14 +36,17 @@ struct GradTc {
     const __nv_bfloat16 *v;
     __nv_bfloat16 *dv;
     float *dbeta, *dlg;
-    int H, Hk, N, layout, nblk;
+    int H, Hk, N, layout, nblk, items;
     unsigned int *err, *err_where;
     unsigned long long limit_ns;
 };
-struct GradSmall {
+struct GradUnit {   // what a unit leaves for the sums over its tokens
     Gates gates;
     float db[kDC], vdv[kDC], qdq[4][kDC], gs[kGThr / 32];
-    uint64_t kq_full, y_full, pf_done, s_done, all_done;
+};
+struct GradSmall {
+    GradUnit unit[2];
+    uint64_t kq_full[2], y_full, pf_done, s_done, all_done;
     uint32_t tmem_base;
     volatile int abort_flag;
 };
@@ -47,7 +54,7 @@ template <int D, int DV> struct GradLay {
     static constexpr int kT = (D / 64) * 8192;            // K or Q, slabs of 64 features
     static constexpr int kX = (DV / 64) * 16384;          // per 64 columns: 64 rows, 64 rows
     static constexpr int kE = (DV / 64) * 8192;
-    static constexpr int oK = 0, oQ = oK + kT, oX1 = oQ + kT, oX2 = oX1 + kX, oEm = oX2 + kX, oEl = oEm + kE,
+    static constexpr int oKQ = 0, oX1 = 4 * kT, oX2 = oX1 + kX, oEm = oX2 + kX, oEl = oEm + kE,
                          oP = oEl + kE, oPT = oP + 3 * 8192, oF = oPT + 2 * 8192, oSmall = oF + 2 * 8192;
     static constexpr int total = oSmall + (int)sizeof(GradSmall);
     static constexpr int request = total + 1024;
@@ -84,7 +91,8 @@ __device__ __forceinline__ float reduce16(float (&x)[16], int lane) {
     return x[0] + __shfl_xor_sync(0xffffffffu, x[0], 16);
 }
 
-template <int D, int DV>
+// ONE: a single value head to a key head, whose gradients then need no sums.
+template <int D, int DV, bool ONE>
 __global__ void __launch_bounds__(kGThr, 1)
 delta_grad_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                      const __grid_constant__ CUtensorMap ymap, const __grid_constant__ CUtensorMap dqmap,
@@ -93,16 +101,16 @@ delta_grad_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     GradSmall &S = *reinterpret_cast<GradSmall *>(sm + Lay::oSmall);
-    uint8_t *sK = sm + Lay::oK, *sQ = sm + Lay::oQ, *sX1 = sm + Lay::oX1, *sX2 = sm + Lay::oX2, *sEm = sm + Lay::oEm,
+    uint8_t *sKQ = sm + Lay::oKQ, *sX1 = sm + Lay::oX1, *sX2 = sm + Lay::oX2, *sEm = sm + Lay::oEm,
             *sEl = sm + Lay::oEl, *sP = sm + Lay::oP, *sPT = sm + Lay::oPT, *sF = sm + Lay::oF;
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
-    const int nblk = p.nblk, blk = blockIdx.x % nblk, bk = blockIdx.x / nblk, b = bk / p.Hk, hk = bk % p.Hk;
-    const int group = p.H / p.Hk, t0 = blk * kDC, n_in = min(kDC, p.N - t0);
+    const int nblk = p.nblk, group = ONE ? 1 : p.H / p.Hk;
     const Guard g{&S.abort_flag, p.err, p.err_where, p.limit_ns};
 
     if (tid == 0) {
         S.abort_flag = 0;
-        mbar_init(&S.kq_full, 1);
+        mbar_init(&S.kq_full[0], 1);
+        mbar_init(&S.kq_full[1], 1);
         mbar_init(&S.y_full, 1);
         mbar_init(&S.pf_done, 1);
         mbar_init(&S.s_done, 1);
@@ -117,335 +125,438 @@ delta_grad_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
     __syncthreads();
     tc_fence_after();
     const uint32_t tb = __shfl_sync(0xffffffffu, S.tmem_base, 0);
-    const int wq = warp & 3, row = wq * 32 + lane, cg = warp >> 2;   // TMEM lane; quarter of the columns
-    const uint32_t lb = (uint32_t)(wq * 32) << 16;
-    constexpr int SC = DV / 4;   // state columns of a thread
-    const bool live = row < D;   // warp-uniform: lanes with a feature
-    auto load_rows = [&](const float *src, float (&x)[SC]) {
-#pragma unroll
-        for (int i = 0; i < SC; i += 4)
-            *reinterpret_cast<float4 *>(x + i) =
-                __ldg(reinterpret_cast<const float4 *>(src + (size_t)row * DV + cg * SC + i));
-    };
 
-    if (tid == 0) {
-        mbar_arrive_expect_tx(&S.kq_full, 2 * kDC * D * 2);
+    constexpr uint32_t i64 = idesc_bf16(128, kDC, 0, 0), iT = idesc_bf16(128, kDC, 1, 0);
+    auto load_kq = [&](int it, int stage) {
+        uint64_t *bar = &S.kq_full[stage];
+        const int t0 = it % nblk * kDC, b = it / nblk / p.Hk, hk = it / nblk % p.Hk;
+        mbar_arrive_expect_tx(bar, 2 * kDC * D * 2);
 #pragma unroll
         for (int f = 0; f < D / 64; ++f) {
-            tma_load_4d(sK + f * 8192, &kmap, &S.kq_full, f * 64, t0, hk, b);
-            tma_load_4d(sQ + f * 8192, &qmap, &S.kq_full, f * 64, t0, hk, b);
+            tma_load_4d(sKQ + stage * 2 * Lay::kT + f * 8192, &kmap, bar, f * 64, t0, hk, b);
+            tma_load_4d(sKQ + stage * 2 * Lay::kT + Lay::kT + f * 8192, &qmap, bar, f * 64, t0, hk, b);
         }
-    }
-    float dq[16], dk[16];   // feature `row`, tokens 16 cg ..: sums over the value heads
+    };
+    auto load_y = [&](int it, int gi) {
+        const int t0 = it % nblk * kDC, b = it / nblk / p.Hk, h = it / nblk % p.Hk * group + gi;
+        mbar_arrive_expect_tx(&S.y_full, kDC * DV * 2);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) dq[i] = dk[i] = 0.f;
-    bool failed = false;
-    const size_t st = (size_t)D * DV;
-
-    for (int gi = 0; gi < group && !failed; ++gi) {
-        const int h = hk * group + gi;
-        const size_t bh = (size_t)b * p.H + h;
-        const TokenRows rv = token_rows(p.layout, b, h, p.H, p.N, DV), rs = token_rows(p.layout, b, h, p.H, p.N, 1);
-        const float *S0 = p.S_ck + (bh * (nblk + 1) + blk) * st, *G1 = p.G_ck + (bh * nblk + blk) * st;
-        if (tid == 0) {
-            mbar_arrive_expect_tx(&S.y_full, kDC * DV * 2);
-#pragma unroll
-            for (int f = 0; f < DV / 64; ++f) tma_load_4d(sX1 + f * 16384, &ymap, &S.y_full, f * 64, t0, h, b);
-        }
-        float x[SC];
-        if (live) load_rows(S0, x);
-        if (warp == 1) {
-            float bv[2], gv[2];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int t = t0 + 2 * lane + i;
-                bv[i] = t < p.N ? p.beta[rs.at(t)] : 0.f;
-                gv[i] = t < p.N && p.lg ? p.lg[rs.at(t)] : 0.f;
-            }
-            block_gates<false>(S.gates, bv, gv, lane);
-        }
-        // ---- e and du as pieces, tokens x dv; dv = b du and the tokens' sums
-#pragma unroll
-        for (int it = 0; it < DV / 64; ++it) {
-            const int item = it * kGThr + tid, t = item / (DV / 8), c = item % (DV / 8) * 8;
-            float e[8], du[8];
-            float bt = 0.f, db = 0.f, vd = 0.f;
-            if (t < n_in) {
-                const size_t o = (bh * p.N + t0 + t) * DV + c, ov = rv.at(t0 + t) + c;
-                load_vec<8>(p.e + o, e);
-                load_vec<8>(p.du + o, du);
-                bt = p.beta[rs.at(t0 + t)];
-                float vv[8];
-                load_vec<8>(p.v + ov, vv);
-                uint32_t w[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) w[j] = pack_bf16x2(bt * du[2 * j], bt * du[2 * j + 1]);
-                *reinterpret_cast<uint4 *>(p.dv + ov) = make_uint4(w[0], w[1], w[2], w[3]);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    db = fmaf(du[j], e[j], db);
-                    vd = fmaf(vv[j], bt * du[j], vd);
-                }
-            } else {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) e[j] = du[j] = 0.f;
-            }
-#pragma unroll
-            for (int o = DV / 16; o > 0; o >>= 1) {
-                db += __shfl_xor_sync(0xffffffffu, db, o);
-                vd += __shfl_xor_sync(0xffffffffu, vd, o);
-            }
-            if (c == 0) { S.db[t] = db; S.vdv[t] = vd; }
-            uint32_t hi[4], mi[4], lo[4];
-            const uint32_t o16 = (c >> 6) * 16384 + sw128_off(t, c & 63), o8 = (c >> 6) * 8192 + sw128_off(t, c & 63);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) split3(e[2 * j], e[2 * j + 1], hi[j], mi[j], lo[j]);
-            *reinterpret_cast<uint4 *>(sX2 + o16) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            *reinterpret_cast<uint4 *>(sEm + o8) = make_uint4(mi[0], mi[1], mi[2], mi[3]);
-            *reinterpret_cast<uint4 *>(sEl + o8) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) split2(du[2 * j], du[2 * j + 1], hi[j], mi[j]);
-            *reinterpret_cast<uint4 *>(sX1 + 8192 + o16) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            *reinterpret_cast<uint4 *>(sX2 + 8192 + o16) = make_uint4(mi[0], mi[1], mi[2], mi[3]);
-        }
-        fence_proxy_async();
-        if (live) put_pieces<SC, 3>(tb + lb + gS + cg * (SC / 2), DV / 2, x);
-        tmem_wait_st();
-        tc_fence_before();
-        bool ok = mbar_wait<1>(&S.y_full, gi & 1, g, 1);
-        if (gi == 0) ok = ok && mbar_wait<1>(&S.kq_full, 0, g, 2);
-        if ((failed = !__syncthreads_and(ok))) break;
-
-        // ---- scores, and what S gives
-        if (warp == 0) {
-            const uint32_t leader = elect_leader();
-            tc_fence_after();
-            constexpr uint32_t i64 = idesc_bf16(128, kDC, 0, 0);
-            const uint64_t x1 = desc_k(smem_u32(sX1)), x2 = desc_k(smem_u32(sX2));
-            // [dy; du_h] (e_l, e_m, e_h), small ones first, and du_m e_h (the upper rows unused)
-#pragma unroll 1
-            for (int o = 0; o < 4; ++o) {
-                const bool eh = o >= 2;
-                const uint64_t a = o == 3 ? x2 : x1, bd = eh ? x2 : desc_k(smem_u32(o ? sEm : sEl));
-                const uint32_t d = tb + gPF + (o == 3 ? 64 : 0), slab = eh ? 16384 / 16 : 8192 / 16;
-#pragma unroll
-                for (int ks = 0; ks < DV / 16; ++ks)
-                    mma_ss_if(leader, d, a + (ks >> 2) * 1024 + (ks & 3) * 2, bd + (ks >> 2) * slab + (ks & 3) * 2,
-                              i64, (o != 0 && o != 3) || ks > 0);
-            }
-            mma_commit_if(leader, &S.pf_done);
-            // S dy^T from three pieces, S du^T from (m, m) (m, h) (h, m) (h, h)
-#pragma unroll 1
-            for (int pc = 2; pc >= 0; --pc)
-                mma_rows<DV / 16, 16384>(leader, tb + gQ, tb + gS + pc * (DV / 2), smem_u32(sX1), i64, pc < 2);
-#pragma unroll 1
-            for (int o = 0; o < 4; ++o)
-                mma_rows<DV / 16, 16384>(leader, tb + gSu, tb + gS + (o < 2) * (DV / 2),
-                                         smem_u32(o & 1 ? sX1 : sX2) + 8192, i64, o > 0);
-            mma_commit_if(leader, &S.s_done);
-        }
-        __syncwarp();
-        // ---- G, <G, S'>
-        float gs = 0.f;
-        if (live) {
-            load_rows(G1, x);
-            if (p.lg) {
-                float y[SC];
-                load_rows(S0 + st, y);
-#pragma unroll
-                for (int i = 0; i < SC; ++i) gs = fmaf(x[i], y[i], gs);
-            }
-        }
-        gs = warp_sum(gs);
-        if (lane == 0) S.gs[warp] = gs;
-        // ---- P, P^T and F from the scores; 16 columns of a row
-        ok = mbar_wait<1>(&S.pf_done, gi & 1, g, 3);
-        ok = __all_sync(0xffffffffu, ok);
-        uint32_t sc[16], sc2[16];
-        if (ok) {
-            tc_fence_after();
-            tmem_ld16(tb + lb + gPF + cg * 16, sc);
-            tmem_ld16(tb + lb + gPF + 64 + cg * 16, sc2);
-            tmem_wait_ld();
-            tc_fence_before();
-        }
-        if ((failed = !__syncthreads_and(ok))) break;   // the scores have been read
+        for (int f = 0; f < DV / 64; ++f) tma_load_4d(sX1 + f * 16384, &ymap, &S.y_full, f * 64, t0, h, b);
+    };
+    // scores, and what S gives
+    auto issue_first = [&]() {
+        const uint32_t leader = elect_leader();
         tc_fence_after();
-        if (live) put_pieces<SC, 2>(tb + lb + gG + cg * (SC / 2), DV / 2, x);
-        {
-            const int i = row & 63, j0 = cg * 16;
-            float w[16];
-            if (row >= 64) {
-#pragma unroll
-                for (int j = 0; j < 16; ++j) sc[j] = f2u(u2f(sc[j]) + u2f(sc2[j]));
-            }
-            decayed16<false, false>(S.gates, i, j0, sc, w);
-            if (row < 64) {
-                uint32_t hi[8], mi[8], lo[8];
-#pragma unroll
-                for (int j = 0; j < 16; ++j) w[j] = j0 + j <= i ? w[j] : 0.f;
-#pragma unroll
-                for (int j = 0; j < 8; ++j) split3(w[2 * j], w[2 * j + 1], hi[j], mi[j], lo[j]);
-#pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    const uint32_t o = sw128_off(i, j0 + 8 * q);
-                    *reinterpret_cast<uint4 *>(sP + o) = make_uint4(hi[4 * q], hi[4 * q + 1], hi[4 * q + 2], hi[4 * q + 3]);
-                    *reinterpret_cast<uint4 *>(sP + 8192 + o) = make_uint4(mi[4 * q], mi[4 * q + 1], mi[4 * q + 2], mi[4 * q + 3]);
-                    *reinterpret_cast<uint4 *>(sP + 16384 + o) = make_uint4(lo[4 * q], lo[4 * q + 1], lo[4 * q + 2], lo[4 * q + 3]);
-                }
-#pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    const uint32_t o = sw128_off(j0 + j, i), sh = (j & 1) * 16;
-                    *reinterpret_cast<uint16_t *>(sPT + o) = (uint16_t)(hi[j >> 1] >> sh);
-                    *reinterpret_cast<uint16_t *>(sPT + 8192 + o) = (uint16_t)(mi[j >> 1] >> sh);
-                }
-            } else {
-                const float nb = -S.gates.b[i];
-#pragma unroll
-                for (int j = 0; j < 16; j += 2) {
-                    uint32_t hi, mi;
-                    split2(j0 + j < i ? nb * w[j] : 0.f, j0 + j + 1 < i ? nb * w[j + 1] : 0.f, hi, mi);
-#pragma unroll
-                    for (int e = 0; e < 2; ++e)
-                        if (j0 + j + e <= i) {   // both of F_ij and F_ji (zero on the diagonal)
-                            const uint32_t o = sw128_off(i, j0 + j + e), ot = sw128_off(j0 + j + e, i);
-                            const uint16_t a = (uint16_t)(hi >> (16 * e)), m = (uint16_t)(mi >> (16 * e));
-                            *reinterpret_cast<uint16_t *>(sF + o) = a;
-                            *reinterpret_cast<uint16_t *>(sF + 8192 + o) = m;
-                            *reinterpret_cast<uint16_t *>(sF + ot) = a;
-                            *reinterpret_cast<uint16_t *>(sF + 8192 + ot) = m;
-                        }
-                }
-            }
-        }
-        fence_proxy_async();
-        tmem_wait_st();
-        tc_fence_before();
-        ok = __all_sync(0xffffffffu, mbar_wait<1>(&S.s_done, gi & 1, g, 4));   // S's place is free
-        if ((failed = !__syncthreads_and(ok))) break;
-
-        // ---- what G gives, K^T P^T, Q^T P + K^T F
-        if (warp == 0) {
-            const uint32_t leader = elect_leader();
-            tc_fence_after();
-            constexpr uint32_t i64 = idesc_bf16(128, kDC, 0, 0), iT = idesc_bf16(128, kDC, 1, 0);
+        const uint64_t x1 = desc_k(smem_u32(sX1)), x2 = desc_k(smem_u32(sX2));
+        // [dy; du_h] (e_l, e_m, e_h), small ones first, and du_m e_h (the upper rows unused)
 #pragma unroll 1
-            for (int o = 0; o < 5; ++o) {   // pieces (G, e): (h, l) (m, m) (m, h) (h, m) (h, h)
-                const uint32_t a = tb + gG + (o == 1 || o == 2 ? DV / 2 : 0);
-                if (o == 2 || o == 4)
-                    mma_rows<DV / 16, 16384>(leader, tb + gGe, a, smem_u32(sX2), i64, true);
-                else
-                    mma_rows<DV / 16, 8192>(leader, tb + gGe, a, smem_u32(o ? sEm : sEl), i64, o > 0);
-            }
-            // features 64 .. 127 repeat the others where there are none
-            const uint64_t kd = smem_desc(smem_u32(sK), D > 64 ? 8192 : 0, 1024, kSwizzle128B);
-            const uint64_t qd = smem_desc(smem_u32(sQ), D > 64 ? 8192 : 0, 1024, kSwizzle128B);
-            const uint64_t pd = desc_k(smem_u32(sP)), ptd = desc_k(smem_u32(sPT)), fd = desc_k(smem_u32(sF));
-#pragma unroll 1
-            for (int pc = 2; pc >= 0; --pc)
+        for (int o = 0; o < 4; ++o) {
+            const bool eh = o >= 2;
+            const uint64_t a = o == 3 ? x2 : x1, bd = eh ? x2 : desc_k(smem_u32(o ? sEm : sEl));
+            const uint32_t d = tb + gPF + (o == 3 ? 64 : 0), slab = eh ? 16384 / 16 : 8192 / 16;
 #pragma unroll
-                for (int ks = 0; ks < kDC / 16; ++ks)
-                    mma_ss_if(leader, tb + gQ2, kd + ks * 128, pd + pc * 512 + ks * 2, iT, pc < 2 || ks > 0);
-#pragma unroll 1
-            for (int o = 0; o < 4; ++o) {   // (Q, P_m) (K, F_m) (Q, P_h) (K, F_h)
-                const uint64_t a = o & 1 ? kd : qd, bd = (o & 1 ? fd : ptd) + (o < 2 ? 512 : 0);
-#pragma unroll
-                for (int ks = 0; ks < kDC / 16; ++ks)
-                    mma_ss_if(leader, tb + gK2, a + ks * 128, bd + ks * 2, iT, o > 0 || ks > 0);
-            }
-            mma_commit_if(leader, &S.all_done);
+            for (int ks = 0; ks < DV / 16; ++ks)
+                mma_ss_if(leader, d, a + (ks >> 2) * 1024 + (ks & 3) * 2, bd + (ks >> 2) * slab + (ks & 3) * 2,
+                          i64, (o != 0 && o != 3) || ks > 0);
         }
-        __syncwarp();
-        ok = __all_sync(0xffffffffu, mbar_wait<1>(&S.all_done, gi & 1, g, 5));
-        if (ok && live) {
-            tc_fence_after();
-            const Gates &G = S.gates;
-            const int j0 = cg * 16;
-            uint32_t a[16], a2[16];
-            float c[16], w[16], xq[16];
-            tmem_ld16(tb + lb + gQ + j0, a);
-            tmem_ld16(tb + lb + gQ2 + j0, a2);
-            load16(&G.c[j0], c);
-            tmem_wait_ld();
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {
-                const float y = fmaf(c[j], u2f(a[j]), u2f(a2[j]));
-                dq[j] += y;
-                const uint16_t qv = *reinterpret_cast<const uint16_t *>(sQ + (row >> 6) * 8192 + sw128_off(j0 + j, row & 63));
-                xq[j] = y * __uint_as_float((uint32_t)qv << 16);
-            }
-            if (p.lg) {
-                const float s = reduce16(xq, lane);
-                if (lane < 16) S.qdq[wq][j0 + lane] = s;
-            }
-            tmem_ld16(tb + lb + gGe + j0, a);
-            tmem_ld16(tb + lb + gSu + j0, a2);
-            load16(&G.w[j0], w);
-            tmem_wait_ld();
-#pragma unroll
-            for (int j = 0; j < 16; ++j) dk[j] = fmaf(w[j], u2f(a[j]), dk[j]);
-            load16(&G.b[j0], w);
-            tmem_ld16(tb + lb + gK2 + j0, a);
-            tmem_wait_ld();
-#pragma unroll
-            for (int j = 0; j < 16; ++j) dk[j] += fmaf(-(w[j] * c[j]), u2f(a2[j]), u2f(a[j]));
-            tc_fence_before();
-        }
-        if ((failed = !__syncthreads_and(ok))) break;
+        mma_commit_if(leader, &S.pf_done);
+        // S dy^T from three pieces, S du^T from (m, m) (m, h) (h, m) (h, h)
+#pragma unroll 1
+        for (int pc = 2; pc >= 0; --pc)
+            mma_rows<DV / 16, 16384>(leader, tb + gQ, tb + gS + pc * (DV / 2), smem_u32(sX1), i64, pc < 2);
+#pragma unroll 1
+        for (int o = 0; o < 4; ++o)
+            mma_rows<DV / 16, 16384>(leader, tb + gSu, tb + gS + (o < 2) * (DV / 2),
+                                     smem_u32(o & 1 ? sX1 : sX2) + 8192, i64, o > 0);
+        mma_commit_if(leader, &S.s_done);
+    };
+    // what G gives, K^T P^T, Q^T P + K^T F, the latter two in S's place
+    auto issue_second = [&](int stage) {
+        const uint32_t leader = elect_leader();
         tc_fence_after();
-        if (tid < n_in) p.dbeta[rs.at(t0 + tid)] = S.db[tid];
-        if (warp == 15 && p.lg) {   // running sums from the block's end, two tokens a lane
-            F2 x2[2];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int t = 2 * lane + i;
-                float q = S.qdq[0][t] + S.qdq[1][t];
-                if (D > 64) q += S.qdq[2][t] + S.qdq[3][t];
-                const float d = q - S.vdv[t], z = d - q;
-                x2[i] = {d, (q - (d - z)) - (S.vdv[t] + z)};
-            }
-            float e = lane < kGThr / 32 ? S.gs[lane] : 0.f;
-            e = warp_sum(e);
-            x2[0] = f2sum2(x2[0], x2[1]);
-            F2 s = x2[0];
 #pragma unroll 1
-            for (int o = 1; o < 32; o <<= 1) {
-                const F2 y = {__shfl_down_sync(0xffffffffu, s.h, o), __shfl_down_sync(0xffffffffu, s.l, o)};
-                if (lane + o < 32) s = f2sum2(s, y);
-            }
-            F2 after = {__shfl_down_sync(0xffffffffu, s.h, 1), __shfl_down_sync(0xffffffffu, s.l, 1)};
-            if (lane == 31) after = {0.f, 0.f};
-            const F2 tail = {e, 0.f};
-            const F2 first = f2sum2(tail, s), second = f2sum2(tail, f2sum2(after, x2[1]));
-            if (2 * lane < n_in) p.dlg[rs.at(t0 + 2 * lane)] = first.h + first.l;
-            if (2 * lane + 1 < n_in) p.dlg[rs.at(t0 + 2 * lane + 1)] = second.h + second.l;
+        for (int o = 0; o < 5; ++o) {   // pieces (G, e): (h, l) (m, m) (m, h) (h, m) (h, h)
+            const uint32_t a = tb + gG + (o == 1 || o == 2 ? DV / 2 : 0);
+            if (o == 2 || o == 4)
+                mma_rows<DV / 16, 16384>(leader, tb + gGe, a, smem_u32(sX2), i64, true);
+            else
+                mma_rows<DV / 16, 8192>(leader, tb + gGe, a, smem_u32(o ? sEm : sEl), i64, o > 0);
         }
-        __syncthreads();   // the small arrays may be written again
-    }
-    if (!failed) {   // dq and dk through shared memory (the pieces' place): tokens x features
-        if (live) {
+        // features 64 .. 127 repeat the others where there are none
+        const uint32_t sk = smem_u32(sKQ) + stage * 2 * Lay::kT;
+        const uint64_t kd = smem_desc(sk, D > 64 ? 8192 : 0, 1024, kSwizzle128B);
+        const uint64_t qd = smem_desc(sk + Lay::kT, D > 64 ? 8192 : 0, 1024, kSwizzle128B);
+        const uint64_t pd = desc_k(smem_u32(sP)), ptd = desc_k(smem_u32(sPT)), fd = desc_k(smem_u32(sF));
+#pragma unroll 1
+        for (int pc = 2; pc >= 0; --pc)
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
-                const uint32_t o = (row >> 6) * 8192 + sw128_off(cg * 16 + j, row & 63);
-                *reinterpret_cast<__nv_bfloat16 *>(sX1 + o) = __float2bfloat16_rn(dq[j]);
-                *reinterpret_cast<__nv_bfloat16 *>(sX2 + o) = __float2bfloat16_rn(dk[j]);
-            }
+            for (int ks = 0; ks < kDC / 16; ++ks)
+                mma_ss_if(leader, tb + gQ2, kd + ks * 128, pd + pc * 512 + ks * 2, iT, pc < 2 || ks > 0);
+#pragma unroll 1
+        for (int o = 0; o < 4; ++o) {   // (Q, P_m) (K, F_m) (Q, P_h) (K, F_h)
+            const uint64_t a = o & 1 ? kd : qd, bd = (o & 1 ? fd : ptd) + (o < 2 ? 512 : 0);
+#pragma unroll
+            for (int ks = 0; ks < kDC / 16; ++ks)
+                mma_ss_if(leader, tb + gK2, a + ks * 128, bd + ks * 2, iT, o > 0 || ks > 0);
         }
-        fence_proxy_async();
-        __syncthreads();
-        if (tid == 0) {
+        mma_commit_if(leader, &S.all_done);
+    };
+
+    if (warp == 0 && elect_leader()) {
+        load_kq(blockIdx.x, 0);
+        load_y(blockIdx.x, 0);
+    }
+    __syncwarp();
+    {
+        const int wq = warp & 3, row = wq * 32 + lane, cg = warp >> 2;   // TMEM lane; quarter of the columns
+        const uint32_t lb = (uint32_t)(wq * 32) << 16;
+        constexpr int SC = DV / 4;   // state columns of a thread
+        const bool live = row < D;   // warp-uniform: lanes with a feature
+        const size_t st = (size_t)D * DV;
+        // A state row by row: four lines of 64 features' rows a warp (whole rows; a lane reading its
+        // own row took 50 cycles a load instruction), and from there to the lanes through P's place.
+        constexpr int LR = 32 / (DV / 4), NL = 4 / LR, kPitch = DV + 4;   // rows of a load, loads of a half
+        const int lr = warp * 4 + lane / (DV / 4), lc = lane % (DV / 4) * 4;
+        constexpr int XL = D / 64 * NL * 4;
+        auto load_rows = [&](const float *src, float (&x)[XL]) {
+#pragma unroll
+            for (int f = 0; f < D / 64; ++f)
+#pragma unroll
+                for (int i = 0; i < NL; ++i)
+                    *reinterpret_cast<float4 *>(x + (f * NL + i) * 4) = __ldg(
+                        reinterpret_cast<const float4 *>(src + (size_t)(f * 64 + lr + i * LR) * DV + lc));
+        };
+        // what load_rows left, as pieces at TMEM column `at`; every thread calls it, behind a barrier
+        // (P's place is free), and what writes there next waits for another
+        auto place = [&](bool three, const float (&x)[XL], uint32_t at) {
+            float *buf = reinterpret_cast<float *>(sP);
 #pragma unroll
             for (int f = 0; f < D / 64; ++f) {
-                tma_store_4d(&dqmap, sX1 + f * 8192, f * 64, t0, hk, b);
-                tma_store_4d(&dkmap, sX2 + f * 8192, f * 64, t0, hk, b);
+                if (f > 0) named_bar(kBarG, kGThr);
+#pragma unroll
+                for (int i = 0; i < NL; ++i)
+                    *reinterpret_cast<float4 *>(buf + (lr + i * LR) * kPitch + lc) =
+                        *reinterpret_cast<const float4 *>(x + (f * NL + i) * 4);
+                named_bar(kBarG, kGThr);
+                if ((row >> 6) == f) {
+#pragma unroll
+                    for (int i = 0; i < SC; i += 16) {
+                        float y[16];
+                        load16(buf + (row & 63) * kPitch + cg * SC + i, y);
+                        const uint32_t col = tb + lb + at + (cg * SC + i) / 2;
+                        if (three) put_pieces<16, 3>(col, DV / 2, y);
+                        else put_pieces<16, 2>(col, DV / 2, y);
+                    }
+                }
             }
-            bulk_commit();
-            bulk_wait<0>();
+        };
+        auto any_failed = [](bool f) { return __any_sync(0xffffffffu, group_any<kBarG, kGThr>(f)) != 0; };
+        // index of S before block blk of value head gi of item it's key head
+        auto head_of = [&](int it, int gi) {
+            return (size_t)(it / nblk / p.Hk) * p.H + it / nblk % p.Hk * group + gi;
+        };
+        auto s_at = [&](int it, int gi) { return p.S_ck + (head_of(it, gi) * (nblk + 1) + it % nblk) * st; };
+        // the sums over a unit's tokens, once every warp has left its epilogue
+        auto finish = [&](int it, int gi, const GradUnit &U) {
+            const int b = it / nblk / p.Hk, h = it / nblk % p.Hk * group + gi, t0 = it % nblk * kDC;
+            const int n_in = min(kDC, p.N - t0);
+            const TokenRows rs = token_rows(p.layout, b, h, p.H, p.N, 1);
+            if (tid < n_in) p.dbeta[rs.at(t0 + tid)] = U.db[tid];
+            if (warp == 15 && p.lg) {   // running sums from the block's end, two tokens a lane
+                F2 x2[2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int t = 2 * lane + i;
+                    float q = U.qdq[0][t] + U.qdq[1][t];
+                    if (D > 64) q += U.qdq[2][t] + U.qdq[3][t];
+                    const float d = q - U.vdv[t], z = d - q;
+                    x2[i] = {d, (q - (d - z)) - (U.vdv[t] + z)};
+                }
+                const float e = warp_sum(lane < kGThr / 32 ? U.gs[lane] : 0.f);
+                x2[0] = f2sum2(x2[0], x2[1]);
+                F2 s = x2[0];
+#pragma unroll 1
+                for (int o = 1; o < 32; o <<= 1) {
+                    const F2 y = {__shfl_down_sync(0xffffffffu, s.h, o), __shfl_down_sync(0xffffffffu, s.l, o)};
+                    if (lane + o < 32) s = f2sum2(s, y);
+                }
+                F2 after = {__shfl_down_sync(0xffffffffu, s.h, 1), __shfl_down_sync(0xffffffffu, s.l, 1)};
+                if (lane == 31) after = {0.f, 0.f};
+                const F2 tail = {e, 0.f}, first = f2sum2(tail, s), second = f2sum2(tail, f2sum2(after, x2[1]));
+                if (2 * lane < n_in) p.dlg[rs.at(t0 + 2 * lane)] = first.h + first.l;
+                if (2 * lane + 1 < n_in) p.dlg[rs.at(t0 + 2 * lane + 1)] = second.h + second.l;
+            }
+        };
+
+        float dq[16], dk[16];   // feature `row`, tokens 16 cg ..: sums over the value heads
+        bool failed = false;
+        int u = 0, k = 0, last_it = 0, last_gi = 0;
+        for (int it = blockIdx.x; it < p.items && !failed; it += gridDim.x, ++k) {
+            const int blk = it % nblk, b = it / nblk / p.Hk, hk = it / nblk % p.Hk;
+            const int t0 = blk * kDC, n_in = min(kDC, p.N - t0);
+            const uint8_t *sQ = sKQ + (k & 1) * 2 * Lay::kT + Lay::kT;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) dq[i] = dk[i] = 0.f;
+            for (int gi = 0; gi < group; ++gi, ++u) {
+                const int h = hk * group + gi;
+                const size_t bh = head_of(it, gi);
+                const TokenRows rv = token_rows(p.layout, b, h, p.H, p.N, DV),
+                                rs = token_rows(p.layout, b, h, p.H, p.N, 1);
+                GradUnit &U = S.unit[u & 1];
+                float x[XL];   // rows of S, later of G
+                load_rows(s_at(it, gi), x);
+                if (warp == 1) {
+                    float bv[2], gv[2];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const int t = t0 + 2 * lane + i;
+                        bv[i] = t < p.N ? p.beta[rs.at(t)] : 0.f;
+                        gv[i] = t < p.N && p.lg ? p.lg[rs.at(t)] : 0.f;
+                    }
+                    block_gates<false>(U.gates, bv, gv, lane);
+                }
+                // ---- e and du as pieces, tokens x dv; dv = b du and the tokens' sums
+#pragma unroll
+                for (int i0 = 0; i0 < DV / 64; ++i0) {
+                    const int e0 = i0 * kGThr + tid, t = e0 / (DV / 8), c = e0 % (DV / 8) * 8;
+                    float e[8], du[8];
+                    float bt = 0.f, db = 0.f, vd = 0.f;
+                    if (t < n_in) {
+                        const size_t o = (bh * p.N + t0 + t) * DV + c, ov = rv.at(t0 + t) + c;
+                        load_vec<8>(p.e + o, e);
+                        load_vec<8>(p.du + o, du);
+                        bt = p.beta[rs.at(t0 + t)];
+                        float vv[8];
+                        load_vec<8>(p.v + ov, vv);
+                        uint32_t w[4];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) w[j] = pack_bf16x2(bt * du[2 * j], bt * du[2 * j + 1]);
+                        *reinterpret_cast<uint4 *>(p.dv + ov) = make_uint4(w[0], w[1], w[2], w[3]);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            db = fmaf(du[j], e[j], db);
+                            vd = fmaf(vv[j], bt * du[j], vd);
+                        }
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) e[j] = du[j] = 0.f;
+                    }
+#pragma unroll
+                    for (int o = DV / 16; o > 0; o >>= 1) {
+                        db += __shfl_xor_sync(0xffffffffu, db, o);
+                        vd += __shfl_xor_sync(0xffffffffu, vd, o);
+                    }
+                    if (c == 0) { U.db[t] = db; U.vdv[t] = vd; }
+                    uint32_t hi[4], mi[4], lo[4];
+                    const uint32_t o16 = (c >> 6) * 16384 + sw128_off(t, c & 63),
+                                   o8 = (c >> 6) * 8192 + sw128_off(t, c & 63);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) split3(e[2 * j], e[2 * j + 1], hi[j], mi[j], lo[j]);
+                    *reinterpret_cast<uint4 *>(sX2 + o16) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                    *reinterpret_cast<uint4 *>(sEm + o8) = make_uint4(mi[0], mi[1], mi[2], mi[3]);
+                    *reinterpret_cast<uint4 *>(sEl + o8) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) split2(du[2 * j], du[2 * j + 1], hi[j], mi[j]);
+                    *reinterpret_cast<uint4 *>(sX1 + 8192 + o16) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                    *reinterpret_cast<uint4 *>(sX2 + 8192 + o16) = make_uint4(mi[0], mi[1], mi[2], mi[3]);
+                }
+                fence_proxy_async();
+                // the unit before: its accumulators lie where S goes, its sums are complete
+                if (tid == 0) bulk_wait_read<0>();   // an item's dq and dk have left P's place
+                if (u > 0) {
+                    if ((failed = any_failed(false))) break;
+                    tc_fence_after();
+                    finish(last_it, last_gi, S.unit[~u & 1]);
+                }
+                place(true, x, gS);
+                last_it = it;
+                last_gi = gi;
+                tmem_wait_st();
+                tc_fence_before();
+                // ---- G and S', in flight while the MMAs are issued
+                float y[XL];
+                load_rows(p.G_ck + (bh * nblk + blk) * st, x);
+                if (p.lg) load_rows(s_at(it, gi) + st, y);
+                bool ok = true;
+                if (warp == 0)
+                    ok = mbar_wait<1>(&S.kq_full[k & 1], (k >> 1) & 1, g, 1) && mbar_wait<1>(&S.y_full, u & 1, g, 2);
+                if ((failed = any_failed(!ok))) break;   // every operand is there
+                const int next = it + (int)gridDim.x;
+                if (warp == 0) {
+                    if (gi == 0 && next < p.items) {   // the item before has been left by all
+                        if (elect_leader()) load_kq(next, (k & 1) ^ 1);
+                        __syncwarp();
+                    }
+                    issue_first();
+                }
+                float gs = 0.f;
+                if (p.lg) {
+#pragma unroll
+                    for (int i = 0; i < XL; ++i) gs = fmaf(x[i], y[i], gs);
+                }
+                gs = warp_sum(gs);
+                if (lane == 0) U.gs[warp] = gs;
+                // ---- P, P^T and F from the scores; 16 columns of a row
+                ok = __all_sync(0xffffffffu, mbar_wait<1>(&S.pf_done, u & 1, g, 6));
+                uint32_t sc[16];
+                if (ok) {
+                    tc_fence_after();
+                    tmem_ld16(tb + lb + gPF + cg * 16, sc);
+                    if (row >= 64) {
+                        uint32_t sc2[16];
+                        tmem_ld16(tb + lb + gPF + 64 + cg * 16, sc2);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) sc[j] = f2u(u2f(sc[j]) + u2f(sc2[j]));
+                    }
+                    tmem_wait_ld();
+                    tc_fence_before();
+                }
+                if ((failed = any_failed(!ok))) break;   // the scores have been read
+                tc_fence_after();
+                place(false, x, gG);
+                named_bar(kBarG, kGThr);
+                // the next unit's values on their way
+                const int nit = gi + 1 < group ? it : next, ngi = gi + 1 < group ? gi + 1 : 0;
+                if (warp == 0 && nit < p.items && elect_leader()) {
+                    const size_t nbh = head_of(nit, ngi), nt = nbh * p.N + nit % nblk * kDC;
+                    const uint32_t bytes = min(kDC, p.N - nit % nblk * kDC) * DV * 4;
+                    prefetch_l2(s_at(nit, ngi), D * DV * 4);
+                    prefetch_l2(p.G_ck + (nbh * nblk + nit % nblk) * st, D * DV * 4);
+                    prefetch_l2(p.e + nt * DV, bytes);
+                    prefetch_l2(p.du + nt * DV, bytes);
+                }
+                __syncwarp();
+                {
+                    const int i = row & 63, j0 = cg * 16;
+                    float w[16];
+                    decayed16<false, false>(U.gates, i, j0, sc, w);
+                    if (row < 64) {
+                        uint32_t hi[8], mi[8], lo[8];
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) w[j] = j0 + j <= i ? w[j] : 0.f;
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) split3(w[2 * j], w[2 * j + 1], hi[j], mi[j], lo[j]);
+#pragma unroll
+                        for (int q = 0; q < 2; ++q) {
+                            const uint32_t o = sw128_off(i, j0 + 8 * q);
+                            *reinterpret_cast<uint4 *>(sP + o) =
+                                make_uint4(hi[4 * q], hi[4 * q + 1], hi[4 * q + 2], hi[4 * q + 3]);
+                            *reinterpret_cast<uint4 *>(sP + 8192 + o) =
+                                make_uint4(mi[4 * q], mi[4 * q + 1], mi[4 * q + 2], mi[4 * q + 3]);
+                            *reinterpret_cast<uint4 *>(sP + 16384 + o) =
+                                make_uint4(lo[4 * q], lo[4 * q + 1], lo[4 * q + 2], lo[4 * q + 3]);
+                        }
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            const uint32_t o = sw128_off(j0 + j, i), sh = (j & 1) * 16;
+                            *reinterpret_cast<uint16_t *>(sPT + o) = (uint16_t)(hi[j >> 1] >> sh);
+                            *reinterpret_cast<uint16_t *>(sPT + 8192 + o) = (uint16_t)(mi[j >> 1] >> sh);
+                        }
+                    } else {
+                        const float nb = -U.gates.b[i];
+#pragma unroll
+                        for (int j = 0; j < 16; j += 2) {
+                            uint32_t hi, mi;
+                            split2(j0 + j < i ? nb * w[j] : 0.f, j0 + j + 1 < i ? nb * w[j + 1] : 0.f, hi, mi);
+#pragma unroll
+                            for (int e = 0; e < 2; ++e)
+                                if (j0 + j + e <= i) {   // both of F_ij and F_ji (zero on the diagonal)
+                                    const uint32_t o = sw128_off(i, j0 + j + e), ot = sw128_off(j0 + j + e, i);
+                                    const uint16_t a = (uint16_t)(hi >> (16 * e)), m = (uint16_t)(mi >> (16 * e));
+                                    *reinterpret_cast<uint16_t *>(sF + o) = a;
+                                    *reinterpret_cast<uint16_t *>(sF + 8192 + o) = m;
+                                    *reinterpret_cast<uint16_t *>(sF + ot) = a;
+                                    *reinterpret_cast<uint16_t *>(sF + 8192 + ot) = m;
+                                }
+                        }
+                    }
+                }
+                fence_proxy_async();
+                tmem_wait_st();
+                tc_fence_before();
+                if (warp == 0) ok = __all_sync(0xffffffffu, mbar_wait<1>(&S.s_done, u & 1, g, 4));
+                if ((failed = any_failed(!ok))) break;
+                if (warp == 0) {
+                    if (nit < p.items) {   // dy has been used
+                        if (elect_leader()) load_y(nit, ngi);
+                        __syncwarp();
+                    }
+                    issue_second(k & 1);
+                }
+                // ---- gradients
+                ok = mbar_wait<1>(&S.kq_full[k & 1], (k >> 1) & 1, g, 7) && mbar_wait<1>(&S.all_done, u & 1, g, 8);
+                if (!__all_sync(0xffffffffu, ok)) { failed = true; }
+                if (!failed && live) {
+                    tc_fence_after();
+                    const Gates &G = U.gates;
+                    const int j0 = cg * 16;
+                    uint32_t a[16], a2[16];
+                    float c[16], w[16];
+                    tmem_ld16(tb + lb + gQ + j0, a);
+                    tmem_ld16(tb + lb + gQ2 + j0, a2);
+                    load16(&G.c[j0], c);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        const float y = fmaf(c[j], u2f(a[j]), u2f(a2[j]));
+                        dq[j] += y;
+                        const uint16_t qv =
+                            *reinterpret_cast<const uint16_t *>(sQ + (row >> 6) * 8192 + sw128_off(j0 + j, row & 63));
+                        w[j] = y * __uint_as_float((uint32_t)qv << 16);
+                    }
+                    if (p.lg) {
+                        const float s = reduce16(w, lane);
+                        if (lane < 16) U.qdq[wq][j0 + lane] = s;
+                    }
+                    tmem_ld16(tb + lb + gGe + j0, a);
+                    tmem_ld16(tb + lb + gSu + j0, a2);
+                    load16(&G.w[j0], w);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) dk[j] = fmaf(w[j], u2f(a[j]), dk[j]);
+                    load16(&G.b[j0], w);
+                    tmem_ld16(tb + lb + gK2 + j0, a);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) dk[j] += fmaf(-(w[j] * c[j]), u2f(a2[j]), u2f(a[j]));
+                    tc_fence_before();
+                }
+                if (failed) {   // every warp meets at the next barrier, or at the end
+                    any_failed(true);
+                    break;
+                }
+            }
+            if (failed) break;
+            // ---- dq and dk through P's place: tokens x features
+            if (live) {
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    const uint32_t o = (row >> 6) * 8192 + sw128_off(cg * 16 + j, row & 63);
+                    *reinterpret_cast<__nv_bfloat16 *>(sP + o) = __float2bfloat16_rn(dq[j]);
+                    *reinterpret_cast<__nv_bfloat16 *>(sP + (D / 64) * 8192 + o) = __float2bfloat16_rn(dk[j]);
+                }
+            }
+            fence_proxy_async();
+            if ((failed = any_failed(false))) break;
+            if (tid == 0) {
+#pragma unroll
+                for (int f = 0; f < D / 64; ++f) {
+                    tma_store_4d(&dqmap, sP + f * 8192, f * 64, t0, hk, b);
+                    tma_store_4d(&dkmap, sP + (D / 64 + f) * 8192, f * 64, t0, hk, b);
+                }
+                bulk_commit();
+            }
         }
-    } else if (tid == 0) {   // let copies and MMAs in flight finish
-        mma_commit(&S.all_done);
-        const uint64_t until = globaltimer_ns() + g.limit_ns;
-        while (globaltimer_ns() < until && !mbar_try_wait(&S.kq_full, 0)) {}
+        if (!failed && u > 0) finish(last_it, last_gi, S.unit[~u & 1]);   // behind the last item's barrier
+        if (tid == 0) bulk_wait<0>();
+        if (failed && warp == 0) {   // let MMAs and copies in flight finish
+            if (elect_leader()) mma_commit(&S.all_done);
+            const uint64_t until = globaltimer_ns() + g.limit_ns;
+            while (globaltimer_ns() < until && !(mbar_try_wait(&S.kq_full[k & 1], (k >> 1) & 1) &&
+                                                 mbar_try_wait(&S.y_full, u & 1))) {}
+        }
+        __syncwarp();
     }
     tc_fence_before();
     __syncthreads();
@@ -455,7 +566,7 @@ delta_grad_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
     }
 }
 
-template <int D, int DV> cudaError_t launch_grad_tc(const DeltaArgs &a) {
+template <int D, int DV, bool ONE> cudaError_t launch_grad_tc(const DeltaArgs &a) {
     CUtensorMap qm, km, ym, dqm, dkm;
     if (!encode_tokens(&qm, a.q, a.layout, a.B, a.Hk, a.N, D) ||
         !encode_tokens(&km, a.k, a.layout, a.B, a.Hk, a.N, D) ||
@@ -471,25 +582,31 @@ template <int D, int DV> cudaError_t launch_grad_tc(const DeltaArgs &a) {
     p.dv = static_cast<__nv_bfloat16 *>(a.dv_grad);
     p.dbeta = a.dbeta; p.dlg = a.dlog_gate;
     p.H = a.H; p.Hk = a.Hk; p.N = a.N; p.layout = a.layout; p.nblk = delta_blocks(a.N);
+    p.items = p.nblk * a.B * a.Hk;
     WsHeader *hdr = static_cast<WsHeader *>(a.ws);
     p.err = &hdr->error;
     p.err_where = &hdr->error_where;
     const long long lim = debug_fault().wait_limit_ns;
     p.limit_ns = lim > 0 ? (unsigned long long)lim : 1000000000ull;
-    auto kern = delta_grad_tc_kernel<D, DV>;
+    auto kern = delta_grad_tc_kernel<D, DV, ONE>;
     constexpr int smem = GradLay<D, DV>::request;
-    static_assert(smem <= 232448, "shared memory of a CTA");
+    static_assert(smem <= 232448 && 2 * (D / 64) * 8192 <= 5 * 8192, "shared memory of a CTA");
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    kern<<<(unsigned)p.nblk * a.B * a.Hk, kGThr, smem, a.stream>>>(qm, km, ym, dqm, dkm, p);
+    const int sms = num_sms();
+    kern<<<p.items < sms ? p.items : sms, kGThr, smem, a.stream>>>(qm, km, ym, dqm, dkm, p);
     return cudaGetLastError();
+}
+
+template <bool ONE> cudaError_t launch_grad_dims(const DeltaArgs &a) {
+    if (a.d == 64) return a.dv == 64 ? launch_grad_tc<64, 64, ONE>(a) : launch_grad_tc<64, 128, ONE>(a);
+    return a.dv == 64 ? launch_grad_tc<128, 64, ONE>(a) : launch_grad_tc<128, 128, ONE>(a);
 }
 
 }  // namespace
 
 cudaError_t launch_delta_grad_tc(const DeltaArgs &a) {
-    if (a.d == 64) return a.dv == 64 ? launch_grad_tc<64, 64>(a) : launch_grad_tc<64, 128>(a);
-    return a.dv == 64 ? launch_grad_tc<128, 64>(a) : launch_grad_tc<128, 128>(a);
+    return a.H == a.Hk ? launch_grad_dims<true>(a) : launch_grad_dims<false>(a);
 }
 
 }  // namespace la
