@@ -24,7 +24,8 @@
 // Roles (16 warps): warps 0-7 carry the chain (two threads a row, each half of
 // the columns; the float32 state lives in their registers); warps 8 and 9 turn
 // K K^T of the even blocks into T, warps 10 and 11 that of the odd ones, both
-// ahead of the chain; warps 12-15 turn Q K^T into P (two of them) and write y.
+// ahead of the chain; warps 12-15 turn Q K^T into P (two of them), make P e and
+// write y.
 // The rows of [K; Q] K^T are TMEM lanes, which a warp reaches by its number
 // mod 4: so odd blocks hold Q before K.  The chain's first warp issues its
 // MMAs and the TMA loads.
@@ -57,7 +58,7 @@ struct DeltaTc {
 
 struct DeltaSmall {
     Gates gates[4];
-    uint64_t kq_full[kStages], v_full[2], kk_full, kk_read, g_ready[2], t_ready[2], t_free[2], p_ready, ks_done, qs_done, e_done, s_done, pu_done, o_read, drain[3];
+    uint64_t kq_full[kStages], v_full[2], kk_full, kk_read, g_ready[2], t_ready[2], t_free[2], p_ready, ks_done, qs_done, e_done, s_done, e_read, pu_done, o_read, drain[4];
     uint32_t tmem_base;
     volatile int abort_flag;
 };
@@ -112,7 +113,7 @@ delta_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
             mbar_init(&S.g_ready[i], 32);
             mbar_init(&S.t_free[i], 1);
         }
-        for (int i = 0; i < 3; ++i) mbar_init(&S.drain[i], 1);
+        for (int i = 0; i < 4; ++i) mbar_init(&S.drain[i], 1);
         mbar_init(&S.kk_full, 1);
         mbar_init(&S.kk_read, Y ? 2 * kInner : kInner);   // a thread for each row of K, and of Q
         mbar_init(&S.p_ready, 64);
@@ -120,7 +121,8 @@ delta_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
         mbar_init(&S.qs_done, 1);
         mbar_init(&S.e_done, 1);
         mbar_init(&S.s_done, 1);
-        mbar_init(&S.pu_done, 2);       // the MMAs, and their issuer's own arrival
+        mbar_init(&S.e_read, 1);
+        mbar_init(&S.pu_done, 1);
         mbar_init(&S.o_read, kOut);
         fence_mbar_init();
         prefetch_tmap(&kmap);
@@ -333,50 +335,23 @@ delta_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
                         mma_ts_if(leader, tb + kColSD, tb + kColW + pc * 32 + ks * 8, kd + ks * 128, iS,
                                   pc < 2 || ks > 0);
                 mma_commit_if(leader, &S.s_done);
+                if (Y && leader) mbar_arrive(&S.e_read);
+                __syncwarp();
             }
-            // ---- e once more: for y's second part, P e, or to the workspace
-            if (!SEG && live) {
+            if (SAVE && live) {   // ---- e to the workspace
 #pragma unroll 1
                 for (int u = 0; u < 2; ++u) {
                     const int j0 = half * 32 + u * 16;
                     uint32_t acc[16];
                     tmem_ld16(tb + lb + kColKS + j0, acc);
                     tmem_wait_ld();
-                    if (Y) {
-                        uint32_t hi[8], mi[8];
+                    const int tok = (blk0 + n) * kDC + j0, in = p.N - tok;
+                    float *dst = p.e + ((size_t)bh * p.N + tok) * DV + row;
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) split2(u2f(acc[2 * i]), u2f(acc[2 * i + 1]), hi[i], mi[i]);
-                        const uint32_t ce = tb + lb + kColE + j0 / 2;
-                        tmem_st8(ce, hi);
-                        tmem_st8(ce + 32, mi);
-                    } else {
-                        const int tok = (blk0 + n) * kDC + j0, in = p.N - tok;
-                        float *dst = p.e + ((size_t)bh * p.N + tok) * DV + row;
-#pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            if (i < in) dst[(size_t)i * DV] = u2f(acc[i]);
-                    }
+                    for (int i = 0; i < 16; ++i)
+                        if (i < in) dst[(size_t)i * DV] = u2f(acc[i]);
                 }
-                tmem_wait_st();
                 tc_fence_before();
-            }
-            if (Y) {
-                if ((failed = any_failed(false))) break;
-                if (warp == 0) {
-                    ok = __all_sync(0xffffffffu, mbar_wait<1>(&S.p_ready, n & 1, g, 8));
-                    if (ok) {
-                        const uint32_t leader = elect_leader();
-                        tc_fence_after();
-                        const uint32_t sp = smem_u32(sP);
-#pragma unroll 1
-                        for (int o = 0; o < 3; ++o)   // pieces (e, P): (0, 1) (1, 0) (0, 0)
-                            mma_rows<kDC / 16, 0>(leader, tb + kColKS, tb + kColE + (o == 1) * 32,
-                                                  sp + (o == 0) * 8192, i64, o > 0);
-                        mma_commit_if(leader, &S.pu_done);
-                        if (leader) mbar_arrive(&S.pu_done);
-                        __syncwarp();
-                    }
-                }
             }
             ok = ok && mbar_wait<1>(&S.s_done, n & 1, g, 9);
             ok = __all_sync(0xffffffffu, ok);
@@ -595,12 +570,46 @@ delta_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
         }
         for (int n = 0; n < nblk; ++n) {
             const Gates &G = S.gates[n & 3];
-            bool ok = good;
+            // the gates, for the warps that have not waited for them with the scores (waiting again
+            // could miss the phase: the next block's scores let the one after them come)
+            bool ok = good && (rows_of_q(n) || mbar_wait<1>(&S.g_ready[n & 1], (n >> 1) & 1, g, 31));
             const bool next = n + 1 < nblk && rows_of_q(n + 1);
             if (next) ok = ok && read_scores(n + 1);
-            ok = ok && mbar_wait<1>(&S.pu_done, n & 1, g, 30);
+            ok = ok && mbar_wait<1>(&S.e_done, n & 1, g, 32);
+            ok = ok && mbar_wait<1>(&S.qs_done, n & 1, g, 33);
             ok = __all_sync(0xffffffffu, ok);
+            if (ok && row < DV) {   // e as two pieces, in the place of the state's
+                tc_fence_after();
+#pragma unroll 1
+                for (int j0 = 0; j0 < kDC; j0 += 16) {
+                    uint32_t acc[16], hi[8], mi[8];
+                    tmem_ld16(tb + lb + kColKS + j0, acc);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) split2(u2f(acc[2 * i]), u2f(acc[2 * i + 1]), hi[i], mi[i]);
+                    tmem_st8(tb + lb + kColE + j0 / 2, hi);
+                    tmem_st8(tb + lb + kColE + j0 / 2 + 32, mi);
+                }
+                tmem_wait_st();
+                tc_fence_before();
+            }
             if (tid == kChain + 2 * kInner) bulk_wait_read<0>();   // the last y has left its tile
+            if (__any_sync(0xffffffffu, group_any<kBarOut, kOut>(!ok))) break;
+            if (warp == 12) {   // P e over e, which the chain has read
+                ok = mbar_wait<1>(&S.p_ready, n & 1, g, 8) && mbar_wait<1>(&S.e_read, n & 1, g, 34);
+                ok = __all_sync(0xffffffffu, ok);
+                if (ok) {
+                    const uint32_t leader = elect_leader();
+                    tc_fence_after();
+                    const uint32_t sp = smem_u32(sP);
+#pragma unroll 1
+                    for (int o = 0; o < 3; ++o)   // pieces (e, P): (0, 1) (1, 0) (0, 0)
+                        mma_rows<kDC / 16, 0>(leader, tb + kColKS, tb + kColE + (o == 1) * 32, sp + (o == 0) * 8192,
+                                              i64, o > 0);
+                    mma_commit_if(leader, &S.pu_done);
+                }
+            }
+            ok = ok && mbar_wait<1>(&S.pu_done, n & 1, g, 30);
             if (__any_sync(0xffffffffu, group_any<kBarOut, kOut>(!ok))) break;
             tc_fence_after();
             if (row < DV) {   // y = c . (Q S) + P e, 16 rows x 32 tokens at a time, through shared memory
@@ -641,6 +650,10 @@ delta_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
             if (next) make_p(n + 1);
         }
         if (tid == kChain + 2 * kInner) bulk_wait<0>();
+        if (warp == 12 && elect_leader()) {
+            mma_commit(&S.drain[3]);
+            drain_wait(&S.drain[3], 0, g.limit_ns);
+        }
         __syncwarp();
     }
     tc_fence_before();
