@@ -555,6 +555,8 @@ delta_rev_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
         tc_fence_after();
         tmem_dealloc(tb, 512);
     }
+    // what follows in the stream waits for this kernel, and so for the states' pass beside it
+    griddep_wait();
 }
 
 template <int D, int DV> cudaError_t launch_rev(const DeltaArgs &a) {
@@ -580,8 +582,8 @@ template <int D, int DV> cudaError_t launch_rev(const DeltaArgs &a) {
     static_assert(smem <= 232448, "shared memory of a CTA");
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    kern<<<a.B * a.H, kChain + 2 * kInner + kOut, smem, a.stream>>>(qm, km, ym, p);
-    return cudaGetLastError();
+    // beside the states' pass, where the heads leave SMs idle
+    return launch_overlapped(kern, dim3(a.B * a.H), dim3(kChain + 2 * kInner + kOut), smem, a.stream, qm, km, ym, p);
 }
 
 }  // namespace

@@ -104,6 +104,7 @@ delta_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
     const int blk0 = seg * p.seg_blocks, nblk = min(p.seg_blocks, p.nblk - blk0);   // blocks of this item
     const Guard g{&S.abort_flag, p.err, p.err_where, p.limit_ns};
 
+    if (SAVE) griddep_launch_dependents();   // the reverse pass needs nothing of this one
     if (tid == 0) {
         S.abort_flag = 0;
         for (int i = 0; i < kStages; ++i) mbar_init(&S.kq_full[i], 1);
