@@ -464,7 +464,9 @@ LA_API la_status la_forward_delta(const void *q, const void *k, const void *v, v
 /*
  * Workspace size in bytes for la_backward_delta (0 for N == 0 and for
  * unsupported arguments): a status header, the states and their gradients at
- * every 64th token, and two float32 rows of dv per token.
+ * every 64th token, two float32 rows of dv per token and, when few heads make
+ * the call split the sequence into segments, their states and maps; so it
+ * depends on the current device's SM count.
  */
 LA_API size_t la_delta_backward_workspace_bytes(int B, int H, int Hk, int N, int d, int dv,
                                                 la_dtype dt);

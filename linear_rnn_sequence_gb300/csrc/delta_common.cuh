@@ -56,9 +56,10 @@ template <int N> __device__ __forceinline__ void load_vec(const __nv_bfloat16 *p
 }
 
 // Workspace of the gradients, in floats behind the status header: the states before each block and
-// the final one, their gradients after each block, e and du of every token (head-major).
+// the final one, their gradients after each block, e and du of every token (head-major), and what
+// a split of the sequence takes.
 struct DeltaBwdWs {
-    float *S, *G, *e, *du;
+    float *S, *G, *e, *du, *split;
 };
 __host__ __device__ __forceinline__ int delta_blocks(int N) { return (N + kDeltaC - 1) / kDeltaC; }
 inline DeltaBwdWs delta_bwd_ws(const DeltaArgs &a) {
@@ -68,6 +69,7 @@ inline DeltaBwdWs delta_bwd_ws(const DeltaArgs &a) {
     w.G = w.S + BH * (nc + 1) * st;
     w.e = w.G + BH * nc * st;
     w.du = w.e + BH * a.N * a.dv;
+    w.split = w.du + BH * a.N * a.dv;
     return w;
 }
 

@@ -282,13 +282,13 @@ template <typename T> cudaError_t launch_grad_t(const DeltaArgs &a) {
 
 size_t delta_backward_workspace(const DeltaArgs &a) {
     const size_t BH = (size_t)a.B * a.H, nc = delta_blocks(a.N), st = (size_t)a.d * a.dv;
-    return sizeof(WsHeader) + 4 * (BH * (2 * nc + 1) * st + 2 * BH * a.N * a.dv);
+    return sizeof(WsHeader) + 4 * (BH * (2 * nc + 1) * st + 2 * BH * a.N * a.dv +
+                                   (delta_tc_supported(a) ? delta_tc_split_floats(a) : 0));
 }
 
 cudaError_t launch_delta_backward(const DeltaArgs &a) {
     if (delta_tc_supported(a)) {
-        cudaError_t e = launch_delta_states_tc(a);
-        if (e == cudaSuccess) e = launch_delta_reverse_tc(a);
+        const cudaError_t e = launch_delta_passes_tc(a);
         return e == cudaSuccess ? launch_delta_grad_tc(a) : e;
     }
     cudaError_t e = launch_delta_states_simt(a);

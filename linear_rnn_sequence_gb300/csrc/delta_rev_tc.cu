@@ -29,9 +29,11 @@ constexpr uint32_t kColKK = 448;
 struct RevTc {
     const float *beta, *lg;
     int H, group, N, layout, nblk;
-    const float *dS_out;
+    int nseg, seg_blocks;          // segments of a head, blocks of one
+    const float *G_end;            // by (head, segment); null: zero
     float *dS_in;
     float *G_ck, *du;
+    float *G_local;                // LOCAL, by (head, segment)
     unsigned int *err, *err_where;
     unsigned long long limit_ns;
     int drop_item;
@@ -50,8 +52,9 @@ template <int D, int DV> struct RevLay {
     static constexpr int request = total + 1024;
 };
 
-// n counts steps: step n is block nblk - 1 - n.
-template <int D, int DV>
+// n counts steps: step n is block nblk - 1 - n of the item's segment.  LOCAL: segments but the first
+// of each head, from a zero G at their ends, leaving G at their starts and nothing else.
+template <int D, int DV, bool LOCAL>
 __global__ void __launch_bounds__(kChain + 2 * kInner + kOut, 1)
 delta_rev_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                  const __grid_constant__ CUtensorMap ymap, const RevTc p) {
@@ -61,8 +64,10 @@ delta_rev_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
     RevSmall &S = *reinterpret_cast<RevSmall *>(sm + Lay::oSmall);
     uint8_t *sKQ = sm + Lay::oKQ, *sV = sm + Lay::oV, *sT = sm + Lay::oT, *sP = sm + Lay::oP;
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
-    const int bh = blockIdx.x, b = bh / p.H, h = bh - b * p.H, hk = h / p.group;
-    const int nblk = p.nblk;
+    const int segs = LOCAL ? p.nseg - 1 : p.nseg, bh = blockIdx.x / segs, seg = blockIdx.x - bh * segs + (LOCAL ? 1 : 0);
+    const int b = bh / p.H, h = bh - b * p.H, hk = h / p.group;
+    const int blk0 = seg * p.seg_blocks, nblk = min(p.seg_blocks, p.nblk - blk0);   // blocks of this item
+    const size_t item = (size_t)bh * p.nseg + seg;
     const Guard g{&S.abort_flag, p.err, p.err_where, p.limit_ns};
 
     if (tid == 0) {
@@ -112,9 +117,9 @@ delta_rev_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
             uint64_t *bar = &S.kq_full[n % kStages];
             mbar_arrive_expect_tx(bar, 2 * kDC * D * 2);
             ++kq_issued;
-            if (n == 0 && bh == p.drop_item) return;   // test hook: announced, never issued
+            if (n == 0 && (int)blockIdx.x == p.drop_item) return;   // test hook: announced, never issued
             uint8_t *dst = sKQ + (n % kStages) * Lay::kKQ;
-            const int tok = (nblk - 1 - n) * kDC;
+            const int tok = (blk0 + nblk - 1 - n) * kDC;
 #pragma unroll
             for (int f = 0; f < D / 64; ++f) {
                 tma_load_4d(dst + f * 16384 + (n & 1) * 8192, &kmap, bar, f * 64, tok, hk, b);
@@ -128,7 +133,7 @@ delta_rev_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
             uint8_t *dst = sV + (n & 1) * Lay::kV;
 #pragma unroll
             for (int f = 0; f < DV / 64; ++f)
-                tma_load_4d(dst + f * 8192, &ymap, bar, f * 64, (nblk - 1 - n) * kDC, h, b);
+                tma_load_4d(dst + f * 8192, &ymap, bar, f * 64, (blk0 + nblk - 1 - n) * kDC, h, b);
         };
         if (warp == 0 && elect_leader()) {   // always the same lane: it keeps the counts
             for (int n = 0; n < kStages && n < nblk; ++n) {
@@ -138,9 +143,10 @@ delta_rev_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
         }
         __syncwarp();
         float st[SC];
-        const size_t sbase = (size_t)bh * D * DV + (size_t)half * SC * DV + row;
+        const size_t sbase = (size_t)half * SC * DV + row;
 #pragma unroll
-        for (int i = 0; i < SC; ++i) st[i] = live && p.dS_out ? p.dS_out[sbase + (size_t)i * DV] : 0.f;
+        for (int i = 0; i < SC; ++i)
+            st[i] = !LOCAL && live && p.G_end ? p.G_end[item * D * DV + sbase + (size_t)i * DV] : 0.f;
         auto write_state = [&](float *dst) {
 #pragma unroll
             for (int i = 0; i < SC; ++i) dst[(size_t)i * DV] = st[i];
@@ -155,11 +161,11 @@ delta_rev_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
             tmem_st8(col + D / 2, mi);
             tmem_st8(col + D, lo);
         };
-        float *gck = p.G_ck + ((size_t)bh * nblk + nblk - 1) * D * DV + (size_t)half * SC * DV + row;
+        float *gck = LOCAL ? nullptr : p.G_ck + ((size_t)bh * p.nblk + blk0 + nblk - 1) * D * DV + sbase;
         if (live) {
 #pragma unroll
             for (int i = 0; i < SC; i += 16) put_state(i);
-            write_state(gck);
+            if (!LOCAL) write_state(gck);
         }
         tmem_wait_st();
         tc_fence_before();
@@ -349,18 +355,24 @@ delta_rev_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
                 }
                 tmem_wait_st();
                 tc_fence_before();
-                gck -= D * DV;
-                if (n + 1 < nblk) write_state(gck);
+                if (!LOCAL) {
+                    gck -= D * DV;
+                    if (n + 1 < nblk) write_state(gck);
+                }
             }
             failed = any_failed(!ok);
         }
-        if (!failed && live && p.dS_in) write_state(p.dS_in + sbase);
+        if (LOCAL) {
+            if (!failed && live) write_state(p.G_local + item * D * DV + sbase);
+        } else if (!failed && live && p.dS_in && seg == 0) {
+            write_state(p.dS_in + (size_t)bh * D * DV + sbase);
+        }
         if (warp == 0 && elect_leader()) {
             mma_commit(&S.drain[0]);
             drain_wait(&S.drain[0], 0, g.limit_ns);
             if (S.abort_flag) {   // let the copies in flight land
                 for (int n = max(0, kq_issued - kStages); n < kq_issued; ++n)
-                    if (!(n == 0 && bh == p.drop_item))
+                    if (!(n == 0 && (int)blockIdx.x == p.drop_item))
                         drain_wait(&S.kq_full[n % kStages], (n / kStages) & 1, g.limit_ns);
                 for (int n = max(0, v_issued - 2); n < v_issued; ++n)
                     drain_wait(&S.v_full[n & 1], (n >> 1) & 1, g.limit_ns);
@@ -378,7 +390,7 @@ delta_rev_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
         auto fetch = [&](int n) {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const int tok = (nblk - 1 - n) * kDC + 2 * lane + i;
+                const int tok = (blk0 + nblk - 1 - n) * kDC + 2 * lane + i;
                 bv[i] = tok < p.N ? p.beta[rs.at(tok)] : 0.f;
                 gv[i] = tok < p.N && p.lg ? p.lg[rs.at(tok)] : 0.f;
             }
@@ -531,8 +543,8 @@ delta_rev_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
             ok = ok && __all_sync(0xffffffffu, mbar_wait<1>(&S.e_done, n & 1, g, 30));
             if (!ok) break;
             tc_fence_after();
-            if (row < DV) {
-                const int t0 = (nblk - 1 - n) * kDC, in = p.N - t0;
+            if (!LOCAL && row < DV) {
+                const int t0 = (blk0 + nblk - 1 - n) * kDC, in = p.N - t0;
                 float *dst = p.du + ((size_t)bh * p.N + t0) * DV + row;
 #pragma unroll 1
                 for (int j0 = 0; j0 < kDC; j0 += 16) {
@@ -559,7 +571,8 @@ delta_rev_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
     griddep_wait();
 }
 
-template <int D, int DV> cudaError_t launch_rev(const DeltaArgs &a) {
+template <int D, int DV, bool LOCAL>
+cudaError_t launch_rev(const DeltaArgs &a, int nseg, int seg_blocks, const float *G_end, float *G_local) {
     CUtensorMap qm, km, ym;
     if (!encode_tokens(&qm, a.q, a.layout, a.B, a.Hk, a.N, D) ||
         !encode_tokens(&km, a.k, a.layout, a.B, a.Hk, a.N, D) ||
@@ -569,7 +582,8 @@ template <int D, int DV> cudaError_t launch_rev(const DeltaArgs &a) {
     RevTc p{};
     p.beta = a.beta; p.lg = a.log_gate;
     p.H = a.H; p.group = a.H / a.Hk; p.N = a.N; p.layout = a.layout; p.nblk = delta_blocks(a.N);
-    p.dS_out = a.dS_out; p.dS_in = a.dS_in;
+    p.nseg = nseg; p.seg_blocks = seg_blocks;
+    p.G_end = G_end; p.dS_in = a.dS_in; p.G_local = G_local;
     p.G_ck = w.G; p.du = w.du;
     WsHeader *hdr = static_cast<WsHeader *>(a.ws);
     p.err = &hdr->error;
@@ -577,20 +591,29 @@ template <int D, int DV> cudaError_t launch_rev(const DeltaArgs &a) {
     const long long lim = debug_fault().wait_limit_ns;
     p.limit_ns = lim > 0 ? (unsigned long long)lim : 1000000000ull;
     p.drop_item = debug_fault().drop_load_item;
-    auto kern = delta_rev_kernel<D, DV>;
+    auto kern = delta_rev_kernel<D, DV, LOCAL>;
     constexpr int smem = RevLay<D, DV>::request;
     static_assert(smem <= 232448, "shared memory of a CTA");
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    // beside the states' pass, where the heads leave SMs idle
-    return launch_overlapped(kern, dim3(a.B * a.H), dim3(kChain + 2 * kInner + kOut), smem, a.stream, qm, km, ym, p);
+    // beside the pass launched before it, of which it needs nothing, where the heads leave SMs idle
+    return launch_overlapped(kern, dim3(a.B * a.H * (LOCAL ? nseg - 1 : nseg)), dim3(kChain + 2 * kInner + kOut),
+                             smem, a.stream, qm, km, ym, p);
+}
+template <int D, int DV>
+cudaError_t launch_rev_any(const DeltaArgs &a, int nseg, int seg_blocks, const float *G_end, float *G_local) {
+    return G_local ? launch_rev<D, DV, true>(a, nseg, seg_blocks, G_end, G_local)
+                   : launch_rev<D, DV, false>(a, nseg, seg_blocks, G_end, G_local);
 }
 
 }  // namespace
 
-cudaError_t launch_delta_reverse_tc(const DeltaArgs &a) {
-    if (a.d == 64) return a.dv == 64 ? launch_rev<64, 64>(a) : launch_rev<64, 128>(a);
-    return a.dv == 64 ? launch_rev<128, 64>(a) : launch_rev<128, 128>(a);
+cudaError_t launch_delta_reverse_tc(const DeltaArgs &a, int nseg, int seg_blocks, const float *G_end, float *G_local) {
+    if (a.d == 64)
+        return a.dv == 64 ? launch_rev_any<64, 64>(a, nseg, seg_blocks, G_end, G_local)
+                          : launch_rev_any<64, 128>(a, nseg, seg_blocks, G_end, G_local);
+    return a.dv == 64 ? launch_rev_any<128, 64>(a, nseg, seg_blocks, G_end, G_local)
+                      : launch_rev_any<128, 128>(a, nseg, seg_blocks, G_end, G_local);
 }
 
 }  // namespace la

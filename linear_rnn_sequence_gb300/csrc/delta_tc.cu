@@ -46,11 +46,12 @@ constexpr uint32_t kColKK = 448;                // [K; Q] K^T or, for odd blocks
 struct DeltaTc {
     const float *beta, *lg;
     int H, group, N, layout, nblk;
-    int nseg, seg_blocks, parts;   // segments of a head, blocks of one, CTAs of one (kSegment)
+    int nseg, seg_blocks;          // segments of a head, blocks of one
+    int seg_items, parts;          // kSegment: segments of a head it takes, CTAs of one
     const float *S_in;             // by (head, segment)
     float *S_out;                  // by head
     float *S_ck, *e;               // kSave
-    float *S_local, *Phi;          // kSegment, by (head, segment but the last)
+    float *S_local, *Phi;          // kSegment, by (head, its segment)
     unsigned int *err, *err_where;
     unsigned long long limit_ns;
     int drop_item;
@@ -99,12 +100,12 @@ delta_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     constexpr bool Y = MODE == kForward, SAVE = MODE == kSave, SEG = MODE == kSegment;
     const int part = SEG ? blockIdx.x % p.parts : 0, item = SEG ? blockIdx.x / p.parts : blockIdx.x;
-    const int segs = SEG ? p.nseg - 1 : p.nseg, bh = item / segs, seg = item - bh * segs;
+    const int segs = SEG ? p.seg_items : p.nseg, bh = item / segs, seg = item - bh * segs;
     const int b = bh / p.H, h = bh - b * p.H, hk = h / p.group;
     const int blk0 = seg * p.seg_blocks, nblk = min(p.seg_blocks, p.nblk - blk0);   // blocks of this item
     const Guard g{&S.abort_flag, p.err, p.err_where, p.limit_ns};
 
-    if (SAVE) griddep_launch_dependents();   // the reverse pass needs nothing of this one
+    if (!Y) griddep_launch_dependents();   // a reverse pass that needs nothing of this launch
     if (tid == 0) {
         S.abort_flag = 0;
         for (int i = 0; i < kStages; ++i) mbar_init(&S.kq_full[i], 1);
@@ -665,13 +666,21 @@ delta_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
     }
 }
 
-// States at the segments' starts: P_0 = S_in (or 0), P_{s+1} = Phi_s P_s + S_local_s.  16 columns a
-// CTA, walking the segments; a float32 product of [D x D] by [D x 16] a step.
+// States at the segments' starts: P_0 = S_in (or 0), P_{s+1} = Phi_s P_s + S_local_s; with
+// blockIdx.z = 1 their gradients at the segments' ends, G_{s-1} = Phi_s^T G_s + G_local_s from
+// G_{nseg-1} = dS_out (or 0).  16 columns a CTA, walking the segments; a float32 product of [D x D]
+// by [D x 16] a step.  Phi and the local ends are `items` to a head, P and G nseg.
 constexpr int kPrefixCols = 16, kPrefixThr = 256;
+struct PrefixArgs {
+    const float *Phi, *local[2], *first[2];
+    float *P[2];
+    int nseg, items, DV;
+};
 template <int D>
-__global__ void __launch_bounds__(kPrefixThr)
-delta_prefix_kernel(const float *__restrict__ Phi, const float *__restrict__ S_local,
-                    const float *__restrict__ S_in, float *__restrict__ P, int nseg, int DV) {
+__global__ void __launch_bounds__(kPrefixThr) delta_prefix_kernel(const PrefixArgs p) {
+    const int nseg = p.nseg, DV = p.DV, rev = blockIdx.z;
+    const float *__restrict__ Phi = p.Phi, *__restrict__ S_in = p.first[rev], *__restrict__ S_local = p.local[rev];
+    float *__restrict__ P = p.P[rev];
     constexpr int NC = kPrefixCols * D / kPrefixThr;   // columns of a thread (a row of Phi each)
     __shared__ float Ps[D][kPrefixCols], F[D][33];
     const int bh = blockIdx.x, c0 = blockIdx.y * kPrefixCols;
@@ -680,20 +689,25 @@ delta_prefix_kernel(const float *__restrict__ Phi, const float *__restrict__ S_l
     float x[NC];
 #pragma unroll
     for (int j = 0; j < NC; ++j) x[j] = S_in ? S_in[bh * st + at + j] : 0.f;
-    for (int s = 0;; ++s) {
+    for (int k = 0;; ++k) {
+        const int s = rev ? nseg - 1 - k : k;
 #pragma unroll
         for (int j = 0; j < NC; ++j) {
             Ps[i][c + j] = x[j];
             P[((size_t)bh * nseg + s) * st + at + j] = x[j];
         }
-        if (s == nseg - 1) break;
-        const size_t item = (size_t)bh * (nseg - 1) + s;
+        if (k == nseg - 1) break;
+        const size_t item = (size_t)bh * p.items + s;
 #pragma unroll
         for (int j = 0; j < NC; ++j) x[j] = S_local[item * st + at + j];
         for (int a0 = 0; a0 < D; a0 += 32) {
             __syncthreads();
-            for (int k = threadIdx.x; k < D * 32; k += kPrefixThr)
-                F[k / 32][k % 32] = Phi[item * D * D + (size_t)(k / 32) * D + a0 + k % 32];
+            for (int e = threadIdx.x; e < D * 32; e += kPrefixThr) {
+                if (rev)
+                    F[e % D][e / D] = Phi[item * D * D + (size_t)(a0 + e / D) * D + e % D];
+                else
+                    F[e / 32][e % 32] = Phi[item * D * D + (size_t)(e / 32) * D + a0 + e % 32];
+            }
             __syncthreads();
 #pragma unroll 8
             for (int a = 0; a < 32; ++a) {
@@ -731,6 +745,32 @@ void delta_segments(const DeltaArgs &a, int &nseg, int &seg_blocks) {
     }
 }
 
+// The same for the gradients: the segments' ends and maps, then the states' pass and the local
+// reverse pass, then the reverse pass, against the reverse pass alone with the states' beside it.
+// Block times of the passes: 1, 1, 1.3, 1.4; every pass fills the SMs or takes its chain's length.
+void delta_bwd_segments(const DeltaArgs &a, int &nseg, int &seg_blocks) {
+    const int nblk = delta_blocks(a.N), sms = num_sms(), parts = (a.dv + a.d + 127) / 128;
+    const double BH = (double)a.B * a.H;
+    auto most = [](double x, double y) { return x > y ? x : y; };
+    nseg = 1;
+    seg_blocks = nblk;
+    double best = most(1.4 * nblk, 2.4 * BH * nblk / sms);
+    for (int s = 2; s <= 64 && 2 * s <= nblk; ++s) {
+        const int len = (nblk + s - 1) / s, n = (nblk + len - 1) / len;
+        if (n != s) continue;
+        const double cost = most(3.7 * len, (parts + 3.7) * BH * s * len / sms) + 16 + 0.5 * s;
+        if (cost < best) {
+            best = cost;
+            nseg = s;
+            seg_blocks = len;
+        }
+    }
+}
+// Floats of the split's arrays: by (head, segment) a map, and four states.
+size_t delta_bwd_split_floats(const DeltaArgs &a, int nseg) {
+    return nseg > 1 ? (size_t)a.B * a.H * nseg * ((size_t)a.d * a.d + 4 * (size_t)a.d * a.dv) : 0;
+}
+
 template <int D, int DV, int MODE> cudaError_t launch_tc(const DeltaArgs &a, DeltaTc p) {
     CUtensorMap qm, km, vm, ym{};
     if (!encode_tokens(&qm, a.q, a.layout, a.B, a.Hk, a.N, D) ||
@@ -743,12 +783,17 @@ template <int D, int DV, int MODE> cudaError_t launch_tc(const DeltaArgs &a, Del
     static_assert(smem <= 232448, "shared memory of a CTA");
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    const int ctas = a.B * a.H * (MODE == kSegment ? (p.nseg - 1) * p.parts : p.nseg);
+    const int ctas = a.B * a.H * (MODE == kSegment ? p.seg_items * p.parts : p.nseg);
     kern<<<ctas, kChain + 2 * kInner + (MODE == kForward ? kOut : 0), smem, a.stream>>>(qm, km, vm, ym, p);
     return cudaGetLastError();
 }
 
-template <int D, int DV> cudaError_t launch_dims(const DeltaArgs &a, bool save) {
+template <int D> cudaError_t launch_prefix(const DeltaArgs &a, const PrefixArgs &x, int ways) {
+    delta_prefix_kernel<D><<<dim3(a.B * a.H, a.dv / kPrefixCols, ways), kPrefixThr, 0, a.stream>>>(x);
+    return cudaGetLastError();
+}
+
+template <int D, int DV> DeltaTc tc_params(const DeltaArgs &a) {
     DeltaTc p{};
     p.beta = a.beta; p.lg = a.log_gate;
     p.H = a.H; p.group = a.H / a.Hk; p.N = a.N; p.layout = a.layout; p.nblk = delta_blocks(a.N);
@@ -760,31 +805,54 @@ template <int D, int DV> cudaError_t launch_dims(const DeltaArgs &a, bool save) 
     const long long lim = debug_fault().wait_limit_ns;
     p.limit_ns = lim > 0 ? (unsigned long long)lim : 1000000000ull;
     p.drop_item = debug_fault().drop_load_item;
-    if (save) {
-        const DeltaBwdWs w = delta_bwd_ws(a);
-        p.S_ck = w.S;
-        p.e = w.e;
-        return launch_tc<D, DV, kSave>(a, p);
-    }
+    return p;
+}
+
+template <int D, int DV> cudaError_t launch_forward(const DeltaArgs &a) {
+    DeltaTc p = tc_params<D, DV>(a);
     delta_segments(a, p.nseg, p.seg_blocks);
     if (p.nseg > 1) {
-        const size_t items = (size_t)a.B * a.H * (p.nseg - 1);
+        p.seg_items = p.nseg - 1;
+        const size_t items = (size_t)a.B * a.H * p.seg_items;
         p.S_local = reinterpret_cast<float *>(static_cast<char *>(a.ws) + sizeof(WsHeader));
         p.Phi = p.S_local + items * D * DV;
         float *P = p.Phi + items * D * D;
         cudaError_t e = launch_tc<D, DV, kSegment>(a, p);
+        if (e == cudaSuccess)
+            e = launch_prefix<D>(a, {p.Phi, {p.S_local, nullptr}, {a.S_in, nullptr}, {P, nullptr}, p.nseg,
+                                     p.seg_items, DV}, 1);
         if (e != cudaSuccess) return e;
-        delta_prefix_kernel<D><<<dim3(a.B * a.H, DV / kPrefixCols), kPrefixThr, 0, a.stream>>>(
-            p.Phi, p.S_local, a.S_in, P, p.nseg, DV);
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
         p.S_in = P;
     }
     return launch_tc<D, DV, kForward>(a, p);
 }
 
-cudaError_t launch_all(const DeltaArgs &a, bool save) {
-    if (a.d == 64) return a.dv == 64 ? launch_dims<64, 64>(a, save) : launch_dims<64, 128>(a, save);
-    return a.dv == 64 ? launch_dims<128, 64>(a, save) : launch_dims<128, 128>(a, save);
+// e, the states and their gradients at every block (and dS_in).
+template <int D, int DV> cudaError_t launch_passes(const DeltaArgs &a) {
+    const DeltaBwdWs w = delta_bwd_ws(a);
+    DeltaTc p = tc_params<D, DV>(a);
+    p.S_ck = w.S;
+    p.e = w.e;
+    delta_bwd_segments(a, p.nseg, p.seg_blocks);
+    cudaError_t e = cudaSuccess;
+    const float *G_end = a.dS_out;
+    if (p.nseg > 1) {
+        p.seg_items = p.nseg;
+        const size_t items = (size_t)a.B * a.H * p.nseg, st = (size_t)D * DV;
+        p.Phi = w.split;
+        p.S_local = p.Phi + items * D * D;
+        float *P = p.S_local + items * st, *G_local = P + items * st, *GP = G_local + items * st;
+        e = launch_tc<D, DV, kSegment>(a, p);
+        if (e == cudaSuccess) e = launch_delta_reverse_tc(a, p.nseg, p.seg_blocks, nullptr, G_local);
+        if (e == cudaSuccess)
+            e = launch_prefix<D>(a, {p.Phi, {p.S_local, G_local}, {a.S_in, a.dS_out}, {P, GP}, p.nseg,
+                                     p.seg_items, DV}, 2);
+        if (e != cudaSuccess) return e;
+        p.S_in = P;
+        G_end = GP;
+    }
+    e = launch_tc<D, DV, kSave>(a, p);
+    return e == cudaSuccess ? launch_delta_reverse_tc(a, p.nseg, p.seg_blocks, G_end, nullptr) : e;
 }
 
 }  // namespace
@@ -803,7 +871,18 @@ size_t delta_tc_workspace(const DeltaArgs &a) {
     }
     return sizeof(WsHeader) + 4 * floats;
 }
-cudaError_t launch_delta_forward_tc(const DeltaArgs &a) { return launch_all(a, false); }
-cudaError_t launch_delta_states_tc(const DeltaArgs &a) { return launch_all(a, true); }
+size_t delta_tc_split_floats(const DeltaArgs &a) {
+    int nseg, len;
+    delta_bwd_segments(a, nseg, len);
+    return delta_bwd_split_floats(a, nseg);
+}
+cudaError_t launch_delta_forward_tc(const DeltaArgs &a) {
+    if (a.d == 64) return a.dv == 64 ? launch_forward<64, 64>(a) : launch_forward<64, 128>(a);
+    return a.dv == 64 ? launch_forward<128, 64>(a) : launch_forward<128, 128>(a);
+}
+cudaError_t launch_delta_passes_tc(const DeltaArgs &a) {
+    if (a.d == 64) return a.dv == 64 ? launch_passes<64, 64>(a) : launch_passes<64, 128>(a);
+    return a.dv == 64 ? launch_passes<128, 64>(a) : launch_passes<128, 128>(a);
+}
 
 }  // namespace la

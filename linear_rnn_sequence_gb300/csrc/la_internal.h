@@ -173,8 +173,11 @@ cudaError_t launch_delta_reverse_simt(const DeltaArgs &a);   // and its second
 bool delta_tc_supported(const DeltaArgs &a);
 size_t delta_tc_workspace(const DeltaArgs &a);   // depends on the current device's SM count
 cudaError_t launch_delta_forward_tc(const DeltaArgs &a);
-cudaError_t launch_delta_states_tc(const DeltaArgs &a);
-cudaError_t launch_delta_reverse_tc(const DeltaArgs &a);
+size_t delta_tc_split_floats(const DeltaArgs &a);   // of the gradients' workspace; likewise
+// the gradients' recurrent passes; and the reverse one by segments, from G_end (null: zero) at each
+// segment's end -- or, with G_local, from zero, leaving only the gradient at each segment's start
+cudaError_t launch_delta_passes_tc(const DeltaArgs &a);
+cudaError_t launch_delta_reverse_tc(const DeltaArgs &a, int nseg, int seg_blocks, const float *G_end, float *G_local);
 cudaError_t launch_delta_grad_tc(const DeltaArgs &a);
 size_t delta_backward_workspace(const DeltaArgs &a);
 cudaError_t launch_delta_backward(const DeltaArgs &a);

@@ -616,7 +616,7 @@ def _delta_bytes(device_index, *sizes):   # the split depends on the current dev
 
 
 @functools.lru_cache(maxsize=1024)
-def _delta_backward_bytes(*sizes):
+def _delta_backward_bytes(device_index, *sizes):
     return int(lib().la_delta_backward_workspace_bytes(*sizes))
 
 
@@ -696,7 +696,7 @@ def backward_delta(q, k, v, beta, dy, log_gate=None, S_in=None, grad_S_out=None,
     gS = None
     if S_in is not None or grad_S_out is not None:
         gS = torch.empty(state, dtype=torch.float32, device=q.device)
-    workspace, wa, wbytes = _workspace(workspace, _delta_backward_bytes(*sizes), q)
+    workspace, wa, wbytes = _workspace(workspace, _delta_backward_bytes(dev, *sizes), q)
     st = lib().la_backward_delta(qa, ka, va, _expect("dy", dy, v.shape, v.dtype, dev), ba, la, gq.data_ptr(),
                                  gk.data_ptr(), gv.data_ptr(), gb.data_ptr(), _addr(gl), B, H, Hk, N, d, dv,
                                  dt, LAYOUT[layout], _expect("S_in", S_in, state, torch.float32, dev),

@@ -109,6 +109,7 @@ def test_few_heads_and_many_tokens(d, dv, gate, N):
     y, S = gpu_forward(x, "bnhd", return_state=True)
     y2, S2 = gpu_forward(x, "bnhd", return_state=True)
     assert torch.equal(y, y2) and torch.equal(S, S2)
+    check_backward(x, BF16, "bnhd")
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
