@@ -330,3 +330,103 @@ def test_captured_and_on_another_stream(dtype):
     n = la.layer_norm(y, w, stream=s)
     s.synchronize()
     assert torch.equal(y, want2[0]) and torch.equal(n, want2[2])
+
+
+# ---- run-time failure, without a GPU fault --------------------------------------
+@pytest.mark.parametrize("what,B,H,N", [("forward", 1, 4, 200), ("forward", 1, 2, 4000), ("forward", 40, 4, 130),
+                                         ("backward", 1, 4, 200), ("backward", 1, 2, 4000)])
+def test_a_dropped_copy_times_out_and_the_next_call_is_right(what, B, H, N):
+    """The test hook announces one work item's first tile copy and never issues it: every wait on it
+    runs out, the call records LA_ERR_TIMEOUT, and the context stays usable."""
+    x = on_gpu(R.inputs(B, H, H, N, 64, 64, BF16, seed=41))
+    dy = torch.randn_like(x["v"])
+
+    def call():
+        if what == "forward":
+            return (la.forward_delta(**x, check_status=True),)
+        return la.backward_delta(x["q"], x["k"], x["v"], x["beta"], dy, x["log_gate"], check_status=True)[:5]
+
+    want = call()
+    try:
+        la.set_fault(drop_load_item=1, wait_limit_ns=5_000_000)
+        with pytest.raises(la.LinAttnError) as e:
+            call()
+        assert e.value.status == la.LA_ERR_TIMEOUT
+    finally:
+        la.set_fault(-1, 0)
+    assert all(torch.equal(a, b) for a, b in zip(call(), want))
+
+
+# ---- what the binding refuses ----------------------------------------------------
+def test_binding_refuses():
+    x = on_gpu(R.inputs(1, 4, 2, 40, 64, 64, BF16, state=True))
+    bad = [dict(k=x["k"].float()), dict(v=x["v"][:, :, :39].contiguous()), dict(beta=x["beta"].double()),
+           dict(beta=x["beta"][:, :2].contiguous()), dict(log_gate=x["log_gate"].bfloat16()),
+           dict(S_in=x["S_in"].bfloat16()), dict(S_in=x["S_in"][:, :1].contiguous()), dict(layout="nbhd"),
+           dict(q=x["q"].transpose(2, 3)), dict(v=x["v"].transpose(1, 2).contiguous().transpose(1, 2)),
+           dict(out=x["v"].float()), dict(beta=x["beta"].cpu())]
+    for change in bad:
+        with pytest.raises(ValueError):
+            la.forward_delta(**{**x, **change})
+    with pytest.raises(TypeError):
+        la.forward_delta(**{n: t.half() if n in "qkv" else t for n, t in x.items()})
+    with pytest.raises(la.LinAttnError) as e:   # three heads of v to two of q
+        la.forward_delta(x["q"], x["k"], x["v"][:, :3].contiguous(), x["beta"][:, :3].contiguous())
+    assert e.value.status == la.LA_ERR_INVALID_ARG
+    with pytest.raises(la.LinAttnError) as e:   # over one of its inputs
+        la.forward_delta(**x, out=x["v"])
+    assert e.value.status == la.LA_ERR_INVALID_ARG
+    with pytest.raises(la.LinAttnError) as e:   # rows that start 2 bytes off a 16-byte boundary
+        buf = torch.zeros(x["v"].numel() + 1, dtype=BF16, device="cuda")
+        la.forward_delta(**x, out=buf[1:].view(x["v"].shape))
+    assert e.value.status == la.LA_ERR_INVALID_ARG
+    with pytest.raises(la.LinAttnError) as e:
+        la.backward_delta(x["q"], x["k"], x["v"], x["beta"], x["v"], x["log_gate"],
+                          workspace=torch.empty(1024, dtype=torch.uint8, device="cuda"))
+    assert e.value.status == la.LA_ERR_WORKSPACE
+    with pytest.raises(ValueError):
+        la.layer_norm(torch.zeros(3, 8, device="cuda"), torch.zeros(7, device="cuda"))
+    with pytest.raises(la.LinAttnError):
+        la.layer_norm(torch.zeros(2, 16385, device="cuda"))
+
+
+def test_values_behind_the_inputs_are_not_read():
+    """NaN in memory on either side of every input."""
+    def guarded(t):
+        if t is None:
+            return None
+        buf = torch.full((t.numel() + 2 * 4096,), float("nan"), dtype=t.dtype, device="cuda")
+        view = buf[4096:4096 + t.numel()].view(t.shape)
+        view.copy_(t)
+        return view
+
+    for dtype in (BF16, F32):
+        for N in (1, 70, 300):
+            x = on_gpu(R.inputs(2, 2, 1, N, 64, 64, dtype, state=True, seed=N))
+            g = {n: guarded(t) for n, t in x.items()}
+            dy = torch.randn_like(x["v"])
+            assert all(torch.equal(a, b) for a, b in zip(la.forward_delta(**g, return_state=True),
+                                                         la.forward_delta(**x, return_state=True)))
+            args = ("q", "k", "v", "beta")
+            a = la.backward_delta(*(g[n] for n in args), guarded(dy), g["log_gate"], S_in=g["S_in"])
+            b = la.backward_delta(*(x[n] for n in args), dy, x["log_gate"], S_in=x["S_in"])
+            assert all(torch.equal(s, t) for s, t in zip(a, b))
+
+
+def test_two_calls_in_flight_on_two_streams():
+    xs = [on_gpu(R.inputs(1, 4, 4, 700, 64, 64, BF16, seed=50 + i)) for i in range(2)]
+    dys = [torch.randn_like(x["v"]) for x in xs]
+
+    def call(i, stream=None):
+        x = xs[i]
+        return [la.forward_delta(**x, stream=stream),
+                *la.backward_delta(x["q"], x["k"], x["v"], x["beta"], dys[i], x["log_gate"], stream=stream)[:5]]
+
+    want = [call(0), call(1)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(3):
+        got = [call(i, streams[i]) for i in range(2)]
+        torch.cuda.synchronize()
+        for g, w in zip(got, want):
+            assert all(torch.equal(a, b) for a, b in zip(g, w))
