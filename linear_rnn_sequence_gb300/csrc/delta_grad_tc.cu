@@ -20,7 +20,9 @@
 // operands and accumulators into gradients; warp 0 also issues the MMAs and
 // copies, and has the next unit's float32 values brought into L2 meanwhile.
 // (A warp of its own for that leaves 96 registers a thread, and spills; so does
-// the next unit's S in registers.)
+// the next unit's S in registers.)  B8 H16 N8192 d128: 1.65 ms, 15.6 us a unit
+// and SM; the conversions and the MMAs of a unit follow one another, TMEM and
+// shared memory having no room for a second one.
 #include "delta_tc.cuh"
 
 namespace la {
