@@ -553,32 +553,22 @@ def random_features(x, W, out=None, stream=None):
 
 
 # ---- gated delta rule, layer norm -------------------------------------------
-def _on_device(fn):
-    """Run ``fn`` with its first argument's device and, if given, ``stream`` current, so that what
-    it allocates belongs to the device and stream that use it."""
-    first = fn.__code__.co_varnames[0]
-
-    @functools.wraps(fn)
-    def call(*args, stream=None, **kw):
-        t = args[0] if args else kw[first]
-        if not t.is_cuda:
-            raise ValueError("tensors must be CUDA tensors (no CPU fallback)")
-        if stream is None and t.get_device() == _current_device():
-            return fn(*args, **kw)
-        if stream is not None and stream.device != t.device:
-            raise ValueError("the stream is of another device than the tensors")
-        with torch.cuda.device(t.device), torch.cuda.stream(stream):
-            return fn(*args, **kw)
-    return call
-
-
-# Small calls cost mostly this module's own time, so its checks read each property once.
-_current_device = torch.cuda.current_device
-
-
-# the stream's handle without a Stream object around it, where torch offers that
+# Small calls cost mostly this module's own time, so the calls below read each property once, and take
+# the device's index and the stream's handle without the objects around them where torch offers that.
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda device_index: torch.cuda.current_stream(device_index).cuda_stream)
+
+
+def _elsewhere(fn, stream, t, *args, **kw):
+    """``fn`` with ``t``'s device and, if given, ``stream`` current, so that what it allocates belongs
+    to the device and stream that use it."""
+    if not t.is_cuda:
+        raise ValueError("tensors must be CUDA tensors (no CPU fallback)")
+    if stream is not None and stream.device != t.device:
+        raise ValueError("the stream is of another device than the tensors")
+    with torch.cuda.device(t.device), torch.cuda.stream(stream):
+        return fn(t, *args, **kw)
 
 
 def _addr(t):
@@ -650,9 +640,8 @@ def _delta_inputs(q, k, v, beta, log_gate, layout):
     return (B, H, Hk, N, d, dv, _dtype_code(q)), dev, at
 
 
-@_on_device
 def forward_delta(q, k, v, beta, log_gate=None, S_in=None, return_state=False, out=None,
-                  S_out=None, layout="bhnd", workspace=None, check_status=False):
+                  S_out=None, layout="bhnd", workspace=None, check_status=False, stream=None):
     """The gated delta rule, causal:
     S_t = a_t (I - b_t k_t k_t^T) S_{t-1} + b_t k_t v_t^T, y_t = S_t^T q_t, a_t = exp(log_gate_t).
 
@@ -661,6 +650,9 @@ def forward_delta(q, k, v, beta, log_gate=None, S_in=None, return_state=False, o
     them.  Returns y in v's shape and dtype (and the final state [B,H,d,dv], float32, when
     ``return_state``).  S_in: the initial state; S_out may be S_in.
     """
+    if stream is not None or not q.is_cuda or q.get_device() != _current_device():
+        return _elsewhere(forward_delta, stream, q, k, v, beta, log_gate, S_in, return_state, out, S_out, layout,
+                          workspace, check_status)
     sizes, dev, (qa, ka, va, ba, la) = _delta_inputs(q, k, v, beta, log_gate, layout)
     B, H, Hk, N, d, dv, dt = sizes
     state = (B, H, d, dv)
@@ -680,14 +672,16 @@ def forward_delta(q, k, v, beta, log_gate=None, S_in=None, return_state=False, o
     return (out, S_out) if return_state else out
 
 
-@_on_device
 def backward_delta(q, k, v, beta, dy, log_gate=None, S_in=None, grad_S_out=None, layout="bhnd",
-                   workspace=None, check_status=False):
+                   workspace=None, check_status=False, stream=None):
     """Gradients of ``forward_delta`` for dy = dL/dy (dtype and shape of v) and grad_S_out = dL/dS
     of the final state (None: zero).  Returns (grad_q, grad_k, grad_v, grad_beta, grad_log_gate,
     grad_S_in): the first three in the inputs' dtype, the others float32; grad_log_gate is None
     without log_gate, grad_S_in is None unless S_in or grad_S_out is given.
     """
+    if stream is not None or not q.is_cuda or q.get_device() != _current_device():
+        return _elsewhere(backward_delta, stream, q, k, v, beta, dy, log_gate, S_in, grad_S_out, layout, workspace,
+                          check_status)
     sizes, dev, (qa, ka, va, ba, la) = _delta_inputs(q, k, v, beta, log_gate, layout)
     B, H, Hk, N, d, dv, dt = sizes
     state = (B, H, d, dv)
@@ -708,11 +702,12 @@ def backward_delta(q, k, v, beta, dy, log_gate=None, S_in=None, grad_S_out=None,
     return gq, gk, gv, gb, gl, gS
 
 
-@_on_device
-def decode_step_delta(q, k, v, beta, S, log_gate=None, S_out=None, out=None):
+def decode_step_delta(q, k, v, beta, S, log_gate=None, S_out=None, out=None, stream=None):
     """One token of ``forward_delta``: q, k [B,Hk,d]; v [B,H,dv]; beta, log_gate [B,H] float32;
     S [B,H,d,dv] float32, updated in place unless ``S_out`` is given.  Returns y [B,H,dv] in v's dtype.
     """
+    if stream is not None or not q.is_cuda or q.get_device() != _current_device():
+        return _elsewhere(decode_step_delta, stream, q, k, v, beta, S, log_gate, S_out, out)
     shape, vs = q.shape, v.shape
     if len(shape) != 3 or len(vs) != 3:
         raise ValueError("q, k and v must have three dimensions")
@@ -732,18 +727,19 @@ def decode_step_delta(q, k, v, beta, S, log_gate=None, S_out=None, out=None):
     return out
 
 
-@_on_device
-def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, return_stats=False, out=None):
+def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, return_stats=False, out=None, stream=None):
     """(x - mean) * rstd * weight + bias over the last dimension (at most 16384 values, bf16 or
     fp32); weight, bias: float32 [D] or None.  Returns y in x's dtype (and mean, rstd, float32 in
     x's shape without its last dimension, when ``return_stats``).  ``out`` may be x."""
+    if stream is not None or not x.is_cuda or x.get_device() != _current_device():
+        return _elsewhere(layer_norm, stream, x, weight, bias, eps, return_stats, out)
     shape, dev, f32 = x.shape, x.get_device(), torch.float32
     D = shape[-1]
     if out is None:
         out = torch.empty_like(x)
     mean = rstd = None
     if return_stats:
-        mean = torch.empty(shape[:-1], dtype=f32, device=x.device)
+        mean = x.new_empty(shape[:-1], dtype=f32)
         rstd = torch.empty_like(mean)
     st = lib().la_layer_norm(_expect("x", x, shape, x.dtype, dev), _expect("out", out, shape, x.dtype, dev),
                              _expect("weight", weight, (D,), f32, dev), _expect("bias", bias, (D,), f32, dev),
@@ -758,11 +754,12 @@ def _norm_backward_bytes(device_index, rows, D, dt):   # as many sums as the dev
     return int(lib().la_layer_norm_backward_workspace_bytes(rows, D, dt))
 
 
-@_on_device
-def layer_norm_backward(dy, x, mean, rstd, weight=None, sums=None, workspace=None):
+def layer_norm_backward(dy, x, mean, rstd, weight=None, sums=None, workspace=None, stream=None):
     """Gradients of ``layer_norm`` from its mean and rstd: (grad_x, grad_weight, grad_bias), the
     first in x's dtype, the sums float32 [D].  ``sums`` says whether to compute the latter two
     (default: when weight is given); they are None otherwise."""
+    if stream is not None or not dy.is_cuda or dy.get_device() != _current_device():
+        return _elsewhere(layer_norm_backward, stream, dy, x, mean, rstd, weight, sums, workspace)
     shape, dev, f32 = x.shape, x.get_device(), torch.float32
     D, dt = shape[-1], _dtype_code(x)
     gx = torch.empty_like(x)
@@ -770,7 +767,7 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, sums=None, workspace=Non
     gw = gb = wa = None
     wbytes = 0
     if weight is not None if sums is None else sums:
-        gw = torch.empty(D, dtype=f32, device=x.device)
+        gw = x.new_empty(D, dtype=f32)
         gb = torch.empty_like(gw)
         workspace, wa, wbytes = _workspace(workspace, _norm_backward_bytes(dev, rows, D, dt), x)
     st = lib().la_layer_norm_backward(_expect("dy", dy, shape, x.dtype, dev), _expect("x", x, shape, x.dtype, dev),
