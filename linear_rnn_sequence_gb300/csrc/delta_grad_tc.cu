@@ -29,9 +29,9 @@ namespace la {
 namespace {
 
 constexpr int kGThr = 512, kBarG = 1;
-// TMEM columns: pieces of S (3 DV/2); the scores' two accumulators, then the pieces of G (2 DV/2);
-// S dy^T, G e^T, S du^T.  K^T P^T and Q^T P + K^T F take the place of S.
-constexpr uint32_t gS = 0, gPF = 192, gG = 192, gQ = 320, gGe = 384, gSu = 448, gQ2 = 0, gK2 = 64;
+// TMEM columns: pieces of S (3 DV/2); the scores' two accumulators, then two pieces of G (2 DV/2);
+// S dy^T; the third piece of G; S du^T.  K^T P^T, Q^T P + K^T F and G e^T take the place of S.
+constexpr uint32_t gS = 0, gPF = 192, gG = 192, gQ = 320, gGl = 384, gSu = 448, gQ2 = 0, gK2 = 64, gGe = 128;
 
 struct GradTc {
     const float *beta, *lg, *S_ck, *G_ck, *e, *du;
@@ -48,35 +48,34 @@ struct GradUnit {   // what a unit leaves for the sums over its tokens
 };
 struct GradSmall {
     GradUnit unit[2];
-    uint64_t kq_full[2], y_full, pf_done, s_done, all_done;
+    uint64_t kq_full, y_full, sg_full, pf_done, s_done, all_done, drained;
     uint32_t tmem_base;
+    int loads[3];   // issued to the first three
     volatile int abort_flag;
 };
 template <int D, int DV> struct GradLay {
     static constexpr int kT = (D / 64) * 8192;            // K or Q, slabs of 64 features
     static constexpr int kX = (DV / 64) * 16384;          // per 64 columns: 64 rows, 64 rows
     static constexpr int kE = (DV / 64) * 8192;
-    static constexpr int oKQ = 0, oX1 = 4 * kT, oX2 = oX1 + kX, oEm = oX2 + kX, oEl = oEm + kE,
-                         oP = oEl + kE, oPT = oP + 3 * 8192, oF = oPT + 2 * 8192, oSmall = oF + 2 * 8192;
+    static constexpr int kSG = D * DV * 4;                // S or G; P, P^T and F take its place
+    static constexpr int kStage = 2 * kT;                 // dq and dk: e's lower pieces' place where it fits
+    static constexpr int oKQ = 0, oX1 = 2 * kT, oX2 = oX1 + kX, oEm = oX2 + kX, oEl = oEm + kE,
+                         oSG = oEl + kE, oPT = oSG + 3 * 8192, oF = oPT + 2 * 8192,
+                         oEnd = oSG + (kSG > 7 * 8192 ? kSG : 7 * 8192),
+                         oStage = kStage <= 2 * kE ? oEm : oEnd,
+                         oSmall = oEnd + (kStage <= 2 * kE ? 0 : kStage);
     static constexpr int total = oSmall + (int)sizeof(GradSmall);
     static constexpr int request = total + 1024;
 };
 
-// Columns of x (one row of a thread, COLS of them) as NP pieces into TMEM, `stride` columns apart.
-template <int COLS, int NP>
-__device__ __forceinline__ void put_pieces(uint32_t at, uint32_t stride, const float (&x)[COLS]) {
+// 16 columns of a thread's row as three pieces into TMEM: `stride` columns apart, and at `low`.
+__device__ __forceinline__ void put_pieces(uint32_t at, uint32_t stride, uint32_t low, const float (&x)[16]) {
+    uint32_t hi[8], mi[8], lo[8];
 #pragma unroll
-    for (int i = 0; i < COLS; i += 16) {
-        uint32_t hi[8], mi[8], lo[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            if (NP == 3) split3(x[i + 2 * j], x[i + 2 * j + 1], hi[j], mi[j], lo[j]);
-            else split2(x[i + 2 * j], x[i + 2 * j + 1], hi[j], mi[j]);
-        }
-        tmem_st8(at + i / 2, hi);
-        tmem_st8(at + stride + i / 2, mi);
-        if (NP == 3) tmem_st8(at + 2 * stride + i / 2, lo);
-    }
+    for (int j = 0; j < 8; ++j) split3(x[2 * j], x[2 * j + 1], hi[j], mi[j], lo[j]);
+    tmem_st8(at, hi);
+    tmem_st8(at + stride, mi);
+    tmem_st8(low, lo);
 }
 
 // Sum of x[t] over the warp's 32 lanes for t = 0 .. 15; lanes 0 .. 15 get that of t = lane.
@@ -98,22 +97,26 @@ template <int D, int DV, bool ONE>
 __global__ void __launch_bounds__(kGThr, 1)
 delta_grad_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                      const __grid_constant__ CUtensorMap ymap, const __grid_constant__ CUtensorMap dqmap,
-                     const __grid_constant__ CUtensorMap dkmap, const GradTc p) {
+                     const __grid_constant__ CUtensorMap dkmap, const __grid_constant__ CUtensorMap smap,
+                     const __grid_constant__ CUtensorMap gmap, const GradTc p) {
     using Lay = GradLay<D, DV>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     GradSmall &S = *reinterpret_cast<GradSmall *>(sm + Lay::oSmall);
     uint8_t *sKQ = sm + Lay::oKQ, *sX1 = sm + Lay::oX1, *sX2 = sm + Lay::oX2, *sEm = sm + Lay::oEm,
-            *sEl = sm + Lay::oEl, *sP = sm + Lay::oP, *sPT = sm + Lay::oPT, *sF = sm + Lay::oF;
+            *sEl = sm + Lay::oEl, *sSG = sm + Lay::oSG, *sP = sSG, *sPT = sm + Lay::oPT, *sF = sm + Lay::oF,
+            *sStage = sm + Lay::oStage;
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const int nblk = p.nblk, group = ONE ? 1 : p.H / p.Hk;
     const Guard g{&S.abort_flag, p.err, p.err_where, p.limit_ns};
 
     if (tid == 0) {
         S.abort_flag = 0;
-        mbar_init(&S.kq_full[0], 1);
-        mbar_init(&S.kq_full[1], 1);
+        mbar_init(&S.kq_full, 1);
         mbar_init(&S.y_full, 1);
+        mbar_init(&S.sg_full, 1);
+        mbar_init(&S.drained, 1);
+        S.loads[0] = S.loads[1] = S.loads[2] = 0;
         mbar_init(&S.pf_done, 1);
         mbar_init(&S.s_done, 1);
         mbar_init(&S.all_done, 1);
@@ -129,28 +132,40 @@ delta_grad_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
     const uint32_t tb = __shfl_sync(0xffffffffu, S.tmem_base, 0);
 
     constexpr uint32_t i64 = idesc_bf16(128, kDC, 0, 0), iT = idesc_bf16(128, kDC, 1, 0);
-    auto load_kq = [&](int it, int stage) {
-        uint64_t *bar = &S.kq_full[stage];
+    auto load_kq = [&](int it) {
         const int t0 = it % nblk * kDC, b = it / nblk / p.Hk, hk = it / nblk % p.Hk;
-        mbar_arrive_expect_tx(bar, 2 * kDC * D * 2);
+        mbar_arrive_expect_tx(&S.kq_full, 2 * kDC * D * 2);
+        ++S.loads[0];
 #pragma unroll
         for (int f = 0; f < D / 64; ++f) {
-            tma_load_4d(sKQ + stage * 2 * Lay::kT + f * 8192, &kmap, bar, f * 64, t0, hk, b);
-            tma_load_4d(sKQ + stage * 2 * Lay::kT + Lay::kT + f * 8192, &qmap, bar, f * 64, t0, hk, b);
+            tma_load_4d(sKQ + f * 8192, &kmap, &S.kq_full, f * 64, t0, hk, b);
+            tma_load_4d(sKQ + Lay::kT + f * 8192, &qmap, &S.kq_full, f * 64, t0, hk, b);
         }
     };
     auto load_y = [&](int it, int gi) {
         const int t0 = it % nblk * kDC, b = it / nblk / p.Hk, h = it / nblk % p.Hk * group + gi;
         mbar_arrive_expect_tx(&S.y_full, kDC * DV * 2);
+        ++S.loads[1];
 #pragma unroll
         for (int f = 0; f < DV / 64; ++f) tma_load_4d(sX1 + f * 16384, &ymap, &S.y_full, f * 64, t0, h, b);
     };
+    // index of value head gi of item it's key head
+    auto head_of = [&](int it, int gi) { return (size_t)(it / nblk / p.Hk) * p.H + it / nblk % p.Hk * group + gi; };
+    // S before a unit's block, or G after it: slabs of 32 columns
+    auto load_sg = [&](bool G, int it, int gi) {
+        const int at = (int)(head_of(it, gi) * (nblk + !G)) + it % nblk;
+        mbar_arrive_expect_tx(&S.sg_full, Lay::kSG);
+        ++S.loads[2];
+#pragma unroll
+        for (int f = 0; f < DV / 32; ++f)
+            tma_load_3d(sSG + f * D * 128, G ? &gmap : &smap, &S.sg_full, f * 32, 0, at);
+    };
     // scores, and what S gives
     auto issue_first = [&]() {
-        const uint32_t leader = elect_leader();
         tc_fence_after();
         const uint64_t x1 = desc_k(smem_u32(sX1)), x2 = desc_k(smem_u32(sX2));
         // [dy; du_h] (e_l, e_m, e_h), small ones first, and du_m e_h (the upper rows unused)
+        uint32_t leader = elect_leader();
 #pragma unroll 1
         for (int o = 0; o < 4; ++o) {
             const bool eh = o >= 2;
@@ -163,37 +178,45 @@ delta_grad_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
         }
         mma_commit_if(leader, &S.pf_done);
         // S dy^T from three pieces, S du^T from (m, m) (m, h) (h, m) (h, h)
+        leader = elect_leader();
 #pragma unroll 1
         for (int pc = 2; pc >= 0; --pc)
             mma_rows<DV / 16, 16384>(leader, tb + gQ, tb + gS + pc * (DV / 2), smem_u32(sX1), i64, pc < 2);
+        leader = elect_leader();
 #pragma unroll 1
         for (int o = 0; o < 4; ++o)
             mma_rows<DV / 16, 16384>(leader, tb + gSu, tb + gS + (o < 2) * (DV / 2),
                                      smem_u32(o & 1 ? sX1 : sX2) + 8192, i64, o > 0);
         mma_commit_if(leader, &S.s_done);
     };
-    // what G gives, K^T P^T, Q^T P + K^T F, the latter two in S's place
-    auto issue_second = [&](int stage) {
+    // what G gives, where the lowest pieces of S were
+    auto issue_g = [&]() {
         const uint32_t leader = elect_leader();
         tc_fence_after();
 #pragma unroll 1
-        for (int o = 0; o < 5; ++o) {   // pieces (G, e): (h, l) (m, m) (m, h) (h, m) (h, h)
-            const uint32_t a = tb + gG + (o == 1 || o == 2 ? DV / 2 : 0);
-            if (o == 2 || o == 4)
-                mma_rows<DV / 16, 16384>(leader, tb + gGe, a, smem_u32(sX2), i64, true);
+        for (int o = 0; o < 6; ++o) {   // pieces (G, e): (l, h) (h, l) (m, m) (m, h) (h, m) (h, h)
+            const uint32_t a = tb + (o == 0 ? gGl : gG + (o == 2 || o == 3 ? DV / 2 : 0));
+            if (o == 0 || o == 3 || o == 5)
+                mma_rows<DV / 16, 16384>(leader, tb + gGe, a, smem_u32(sX2), i64, o > 0);
             else
-                mma_rows<DV / 16, 8192>(leader, tb + gGe, a, smem_u32(o ? sEm : sEl), i64, o > 0);
+                mma_rows<DV / 16, 8192>(leader, tb + gGe, a, smem_u32(o == 1 ? sEl : sEm), i64, true);
         }
+    };
+    // K^T P^T, Q^T P + K^T F in S's place
+    auto issue_second = [&]() {
+        tc_fence_after();
         // features 64 .. 127 repeat the others where there are none
-        const uint32_t sk = smem_u32(sKQ) + stage * 2 * Lay::kT;
+        const uint32_t sk = smem_u32(sKQ);
         const uint64_t kd = smem_desc(sk, D > 64 ? 8192 : 0, 1024, kSwizzle128B);
         const uint64_t qd = smem_desc(sk + Lay::kT, D > 64 ? 8192 : 0, 1024, kSwizzle128B);
         const uint64_t pd = desc_k(smem_u32(sP)), ptd = desc_k(smem_u32(sPT)), fd = desc_k(smem_u32(sF));
+        uint32_t leader = elect_leader();
 #pragma unroll 1
         for (int pc = 2; pc >= 0; --pc)
 #pragma unroll
             for (int ks = 0; ks < kDC / 16; ++ks)
                 mma_ss_if(leader, tb + gQ2, kd + ks * 128, pd + pc * 512 + ks * 2, iT, pc < 2 || ks > 0);
+        leader = elect_leader();
 #pragma unroll 1
         for (int o = 0; o < 4; ++o) {   // (Q, P_m) (K, F_m) (Q, P_h) (K, F_h)
             const uint64_t a = o & 1 ? kd : qd, bd = (o & 1 ? fd : ptd) + (o < 2 ? 512 : 0);
@@ -205,8 +228,9 @@ delta_grad_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
     };
 
     if (warp == 0 && elect_leader()) {
-        load_kq(blockIdx.x, 0);
+        load_kq(blockIdx.x);
         load_y(blockIdx.x, 0);
+        load_sg(false, blockIdx.x, 0);
     }
     __syncwarp();
     {
@@ -215,49 +239,17 @@ delta_grad_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
         constexpr int SC = DV / 4;   // state columns of a thread
         const bool live = row < D;   // warp-uniform: lanes with a feature
         const size_t st = (size_t)D * DV;
-        // A state row by row: four lines of 64 features' rows a warp (whole rows; a lane reading its
-        // own row took 50 cycles a load instruction), and from there to the lanes through P's place.
-        constexpr int LR = 32 / (DV / 4), NL = 4 / LR, kPitch = DV + 4;   // rows of a load, loads of a half
-        const int lr = warp * 4 + lane / (DV / 4), lc = lane % (DV / 4) * 4;
-        constexpr int XL = D / 64 * NL * 4;
-        auto load_rows = [&](const float *src, float (&x)[XL]) {
+        // A thread's columns of its row of S or G: chunks of 16 bytes at c ^ (row & 7) of their slab, so
+        // that eight lanes' reads spread over all banks.
+        auto row16 = [&](int i, float (&x)[16]) {   // columns cg SC + i ..
+            const int c = cg * SC + i;
+            const uint8_t *at = sSG + (c >> 5) * D * 128 + row * 128;
 #pragma unroll
-            for (int f = 0; f < D / 64; ++f)
-#pragma unroll
-                for (int i = 0; i < NL; ++i)
-                    *reinterpret_cast<float4 *>(x + (f * NL + i) * 4) = __ldg(
-                        reinterpret_cast<const float4 *>(src + (size_t)(f * 64 + lr + i * LR) * DV + lc));
-        };
-        // what load_rows left, as pieces at TMEM column `at`; every thread calls it, behind a barrier
-        // (P's place is free), and what writes there next waits for another
-        auto place = [&](bool three, const float (&x)[XL], uint32_t at) {
-            float *buf = reinterpret_cast<float *>(sP);
-#pragma unroll
-            for (int f = 0; f < D / 64; ++f) {
-                if (f > 0) named_bar(kBarG, kGThr);
-#pragma unroll
-                for (int i = 0; i < NL; ++i)
-                    *reinterpret_cast<float4 *>(buf + (lr + i * LR) * kPitch + lc) =
-                        *reinterpret_cast<const float4 *>(x + (f * NL + i) * 4);
-                named_bar(kBarG, kGThr);
-                if ((row >> 6) == f) {
-#pragma unroll
-                    for (int i = 0; i < SC; i += 16) {
-                        float y[16];
-                        load16(buf + (row & 63) * kPitch + cg * SC + i, y);
-                        const uint32_t col = tb + lb + at + (cg * SC + i) / 2;
-                        if (three) put_pieces<16, 3>(col, DV / 2, y);
-                        else put_pieces<16, 2>(col, DV / 2, y);
-                    }
-                }
-            }
+            for (int j = 0; j < 4; ++j)
+                *reinterpret_cast<float4 *>(x + 4 * j) =
+                    *reinterpret_cast<const float4 *>(at + ((((c & 31) >> 2) + j) ^ (row & 7)) * 16);
         };
         auto any_failed = [](bool f) { return __any_sync(0xffffffffu, group_any<kBarG, kGThr>(f)) != 0; };
-        // index of S before block blk of value head gi of item it's key head
-        auto head_of = [&](int it, int gi) {
-            return (size_t)(it / nblk / p.Hk) * p.H + it / nblk % p.Hk * group + gi;
-        };
-        auto s_at = [&](int it, int gi) { return p.S_ck + (head_of(it, gi) * (nblk + 1) + it % nblk) * st; };
         // the sums over a unit's tokens, once every warp has left its epilogue
         auto finish = [&](int it, int gi, const GradUnit &U) {
             const int b = it / nblk / p.Hk, h = it / nblk % p.Hk * group + gi, t0 = it % nblk * kDC;
@@ -296,7 +288,6 @@ delta_grad_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
         for (int it = blockIdx.x; it < p.items && !failed; it += gridDim.x, ++k) {
             const int blk = it % nblk, b = it / nblk / p.Hk, hk = it / nblk % p.Hk;
             const int t0 = blk * kDC, n_in = min(kDC, p.N - t0);
-            const uint8_t *sQ = sKQ + (k & 1) * 2 * Lay::kT + Lay::kT;
 #pragma unroll
             for (int i = 0; i < 16; ++i) dq[i] = dk[i] = 0.f;
             for (int gi = 0; gi < group; ++gi, ++u) {
@@ -305,44 +296,46 @@ delta_grad_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
                 const TokenRows rv = token_rows(p.layout, b, h, p.H, p.N, DV),
                                 rs = token_rows(p.layout, b, h, p.H, p.N, 1);
                 GradUnit &U = S.unit[u & 1];
-                float x[XL];   // rows of S, later of G
-                load_rows(s_at(it, gi), x);
-                if (warp == 1) {
-                    float bv[2], gv[2];
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const int t = t0 + 2 * lane + i;
-                        bv[i] = t < p.N ? p.beta[rs.at(t)] : 0.f;
-                        gv[i] = t < p.N && p.lg ? p.lg[rs.at(t)] : 0.f;
-                    }
-                    block_gates<false>(U.gates, bv, gv, lane);
-                }
                 // ---- e and du as pieces, tokens x dv; dv = b du and the tokens' sums
+                constexpr int NT = DV / 64;
+                float e[NT][8], du[NT][8], bt[NT];
+                uint4 vw[NT];
 #pragma unroll
-                for (int i0 = 0; i0 < DV / 64; ++i0) {
-                    const int e0 = i0 * kGThr + tid, t = e0 / (DV / 8), c = e0 % (DV / 8) * 8;
-                    float e[8], du[8];
-                    float bt = 0.f, db = 0.f, vd = 0.f;
+                for (int i = 0; i < NT; ++i) {   // on their way while the unit before is finished
+                    const int e0 = i * kGThr + tid, t = e0 / (DV / 8), c = e0 % (DV / 8) * 8;
+                    bt[i] = 0.f;
+                    vw[i] = make_uint4(0u, 0u, 0u, 0u);
                     if (t < n_in) {
-                        const size_t o = (bh * p.N + t0 + t) * DV + c, ov = rv.at(t0 + t) + c;
-                        load_vec<8>(p.e + o, e);
-                        load_vec<8>(p.du + o, du);
-                        bt = p.beta[rs.at(t0 + t)];
-                        float vv[8];
-                        load_vec<8>(p.v + ov, vv);
-                        uint32_t w[4];
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) w[j] = pack_bf16x2(bt * du[2 * j], bt * du[2 * j + 1]);
-                        *reinterpret_cast<uint4 *>(p.dv + ov) = make_uint4(w[0], w[1], w[2], w[3]);
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            db = fmaf(du[j], e[j], db);
-                            vd = fmaf(vv[j], bt * du[j], vd);
-                        }
+                        const size_t o = (bh * p.N + t0 + t) * DV + c;
+                        load_vec<8>(p.e + o, e[i]);
+                        load_vec<8>(p.du + o, du[i]);
+                        bt[i] = p.beta[rs.at(t0 + t)];
+                        vw[i] = __ldg(reinterpret_cast<const uint4 *>(p.v + rv.at(t0 + t) + c));
                     } else {
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) e[j] = du[j] = 0.f;
+                        for (int j = 0; j < 8; ++j) e[i][j] = du[i][j] = 0.f;
                     }
+                }
+                if (tid == 0) bulk_wait_read<0>();   // an item's dq and dk have been stored
+                if (u > 0) {   // the unit before: its accumulators lie where S goes, its sums are complete
+                    if ((failed = any_failed(false))) break;
+                    tc_fence_after();
+                }
+#pragma unroll
+                for (int i = 0; i < NT; ++i) {
+                    const int e0 = i * kGThr + tid, t = e0 / (DV / 8), c = e0 % (DV / 8) * 8;
+                    const uint32_t v2[4] = {vw[i].x, vw[i].y, vw[i].z, vw[i].w};
+                    float db = 0.f, vd = 0.f, g2[8];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        g2[j] = bt[i] * du[i][j];
+                        db = fmaf(du[i][j], e[i][j], db);
+                        vd = fmaf(j & 1 ? bf16_hi_f(v2[j >> 1]) : bf16_lo_f(v2[j >> 1]), g2[j], vd);
+                    }
+                    if (t < n_in)
+                        *reinterpret_cast<uint4 *>(p.dv + rv.at(t0 + t) + c) =
+                            make_uint4(pack_bf16x2(g2[0], g2[1]), pack_bf16x2(g2[2], g2[3]),
+                                       pack_bf16x2(g2[4], g2[5]), pack_bf16x2(g2[6], g2[7]));
 #pragma unroll
                     for (int o = DV / 16; o > 0; o >>= 1) {
                         db += __shfl_xor_sync(0xffffffffu, db, o);
@@ -353,51 +346,53 @@ delta_grad_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
                     const uint32_t o16 = (c >> 6) * 16384 + sw128_off(t, c & 63),
                                    o8 = (c >> 6) * 8192 + sw128_off(t, c & 63);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) split3(e[2 * j], e[2 * j + 1], hi[j], mi[j], lo[j]);
+                    for (int j = 0; j < 4; ++j) split3(e[i][2 * j], e[i][2 * j + 1], hi[j], mi[j], lo[j]);
                     *reinterpret_cast<uint4 *>(sX2 + o16) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
                     *reinterpret_cast<uint4 *>(sEm + o8) = make_uint4(mi[0], mi[1], mi[2], mi[3]);
                     *reinterpret_cast<uint4 *>(sEl + o8) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) split2(du[2 * j], du[2 * j + 1], hi[j], mi[j]);
+                    for (int j = 0; j < 4; ++j) split2(du[i][2 * j], du[i][2 * j + 1], hi[j], mi[j]);
                     *reinterpret_cast<uint4 *>(sX1 + 8192 + o16) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
                     *reinterpret_cast<uint4 *>(sX2 + 8192 + o16) = make_uint4(mi[0], mi[1], mi[2], mi[3]);
                 }
                 fence_proxy_async();
-                // the unit before: its accumulators lie where S goes, its sums are complete
-                if (tid == 0) bulk_wait_read<0>();   // an item's dq and dk have left P's place
-                if (u > 0) {
-                    if ((failed = any_failed(false))) break;
-                    tc_fence_after();
-                    finish(last_it, last_gi, S.unit[~u & 1]);
+                float x[SC];   // of S
+                bool ok = __all_sync(0xffffffffu, mbar_wait<1>(&S.sg_full, 0, g, 3));
+                if (ok && live) {
+#pragma unroll
+                    for (int i = 0; i < SC; i += 16) {
+                        float (&y)[16] = *reinterpret_cast<float (*)[16]>(x + i);
+                        row16(i, y);
+                        const uint32_t col = tb + lb + gS + (cg * SC + i) / 2;
+                        put_pieces(col, DV / 2, col + DV, y);
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < SC; ++i) x[i] = 0.f;
                 }
-                place(true, x, gS);
-                last_it = it;
-                last_gi = gi;
                 tmem_wait_st();
                 tc_fence_before();
-                // ---- G and S', in flight while the MMAs are issued
-                float y[XL];
-                load_rows(p.G_ck + (bh * nblk + blk) * st, x);
-                if (p.lg) load_rows(s_at(it, gi) + st, y);
-                bool ok = true;
-                if (warp == 0)
-                    ok = mbar_wait<1>(&S.kq_full[k & 1], (k >> 1) & 1, g, 1) && mbar_wait<1>(&S.y_full, u & 1, g, 2);
+                if (warp == 0) ok = mbar_wait<1>(&S.y_full, u & 1, g, 2) && ok;
                 if ((failed = any_failed(!ok))) break;   // every operand is there
                 const int next = it + (int)gridDim.x;
                 if (warp == 0) {
-                    if (gi == 0 && next < p.items) {   // the item before has been left by all
-                        if (elect_leader()) load_kq(next, (k & 1) ^ 1);
-                        __syncwarp();
-                    }
+                    if (elect_leader()) load_sg(true, it, gi);
+                    __syncwarp();
                     issue_first();
                 }
-                float gs = 0.f;
-                if (p.lg) {
+                if (warp == 1) {
+                    float bv[2], gv[2];
 #pragma unroll
-                    for (int i = 0; i < XL; ++i) gs = fmaf(x[i], y[i], gs);
+                    for (int i = 0; i < 2; ++i) {
+                        const int t = t0 + 2 * lane + i;
+                        bv[i] = t < p.N ? p.beta[rs.at(t)] : 0.f;
+                        gv[i] = t < p.N && p.lg ? p.lg[rs.at(t)] : 0.f;
+                    }
+                    block_gates<false>(U.gates, bv, gv, lane);
                 }
-                gs = warp_sum(gs);
-                if (lane == 0) U.gs[warp] = gs;
+                if (u > 0) finish(last_it, last_gi, S.unit[~u & 1]);
+                last_it = it;
+                last_gi = gi;
                 // ---- P, P^T and F from the scores; 16 columns of a row
                 ok = __all_sync(0xffffffffu, mbar_wait<1>(&S.pf_done, u & 1, g, 6));
                 uint32_t sc[16];
@@ -414,16 +409,35 @@ delta_grad_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
                     tmem_wait_ld();
                     tc_fence_before();
                 }
+                ok = mbar_wait<1>(&S.sg_full, 1, g, 5) && ok;
                 if ((failed = any_failed(!ok))) break;   // the scores have been read
                 tc_fence_after();
-                place(false, x, gG);
-                named_bar(kBarG, kGThr);
+                float gs = 0.f;   // this thread's terms of <G, S>
+                if (live) {
+#pragma unroll
+                    for (int i = 0; i < SC; i += 16) {
+                        float y[16];
+                        row16(i, y);
+                        const uint32_t col = tb + lb + gG + (cg * SC + i) / 2;
+                        put_pieces(col, DV / 2, col + (gGl - gG), y);
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) gs = fmaf(x[i + j], y[j], gs);
+                    }
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                if ((failed = any_failed(false))) break;   // G has been read
                 // the next unit's values on their way
                 const int nit = gi + 1 < group ? it : next, ngi = gi + 1 < group ? gi + 1 : 0;
-                if (warp == 0 && nit < p.items && elect_leader()) {
+                if (warp == 0) {
+                    ok = __all_sync(0xffffffffu, mbar_wait<1>(&S.s_done, u & 1, g, 4));
+                    if (ok) issue_g();
+                }
+                if (warp == 0 && ok && nit < p.items && elect_leader()) {
+                    load_y(nit, ngi);   // dy has been used
                     const size_t nbh = head_of(nit, ngi), nt = nbh * p.N + nit % nblk * kDC;
                     const uint32_t bytes = min(kDC, p.N - nit % nblk * kDC) * DV * 4;
-                    prefetch_l2(s_at(nit, ngi), D * DV * 4);
+                    prefetch_l2(p.S_ck + (nbh * (nblk + 1) + nit % nblk) * st, D * DV * 4);
                     prefetch_l2(p.G_ck + (nbh * nblk + nit % nblk) * st, D * DV * 4);
                     prefetch_l2(p.e + nt * DV, bytes);
                     prefetch_l2(p.du + nt * DV, bytes);
@@ -475,20 +489,17 @@ delta_grad_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
                     }
                 }
                 fence_proxy_async();
-                tmem_wait_st();
-                tc_fence_before();
-                if (warp == 0) ok = __all_sync(0xffffffffu, mbar_wait<1>(&S.s_done, u & 1, g, 4));
+                if (warp == 0) ok = ok && __all_sync(0xffffffffu, mbar_wait<1>(&S.kq_full, k & 1, g, 1));
                 if ((failed = any_failed(!ok))) break;
-                if (warp == 0) {
-                    if (nit < p.items) {   // dy has been used
-                        if (elect_leader()) load_y(nit, ngi);
-                        __syncwarp();
-                    }
-                    issue_second(k & 1);
-                }
+                if (warp == 0) issue_second();
                 // ---- gradients
-                ok = mbar_wait<1>(&S.kq_full[k & 1], (k >> 1) & 1, g, 7) && mbar_wait<1>(&S.all_done, u & 1, g, 8);
+                ok = mbar_wait<1>(&S.kq_full, k & 1, g, 7) && mbar_wait<1>(&S.all_done, u & 1, g, 8);
                 if (!__all_sync(0xffffffffu, ok)) { failed = true; }
+                if (!failed && warp == 0 && nit < p.items) {   // P, P^T and F have been used
+                    if (elect_leader()) load_sg(false, nit, ngi);
+                    __syncwarp();
+                }
+                float gw = 0.f;
                 if (!failed && live) {
                     tc_fence_after();
                     const Gates &G = U.gates;
@@ -504,7 +515,7 @@ delta_grad_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
                         const float y = fmaf(c[j], u2f(a[j]), u2f(a2[j]));
                         dq[j] += y;
                         const uint16_t qv =
-                            *reinterpret_cast<const uint16_t *>(sQ + (row >> 6) * 8192 + sw128_off(j0 + j, row & 63));
+                            *reinterpret_cast<const uint16_t *>(sKQ + Lay::kT + (row >> 6) * 8192 + sw128_off(j0 + j, row & 63));
                         w[j] = y * __uint_as_float((uint32_t)qv << 16);
                     }
                     if (p.lg) {
@@ -516,7 +527,13 @@ delta_grad_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
                     load16(&G.w[j0], w);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) dk[j] = fmaf(w[j], u2f(a[j]), dk[j]);
+                    for (int j = 0; j < 16; ++j) {
+                        const float y = w[j] * u2f(a[j]);
+                        dk[j] += y;
+                        const uint16_t kv =
+                            *reinterpret_cast<const uint16_t *>(sKQ + (row >> 6) * 8192 + sw128_off(j0 + j, row & 63));
+                        gw = fmaf(y, __uint_as_float((uint32_t)kv << 16), gw);
+                    }
                     load16(&G.b[j0], w);
                     tmem_ld16(tb + lb + gK2 + j0, a);
                     tmem_wait_ld();
@@ -524,19 +541,23 @@ delta_grad_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
                     for (int j = 0; j < 16; ++j) dk[j] += fmaf(-(w[j] * c[j]), u2f(a2[j]), u2f(a[j]));
                     tc_fence_before();
                 }
+                if (p.lg) {   // <G, S'> = c_C <G, S> + sum_j w_j (G e)_j . k_j
+                    gs = warp_sum(fmaf(U.gates.cC, gs, gw));
+                    if (lane == 0) U.gs[warp] = gs;
+                }
                 if (failed) {   // every warp meets at the next barrier, or at the end
                     any_failed(true);
                     break;
                 }
             }
             if (failed) break;
-            // ---- dq and dk through P's place: tokens x features
+            // ---- dq and dk: tokens x features
             if (live) {
 #pragma unroll
                 for (int j = 0; j < 16; ++j) {
                     const uint32_t o = (row >> 6) * 8192 + sw128_off(cg * 16 + j, row & 63);
-                    *reinterpret_cast<__nv_bfloat16 *>(sP + o) = __float2bfloat16_rn(dq[j]);
-                    *reinterpret_cast<__nv_bfloat16 *>(sP + (D / 64) * 8192 + o) = __float2bfloat16_rn(dk[j]);
+                    *reinterpret_cast<__nv_bfloat16 *>(sStage + o) = __float2bfloat16_rn(dq[j]);
+                    *reinterpret_cast<__nv_bfloat16 *>(sStage + (D / 64) * 8192 + o) = __float2bfloat16_rn(dk[j]);
                 }
             }
             fence_proxy_async();
@@ -544,19 +565,23 @@ delta_grad_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
             if (tid == 0) {
 #pragma unroll
                 for (int f = 0; f < D / 64; ++f) {
-                    tma_store_4d(&dqmap, sP + f * 8192, f * 64, t0, hk, b);
-                    tma_store_4d(&dkmap, sP + (D / 64 + f) * 8192, f * 64, t0, hk, b);
+                    tma_store_4d(&dqmap, sStage + f * 8192, f * 64, t0, hk, b);
+                    tma_store_4d(&dkmap, sStage + (D / 64 + f) * 8192, f * 64, t0, hk, b);
                 }
                 bulk_commit();
+                if (it + (int)gridDim.x < p.items) load_kq(it + (int)gridDim.x);   // K and Q have been used
             }
         }
         if (!failed && u > 0) finish(last_it, last_gi, S.unit[~u & 1]);   // behind the last item's barrier
         if (tid == 0) bulk_wait<0>();
         if (failed && warp == 0) {   // let MMAs and copies in flight finish
-            if (elect_leader()) mma_commit(&S.all_done);
-            const uint64_t until = globaltimer_ns() + g.limit_ns;
-            while (globaltimer_ns() < until && !(mbar_try_wait(&S.kq_full[k & 1], (k >> 1) & 1) &&
-                                                 mbar_try_wait(&S.y_full, u & 1))) {}
+            __syncwarp();
+            if (elect_leader()) mma_commit(&S.drained);
+            const uint64_t until = globaltimer_ns() + 1000000000ull;
+            auto done = [](uint64_t *bar, int n) { return n == 0 || mbar_try_wait(bar, (n - 1) & 1); };
+            while (globaltimer_ns() < until &&
+                   !(done(&S.kq_full, S.loads[0]) && done(&S.y_full, S.loads[1]) && done(&S.sg_full, S.loads[2]) &&
+                     mbar_try_wait(&S.drained, 0))) {}
         }
         __syncwarp();
     }
@@ -569,21 +594,26 @@ delta_grad_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
 }
 
 template <int D, int DV, bool ONE> cudaError_t launch_grad_tc(const DeltaArgs &a) {
-    CUtensorMap qm, km, ym, dqm, dkm;
+    CUtensorMap qm, km, ym, dqm, dkm, sm, gm;
+    const DeltaBwdWs w = delta_bwd_ws(a);
+    const int nblk = delta_blocks(a.N), BH = a.B * a.H;
     if (!encode_tokens(&qm, a.q, a.layout, a.B, a.Hk, a.N, D) ||
         !encode_tokens(&km, a.k, a.layout, a.B, a.Hk, a.N, D) ||
         !encode_tokens(&ym, a.dy, a.layout, a.B, a.H, a.N, DV) ||
         !encode_tokens(&dqm, a.dq, a.layout, a.B, a.Hk, a.N, D) ||
-        !encode_tokens(&dkm, a.dk, a.layout, a.B, a.Hk, a.N, D))
+        !encode_tokens(&dkm, a.dk, a.layout, a.B, a.Hk, a.N, D) ||
+        !encode_3d(&sm, w.S, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, DV, D, BH * (nblk + 1), 32, D,
+                   CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !encode_3d(&gm, w.G, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, DV, D, BH * nblk, 32, D,
+                   CU_TENSOR_MAP_SWIZZLE_128B))
         return cudaErrorInvalidValue;
-    const DeltaBwdWs w = delta_bwd_ws(a);
     GradTc p{};
     p.beta = a.beta; p.lg = a.log_gate;
     p.S_ck = w.S; p.G_ck = w.G; p.e = w.e; p.du = w.du;
     p.v = static_cast<const __nv_bfloat16 *>(a.v);
     p.dv = static_cast<__nv_bfloat16 *>(a.dv_grad);
     p.dbeta = a.dbeta; p.dlg = a.dlog_gate;
-    p.H = a.H; p.Hk = a.Hk; p.N = a.N; p.layout = a.layout; p.nblk = delta_blocks(a.N);
+    p.H = a.H; p.Hk = a.Hk; p.N = a.N; p.layout = a.layout; p.nblk = nblk;
     p.items = p.nblk * a.B * a.Hk;
     WsHeader *hdr = static_cast<WsHeader *>(a.ws);
     p.err = &hdr->error;
@@ -592,11 +622,11 @@ template <int D, int DV, bool ONE> cudaError_t launch_grad_tc(const DeltaArgs &a
     p.limit_ns = lim > 0 ? (unsigned long long)lim : 1000000000ull;
     auto kern = delta_grad_tc_kernel<D, DV, ONE>;
     constexpr int smem = GradLay<D, DV>::request;
-    static_assert(smem <= 232448 && 2 * (D / 64) * 8192 <= 5 * 8192, "shared memory of a CTA");
+    static_assert(smem <= 232448, "shared memory of a CTA");
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     const int sms = num_sms();
-    kern<<<p.items < sms ? p.items : sms, kGThr, smem, a.stream>>>(qm, km, ym, dqm, dkm, p);
+    kern<<<p.items < sms ? p.items : sms, kGThr, smem, a.stream>>>(qm, km, ym, dqm, dkm, sm, gm, p);
     return cudaGetLastError();
 }
 
