@@ -14,15 +14,21 @@
 // q . dq and v . dv.  What only dk depends on, which is rounded to bf16, takes
 // two pieces (2^-16).
 //
-// Bound by HBM: S, G, e and du are read once (S of the next block too, from
-// L2, for <G, S'>), 192 KB a block at d = dv = 128 beside the 112 KB of inputs
-// and outputs.  Persistent CTAs, one an SM: 16 warps turn float32 rows into
-// operands and accumulators into gradients; warp 0 also issues the MMAs and
-// copies, and has the next unit's float32 values brought into L2 meanwhile.
-// (A warp of its own for that leaves 96 registers a thread, and spills; so does
-// the next unit's S in registers.)  B8 H16 N8192 d128: 1.65 ms, 15.6 us a unit
-// and SM; the conversions and the MMAs of a unit follow one another, TMEM and
-// shared memory having no room for a second one.
+// <G, S'> of the gates' gradient, S' the state behind the block, takes no other
+// read: S' = c_C S + K^T W, so it is c_C <G, S> + sum_j w_j (G e)_j . k_j.
+//
+// S, G, e and du are read once, 192 KB a block at d = dv = 128 beside the 112 KB
+// of inputs and outputs: 0.75 ms of HBM for B8 H16 N8192, where the kernel takes
+// 1.2 ms (22,000 cycles a unit and SM).  Persistent CTAs, one an SM: 16 warps turn float32
+// values into operands and accumulators into gradients, warp 0 also issues the
+// MMAs.  Every operand is copied to shared memory while the unit before, or the
+// MMAs, still run: S and then G as swizzled slabs, whose rows a lane reads without
+// bank conflicts, in the place that P and F take later; e and du where their
+// pieces go.  (Through registers, with S' read too, a unit took 27,500 cycles,
+// 14,000 of them in loads that nothing else covered.)  What is left alternates
+// between the MMAs (5,900 cycles at the pipe's rate) and the conversions, TMEM and shared
+// memory having no room for a second unit; a warp of its own to issue MMAs would leave
+// 96 registers a thread, and spills.
 #include "delta_tc.cuh"
 
 namespace la {
@@ -48,9 +54,9 @@ struct GradUnit {   // what a unit leaves for the sums over its tokens
 };
 struct GradSmall {
     GradUnit unit[2];
-    uint64_t kq_full, y_full, sg_full, pf_done, s_done, all_done, drained;
+    uint64_t kq_full, y_full, sg_full, eu_full, pf_done, s_done, all_done, drained;
     uint32_t tmem_base;
-    int loads[3];   // issued to the first three
+    int loads[4];   // issued to the first four
     volatile int abort_flag;
 };
 template <int D, int DV> struct GradLay {
@@ -58,12 +64,11 @@ template <int D, int DV> struct GradLay {
     static constexpr int kX = (DV / 64) * 16384;          // per 64 columns: 64 rows, 64 rows
     static constexpr int kE = (DV / 64) * 8192;
     static constexpr int kSG = D * DV * 4;                // S or G; P, P^T and F take its place
-    static constexpr int kStage = 2 * kT;                 // dq and dk: e's lower pieces' place where it fits
+    static constexpr bool kOwnQ = D + DV < 256;           // dq's tile has a place of its own, or du's
     static constexpr int oKQ = 0, oX1 = 2 * kT, oX2 = oX1 + kX, oEm = oX2 + kX, oEl = oEm + kE,
                          oSG = oEl + kE, oPT = oSG + 3 * 8192, oF = oPT + 2 * 8192,
-                         oEnd = oSG + (kSG > 7 * 8192 ? kSG : 7 * 8192),
-                         oStage = kStage <= 2 * kE ? oEm : oEnd,
-                         oSmall = oEnd + (kStage <= 2 * kE ? 0 : kStage);
+                         oDK = oSG + (kSG > 7 * 8192 ? kSG : 7 * 8192), oDQ = kOwnQ ? oDK + kT : oX1 + 8192,
+                         kDQ = kOwnQ ? 8192 : 16384, oSmall = oDK + (kOwnQ ? 2 : 1) * kT;
     static constexpr int total = oSmall + (int)sizeof(GradSmall);
     static constexpr int request = total + 1024;
 };
@@ -105,7 +110,7 @@ delta_grad_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
     GradSmall &S = *reinterpret_cast<GradSmall *>(sm + Lay::oSmall);
     uint8_t *sKQ = sm + Lay::oKQ, *sX1 = sm + Lay::oX1, *sX2 = sm + Lay::oX2, *sEm = sm + Lay::oEm,
             *sEl = sm + Lay::oEl, *sSG = sm + Lay::oSG, *sP = sSG, *sPT = sm + Lay::oPT, *sF = sm + Lay::oF,
-            *sStage = sm + Lay::oStage;
+            *sDK = sm + Lay::oDK, *sDQ = sm + Lay::oDQ;
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const int nblk = p.nblk, group = ONE ? 1 : p.H / p.Hk;
     const Guard g{&S.abort_flag, p.err, p.err_where, p.limit_ns};
@@ -115,8 +120,10 @@ delta_grad_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
         mbar_init(&S.kq_full, 1);
         mbar_init(&S.y_full, 1);
         mbar_init(&S.sg_full, 1);
+        mbar_init(&S.eu_full, 1);
         mbar_init(&S.drained, 1);
-        S.loads[0] = S.loads[1] = S.loads[2] = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) S.loads[i] = 0;
         mbar_init(&S.pf_done, 1);
         mbar_init(&S.s_done, 1);
         mbar_init(&S.all_done, 1);
@@ -159,6 +166,16 @@ delta_grad_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
 #pragma unroll
         for (int f = 0; f < DV / 32; ++f)
             tma_load_3d(sSG + f * D * 128, G ? &gmap : &smap, &S.sg_full, f * 32, 0, at);
+    };
+    // e and du of a unit, float32, where their pieces go
+    auto load_eu = [&](int it, int gi) {
+        const int t0 = it % nblk * kDC;
+        const size_t o = (head_of(it, gi) * p.N + t0) * DV;
+        const uint32_t bytes = min(kDC, p.N - t0) * DV * 4;
+        mbar_arrive_expect_tx(&S.eu_full, 2 * bytes);
+        ++S.loads[3];
+        bulk_load(sEm, p.e + o, bytes, &S.eu_full);
+        bulk_load(sX2, p.du + o, bytes, &S.eu_full);
     };
     // scores, and what S gives
     auto issue_first = [&]() {
@@ -231,6 +248,7 @@ delta_grad_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
         load_kq(blockIdx.x);
         load_y(blockIdx.x, 0);
         load_sg(false, blockIdx.x, 0);
+        load_eu(blockIdx.x, 0);
     }
     __syncwarp();
     {
@@ -239,6 +257,7 @@ delta_grad_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
         constexpr int SC = DV / 4;   // state columns of a thread
         const bool live = row < D;   // warp-uniform: lanes with a feature
         const size_t st = (size_t)D * DV;
+        constexpr int kCopier = kGThr / 2;   // the thread of most copies
         // A thread's columns of its row of S or G: chunks of 16 bytes at c ^ (row & 7) of their slab, so
         // that eight lanes' reads spread over all banks.
         auto row16 = [&](int i, float (&x)[16]) {   // columns cg SC + i ..
@@ -300,27 +319,33 @@ delta_grad_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
                 constexpr int NT = DV / 64;
                 float e[NT][8], du[NT][8], bt[NT];
                 uint4 vw[NT];
+                bool ok = __all_sync(0xffffffffu, mbar_wait<1>(&S.eu_full, u & 1, g, 9));
 #pragma unroll
-                for (int i = 0; i < NT; ++i) {   // on their way while the unit before is finished
+                for (int i = 0; i < NT; ++i) {
                     const int e0 = i * kGThr + tid, t = e0 / (DV / 8), c = e0 % (DV / 8) * 8;
                     bt[i] = 0.f;
                     vw[i] = make_uint4(0u, 0u, 0u, 0u);
                     if (t < n_in) {
-                        const size_t o = (bh * p.N + t0 + t) * DV + c;
-                        load_vec<8>(p.e + o, e[i]);
-                        load_vec<8>(p.du + o, du[i]);
                         bt[i] = p.beta[rs.at(t0 + t)];
                         vw[i] = __ldg(reinterpret_cast<const uint4 *>(p.v + rv.at(t0 + t) + c));
-                    } else {
+                    }
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) e[i][j] = du[i][j] = 0.f;
+                    for (int j = 0; j < 8; ++j) e[i][j] = du[i][j] = 0.f;
+                    if (t < n_in) {
+#pragma unroll
+                        for (int j = 0; j < 8; j += 4) {
+                            *reinterpret_cast<float4 *>(&e[i][j]) =
+                                *reinterpret_cast<const float4 *>(sEm + (t * DV + c + j) * 4);
+                            *reinterpret_cast<float4 *>(&du[i][j]) =
+                                *reinterpret_cast<const float4 *>(sX2 + (t * DV + c + j) * 4);
+                        }
                     }
                 }
-                if (tid == 0) bulk_wait_read<0>();   // an item's dq and dk have been stored
-                if (u > 0) {   // the unit before: its accumulators lie where S goes, its sums are complete
-                    if ((failed = any_failed(false))) break;
-                    tc_fence_after();
-                }
+                // every value is in registers, an item's dq and dk have been stored, and the unit
+                // before is done: its accumulators lie where S goes, its sums are complete
+                if (tid == kCopier) bulk_wait_read<0>();
+                if ((failed = any_failed(!ok))) break;
+                tc_fence_after();
 #pragma unroll
                 for (int i = 0; i < NT; ++i) {
                     const int e0 = i * kGThr + tid, t = e0 / (DV / 8), c = e0 % (DV / 8) * 8;
@@ -357,7 +382,7 @@ delta_grad_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
                 }
                 fence_proxy_async();
                 float x[SC];   // of S
-                bool ok = __all_sync(0xffffffffu, mbar_wait<1>(&S.sg_full, 0, g, 3));
+                ok = __all_sync(0xffffffffu, mbar_wait<1>(&S.sg_full, 0, g, 3));
                 if (ok && live) {
 #pragma unroll
                     for (int i = 0; i < SC; i += 16) {
@@ -433,14 +458,14 @@ delta_grad_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
                     ok = __all_sync(0xffffffffu, mbar_wait<1>(&S.s_done, u & 1, g, 4));
                     if (ok) issue_g();
                 }
-                if (warp == 0 && ok && nit < p.items && elect_leader()) {
-                    load_y(nit, ngi);   // dy has been used
+                if (warp == 0 && ok && nit < p.items && elect_leader()) load_y(nit, ngi);   // dy has been used
+                if (tid == kCopier && nit < p.items) {
                     const size_t nbh = head_of(nit, ngi), nt = nbh * p.N + nit % nblk * kDC;
                     const uint32_t bytes = min(kDC, p.N - nit % nblk * kDC) * DV * 4;
-                    prefetch_l2(p.S_ck + (nbh * (nblk + 1) + nit % nblk) * st, D * DV * 4);
-                    prefetch_l2(p.G_ck + (nbh * nblk + nit % nblk) * st, D * DV * 4);
                     prefetch_l2(p.e + nt * DV, bytes);
                     prefetch_l2(p.du + nt * DV, bytes);
+                    prefetch_l2(p.S_ck + (nbh * (nblk + 1) + nit % nblk) * st, D * DV * 4);
+                    prefetch_l2(p.G_ck + (nbh * nblk + nit % nblk) * st, D * DV * 4);
                 }
                 __syncwarp();
                 {
@@ -495,10 +520,11 @@ delta_grad_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
                 // ---- gradients
                 ok = mbar_wait<1>(&S.kq_full, k & 1, g, 7) && mbar_wait<1>(&S.all_done, u & 1, g, 8);
                 if (!__all_sync(0xffffffffu, ok)) { failed = true; }
-                if (!failed && warp == 0 && nit < p.items) {   // P, P^T and F have been used
-                    if (elect_leader()) load_sg(false, nit, ngi);
-                    __syncwarp();
+                if (!failed && tid == kCopier && nit < p.items) {   // e, du, P, P^T and F have been used
+                    load_eu(nit, ngi);
+                    load_sg(false, nit, ngi);
                 }
+                __syncwarp();
                 float gw = 0.f;
                 if (!failed && live) {
                     tc_fence_after();
@@ -555,33 +581,33 @@ delta_grad_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
             if (live) {
 #pragma unroll
                 for (int j = 0; j < 16; ++j) {
-                    const uint32_t o = (row >> 6) * 8192 + sw128_off(cg * 16 + j, row & 63);
-                    *reinterpret_cast<__nv_bfloat16 *>(sStage + o) = __float2bfloat16_rn(dq[j]);
-                    *reinterpret_cast<__nv_bfloat16 *>(sStage + (D / 64) * 8192 + o) = __float2bfloat16_rn(dk[j]);
+                    const uint32_t o = sw128_off(cg * 16 + j, row & 63);
+                    *reinterpret_cast<__nv_bfloat16 *>(sDQ + (row >> 6) * Lay::kDQ + o) = __float2bfloat16_rn(dq[j]);
+                    *reinterpret_cast<__nv_bfloat16 *>(sDK + (row >> 6) * 8192 + o) = __float2bfloat16_rn(dk[j]);
                 }
             }
             fence_proxy_async();
             if ((failed = any_failed(false))) break;
-            if (tid == 0) {
+            if (tid == kCopier) {
 #pragma unroll
                 for (int f = 0; f < D / 64; ++f) {
-                    tma_store_4d(&dqmap, sStage + f * 8192, f * 64, t0, hk, b);
-                    tma_store_4d(&dkmap, sStage + (D / 64 + f) * 8192, f * 64, t0, hk, b);
+                    tma_store_4d(&dqmap, sDQ + f * Lay::kDQ, f * 64, t0, hk, b);
+                    tma_store_4d(&dkmap, sDK + f * 8192, f * 64, t0, hk, b);
                 }
                 bulk_commit();
                 if (it + (int)gridDim.x < p.items) load_kq(it + (int)gridDim.x);   // K and Q have been used
             }
         }
         if (!failed && u > 0) finish(last_it, last_gi, S.unit[~u & 1]);   // behind the last item's barrier
-        if (tid == 0) bulk_wait<0>();
+        if (tid == kCopier) bulk_wait<0>();
         if (failed && warp == 0) {   // let MMAs and copies in flight finish
             __syncwarp();
             if (elect_leader()) mma_commit(&S.drained);
             const uint64_t until = globaltimer_ns() + 1000000000ull;
             auto done = [](uint64_t *bar, int n) { return n == 0 || mbar_try_wait(bar, (n - 1) & 1); };
             while (globaltimer_ns() < until &&
-                   !(done(&S.kq_full, S.loads[0]) && done(&S.y_full, S.loads[1]) && done(&S.sg_full, S.loads[2]) &&
-                     mbar_try_wait(&S.drained, 0))) {}
+                   !(done(&S.kq_full, S.loads[0]) && done(&S.y_full, S.loads[1]) &&
+                     done(&S.sg_full, S.loads[2]) && done(&S.eu_full, S.loads[3]) && mbar_try_wait(&S.drained, 0))) {}
         }
         __syncwarp();
     }
