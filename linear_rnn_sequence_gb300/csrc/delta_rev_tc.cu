@@ -165,7 +165,6 @@ delta_rev_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
         if (live) {
 #pragma unroll
             for (int i = 0; i < SC; i += 16) put_state(i);
-            if (!LOCAL) write_state(gck);
         }
         tmem_wait_st();
         tc_fence_before();
@@ -210,6 +209,7 @@ delta_rev_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
                     mma_commit_if(leader, &S.py_done);
                 }
             }
+            if (!LOCAL && live) write_state(gck);   // beside K G
             // ---- the right-hand side D_C . (K G) + P0^T dy
             ok = ok && mbar_wait<1>(&S.v_full[n & 1], (n >> 1) & 1, g, 10);
             ok = ok && mbar_wait<1>(&S.t_ready[n & 1], (n >> 1) & 1, g, 4);
@@ -355,10 +355,7 @@ delta_rev_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
                 }
                 tmem_wait_st();
                 tc_fence_before();
-                if (!LOCAL) {
-                    gck -= D * DV;
-                    if (n + 1 < nblk) write_state(gck);
-                }
+                if (!LOCAL) gck -= D * DV;
             }
             failed = any_failed(!ok);
         }

@@ -211,7 +211,6 @@ delta_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
         if (live) {
 #pragma unroll
             for (int i = 0; i < SC; i += 16) put_state(i);
-            if (SAVE) write_state(sck, DV);
         }
         tmem_wait_st();
         tc_fence_before();
@@ -237,6 +236,7 @@ delta_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
                     mma_commit_if(leader, &S.ks_done);
                 }
             }
+            if (SAVE && live) write_state(sck, DV);   // beside K S
             // ---- r = v - c . (K S)
             ok = ok && mbar_wait<1>(&S.v_full[n & 1], (n >> 1) & 1, g, 3);
             ok = ok && mbar_wait<1>(&S.t_ready[n & 1], (n >> 1) & 1, g, 4);
@@ -392,10 +392,10 @@ delta_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
                 tmem_wait_st();
                 tc_fence_before();
                 sck += D * DV;
-                if (SAVE && (n + 1 < nblk || seg == segs - 1)) write_state(sck, DV);
             }
             failed = any_failed(!ok);
         }
+        if (SAVE && !failed && live && seg == segs - 1) write_state(sck, DV);
         if (SEG) {
             if (!failed && live && values)
                 write_state(p.S_local + (size_t)item * D * DV + (size_t)half * SC * DV + col_of, DV);
