@@ -12,7 +12,7 @@
 // It is the forward kernel run backwards, with its layout (a TMEM lane for
 // each of the dv columns of G), its pieces and its roles.  Two operands come
 // on top: dy^T P0 straight from the dy tile (exact bf16, dv-major), and c . dy
-// as pieces, made while T^T (...) runs.  In TMEM the right-hand side takes the
+// as pieces, made beside the right-hand side by the warps of P0.  In TMEM the right-hand side takes the
 // upper part of the place of G's pieces, c . dy the lower one, and -b c . du
 // that of the right-hand side.  B8 H16 N8192 d128: 0.92 ms (7.2 us a block).
 #include "delta_tc.cuh"
@@ -41,7 +41,7 @@ struct RevTc {
 struct RevSmall {
     Gates gates[4];
     uint64_t kq_full[kStages], v_full[2], kk_full, kk_read, g_ready[2], t_ready[2], t_free[2], p_ready, ks_done,
-        py_done, e_done, s_done, o_read, drain[3];
+        py_done, cy_ready, e_done, s_done, o_read, drain[3];
     uint32_t tmem_base;
     volatile int abort_flag;
 };
@@ -85,6 +85,7 @@ delta_rev_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
         mbar_init(&S.p_ready, 64);
         mbar_init(&S.ks_done, 1);
         mbar_init(&S.py_done, 1);
+        mbar_init(&S.cy_ready, kOut);
         mbar_init(&S.e_done, 1);
         mbar_init(&S.s_done, 1);
         mbar_init(&S.o_read, kOut);
@@ -211,7 +212,6 @@ delta_rev_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
             }
             if (!LOCAL && live) write_state(gck);   // beside K G
             // ---- the right-hand side D_C . (K G) + P0^T dy
-            ok = ok && mbar_wait<1>(&S.v_full[n & 1], (n >> 1) & 1, g, 10);
             ok = ok && mbar_wait<1>(&S.t_ready[n & 1], (n >> 1) & 1, g, 4);
             ok = ok && mbar_wait<1>(&S.ks_done, n & 1, g, 5);
             ok = ok && mbar_wait<1>(&S.py_done, n & 1, g, 6);
@@ -255,47 +255,24 @@ delta_rev_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
                 mma_commit_if(leader, &S.e_done);
                 mma_commit_if(leader, &S.t_free[n & 1]);
             }
-            // ---- meanwhile c . dy
-            if (live) {
-                const uint8_t *ty = sV + (n & 1) * Lay::kV + (row >> 6) * 8192 + half * 32 * 128 + (row & 7) * 2;
-                const uint32_t ch = (uint32_t)(row & 63) >> 3;
-#pragma unroll 1
-                for (int u = 0; u < 2; ++u) {
-                    const int j0 = half * 32 + u * 16;
-                    uint32_t hi[8], mi[8], lo[8];
-                    float r[16], c[16];
-#pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                        r[j] = __uint_as_float((uint32_t)*reinterpret_cast<const uint16_t *>(
-                                   ty + (u * 16 + j) * 128 + ((ch ^ (j & 7)) << 4)) << 16);
-                    load16(&G.c[j0], c);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        split3(c[2 * i] * r[2 * i], c[2 * i + 1] * r[2 * i + 1], hi[i], mi[i], lo[i]);
-                    const uint32_t col = tb + lb + kColCY + j0 / 2;
-                    tmem_st8(col, hi);
-                    tmem_st8(col + 32, mi);
-                    tmem_st8(col + 64, lo);
-                }
-                tmem_wait_st();
-                tc_fence_before();
-            }
-            if ((failed = any_failed(false))) break;
             const uint64_t kd = smem_desc(kk, 16384, 1024, kSwizzle128B), qd = smem_desc(qq, 16384, 1024, kSwizzle128B);
             if (warp == 0) {   // the small pieces of Q^T (c . dy); its large ones come with the others'
-                const uint32_t leader = elect_leader();
-                tc_fence_after();
+                ok = __all_sync(0xffffffffu, mbar_wait<1>(&S.cy_ready, n & 1, g, 11));
+                if (ok) {
+                    const uint32_t leader = elect_leader();
+                    tc_fence_after();
 #pragma unroll 1
-                for (int pc = 2; pc >= 1; --pc)
+                    for (int pc = 2; pc >= 1; --pc)
 #pragma unroll
-                    for (int ks = 0; ks < kDC / 16; ++ks)
-                        mma_ts_if(leader, tb + kColSD, tb + kColCY + pc * 32 + ks * 8, qd + ks * 128, iS,
-                                  pc < 2 || ks > 0);
-                if (leader && n + 2 < nblk) load_v(n + 2);   // dy has been read, P0^T dy is done
-                __syncwarp();
+                        for (int ks = 0; ks < kDC / 16; ++ks)
+                            mma_ts_if(leader, tb + kColSD, tb + kColCY + pc * 32 + ks * 8, qd + ks * 128, iS,
+                                      pc < 2 || ks > 0);
+                    if (leader && n + 2 < nblk) load_v(n + 2);   // dy has been read, P0^T dy is done
+                    __syncwarp();
+                }
             }
             // ---- -b c . du
-            ok = __all_sync(0xffffffffu, mbar_wait<1>(&S.e_done, n & 1, g, 7));
+            ok = ok && __all_sync(0xffffffffu, mbar_wait<1>(&S.e_done, n & 1, g, 7));
             if (ok && live) {
                 tc_fence_after();
 #pragma unroll 1
@@ -532,9 +509,43 @@ delta_rev_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
             if (ok) make_p(0);
         }
         for (int n = 0; n < nblk; ++n) {
-            if (n + 1 < nblk && rows_of_q(n + 1)) {
-                ok = ok && read_scores(n + 1);
-                ok = ok && __all_sync(0xffffffffu, mbar_wait<1>(&S.py_done, n & 1, g, 29));
+            const bool q_next = rows_of_q(n + 1), p_next = q_next && n + 1 < nblk;
+            // these gates, seen by the other half when it made P; the next ones' phase cannot end before
+            if (q_next) ok = ok && __all_sync(0xffffffffu, mbar_wait<1>(&S.g_ready[n & 1], (n >> 1) & 1, g, 28));
+            if (p_next) ok = ok && read_scores(n + 1);
+            // ---- c . dy, where G's pieces were
+            ok = ok && __all_sync(0xffffffffu, mbar_wait<1>(&S.ks_done, n & 1, g, 29) &&
+                                                   mbar_wait<1>(&S.v_full[n & 1], (n >> 1) & 1, g, 10));
+            if (ok) {
+                if (row < DV) {
+                    tc_fence_after();
+                    const float *c_of = S.gates[n & 3].c;
+                    const uint8_t *ty = sV + (n & 1) * Lay::kV + (row >> 6) * 8192 + (row & 7) * 2;
+                    const uint32_t ch = (uint32_t)(row & 63) >> 3;
+#pragma unroll 1
+                    for (int j0 = 0; j0 < kDC; j0 += 16) {
+                        uint32_t hi[8], mi[8], lo[8];
+                        float r[16], c[16];
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            r[j] = __uint_as_float((uint32_t)*reinterpret_cast<const uint16_t *>(
+                                       ty + (j0 + j) * 128 + ((ch ^ (j & 7)) << 4)) << 16);
+                        load16(c_of + j0, c);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            split3(c[2 * i] * r[2 * i], c[2 * i + 1] * r[2 * i + 1], hi[i], mi[i], lo[i]);
+                        const uint32_t col = tb + lb + kColCY + j0 / 2;
+                        tmem_st8(col, hi);
+                        tmem_st8(col + 32, mi);
+                        tmem_st8(col + 64, lo);
+                    }
+                    tmem_wait_st();
+                    tc_fence_before();
+                }
+                mbar_arrive(&S.cy_ready);
+            }
+            if (p_next) {   // where this step's has been used
+                ok = ok && __all_sync(0xffffffffu, mbar_wait<1>(&S.py_done, n & 1, g, 31));
                 if (ok) make_p(n + 1);
             }
             ok = ok && __all_sync(0xffffffffu, mbar_wait<1>(&S.e_done, n & 1, g, 30));
