@@ -734,6 +734,8 @@ def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, return_stats=False,
     if stream is not None or not x.is_cuda or x.get_device() != _current_device():
         return _elsewhere(layer_norm, stream, x, weight, bias, eps, return_stats, out)
     shape, dev, f32 = x.shape, x.get_device(), torch.float32
+    if not shape:
+        raise ValueError("x must have at least one dimension")
     D = shape[-1]
     if out is None:
         out = torch.empty_like(x)
@@ -761,6 +763,8 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, sums=None, workspace=Non
     if stream is not None or not dy.is_cuda or dy.get_device() != _current_device():
         return _elsewhere(layer_norm_backward, stream, dy, x, mean, rstd, weight, sums, workspace)
     shape, dev, f32 = x.shape, x.get_device(), torch.float32
+    if not shape:
+        raise ValueError("x must have at least one dimension")
     D, dt = shape[-1], _dtype_code(x)
     gx = torch.empty_like(x)
     rows = x.numel() // D if D else 0

@@ -112,6 +112,15 @@ def test_few_heads_and_many_tokens(d, dv, gate, N):
     check_backward(x, BF16, "bnhd")
 
 
+@pytest.mark.parametrize("d,dv", [(64, 64), (128, 128), (64, 128), (128, 64)])
+@pytest.mark.parametrize("B,H,Hk,N", [(3, 6, 2, 1800), (5, 6, 6, 610), (40, 8, 8, 40)])
+def test_more_blocks_than_sms(d, dv, B, H, Hk, N):
+    """Persistent CTAs of the gradients' products take several blocks each: of one value head, of three
+    that share a key head, and of the ragged ends alone."""
+    x = R.inputs(B, H, Hk, N, d, dv, BF16, gate="any" if N > 1000 else "open", state=H != Hk, seed=N + d + dv)
+    check_backward(x, BF16)
+
+
 @pytest.mark.parametrize("dtype", [BF16, F32])
 def test_a_sequence_in_parts(dtype):
     x = on_gpu(R.inputs(2, 2, 2, 300, 64, 64, dtype, state=True, seed=8))
@@ -388,6 +397,14 @@ def test_binding_refuses():
         la.layer_norm(torch.zeros(3, 8, device="cuda"), torch.zeros(7, device="cuda"))
     with pytest.raises(la.LinAttnError):
         la.layer_norm(torch.zeros(2, 16385, device="cuda"))
+
+
+def test_layer_norm_of_a_scalar_is_refused():
+    x = torch.zeros((), device="cuda")
+    with pytest.raises(ValueError):
+        la.layer_norm(x)
+    with pytest.raises(ValueError):
+        la.layer_norm_backward(x, x, x, x)
 
 
 def test_values_behind_the_inputs_are_not_read():
