@@ -12,6 +12,7 @@
 // 0.11 us a token (B1 H2 N256 d32: 36 us; 61 without these).  It serves float32
 // inputs and widths of 32, and bf16 sequences of fewer than 32 tokens.
 #include "delta_common.cuh"
+#include "tc_common.cuh"
 
 namespace la {
 namespace {
@@ -146,6 +147,7 @@ __global__ void __launch_bounds__(kThr) delta_forward_kernel(const DeltaSimt p) 
     constexpr int R = D / 8, P = R / 2;
     __shared__ __align__(16) float ks[2][kTile][D], qs[2][SAVE ? 1 : kTile][D];
     __shared__ float vs[2][kTile][kCols], os[2][kTile][kCols], bs[2][kTile], as[2][kTile];
+    if (SAVE) griddep_launch_dependents();   // the reverse pass, which needs nothing of this one
     const int bh = blockIdx.x, b = bh / p.H, h = bh % p.H, c0 = blockIdx.y * kCols;
     const int tid = threadIdx.x, col = tid >> 3, part = tid & 7;
     const TokenRows rk = token_rows(p.layout, b, h / (p.H / p.Hk), p.Hk, p.N, D);
@@ -302,6 +304,7 @@ __global__ void __launch_bounds__(kThr) delta_reverse_kernel(const DeltaSimt p) 
     __syncthreads();
     write_out(0, bf ^ 1);
     if (p.dS_in) keep(p.dS_in + bh * st);
+    griddep_wait();   // what follows in the stream waits for this kernel, and so for the states' pass beside it
 }
 
 DeltaSimt params(const DeltaArgs &a) {
@@ -325,6 +328,11 @@ cudaError_t launch_d(const DeltaArgs &a, int what) {
     }
     if (what == 0) delta_forward_kernel<D, T, false><<<grid, kThr, 0, a.stream>>>(p);
     if (what == 1) delta_forward_kernel<D, T, true><<<grid, kThr, 0, a.stream>>>(p);
+    // Beside the states' pass where both fit the SMs, one CTA each (B2 H4 N777 d64, 32 CTAs: 184 us for the
+    // gradients, 266 one after the other).  Where they share SMs the second pass's CTAs crowd on the
+    // emptier ones: 128 CTAs of d = 128, 2048 tokens: 1516 us, 1080 one after the other.
+    if (what == 2 && 2 * (long long)grid.x * grid.y <= num_sms())
+        return launch_overlapped(delta_reverse_kernel<D, T>, grid, dim3(kThr), 0, a.stream, p);
     if (what == 2) delta_reverse_kernel<D, T><<<grid, kThr, 0, a.stream>>>(p);
     return cudaGetLastError();
 }
