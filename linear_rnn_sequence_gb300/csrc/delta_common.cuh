@@ -55,6 +55,17 @@ template <int N> __device__ __forceinline__ void load_vec(const __nv_bfloat16 *p
     }
 }
 
+// A float32 pair h + l, |l| at most half a step of h: sums keep about 46 bits.
+struct F2 {
+    float h, l;
+};
+__device__ __forceinline__ F2 f2sum2(F2 a, F2 b) {
+    const float s = a.h + b.h, t = s - a.h;
+    const float l = ((a.h - (s - t)) + (b.h - t)) + (a.l + b.l);
+    const float h = s + l;
+    return {h, l - (h - s)};
+}
+
 // Workspace of the gradients, in floats behind the status header: the states before each block and
 // the final one, their gradients after each block, e and du of every token (head-major), and what
 // a split of the sequence takes.

@@ -72,20 +72,30 @@ __global__ void __launch_bounds__(kThr) delta_grad_kernel(const GradParams p) {
         const float *S0 = p.S_ck + (bh * (nc + 1) + blk) * st, *S1 = S0 + st;
         const float *G1 = p.G_ck + (bh * nc + blk) * st;
         __syncthreads();
-        // running sums of the log gates as unevaluated pairs hi + lo, so that differences of two
-        // of them keep their precision behind a nearly closed gate
-        if (tid < kDeltaC) {   // exp(-1e4) is 0; keeps -inf out
-            const float x = tid < n && p.lg ? p.lg[rs.at(t0 + tid)] : 0.f;
-            s.qdq[tid] = x < -1e4f ? -1e4f : x;
-        }
-        __syncthreads();
-        if (tid == 0) {
-            double sum = 0.0;
-            for (int i = 0; i < kDeltaC; ++i) {
-                sum += (double)s.qdq[i];
-                const float f = (float)sum;
-                s.hi[i] = f;
-                s.lo[i] = (float)(sum - (double)f);
+        // running sums of the log gates as pairs hi + lo, so that differences of two of them keep
+        // their precision behind a nearly closed gate; one warp, two tokens a lane
+        if (tid < 32) {
+            F2 x[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {   // exp(-1e4) is 0; keeps -inf out
+                const int t = 2 * tid + i;
+                const float v = t < n && p.lg ? p.lg[rs.at(t0 + t)] : 0.f;
+                x[i] = {v < -1e4f ? -1e4f : v, 0.f};
+            }
+            x[1] = f2sum2(x[0], x[1]);
+            F2 sum = x[1];
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const F2 y = {__shfl_up_sync(0xffffffffu, sum.h, o), __shfl_up_sync(0xffffffffu, sum.l, o)};
+                if (tid >= o) sum = f2sum2(y, sum);
+            }
+            F2 before = {__shfl_up_sync(0xffffffffu, sum.h, 1), __shfl_up_sync(0xffffffffu, sum.l, 1)};
+            if (tid == 0) before = {0.f, 0.f};
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const F2 y = f2sum2(before, x[i]);
+                s.hi[2 * tid + i] = y.h;
+                s.lo[2 * tid + i] = y.l;
             }
         }
         if (tid < kDeltaC) {
@@ -233,13 +243,27 @@ __global__ void __launch_bounds__(kThr) delta_grad_kernel(const GradParams p) {
         }
         __syncthreads();
         if (tid < n) p.dbeta[rs.at(t0 + tid)] = s.db[tid];
-        if (p.lg && tid == 0) {
-            double x = 0.0;
-            for (int w = 0; w < kThr / 32; ++w) x += s.red[w];
-            for (int i = n - 1; i >= 0; --i) {
-                x += (double)s.qdq[i] - (double)s.vdv[i];
-                p.dlg[rs.at(t0 + i)] = (float)x;
+        if (p.lg && tid < 32) {   // running sums from the block's end, two tokens a lane
+            F2 x[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {   // q . dq - v . dv, exactly
+                const int t = 2 * tid + i;
+                const float qd = t < n ? s.qdq[t] : 0.f, vd = t < n ? s.vdv[t] : 0.f, d = qd - vd, z = d - qd;
+                x[i] = {d, (qd - (d - z)) - (vd + z)};
             }
+            const float e = warp_sum(tid < kThr / 32 ? s.red[tid] : 0.f);
+            x[0] = f2sum2(x[0], x[1]);
+            F2 sum = x[0];
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const F2 y = {__shfl_down_sync(0xffffffffu, sum.h, o), __shfl_down_sync(0xffffffffu, sum.l, o)};
+                if (tid + o < 32) sum = f2sum2(sum, y);
+            }
+            F2 after = {__shfl_down_sync(0xffffffffu, sum.h, 1), __shfl_down_sync(0xffffffffu, sum.l, 1)};
+            if (tid == 31) after = {0.f, 0.f};
+            const F2 end = {e, 0.f}, first = f2sum2(end, sum), second = f2sum2(end, f2sum2(after, x[1]));
+            if (2 * tid < n) p.dlg[rs.at(t0 + 2 * tid)] = first.h + first.l;
+            if (2 * tid + 1 < n) p.dlg[rs.at(t0 + 2 * tid + 1)] = second.h + second.l;
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i)

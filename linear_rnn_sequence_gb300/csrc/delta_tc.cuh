@@ -49,17 +49,6 @@ __device__ __forceinline__ void load16(const float *p, float (&x)[16]) {
         *reinterpret_cast<float4 *>(x + i) = *reinterpret_cast<const float4 *>(p + i);
 }
 
-// A float32 pair h + l, |l| at most half a step of h: sums keep about 46 bits.
-struct F2 {
-    float h, l;
-};
-__device__ __forceinline__ F2 f2sum2(F2 a, F2 b) {
-    const float s = a.h + b.h, t = s - a.h;
-    const float l = ((a.h - (s - t)) + (b.h - t)) + (a.l + b.l);
-    const float h = s + l;
-    return {h, l - (h - s)};
-}
-
 // The gates of a block: running log2 sums as pairs hi + lo (differences of two of
 // them keep their precision behind a nearly closed gate), c, w = D_Cj b_j, b, f; w and f without
 // b_j for the reverse pass.  One warp; two tokens a lane.
