@@ -20,7 +20,7 @@
 namespace la {
 namespace {
 
-constexpr int kThr = 256;
+constexpr int kThr = 512;
 constexpr int kSl = 16;        // dv slice staged at a time
 constexpr int kP = kDeltaC + 4;   // padded row of the transposed stages
 
@@ -46,11 +46,11 @@ template <int D> struct GradSmem {
 };
 
 template <int D, typename T>
-__global__ void __launch_bounds__(kThr) delta_grad_kernel(const GradParams p) {
+__global__ void __launch_bounds__(kThr, D == 32 ? 2 : 1) delta_grad_kernel(const GradParams p) {
     extern __shared__ __align__(16) unsigned char raw[];
     GradSmem<D> &s = *reinterpret_cast<GradSmem<D> *>(raw);
-    constexpr int CW = D / 16;   // features of a thread: 4 tokens x CW
-    const int tid = threadIdx.x, ti = tid >> 4, tj = tid & 15;   // tokens 4 ti.., features CW tj..
+    constexpr int CW = D / 32;   // features of a thread: 4 tokens x CW
+    const int tid = threadIdx.x, ti = tid >> 5, tj = tid & 31;   // tokens 4 ti.., features tj + 32 j
     const int nc = delta_blocks(p.N), blk = blockIdx.x % nc, t0 = blk * kDeltaC;
     const int bk = blockIdx.x / nc, b = bk / p.Hk, hk = bk % p.Hk, group = p.H / p.Hk;
     const int n = min(kDeltaC, p.N - t0);
@@ -109,11 +109,11 @@ __global__ void __launch_bounds__(kThr) delta_grad_kernel(const GradParams p) {
             s.cC[tid] = decay(n - 1, tid);
         }
 
-        float P[4][4], F[4][4], aq[4][CW], ak[4][CW], as[4][CW];
+        float P[4][2], F[4][2], aq[4][CW], ak[4][CW], as[4][CW];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) P[i][j] = F[i][j] = 0.f;
+            for (int j = 0; j < 2; ++j) P[i][j] = F[i][j] = 0.f;
 #pragma unroll
             for (int j = 0; j < CW; ++j) aq[i][j] = ak[i][j] = as[i][j] = 0.f;
         }
@@ -153,19 +153,19 @@ __global__ void __launch_bounds__(kThr) delta_grad_kernel(const GradParams p) {
                 const float4 y4 = *reinterpret_cast<const float4 *>(&s.dyT[c][4 * ti]);
                 const float4 d4 = *reinterpret_cast<const float4 *>(&s.duT[c][4 * ti]);
                 const float4 e4 = *reinterpret_cast<const float4 *>(&s.eT[c][4 * ti]);
-                const float4 f4 = *reinterpret_cast<const float4 *>(&s.eT[c][4 * tj]);
+                const float2 f2 = *reinterpret_cast<const float2 *>(&s.eT[c][2 * tj]);
                 const float yi[4] = {y4.x, y4.y, y4.z, y4.w}, di[4] = {d4.x, d4.y, d4.z, d4.w};
-                const float ei[4] = {e4.x, e4.y, e4.z, e4.w}, ej[4] = {f4.x, f4.y, f4.z, f4.w};
+                const float ei[4] = {e4.x, e4.y, e4.z, e4.w}, ej[2] = {f2.x, f2.y};
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
+                    for (int j = 0; j < 2; ++j) {
                         P[i][j] = fmaf(yi[i], ej[j], P[i][j]);
                         F[i][j] = fmaf(di[i], ej[j], F[i][j]);
                     }
 #pragma unroll
                 for (int j = 0; j < CW; ++j) {
-                    const float S = s.ST[c][tj + 16 * j], G = s.GT[c][tj + 16 * j];
+                    const float S = s.ST[c][tj + 32 * j], G = s.GT[c][tj + 32 * j];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         aq[i][j] = fmaf(yi[i], S, aq[i][j]);
@@ -179,8 +179,8 @@ __global__ void __launch_bounds__(kThr) delta_grad_kernel(const GradParams p) {
         for (int i = 0; i < 4; ++i) {
             const int ii = 4 * ti + i;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int jj = 4 * tj + j;
+            for (int j = 0; j < 2; ++j) {
+                const int jj = 2 * tj + j;
                 const float w = jj <= ii ? decay(ii, jj) * s.b[jj] : 0.f;
                 s.P[ii][jj] = w * P[i][j];
                 if (jj <= ii) {
@@ -217,7 +217,7 @@ __global__ void __launch_bounds__(kThr) delta_grad_kernel(const GradParams p) {
                 }
 #pragma unroll
                 for (int j = 0; j < CW; ++j) {
-                    const float kx = s.rows[t][tj + 16 * j], qx = s.rows2[t][tj + 16 * j];
+                    const float kx = s.rows[t][tj + 32 * j], qx = s.rows2[t][tj + 32 * j];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         aq[i][j] = fmaf(a0[i], kx, aq[i][j]);
@@ -233,9 +233,9 @@ __global__ void __launch_bounds__(kThr) delta_grad_kernel(const GradParams p) {
                 float x = 0.f;
                 if (t < p.N)
 #pragma unroll
-                    for (int j = 0; j < CW; ++j) x = fmaf(to_f(q[rk.at(t) + tj + 16 * j]), aq[i][j], x);
+                    for (int j = 0; j < CW; ++j) x = fmaf(to_f(q[rk.at(t) + tj + 32 * j]), aq[i][j], x);
 #pragma unroll
-                for (int o = 8; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+                for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
                 if (tj == 0) s.qdq[4 * ti + i] = x;
             }
             gs = warp_sum(gs);
@@ -276,8 +276,8 @@ __global__ void __launch_bounds__(kThr) delta_grad_kernel(const GradParams p) {
         if (t >= n) continue;
 #pragma unroll
         for (int j = 0; j < CW; ++j) {
-            ((T *)p.dq)[rk.at(t0 + t) + tj + 16 * j] = from_f<T>(dq[i][j]);
-            ((T *)p.dk)[rk.at(t0 + t) + tj + 16 * j] = from_f<T>(dk[i][j]);
+            ((T *)p.dq)[rk.at(t0 + t) + tj + 32 * j] = from_f<T>(dq[i][j]);
+            ((T *)p.dk)[rk.at(t0 + t) + tj + 32 * j] = from_f<T>(dk[i][j]);
         }
     }
 }
