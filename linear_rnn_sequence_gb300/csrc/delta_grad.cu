@@ -14,7 +14,12 @@
 // the block hands on).
 //
 // A CTA takes one block of one key head, sums over that head's value heads
-// in registers and writes dq and dk once.
+// in registers and writes dq and dk once.  512 threads, a warp for each 4 tokens
+// (its factors of the products are broadcasts), lanes along the features: bound
+// by the latency of the staged slices, which 16 warps cover better than 8
+// (B8 H16 N512 d64 float32: 473 us for the gradients, 568 with 256 threads).  The
+// gates' sums run as float32 pairs in one warp: 64-bit additions by one thread
+// were a quarter of the kernel's time.
 #include "delta_common.cuh"
 
 namespace la {
