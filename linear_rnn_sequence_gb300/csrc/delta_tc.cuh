@@ -89,14 +89,19 @@ template <bool REV> __device__ __forceinline__ void block_gates(Gates &g, const 
 
 // T = (I + A)^-1 in place, for A [64][64] strictly lower triangular with zeros above (row pitch
 // kAP), by the 64 threads of a T group: the four diagonal blocks of 16 by forward substitution, a
-// thread for each column, then twice [[T1, 0], [-T2 A21 T1, T2]].
+// thread for each column, then twice [[T1, 0], [-T2 A21 T1, T2]].  In the second merge a warp has
+// half of the product's columns (with T1 on the right), then half of its rows (with T2 on the left), and
+// leaves out the terms that are zero for all of them.
 template <int SZ> __device__ __forceinline__ void merge_blocks(float *A, int t, int bar) {
     constexpr int RT = SZ / 8, PER = SZ * SZ / 4 / RT;   // rows of a thread (x 4 columns), threads a pair
-    const int pair = t / PER, q = t % PER;
-    const int r = q / (SZ / 4) * RT, c = q % (SZ / 4) * 4;
+    const int pair = t / PER, q = t % PER, half = SZ == 32 ? q >> 5 : 0;
     float *T1 = A + pair * 2 * SZ * (kAP + 1), *A21 = T1 + SZ * kAP, *T2 = A21 + SZ;
 #pragma unroll 1
     for (int step = 0; step < 2; ++step) {   // A21 <- A21 T1, then A21 <- -T2 A21
+        const bool by_col = SZ == 32 && step == 0;
+        const int r = by_col ? q % 8 : q / (SZ / 4) * RT, rs = by_col ? 8 * kAP : kAP;   // first row, row stride
+        const int c = by_col ? q / 8 * 4 : q % (SZ / 4) * 4;
+        const int m0 = by_col ? half * 16 : 0, m1 = SZ == 32 && step == 1 ? half * 16 + 16 : SZ;
         const float *L = (step ? T2 : A21) + r * kAP, *Rm = (step ? A21 : T1) + c;
         float acc[RT][4];
 #pragma unroll
@@ -104,11 +109,11 @@ template <int SZ> __device__ __forceinline__ void merge_blocks(float *A, int t, 
 #pragma unroll
             for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
 #pragma unroll 2
-        for (int m = 0; m < SZ; m += 4) {
+        for (int m = m0; m < m1; m += 4) {
             float l[RT][4];
 #pragma unroll
             for (int i = 0; i < RT; ++i)
-                *reinterpret_cast<float4 *>(l[i]) = *reinterpret_cast<const float4 *>(L + i * kAP + m);
+                *reinterpret_cast<float4 *>(l[i]) = *reinterpret_cast<const float4 *>(L + i * rs + m);
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 const float4 x = *reinterpret_cast<const float4 *>(Rm + (m + k) * kAP);
@@ -125,7 +130,7 @@ template <int SZ> __device__ __forceinline__ void merge_blocks(float *A, int t, 
         const float sg = step ? -1.f : 1.f;
 #pragma unroll
         for (int i = 0; i < RT; ++i)
-            *reinterpret_cast<float4 *>(A21 + (r + i) * kAP + c) =
+            *reinterpret_cast<float4 *>(A21 + r * kAP + i * rs + c) =
                 make_float4(sg * acc[i][0], sg * acc[i][1], sg * acc[i][2], sg * acc[i][3]);
         named_bar(bar, kInner);
     }
