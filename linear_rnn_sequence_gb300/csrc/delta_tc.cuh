@@ -103,11 +103,9 @@ template <int SZ> __device__ __forceinline__ void merge_blocks(float *A, int t, 
         const int c = by_col ? q / 8 * 4 : q % (SZ / 4) * 4;
         const int m0 = by_col ? half * 16 : 0, m1 = SZ == 32 && step == 1 ? half * 16 + 16 : SZ;
         const float *L = (step ? T2 : A21) + r * kAP, *Rm = (step ? A21 : T1) + c;
-        float acc[RT][4];
+        uint64_t acc[RT][2];
 #pragma unroll
-        for (int i = 0; i < RT; ++i)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
+        for (int i = 0; i < RT; ++i) acc[i][0] = acc[i][1] = 0ull;
 #pragma unroll 2
         for (int m = m0; m < m1; m += 4) {
             float l[RT][4];
@@ -116,22 +114,25 @@ template <int SZ> __device__ __forceinline__ void merge_blocks(float *A, int t, 
                 *reinterpret_cast<float4 *>(l[i]) = *reinterpret_cast<const float4 *>(L + i * rs + m);
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                const float4 x = *reinterpret_cast<const float4 *>(Rm + (m + k) * kAP);
+                const ulonglong2 x = *reinterpret_cast<const ulonglong2 *>(Rm + (m + k) * kAP);
 #pragma unroll
                 for (int i = 0; i < RT; ++i) {
-                    acc[i][0] = fmaf(l[i][k], x.x, acc[i][0]);
-                    acc[i][1] = fmaf(l[i][k], x.y, acc[i][1]);
-                    acc[i][2] = fmaf(l[i][k], x.z, acc[i][2]);
-                    acc[i][3] = fmaf(l[i][k], x.w, acc[i][3]);
+                    const uint64_t l2 = f2pack(l[i][k], l[i][k]);
+                    acc[i][0] = f2fma(l2, x.x, acc[i][0]);
+                    acc[i][1] = f2fma(l2, x.y, acc[i][1]);
                 }
             }
         }
         named_bar(bar, kInner);
         const float sg = step ? -1.f : 1.f;
 #pragma unroll
-        for (int i = 0; i < RT; ++i)
+        for (int i = 0; i < RT; ++i) {
+            float y[4];
+            f2unpack(acc[i][0], y[0], y[1]);
+            f2unpack(acc[i][1], y[2], y[3]);
             *reinterpret_cast<float4 *>(A21 + r * kAP + i * rs + c) =
-                make_float4(sg * acc[i][0], sg * acc[i][1], sg * acc[i][2], sg * acc[i][3]);
+                make_float4(sg * y[0], sg * y[1], sg * y[2], sg * y[3]);
+        }
         named_bar(bar, kInner);
     }
 }
