@@ -223,13 +223,14 @@ delta_rev_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
                 for (int u = 0; u < 2; ++u) {
                     const int j0 = half * 32 + u * 16;
                     uint32_t gk[16], py[16], hi[8], mi[8], lo[8];
-                    float w[16];
+                    float w[16], z[16];
                     tmem_ld16(tb + lb + kColGK + j0, gk);
                     tmem_ld16(tb + lb + kColPY + j0, py);
                     load16(&G.w[j0], w);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) w[j] = fmaf(w[j], u2f(gk[j]), u2f(py[j]));
+                    for (int j = 0; j < 16; ++j) z[j] = u2f(py[j]);
+                    fma16(w, gk, z);
 #pragma unroll
                     for (int i = 0; i < 8; ++i) split3(w[2 * i], w[2 * i + 1], hi[i], mi[i], lo[i]);
                     const uint32_t col = tb + lb + kColR + j0 / 2;
@@ -286,7 +287,9 @@ delta_rev_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
                     load16(&G.c[j0], c);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) w[j] = -(w[j] * c[j]) * u2f(acc[j]);
+                    for (int j = 0; j < 16; j += 2)
+                        f2unpack(f2mul(f2pack(-w[j], -w[j + 1]), f2pack(c[j], c[j + 1])), w[j], w[j + 1]);
+                    mul16(w, acc);
 #pragma unroll
                     for (int i = 0; i < 8; ++i) split3(w[2 * i], w[2 * i + 1], hi[i], mi[i], lo[i]);
                     const uint32_t col = tb + lb + kColW + j0 / 2;

@@ -265,9 +265,10 @@ delta_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
                     load16(&G.c[j0], c);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) r[j] = fmaf(-c[j], u2f(acc[j]), r[j]);
+                    for (int j = 0; j < 16; ++j) c[j] = -c[j];
+                    fma16(c, acc, r);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) split3(r[2 * i], r[2 * i + 1], hi[i], mi[i], lo[i]);
+                    for (int i = 0; i < 8; ++i) split3(c[2 * i], c[2 * i + 1], hi[i], mi[i], lo[i]);
                     const uint32_t col = tb + lb + kColR + j0 / 2;
                     tmem_st8(col, hi);
                     tmem_st8(col + 32, mi);
@@ -312,9 +313,9 @@ delta_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
                     tmem_ld16(tb + lb + kColKS + j0, acc);
                     load16(&G.w[j0], w);
                     tmem_wait_ld();
+                    mul16(w, acc);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        split3(w[2 * i] * u2f(acc[2 * i]), w[2 * i + 1] * u2f(acc[2 * i + 1]), hi[i], mi[i], lo[i]);
+                    for (int i = 0; i < 8; ++i) split3(w[2 * i], w[2 * i + 1], hi[i], mi[i], lo[i]);
                     if (Y && u == 0) {   // W takes the place of the state's pieces
                         ok = __all_sync(0xffffffffu, mbar_wait<1>(&S.qs_done, n & 1, g, 6));
                         if (!ok) break;
@@ -506,9 +507,10 @@ delta_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
             named_bar(bar, kInner);
 #pragma unroll
             for (int q = 0; q < 8; ++q) {
-                uint32_t hi[4], mi[4], lo[4];
+                uint32_t hi[4] = {}, mi[4] = {}, lo[4] = {};
+                if (8 * q <= (t | 31))   // warp-uniform: zeros otherwise
 #pragma unroll
-                for (int e = 0; e < 4; ++e) split3(x[8 * q + 2 * e], x[8 * q + 2 * e + 1], hi[e], mi[e], lo[e]);
+                    for (int e = 0; e < 4; ++e) split3(x[8 * q + 2 * e], x[8 * q + 2 * e + 1], hi[e], mi[e], lo[e]);
                 const uint32_t o = sw128_off(t, 8 * q);
                 *reinterpret_cast<uint4 *>(sTg + o) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
                 *reinterpret_cast<uint4 *>(sTg + 8192 + o) = make_uint4(mi[0], mi[1], mi[2], mi[3]);

@@ -139,19 +139,17 @@ template <int SZ> __device__ __forceinline__ void merge_blocks(float *A, int t, 
 __device__ __forceinline__ void invert_unit_lower(float *A, int t, int bar) {
     float *blk = A + (t >> 4) * 16 * (kAP + 1);
     const int c = t & 15;
-    float x[16];
+    float x[16] = {};
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-        float v = i == c ? 1.f : 0.f, w = 0.f;
+        uint64_t v = 0ull;   // of even and of odd j; A_ii is zero
 #pragma unroll
         for (int j = 0; j < i; j += 4) {
-            const float4 a = *reinterpret_cast<const float4 *>(blk + i * kAP + j);
-            v = fmaf(-a.x, x[j], v);
-            if (j + 1 < i) w = fmaf(-a.y, x[j + 1], w);
-            if (j + 2 < i) v = fmaf(-a.z, x[j + 2], v);
-            if (j + 3 < i) w = fmaf(-a.w, x[j + 3], w);
+            const ulonglong2 a = *reinterpret_cast<const ulonglong2 *>(blk + i * kAP + j);
+            v = f2fma(a.x, f2pack(x[j], x[j + 1]), v);
+            if (j + 2 < i) v = f2fma(a.y, f2pack(x[j + 2], x[j + 3]), v);
         }
-        x[i] = v + w;
+        x[i] = (i == c ? 1.f : 0.f) - f2sum(v);
     }
     named_bar(bar, kInner);
 #pragma unroll
@@ -161,6 +159,19 @@ __device__ __forceinline__ void invert_unit_lower(float *A, int t, int bar) {
     merge_blocks<32>(A, t, bar);
 }
 
+// x <- a x and x <- a x + b, by pairs.
+__device__ __forceinline__ void mul16(float (&x)[16], const uint32_t (&a)[16]) {
+#pragma unroll
+    for (int j = 0; j < 16; j += 2)
+        f2unpack(f2mul(f2pack(x[j], x[j + 1]), f2pack(u2f(a[j]), u2f(a[j + 1]))), x[j], x[j + 1]);
+}
+__device__ __forceinline__ void fma16(float (&x)[16], const uint32_t (&a)[16], const float (&b)[16]) {
+#pragma unroll
+    for (int j = 0; j < 16; j += 2)
+        f2unpack(f2fma(f2pack(x[j], x[j + 1]), f2pack(u2f(a[j]), u2f(a[j + 1])), f2pack(b[j], b[j + 1])), x[j],
+                 x[j + 1]);
+}
+
 // x_j = D_ij b_j s_j (REV: D_ij s_j) for 16 columns j0.. of row i (s: 16 scores; LD: still in flight from TMEM).
 template <bool LD, bool REV>
 __device__ __forceinline__ void decayed16(const Gates &G, int i, int j0, const uint32_t (&s)[16], float (&x)[16]) {
@@ -168,8 +179,10 @@ __device__ __forceinline__ void decayed16(const Gates &G, int i, int j0, const u
         const float c = G.c[i];
         load16(&G.f[j0], x);
         if (LD) tmem_wait_ld();
+        const uint64_t c2 = f2pack(c, c);
 #pragma unroll
-        for (int j = 0; j < 16; ++j) x[j] = c * x[j] * u2f(s[j]);
+        for (int j = 0; j < 16; j += 2)
+            f2unpack(f2mul(f2mul(c2, f2pack(x[j], x[j + 1])), f2pack(u2f(s[j]), u2f(s[j + 1]))), x[j], x[j + 1]);
     } else {
         const float hi = G.hi[i], lo = G.lo[i];
         float y[16];
