@@ -551,13 +551,15 @@ delta_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
             const int i = row & 63;
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
-                uint32_t hi[8], mi[8];
-                float x[16];
-                decayed16<false, false>(G, i, 16 * u, sc[u], x);
+                uint32_t hi[8] = {}, mi[8] = {};
+                if (16 * u <= (i | 31)) {   // warp-uniform: zeros otherwise
+                    float x[16];
+                    decayed16<false, false>(G, i, 16 * u, sc[u], x);
 #pragma unroll
-                for (int j = 0; j < 16; ++j) x[j] = 16 * u + j <= i ? x[j] : 0.f;
+                    for (int j = 0; j < 16; ++j) x[j] = 16 * u + j <= i ? x[j] : 0.f;
 #pragma unroll
-                for (int j = 0; j < 8; ++j) split2(x[2 * j], x[2 * j + 1], hi[j], mi[j]);
+                    for (int j = 0; j < 8; ++j) split2(x[2 * j], x[2 * j + 1], hi[j], mi[j]);
+                }
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
                     const uint32_t o = sw128_off(i, 16 * u + 8 * q);
