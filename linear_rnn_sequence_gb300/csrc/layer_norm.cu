@@ -4,8 +4,8 @@
 // registers between its statistics and its result, and the variance is taken
 // about the mean (a second pass over registers) rather than as a difference of
 // squares.  G threads share a row (16, 32, or a whole CTA for long rows) and
-// load 16-byte vectors, or single values where the row length or a pointer is
-// not a multiple of 16 bytes.  1048576 x 128 bf16: 93 us, 5.8 TB/s of the 6.8
+// load 16-byte vectors, or two values or one where the row length or a pointer is
+// not a multiple of 16 bytes or of two values.  1048576 x 128 bf16: 93 us, 5.8 TB/s of the 6.8
 // that a copy reaches; gradients at 65536 x 2048: 154 us, 5.2 TB/s.
 //
 // The gradient kernel keeps the column sums of dy xh and dy of all its rows in
@@ -25,6 +25,27 @@ template <typename T> struct Vec<T, 1> {
     static __device__ __forceinline__ Raw zero() { return from_f<T>(0.f); }
     static __device__ __forceinline__ void unpack(Raw r, float (&x)[1]) { x[0] = to_f(r); }
     static __device__ __forceinline__ void store(T *p, const float (&x)[1]) { *p = from_f<T>(x[0]); }
+};
+template <> struct Vec<float, 2> {
+    using Raw = float2;
+    static __device__ __forceinline__ Raw load(const float *p) { return *reinterpret_cast<const float2 *>(p); }
+    static __device__ __forceinline__ Raw zero() { return make_float2(0.f, 0.f); }
+    static __device__ __forceinline__ void unpack(Raw r, float (&x)[2]) { x[0] = r.x; x[1] = r.y; }
+    static __device__ __forceinline__ void store(float *p, const float (&x)[2]) {
+        *reinterpret_cast<float2 *>(p) = make_float2(x[0], x[1]);
+    }
+};
+template <> struct Vec<__nv_bfloat16, 2> {
+    using Raw = unsigned;
+    static __device__ __forceinline__ Raw load(const __nv_bfloat16 *p) { return *reinterpret_cast<const unsigned *>(p); }
+    static __device__ __forceinline__ Raw zero() { return 0u; }
+    static __device__ __forceinline__ void unpack(Raw r, float (&x)[2]) {
+        x[0] = tc::bf16_lo_f(r);
+        x[1] = tc::bf16_hi_f(r);
+    }
+    static __device__ __forceinline__ void store(__nv_bfloat16 *p, const float (&x)[2]) {
+        *reinterpret_cast<unsigned *>(p) = tc::pack_bf16x2(x[0], x[1]);
+    }
 };
 template <> struct Vec<float, 4> {
     using Raw = float4;
@@ -358,7 +379,7 @@ int backward_ctas(long long rows, int rows_per_cta) {
     return (int)(need < most ? (need > 0 ? need : 1) : most);
 }
 
-bool vec16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned(const void *p, size_t bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
 
 template <typename T, int E, int V, int G, int RW, int THR>
 cudaError_t go(const LayerNormArgs &a, bool backward) {
@@ -385,19 +406,28 @@ cudaError_t go(const LayerNormArgs &a, bool backward) {
 // a row.  Two rows of a group at once, beside the next two on their way, where a thread has one vector
 // of a row (1048576 x 128 bf16: 92 us, 101 without the next ones, 121 with four rows and without);
 // one row where it has more, and for few rows, which want threads rather than rows in flight.
+// Pairs and single values: a warp to a row as far as its registers go, and threads that fit the row beyond
+// (gradients, 61688 x 158 float32: 36 us, 127 with 256 threads a row; 13550 x 2090 bf16: 60 us, 135 by single values).
 template <typename T, int E, int V, int G, int THR>
 cudaError_t rows_in_flight(const LayerNormArgs &a, bool bwd) {
-    constexpr int RW = V * E <= 8 ? 2 : 1;
+    constexpr int RW = V * E <= (E > 2 ? 8 : 4) ? 2 : 1;
     if (RW == 1 || a.rows >= 4LL * RW * sm_count() * (THR / G)) return go<T, E, V, G, RW, THR>(a, bwd);
     return go<T, E, V, G, 1, THR>(a, bwd);
 }
 template <typename T, int E> cudaError_t shape(const LayerNormArgs &a, bool bwd) {
     const int n = (a.D + E - 1) / E;
-    if (E == 1) {
+    if (E <= 2) {   // rows that start anywhere: a warp takes up to 512 values
+        if (n <= 16) return rows_in_flight<T, E, 1, 16, 256>(a, bwd);
+        if (n <= 32) return rows_in_flight<T, E, 1, 32, 256>(a, bwd);
+        if (n <= 64) return rows_in_flight<T, E, 2, 32, 256>(a, bwd);
         if (n <= 128) return rows_in_flight<T, E, 4, 32, 256>(a, bwd);
+        if (n <= 256) return rows_in_flight<T, E, 8, 32, 256>(a, bwd);
+        if (E == 1 && n <= 512) return rows_in_flight<T, E, 16 / E, 32, 256>(a, bwd);
         if (n <= 1024) return rows_in_flight<T, E, 4, 256, 256>(a, bwd);
-        if (n <= 4096) return rows_in_flight<T, E, 16, 256, 256>(a, bwd);
-        return rows_in_flight<T, E, 16, 1024, 1024>(a, bwd);
+        if (n <= 2048) return rows_in_flight<T, E, 8, 256, 256>(a, bwd);
+        if (n <= 4096) return rows_in_flight<T, E, 8, 512, 512>(a, bwd);
+        if (n <= 8192) return rows_in_flight<T, E, 8, 1024, 1024>(a, bwd);
+        return rows_in_flight<T, E, 16 / E, 1024, 1024>(a, bwd);
     }
     if (n <= 16) return rows_in_flight<T, E, 1, 16, 256>(a, bwd);
     if (n <= 32) return rows_in_flight<T, E, 1, 32, 256>(a, bwd);
@@ -411,8 +441,12 @@ template <typename T, int E> cudaError_t shape(const LayerNormArgs &a, bool bwd)
 
 template <typename T> cudaError_t run(const LayerNormArgs &a, bool bwd) {
     constexpr int E = 16 / (int)sizeof(T);
-    const bool wide = a.D % E == 0 && vec16(a.x) && (bwd ? vec16(a.dy) && vec16(a.dx) : vec16(a.y));
-    return wide ? shape<T, E>(a, bwd) : shape<T, 1>(a, bwd);
+    auto by = [&](int e) {
+        const size_t n = e * sizeof(T);
+        return a.D % e == 0 && aligned(a.x, n) && (bwd ? aligned(a.dy, n) && aligned(a.dx, n) : aligned(a.y, n));
+    };
+    if (by(E)) return shape<T, E>(a, bwd);
+    return by(2) ? shape<T, 2>(a, bwd) : shape<T, 1>(a, bwd);
 }
 
 cudaError_t dispatch(const LayerNormArgs &a, bool bwd) {

@@ -253,6 +253,30 @@ def test_layer_norm(dtype, rows, D, affine):
     assert only[1] is None and torch.equal(only[0], gx)
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("rows,D", [(9001, 22), (40009, 31), (30001, 46), (20003, 65), (6007, 158), (5003, 333), (3001, 510),
+                                    (777, 1062), (333, 2090), (100, 4431), (50, 6290), (20, 12290), (3, 16382)])
+def test_layer_norm_of_rows_that_start_anywhere(dtype, rows, D):
+    test_layer_norm(dtype, rows, D, True)
+
+
+@pytest.mark.parametrize("offset", [1, 2, 4])
+def test_layer_norm_off_its_vectors(offset):
+    """Even widths whose rows start 2, 4 or 8 bytes off: single values or pairs, in x, y, dy and dx alike."""
+    for D in (96, 158):
+        buf, out = torch.randn(2, 50 * D + offset, device="cuda").to(BF16)
+        x, y = buf[offset:].view(50, D), out[offset:].view(50, D)
+        got, mean, rstd = la.layer_norm(x, out=y, return_stats=True)
+        want, mr, rr = R.layer_norm(x.cpu())
+        assert got is y
+        R.check(y, want, "y", R_NORM)
+        gx, _, _ = la.layer_norm_backward(y, x, mean, rstd)
+        gxr, _, _ = R.layer_norm_backward(y.cpu(), x.cpu(), mean.cpu(), rstd.cpu())
+        # y lies almost along xh, so the gradient is a small difference of terms of the size of dy rstd
+        scale = (y.cpu().double() * rr[:, None]).square().mean().sqrt() / gxr.square().mean().sqrt()
+        R.check(gx, gxr, "grad_x", R_NORM * max(1.0, scale.item()))
+
+
 def test_layer_norm_unaligned_rows_and_in_place():
     # rows that start 2 bytes off a 16-byte boundary, and y written over x
     buf = torch.randn(4 * 128 + 1, device="cuda").to(BF16)
