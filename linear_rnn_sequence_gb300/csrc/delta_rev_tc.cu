@@ -14,8 +14,10 @@
 // on top: dy^T P0 straight from the dy tile (exact bf16, dv-major), and c . dy
 // as pieces, made beside the right-hand side by the warps of P0.  In TMEM the
 // right-hand side takes the upper part of the place of G's pieces, c . dy the
-// lower one, and -b c . du that of the right-hand side.  G is written while the next block's K G runs.
-// B8 H16 N8192 d128: 0.76 ms (6.0 us a block; 0.92 with c . dy made by the chain and G written in it).
+// lower one, and -b c . du that of the right-hand side.  G is
+// written while the next block's K G runs.
+// B8 H16 N8192 d128: 0.69 ms (5.4 us a block; with c . dy made by the chain and G written
+// in it, 0.13 ms more).
 #include "delta_tc.cuh"
 
 namespace la {

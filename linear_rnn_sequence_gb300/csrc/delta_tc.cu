@@ -26,9 +26,9 @@
 // K K^T of the even blocks into T, warps 10 and 11 that of the odd ones, both
 // ahead of the chain; warps 12-15 turn Q K^T into P (two of them), make P e and
 // write y.
-// Bound by the chain of a block, about 10 K cycles of which the tensor pipe is
-// busy a third: B8 H16 N8192 d128 0.67 ms, 1.6 TB/s; B1 H32 N131072 d64, split
-// in four, 3.7 ms.
+// Bound by the chain of a block, about 9 K cycles of which the tensor pipe is
+// busy a third: B8 H16 N8192 d128 0.61 ms, 1.8 TB/s; B1 H32 N131072 d64, split
+// in four, 3.5 ms.
 // The rows of [K; Q] K^T are TMEM lanes, which a warp reaches by its number
 // mod 4: so odd blocks hold Q before K.  The chain's first warp issues its
 // MMAs and the TMA loads.
@@ -731,7 +731,7 @@ __global__ void __launch_bounds__(kPrefixThr) delta_prefix_kernel(const PrefixAr
 // each head then run once more, ahead, from an empty state (ceil((dv + d) / 128) CTAs each), and
 // their ends are joined.  In units of a block's time (about 5 us): a wave of CTAs takes its
 // segments' length; a second start, the join and their launches take about 8 + nseg / 2 (24 heads of
-// 17 blocks: 94 us whole, 103 us in four; 32 heads of 2048 blocks: 8.4 ms whole, 3.6 ms in four).
+// 17 blocks: 94 us whole, 103 us in four; 32 heads of 2048 blocks: 8.4 ms whole, 3.5 ms in four).
 void delta_segments(const DeltaArgs &a, int &nseg, int &seg_blocks) {
     const int nblk = delta_blocks(a.N), sms = num_sms(), parts = (a.dv + a.d + 127) / 128;
     const long long BH = (long long)a.B * a.H;
