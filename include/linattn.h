@@ -567,6 +567,13 @@ LA_API la_status la_workspace_status(const void *workspace, size_t workspace_byt
 LA_API void la_debug_set_fault(int drop_load_item, long long wait_limit_ns);
 
 /*
+ * Test hook of the same kind: the warps that write y in la_forward_delta's
+ * tensor-core kernel start `ns` nanoseconds late (0 to 1000000; 0: off).  No
+ * result depends on it.
+ */
+LA_API void la_debug_set_stall(long long ns);
+
+/*
  * Test hook (no counterpart on the pages): writes to out[i] (bf16) the
  * feature residual that the tensor-core kernels feed to the MMAs for the bf16
  * input x[i]: phi(x) - c rounded to bf16, phi(x) = elu(x) + 1 ("Mapas de

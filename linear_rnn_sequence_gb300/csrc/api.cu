@@ -736,4 +736,6 @@ void la_debug_set_fault(int drop_load_item, long long wait_limit_ns) {
     debug_fault().wait_limit_ns = wait_limit_ns;
 }
 
+void la_debug_set_stall(long long ns) { debug_fault().stall_ns = ns < 0 ? 0 : ns > 1000000 ? 1000000 : ns; }
+
 }  // extern "C"

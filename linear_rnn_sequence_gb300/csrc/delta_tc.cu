@@ -56,13 +56,13 @@ struct DeltaTc {
     float *S_ck, *e;               // kSave
     float *S_local, *Phi;          // kSegment, by (head, its segment)
     unsigned int *err, *err_where;
-    unsigned long long limit_ns;
+    unsigned long long limit_ns, stall_ns;   // stall_ns, drop_item: test hooks
     int drop_item;
 };
 
 struct DeltaSmall {
     Gates gates[4];
-    uint64_t kq_full[kStages], v_full[2], kk_full, kk_read, g_ready[2], t_ready[2], t_free[2], p_ready, ks_done, qs_done, e_done, s_done, e_read, pu_done, o_read, drain[4];
+    uint64_t kq_full[kStages], v_full[2], kk_full, kk_read[2], g_ready[2], t_ready[2], t_free[2], p_ready, ks_done, qs_done, e_done, s_done, e_read, pu_done, o_read, drain[4];
     uint32_t tmem_base;
     volatile int abort_flag;
 };
@@ -117,10 +117,10 @@ delta_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
             mbar_init(&S.t_ready[i], kInner);
             mbar_init(&S.g_ready[i], 32);
             mbar_init(&S.t_free[i], 1);
+            mbar_init(&S.kk_read[i], Y ? 2 * kInner : kInner);   // a thread for each row of K, and of Q
         }
         for (int i = 0; i < 4; ++i) mbar_init(&S.drain[i], 1);
         mbar_init(&S.kk_full, 1);
-        mbar_init(&S.kk_read, Y ? 2 * kInner : kInner);   // a thread for each row of K, and of Q
         mbar_init(&S.p_ready, 64);
         mbar_init(&S.ks_done, 1);
         mbar_init(&S.qs_done, 1);
@@ -446,8 +446,10 @@ delta_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
             // is y n - 4 (block n - 2's K S waited for y n - 3)
             Gates &G = S.gates[n & 3];
             bool ok = n < 2 || mbar_wait<1>(&S.t_free[grp], ((n >> 1) - 1) & 1, g, 23);
-            // the block before's [K; Q] K^T and gates have been read
-            if (n > 0) ok = ok && mbar_wait<1>(&S.kk_read, (n - 1) & 1, g, 24);
+            // the block before's [K; Q] K^T and gates have been read, and so those of every block before
+            // it: a barrier for the even and one for the odd blocks, since the phase after block n - 2's
+            // has the parity of the one before it, and the scores of block 0 may be read late
+            if (n > 0) ok = ok && mbar_wait<1>(&S.kk_read[~n & 1], ((n - 1) >> 1) & 1, g, 24);
             if (!gates_warp) {
                 ok = ok && mbar_wait<1>(&S.kq_full[n % kStages], (n / kStages) & 1, g, 20);
                 ok = __all_sync(0xffffffffu, ok);
@@ -495,7 +497,7 @@ delta_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
                             make_float4(x[j], x[j + 1], x[j + 2], x[j + 3]);
                 }
                 tc_fence_before();
-                mbar_arrive(&S.kk_read);
+                mbar_arrive(&S.kk_read[grp]);
             }
             if (any_out(!ok)) break;   // A complete
             invert_unit_lower(A, t, bar);
@@ -542,7 +544,7 @@ delta_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
                 for (int u = 0; u < 4; ++u) tmem_ld16(tb + lb + kColKK + 16 * u, sc[u]);
                 tmem_wait_ld();
                 tc_fence_before();
-                mbar_arrive(&S.kk_read);
+                mbar_arrive(&S.kk_read[n & 1]);
             }
             return ok;
         };
@@ -572,6 +574,8 @@ delta_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
             fence_proxy_async();
             mbar_arrive(&S.p_ready);
         };
+        if (p.stall_ns)
+            for (const uint64_t t0 = globaltimer_ns(); globaltimer_ns() - t0 < p.stall_ns;) __nanosleep(1000);
         bool good = true;
         if (rows_of_q(0)) {
             good = read_scores(0);
@@ -812,6 +816,7 @@ template <int D, int DV> DeltaTc tc_params(const DeltaArgs &a) {
     const long long lim = debug_fault().wait_limit_ns;
     p.limit_ns = lim > 0 ? (unsigned long long)lim : 1000000000ull;
     p.drop_item = debug_fault().drop_load_item;
+    p.stall_ns = (unsigned long long)debug_fault().stall_ns;
     return p;
 }
 

@@ -123,6 +123,7 @@ static_assert(sizeof(WsHeader) == 256, "workspace header must be 256 bytes");
 struct DebugFault {
     int drop_load_item = -1;      // work item whose first tile copy is never issued
     long long wait_limit_ns = 0;  // <= 0: default limit of every bounded wait
+    long long stall_ns = 0;       // how late the delta rule's output warps start
 };
 DebugFault &debug_fault();
 

@@ -96,6 +96,8 @@ def lib():
             L.la_workspace_status.restype = i
             L.la_debug_set_fault.argtypes = [i, ctypes.c_longlong]
             L.la_debug_set_fault.restype = None
+            L.la_debug_set_stall.argtypes = [ctypes.c_longlong]
+            L.la_debug_set_stall.restype = None
             L.la_debug_feature_bf16.argtypes = [vp, vp, ctypes.c_longlong, f, vp]
             L.la_debug_feature_bf16.restype = i
             L.la_forward_noncausal_noalloc.argtypes = [vp, vp, vp, vp, i, i, i, i, i, i, f, vp,
@@ -441,6 +443,12 @@ def workspace_header(workspace) -> tuple[int, int]:
 def set_fault(drop_load_item: int = -1, wait_limit_ns: int = 0) -> None:
     """Test hook: see la_debug_set_fault in include/linattn.h."""
     lib().la_debug_set_fault(int(drop_load_item), int(wait_limit_ns))
+
+
+def set_stall(ns: int = 0) -> None:
+    """Test hook: see la_debug_set_stall in include/linattn.h."""
+    lib().la_debug_set_stall(int(ns))
+
 
 def _gate_dim(gate, lead, d):
     """gate_dim of a gate tensor whose leading shape is ``lead`` (1 or d)."""

@@ -390,6 +390,21 @@ def test_a_dropped_copy_times_out_and_the_next_call_is_right(what, B, H, N):
     assert all(torch.equal(a, b) for a, b in zip(call(), want))
 
 
+@pytest.mark.parametrize("N", [40, 64, 65, 129, 200, 333, 1000, 4000])
+@pytest.mark.parametrize("d,dv", [(64, 64), (128, 128)])
+def test_late_output_warps(N, d, dv):
+    """The test hook starts the warps that read a block's scores and write y a good deal later than the
+    other blocks' inverses take: nothing overtakes them."""
+    x = on_gpu(R.inputs(2, 2, 1, N, d, dv, BF16, state=True, seed=N + d))
+    want = la.forward_delta(**x, return_state=True, check_status=True)
+    try:
+        la.set_stall(300_000)
+        got = la.forward_delta(**x, return_state=True, check_status=True)
+    finally:
+        la.set_stall(0)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
 # ---- what the binding refuses ----------------------------------------------------
 def test_binding_refuses():
     x = on_gpu(R.inputs(1, 4, 2, 40, 64, 64, BF16, state=True))
