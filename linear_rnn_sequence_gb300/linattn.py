@@ -225,7 +225,7 @@ def forward_causal(q, k, v, eps: float = 1e-6, S_in=None, z_in=None, return_stat
                                  float(eps), _ptr(S_in), _ptr(z_in), _ptr(S_out), _ptr(z_out),
                                  _ptr(workspace), wbytes, _stream_handle(stream, q.device))
     _raise(st, "la_forward_causal")
-    if check_status and workspace is not None:
+    if check_status and need and workspace is not None:   # without need nothing is recorded there
         err, where = workspace_header(workspace)
         if err != LA_OK:
             raise LinAttnError(err, f"la_forward_causal (run time, wait site {where})")
@@ -262,7 +262,7 @@ def forward_causal_decay(q, k, v, gamma, eps: float = 1e-6, S_in=None, z_in=None
                                        _ptr(S_out), _ptr(z_out), _ptr(workspace), wbytes,
                                        _stream_handle(stream, q.device))
     _raise(st, "la_forward_causal_decay")
-    if check_status and workspace is not None:
+    if check_status and need and workspace is not None:   # without need nothing is recorded there
         err, where = workspace_header(workspace)
         if err != LA_OK:
             raise LinAttnError(err, f"la_forward_causal_decay (run time, wait site {where})")
@@ -618,8 +618,8 @@ def _delta_backward_bytes(device_index, *sizes):
     return int(lib().la_delta_backward_workspace_bytes(*sizes))
 
 
-def _check_run_time(workspace, where):
-    if workspace is not None:
+def _check_run_time(workspace, need, where):
+    if need:   # a call that needs no workspace records nothing in one it is given
         err, site = workspace_header(workspace)
         if err != LA_OK:
             raise LinAttnError(err, f"{where} (run time, wait site {site})")
@@ -668,7 +668,8 @@ def forward_delta(q, k, v, beta, log_gate=None, S_in=None, return_state=False, o
         out = torch.empty_like(v)
     if return_state and S_out is None:
         S_out = torch.empty(state, dtype=torch.float32, device=q.device)
-    workspace, wa, wbytes = _workspace(workspace, _delta_bytes(dev, *sizes), q)
+    need = _delta_bytes(dev, *sizes)
+    workspace, wa, wbytes = _workspace(workspace, need, q)
     st = lib().la_forward_delta(qa, ka, va, _expect("out", out, v.shape, v.dtype, dev), ba, la, B, H, Hk,
                                 N, d, dv, dt, LAYOUT[layout],
                                 _expect("S_in", S_in, state, torch.float32, dev),
@@ -676,7 +677,7 @@ def forward_delta(q, k, v, beta, log_gate=None, S_in=None, return_state=False, o
                                 _current_stream(dev))
     _raise(st, "la_forward_delta")
     if check_status:
-        _check_run_time(workspace, "la_forward_delta")
+        _check_run_time(workspace, need, "la_forward_delta")
     return (out, S_out) if return_state else out
 
 
@@ -698,7 +699,8 @@ def backward_delta(q, k, v, beta, dy, log_gate=None, S_in=None, grad_S_out=None,
     gS = None
     if S_in is not None or grad_S_out is not None:
         gS = torch.empty(state, dtype=torch.float32, device=q.device)
-    workspace, wa, wbytes = _workspace(workspace, _delta_backward_bytes(dev, *sizes), q)
+    need = _delta_backward_bytes(dev, *sizes)
+    workspace, wa, wbytes = _workspace(workspace, need, q)
     st = lib().la_backward_delta(qa, ka, va, _expect("dy", dy, v.shape, v.dtype, dev), ba, la, gq.data_ptr(),
                                  gk.data_ptr(), gv.data_ptr(), gb.data_ptr(), _addr(gl), B, H, Hk, N, d, dv,
                                  dt, LAYOUT[layout], _expect("S_in", S_in, state, torch.float32, dev),
@@ -706,7 +708,7 @@ def backward_delta(q, k, v, beta, dy, log_gate=None, S_in=None, grad_S_out=None,
                                  wa, wbytes, _current_stream(dev))
     _raise(st, "la_backward_delta")
     if check_status:
-        _check_run_time(workspace, "la_backward_delta")
+        _check_run_time(workspace, need, "la_backward_delta")
     return gq, gk, gv, gb, gl, gS
 
 

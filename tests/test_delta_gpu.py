@@ -390,6 +390,21 @@ def test_a_dropped_copy_times_out_and_the_next_call_is_right(what, B, H, N):
     assert all(torch.equal(a, b) for a, b in zip(call(), want))
 
 
+@pytest.mark.parametrize("dtype,d,N", [(F32, 64, 70), (F32, 64, 0), (BF16, 32, 70), (BF16, 64, 5), (BF16, 64, 0)])
+def test_status_of_a_call_that_needs_no_workspace(dtype, d, N):
+    """Such a call leaves a given workspace alone: what an earlier one recorded there is not its status."""
+    x = on_gpu(R.inputs(1, 2, 2, N, d, d, dtype, state=True, seed=7))
+    marked = torch.full((1 << 22,), 255, dtype=torch.uint8, device="cuda")
+    y = la.forward_delta(**x, workspace=marked, check_status=True)
+    assert torch.equal(y, la.forward_delta(**x)) and (marked == 255).all()
+    if N == 0:   # the gradients need none either
+        la.backward_delta(x["q"], x["k"], x["v"], x["beta"], x["v"], x["log_gate"], workspace=marked, check_status=True)
+    if dtype == F32 and N:   # nor do the causal calls of this dtype
+        gamma = torch.full((2,), 0.9, device="cuda")
+        la.forward_causal(x["q"], x["k"], x["v"], workspace=marked, check_status=True)
+        la.forward_causal_decay(x["q"], x["k"], x["v"], gamma, workspace=marked, check_status=True)
+
+
 @pytest.mark.parametrize("N", [40, 64, 65, 129, 200, 333, 1000, 4000])
 @pytest.mark.parametrize("d,dv", [(64, 64), (128, 128)])
 def test_late_output_warps(N, d, dv):
