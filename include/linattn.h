@@ -448,7 +448,10 @@ LA_API size_t la_delta_workspace_bytes(int B, int H, int Hk, int N, int d, int d
  *            gate: the state restarts); NULL means no gate (a_t = 1).
  *   S_in     float32 [B][H][d][dv] or NULL (zero); S_out the final state or
  *            NULL; S_out may equal S_in.
- * A padding token with beta = 0 and log_gate = 0 leaves the state as it was.
+ * A padding token with beta = 0 and log_gate = 0 leaves the state as it was if
+ * its k and v are finite.  A value that is not finite reaches y of its own token
+ * and of later ones and the states behind it, as the recurrence has it, and
+ * nothing before its token.
  * d, dv in {32, 64, 128}; B, H, Hk >= 1; N >= 0 (N = 0 writes S_out only);
  * B*H*N*max(d, dv) < 2^31 and B*H*d*dv < 2^31.  q, k, v, y, S_in and S_out
  * 16-byte aligned, beta and log_gate 4-byte aligned.  y must overlap no other
@@ -486,7 +489,8 @@ LA_API size_t la_delta_backward_workspace_bytes(int B, int H, int Hk, int N, int
  * rounded); grad_beta and grad_log_gate are float32 in beta's layout.
  * grad_log_gate and log_gate are both given or both NULL; grad_S_in may be
  * NULL.  No output may overlap another buffer.  Same inputs as the forward;
- * the states are recomputed.
+ * the states are recomputed.  The inputs have to be finite (log_gate -inf
+ * apart): one that is not may make any gradient of its key head's heads NaN.
  */
 LA_API la_status la_backward_delta(const void *q, const void *k, const void *v, const void *dy,
                                    const float *beta, const float *log_gate, void *grad_q,

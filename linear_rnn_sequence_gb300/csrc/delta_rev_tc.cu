@@ -440,7 +440,7 @@ delta_rev_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
                 mbar_arrive(&S.kk_read);
             }
             if (any_out(!ok)) break;   // A complete
-            invert_unit_lower(A, t, bar);
+            invert_unit_lower<false>(A, t, bar, nullptr);
             // T^T's pieces over A: a thread's row (T's column) is in registers before any is written
             float x[kDC];
 #pragma unroll

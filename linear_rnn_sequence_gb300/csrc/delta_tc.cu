@@ -29,6 +29,12 @@
 // Bound by the chain of a block, about 9 K cycles of which the tensor pipe is
 // busy a third: B8 H16 N8192 d128 0.61 ms, 1.8 TB/s; B1 H32 N131072 d64, split
 // in four, 3.5 ms.
+// What is not finite must reach no token before its own, but the MMAs run over whole blocks, in which the
+// zeros above the diagonals of T and P meet later tokens' r and e.  So the kernel notes a row of y that is not
+// finite, and items with one run again, by a second launch whose other
+// CTAs end at once: there a thread leaves out what follows the first value of its row of r or e that is not
+// finite, and y and the state become NaN from there on.  (Those checks in every run took 8 to 10% of its time;
+// the note and the second launch take 1 us of a short call, and of B8 H16 N8192 d128 609 -> 616 us.)
 // The rows of [K; Q] K^T are TMEM lanes, which a warp reaches by its number
 // mod 4: so odd blocks hold Q before K.  The chain's first warp issues its
 // MMAs and the TMA loads.
@@ -55,6 +61,7 @@ struct DeltaTc {
     float *S_out;                  // by head
     float *S_ck, *e;               // kSave
     float *S_local, *Phi;          // kSegment, by (head, its segment)
+    unsigned int *redo;            // by (head, segment): y is not finite, kCareful has to run
     unsigned int *err, *err_where;
     unsigned long long limit_ns, stall_ns;   // stall_ns, drop_item: test hooks
     int drop_item;
@@ -62,7 +69,11 @@ struct DeltaTc {
 
 struct DeltaSmall {
     Gates gates[4];
-    uint64_t kq_full[kStages], v_full[2], kk_full, kk_read[2], g_ready[2], t_ready[2], t_free[2], p_ready, ks_done, qs_done, e_done, s_done, e_read, pu_done, o_read, drain[4];
+    uint64_t kq_full[kStages], v_full[2], kk_full, kk_read[2], g_ready[2], t_ready[2], t_free[2], p_ready, ks_done, qs_done, e_done, s_done, e_read, r_ready, pu_done, o_read, drain[4];
+    int first[2][128];   // kCareful, by half of the tokens and row of r: its first value that is not finite, or kDC
+    int cut[128];        // kCareful, by row of y: the first that is not finite, where the warp has one
+    int t_bad[2][2];     // kCareful, by T group and turn: the first row of T that is not what it should be, or kDC
+    int y_bad;
     uint32_t tmem_base;
     volatile int abort_flag;
 };
@@ -80,15 +91,18 @@ template <int D, int DV> struct DeltaLay {
 // What a launch computes.
 enum DeltaMode {
     kForward,   // y, from the initial state of each (head, segment)
+    kCareful,   // the same for those whose y is not finite
     kSave,      // the backward's first pass: e, and the state before every block and after the last
     kSegment    // segments from an empty state (rows < dv), and the segments' maps of the state:
                 // S_end = Phi S_start + S_local, row dv + a being column a of Phi (from a unit state,
                 // without values); `parts` CTAs of 128 rows each
 };
 
-// Only kForward launches warps 12-15.
+constexpr bool writes_y(int mode) { return mode == kForward || mode == kCareful; }
+
+// Only kForward and kCareful launch warps 12-15.
 template <int D, int DV, int MODE>
-__global__ void __launch_bounds__(kChain + 2 * kInner + (MODE == kForward ? kOut : 0), 1)
+__global__ void __launch_bounds__(kChain + 2 * kInner + (writes_y(MODE) ? kOut : 0), 1)
 delta_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                 const __grid_constant__ CUtensorMap vmap, const __grid_constant__ CUtensorMap ymap,
                 const DeltaTc p) {
@@ -101,7 +115,7 @@ delta_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
             *sY = sm + Lay::oY;
     // warp-uniform to the compiler too
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
-    constexpr bool Y = MODE == kForward, SAVE = MODE == kSave, SEG = MODE == kSegment;
+    constexpr bool Y = writes_y(MODE), CARE = MODE == kCareful, SAVE = MODE == kSave, SEG = MODE == kSegment;
     const int part = SEG ? blockIdx.x % p.parts : 0, item = SEG ? blockIdx.x / p.parts : blockIdx.x;
     const int segs = SEG ? p.seg_items : p.nseg, bh = item / segs, seg = item - bh * segs;
     const int b = bh / p.H, h = bh - b * p.H, hk = h / p.group;
@@ -109,8 +123,16 @@ delta_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
     const Guard g{&S.abort_flag, p.err, p.err_where, p.limit_ns};
 
     if (!Y) griddep_launch_dependents();   // a reverse pass that needs nothing of this launch
+    if (CARE) {
+        griddep_wait();
+        if (p.redo[item] == 0) return;
+    }
+    // the state over the one that kCareful would start from: not before it is known that it need not run
+    const bool in_place = MODE == kForward && p.S_out && p.S_in == p.S_out;
     if (tid == 0) {
         S.abort_flag = 0;
+        S.y_bad = 0;
+        for (int i = 0; i < 4; ++i) S.t_bad[i >> 1][i & 1] = kDC;
         for (int i = 0; i < kStages; ++i) mbar_init(&S.kq_full[i], 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&S.v_full[i], 1);
@@ -127,6 +149,7 @@ delta_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
         mbar_init(&S.e_done, 1);
         mbar_init(&S.s_done, 1);
         mbar_init(&S.e_read, 1);
+        mbar_init(&S.r_ready, 1);
         mbar_init(&S.pu_done, 1);
         mbar_init(&S.o_read, kOut);
         fence_mbar_init();
@@ -247,6 +270,7 @@ delta_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
                 // v of token j: chunk (row / 8) ^ (j % 8) of the token's 128-byte row
                 const uint8_t *tv = sV + (n & 1) * Lay::kV + (row >> 6) * 8192 + half * 32 * 128 + (row & 7) * 2;
                 const uint32_t ch = (uint32_t)(row & 63) >> 3;
+                int first = kDC;
 #pragma unroll 1
                 for (int u = 0; u < 2; ++u) {
                     const int j0 = half * 32 + u * 16;
@@ -267,6 +291,7 @@ delta_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
 #pragma unroll
                     for (int j = 0; j < 16; ++j) c[j] = -c[j];
                     fma16(c, acc, r);
+                    if (CARE) cut16(c, j0, first);
 #pragma unroll
                     for (int i = 0; i < 8; ++i) split3(c[2 * i], c[2 * i + 1], hi[i], mi[i], lo[i]);
                     const uint32_t col = tb + lb + kColR + j0 / 2;
@@ -274,6 +299,7 @@ delta_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
                     tmem_st8(col + 32, mi);
                     tmem_st8(col + 64, lo);
                 }
+                if (CARE) S.first[half][row] = first;
                 tmem_wait_st();
                 tc_fence_before();
             }
@@ -299,6 +325,7 @@ delta_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
                         mma_rows<D / 16, 16384>(leader, tb + kColQS, tb + kColSP + pc * (D / 2), qq, i64, pc < 1);
                     mma_commit_if(leader, &S.qs_done);
                 }
+                if (CARE && leader) mbar_arrive(&S.r_ready);
                 if (leader && n + 2 < nblk) load_v(n + 2);   // every thread has read this block's v
                 __syncwarp();
             }
@@ -314,6 +341,7 @@ delta_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
                     load16(&G.w[j0], w);
                     tmem_wait_ld();
                     mul16(w, acc);
+                    if (CARE && min(S.first[0][row], S.first[1][row]) < kDC) w[0] = nan_f();
 #pragma unroll
                     for (int i = 0; i < 8; ++i) split3(w[2 * i], w[2 * i + 1], hi[i], mi[i], lo[i]);
                     if (Y && u == 0) {   // W takes the place of the state's pieces
@@ -397,6 +425,10 @@ delta_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
             failed = any_failed(!ok);
         }
         if (SAVE && !failed && live && seg == segs - 1) write_state(sck, DV);
+        if (in_place) {
+            named_bar(kBarEnd, kChain + kOut);
+            failed = failed || S.y_bad;
+        }
         if (SEG) {
             if (!failed && live && values)
                 write_state(p.S_local + (size_t)item * D * DV + (size_t)half * SC * DV + col_of, DV);
@@ -500,12 +532,16 @@ delta_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
                 mbar_arrive(&S.kk_read[grp]);
             }
             if (any_out(!ok)) break;   // A complete
-            invert_unit_lower(A, t, bar);
+            int *bad = &S.t_bad[grp][(n >> 1) & 1];
+            // the other turn's has been read before that barrier, and is used again behind several more
+            if (CARE && t == 0) S.t_bad[grp][~(n >> 1) & 1] = kDC;
+            invert_unit_lower<CARE>(A, t, bar, bad);
             // T's pieces over A: a thread's row is in registers before any is written
             float x[kDC];
 #pragma unroll
             for (int j = 0; j < kDC; j += 4)
                 *reinterpret_cast<float4 *>(x + j) = *reinterpret_cast<const float4 *>(A + t * kAP + j);
+            if (CARE && t >= *bad) x[0] = nan_f();   // and with it e_t
             named_bar(bar, kInner);
 #pragma unroll
             for (int q = 0; q < 8; ++q) {
@@ -577,6 +613,7 @@ delta_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
         if (p.stall_ns)
             for (const uint64_t t0 = globaltimer_ns(); globaltimer_ns() - t0 < p.stall_ns;) __nanosleep(1000);
         bool good = true;
+        uint32_t z = 0;   // 0 y: anything else where y is not finite
         if (rows_of_q(0)) {
             good = read_scores(0);
             if (good) make_p(0);
@@ -588,21 +625,32 @@ delta_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
             bool ok = good && (rows_of_q(n) || mbar_wait<1>(&S.g_ready[n & 1], (n >> 1) & 1, g, 31));
             const bool next = n + 1 < nblk && rows_of_q(n + 1);
             if (next) ok = ok && read_scores(n + 1);
+            if (CARE) ok = ok && mbar_wait<1>(&S.r_ready, n & 1, g, 35);
             ok = ok && mbar_wait<1>(&S.e_done, n & 1, g, 32);
             ok = ok && mbar_wait<1>(&S.qs_done, n & 1, g, 33);
             ok = __all_sync(0xffffffffu, ok);
             if (ok && row < DV) {   // e as two pieces, in the place of the state's
                 tc_fence_after();
+                int first = CARE ? min(S.first[0][row], S.first[1][row]) : kDC;
 #pragma unroll 1
                 for (int j0 = 0; j0 < kDC; j0 += 16) {
                     uint32_t acc[16], hi[8], mi[8];
                     tmem_ld16(tb + lb + kColKS + j0, acc);
                     tmem_wait_ld();
+                    if (CARE) {
+                        float x[16];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) x[i] = u2f(acc[i]);
+                        cut16(x, j0, first);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) acc[i] = f2u(x[i]);
+                    }
 #pragma unroll
                     for (int i = 0; i < 8; ++i) split2(u2f(acc[2 * i]), u2f(acc[2 * i + 1]), hi[i], mi[i]);
                     tmem_st8(tb + lb + kColE + j0 / 2, hi);
                     tmem_st8(tb + lb + kColE + j0 / 2 + 32, mi);
                 }
+                if (CARE) S.cut[row] = first;   // read by the same warp, behind a barrier
                 tmem_wait_st();
                 tc_fence_before();
             }
@@ -644,6 +692,16 @@ delta_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
                         o[k] = pack_bf16x2(fmaf(ck.x, u2f(qs[2 * k]), u2f(pe[2 * k])),
                                            fmaf(ck.y, u2f(qs[2 * k + 1]), u2f(pe[2 * k + 1])));
                     }
+                    if (CARE) {
+                        const int *at = &S.cut[wq * 32 + hl * 16 + lane / 4], f[2] = {at[0], at[8]};
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            const int tok = j0 + 8 * (k >> 1) + tq;
+                            o[k] |= (tok >= f[k & 1] ? 0x7FFFu : 0u) | (tok + 1 >= f[k & 1] ? 0x7FFF0000u : 0u);
+                        }
+                    } else {   // what leaks makes a row's P e NaN for every token: two of each row will do
+                        z = fma_bf16x2(o[1], 0u, fma_bf16x2(o[0], 0u, z));
+                    }
                     // matrices (group, row half): lane 8 m + i addresses token i of group m / 2, chunk m % 2
                     const int dv0 = wq * 32 + hl * 16 + ((lane >> 3) & 1) * 8, tok = j0 + (lane >> 4) * 8 + (lane & 7);
                     const uint32_t at = smem_u32(sY) + (dv0 >> 6) * 8192 + sw128_off(tok, dv0 & 63);
@@ -662,6 +720,12 @@ delta_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
             }
             if (next) make_p(n + 1);
         }
+        if (!CARE) {
+            if (z & 0x7FFF7FFFu) S.y_bad = 1;
+            if (in_place) named_bar(kBarEnd, kChain + kOut);
+            else named_bar(kBarOut, kOut);
+            if (tid == kChain + 2 * kInner) p.redo[item] = S.y_bad && !S.abort_flag;
+        }
         if (tid == kChain + 2 * kInner) bulk_wait<0>();
         if (warp == 12 && elect_leader()) {
             mma_commit(&S.drain[3]);
@@ -669,6 +733,7 @@ delta_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
         }
         __syncwarp();
     }
+    if (MODE == kForward) griddep_launch_dependents();   // kCareful: late, for it takes whole SMs
     tc_fence_before();
     __syncthreads();
     if (warp == 0) {
@@ -787,7 +852,7 @@ template <int D, int DV, int MODE> cudaError_t launch_tc(const DeltaArgs &a, Del
     if (!encode_tokens(&qm, a.q, a.layout, a.B, a.Hk, a.N, D) ||
         !encode_tokens(&km, a.k, a.layout, a.B, a.Hk, a.N, D) ||
         !encode_tokens(&vm, a.v, a.layout, a.B, a.H, a.N, DV) ||
-        (MODE == kForward && !encode_tokens(&ym, a.y, a.layout, a.B, a.H, a.N, DV)))
+        (writes_y(MODE) && !encode_tokens(&ym, a.y, a.layout, a.B, a.H, a.N, DV)))
         return cudaErrorInvalidValue;
     auto kern = delta_tc_kernel<D, DV, MODE>;
     constexpr int smem = DeltaLay<D, DV>::request;
@@ -795,7 +860,9 @@ template <int D, int DV, int MODE> cudaError_t launch_tc(const DeltaArgs &a, Del
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     const int ctas = a.B * a.H * (MODE == kSegment ? p.seg_items * p.parts : p.nseg);
-    kern<<<ctas, kChain + 2 * kInner + (MODE == kForward ? kOut : 0), smem, a.stream>>>(qm, km, vm, ym, p);
+    const dim3 block(kChain + 2 * kInner + (writes_y(MODE) ? kOut : 0));
+    if (MODE == kCareful) return launch_overlapped(kern, dim3(ctas), block, smem, a.stream, qm, km, vm, ym, p);
+    kern<<<ctas, block, smem, a.stream>>>(qm, km, vm, ym, p);
     return cudaGetLastError();
 }
 
@@ -820,13 +887,17 @@ template <int D, int DV> DeltaTc tc_params(const DeltaArgs &a) {
     return p;
 }
 
+size_t redo_bytes(const DeltaArgs &a, int nseg) { return ((size_t)a.B * a.H * nseg * 4 + 255) / 256 * 256; }
+
 template <int D, int DV> cudaError_t launch_forward(const DeltaArgs &a) {
     DeltaTc p = tc_params<D, DV>(a);
     delta_segments(a, p.nseg, p.seg_blocks);
+    char *behind = static_cast<char *>(a.ws) + sizeof(WsHeader);
+    p.redo = reinterpret_cast<unsigned int *>(behind);
     if (p.nseg > 1) {
         p.seg_items = p.nseg - 1;
         const size_t items = (size_t)a.B * a.H * p.seg_items;
-        p.S_local = reinterpret_cast<float *>(static_cast<char *>(a.ws) + sizeof(WsHeader));
+        p.S_local = reinterpret_cast<float *>(behind + redo_bytes(a, p.nseg));
         p.Phi = p.S_local + items * D * DV;
         float *P = p.Phi + items * D * D;
         cudaError_t e = launch_tc<D, DV, kSegment>(a, p);
@@ -836,7 +907,8 @@ template <int D, int DV> cudaError_t launch_forward(const DeltaArgs &a) {
         if (e != cudaSuccess) return e;
         p.S_in = P;
     }
-    return launch_tc<D, DV, kForward>(a, p);
+    const cudaError_t e = launch_tc<D, DV, kForward>(a, p);
+    return e == cudaSuccess ? launch_tc<D, DV, kCareful>(a, p) : e;
 }
 
 // e, the states and their gradients at every block (and dS_in).
@@ -872,7 +944,7 @@ template <int D, int DV> cudaError_t launch_passes(const DeltaArgs &a) {
 bool delta_tc_supported(const DeltaArgs &a) {
     return a.dt == LA_DTYPE_BF16 && (a.d == 64 || a.d == 128) && (a.dv == 64 || a.dv == 128);
 }
-// header | (split sequences) the segments' ends and maps, the states at their starts
+// header | items to run again | (split sequences) the segments' ends and maps, the states at their starts
 size_t delta_tc_workspace(const DeltaArgs &a) {
     int nseg, len;
     delta_segments(a, nseg, len);
@@ -881,7 +953,7 @@ size_t delta_tc_workspace(const DeltaArgs &a) {
         const size_t BH = (size_t)a.B * a.H, st = (size_t)a.d * a.dv;
         floats = BH * (nseg - 1) * (st + (size_t)a.d * a.d) + BH * nseg * st;
     }
-    return sizeof(WsHeader) + 4 * floats;
+    return sizeof(WsHeader) + redo_bytes(a, nseg) + 4 * floats;
 }
 size_t delta_tc_split_floats(const DeltaArgs &a) {
     int nseg, len;

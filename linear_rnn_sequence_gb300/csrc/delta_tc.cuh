@@ -12,7 +12,8 @@ namespace {
 constexpr int kDC = kDeltaC;   // tokens of a block
 constexpr int kStages = 3;     // K and Q tiles in flight
 constexpr int kChain = 256, kInner = 64, kOut = 128;   // threads: chain; each T group; P and y
-constexpr int kBarChain = 1, kBarInner = 2;   // kBarInner + 1: the second T group
+constexpr int kBarChain = 1, kBarInner = 2;   // kBarInner + 1: the second T group; + 2: P and y
+constexpr int kBarEnd = kBarInner + 3;
 constexpr int kAP = kDC + 4;   // floats of a row of A: rows four banks apart
 
 struct Gates {   // of one block
@@ -38,10 +39,27 @@ __device__ __forceinline__ void split2(float x0, float x1, uint32_t &h, uint32_t
     f2unpack(f2sub(f2pack(x0, x1), f2pack(bf16_lo_f(h), bf16_hi_f(h))), r0, r1);
     m = pack_bf16x2(r0, r1);
 }
+__device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t c) {
+    uint32_t r;
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+    return r;
+}
 __device__ __forceinline__ uint64_t f2fma(uint64_t a, uint64_t b, uint64_t c) {
     uint64_t r;
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
     return r;
+}
+constexpr float kMost = 3.3895314e38f;   // bf16's largest; what is larger, or no number, counts as not finite
+__device__ __forceinline__ bool finite(float x) { return fabsf(x) <= kMost; }
+__device__ __forceinline__ float nan_f() { return u2f(0x7FFFFFFFu); }
+// Zeroes x from its first value that is not finite on, whose index (x[0]'s: j0) `first` becomes; all of x where
+// an earlier one is known.
+__device__ __forceinline__ void cut16(float (&x)[16], int j0, int &first) {
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+        if (j0 + j < first && !finite(x[j])) first = j0 + j;
+        if (j0 + j >= first) x[j] = 0.f;
+    }
 }
 __device__ __forceinline__ void load16(const float *p, float (&x)[16]) {
 #pragma unroll
@@ -91,8 +109,10 @@ template <bool REV> __device__ __forceinline__ void block_gates(Gates &g, const 
 // kAP), by the 64 threads of a T group: the four diagonal blocks of 16 by forward substitution, a
 // thread for each column, then twice [[T1, 0], [-T2 A21 T1, T2]].  In the second merge a warp has
 // half of the product's columns (with T1 on the right), then half of its rows (with T2 on the left), and
-// leaves out the terms that are zero for all of them.
-template <int SZ> __device__ __forceinline__ void merge_blocks(float *A, int t, int bar) {
+// leaves out the terms that are zero for all of them.  The zeros above T2's diagonal meet rows of A21 T1
+// that come later: with CARE, those that are not finite are zeroed, and *bad becomes the first of them, from
+// which on T is not what it should be.  (What is not finite in T1 or T2 stays in its row and later ones by itself.)
+template <int SZ, bool CARE> __device__ __forceinline__ void merge_blocks(float *A, int t, int bar, int *bad) {
     constexpr int RT = SZ / 8, PER = SZ * SZ / 4 / RT;   // rows of a thread (x 4 columns), threads a pair
     const int pair = t / PER, q = t % PER, half = SZ == 32 ? q >> 5 : 0;
     float *T1 = A + pair * 2 * SZ * (kAP + 1), *A21 = T1 + SZ * kAP, *T2 = A21 + SZ;
@@ -130,13 +150,17 @@ template <int SZ> __device__ __forceinline__ void merge_blocks(float *A, int t, 
             float y[4];
             f2unpack(acc[i][0], y[0], y[1]);
             f2unpack(acc[i][1], y[2], y[3]);
+            if (CARE && step == 0 && !(finite(y[0]) && finite(y[1]) && finite(y[2]) && finite(y[3]))) {
+                atomicMin(bad, pair * 2 * SZ + SZ + r + i * (rs / kAP));
+                y[0] = y[1] = y[2] = y[3] = 0.f;
+            }
             *reinterpret_cast<float4 *>(A21 + r * kAP + i * rs + c) =
                 make_float4(sg * y[0], sg * y[1], sg * y[2], sg * y[3]);
         }
         named_bar(bar, kInner);
     }
 }
-__device__ __forceinline__ void invert_unit_lower(float *A, int t, int bar) {
+template <bool CARE> __device__ __forceinline__ void invert_unit_lower(float *A, int t, int bar, int *bad) {
     float *blk = A + (t >> 4) * 16 * (kAP + 1);
     const int c = t & 15;
     float x[16] = {};
@@ -155,8 +179,8 @@ __device__ __forceinline__ void invert_unit_lower(float *A, int t, int bar) {
 #pragma unroll
     for (int i = 0; i < 16; ++i) blk[i * kAP + c] = x[i];
     named_bar(bar, kInner);
-    merge_blocks<16>(A, t, bar);
-    merge_blocks<32>(A, t, bar);
+    merge_blocks<16, CARE>(A, t, bar, bad);
+    merge_blocks<32, CARE>(A, t, bar, bad);
 }
 
 // x <- a x and x <- a x + b, by pairs.

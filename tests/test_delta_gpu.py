@@ -461,6 +461,48 @@ def test_layer_norm_of_a_scalar_is_refused():
         la.layer_norm_backward(x, x, x, x)
 
 
+@pytest.mark.parametrize("dtype,N", [(BF16, 200), (BF16, 20), (F32, 100)])
+@pytest.mark.parametrize("d,dv", [(64, 64), (128, 128), (64, 128), (128, 64)])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+@pytest.mark.parametrize("what", ["q", "k", "v", "beta", "log_gate"])
+def test_what_is_not_finite_reaches_no_earlier_token(what, value, d, dv, dtype, N):
+    """One such value in one head: y and the state are not finite where the recurrence's are not, and nowhere
+    else; all else keeps its bits (and, where a gate that is no number sends its block down the general path of
+    the gates, its bound)."""
+    for t in (0, 1, 17, 30, 62, 63, 64, 100, 199):
+        if t >= N:
+            break
+        x = R.inputs(1, 3, 3, N, d, dv, dtype, state=t % 2 == 1, seed=t)
+        clean = gpu_forward(x, return_state=True)
+        x[what] = x[what].clone()
+        x[what][(0, 1, t, 5) if what in "qkv" else (0, 1, t)] = value
+        got, want = gpu_forward(x, return_state=True), R.forward(x)
+        for g, w, c in zip(got, want, clean):
+            ok = torch.isfinite(w)
+            assert torch.equal(torch.isfinite(g).cpu(), ok), (t, what)
+            if what != "log_gate":
+                assert torch.equal(g.cpu()[ok], c.cpu()[ok]), (t, what)
+            elif ok.any():
+                R.check(g.cpu()[ok], w[ok], what)
+
+
+@pytest.mark.parametrize("N", [40, 200])
+@pytest.mark.parametrize("d,dv", [(64, 64), (128, 128)])
+@pytest.mark.parametrize("scale", [30.0, 1e4, 1e15, 1e30])
+def test_overflow_reaches_no_earlier_token(scale, d, dv, N):
+    """Keys and values of any size from token t on, as what lies behind a prompt's end may be: the tokens
+    before it keep their bits."""
+    for t in (3, 21, 37, 70, 150):
+        if t >= N:
+            break
+        x = R.inputs(2, 2, 1, N, d, dv, BF16, state=True, seed=t)
+        clean = gpu_forward(x)
+        x["k"][:, :, t:] *= scale
+        x["v"][:, :, t:] *= scale
+        y = gpu_forward(x)
+        assert torch.equal(y[:, :, :t], clean[:, :, :t]), t
+
+
 def test_values_behind_the_inputs_are_not_read():
     """NaN in memory on either side of every input."""
     def guarded(t):
