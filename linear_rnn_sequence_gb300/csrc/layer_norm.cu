@@ -415,11 +415,11 @@ cudaError_t rows_in_flight(const LayerNormArgs &a, bool bwd) {
     return go<T, E, V, G, 1, THR>(a, bwd);
 }
 template <typename T, int E> cudaError_t shape(const LayerNormArgs &a, bool bwd) {
-    const int n = (a.D + E - 1) / E;
-    if (E <= 2) {   // rows that start anywhere: a warp takes up to 512 values
-        if (n <= 16) return rows_in_flight<T, E, 1, 16, 256>(a, bwd);
-        if (n <= 32) return rows_in_flight<T, E, 1, 32, 256>(a, bwd);
-        if (n <= 64) return rows_in_flight<T, E, 2, 32, 256>(a, bwd);
+    const int n = (a.D + E - 1) / E;   // up to 16384 / E
+    if (n <= 16) return rows_in_flight<T, E, 1, 16, 256>(a, bwd);
+    if (n <= 32) return rows_in_flight<T, E, 1, 32, 256>(a, bwd);
+    if (n <= 64) return rows_in_flight<T, E, 2, 32, 256>(a, bwd);
+    if constexpr (E <= 2) {   // rows that start anywhere: a warp takes up to 512 values
         if (n <= 128) return rows_in_flight<T, E, 4, 32, 256>(a, bwd);
         if (n <= 256) return rows_in_flight<T, E, 8, 32, 256>(a, bwd);
         if (E == 1 && n <= 512) return rows_in_flight<T, E, 16 / E, 32, 256>(a, bwd);
@@ -428,15 +428,13 @@ template <typename T, int E> cudaError_t shape(const LayerNormArgs &a, bool bwd)
         if (n <= 4096) return rows_in_flight<T, E, 8, 512, 512>(a, bwd);
         if (n <= 8192) return rows_in_flight<T, E, 8, 1024, 1024>(a, bwd);
         return rows_in_flight<T, E, 16 / E, 1024, 1024>(a, bwd);
+    } else {
+        if (n <= 256) return rows_in_flight<T, E, 1, 256, 256>(a, bwd);
+        if (n <= 512) return rows_in_flight<T, E, 2, 256, 256>(a, bwd);
+        if (n <= 1024) return rows_in_flight<T, E, 2, 512, 512>(a, bwd);
+        if (E == 8 || n <= 2048) return rows_in_flight<T, E, 2, 1024, 1024>(a, bwd);
+        return rows_in_flight<T, E, E == 8 ? 2 : 4, 1024, 1024>(a, bwd);
     }
-    if (n <= 16) return rows_in_flight<T, E, 1, 16, 256>(a, bwd);
-    if (n <= 32) return rows_in_flight<T, E, 1, 32, 256>(a, bwd);
-    if (n <= 64) return rows_in_flight<T, E, 2, 32, 256>(a, bwd);
-    if (n <= 256) return rows_in_flight<T, E, 1, 256, 256>(a, bwd);
-    if (n <= 512) return rows_in_flight<T, E, 2, 256, 256>(a, bwd);
-    if (n <= 1024) return rows_in_flight<T, E, 2, 512, 512>(a, bwd);
-    if (n <= 2048) return rows_in_flight<T, E, 2, 1024, 1024>(a, bwd);
-    return rows_in_flight<T, E, 4, 1024, 1024>(a, bwd);
 }
 
 template <typename T> cudaError_t run(const LayerNormArgs &a, bool bwd) {
