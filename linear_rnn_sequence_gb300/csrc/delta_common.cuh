@@ -33,28 +33,6 @@ template <> __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float
     return __float2bfloat16_rn(x);
 }
 
-// N consecutive values (N * sizeof(T) a multiple of 16, p 16-byte aligned) as floats.
-template <int N> __device__ __forceinline__ void load_vec(const float *p, float (&x)[N]) {
-#pragma unroll
-    for (int i = 0; i < N; i += 4) {
-        const float4 f = __ldg(reinterpret_cast<const float4 *>(p + i));
-        x[i] = f.x; x[i + 1] = f.y; x[i + 2] = f.z; x[i + 3] = f.w;
-    }
-}
-template <int N> __device__ __forceinline__ void load_vec(const __nv_bfloat16 *p, float (&x)[N]) {
-    static_assert(N % 8 == 0, "16-byte vectors");
-#pragma unroll
-    for (int i = 0; i < N; i += 8) {
-        const uint4 w = __ldg(reinterpret_cast<const uint4 *>(p + i));
-        const unsigned u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            x[i + 2 * j] = __uint_as_float(u[j] << 16);
-            x[i + 2 * j + 1] = __uint_as_float(u[j] & 0xFFFF0000u);
-        }
-    }
-}
-
 // A float32 pair h + l, |l| at most half a step of h: sums keep about 46 bits.
 struct F2 {
     float h, l;
