@@ -403,14 +403,16 @@ cudaError_t go(const LayerNormArgs &a, bool backward) {
 }
 
 // The threads of a row, the vectors of a thread and the rows in flight, by the number n of vectors in
-// a row.  Two rows of a group at once, beside the next two on their way, where a thread has one vector
-// of a row (1048576 x 128 bf16: 92 us, 101 without the next ones, 121 with four rows and without);
-// one row where it has more, and for few rows, which want threads rather than rows in flight.
+// a row.  Two rows of a group at once, beside the next two on their way, where a thread has at most eight
+// values of a row, or four of those that go by pairs or one by one (1048576 x 128 bf16: 93 us, 101 without the
+// next ones, 121 with four rows and without; gradients of 16384 x 4096 float32: 134 us, 152 by one row), but not
+// with 1024 threads, whose 64 registers do not hold them (gradients of 13107 x 5120 float32: 184 us, 440 by
+// two); one row where it has more, and for few rows, which want threads rather than rows in flight.
 // Pairs and single values: a warp to a row as far as its registers go, and threads that fit the row beyond
 // (gradients, 61688 x 158 float32: 36 us, 127 with 256 threads a row; 13550 x 2090 bf16: 60 us, 135 by single values).
 template <typename T, int E, int V, int G, int THR>
 cudaError_t rows_in_flight(const LayerNormArgs &a, bool bwd) {
-    constexpr int RW = V * E <= (E > 2 ? 8 : 4) ? 2 : 1;
+    constexpr int RW = V * E <= (E > 2 ? 8 : 4) && THR < 1024 ? 2 : 1;
     if (RW == 1 || a.rows >= 4LL * RW * sm_count() * (THR / G)) return go<T, E, V, G, RW, THR>(a, bwd);
     return go<T, E, V, G, 1, THR>(a, bwd);
 }
