@@ -260,6 +260,15 @@ def test_layer_norm_of_rows_that_start_anywhere(dtype, rows, D):
     test_layer_norm(dtype, rows, D, True)
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("rows,D", [(90011, 64), (90011, 128), (45007, 256), (22511, 512), (7001, 768), (5003, 1024), (7001, 1536),
+                                    (5003, 2048), (4001, 4096), (2003, 5120), (2003, 8192), (1901, 16384)])
+def test_layer_norm_of_many_rows(dtype, rows, D):
+    """Whole vectors, several steps of a CTA in both directions, two rows in flight where the rule has them, and a
+    last step that is not full: sums and rows read ahead have to be those of their own step."""
+    test_layer_norm(dtype, rows, D, True)
+
+
 @pytest.mark.parametrize("offset", [1, 2, 4])
 def test_layer_norm_off_its_vectors(offset):
     """Even widths whose rows start 2, 4 or 8 bytes off: single values or pairs, in x, y, dy and dx alike."""
