@@ -495,6 +495,41 @@ def test_what_is_not_finite_reaches_no_earlier_token(what, value, d, dv, dtype, 
                 R.check(g.cpu()[ok], w[ok], what)
 
 
+@pytest.mark.parametrize("B,H,N,t", [(1, 2, 2500, 1400), (40, 5, 100, 70)])
+@pytest.mark.parametrize("what", ["k", "v"])
+def test_what_is_not_finite_in_long_sequences_and_many_heads(what, B, H, N, t):
+    """The same for sequences split into segments, and for more heads than SMs; with the final state written
+    over the initial one, and replayed from a captured graph."""
+    x = R.inputs(B, H, H, N, 64, 64, BF16, state=True, seed=N)
+    clean = gpu_forward(x, return_state=True)
+    bad = {**x, what: x[what].clone()}
+    bad[what][B - 1, 1, t, 5] = float("nan")
+    bad[what][B - 1, 0, N - 1, 7] = float("inf")
+    want = R.forward(bad)
+
+    def check(got):
+        for g, w, c in zip(got, want, clean):
+            ok = torch.isfinite(w)
+            assert not ok.all() and torch.equal(torch.isfinite(g).cpu(), ok)
+            assert torch.equal(g.cpu()[ok], c.cpu()[ok])
+
+    check(gpu_forward(bad, return_state=True))
+    xg = on_gpu(bad)
+    y, _ = la.forward_delta(**xg, S_out=xg["S_in"], return_state=True)
+    check((y, xg["S_in"]))
+    xg = on_gpu(x)
+    la.forward_delta(**xg)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = la.forward_delta(**xg, return_state=True)
+    xg[what].copy_(bad[what])
+    graph.replay()
+    check(got)
+    xg[what].copy_(x[what])
+    graph.replay()
+    assert all(torch.equal(g, c) for g, c in zip(got, clean))
+
+
 @pytest.mark.parametrize("N", [40, 200])
 @pytest.mark.parametrize("d,dv", [(64, 64), (128, 128)])
 @pytest.mark.parametrize("scale", [30.0, 1e4, 1e15, 1e30])
