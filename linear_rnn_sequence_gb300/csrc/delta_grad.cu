@@ -17,7 +17,7 @@
 // in registers and writes dq and dk once.  512 threads, a warp for each 4 tokens
 // (its factors of the products are broadcasts), lanes along the features: bound
 // by the latency of the staged slices, which 16 warps cover better than 8
-// (B8 H16 N512 d64 float32: 473 us for the gradients, 568 with 256 threads).  The
+// (B8 H16 N512 d64 float32: 473 us for the gradients, 568 with 256 threads; at d = 128 up to 152 bytes a thread spill).  The
 // gates' sums run as float32 pairs in one warp: 64-bit additions by one thread
 // were a quarter of the kernel's time.
 #include "delta_common.cuh"

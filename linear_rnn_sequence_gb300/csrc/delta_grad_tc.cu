@@ -10,9 +10,10 @@
 //     F_ij = F_ji = -b_i D_ij b_j (du_i . e_j)  (j < i),
 // the scores dy_i . e_j and du_i . e_j as one product of the stacked rows
 // [dy; du].  dq and its scores are computed to float32 (three pieces of each
-// float32 operand, see delta_tc.cu): the gates' gradient is a difference of
-// q . dq and v . dv.  What only dk depends on, which is rounded to bf16, takes
-// two pieces (2^-16).
+// float32 operand, see delta_tc.cu), and so is G e^T: the gates' gradient is a difference of
+// q . dq and v . dv, and <G, S'>.  What only dk depends on, which is rounded to bf16, takes
+// two pieces: du and F rounded to nearest (at most 2^-17 is left), S and P^T the top two of their
+// three (less than 2^-15, always of their sign); du's middle by e's middle and low pieces are dropped (2^-15).
 //
 // <G, S'> of the gates' gradient, S' the state behind the block, takes no other
 // read: S' = c_C S + K^T W, so it is c_C <G, S> + sum_j w_j (G e)_j . k_j.

@@ -249,8 +249,8 @@ delta_rev_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
                 const uint32_t leader = elect_leader();
                 tc_fence_after();
                 const uint32_t t = smem_u32(sT) + (n & 1) * Lay::kT;
-                // the pieces (of the right-hand side, of T^T) whose product is above 2^-24 of the
-                // whole, small ones first: (2, 0) (0, 2) (1, 1) (1, 0) (0, 1) (0, 0)
+                // the pieces (of the right-hand side, of T^T) but those whose product is below 2^-22 of
+                // the whole, small ones first: (2, 0) (0, 2) (1, 1) (1, 0) (0, 1) (0, 0)
 #pragma unroll 1
                 for (int o = 0; o < 6; ++o) {
                     const int pr = (0x201100u >> (20 - 4 * o)) & 3, pt = (0x021010u >> (20 - 4 * o)) & 3;

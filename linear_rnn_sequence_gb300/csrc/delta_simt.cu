@@ -328,8 +328,8 @@ cudaError_t launch_d(const DeltaArgs &a, int what) {
     }
     if (what == 0) delta_forward_kernel<D, T, false><<<grid, kThr, 0, a.stream>>>(p);
     if (what == 1) delta_forward_kernel<D, T, true><<<grid, kThr, 0, a.stream>>>(p);
-    // Beside the states' pass where both fit the SMs, one CTA each (B2 H4 N777 d64, 32 CTAs: 184 us for the
-    // gradients, 266 one after the other).  Where they share SMs the second pass's CTAs crowd on the
+    // Beside the states' pass where both fit the SMs, one CTA each (B2 H4 N777 d64, 32 CTAs: 156 us for the
+    // gradients, 237 one after the other).  Where they share SMs the second pass's CTAs crowd on the
     // emptier ones: 128 CTAs of d = 128, 2048 tokens: 1516 us, 1080 one after the other.
     if (what == 2 && 2 * (long long)grid.x * grid.y <= num_sms())
         return launch_overlapped(delta_reverse_kernel<D, T>, grid, dim3(kThr), 0, a.stream, p);

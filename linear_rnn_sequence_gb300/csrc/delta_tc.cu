@@ -15,11 +15,14 @@
 //
 // Precision: states, e and T are float32 values.  A float32 operand enters
 // the MMAs as three bf16 pieces that add up to it exactly (the top, middle and
-// low 8 bits of its significand, by truncation), so K S and K^T W, whose other
+// low 8 bits of its significand, by truncation: the middle one is below 2^-7
+// of it, the low one below 2^-15), so K S and K^T W, whose other
 // operand is the bf16 input itself, lose nothing but the accumulator's
-// float32 rounding, and T r drops only the products of pieces below 2^-24.
-// What only y depends on, which is rounded to bf16 anyway, takes two pieces
-// (2^-16): Q S and P e.
+// float32 rounding, and T r drops the middle by low products, each below 2^-22
+// of its term and of its sign (2^-24.7 of it on average).
+// What only y depends on, which is rounded to bf16 anyway, takes two pieces:
+// of the state in Q S the top two (less than 2^-15 is left, always of its sign), of P and
+// e in P e two rounded to nearest (2^-17 is left of each, at most).
 //
 // Roles (16 warps): warps 0-7 carry the chain (two threads a row, each half of
 // the columns; the float32 state lives in their registers); warps 8 and 9 turn
@@ -27,7 +30,7 @@
 // ahead of the chain; warps 12-15 turn Q K^T into P (two of them), make P e and
 // write y.
 // Bound by the chain of a block, about 9 K cycles of which the tensor pipe is
-// busy a third: B8 H16 N8192 d128 0.61 ms, 1.8 TB/s; B1 H32 N131072 d64, split
+// busy a third: B8 H16 N8192 d128 0.62 ms, 1.8 TB/s; B1 H32 N131072 d64, split
 // in four, 3.5 ms.
 // What is not finite must reach no token before its own, but the MMAs run over whole blocks, in which the
 // zeros above the diagonals of T and P meet later tokens' r and e.  So the kernel notes a row of y that is not
@@ -309,7 +312,7 @@ delta_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
                 const uint32_t leader = elect_leader();
                 tc_fence_after();
                 const uint32_t t = smem_u32(sT) + (n & 1) * Lay::kT;
-                // the pieces (r, T) whose product is above 2^-24 of the whole, small ones first:
+                // the pieces (r, T) but those whose product is below 2^-22 of the whole, small ones first:
                 // (2, 0) (0, 2) (1, 1) (1, 0) (0, 1) (0, 0)
 #pragma unroll 1
                 for (int o = 0; o < 6; ++o) {

@@ -32,7 +32,7 @@ __device__ __forceinline__ void split3(float x0, float x1, uint32_t &h, uint32_t
     f2unpack(f2sub(f2pack(r0, r1), f2pack(u2f(b0 & 0xFFFF0000u), u2f(b1 & 0xFFFF0000u))), r0, r1);
     l = __byte_perm(f2u(r0), f2u(r1), 0x7632);
 }
-// Two pieces, each rounded to nearest: 2^-18 of x is left.
+// Two pieces, each rounded to nearest: at most 2^-17 of x is left.
 __device__ __forceinline__ void split2(float x0, float x1, uint32_t &h, uint32_t &m) {
     h = pack_bf16x2(x0, x1);
     float r0, r1;
