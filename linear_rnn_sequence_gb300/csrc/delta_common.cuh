@@ -33,15 +33,16 @@ template <> __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float
     return __float2bfloat16_rn(x);
 }
 
-// A float32 pair h + l, |l| at most half a step of h: sums keep about 46 bits.
+// A float32 pair h + l, |l| at most half a step of h: sums keep about 46 bits.  The _rn forms are not
+// contracted: where h is a product, a fused multiply-add would bring its low part in a second time.
 struct F2 {
     float h, l;
 };
 __device__ __forceinline__ F2 f2sum2(F2 a, F2 b) {
-    const float s = a.h + b.h, t = s - a.h;
-    const float l = ((a.h - (s - t)) + (b.h - t)) + (a.l + b.l);
-    const float h = s + l;
-    return {h, l - (h - s)};
+    const float s = __fadd_rn(a.h, b.h), t = __fsub_rn(s, a.h);
+    const float l = __fadd_rn(__fadd_rn(__fsub_rn(a.h, __fsub_rn(s, t)), __fsub_rn(b.h, t)), __fadd_rn(a.l, b.l));
+    const float h = __fadd_rn(s, l);
+    return {h, __fsub_rn(l, __fsub_rn(h, s))};
 }
 
 // Workspace of the gradients, in floats behind the status header: the states before each block and

@@ -75,7 +75,7 @@ template <bool REV> __device__ __forceinline__ void block_gates(Gates &g, const 
     F2 x[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {   // 2^-14427 is 0; keeps -inf out
-        const float v = lg[i] < -1e4f ? -1e4f : lg[i], h = v * kL;
+        const float v = lg[i] < -1e4f ? -1e4f : lg[i], h = __fmul_rn(v, kL);
         x[i] = {h, fmaf(v, kL, -h) + v * kLl};
     }
     x[1] = f2sum2(x[0], x[1]);

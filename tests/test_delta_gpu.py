@@ -81,6 +81,21 @@ def test_gates_and_shared_heads(gate, group, dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("group", [1, 2])
+@pytest.mark.parametrize("d,dv", [(64, 64), (128, 128), (64, 128), (128, 64)])
+@pytest.mark.parametrize("gate", [-9999.0, -1234.5, -60.0, -float("inf")])
+def test_gates_that_all_but_close(gate, d, dv, group, dtype):
+    """Among open gates a few that close as good as wholly: differences of running sums of logarithms that are
+    thousands apart, whose last places still are the open gates."""
+    for seed, N in ((0, 64), (2, 150)):
+        x = R.inputs(1, 4, 4 // group, N, d, dv, dtype, state=seed == 0, seed=seed)
+        g = torch.Generator().manual_seed(seed + 1)
+        x["log_gate"][torch.rand(1, 4, N, generator=g) < 0.05] = gate
+        check_forward(x)
+        check_backward(x, dtype)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
 def test_equal_keys_and_full_writes(dtype):
     # the same key again and again with b = 1: the hardest inverse of a block
     x = R.inputs(1, 2, 2, 140, 64, 64, dtype, gate=None, state=True, seed=4)
