@@ -421,9 +421,9 @@ LA_API la_status la_noalloc_status(void *stream);
 /*
  * Workspace size in bytes for la_forward_delta with these sizes: 0 where the
  * call needs none, and for unsupported arguments.  It holds the run-time
- * status header, a word for each head and segment and, when few heads make the
- * call split the sequence into segments, the segments' states and maps of the
- * state, so it depends on the current device's SM count.
+ * status header and, when few heads make the call split the sequence into
+ * segments, the segments' states and maps of the state, so it depends on the
+ * current device's SM count.
  */
 LA_API size_t la_delta_workspace_bytes(int B, int H, int Hk, int N, int d, int dv, la_dtype dt);
 

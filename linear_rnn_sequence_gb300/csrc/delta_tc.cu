@@ -34,10 +34,10 @@
 // in four, 3.5 ms.
 // What is not finite must reach no token before its own, but the MMAs run over whole blocks, in which the
 // zeros above the diagonals of T and P meet later tokens' r and e.  So the kernel notes a row of y that is not
-// finite, and items with one run again, by a second launch whose other
-// CTAs end at once: there a thread leaves out what follows the first value of its row of r or e that is not
-// finite, and y and the state become NaN from there on.  (Those checks in every run took 8 to 10% of its time;
-// the note and the second launch take 1 us of a short call, and of B8 H16 N8192 d128 609 -> 616 us.)
+// finite, and a CTA with one runs again, with CARE: there a thread leaves out what follows the first value of
+// its row of r or e that is not finite, and y and the state become NaN from there on.  (Those checks in every
+// run took 8 to 10% of its time, the loops' code being as large as the instruction cache; a second launch for
+// the second run took 4 us of the host's time a call; this takes 1% of B8 H16 N8192 d128, 609 -> 617 us.)
 // The rows of [K; Q] K^T are TMEM lanes, which a warp reaches by its number
 // mod 4: so odd blocks hold Q before K.  The chain's first warp issues its
 // MMAs and the TMA loads.
@@ -64,7 +64,6 @@ struct DeltaTc {
     float *S_out;                  // by head
     float *S_ck, *e;               // kSave
     float *S_local, *Phi;          // kSegment, by (head, its segment)
-    unsigned int *redo;            // by (head, segment): y is not finite, kCareful has to run
     unsigned int *err, *err_where;
     unsigned long long limit_ns, stall_ns;   // stall_ns, drop_item: test hooks
     int drop_item;
@@ -73,10 +72,10 @@ struct DeltaTc {
 struct DeltaSmall {
     Gates gates[4];
     uint64_t kq_full[kStages], v_full[2], kk_full, kk_read[2], g_ready[2], t_ready[2], t_free[2], p_ready, ks_done, qs_done, e_done, s_done, e_read, r_ready, pu_done, o_read, drain[4];
-    int first[2][128];   // kCareful, by half of the tokens and row of r: its first value that is not finite, or kDC
-    int cut[128];        // kCareful, by row of y: the first that is not finite, where the warp has one
-    int t_bad[2][2];     // kCareful, by T group and turn: the first row of T that is not what it should be, or kDC
-    int y_bad;
+    int first[2][128];   // CARE, by half of the tokens and row of r: its first value that is not finite, or kDC
+    int cut[128];        // CARE, by row of y: the first that is not finite, where the warp has one
+    int t_bad[2][2];     // CARE, by T group and turn: the first row of T that is not what it should be, or kDC
+    int y_bad;           // y is not finite somewhere
     uint32_t tmem_base;
     volatile int abort_flag;
 };
@@ -94,80 +93,62 @@ template <int D, int DV> struct DeltaLay {
 // What a launch computes.
 enum DeltaMode {
     kForward,   // y, from the initial state of each (head, segment)
-    kCareful,   // the same for those whose y is not finite
     kSave,      // the backward's first pass: e, and the state before every block and after the last
     kSegment    // segments from an empty state (rows < dv), and the segments' maps of the state:
                 // S_end = Phi S_start + S_local, row dv + a being column a of Phi (from a unit state,
                 // without values); `parts` CTAs of 128 rows each
 };
 
-constexpr bool writes_y(int mode) { return mode == kForward || mode == kCareful; }
+template <bool Y> __device__ __forceinline__ void init_barriers(DeltaSmall &S) {
+    for (int i = 0; i < kStages; ++i) mbar_init(&S.kq_full[i], 1);
+    for (int i = 0; i < 2; ++i) {
+        mbar_init(&S.v_full[i], 1);
+        mbar_init(&S.t_ready[i], kInner);
+        mbar_init(&S.g_ready[i], 32);
+        mbar_init(&S.t_free[i], 1);
+        mbar_init(&S.kk_read[i], Y ? 2 * kInner : kInner);   // a thread for each row of K, and of Q
+    }
+    for (int i = 0; i < 4; ++i) mbar_init(&S.drain[i], 1);
+    mbar_init(&S.kk_full, 1);
+    mbar_init(&S.p_ready, 64);
+    mbar_init(&S.ks_done, 1);
+    mbar_init(&S.qs_done, 1);
+    mbar_init(&S.e_done, 1);
+    mbar_init(&S.s_done, 1);
+    mbar_init(&S.e_read, 1);
+    mbar_init(&S.r_ready, 1);
+    mbar_init(&S.pu_done, 1);
+    mbar_init(&S.o_read, kOut);
+    fence_mbar_init();
+}
 
-// Only kForward and kCareful launch warps 12-15.
-template <int D, int DV, int MODE>
-__global__ void __launch_bounds__(kChain + 2 * kInner + (writes_y(MODE) ? kOut : 0), 1)
-delta_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
-                const __grid_constant__ CUtensorMap vmap, const __grid_constant__ CUtensorMap ymap,
-                const DeltaTc p) {
-    using Lay = DeltaLay<D, DV>;
+// The launch's shared memory, aligned by an offset, so that the compiler still sees shared memory.
+__device__ __forceinline__ uint8_t *aligned_smem() {
     extern __shared__ uint8_t smem_raw[];
-    // aligned by an offset, so that the compiler still sees shared memory
-    uint8_t *sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    return smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+}
+
+// One run over an item: what each warp does.
+template <int D, int DV, int MODE, bool CARE>
+__device__ __forceinline__ void delta_run(const CUtensorMap &qmap, const CUtensorMap &kmap, const CUtensorMap &vmap,
+                                          const CUtensorMap &ymap, const DeltaTc &p) {
+    using Lay = DeltaLay<D, DV>;
+    uint8_t *sm = aligned_smem();
     DeltaSmall &S = *reinterpret_cast<DeltaSmall *>(sm + Lay::oSmall);
+    const uint32_t tb = __shfl_sync(0xffffffffu, S.tmem_base, 0);
     uint8_t *sKQ = sm + Lay::oKQ, *sV = sm + Lay::oV, *sT = sm + Lay::oT, *sP = sm + Lay::oP,
             *sY = sm + Lay::oY;
     // warp-uniform to the compiler too
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
-    constexpr bool Y = writes_y(MODE), CARE = MODE == kCareful, SAVE = MODE == kSave, SEG = MODE == kSegment;
+    constexpr bool Y = MODE == kForward, SAVE = MODE == kSave, SEG = MODE == kSegment;
     const int part = SEG ? blockIdx.x % p.parts : 0, item = SEG ? blockIdx.x / p.parts : blockIdx.x;
     const int segs = SEG ? p.seg_items : p.nseg, bh = item / segs, seg = item - bh * segs;
     const int b = bh / p.H, h = bh - b * p.H, hk = h / p.group;
     const int blk0 = seg * p.seg_blocks, nblk = min(p.seg_blocks, p.nblk - blk0);   // blocks of this item
     const Guard g{&S.abort_flag, p.err, p.err_where, p.limit_ns};
 
-    if (!Y) griddep_launch_dependents();   // a reverse pass that needs nothing of this launch
-    if (CARE) {
-        griddep_wait();
-        if (p.redo[item] == 0) return;
-    }
-    // the state over the one that kCareful would start from: not before it is known that it need not run
-    const bool in_place = MODE == kForward && p.S_out && p.S_in == p.S_out;
-    if (tid == 0) {
-        S.abort_flag = 0;
-        S.y_bad = 0;
-        for (int i = 0; i < 4; ++i) S.t_bad[i >> 1][i & 1] = kDC;
-        for (int i = 0; i < kStages; ++i) mbar_init(&S.kq_full[i], 1);
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&S.v_full[i], 1);
-            mbar_init(&S.t_ready[i], kInner);
-            mbar_init(&S.g_ready[i], 32);
-            mbar_init(&S.t_free[i], 1);
-            mbar_init(&S.kk_read[i], Y ? 2 * kInner : kInner);   // a thread for each row of K, and of Q
-        }
-        for (int i = 0; i < 4; ++i) mbar_init(&S.drain[i], 1);
-        mbar_init(&S.kk_full, 1);
-        mbar_init(&S.p_ready, 64);
-        mbar_init(&S.ks_done, 1);
-        mbar_init(&S.qs_done, 1);
-        mbar_init(&S.e_done, 1);
-        mbar_init(&S.s_done, 1);
-        mbar_init(&S.e_read, 1);
-        mbar_init(&S.r_ready, 1);
-        mbar_init(&S.pu_done, 1);
-        mbar_init(&S.o_read, kOut);
-        fence_mbar_init();
-        prefetch_tmap(&kmap);
-        prefetch_tmap(&vmap);
-        if (Y) prefetch_tmap(&qmap);
-    }
-    if (warp == 0) {
-        tmem_alloc(&S.tmem_base, 512);
-        tmem_relinquish();
-    }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tb = __shfl_sync(0xffffffffu, S.tmem_base, 0);
+    // the state over the one that a second run starts from: not before it is known that there is none
+    const bool in_place = Y && !CARE && p.S_out && p.S_in == p.S_out;
     const int wq = warp & 3, row = wq * 32 + lane;
     const uint32_t lb = (uint32_t)(wq * 32) << 16;
     constexpr uint32_t i64 = idesc_bf16(128, kDC, 0, 0);
@@ -726,8 +707,6 @@ delta_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
         if (!CARE) {
             if (z & 0x7FFF7FFFu) S.y_bad = 1;
             if (in_place) named_bar(kBarEnd, kChain + kOut);
-            else named_bar(kBarOut, kOut);
-            if (tid == kChain + 2 * kInner) p.redo[item] = S.y_bad && !S.abort_flag;
         }
         if (tid == kChain + 2 * kInner) bulk_wait<0>();
         if (warp == 12 && elect_leader()) {
@@ -736,12 +715,51 @@ delta_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
         }
         __syncwarp();
     }
-    if (MODE == kForward) griddep_launch_dependents();   // kCareful: late, for it takes whole SMs
+}
+
+// Only kForward launches warps 12-15.
+template <int D, int DV, int MODE>
+__global__ void __launch_bounds__(kChain + 2 * kInner + (MODE == kForward ? kOut : 0), 1)
+delta_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
+                const __grid_constant__ CUtensorMap vmap, const __grid_constant__ CUtensorMap ymap,
+                const DeltaTc p) {
+    constexpr bool Y = MODE == kForward;
+    DeltaSmall &S = *reinterpret_cast<DeltaSmall *>(aligned_smem() + DeltaLay<D, DV>::oSmall);
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+    if (!Y) griddep_launch_dependents();   // a reverse pass that needs nothing of this launch
+    if (tid == 0) {
+        S.abort_flag = 0;
+        S.y_bad = 0;
+        init_barriers<Y>(S);
+        prefetch_tmap(&kmap);
+        prefetch_tmap(&vmap);
+        if (Y) prefetch_tmap(&qmap);
+    }
+    if (warp == 0) {
+        tmem_alloc(&S.tmem_base, 512);
+        tmem_relinquish();
+    }
     tc_fence_before();
     __syncthreads();
+    tc_fence_after();
+    delta_run<D, DV, MODE, false>(qmap, kmap, vmap, ymap, p);
+    tc_fence_before();
+    __syncthreads();
+    if (Y && S.y_bad && !S.abort_flag) {   // nothing is in flight: every copy and MMA has been waited for
+        if (tid == 0) {
+            for (uint64_t *b = S.kq_full; b <= &S.drain[3]; ++b) mbar_inval(b);
+            init_barriers<Y>(S);
+            for (int i = 0; i < 4; ++i) S.t_bad[i >> 1][i & 1] = kDC;
+        }
+        __syncthreads();
+        tc_fence_after();
+        delta_run<D, DV, MODE, true>(qmap, kmap, vmap, ymap, p);   // in line: a call's registers cost 7%
+        tc_fence_before();
+        __syncthreads();
+    }
     if (warp == 0) {
         tc_fence_after();
-        tmem_dealloc(tb, 512);
+        tmem_dealloc(S.tmem_base, 512);
     }
 }
 
@@ -855,7 +873,7 @@ template <int D, int DV, int MODE> cudaError_t launch_tc(const DeltaArgs &a, Del
     if (!encode_tokens(&qm, a.q, a.layout, a.B, a.Hk, a.N, D) ||
         !encode_tokens(&km, a.k, a.layout, a.B, a.Hk, a.N, D) ||
         !encode_tokens(&vm, a.v, a.layout, a.B, a.H, a.N, DV) ||
-        (writes_y(MODE) && !encode_tokens(&ym, a.y, a.layout, a.B, a.H, a.N, DV)))
+        (MODE == kForward && !encode_tokens(&ym, a.y, a.layout, a.B, a.H, a.N, DV)))
         return cudaErrorInvalidValue;
     auto kern = delta_tc_kernel<D, DV, MODE>;
     constexpr int smem = DeltaLay<D, DV>::request;
@@ -863,9 +881,7 @@ template <int D, int DV, int MODE> cudaError_t launch_tc(const DeltaArgs &a, Del
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     const int ctas = a.B * a.H * (MODE == kSegment ? p.seg_items * p.parts : p.nseg);
-    const dim3 block(kChain + 2 * kInner + (writes_y(MODE) ? kOut : 0));
-    if (MODE == kCareful) return launch_overlapped(kern, dim3(ctas), block, smem, a.stream, qm, km, vm, ym, p);
-    kern<<<ctas, block, smem, a.stream>>>(qm, km, vm, ym, p);
+    kern<<<ctas, kChain + 2 * kInner + (MODE == kForward ? kOut : 0), smem, a.stream>>>(qm, km, vm, ym, p);
     return cudaGetLastError();
 }
 
@@ -890,17 +906,13 @@ template <int D, int DV> DeltaTc tc_params(const DeltaArgs &a) {
     return p;
 }
 
-size_t redo_bytes(const DeltaArgs &a, int nseg) { return ((size_t)a.B * a.H * nseg * 4 + 255) / 256 * 256; }
-
 template <int D, int DV> cudaError_t launch_forward(const DeltaArgs &a) {
     DeltaTc p = tc_params<D, DV>(a);
     delta_segments(a, p.nseg, p.seg_blocks);
-    char *behind = static_cast<char *>(a.ws) + sizeof(WsHeader);
-    p.redo = reinterpret_cast<unsigned int *>(behind);
     if (p.nseg > 1) {
         p.seg_items = p.nseg - 1;
         const size_t items = (size_t)a.B * a.H * p.seg_items;
-        p.S_local = reinterpret_cast<float *>(behind + redo_bytes(a, p.nseg));
+        p.S_local = reinterpret_cast<float *>(static_cast<char *>(a.ws) + sizeof(WsHeader));
         p.Phi = p.S_local + items * D * DV;
         float *P = p.Phi + items * D * D;
         cudaError_t e = launch_tc<D, DV, kSegment>(a, p);
@@ -910,8 +922,7 @@ template <int D, int DV> cudaError_t launch_forward(const DeltaArgs &a) {
         if (e != cudaSuccess) return e;
         p.S_in = P;
     }
-    const cudaError_t e = launch_tc<D, DV, kForward>(a, p);
-    return e == cudaSuccess ? launch_tc<D, DV, kCareful>(a, p) : e;
+    return launch_tc<D, DV, kForward>(a, p);
 }
 
 // e, the states and their gradients at every block (and dS_in).
@@ -947,7 +958,7 @@ template <int D, int DV> cudaError_t launch_passes(const DeltaArgs &a) {
 bool delta_tc_supported(const DeltaArgs &a) {
     return a.dt == LA_DTYPE_BF16 && (a.d == 64 || a.d == 128) && (a.dv == 64 || a.dv == 128);
 }
-// header | items to run again | (split sequences) the segments' ends and maps, the states at their starts
+// header | (split sequences) the segments' ends and maps, the states at their starts
 size_t delta_tc_workspace(const DeltaArgs &a) {
     int nseg, len;
     delta_segments(a, nseg, len);
@@ -956,7 +967,7 @@ size_t delta_tc_workspace(const DeltaArgs &a) {
         const size_t BH = (size_t)a.B * a.H, st = (size_t)a.d * a.dv;
         floats = BH * (nseg - 1) * (st + (size_t)a.d * a.d) + BH * nseg * st;
     }
-    return sizeof(WsHeader) + redo_bytes(a, nseg) + 4 * floats;
+    return sizeof(WsHeader) + 4 * floats;
 }
 size_t delta_tc_split_floats(const DeltaArgs &a) {
     int nseg, len;
