@@ -89,6 +89,19 @@ typedef enum {
     LA_LAYOUT_BNHD = 1        /* [B][N][heads][width]: heads inside tokens     */
 } la_layout;
 
+/* The norm of la_norm_rotate. */
+typedef enum {
+    LA_NORM_NONE = 0,
+    LA_NORM_RMS = 1,          /* x / sqrt(mean(x^2) + eps)                     */
+    LA_NORM_L2 = 2            /* x / sqrt(sum(x^2) + eps): unit length         */
+} la_norm;
+
+/* Which of a head's values la_norm_rotate turns together. */
+typedef enum {
+    LA_PAIRS_HALVES = 0,      /* values e and e + pairs                        */
+    LA_PAIRS_ADJACENT = 1     /* values 2 e and 2 e + 1                        */
+} la_pairs;
+
 /* Human-readable name of a status code (static string, never NULL). */
 LA_API const char *la_status_string(la_status s);
 
@@ -545,6 +558,65 @@ LA_API la_status la_layer_norm_backward(const void *dy, const void *x, const flo
                                         float *grad_weight, float *grad_bias, long long rows, int D,
                                         la_dtype dt, void *workspace, size_t workspace_bytes,
                                         void *stream);
+
+/*
+ * Queries and keys normed by head, weighted and rotated by position, in one
+ * pass: what stands between a layer's projections and the sequence calls above
+ * (the pages have no counterpart; the delta rule asks for keys of unit length).
+ * With c = 1/d (LA_NORM_RMS) or 1 (LA_NORM_L2), for each row x of d values:
+ *     u = x s * weight,   s = 1 / sqrt(c sum(x^2) + eps)   (LA_NORM_NONE: s = 1),
+ *     (u_a, u_b) <- (u_a cos f - u_b sin f, u_b cos f + u_a sin f),  f = position * freq[e],
+ * for the `rotated` pairs (a, b) of `pairs`: (e, e + rotated) or (2 e, 2 e + 1), e < rotated;
+ * the values behind the first 2 rotated are not turned.
+ *   q, k       dtype dt, Hq and Hk heads of width d; q_out, k_out alike, rounded once to dt.
+ *   strides    NULL: all four contiguous in `layout` ([B][heads][N][d] or [B][N][heads][d]).
+ *              Otherwise HOST array of 12: the strides in elements from one batch row, head and
+ *              token to the next, of q, k, q_out and k_out (a row's values are contiguous), so that
+ *              q and k may be parts of a projection's whole output.  No negative ones; rows of an
+ *              output must not overlap each other.
+ *   weights    float32 [d], each may be NULL (ones).
+ *   freq       float64 [rotated], radians a position; NULL with rotated = 0.  Angles are formed as
+ *              fractions of a turn in 64-bit integers: far positions lose nothing.  A frequency that
+ *              is not finite, or of 2^64 and more, makes what it turns NaN.
+ *   positions  int64, of batch row b and token t at positions[b positions_stride + t]; NULL: t.
+ * 2 <= d <= 256, even (else LA_ERR_UNSUPPORTED); 0 <= 2 rotated <= d; B, Hq, Hk >= 1,
+ * Hq + Hk < 65536; N >= 0; B*N < 2^31; eps finite and > 0 (not read without a norm).  Pointers to q,
+ * k and the outputs aligned to their element size (16 bytes, and strides and sizes to match, are
+ * faster), weights to 4, freq and positions to 8 bytes.  q_out may be q and k_out may be k, with the
+ * same strides; no other output may overlap an input or output.  The sums are float32.
+ * A single token of each sequence: N = 1.
+ */
+LA_API la_status la_norm_rotate(const void *q, const void *k, void *q_out, void *k_out,
+                                const long long *strides, int B, int Hq, int Hk, int N, int d,
+                                la_dtype dt, la_layout layout, la_norm norm, float eps,
+                                const float *q_weight, const float *k_weight, const double *freq,
+                                int rotated, la_pairs pairs, const long long *positions,
+                                long long positions_stride, void *stream);
+
+/* Workspace size in bytes for la_norm_rotate_backward (0 for unsupported arguments): per-CTA
+ * sums of the weights' gradients; it depends on the current device's SM count. */
+LA_API size_t la_norm_rotate_backward_workspace_bytes(int B, int Hq, int Hk, int N, int d,
+                                                      la_dtype dt);
+
+/*
+ * Gradients of la_norm_rotate for gq_out = dL/dq_out and gk_out = dL/dk_out: with g the gradient
+ * turned back, xh = x s,
+ *     grad_x = s (g * weight - c xh sum(g * weight * xh)),   grad_weight = sum over rows of g xh.
+ * strides: NULL, or HOST array of 18: of q, k, gq_out, gk_out, grad_q and grad_k.  grad_q may be q
+ * or gq_out and grad_k may be k or gk_out, with the same strides.  grad_q_weight, grad_k_weight:
+ * float32 [d], each may be NULL; rows are summed in a fixed order (the result does not vary between
+ * runs on one device).  The workspace (256-byte aligned) may be NULL when neither is asked for.  The
+ * rest as in la_norm_rotate.
+ */
+LA_API la_status la_norm_rotate_backward(const void *q, const void *k, const void *gq_out,
+                                         const void *gk_out, void *grad_q, void *grad_k,
+                                         const long long *strides, int B, int Hq, int Hk, int N, int d,
+                                         la_dtype dt, la_layout layout, la_norm norm, float eps,
+                                         const float *q_weight, const float *k_weight,
+                                         const double *freq, int rotated, la_pairs pairs,
+                                         const long long *positions, long long positions_stride,
+                                         float *grad_q_weight, float *grad_k_weight, void *workspace,
+                                         size_t workspace_bytes, void *stream);
 
 /*
  * Synchronise `stream` and report the run-time status recorded in a

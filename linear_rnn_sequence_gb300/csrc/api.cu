@@ -721,6 +721,224 @@ la_status la_layer_norm_backward(const void *dy, const void *x, const float *mea
     return from_cuda(launch_layer_norm_backward(a));
 }
 
+}  // extern "C"
+
+namespace la {
+namespace {
+
+// Rows of d elements at p + b st[0] + h st[1] + t st[2].
+struct Rows {
+    HeadsView v;
+    long long n[3];   // batch rows, heads, tokens
+    int d, es;
+    long long st(int i) const { return i == 0 ? v.b : i == 1 ? v.h : v.t; }
+    long long extent() const {   // elements from the first to the end of the last
+        long long e = d;
+        for (int i = 0; i < 3; ++i) e += (n[i] - 1) * st(i);
+        return e;
+    }
+};
+
+HeadsView heads_view(const void *p, const long long *st, la_layout layout, int heads, int N, int d) {
+    HeadsView v{const_cast<void *>(p), 0, 0, 0};
+    if (st) {
+        v.b = st[0]; v.h = st[1]; v.t = st[2];
+    } else if (layout == LA_LAYOUT_BHND) {
+        v.b = (long long)heads * N * d; v.h = (long long)N * d; v.t = d;
+    } else {
+        v.b = (long long)N * heads * d; v.h = d; v.t = (long long)heads * d;
+    }
+    return v;
+}
+
+bool strides_ok(const Rows &r) {
+    long long room = 1LL << 60;
+    for (int i = 0; i < 3; ++i) {
+        if (r.st(i) < 0) return false;
+        if (r.n[i] > 1 && r.st(i) > room / (r.n[i] - 1)) return false;
+        if (r.n[i] > 1) room -= (r.n[i] - 1) * r.st(i);
+    }
+    return room > 0;
+}
+
+// Order of the dimensions by the strides s, the widest first.
+void widest_first(const long long (&s)[3], int (&o)[3]) {
+    o[0] = 0; o[1] = 1; o[2] = 2;
+    for (int i = 0; i < 2; ++i)
+        for (int j = 0; j < 2 - i; ++j)
+            if (s[o[j]] < s[o[j + 1]]) { const int x = o[j]; o[j] = o[j + 1]; o[j + 1] = x; }
+}
+
+// May two rows of it share elements?
+bool rows_overlap_each_other(const Rows &r) {
+    const long long s[3] = {r.n[0] > 1 ? r.st(0) : 0, r.n[1] > 1 ? r.st(1) : 0, r.n[2] > 1 ? r.st(2) : 0};
+    int o[3];
+    widest_first(s, o);
+    long long inner = r.d;
+    for (int i = 2; i >= 0; --i) {
+        if (r.n[o[i]] == 1) continue;
+        if (s[o[i]] < inner) return true;
+        inner += (r.n[o[i]] - 1) * s[o[i]];
+    }
+    return false;
+}
+
+// May a row of a and a row of b share bytes?  Parts of one buffer, whose common strides keep them apart, do not;
+// what cannot be told counts as shared.
+bool rows_overlap(const Rows &a, const Rows &b) {
+    const uintptr_t pa = reinterpret_cast<uintptr_t>(a.v.p), pb = reinterpret_cast<uintptr_t>(b.v.p);
+    if (pa > pb) return rows_overlap(b, a);
+    if ((uintptr_t)a.extent() * a.es <= pb - pa) return false;
+    if ((pb - pa) % a.es) return true;
+    const long long apart = (long long)((pb - pa) / a.es);
+    long long s[3];
+    for (int i = 0; i < 3; ++i) {
+        if (a.n[i] > 1 && b.n[i] > 1 && a.st(i) != b.st(i)) return true;
+        s[i] = a.n[i] > 1 ? a.st(i) : b.n[i] > 1 ? b.st(i) : 0;
+    }
+    int o[3];
+    widest_first(s, o);
+    long long ea = a.extent(), eb = b.extent();
+    for (int i = 0; i < 3 && s[o[i]] > 0; ++i) {   // all rows of a, and of b, at the same place modulo this stride?
+        ea -= (a.n[o[i]] - 1) * a.st(o[i]);
+        eb -= (b.n[o[i]] - 1) * b.st(o[i]);
+        const long long w = s[o[i]], at = apart % w;
+        bool whole = true;
+        for (int j = 0; j < i; ++j) whole = whole && s[o[j]] % w == 0;
+        if (whole && at >= ea && at + eb <= w) return false;
+    }
+    return true;
+}
+
+bool same_rows(const Rows &a, const Rows &b) {
+    if (a.v.p != b.v.p) return false;
+    for (int i = 0; i < 3; ++i)
+        if (a.n[i] != b.n[i] || (a.n[i] > 1 && a.st(i) != b.st(i))) return false;
+    return true;
+}
+
+bool overlap_rows(const Rows &r, const void *p, size_t bytes) {
+    return overlap(r.v.p, (size_t)r.extent() * r.es, p, bytes);
+}
+
+la_status check_norm_rotate(int B, int Hq, int Hk, int N, int d, la_dtype dt) {
+    if (dt != LA_DTYPE_F32 && dt != LA_DTYPE_BF16) return LA_ERR_UNSUPPORTED;
+    if (B < 1 || Hq < 1 || Hk < 1 || N < 0 || Hq >= 65536 - (long long)Hk) return LA_ERR_INVALID_ARG;
+    if (d < 2 || d > 256 || d % 2) return LA_ERR_UNSUPPORTED;
+    if ((long long)B * N >= (1LL << 31)) return LA_ERR_INVALID_ARG;
+    return LA_OK;
+}
+
+// Everything that both directions check; bufs: count / 2 tensors of q's heads and of k's in turn, the
+// last two outputs.
+la_status norm_rotate_args(NormRotateArgs &a, const void *const *bufs, int count, const long long *strides,
+                           la_layout layout, const long long *positions, long long positions_stride) {
+    la_status st = check_norm_rotate(a.B, a.Hq, a.Hk, a.N, a.d, a.dt);
+    if (st != LA_OK) return st;
+    if (layout != LA_LAYOUT_BHND && layout != LA_LAYOUT_BNHD) return LA_ERR_UNSUPPORTED;
+    if (a.norm != LA_NORM_NONE && a.norm != LA_NORM_RMS && a.norm != LA_NORM_L2) return LA_ERR_UNSUPPORTED;
+    if (a.pairs != LA_PAIRS_HALVES && a.pairs != LA_PAIRS_ADJACENT) return LA_ERR_UNSUPPORTED;
+    if (a.norm != LA_NORM_NONE && (!(a.eps > 0.f) || !std::isfinite(a.eps))) return LA_ERR_INVALID_ARG;
+    if (a.r < 0 || a.r > a.d / 2 || (a.r > 0 && !a.freq)) return LA_ERR_INVALID_ARG;
+    const uintptr_t at8 = reinterpret_cast<uintptr_t>(a.r ? a.freq : nullptr) | reinterpret_cast<uintptr_t>(positions);
+    if (!aligned4(a.wq) || !aligned4(a.wk) || (at8 & 7u)) return LA_ERR_INVALID_ARG;
+    if (positions && (positions_stride < 0 || (a.B > 1 && positions_stride > (1LL << 59) / (a.B - 1)))) return LA_ERR_INVALID_ARG;
+    if (a.N == 0) return LA_OK;
+    const int es = (int)esize(a.dt);
+    HeadsView *views[] = {&a.q, &a.k, &a.gq, &a.gk, &a.yq, &a.yk};
+    Rows rows[6];
+    for (int i = 0; i < count; ++i) {
+        const int heads = i % 2 ? a.Hk : a.Hq;
+        if (!bufs[i] || reinterpret_cast<uintptr_t>(bufs[i]) % es) return LA_ERR_INVALID_ARG;
+        rows[i] = {heads_view(bufs[i], strides ? strides + 3 * i : nullptr, layout, heads, a.N, a.d), {a.B, heads, a.N}, a.d, es};
+        if (!strides_ok(rows[i])) return LA_ERR_INVALID_ARG;
+        for (int j = 0; j < 3; ++j)   // a stride that is not stepped along says nothing
+            if (rows[i].n[j] == 1) (j == 0 ? rows[i].v.b : j == 1 ? rows[i].v.h : rows[i].v.t) = 0;
+        *views[i < count - 2 ? i : i - count + 6] = rows[i].v;
+    }
+    const long long tokens = (a.B - 1) * positions_stride + a.N;
+    for (int o = count - 2; o < count; ++o) {
+        if (rows_overlap_each_other(rows[o])) return LA_ERR_INVALID_ARG;
+        for (int i = 0; i < o; ++i) {
+            const bool in_place = i < count - 2 && i % 2 == o % 2 && same_rows(rows[o], rows[i]);
+            if (!in_place && rows_overlap(rows[o], rows[i])) return LA_ERR_INVALID_ARG;
+        }
+        if (overlap_rows(rows[o], a.wq, a.d * 4) || overlap_rows(rows[o], a.wk, a.d * 4) ||
+            overlap_rows(rows[o], a.freq, (size_t)a.r * 8) || overlap_rows(rows[o], positions, (size_t)tokens * 8))
+            return LA_ERR_INVALID_ARG;
+    }
+    a.positions = positions;
+    a.pos_batch = positions_stride;
+    return LA_OK;
+}
+
+NormRotateArgs rotate_args(int B, int Hq, int Hk, int N, int d, la_dtype dt, la_norm norm, float eps,
+                           const float *wq, const float *wk, const double *freq, int rotated, la_pairs pairs,
+                           void *stream) {
+    NormRotateArgs a{};
+    a.B = B; a.Hq = Hq; a.Hk = Hk; a.N = N; a.d = d; a.dt = dt; a.norm = norm; a.pairs = pairs; a.eps = eps;
+    a.wq = wq; a.wk = wk; a.freq = freq; a.r = rotated; a.stream = static_cast<cudaStream_t>(stream);
+    return a;
+}
+
+}  // namespace
+}  // namespace la
+
+extern "C" {
+
+la_status la_norm_rotate(const void *q, const void *k, void *q_out, void *k_out, const long long *strides, int B,
+                         int Hq, int Hk, int N, int d, la_dtype dt, la_layout layout, la_norm norm, float eps,
+                         const float *q_weight, const float *k_weight, const double *freq, int rotated,
+                         la_pairs pairs, const long long *positions, long long positions_stride, void *stream) {
+    NormRotateArgs a = rotate_args(B, Hq, Hk, N, d, dt, norm, eps, q_weight, k_weight, freq, rotated, pairs, stream);
+    const void *bufs[] = {q, k, q_out, k_out};
+    const la_status st = norm_rotate_args(a, bufs, 4, strides, layout, positions, positions_stride);
+    if (st != LA_OK || N == 0) return st;
+    return from_cuda(launch_norm_rotate(a));
+}
+
+size_t la_norm_rotate_backward_workspace_bytes(int B, int Hq, int Hk, int N, int d, la_dtype dt) {
+    if (check_norm_rotate(B, Hq, Hk, N, d, dt) != LA_OK || N == 0) return 0;
+    return norm_rotate_partials(rotate_args(B, Hq, Hk, N, d, dt, LA_NORM_RMS, 1.f, nullptr, nullptr, nullptr, 0,
+                                            LA_PAIRS_HALVES, nullptr)) * 4;
+}
+
+la_status la_norm_rotate_backward(const void *q, const void *k, const void *gq_out, const void *gk_out, void *grad_q,
+                                  void *grad_k, const long long *strides, int B, int Hq, int Hk, int N, int d,
+                                  la_dtype dt, la_layout layout, la_norm norm, float eps, const float *q_weight,
+                                  const float *k_weight, const double *freq, int rotated, la_pairs pairs,
+                                  const long long *positions, long long positions_stride, float *grad_q_weight,
+                                  float *grad_k_weight, void *workspace, size_t workspace_bytes, void *stream) {
+    NormRotateArgs a = rotate_args(B, Hq, Hk, N, d, dt, norm, eps, q_weight, k_weight, freq, rotated, pairs, stream);
+    const void *bufs[] = {q, k, gq_out, gk_out, grad_q, grad_k};
+    la_status st = norm_rotate_args(a, bufs, 6, strides, layout, positions, positions_stride);
+    if (st != LA_OK) return st;
+    if (!aligned4(grad_q_weight) || !aligned4(grad_k_weight)) return LA_ERR_INVALID_ARG;
+    const size_t nd = (size_t)d * 4;
+    if (N == 0) {   // empty sums
+        cudaError_t e = grad_q_weight ? cudaMemsetAsync(grad_q_weight, 0, nd, a.stream) : cudaSuccess;
+        if (e == cudaSuccess && grad_k_weight) e = cudaMemsetAsync(grad_k_weight, 0, nd, a.stream);
+        return from_cuda(e);
+    }
+    const bool sums = grad_q_weight || grad_k_weight;
+    const size_t need = sums ? la_norm_rotate_backward_workspace_bytes(B, Hq, Hk, N, d, dt) : 0;
+    if ((st = check_ws(workspace, workspace_bytes, need)) != LA_OK) return st;
+    const Buf out[] = {{grad_q_weight, nd}, {grad_k_weight, nd}, {sums ? workspace : nullptr, need}};
+    const Buf in[] = {{q_weight, nd}, {k_weight, nd}, {freq, (size_t)rotated * 8},
+                      {positions, (size_t)((B - 1) * positions_stride + N) * 8}};
+    if (clash(in, out)) return LA_ERR_INVALID_ARG;
+    const HeadsView views[] = {a.q, a.k, a.gq, a.gk, a.yq, a.yk};
+    for (int i = 0; i < 6; ++i) {
+        const Rows r{views[i], {B, i % 2 ? Hk : Hq, N}, d, (int)esize(dt)};
+        for (const Buf &o : out)
+            if (overlap_rows(r, o.p, o.n)) return LA_ERR_INVALID_ARG;
+    }
+    a.dwq = grad_q_weight;
+    a.dwk = grad_k_weight;
+    a.partials = sums ? static_cast<float *>(workspace) : nullptr;
+    return from_cuda(launch_norm_rotate_grad(a));
+}
+
 la_status la_workspace_status(const void *workspace, size_t workspace_bytes, void *stream) {
     if (!workspace || workspace_bytes < sizeof(WsHeader)) return LA_ERR_WORKSPACE;
     cudaStream_t s = static_cast<cudaStream_t>(stream);

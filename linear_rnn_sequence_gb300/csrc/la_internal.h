@@ -110,6 +110,30 @@ struct LayerNormArgs {
     float *partials = nullptr;
 };
 
+// Rows of heads: row (b, h, t) starts at p + b sb + h sh + t st (elements).
+struct HeadsView {
+    void *p;
+    long long b, h, t;
+};
+// Norm and rotation of queries and keys, and the gradients; pointers are device pointers.
+struct NormRotateArgs {
+    HeadsView q, k, yq, yk;         // inputs; outputs, or the inputs' gradients
+    HeadsView gq, gk;               // gradients of the outputs (forward: null)
+    int B, Hq, Hk, N, d;
+    la_dtype dt;
+    la_norm norm;
+    la_pairs pairs;
+    float eps;
+    const float *wq, *wk;           // nullable
+    const double *freq;
+    int r;                          // rotated pairs
+    const long long *positions;     // nullable
+    long long pos_batch;
+    float *dwq = nullptr, *dwk = nullptr;   // nullable
+    float *partials = nullptr;
+    cudaStream_t stream;
+};
+
 // Workspace header written at the start of every workspace (256 bytes).
 struct WsHeader {
     unsigned int error;         // 0 = ok, else an la_status value (LA_ERR_TIMEOUT)
@@ -186,5 +210,10 @@ cudaError_t launch_delta_step(const DeltaArgs &a);
 cudaError_t launch_layer_norm(const LayerNormArgs &a);
 size_t layer_norm_partials(long long rows, int D, la_dtype dt);   // floats of `partials`
 cudaError_t launch_layer_norm_backward(const LayerNormArgs &a);
+
+// norm and rotation of queries and keys
+cudaError_t launch_norm_rotate(const NormRotateArgs &a);
+size_t norm_rotate_partials(const NormRotateArgs &a);   // floats of `partials`; by the current device's SMs
+cudaError_t launch_norm_rotate_grad(const NormRotateArgs &a);
 
 }  // namespace la

@@ -1,7 +1,8 @@
 """ctypes binding of liblinattn.so (C ABI: include/linattn.h).
 
 Argument marshalling only: every step of the computation runs in the CUDA
-kernels behind the C entry points.  Tensors must be contiguous CUDA tensors;
+kernels behind the C entry points.  Tensors must be contiguous CUDA tensors
+(``norm_rotate`` and its gradients take strided ones);
 outputs and workspaces are allocated here with torch (the library allocates
 nothing).  There is no CPU fallback: a missing or unbuildable library raises.
 
@@ -14,6 +15,7 @@ Names follow the C ABI:
   ``random_features`` -> the gated and feature-map entry points
 * ``forward_delta``, ``backward_delta``, ``decode_step_delta`` -> the gated delta rule
 * ``layer_norm``, ``layer_norm_backward`` -> the norm that follows it
+* ``norm_rotate``, ``norm_rotate_backward`` -> queries and keys normed and rotated by position
 """
 from __future__ import annotations
 
@@ -30,6 +32,8 @@ LA_OK, LA_ERR_INVALID_ARG, LA_ERR_UNSUPPORTED, LA_ERR_CUDA, LA_ERR_TIMEOUT, LA_E
 LA_DTYPE_F32, LA_DTYPE_BF16 = 0, 1
 PHI = {"elu1": 0, "identity": 1}   # la_phi
 LAYOUT = {"bhnd": 0, "bnhd": 1}    # la_layout
+NORM = {None: 0, "rms": 1, "l2": 2}       # la_norm
+PAIRS = {"halves": 0, "adjacent": 1}      # la_pairs
 
 _lock = threading.Lock()
 _lib = None
@@ -137,6 +141,14 @@ def lib():
             L.la_layer_norm_backward_workspace_bytes.restype = sz
             L.la_layer_norm_backward.argtypes = [vp] * 8 + [ctypes.c_longlong, i, i, vp, sz, vp]
             L.la_layer_norm_backward.restype = i
+            ll = ctypes.c_longlong
+            rotate = [i] * 8 + [f, vp, vp, vp, i, i, vp, ll]   # B .. norm, eps, weights, freq .. positions_stride
+            L.la_norm_rotate.argtypes = [vp] * 5 + rotate + [vp]
+            L.la_norm_rotate.restype = i
+            L.la_norm_rotate_backward_workspace_bytes.argtypes = [i] * 6
+            L.la_norm_rotate_backward_workspace_bytes.restype = sz
+            L.la_norm_rotate_backward.argtypes = [vp] * 7 + rotate + [vp, vp, vp, sz, vp]
+            L.la_norm_rotate_backward.restype = i
             _lib = L
     return _lib
 
@@ -791,3 +803,136 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, sums=None, workspace=Non
                                       _addr(gb), rows, D, dt, wa, wbytes, _current_stream(dev))
     _raise(st, "la_layer_norm_backward")
     return gx, gw, gb
+
+
+# ---- norm and rotation of queries and keys ------------------------------------
+def _rotate_inputs(q, k, freq, positions, norm, q_weight, k_weight, pairs, layout):
+    """Checks what both directions share: (B, Hq, Hk, N, d, dtype code), the device's index, the arguments behind eps,
+    and the order of a tensor's strides (batch, head, token)."""
+    if layout not in LAYOUT or norm not in NORM or pairs not in PAIRS:
+        raise ValueError(f"layout must be one of {sorted(LAYOUT)}, norm of {list(NORM)}, pairs of {sorted(PAIRS)}")
+    shape, ks, f32 = q.shape, k.shape, torch.float32
+    if len(shape) == 4:
+        order = (0, 1, 2) if layout == "bhnd" else (0, 2, 1)
+        B, d, Hq, N, Hk = shape[0], shape[3], shape[order[1]], shape[order[2]], ks[order[1]] if len(ks) == 4 else 0
+        same = len(ks) == 4 and ks[0] == B and ks[3] == d and ks[order[2]] == N
+    elif len(shape) == 3:
+        order, N = (0, 1), 1
+        B, Hq, d = shape
+        Hk = ks[1] if len(ks) == 3 else 0
+        same = len(ks) == 3 and ks[0] == B and ks[2] == d
+    else:
+        raise ValueError("q and k must have four dimensions, or three for single tokens")
+    if not same:
+        raise ValueError("q and k must differ in their number of heads only")
+    dev = q.get_device()
+    rotated = 0
+    if freq is not None:
+        if freq.dim() != 1:
+            raise ValueError("freq must be float64 of one dimension")
+        rotated = freq.shape[0]
+    step = 0
+    if positions is not None:
+        lead = (B,) if len(shape) == 3 else (B, N)
+        if positions.shape == lead:
+            step = 1 if len(shape) == 3 else N
+        elif len(shape) == 4 and positions.shape == (N,):
+            lead = (N,)
+        else:
+            raise ValueError(f"positions must be int64 of shape {lead}" + ("" if len(shape) == 3 else f" or {(N,)}"))
+    elif len(shape) == 3 and rotated:
+        raise ValueError("single tokens need positions")
+    rest = (_expect("q_weight", q_weight, (d,), f32, dev), _expect("k_weight", k_weight, (d,), f32, dev),
+            _expect("freq", freq, (rotated,), torch.float64, dev), rotated, PAIRS[pairs],
+            None if positions is None else _expect("positions", positions, lead, torch.int64, dev), step)
+    return (B, Hq, Hk, N, d, _dtype_code(q)), dev, rest, order
+
+
+def _rows(name, t, like, device_index):
+    """Address of ``t``, of ``like``'s shape and dtype, whose rows are contiguous."""
+    if t.shape != like.shape or t.dtype is not like.dtype:
+        raise ValueError(f"{name} must be {like.dtype} of shape {tuple(like.shape)}, not {t.dtype} of {tuple(t.shape)}")
+    if t.get_device() != device_index:
+        raise ValueError(f"{name} is on {t.device}, not on cuda:{device_index}")
+    if t.stride(-1) != 1 and t.shape[-1] > 1:
+        raise ValueError(f"the last dimension of {name} must be contiguous")
+    return t.data_ptr()
+
+
+def _strides(order, *ts):
+    """The tensors' strides for the C call; None where all are contiguous."""
+    if all(t.is_contiguous() for t in ts):
+        return None
+    flat = []
+    for t in ts:
+        st = t.stride()
+        flat += [st[i] for i in order]
+        if len(order) == 2:
+            flat.append(0)
+    return (ctypes.c_longlong * len(flat))(*flat)
+
+
+def norm_rotate(q, k, freq=None, positions=None, norm="rms", q_weight=None, k_weight=None, eps: float = 1e-6,
+                pairs="halves", layout="bhnd", out=None, stream=None):
+    """Queries and keys normed over each head's d values, weighted and rotated by position, in one pass.
+
+    q: [B,Hq,N,d], k: [B,Hk,N,d] (``layout="bnhd"``: [B,N,H,d]; single tokens: [B,H,d]), bf16 or fp32; the last
+    dimension contiguous, any strides else, so that both may be parts of one projection's output.  norm: "rms"
+    (x / sqrt(mean(x^2) + eps)), "l2" (unit length, x / sqrt(sum(x^2) + eps)) or None; weights: float32 [d] or None.
+    freq: float64 [r], radians a position of the first 2 r values' pairs (e, e + r) ("halves") or
+    (2 e, 2 e + 1) ("adjacent"); None: no rotation.  positions: int64 [B,N] or [N] ([B] for single tokens);
+    None: 0, 1, ... .  Returns (q', k') in the inputs' shape and dtype; ``out`` may be (q, k).
+    """
+    if stream is not None or not q.is_cuda or q.get_device() != _current_device():
+        return _elsewhere(norm_rotate, stream, q, k, freq, positions, norm, q_weight, k_weight, eps, pairs, layout, out)
+    sizes, dev, rest, order = _rotate_inputs(q, k, freq, positions, norm, q_weight, k_weight, pairs, layout)
+    if out is None:
+        out = q.new_empty(q.shape), q.new_empty(k.shape)
+    yq, yk = out
+    if k.dtype is not q.dtype:
+        raise ValueError("q and k must have the same dtype")
+    st = lib().la_norm_rotate(_rows("q", q, q, dev), _rows("k", k, k, dev), _rows("out[0]", yq, q, dev),
+                              _rows("out[1]", yk, k, dev), _strides(order, q, k, yq, yk), *sizes, LAYOUT[layout],
+                              NORM[norm], eps, *rest, _current_stream(dev))
+    _raise(st, "la_norm_rotate")
+    return yq, yk
+
+
+@functools.lru_cache(maxsize=1024)
+def _rotate_backward_bytes(device_index, *sizes):
+    return int(lib().la_norm_rotate_backward_workspace_bytes(*sizes))
+
+
+def norm_rotate_backward(grad_q_out, grad_k_out, q, k, freq=None, positions=None, norm="rms", q_weight=None,
+                         k_weight=None, eps: float = 1e-6, pairs="halves", layout="bhnd", sums=None, out=None,
+                         workspace=None, stream=None):
+    """Gradients of ``norm_rotate`` for those of its outputs (their shape and dtype, strides as q and k):
+    (grad_q, grad_k, grad_q_weight, grad_k_weight), the first two in q's dtype, the sums float32 [d].
+    ``sums`` says whether to compute those (default: each where its weight is given); they are None otherwise.
+    ``out``: where grad_q and grad_k go; they may be q and k, or the outputs' gradients."""
+    if stream is not None or not q.is_cuda or q.get_device() != _current_device():
+        if stream is not None and stream.device != q.device:
+            raise ValueError("the stream is of another device than the tensors")
+        return _elsewhere(norm_rotate_backward, stream, grad_q_out, grad_k_out, q, k, freq, positions, norm, q_weight,
+                          k_weight, eps, pairs, layout, sums, out, workspace)
+    sizes, dev, rest, order = _rotate_inputs(q, k, freq, positions, norm, q_weight, k_weight, pairs, layout)
+    if k.dtype is not q.dtype:
+        raise ValueError("q and k must have the same dtype")
+    if out is None:
+        out = q.new_empty(q.shape), q.new_empty(k.shape)
+    yq, yk = out
+    d = sizes[4]
+    gwq = q.new_empty(d, dtype=torch.float32) if (q_weight is not None if sums is None else sums) else None
+    gwk = q.new_empty(d, dtype=torch.float32) if (k_weight is not None if sums is None else sums) else None
+    wa, wbytes = None, 0
+    if gwq is not None or gwk is not None:
+        workspace, wa, wbytes = _workspace(workspace, _rotate_backward_bytes(dev, *sizes), q)
+    st = lib().la_norm_rotate_backward(_rows("q", q, q, dev), _rows("k", k, k, dev),
+                                       _rows("grad_q_out", grad_q_out, q, dev),
+                                       _rows("grad_k_out", grad_k_out, k, dev), _rows("out[0]", yq, q, dev),
+                                       _rows("out[1]", yk, k, dev),
+                                       _strides(order, q, k, grad_q_out, grad_k_out, yq, yk), *sizes,
+                                       LAYOUT[layout], NORM[norm], eps, *rest, _addr(gwq), _addr(gwk), wa, wbytes,
+                                       _current_stream(dev))
+    _raise(st, "la_norm_rotate_backward")
+    return yq, yk, gwq, gwk
