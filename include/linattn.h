@@ -619,6 +619,67 @@ LA_API la_status la_norm_rotate_backward(const void *q, const void *k, const voi
                                          size_t workspace_bytes, void *stream);
 
 /*
+ * Workspace size in bytes for la_forward_retention with these sizes: 0 where the call needs none, and
+ * for unsupported arguments.  It holds the run-time status header and states within the sequence (of
+ * blocks, or of the segments that few heads make the call split it into), so it depends on the current
+ * device's SM count.
+ */
+LA_API size_t la_retention_workspace_bytes(int B, int H, int N, int d, int dv, la_dtype dt);
+
+/*
+ * Retention, causal ("Linear Attention/es", "Variantes y extensiones", RetNet: a decay for each head,
+ * without feature map and denominator, so that queries and keys may have any sign, as rotated ones
+ * (la_norm_rotate) do; la_forward_causal_decay is the form with both):
+ *     S_t = gamma_h S_{t-1} + k_t v_t^T,   y_t = S_t^T q_t.
+ * There is no scale; y is usually layer-normed (la_layer_norm).
+ *   q, k     dtype dt, H heads of width d, [B][H][N][d] or (LA_LAYOUT_BNHD) [B][N][H][d].
+ *   v, y     dtype dt, H heads of width dv, laid out alike.  y is rounded once, to dt, from float32.
+ *   gamma    DEVICE array of H floats in [0, 1], 4-byte aligned, shared by the batch rows; its values are
+ *            not checked (one outside [0, 1] gives a meaningless result, not an error).  Gamma 0 leaves
+ *            each token its own key and value.
+ *   S_in     float32 [B][H][d][dv] or NULL (zero); S_out the final state or NULL; S_out may equal S_in.
+ * Padding goes in front: tokens with k = 0 and v = 0 before the first leave a state that starts from zero
+ * as it is; behind the last they would decay it.
+ * A value that is not finite reaches y of its own token and of later ones and the states behind it, and
+ * nothing before its token: what the recurrence makes infinite or NaN there may be either.
+ * d, dv in {32, 64, 128}; B, H >= 1; N >= 0 (N = 0 writes S_out only); B*H*N*max(d, dv) < 2^31 and
+ * B*H*d*dv < 2^31.  q, k, v, y, S_in and S_out 16-byte aligned.  y must overlap no other buffer, S_out no
+ * other than an identical S_in.  States and sums are kept in float32 for both dtypes.
+ */
+LA_API la_status la_forward_retention(const void *q, const void *k, const void *v, void *y,
+                                      const float *gamma, int B, int H, int N, int d, int dv, la_dtype dt,
+                                      la_layout layout, const float *S_in, float *S_out,
+                                      void *workspace, size_t workspace_bytes, void *stream);
+
+/* Workspace size in bytes for la_backward_retention (0 where the call needs none, and for unsupported
+ * arguments); it depends on the current device's SM count. */
+LA_API size_t la_retention_backward_workspace_bytes(int B, int H, int N, int d, int dv, la_dtype dt);
+
+/*
+ * Gradients of la_forward_retention for dy = dL/dy (dtype dt, layout and shape of y) and, optionally,
+ * grad_S_out = dL/dS_N (float32; NULL: zero).  With G_t = q_t dy_t^T + gamma G_{t+1} (G_N with grad_S_out):
+ *     grad_q_t = S_t dy_t,   grad_k_t = G_t v_t,   grad_v_t = G_t^T k_t,   grad_S_in = gamma G_1,
+ * the first the retention of (dy, v, k), the others retentions from behind of (v, dy, q) and (k, q, dy).
+ * grad_q, grad_k, grad_v have the dtype and layout of q, k, v; grad_S_in may be NULL.  The gradient with
+ * respect to gamma is not computed.  No output may overlap another buffer.  The rest as in the forward; a
+ * value that is not finite reaches grad_q of later tokens and grad_k and grad_v of earlier ones, and its own.
+ */
+LA_API la_status la_backward_retention(const void *q, const void *k, const void *v, const void *dy,
+                                       const float *gamma, void *grad_q, void *grad_k, void *grad_v, int B,
+                                       int H, int N, int d, int dv, la_dtype dt, la_layout layout,
+                                       const float *S_in, const float *grad_S_out, float *grad_S_in,
+                                       void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * One token of retention per (b, h): S_out = gamma_h S_in + k v^T (both float32 [B][H][d][dv]; S_out may
+ * equal S_in: in place) and y = S_out^T q.  q, k: [B][H][d], v, y: [B][H][dv] of dtype dt; gamma as in
+ * la_forward_retention, sizes and alignment too.
+ */
+LA_API la_status la_decode_step_retention(const void *q, const void *k, const void *v, void *y,
+                                          const float *gamma, const float *S_in, float *S_out, int B, int H,
+                                          int d, int dv, la_dtype dt, void *stream);
+
+/*
  * Synchronise `stream` and report the run-time status recorded in a
  * workspace by the last call that used it: LA_OK, or LA_ERR_TIMEOUT when one
  * of its bounded waits ran out (its outputs are then undefined).  The next

@@ -939,6 +939,122 @@ la_status la_norm_rotate_backward(const void *q, const void *k, const void *gq_o
     return from_cuda(launch_norm_rotate_grad(a));
 }
 
+}  // extern "C"
+
+namespace la {
+namespace {
+
+RetainArgs retain_args(const void *q, const void *k, const void *v, void *y, const float *gamma, int B, int H, int N,
+                       int d, int dv, la_dtype dt, la_layout layout, const float *S_in, float *S_out, bool rev,
+                       bool trans, void *ws, void *stream) {
+    RetainArgs a{};
+    a.q = q; a.k = k; a.v = v; a.y = y; a.gamma = gamma;
+    a.B = B; a.H = H; a.N = N; a.d = d; a.dv = dv; a.dt = dt; a.layout = layout;
+    a.S_in = S_in; a.S_out = S_out; a.rev = rev; a.trans = trans; a.ws = ws;
+    a.stream = static_cast<cudaStream_t>(stream);
+    return a;
+}
+
+// Any call of these sizes: with a final state or without.
+size_t retain_ws_bytes(int B, int H, int N, int d, int dv, la_dtype dt) {
+    if (check_delta(B, H, H, N, d, dv, dt) != LA_OK || N == 0) return 0;
+    float some;
+    return sizeof(WsHeader) + retain_simt_workspace(retain_args(nullptr, nullptr, nullptr, nullptr, nullptr, B, H, N, d, dv, dt,
+                                                                LA_LAYOUT_BHND, nullptr, &some, false, false, nullptr, nullptr));
+}
+
+cudaError_t launch_retain(const RetainArgs &a) { return launch_retain_simt(a); }
+
+}  // namespace
+}  // namespace la
+
+extern "C" {
+
+size_t la_retention_workspace_bytes(int B, int H, int N, int d, int dv, la_dtype dt) {
+    return retain_ws_bytes(B, H, N, d, dv, dt);
+}
+
+la_status la_forward_retention(const void *q, const void *k, const void *v, void *y, const float *gamma, int B, int H,
+                               int N, int d, int dv, la_dtype dt, la_layout layout, const float *S_in, float *S_out,
+                               void *workspace, size_t workspace_bytes, void *stream) {
+    la_status st = check_delta(B, H, H, N, d, dv, dt);
+    if (st != LA_OK) return st;
+    if (layout != LA_LAYOUT_BHND && layout != LA_LAYOUT_BNHD) return LA_ERR_UNSUPPORTED;
+    const size_t es = esize(dt), T = (size_t)B * H * N, sb = (size_t)B * H * d * dv * 4;
+    if (!aligned16(S_in) || !aligned16(S_out)) return LA_ERR_INVALID_ARG;
+    if (S_in != S_out && overlap(S_in, sb, S_out, sb)) return LA_ERR_INVALID_ARG;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (N == 0) return from_cuda(copy_state(S_out, S_in, sb, s));   // no tokens: q .. gamma may be NULL
+    if (!gamma || !aligned4(gamma)) return LA_ERR_INVALID_ARG;
+    const void *need16[] = {q, k, v, y};
+    for (const void *p : need16)
+        if (!p || !aligned16(p)) return LA_ERR_INVALID_ARG;
+    const size_t need = la_retention_workspace_bytes(B, H, N, d, dv, dt);
+    if ((st = check_ws(workspace, workspace_bytes, need)) != LA_OK) return st;
+    const Buf in[] = {{q, T * d * es}, {k, T * d * es}, {v, T * dv * es}, {gamma, (size_t)H * 4},
+                      {S_in != S_out ? S_in : nullptr, sb}};
+    const Buf out[] = {{y, T * dv * es}, {S_out, sb}, {need ? workspace : nullptr, need}};
+    if (clash(in, out)) return LA_ERR_INVALID_ARG;
+    if (need && cudaMemsetAsync(workspace, 0, sizeof(WsHeader), s) != cudaSuccess) return LA_ERR_CUDA;
+    return from_cuda(launch_retain(retain_args(q, k, v, y, gamma, B, H, N, d, dv, dt, layout, S_in, S_out, false, false, need ? workspace : nullptr,
+                                               stream)));
+}
+
+size_t la_retention_backward_workspace_bytes(int B, int H, int N, int d, int dv, la_dtype dt) {
+    return retain_ws_bytes(B, H, N, d, dv, dt);
+}
+
+la_status la_backward_retention(const void *q, const void *k, const void *v, const void *dy, const float *gamma,
+                                void *grad_q, void *grad_k, void *grad_v, int B, int H, int N, int d, int dv,
+                                la_dtype dt, la_layout layout, const float *S_in, const float *grad_S_out,
+                                float *grad_S_in, void *workspace, size_t workspace_bytes, void *stream) {
+    la_status st = check_delta(B, H, H, N, d, dv, dt);
+    if (st != LA_OK) return st;
+    if (layout != LA_LAYOUT_BHND && layout != LA_LAYOUT_BNHD) return LA_ERR_UNSUPPORTED;
+    const size_t es = esize(dt), T = (size_t)B * H * N, sb = (size_t)B * H * d * dv * 4;
+    if (!aligned16(S_in) || !aligned16(grad_S_out) || !aligned16(grad_S_in)) return LA_ERR_INVALID_ARG;
+    if (overlap(grad_S_in, sb, S_in, sb) || overlap(grad_S_in, sb, grad_S_out, sb)) return LA_ERR_INVALID_ARG;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (N == 0) return from_cuda(copy_state(grad_S_in, grad_S_out, sb, s));
+    if (!gamma || !aligned4(gamma)) return LA_ERR_INVALID_ARG;
+    const void *need16[] = {q, k, v, dy, grad_q, grad_k, grad_v};
+    for (const void *p : need16)
+        if (!p || !aligned16(p)) return LA_ERR_INVALID_ARG;
+    const size_t need = la_retention_backward_workspace_bytes(B, H, N, d, dv, dt);
+    if ((st = check_ws(workspace, workspace_bytes, need)) != LA_OK) return st;
+    const Buf in[] = {{q, T * d * es}, {k, T * d * es}, {v, T * dv * es}, {dy, T * dv * es}, {gamma, (size_t)H * 4},
+                      {S_in, sb}, {grad_S_out, sb}};
+    const Buf out[] = {{grad_q, T * d * es}, {grad_k, T * d * es}, {grad_v, T * dv * es}, {grad_S_in, sb},
+                       {need ? workspace : nullptr, need}};
+    if (clash(in, out)) return LA_ERR_INVALID_ARG;
+    if (need && cudaMemsetAsync(workspace, 0, sizeof(WsHeader), s) != cudaSuccess) return LA_ERR_CUDA;
+    void *ws = need ? workspace : nullptr;
+    cudaError_t e = launch_retain(retain_args(dy, v, k, grad_q, gamma, B, H, N, dv, d, dt, layout, S_in, nullptr, false, true, ws, stream));
+    if (e == cudaSuccess)
+        e = launch_retain(retain_args(v, dy, q, grad_k, gamma, B, H, N, dv, d, dt, layout, grad_S_out, nullptr, true, true, ws, stream));
+    if (e == cudaSuccess)
+        e = launch_retain(retain_args(k, q, dy, grad_v, gamma, B, H, N, d, dv, dt, layout, grad_S_out, grad_S_in, true, false, ws, stream));
+    return from_cuda(e);
+}
+
+la_status la_decode_step_retention(const void *q, const void *k, const void *v, void *y, const float *gamma,
+                                   const float *S_in, float *S_out, int B, int H, int d, int dv, la_dtype dt,
+                                   void *stream) {
+    la_status st = check_delta(B, H, H, 1, d, dv, dt);
+    if (st != LA_OK) return st;
+    const void *need16[] = {q, k, v, y, S_in, S_out};
+    for (const void *p : need16)
+        if (!p || !aligned16(p)) return LA_ERR_INVALID_ARG;
+    if (!gamma || !aligned4(gamma)) return LA_ERR_INVALID_ARG;
+    const size_t es = esize(dt), T = (size_t)B * H, sb = T * d * dv * 4;
+    const Buf in[] = {{q, T * d * es}, {k, T * d * es}, {v, T * dv * es}, {gamma, (size_t)H * 4},
+                      {S_in != S_out ? S_in : nullptr, sb}};
+    const Buf out[] = {{y, T * dv * es}, {S_out, sb}};
+    if (clash(in, out)) return LA_ERR_INVALID_ARG;
+    return from_cuda(launch_retain_step(retain_args(q, k, v, y, gamma, B, H, 1, d, dv, dt, LA_LAYOUT_BHND, S_in, S_out,
+                                                    false, false, nullptr, stream)));
+}
+
 la_status la_workspace_status(const void *workspace, size_t workspace_bytes, void *stream) {
     if (!workspace || workspace_bytes < sizeof(WsHeader)) return LA_ERR_WORKSPACE;
     cudaStream_t s = static_cast<cudaStream_t>(stream);

@@ -110,6 +110,25 @@ struct LayerNormArgs {
     float *partials = nullptr;
 };
 
+// Retention, or one of its gradients, which are retentions of other tensors: y_i = sum over j of
+// gamma^|i - j| (q_i . k_j) v_j and the state's part, j <= i, or (rev) j >= i with the state coming from
+// behind.  The state [d][dv], or (trans) stored as [dv][d], is that before the first token taken; rev: as
+// seen from that token, so that S_in enters the last token's y without a decay, and S_out is decayed once
+// more than the first token's.
+struct RetainArgs {
+    const void *q, *k, *v;
+    void *y;
+    const float *gamma;          // [H]
+    int B, H, N, d, dv;
+    la_dtype dt;
+    la_layout layout;
+    const float *S_in;           // nullable (zero)
+    float *S_out;                // nullable
+    bool rev, trans;
+    void *ws;                    // starts with a status header
+    cudaStream_t stream;
+};
+
 // Rows of heads: row (b, h, t) starts at p + b sb + h sh + t st (elements).
 struct HeadsView {
     void *p;
@@ -215,5 +234,10 @@ cudaError_t launch_layer_norm_backward(const LayerNormArgs &a);
 cudaError_t launch_norm_rotate(const NormRotateArgs &a);
 size_t norm_rotate_partials(const NormRotateArgs &a);   // floats of `partials`; by the current device's SMs
 cudaError_t launch_norm_rotate_grad(const NormRotateArgs &a);
+
+// retention (CUDA cores, float32), and a single token of it
+size_t retain_simt_workspace(const RetainArgs &a);
+cudaError_t launch_retain_simt(const RetainArgs &a);
+cudaError_t launch_retain_step(const RetainArgs &a);
 
 }  // namespace la

@@ -1,0 +1,300 @@
+// retention_simt.cu -- retention on the CUDA cores, in float32: blocks of 64 tokens in three launches.
+//
+//   1. each block's own sum of k_j v_j^T, at the weights of its end (a CTA a block);
+//   2. the states before the blocks, one after another over the sums (a thread for four of a state's values);
+//   3. each block's y from its state (a CTA a block): scores, their product with v, the state's part.
+// Every block of 1 and 3 runs at once, so a long sequence of few heads fills the GPU as well as many short ones
+// do.  Bound by the float32 multiplications: 4 (32 + d) dv + 64 d ... a token of a head; the states' way through memory
+// (three times 4 d dv bytes a block) is the rest.
+// It serves float32 inputs, widths of 32, and short bf16 sequences.
+#include "retention.cuh"
+
+namespace la {
+namespace {
+
+constexpr int kRC = 64;       // tokens of a block
+constexpr int kRThr = 256;    // 16 x 16 threads
+constexpr int kScanThr = 128;
+constexpr int kPad = 4;       // floats behind a row of Q, K and P: rows four banks apart
+
+struct RetainSimt {
+    const void *q, *k, *v;
+    void *y;
+    const float *gamma, *S_in;
+    float *S_out, *states;    // states: [head][block][d][dv]
+    int H, N, layout, nblk;
+    bool rev, trans;
+};
+
+// Rows t0.. of a head as floats into dst (rows LD floats apart), zeros from token n on.
+template <int W, int LD, typename T>
+__device__ __forceinline__ void stage(float *dst, const T *src, TokenRows r, int t0, int n) {
+    constexpr int V = 16 / (int)sizeof(T), ROW = W / V;
+    for (int e = threadIdx.x; e < kRC * ROW; e += kRThr) {
+        const int t = e / ROW, f = e % ROW * V;
+        float x[V];
+        if (t < n) {
+            const uint4 u = __ldg(reinterpret_cast<const uint4 *>(src + r.at(t0 + t) + f));
+            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                x[i] = V == 4 ? __uint_as_float(w[i & 3]) : __uint_as_float(i & 1 ? w[i >> 1 & 3] & 0xFFFF0000u : w[i >> 1 & 3] << 16);
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; ++i) x[i] = 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < V; i += 4) *reinterpret_cast<float4 *>(dst + t * LD + f + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+    }
+}
+
+// A thread's columns of a row of W values: groups of G, 16 G apart.
+template <int W> struct Cols {
+    static constexpr int G = W / 16 < 4 ? W / 16 : 4, NG = W / 16 / G, N = G * NG;
+    static __device__ __forceinline__ void load(const float *row, int tx, float (&x)[N]) {
+#pragma unroll
+        for (int i = 0; i < NG; ++i) {
+            const float *p = row + i * 16 * G + tx * G;
+            if (G == 4) {
+                const float4 t = *reinterpret_cast<const float4 *>(p);
+                x[i * G] = t.x; x[i * G + 1 % G] = t.y; x[i * G + 2 % G] = t.z; x[i * G + 3 % G] = t.w;
+            } else {
+                const float2 t = *reinterpret_cast<const float2 *>(p);
+                x[i * G] = t.x; x[i * G + 1 % G] = t.y;
+            }
+        }
+    }
+    static __device__ __forceinline__ int at(int tx, int c) { return c / G * 16 * G + tx * G + c % G; }
+};
+
+template <int D, int DV, typename T>
+__global__ void __launch_bounds__(kRThr) retain_sums_kernel(const RetainSimt p) {
+    extern __shared__ float sm[];
+    float *K = sm, *V = K + kRC * D;
+    __shared__ float w[kRC];
+    const int bh = blockIdx.x / p.nblk, blk = blockIdx.x % p.nblk, b = bh / p.H, h = bh % p.H, t0 = blk * kRC, n = min(kRC, p.N - t0);
+    if (threadIdx.x < kRC) w[threadIdx.x] = (int)threadIdx.x < n ? gamma_power(p.gamma[h], key_exp(p.rev, threadIdx.x, n)) : 0.f;
+    stage<D, D>(K, (const T *)p.k, token_rows(p.layout, b, h, p.H, p.N, D), t0, n);
+    stage<DV, DV>(V, (const T *)p.v, token_rows(p.layout, b, h, p.H, p.N, DV), t0, n);
+    __syncthreads();
+    using CA = Cols<D>;
+    using CC = Cols<DV>;
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    float acc[CA::N][CC::N];
+#pragma unroll
+    for (int a = 0; a < CA::N; ++a)
+#pragma unroll
+        for (int c = 0; c < CC::N; ++c) acc[a][c] = 0.f;
+#pragma unroll 4
+    for (int j = 0; j < n; ++j) {
+        float x[CA::N], y[CC::N];
+        CA::load(K + j * D, ty, x);
+        CC::load(V + j * DV, tx, y);
+        const float g = w[j];
+#pragma unroll
+        for (int a = 0; a < CA::N; ++a) {
+            x[a] *= g;
+#pragma unroll
+            for (int c = 0; c < CC::N; ++c) acc[a][c] = fmaf(x[a], y[c], acc[a][c]);
+        }
+    }
+    float *out = p.states + ((size_t)bh * p.nblk + blk) * D * DV;
+#pragma unroll
+    for (int a = 0; a < CA::N; ++a)
+#pragma unroll
+        for (int c = 0; c < CC::N; ++c) out[CA::at(ty, a) * DV + CC::at(tx, c)] = acc[a][c];
+}
+
+// The sums become the states before their blocks.
+__global__ void __launch_bounds__(kScanThr) retain_scan_kernel(const RetainSimt p, int D, int DV) {
+    const int st = D * DV, parts = st / 4 / kScanThr;
+    const int bh = blockIdx.x / parts, at = (blockIdx.x % parts * kScanThr + threadIdx.x) * 4;
+    const float g = p.gamma[bh % p.H], whole = gamma_power(g, kRC), last = gamma_power(g, p.N - (p.nblk - 1) * kRC);
+    float4 *s = reinterpret_cast<float4 *>(p.states + (size_t)bh * p.nblk * st + at);
+    const int step = st / 4;
+    // of a state's values in their order here; a transposed state's lie DV apart
+    auto where = [&](int i) { return p.trans ? (size_t)((at + i) % DV) * D + (at + i) / DV : (size_t)at + i; };
+    float x[4] = {0.f, 0.f, 0.f, 0.f};
+    if (p.S_in)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = p.S_in[(size_t)bh * st + where(i)];
+    constexpr int U = 8;
+    for (int k0 = 0; k0 < p.nblk; k0 += U) {
+        float4 u[U];
+#pragma unroll
+        for (int i = 0; i < U; ++i)
+            if (k0 + i < p.nblk) u[i] = s[(size_t)(p.rev ? p.nblk - 1 - k0 - i : k0 + i) * step];
+#pragma unroll
+        for (int i = 0; i < U; ++i)
+            if (k0 + i < p.nblk) {
+                const int blk = p.rev ? p.nblk - 1 - k0 - i : k0 + i;
+                const float f = blk == p.nblk - 1 ? last : whole;
+                s[(size_t)blk * step] = make_float4(x[0], x[1], x[2], x[3]);
+                x[0] = fmaf(f, x[0], u[i].x);
+                x[1] = fmaf(f, x[1], u[i].y);
+                x[2] = fmaf(f, x[2], u[i].z);
+                x[3] = fmaf(f, x[3], u[i].w);
+            }
+    }
+    if (p.S_out)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) p.S_out[(size_t)bh * st + where(i)] = x[i];
+}
+
+// acc[4][C] += sum over 4 j of p[4][4] v[4][C]; DIAG: only where row r may see j.
+template <int N, bool DIAG> __device__ __forceinline__ void four(float (&acc)[4][N], const float *P, int ldp, const float *V, int ldv, int tx, bool rev) {
+    float pr[4][4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        const float4 t = *reinterpret_cast<const float4 *>(P + r * ldp);
+        pr[r][0] = t.x; pr[r][1] = t.y; pr[r][2] = t.z; pr[r][3] = t.w;
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        float v[N];
+        Cols<N * 16>::load(V + j * ldv, tx, v);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            if (DIAG && (rev ? j < r : j > r)) continue;   // a value that is not finite meets no zero
+#pragma unroll
+            for (int c = 0; c < N; ++c) acc[r][c] = fmaf(pr[r][j], v[c], acc[r][c]);
+        }
+    }
+}
+
+template <int D, int DV, typename T> struct OutLay {
+    static constexpr int LQ = D + kPad, LP = kRC + kPad, SR = 32;   // SR: rows of the state at a time
+    static constexpr int over = LP * kRC + SR * DV, k = kRC * LQ > over ? kRC * LQ : over;   // K, then P and rows of S
+    static constexpr int bytes = 4 * (kRC * LQ + k + kRC * DV);
+};
+
+template <int D, int DV, typename T>
+__global__ void __launch_bounds__(kRThr, 2) retain_out_kernel(const RetainSimt p) {
+    using L = OutLay<D, DV, T>;
+    using CC = Cols<DV>;
+    constexpr int C = CC::N;
+    extern __shared__ float sm[];
+    float *Q = sm, *K = Q + kRC * L::LQ, *V = K + L::k, *P = K, *S = P + L::LP * kRC;
+    __shared__ float pw[kRC + 1];
+    const int bh = blockIdx.x / p.nblk, blk = blockIdx.x % p.nblk, b = bh / p.H, h = bh % p.H, t0 = blk * kRC, n = min(kRC, p.N - t0);
+    const bool rev = p.rev;
+    if (threadIdx.x <= kRC) pw[threadIdx.x] = gamma_power(p.gamma[h], threadIdx.x);
+    const TokenRows rk = token_rows(p.layout, b, h, p.H, p.N, D), rv = token_rows(p.layout, b, h, p.H, p.N, DV);
+    stage<D, L::LQ>(Q, (const T *)p.q, rk, t0, n);
+    stage<D, L::LQ>(K, (const T *)p.k, rk, t0, n);
+    stage<DV, DV>(V, (const T *)p.v, rv, t0, n);
+    __syncthreads();
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;   // rows 4 ty ..; scores of columns tx + 16 c
+    float s[4][4] = {};
+#pragma unroll 2
+    for (int a = 0; a < D; a += 4) {
+        float4 x[4], y[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) x[r] = *reinterpret_cast<const float4 *>(Q + (4 * ty + r) * L::LQ + a);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) y[c] = *reinterpret_cast<const float4 *>(K + (tx + 16 * c) * L::LQ + a);
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+                s[r][c] = fmaf(x[r].x, y[c].x, fmaf(x[r].y, y[c].y, fmaf(x[r].z, y[c].z, fmaf(x[r].w, y[c].w, s[r][c]))));
+    }
+    __syncthreads();   // K has been read
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            const int i = 4 * ty + r, j = tx + 16 * c, e = rev ? j - i : i - j;
+            P[i * L::LP + j] = e >= 0 ? s[r][c] * pw[e] : 0.f;
+        }
+    // the state's part, rows of S staged where K was
+    const float *S0 = p.nblk > 1 || p.S_out ? p.states + ((size_t)bh * p.nblk + blk) * D * DV : p.S_in ? p.S_in + (size_t)bh * D * DV : nullptr;
+    const bool trans = p.trans && !(p.nblk > 1 || p.S_out);
+    float acc[4][C];
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int c = 0; c < C; ++c) acc[r][c] = 0.f;
+    if (S0) {
+#pragma unroll 1
+        for (int a0 = 0; a0 < D; a0 += L::SR) {
+            __syncthreads();
+            for (int e = threadIdx.x; e < L::SR * DV; e += kRThr)
+                S[e] = trans ? S0[(size_t)(e % DV) * D + a0 + e / DV] : S0[(size_t)a0 * DV + e];
+            __syncthreads();
+#pragma unroll 2
+            for (int a = 0; a < L::SR; a += 4) four<C, false>(acc, Q + 4 * ty * L::LQ + a0 + a, L::LQ, S + a * DV, DV, tx, rev);
+        }
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int e = inter_exp(rev, 4 * ty + r, n);
+            const float f = e >= 0 ? pw[e] : 0.f;   // none: behind the last token
+#pragma unroll
+            for (int c = 0; c < C; ++c) acc[r][c] *= f;
+        }
+    }
+    __syncthreads();
+    const int d0 = 4 * ty;   // the four columns on the diagonal
+#pragma unroll 2
+    for (int j = rev ? d0 + 4 : 0; j < (rev ? kRC : d0); j += 4) four<C, false>(acc, P + d0 * L::LP + j, L::LP, V + j * DV, DV, tx, rev);
+    if (rev) four<C, true>(acc, P + d0 * L::LP + d0, L::LP, V + d0 * DV, DV, tx, true);
+    else four<C, true>(acc, P + d0 * L::LP + d0, L::LP, V + d0 * DV, DV, tx, false);
+    T *y = (T *)p.y;
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+        if (4 * ty + r < n)
+#pragma unroll
+            for (int c = 0; c < C; ++c) y[rv.at(t0 + 4 * ty + r) + CC::at(tx, c)] = from_f<T>(acc[r][c]);
+}
+
+int blocks_of(int N) { return (N + kRC - 1) / kRC; }
+// One block, and no final state asked for: y comes from S_in itself.
+bool needs_states(const RetainArgs &a) { return a.N > kRC || a.S_out; }
+
+template <int D, int DV, typename T> cudaError_t launch_t(const RetainArgs &a) {
+    RetainSimt p{};
+    p.q = a.q; p.k = a.k; p.v = a.v; p.y = a.y; p.gamma = a.gamma; p.S_in = a.S_in; p.S_out = a.S_out;
+    p.H = a.H; p.N = a.N; p.layout = a.layout; p.nblk = blocks_of(a.N); p.rev = a.rev; p.trans = a.trans;
+    if (a.ws) p.states = reinterpret_cast<float *>(static_cast<char *>(a.ws) + sizeof(WsHeader));
+    const unsigned BH = (unsigned)a.B * a.H, blocks = BH * p.nblk;   // fewer than tokens, which fit 31 bits
+    cudaError_t e = cudaSuccess;
+    if (needs_states(a)) {
+        constexpr int smem = 4 * kRC * (D + DV);
+        e = cudaFuncSetAttribute(retain_sums_kernel<D, DV, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+        retain_sums_kernel<D, DV, T><<<blocks, kRThr, smem, a.stream>>>(p);
+        retain_scan_kernel<<<BH * (D * DV / 4 / kScanThr), kScanThr, 0, a.stream>>>(p, D, DV);
+    }
+    constexpr int smem = OutLay<D, DV, T>::bytes;
+    e = cudaFuncSetAttribute(retain_out_kernel<D, DV, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    retain_out_kernel<D, DV, T><<<blocks, kRThr, smem, a.stream>>>(p);
+    return cudaGetLastError();
+}
+template <int D, typename T> cudaError_t launch_d(const RetainArgs &a) {
+    switch (a.dv) {
+    case 32: return launch_t<D, 32, T>(a);
+    case 64: return launch_t<D, 64, T>(a);
+    case 128: return launch_t<D, 128, T>(a);
+    }
+    return cudaErrorInvalidValue;
+}
+template <typename T> cudaError_t launch(const RetainArgs &a) {
+    switch (a.d) {
+    case 32: return launch_d<32, T>(a);
+    case 64: return launch_d<64, T>(a);
+    case 128: return launch_d<128, T>(a);
+    }
+    return cudaErrorInvalidValue;
+}
+
+}  // namespace
+
+size_t retain_simt_workspace(const RetainArgs &a) {
+    return needs_states(a) ? (size_t)a.B * a.H * blocks_of(a.N) * a.d * a.dv * 4 : 0;
+}
+cudaError_t launch_retain_simt(const RetainArgs &a) {
+    return a.dt == LA_DTYPE_BF16 ? launch<__nv_bfloat16>(a) : launch<float>(a);
+}
+
+}  // namespace la

@@ -15,6 +15,8 @@ Names follow the C ABI:
   ``random_features`` -> the gated and feature-map entry points
 * ``forward_delta``, ``backward_delta``, ``decode_step_delta`` -> the gated delta rule
 * ``layer_norm``, ``layer_norm_backward`` -> the norm that follows it
+* ``forward_retention``, ``backward_retention``, ``decode_step_retention`` -> retention: a decay for
+  each head, no feature map, no denominator
 * ``norm_rotate``, ``norm_rotate_backward`` -> queries and keys normed and rotated by position
 """
 from __future__ import annotations
@@ -149,6 +151,16 @@ def lib():
             L.la_norm_rotate_backward_workspace_bytes.restype = sz
             L.la_norm_rotate_backward.argtypes = [vp] * 7 + rotate + [vp, vp, vp, sz, vp]
             L.la_norm_rotate_backward.restype = i
+            L.la_retention_workspace_bytes.argtypes = [i] * 6
+            L.la_retention_workspace_bytes.restype = sz
+            L.la_forward_retention.argtypes = [vp] * 5 + [i] * 7 + [vp, vp, vp, sz, vp]
+            L.la_forward_retention.restype = i
+            L.la_retention_backward_workspace_bytes.argtypes = [i] * 6
+            L.la_retention_backward_workspace_bytes.restype = sz
+            L.la_backward_retention.argtypes = [vp] * 8 + [i] * 7 + [vp, vp, vp, vp, sz, vp]
+            L.la_backward_retention.restype = i
+            L.la_decode_step_retention.argtypes = [vp] * 7 + [i] * 5 + [vp]
+            L.la_decode_step_retention.restype = i
             _lib = L
     return _lib
 
@@ -936,3 +948,110 @@ def norm_rotate_backward(grad_q_out, grad_k_out, q, k, freq=None, positions=None
                                        _current_stream(dev))
     _raise(st, "la_norm_rotate_backward")
     return yq, yk, gwq, gwk
+
+
+# ---- retention -----------------------------------------------------------------
+@functools.lru_cache(maxsize=1024)
+def _retention_bytes(device_index, *sizes):   # the split depends on the current device
+    return int(lib().la_retention_workspace_bytes(*sizes))
+
+
+@functools.lru_cache(maxsize=1024)
+def _retention_backward_bytes(device_index, *sizes):
+    return int(lib().la_retention_backward_workspace_bytes(*sizes))
+
+
+def _retention_inputs(q, k, v, gamma, layout):
+    """Checks the inputs of a retention call: its sizes (B, H, N, d, dv, dtype code), the device's index and the
+    inputs' addresses."""
+    if layout not in LAYOUT:
+        raise ValueError(f"layout must be one of {sorted(LAYOUT)}")
+    shape, vs = q.shape, v.shape
+    if len(shape) != 4 or len(vs) != 4:
+        raise ValueError("q, k and v must have four dimensions")
+    B, H, N, d = shape if layout == "bhnd" else (shape[0], shape[2], shape[1], shape[3])
+    dev, dt = q.get_device(), q.dtype
+    at = (_expect("q", q, shape, dt, dev), _expect("k", k, shape, dt, dev),
+          _expect("v", v, (*shape[:3], vs[3]), dt, dev), _expect("gamma", gamma, (H,), torch.float32, dev))
+    return (B, H, N, d, vs[3], _dtype_code(q)), dev, at
+
+
+def forward_retention(q, k, v, gamma, S_in=None, return_state=False, out=None, S_out=None, layout="bhnd",
+                      workspace=None, check_status=False, stream=None):
+    """Retention, causal: S_t = gamma_h S_{t-1} + k_t v_t^T, y_t = S_t^T q_t.
+
+    q, k: [B,H,N,d]; v: [B,H,N,dv] (bf16 or fp32; ``layout="bnhd"``: [B,N,H,...]); gamma: float32 [H],
+    in [0, 1].  Returns y in v's shape and dtype (and the final state [B,H,d,dv], float32, when
+    ``return_state``).  S_in: the initial state; S_out may be S_in.  Unlike ``forward_causal_decay`` there is
+    no feature map and no denominator.
+    """
+    if stream is not None or not q.is_cuda or q.get_device() != _current_device():
+        return _elsewhere(forward_retention, stream, q, k, v, gamma, S_in, return_state, out, S_out, layout, workspace,
+                          check_status)
+    sizes, dev, (qa, ka, va, ga) = _retention_inputs(q, k, v, gamma, layout)
+    B, H, N, d, dv, dt = sizes
+    state = (B, H, d, dv)
+    if out is None:
+        out = torch.empty_like(v)
+    if return_state and S_out is None:
+        S_out = torch.empty(state, dtype=torch.float32, device=q.device)
+    need = _retention_bytes(dev, *sizes)
+    workspace, wa, wbytes = _workspace(workspace, need, q)
+    st = lib().la_forward_retention(qa, ka, va, _expect("out", out, v.shape, v.dtype, dev), ga, *sizes,
+                                    LAYOUT[layout], _expect("S_in", S_in, state, torch.float32, dev),
+                                    _expect("S_out", S_out, state, torch.float32, dev), wa, wbytes,
+                                    _current_stream(dev))
+    _raise(st, "la_forward_retention")
+    if check_status:
+        _check_run_time(workspace, need, "la_forward_retention")
+    return (out, S_out) if return_state else out
+
+
+def backward_retention(q, k, v, gamma, dy, S_in=None, grad_S_out=None, layout="bhnd", workspace=None,
+                       check_status=False, stream=None):
+    """Gradients of ``forward_retention`` for dy = dL/dy (dtype and shape of v) and grad_S_out = dL/dS of the final
+    state (None: zero): (grad_q, grad_k, grad_v, grad_S_in), the first three in the inputs' dtype, the last
+    float32, None unless S_in or grad_S_out is given."""
+    if stream is not None or not q.is_cuda or q.get_device() != _current_device():
+        return _elsewhere(backward_retention, stream, q, k, v, gamma, dy, S_in, grad_S_out, layout, workspace,
+                          check_status)
+    sizes, dev, (qa, ka, va, ga) = _retention_inputs(q, k, v, gamma, layout)
+    B, H, N, d, dv, dt = sizes
+    state = (B, H, d, dv)
+    gq, gk, gv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+    gS = None
+    if S_in is not None or grad_S_out is not None:
+        gS = torch.empty(state, dtype=torch.float32, device=q.device)
+    need = _retention_backward_bytes(dev, *sizes)
+    workspace, wa, wbytes = _workspace(workspace, need, q)
+    st = lib().la_backward_retention(qa, ka, va, _expect("dy", dy, v.shape, v.dtype, dev), ga, gq.data_ptr(),
+                                     gk.data_ptr(), gv.data_ptr(), *sizes, LAYOUT[layout],
+                                     _expect("S_in", S_in, state, torch.float32, dev),
+                                     _expect("grad_S_out", grad_S_out, state, torch.float32, dev), _addr(gS), wa,
+                                     wbytes, _current_stream(dev))
+    _raise(st, "la_backward_retention")
+    if check_status:
+        _check_run_time(workspace, need, "la_backward_retention")
+    return gq, gk, gv, gS
+
+
+def decode_step_retention(q, k, v, gamma, S, S_out=None, out=None, stream=None):
+    """One token of ``forward_retention``: q, k [B,H,d]; v [B,H,dv]; gamma [H] float32; S [B,H,d,dv] float32,
+    updated in place unless ``S_out`` is given.  Returns y [B,H,dv] in v's dtype."""
+    if stream is not None or not q.is_cuda or q.get_device() != _current_device():
+        return _elsewhere(decode_step_retention, stream, q, k, v, gamma, S, S_out, out)
+    shape, vs = q.shape, v.shape
+    if len(shape) != 3 or len(vs) != 3:
+        raise ValueError("q, k and v must have three dimensions")
+    B, H, d = shape
+    dv, dev, dt, f32 = vs[2], q.get_device(), q.dtype, torch.float32
+    if out is None:
+        out = torch.empty_like(v)
+    sa = _expect("S", S, (B, H, d, dv), f32, dev)
+    st = lib().la_decode_step_retention(_expect("q", q, shape, dt, dev), _expect("k", k, shape, dt, dev),
+                                        _expect("v", v, (B, H, dv), dt, dev), _expect("out", out, vs, dt, dev),
+                                        _expect("gamma", gamma, (H,), f32, dev), sa,
+                                        sa if S_out is None else _expect("S_out", S_out, (B, H, d, dv), f32, dev),
+                                        B, H, d, dv, _dtype_code(q), _current_stream(dev))
+    _raise(st, "la_decode_step_retention")
+    return out
