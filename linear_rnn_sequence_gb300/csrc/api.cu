@@ -955,15 +955,20 @@ RetainArgs retain_args(const void *q, const void *k, const void *v, void *y, con
     return a;
 }
 
-// Any call of these sizes: with a final state or without.
+bool retain_on_tensor_cores(const RetainArgs &a) { return retain_tc_supported(a); }
+
+// Of the forward or the gradients: with a final state or without, and for both shapes of the state.
 size_t retain_ws_bytes(int B, int H, int N, int d, int dv, la_dtype dt) {
     if (check_delta(B, H, H, N, d, dv, dt) != LA_OK || N == 0) return 0;
     float some;
-    return sizeof(WsHeader) + retain_simt_workspace(retain_args(nullptr, nullptr, nullptr, nullptr, nullptr, B, H, N, d, dv, dt,
-                                                                LA_LAYOUT_BHND, nullptr, &some, false, false, nullptr, nullptr));
+    const RetainArgs a = retain_args(nullptr, nullptr, nullptr, nullptr, nullptr, B, H, N, d, dv, dt, LA_LAYOUT_BHND,
+                                     nullptr, &some, false, false, nullptr, nullptr);
+    return sizeof(WsHeader) + (retain_on_tensor_cores(a) ? retain_tc_workspace(a) : retain_simt_workspace(a));
 }
 
-cudaError_t launch_retain(const RetainArgs &a) { return launch_retain_simt(a); }
+cudaError_t launch_retain(const RetainArgs &a) {
+    return retain_on_tensor_cores(a) ? launch_retain_tc(a) : launch_retain_simt(a);
+}
 
 }  // namespace
 }  // namespace la

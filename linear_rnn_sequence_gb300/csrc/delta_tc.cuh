@@ -236,15 +236,15 @@ __device__ __forceinline__ void mma_rows(uint32_t leader, uint32_t d, uint32_t a
 }
 
 // Map over a token tensor of `heads` heads of width w: (feature, token, head, batch), boxes of 64
-// features x 64 tokens.
-bool encode_tokens(CUtensorMap *m, const void *base, int layout, int B, int heads, int N, int w) {
+// features x `rows` tokens.
+bool encode_tokens(CUtensorMap *m, const void *base, int layout, int B, int heads, int N, int w, int rows = kDC) {
     EncodeTiledFn fn = encode_fn();
     if (!fn) return false;
     const cuuint64_t tok = layout == LA_LAYOUT_BNHD ? (cuuint64_t)heads * w : w;
     const cuuint64_t hd = layout == LA_LAYOUT_BNHD ? w : (cuuint64_t)N * w;
     const cuuint64_t dims[4] = {(cuuint64_t)w, (cuuint64_t)N, (cuuint64_t)heads, (cuuint64_t)B};
     const cuuint64_t strides[3] = {2 * tok, 2 * hd, 2 * (cuuint64_t)heads * N * w};
-    const cuuint32_t box[4] = {64, kDC, 1, 1}, es[4] = {1, 1, 1, 1};
+    const cuuint32_t box[4] = {64, (cuuint32_t)rows, 1, 1}, es[4] = {1, 1, 1, 1};
     return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base), dims, strides, box, es,
               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;

@@ -239,5 +239,12 @@ cudaError_t launch_norm_rotate_grad(const NormRotateArgs &a);
 size_t retain_simt_workspace(const RetainArgs &a);
 cudaError_t launch_retain_simt(const RetainArgs &a);
 cudaError_t launch_retain_step(const RetainArgs &a);
+// Sums of `blocks` blocks of `tokens` tokens a head, [head][block][d][dv], become the states before the blocks;
+// a.S_out too.
+cudaError_t launch_retain_scan(const RetainArgs &a, float *states, int blocks, int tokens);
+// tensor cores (bf16, d and dv in {64, 128})
+bool retain_tc_supported(const RetainArgs &a);
+size_t retain_tc_workspace(const RetainArgs &a);   // depends on the current device's SM count
+cudaError_t launch_retain_tc(const RetainArgs &a);
 
 }  // namespace la

@@ -23,6 +23,7 @@ struct RetainSimt {
     const float *gamma, *S_in;
     float *S_out, *states;    // states: [head][block][d][dv]
     int H, N, layout, nblk;
+    int tokens;               // of a block of the scan
     bool rev, trans;
 };
 
@@ -109,7 +110,7 @@ __global__ void __launch_bounds__(kRThr) retain_sums_kernel(const RetainSimt p) 
 __global__ void __launch_bounds__(kScanThr) retain_scan_kernel(const RetainSimt p, int D, int DV) {
     const int st = D * DV, parts = st / 4 / kScanThr;
     const int bh = blockIdx.x / parts, at = (blockIdx.x % parts * kScanThr + threadIdx.x) * 4;
-    const float g = p.gamma[bh % p.H], whole = gamma_power(g, kRC), last = gamma_power(g, p.N - (p.nblk - 1) * kRC);
+    const float g = p.gamma[bh % p.H], whole = gamma_power(g, p.tokens), last = gamma_power(g, p.N - (p.nblk - 1) * p.tokens);
     float4 *s = reinterpret_cast<float4 *>(p.states + (size_t)bh * p.nblk * st + at);
     const int step = st / 4;
     // of a state's values in their order here; a transposed state's lie DV apart
@@ -263,7 +264,7 @@ template <int D, int DV, typename T> cudaError_t launch_t(const RetainArgs &a) {
         e = cudaFuncSetAttribute(retain_sums_kernel<D, DV, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
         retain_sums_kernel<D, DV, T><<<blocks, kRThr, smem, a.stream>>>(p);
-        retain_scan_kernel<<<BH * (D * DV / 4 / kScanThr), kScanThr, 0, a.stream>>>(p, D, DV);
+        if ((e = launch_retain_scan(a, p.states, p.nblk, kRC)) != cudaSuccess) return e;
     }
     constexpr int smem = OutLay<D, DV, T>::bytes;
     e = cudaFuncSetAttribute(retain_out_kernel<D, DV, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
@@ -292,6 +293,13 @@ template <typename T> cudaError_t launch(const RetainArgs &a) {
 
 size_t retain_simt_workspace(const RetainArgs &a) {
     return needs_states(a) ? (size_t)a.B * a.H * blocks_of(a.N) * a.d * a.dv * 4 : 0;
+}
+cudaError_t launch_retain_scan(const RetainArgs &a, float *states, int blocks, int tokens) {
+    RetainSimt p{};
+    p.gamma = a.gamma; p.S_in = a.S_in; p.S_out = a.S_out; p.states = states;
+    p.H = a.H; p.N = a.N; p.nblk = blocks; p.tokens = tokens; p.rev = a.rev; p.trans = a.trans;
+    retain_scan_kernel<<<(unsigned)a.B * a.H * (a.d * a.dv / 4 / kScanThr), kScanThr, 0, a.stream>>>(p, a.d, a.dv);
+    return cudaGetLastError();
 }
 cudaError_t launch_retain_simt(const RetainArgs &a) {
     return a.dt == LA_DTYPE_BF16 ? launch<__nv_bfloat16>(a) : launch<float>(a);

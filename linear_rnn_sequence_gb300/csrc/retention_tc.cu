@@ -1,0 +1,617 @@
+// retention_tc.cu -- retention on the tensor cores (bf16 inputs, d and dv in {64, 128}): blocks of C = 128
+// tokens, one CTA a head (or a segment of one).
+//
+//   scores  P  = Q K^T                        (128 x 128, K = d)
+//   masked  P~ = gamma^|i-j| P                (bf16, over P in TMEM)
+//   y          = gamma^(i+1) (Q S) + P~ V     (one accumulator: scaled between the two products)
+//   state   S' = gamma^C S + K^T W,           W_j = gamma^(C-1-j) v_j
+// and the same with the exponents of retention.cuh from behind (REV).
+//
+// Only Q S waits for the state, and only by an elementwise step after the block's K^T W: all products of a block but that
+// one can run ahead, so the tensor pipe goes from one to the next while warps work on what they need:
+//   warps 0-3    a row (token) a thread: P~ from P; the scaling of Q S; then y, through shared memory (where the
+//                block's Q was) and a tensor copy;
+//   warps 4-11   W into TMEM as (K^T W)^T's left operand; the state, its columns (of dv) as TMEM lanes, d/2 of each in a
+//                thread's registers; S^T in bf16 to shared memory for Q S;
+//   warp 12      issues copies and MMAs.
+// The MMAs of a block: Q K^T, Q S, the first half of K^T W (64 of d), P~ V, the second half, over the first's
+// accumulator.
+//
+// Precision: the state is float32 in registers, and what is added to it is exact but for the accumulator's float32: W is
+// rounded to float32 once and enters as three bf16 pieces that add up to it (the top, middle and low 8 bits), against
+// bf16 K, small pieces first.  y is rounded to bf16; of what only y depends on, each score and each value of
+// the state that it meets is rounded to bf16 once, to nearest.  These roundings are independent of y's own and of each
+// other: the error is sqrt(2) times that of y's rounding alone.  A second piece of either would cost an eighth more MMAs
+// and, for the state, shared memory that is not there.
+//
+// What is not finite reaches no token before its own: masked scores are zeros, and a value of v that is not finite would
+// make 0 * inf of them.  So the warps that make W look at every v; where one is not finite (a block in which this is so
+// takes a second look), it becomes zero in shared memory, and y NaN from its token on, for its column.
+#include "delta_tc.cuh"
+#include "retention.cuh"
+
+namespace la {
+namespace {
+
+constexpr int kTC = 128;                      // tokens of a block
+constexpr int kState = 256, kRetThr = 13 * 32;   // threads: of the state's warps, all
+constexpr int kBarY = 1, kBarState = 2;
+
+// TMEM columns: P (P~ over its first half), y, half of K^T W, three pieces of W.
+constexpr uint32_t kColP = 0, kColY = 128, kColKV = 256, kColW3 = 320;
+
+struct RetainTc {
+    const float *gamma, *S_in;
+    float *S_out;            // kWhole: the final state, from the last segment taken; kSums: by (head, segment)
+    int H, N, nblk, nseg, seg_blocks;
+    int seg0, segs;          // segments of a head that are launched: seg0 ..
+    bool trans;              // S_in and S_out are [dv][d]
+    unsigned int *err, *err_where;
+    unsigned long long limit_ns;
+    int drop_item;
+};
+
+struct RetainSmall {
+    uint64_t q_full[2], k_full[2], v_full[2], q_free, qk_done, p_ready, s_ready, y_free, qs_done, y_scaled, pv_done, w_ready,
+        kv_done[2], kv_read, drain;
+    float pw[kTC + 4];       // powers of gamma
+    alignas(16) float near[16];          // gamma^(15 - j) (REV: gamma^j)
+    int v_bad[2];            // block index + 1 of a block with a value that is not finite
+    uint8_t first[2][kTC];   // then, by column: how many tokens come before its first one (REV: up to its last one)
+    uint32_t tmem_base;
+    volatile int abort_flag;
+};
+
+template <int D, int DV> struct RetainLay {
+    static constexpr int kQ = (D / 64) * 16384, kV = (DV / 64) * 16384, kS = DV * D * 2;
+    static constexpr bool ownY = DV > D;      // y does not fit where Q was
+    static constexpr int oQ = 0, oK = oQ + 2 * kQ, oV = oK + 2 * kQ, oS = oV + 2 * kV, oY = oS + kS,
+                         oSmall = oY + (ownY ? kV : 0);
+    static constexpr int request = oSmall + (int)sizeof(RetainSmall) + 1024;
+};
+
+enum RetainMode { kWhole, kSums };   // y from each segment's state; each segment's own sum
+
+__device__ __forceinline__ uint8_t *retain_smem() {
+    extern __shared__ uint8_t smem_raw[];
+    return smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+}
+
+template <int D, int DV, bool REV, int MODE>
+__global__ void __launch_bounds__(kRetThr, 1)
+retain_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
+                 const __grid_constant__ CUtensorMap vmap, const __grid_constant__ CUtensorMap ymap, const RetainTc p) {
+    using Lay = RetainLay<D, DV>;
+    constexpr bool OUT = MODE == kWhole;
+    constexpr int NH = D / 64;   // halves of K^T W
+    uint8_t *sm = retain_smem();
+    RetainSmall &S = *reinterpret_cast<RetainSmall *>(sm + Lay::oSmall);
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+    const int bh = blockIdx.x / p.segs, seg = p.seg0 + blockIdx.x % p.segs, b = bh / p.H, h = bh - b * p.H;
+    const int first_blk = seg * p.seg_blocks, nch = min(p.seg_blocks, p.nblk - first_blk);
+    const float gamma = p.gamma[h];
+    // the n-th block taken, and its tokens
+    auto token_of = [&](int n) { return (first_blk + (REV ? nch - 1 - n : n)) * kTC; };
+    auto length_of = [&](int n) { return min(kTC, p.N - token_of(n)); };
+
+    if (tid == 0) {
+        S.abort_flag = 0;
+        S.v_bad[0] = S.v_bad[1] = 0;
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&S.q_full[i], 1);
+            mbar_init(&S.k_full[i], 1);
+            mbar_init(&S.v_full[i], 1);
+            mbar_init(&S.kv_done[i], 1);
+        }
+        mbar_init(&S.q_free, 1);
+        mbar_init(&S.qk_done, 1);
+        mbar_init(&S.p_ready, 128);
+        mbar_init(&S.s_ready, kState);
+        mbar_init(&S.y_free, 128);
+        mbar_init(&S.qs_done, 1);
+        mbar_init(&S.y_scaled, 128);
+        mbar_init(&S.pv_done, 1);
+        mbar_init(&S.w_ready, kState);
+        mbar_init(&S.kv_read, kState / 2);
+        mbar_init(&S.drain, 1);
+        fence_mbar_init();
+        prefetch_tmap(&kmap);
+        prefetch_tmap(&vmap);
+        if (OUT) prefetch_tmap(&qmap);
+    }
+    if (tid >= 64 && tid <= 64 + kTC) S.pw[tid - 64] = gamma_power(gamma, tid - 64);
+    if (tid >= 256 && tid < 272) S.near[tid - 256] = gamma_power(gamma, REV ? tid - 256 : 271 - tid);
+    if (warp == 12) {
+        tmem_alloc(&S.tmem_base, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tb = __shfl_sync(0xffffffffu, S.tmem_base, 0);
+    const Guard g{&S.abort_flag, p.err, p.err_where, p.limit_ns};
+    const int wq = warp & 3, row = wq * 32 + lane;
+    const uint32_t lb = (uint32_t)(wq * 32) << 16;
+    uint8_t *sQ = sm + Lay::oQ, *sK = sm + Lay::oK, *sV = sm + Lay::oV, *sS = sm + Lay::oS;
+
+    if (warp == 12) {
+        // ------------------------------------------------------------ copies and MMAs
+        constexpr uint32_t iP = idesc_bf16(128, kTC, 0, 0), iQS = idesc_bf16(128, DV, 0, 0),
+                           iKV = idesc_bf16(128, 64, 0, 1), iPV = idesc_bf16(128, DV, 0, 1);
+        int q_issued = 0, k_issued = 0, v_issued = 0;   // kept by the elected lane
+        auto load = [&](uint8_t *dst, const CUtensorMap &m, uint64_t *bar, int slabs, int n, bool drop) {
+            mbar_arrive_expect_tx(bar, slabs * 16384);
+            if (drop) return;   // test hook: announced, never issued
+            for (int f = 0; f < slabs; ++f) tma_load_4d(dst + f * 16384, &m, bar, f * 64, token_of(n), h, b);
+        };
+        auto load_q = [&](int n) { load(sQ + (n & 1) * Lay::kQ, qmap, &S.q_full[n & 1], D / 64, n, false); ++q_issued; };
+        auto load_k = [&](int n) {
+            load(sK + (n & 1) * Lay::kQ, kmap, &S.k_full[n & 1], D / 64, n, n == 0 && (int)blockIdx.x == p.drop_item);
+            ++k_issued;
+        };
+        auto load_v = [&](int n) { load(sV + (n & 1) * Lay::kV, vmap, &S.v_full[n & 1], DV / 64, n, false); ++v_issued; };
+        auto prefetch = [&](int n) {
+            for (int f = 0; f < D / 64; ++f) {
+                if (OUT) tma_prefetch_4d(&qmap, f * 64, token_of(n), h, b);
+                tma_prefetch_4d(&kmap, f * 64, token_of(n), h, b);
+            }
+            for (int f = 0; f < DV / 64; ++f) tma_prefetch_4d(&vmap, f * 64, token_of(n), h, b);
+        };
+        if (elect_leader()) {   // always the same lane: it keeps the counts
+            for (int n = 0; n < 2 && n < nch; ++n) {
+                if (OUT) load_q(n);
+                load_k(n);
+                load_v(n);
+            }
+            if (nch > 2) prefetch(2);
+        }
+        __syncwarp();
+        bool ok = true;
+        auto all = [&](bool x) { ok = ok && __all_sync(0xffffffffu, x); };
+        auto kv_half = [&](int n, int half) {   // (K^T W)^T, 64 columns of d
+            const uint32_t leader = elect_leader();
+            tc_fence_after();
+            const uint64_t kd = smem_desc(smem_u32(sK) + (n & 1) * Lay::kQ + half * 16384, 16384, 1024, kSwizzle128B);
+#pragma unroll 1
+            for (int pc = 2; pc >= 0; --pc)
+#pragma unroll
+                for (int ks = 0; ks < kTC / 16; ++ks)
+                    mma_ts_if(leader, tb + kColKV, tb + kColW3 + pc * 64 + ks * 8, kd + ks * 128, iKV, pc < 2 || ks > 0);
+            mma_commit_if(leader, &S.kv_done[half]);
+        };
+        for (int n = 0; n < nch; ++n) {
+            const int s = n & 1, ph = (n >> 1) & 1;
+            all(mbar_wait<1>(&S.k_full[s], ph, g, 1));
+            if (OUT) all(mbar_wait<1>(&S.q_full[s], ph, g, 2));
+            if (!ok) break;
+            if (OUT) {
+                const uint32_t leader = elect_leader();
+                tc_fence_after();
+                const uint64_t qd = desc_k(smem_u32(sQ) + s * Lay::kQ), kd = desc_k(smem_u32(sK) + s * Lay::kQ);
+#pragma unroll
+                for (int ks = 0; ks < D / 16; ++ks) {
+                    const uint32_t o = ((ks >> 2) * 16384 + (ks & 3) * 32) >> 4;
+                    mma_ss_if(leader, tb + kColP, qd + o, kd + o, iP, ks > 0);
+                }
+                mma_commit_if(leader, &S.qk_done);
+            }
+            if (n >= 1) {   // the places of the block before the last are free
+                all(mbar_wait<1>(&S.kv_done[NH - 1], (n - 1) & 1, g, 3));
+                if (OUT) all(mbar_wait<1>(&S.pv_done, (n - 1) & 1, g, 4));
+                if (!ok) break;
+                if (n + 1 < nch && elect_leader()) {
+                    load_k(n + 1);
+                    load_v(n + 1);
+                    if (n + 2 < nch) prefetch(n + 2);
+                }
+                __syncwarp();
+            }
+            if (OUT) {
+                all(mbar_wait<1>(&S.s_ready, n & 1, g, 5));
+                if (n >= 1) all(mbar_wait<1>(&S.y_free, (n - 1) & 1, g, 6));
+                if (!ok) break;
+                const uint32_t leader = elect_leader();
+                tc_fence_after();
+                const uint64_t qd = desc_k(smem_u32(sQ) + s * Lay::kQ), sd = desc_k(smem_u32(sS));
+#pragma unroll
+                for (int ks = 0; ks < D / 16; ++ks)
+                    mma_ss_if(leader, tb + kColY, qd + (uint32_t)(((ks >> 2) * 16384 + (ks & 3) * 32) >> 4),
+                              sd + (uint32_t)(((ks >> 2) * DV * 128 + (ks & 3) * 32) >> 4), iQS, ks > 0);
+                mma_commit_if(leader, &S.qs_done);
+            }
+            all(mbar_wait<1>(&S.w_ready, n & 1, g, 7));
+            if (!ok) break;
+            kv_half(n, 0);
+            if (OUT) {
+                if (n >= 1 && n + 1 < nch) {
+                    all(mbar_wait<1>(&S.q_free, (n - 1) & 1, g, 8));
+                    if (!ok) break;
+                    if (elect_leader()) load_q(n + 1);
+                    __syncwarp();
+                }
+                all(mbar_wait<1>(&S.p_ready, n & 1, g, 9));
+                all(mbar_wait<1>(&S.y_scaled, n & 1, g, 10));
+                if (!ok) break;
+                const uint32_t leader = elect_leader();
+                tc_fence_after();
+                const uint64_t vd = smem_desc(smem_u32(sV) + s * Lay::kV, 16384, 1024, kSwizzle128B);
+#pragma unroll
+                for (int ks = 0; ks < kTC / 16; ++ks)
+                    mma_ts_if(leader, tb + kColY, tb + kColP + ks * 8, vd + ks * 128, iPV, 1);
+                mma_commit_if(leader, &S.pv_done);
+            }
+            if (NH == 2) {
+                all(mbar_wait<1>(&S.kv_read, n & 1, g, 11));
+                if (!ok) break;
+                kv_half(n, 1);
+            }
+        }
+        if (elect_leader()) {
+            mma_commit(&S.drain);
+            drain_wait(&S.drain, 0, g.limit_ns);
+            if (!ok) {   // let the copies in flight land
+                for (int n = max(0, q_issued - 2); n < q_issued; ++n) drain_wait(&S.q_full[n & 1], (n >> 1) & 1, g.limit_ns);
+                for (int n = max(0, k_issued - 2); n < k_issued; ++n)
+                    if (!(n == 0 && (int)blockIdx.x == p.drop_item)) drain_wait(&S.k_full[n & 1], (n >> 1) & 1, g.limit_ns);
+                for (int n = max(0, v_issued - 2); n < v_issued; ++n) drain_wait(&S.v_full[n & 1], (n >> 1) & 1, g.limit_ns);
+            }
+        }
+        __syncwarp();
+    } else if (warp >= 4) {
+        // ------------------------------------------------------------ W and the state
+        constexpr int SC = D / 2;   // state values of a thread: column `row` of dv, half * SC .. of d
+        const int half = (warp - 4) >> 2;
+        const bool live = row < DV;   // warp-uniform
+        float st[SC];
+        if (live && p.S_in) {
+            const float *src = p.S_in + (size_t)(p.nseg > 1 ? bh * p.nseg + seg : bh) * D * DV;
+            if (p.trans) {
+#pragma unroll
+                for (int i = 0; i < SC; i += 4)
+                    *reinterpret_cast<float4 *>(st + i) = *reinterpret_cast<const float4 *>(src + (size_t)row * D + half * SC + i);
+            } else {
+#pragma unroll
+                for (int i = 0; i < SC; ++i) st[i] = src[(size_t)(half * SC + i) * DV + row];
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < SC; ++i) st[i] = 0.f;
+        }
+        auto put_state = [&] {   // S^T in bf16, rows of d
+            if (live) {
+#pragma unroll
+                for (int i = 0; i < SC; i += 8) {
+                    const int c = half * SC + i;
+                    *reinterpret_cast<uint4 *>(sS + (c >> 6) * (DV * 128) + sw128_off(row, c & 63)) =
+                        make_uint4(pack_bf16x2(st[i], st[i + 1]), pack_bf16x2(st[i + 2], st[i + 3]),
+                                   pack_bf16x2(st[i + 4], st[i + 5]), pack_bf16x2(st[i + 6], st[i + 7]));
+                }
+                fence_proxy_async();
+            }
+            mbar_arrive(&S.s_ready);
+        };
+        if (OUT) put_state();
+        bool failed = false;
+        for (int n = 0; n < nch; ++n) {
+            const int L = length_of(n);
+            uint8_t *tv = sV + (n & 1) * Lay::kV;
+            bool ok = mbar_wait<1>(&S.v_full[n & 1], (n >> 1) & 1, g, 20);
+            if (n >= 1) ok = ok && mbar_wait<1>(&S.kv_done[NH - 1], (n - 1) & 1, g, 21);   // W's place is free
+            ok = __all_sync(0xffffffffu, ok);
+            if (ok && live) {
+                tc_fence_after();
+                uint32_t z = 0;   // 0 v: anything else where v is not finite
+                const int tq = (lane & 3) * 2;
+#pragma unroll 1
+                for (int u = 0; u < 2; ++u) {   // 32 tokens
+                    const int t0 = half * 64 + u * 32;
+                    float w[8];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const int j = t0 + (k >> 1) * 8 + tq + (k & 1);
+                        w[k] = S.pw[max(0, key_exp(REV, j, L))];   // behind the last token: of zeros
+                    }
+#pragma unroll
+                    for (int hl = 0; hl < 2; ++hl) {   // 16 columns of dv
+                        uint32_t x[8], hi[8], mi[8], lo[8];
+                        const int c = wq * 4 + hl * 2 + ((lane >> 3) & 1);   // 16-byte chunk of a token's row
+                        const int t = t0 + (lane >> 4) * 8 + (lane & 7);
+                        const uint32_t at = smem_u32(tv) + (c >> 3) * 16384 + t * 128 + (((c & 7) ^ (t & 7)) << 4);
+                        ldmatrix_x4_trans(at, x[0], x[1], x[2], x[3]);
+                        ldmatrix_x4_trans(at + 16 * 128, x[4], x[5], x[6], x[7]);
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {   // tokens 8 (k / 2) + tq and + 1, column lane / 4 + 8 (k % 2)
+                            z = fma_bf16x2(x[k], 0u, z);
+                            float a, bb;
+                            f2unpack(f2mul(f2pack(w[k & 6], w[(k & 6) + 1]), f2pack(bf16_lo_f(x[k]), bf16_hi_f(x[k]))), a, bb);
+                            split3(a, bb, hi[k], mi[k], lo[k]);
+                        }
+                        const uint32_t to = tb + lb + ((uint32_t)hl << 20) + kColW3 + t0 / 2;
+                        tmem_st_16x128b_x4(to, hi);
+                        tmem_st_16x128b_x4(to + 64, mi);
+                        tmem_st_16x128b_x4(to + 128, lo);
+                    }
+                }
+                if (OUT && (z & 0x7FFF7FFFu)) S.v_bad[n & 1] = n + 1;
+                tmem_wait_st();
+                tc_fence_before();
+            }
+            if ((failed = __any_sync(0xffffffffu, group_any<kBarState, kState>(!ok)) != 0)) break;
+            if (OUT && *(volatile int *)&S.v_bad[n & 1] == n + 1) {
+                if (live && half == 0) {
+                    uint8_t *col = tv + (row >> 6) * 16384 + (row & 7) * 2;
+                    int f = REV ? 0 : kTC;
+                    for (int t = 0; t < kTC; ++t) {
+                        uint16_t *v = reinterpret_cast<uint16_t *>(col + t * 128 + ((((row & 63) >> 3) ^ (t & 7)) << 4));
+                        if ((*v & 0x7F80) == 0x7F80) {
+                            *v = 0;
+                            f = REV ? t + 1 : min(f, t);
+                        }
+                    }
+                    S.first[n & 1][row] = (uint8_t)f;
+                    fence_proxy_async();
+                }
+            }
+            mbar_arrive(&S.w_ready);
+            // ---- S' = gamma^L S + K^T W
+            ok = mbar_wait<1>(&S.kv_done[NH == 2 ? half : 0], n & 1, g, 22);
+            ok = __all_sync(0xffffffffu, ok);
+            if (ok && live) {
+                tc_fence_after();
+                const float gl = S.pw[L];
+                const uint64_t g2 = f2pack(gl, gl);
+#pragma unroll
+                for (int i = 0; i < SC; i += 32) {
+                    uint32_t a0[16], a1[16];
+                    const uint32_t from = tb + lb + kColKV + (NH == 2 ? 0 : half * SC) + i;
+                    tmem_ld16(from, a0);
+                    tmem_ld16(from + 16, a1);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int j = 0; j < 16; j += 2) {
+                        f2unpack(f2fma(g2, f2pack(st[i + j], st[i + j + 1]), f2pack(u2f(a0[j]), u2f(a0[j + 1]))), st[i + j],
+                                 st[i + j + 1]);
+                        f2unpack(f2fma(g2, f2pack(st[i + 16 + j], st[i + 17 + j]), f2pack(u2f(a1[j]), u2f(a1[j + 1]))),
+                                 st[i + 16 + j], st[i + 17 + j]);
+                    }
+                }
+                tc_fence_before();
+            }
+            if (NH == 2 && half == 0) mbar_arrive(&S.kv_read);
+            if (OUT && n + 1 < nch) put_state();   // Q S came before K^T W: its operand has been read
+            // a wait that ran out shows in the next block's, or at the end
+            failed = !ok;
+        }
+        failed = __any_sync(0xffffffffu, group_any<kBarState, kState>(failed)) != 0;
+        const bool last = seg == (REV ? 0 : p.nseg - 1);
+        float *dst = OUT ? (p.S_out && last ? p.S_out + (size_t)bh * D * DV : nullptr)
+                         : p.S_out + ((size_t)bh * p.nseg + seg) * D * DV;
+        if (!failed && live && dst) {
+            if (OUT && p.trans) {
+#pragma unroll
+                for (int i = 0; i < SC; i += 4)
+                    *reinterpret_cast<float4 *>(dst + (size_t)row * D + half * SC + i) = make_float4(st[i], st[i + 1], st[i + 2], st[i + 3]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < SC; ++i) dst[(size_t)(half * SC + i) * DV + row] = st[i];
+            }
+        }
+    } else if (OUT) {
+        // ------------------------------------------------------------ P~ and y
+        const uint32_t pcol = tb + lb + kColP, col = tb + lb + kColY;
+        const bool stores = tid == 0;
+        float nr[16];
+        load16(S.near, nr);
+        for (int n = 0; n < nch; ++n) {
+            bool ok = __all_sync(0xffffffffu, mbar_wait<1>(&S.qk_done, n & 1, g, 30));
+            if (ok) {
+                tc_fence_after();
+#pragma unroll 1
+                for (int j0 = 0; j0 < kTC; j0 += 16) {   // over P itself: columns j0 / 2 .. of a row that has been read that far
+                    const int side = j0 - 32 * wq;
+                    uint32_t o[8];
+                    if (REV ? side < 0 : side >= 32) {   // warp-uniform: beyond the diagonal
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) o[j] = 0u;
+                    } else {
+                        uint32_t x[16];
+                        tmem_ld16(pcol + j0, x);
+                        if (side < 0 || side >= 32) {   // gamma^|i - j| = gamma^(to the block's nearest column) near[j]
+                            const float f = S.pw[REV ? j0 - row : row - j0 - 15];
+                            const uint64_t f2 = f2pack(f, f);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) {
+                                float a, bb;
+                                f2unpack(f2mul(f2mul(f2, f2pack(nr[2 * j], nr[2 * j + 1])), f2pack(u2f(x[2 * j]), u2f(x[2 * j + 1]))), a, bb);
+                                o[j] = pack_bf16x2(a, bb);
+                            }
+                        } else {
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) {
+                                const int e0 = REV ? j0 + 2 * j - row : row - j0 - 2 * j, e1 = REV ? e0 + 1 : e0 - 1;
+                                const float a = e0 >= 0 ? S.pw[max(e0, 0)] * u2f(x[2 * j]) : 0.f;
+                                const float bb = e1 >= 0 ? S.pw[max(e1, 0)] * u2f(x[2 * j + 1]) : 0.f;
+                                o[j] = pack_bf16x2(a, bb);
+                            }
+                        }
+                    }
+                    tmem_st8(pcol + j0 / 2, o);
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                mbar_arrive(&S.p_ready);
+            }
+            const int L = length_of(n);
+            ok = ok && __all_sync(0xffffffffu, mbar_wait<1>(&S.qs_done, n & 1, g, 40));
+            if (ok) {
+                tc_fence_after();
+                const float f = S.pw[max(0, inter_exp(REV, row, L))];   // behind the last token: of zeros
+                const uint64_t f2 = f2pack(f, f);
+#pragma unroll 1
+                for (int c = 0; c < DV; c += 32) {
+                    uint32_t a[16], e[16];
+                    tmem_ld16(col + c, a);
+                    tmem_ld16(col + c + 16, e);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int j = 0; j < 16; j += 2) {
+                        float u, v;
+                        f2unpack(f2mul(f2, f2pack(u2f(a[j]), u2f(a[j + 1]))), u, v);
+                        a[j] = f2u(u);
+                        a[j + 1] = f2u(v);
+                        f2unpack(f2mul(f2, f2pack(u2f(e[j]), u2f(e[j + 1]))), u, v);
+                        e[j] = f2u(u);
+                        e[j + 1] = f2u(v);
+                    }
+                    tmem_st16(col + c, a);
+                    tmem_st16(col + c + 16, e);
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                mbar_arrive(&S.y_scaled);
+                ok = __all_sync(0xffffffffu, mbar_wait<1>(&S.pv_done, n & 1, g, 41));
+            }
+            uint8_t *sY = Lay::ownY ? sm + Lay::oY : sQ + (n & 1) * Lay::kQ;   // Q has been read
+            if (Lay::ownY) {   // the last y has left its tile (its copy was waited for below)
+                if (__any_sync(0xffffffffu, group_any<kBarY, 128>(!ok))) break;
+            }
+            if (ok) {
+                tc_fence_after();
+                const bool bad = *(volatile int *)&S.v_bad[n & 1] == n + 1;
+#pragma unroll 1
+                for (int c = 0; c < DV; c += 32) {
+                    uint32_t a[16], e[16], o[16];
+                    tmem_ld16(col + c, a);
+                    tmem_ld16(col + c + 16, e);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        o[j] = pack_bf16x2(u2f(a[2 * j]), u2f(a[2 * j + 1]));
+                        o[8 + j] = pack_bf16x2(u2f(e[2 * j]), u2f(e[2 * j + 1]));
+                    }
+                    if (bad) {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) {
+                            const int f = S.first[n & 1][c + j];
+                            if (REV ? row < f : row >= f) o[j >> 1] |= j & 1 ? 0x7FFF0000u : 0x7FFFu;
+                        }
+                    }
+#pragma unroll
+                    for (int j = 0; j < 16; j += 4)
+                        *reinterpret_cast<uint4 *>(sY + ((c + 2 * j) >> 6) * 16384 + sw128_off(row, (c + 2 * j) & 63)) =
+                            make_uint4(o[j], o[j + 1], o[j + 2], o[j + 3]);
+                }
+                tc_fence_before();
+                mbar_arrive(&S.y_free);
+                fence_proxy_async();
+            }
+            if (__any_sync(0xffffffffu, group_any<kBarY, 128>(!ok))) break;
+            if (stores) {
+#pragma unroll
+                for (int f = 0; f < DV / 64; ++f) tma_store_4d(&ymap, sY + f * 16384, f * 64, token_of(n), h, b);
+                bulk_commit();
+                bulk_wait_read<0>();
+                mbar_arrive(&S.q_free);
+            }
+            __syncwarp();
+        }
+        if (stores) bulk_wait<0>();
+        __syncwarp();
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 12) {
+        tc_fence_after();
+        tmem_dealloc(tb, 512);
+    }
+}
+
+// Segments of a head.  Splitting pays where the heads leave SMs idle: the segments' own sums come first (a block of
+// them costs about 0.6 of a whole one), their ends are joined, and every segment runs from its state.  In units of a
+// block's time, about 2.3 us: a wave of CTAs takes its segments' length, the extra launches and starts about 6.
+void retain_segments(const RetainArgs &a, int &nseg, int &seg_blocks) {
+    const int nblk = (a.N + kTC - 1) / kTC, sms = num_sms();
+    const long long BH = (long long)a.B * a.H;
+    auto waves = [&](long long ctas) { return (double)((ctas + sms - 1) / sms); };
+    nseg = 1;
+    seg_blocks = nblk;
+    if (BH >= sms) return;
+    double best = waves(BH) * nblk;
+    for (int s = 2; s <= 64 && s <= nblk; ++s) {
+        const int len = (nblk + s - 1) / s, n = (nblk + len - 1) / len;
+        if (n != s) continue;
+        const double cost = 1.6 * waves(BH * s) * len + 6;
+        if (cost < best) {
+            best = cost;
+            nseg = s;
+            seg_blocks = len;
+        }
+    }
+}
+
+template <int D, int DV, bool REV, int MODE> cudaError_t launch_mode(const RetainArgs &a, const RetainTc &p) {
+    CUtensorMap qm{}, km, vm, ym{};
+    if (!encode_tokens(&km, a.k, a.layout, a.B, a.H, a.N, D, kTC) || !encode_tokens(&vm, a.v, a.layout, a.B, a.H, a.N, DV, kTC) ||
+        (MODE == kWhole && (!encode_tokens(&qm, a.q, a.layout, a.B, a.H, a.N, D, kTC) ||
+                          !encode_tokens(&ym, a.y, a.layout, a.B, a.H, a.N, DV, kTC))))
+        return cudaErrorInvalidValue;
+    auto kern = retain_tc_kernel<D, DV, REV, MODE>;
+    constexpr int smem = RetainLay<D, DV>::request;
+    static_assert(smem <= 232448, "shared memory of a CTA");
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    kern<<<a.B * a.H * p.segs, kRetThr, smem, a.stream>>>(qm, km, vm, ym, p);
+    return cudaGetLastError();
+}
+
+template <int D, int DV, bool REV> cudaError_t launch_tc(const RetainArgs &a) {
+    RetainTc p{};
+    p.gamma = a.gamma; p.H = a.H; p.N = a.N; p.nblk = (a.N + kTC - 1) / kTC;
+    retain_segments(a, p.nseg, p.seg_blocks);
+    WsHeader *hdr = static_cast<WsHeader *>(a.ws);
+    p.err = &hdr->error;
+    p.err_where = &hdr->error_where;
+    const long long lim = debug_fault().wait_limit_ns;
+    p.limit_ns = lim > 0 ? (unsigned long long)lim : 1000000000ull;
+    p.drop_item = debug_fault().drop_load_item;
+    if (p.nseg > 1) {   // the segments' sums; the last one taken is needed for the final state only
+        float *states = reinterpret_cast<float *>(static_cast<char *>(a.ws) + sizeof(WsHeader));
+        RetainTc s = p;
+        s.S_out = states;
+        s.segs = p.nseg - (a.S_out ? 0 : 1);
+        s.seg0 = REV ? p.nseg - s.segs : 0;
+        cudaError_t e = launch_mode<D, DV, REV, kSums>(a, s);
+        if (e == cudaSuccess) e = launch_retain_scan(a, states, p.nseg, p.seg_blocks * kTC);
+        if (e != cudaSuccess) return e;
+        p.S_in = states;
+    } else {
+        p.S_in = a.S_in;
+        p.S_out = a.S_out;
+        p.trans = a.trans;
+    }
+    p.segs = p.nseg;
+    return launch_mode<D, DV, REV, kWhole>(a, p);
+}
+template <int D, int DV> cudaError_t launch_way(const RetainArgs &a) {
+    return a.rev ? launch_tc<D, DV, true>(a) : launch_tc<D, DV, false>(a);
+}
+
+}  // namespace
+
+bool retain_tc_supported(const RetainArgs &a) {
+    return a.dt == LA_DTYPE_BF16 && (a.d == 64 || a.d == 128) && (a.dv == 64 || a.dv == 128);
+}
+// header | (split sequences) the segments' sums, then states
+size_t retain_tc_workspace(const RetainArgs &a) {
+    int nseg, len;
+    retain_segments(a, nseg, len);
+    return nseg > 1 ? (size_t)a.B * a.H * nseg * a.d * a.dv * 4 : 0;
+}
+cudaError_t launch_retain_tc(const RetainArgs &a) {
+    if (a.d == 64) return a.dv == 64 ? launch_way<64, 64>(a) : launch_way<64, 128>(a);
+    return a.dv == 64 ? launch_way<128, 64>(a) : launch_way<128, 128>(a);
+}
+
+}  // namespace la
