@@ -7,15 +7,17 @@
 //   state   S' = gamma^C S + K^T W,           W_j = gamma^(C-1-j) v_j
 // and the same with the exponents of retention.cuh from behind (REV).
 //
-// Only Q S waits for the state, and only by an elementwise step after the block's K^T W: all products of a block but that
-// one can run ahead, so the tensor pipe goes from one to the next while warps work on what they need:
+// The products that make the state do not wait for what is made of it, and a block's scores are ready before its turn, so
+// the tensor pipe goes from one product to the next while warps work on what they need:
 //   warps 0-3    a row (token) a thread: P~ from P; the scaling of Q S; then y, through shared memory (where the
 //                block's Q was) and a tensor copy;
 //   warps 4-11   W into TMEM as (K^T W)^T's left operand; the state, its columns (of dv) as TMEM lanes, d/2 of each in a
 //                thread's registers; S^T in bf16 to shared memory for Q S;
-//   warp 12      issues copies and MMAs.
-// The MMAs of a block: Q K^T, Q S, the first half of K^T W (64 of d), P~ V, the second half, over the first's
-// accumulator.
+//   warp 12      issues the MMAs: of a block the first half of K^T W (64 of d), Q S, the second half over the first's
+//                accumulator (d = 64: there is one), P~ V, then the next block's Q K^T;
+//   warp 13      issues the copies.
+// W is the one operand without a second place in TMEM: its three pieces, the halves of K^T W and the state's update
+// between them are the chain that bounds a block.
 //
 // Precision: the state is float32 in registers, and what is added to it is exact but for the accumulator's float32: W is
 // rounded to float32 once and enters as three bf16 pieces that add up to it (the top, middle and low 8 bits), against
@@ -25,8 +27,8 @@
 // and, for the state, shared memory that is not there.
 //
 // What is not finite reaches no token before its own: masked scores are zeros, and a value of v that is not finite would
-// make 0 * inf of them.  So the warps that make W look at every v; where one is not finite (a block in which this is so
-// takes a second look), it becomes zero in shared memory, and y NaN from its token on, for its column.
+// make 0 * inf of them.  So the warps that make W look at every v; in a block with one that is not finite, these become zero in
+// shared memory, and y NaN from the first's token on, for its column.
 #include "delta_tc.cuh"
 #include "retention.cuh"
 
@@ -34,8 +36,7 @@ namespace la {
 namespace {
 
 constexpr int kTC = 128;                      // tokens of a block
-constexpr int kState = 256, kRetThr = 13 * 32;   // threads: of the state's warps, all
-constexpr int kBarY = 1, kBarState = 2;
+constexpr int kState = 256, kRetThr = 14 * 32;   // threads: of the state's warps, all
 
 // TMEM columns: P (P~ over its first half), y, half of K^T W, three pieces of W.
 constexpr uint32_t kColP = 0, kColY = 128, kColKV = 256, kColW3 = 320;
@@ -52,12 +53,12 @@ struct RetainTc {
 };
 
 struct RetainSmall {
-    uint64_t q_full[2], k_full[2], v_full[2], q_free, qk_done, p_ready, s_ready, y_free, qs_done, y_scaled, pv_done, w_ready,
-        kv_done[2], kv_read, drain;
-    float pw[kTC + 4];       // powers of gamma
-    alignas(16) float near[16];          // gamma^(15 - j) (REV: gamma^j)
-    int v_bad[2];            // block index + 1 of a block with a value that is not finite
-    uint8_t first[2][kTC];   // then, by column: how many tokens come before its first one (REV: up to its last one)
+    uint64_t q_full[2], k_full[2], v_full[2], pv_done[2], y_written[2], kv_done[2], kv_read, qk_done, p_ready, s_ready,
+        qs_done, y_scaled, y_free, w_ready, drain;
+    float pg[2 * kTC + 4];        // pg[kTC - n] = gamma^n, zeros behind
+    alignas(16) float near[16];   // gamma^(15 - j) (REV: gamma^j)
+    int v_bad[2];                 // block index + 1 of a block with a value that is not finite
+    uint8_t first[2][kTC];        // then, by column: how many tokens come before its first one (REV: up to its last one)
     uint32_t tmem_base;
     volatile int abort_flag;
 };
@@ -66,7 +67,7 @@ template <int D, int DV> struct RetainLay {
     static constexpr int kQ = (D / 64) * 16384, kV = (DV / 64) * 16384, kS = DV * D * 2;
     static constexpr bool ownY = DV > D;      // y does not fit where Q was
     static constexpr int oQ = 0, oK = oQ + 2 * kQ, oV = oK + 2 * kQ, oS = oV + 2 * kV, oY = oS + kS,
-                         oSmall = oY + (ownY ? kV : 0);
+                         oSmall = oY + (ownY ? 2 * kV : 0);
     static constexpr int request = oSmall + (int)sizeof(RetainSmall) + 1024;
 };
 
@@ -101,26 +102,26 @@ retain_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
             mbar_init(&S.q_full[i], 1);
             mbar_init(&S.k_full[i], 1);
             mbar_init(&S.v_full[i], 1);
+            mbar_init(&S.pv_done[i], 1);
+            mbar_init(&S.y_written[i], 128);
             mbar_init(&S.kv_done[i], 1);
         }
-        mbar_init(&S.q_free, 1);
+        mbar_init(&S.kv_read, kState / 2);
         mbar_init(&S.qk_done, 1);
         mbar_init(&S.p_ready, 128);
         mbar_init(&S.s_ready, kState);
-        mbar_init(&S.y_free, 128);
         mbar_init(&S.qs_done, 1);
         mbar_init(&S.y_scaled, 128);
-        mbar_init(&S.pv_done, 1);
+        mbar_init(&S.y_free, 128);
         mbar_init(&S.w_ready, kState);
-        mbar_init(&S.kv_read, kState / 2);
         mbar_init(&S.drain, 1);
         fence_mbar_init();
         prefetch_tmap(&kmap);
         prefetch_tmap(&vmap);
         if (OUT) prefetch_tmap(&qmap);
     }
-    if (tid >= 64 && tid <= 64 + kTC) S.pw[tid - 64] = gamma_power(gamma, tid - 64);
-    if (tid >= 256 && tid < 272) S.near[tid - 256] = gamma_power(gamma, REV ? tid - 256 : 271 - tid);
+    if (tid >= 64 && tid <= 64 + 2 * kTC) S.pg[tid - 64] = tid <= 64 + kTC ? gamma_power(gamma, 64 + kTC - tid) : 0.f;
+    if (tid >= 32 && tid < 48) S.near[tid - 32] = gamma_power(gamma, REV ? tid - 32 : 47 - tid);
     if (warp == 12) {
         tmem_alloc(&S.tmem_base, 512);
         tmem_relinquish();
@@ -132,40 +133,70 @@ retain_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
     const Guard g{&S.abort_flag, p.err, p.err_where, p.limit_ns};
     const int wq = warp & 3, row = wq * 32 + lane;
     const uint32_t lb = (uint32_t)(wq * 32) << 16;
+    const float *pw = S.pg + kTC;   // pw[-n] = gamma^n
     uint8_t *sQ = sm + Lay::oQ, *sK = sm + Lay::oK, *sV = sm + Lay::oV, *sS = sm + Lay::oS;
+    auto y_tile = [&](int n) { return Lay::ownY ? sm + Lay::oY + (n & 1) * Lay::kV : sQ + (n & 1) * Lay::kQ; };
 
-    if (warp == 12) {
-        // ------------------------------------------------------------ copies and MMAs
-        constexpr uint32_t iP = idesc_bf16(128, kTC, 0, 0), iQS = idesc_bf16(128, DV, 0, 0),
-                           iKV = idesc_bf16(128, 64, 0, 1), iPV = idesc_bf16(128, DV, 0, 1);
-        int q_issued = 0, k_issued = 0, v_issued = 0;   // kept by the elected lane
-        auto load = [&](uint8_t *dst, const CUtensorMap &m, uint64_t *bar, int slabs, int n, bool drop) {
-            mbar_arrive_expect_tx(bar, slabs * 16384);
-            if (drop) return;   // test hook: announced, never issued
-            for (int f = 0; f < slabs; ++f) tma_load_4d(dst + f * 16384, &m, bar, f * 64, token_of(n), h, b);
-        };
-        auto load_q = [&](int n) { load(sQ + (n & 1) * Lay::kQ, qmap, &S.q_full[n & 1], D / 64, n, false); ++q_issued; };
-        auto load_k = [&](int n) {
-            load(sK + (n & 1) * Lay::kQ, kmap, &S.k_full[n & 1], D / 64, n, n == 0 && (int)blockIdx.x == p.drop_item);
-            ++k_issued;
-        };
-        auto load_v = [&](int n) { load(sV + (n & 1) * Lay::kV, vmap, &S.v_full[n & 1], DV / 64, n, false); ++v_issued; };
-        auto prefetch = [&](int n) {
-            for (int f = 0; f < D / 64; ++f) {
-                if (OUT) tma_prefetch_4d(&qmap, f * 64, token_of(n), h, b);
-                tma_prefetch_4d(&kmap, f * 64, token_of(n), h, b);
+    if (warp == 13) {
+        // ------------------------------------------------------------ copies
+        if (elect_leader()) {
+            auto load = [&](uint8_t *dst, const CUtensorMap &m, uint64_t *bar, int slabs, int n, bool drop) {
+                mbar_arrive_expect_tx(bar, slabs * 16384);
+                if (drop) return;   // test hook: announced, never issued
+                for (int f = 0; f < slabs; ++f) tma_load_4d(dst + f * 16384, &m, bar, f * 64, token_of(n), h, b);
+            };
+            auto store = [&](int n) {   // y of a block, when it is written
+                if (!mbar_wait<1>(&S.y_written[n & 1], (n >> 1) & 1, g, 1)) return false;
+#pragma unroll
+                for (int f = 0; f < DV / 64; ++f) tma_store_4d(&ymap, y_tile(n) + f * 16384, f * 64, token_of(n), h, b);
+                bulk_commit();
+                return true;
+            };
+            int n = 0;
+            bool q_too = true;   // of block n - 1
+            for (; n < nch; ++n) {
+                const int s = n & 1, ph = (n >> 1) & 1;
+                // the block before the last has been used: its last product is P~ V
+                if (n >= 2 && !mbar_wait<1>(&S.pv_done[s], ph ^ 1, g, 2)) break;
+                load(sK + s * Lay::kQ, kmap, &S.k_full[s], D / 64, n, n == 0 && (int)blockIdx.x == p.drop_item);
+                load(sV + s * Lay::kV, vmap, &S.v_full[s], DV / 64, n, false);
+                if (n >= 1 && n + 1 < nch) {   // the next one into L2, while its places are still taken
+                    for (int f = 0; f < D / 64; ++f) {
+                        tma_prefetch_4d(&kmap, f * 64, token_of(n + 1), h, b);
+                        if (OUT) tma_prefetch_4d(&qmap, f * 64, token_of(n + 1), h, b);
+                    }
+                    for (int f = 0; f < DV / 64; ++f) tma_prefetch_4d(&vmap, f * 64, token_of(n + 1), h, b);
+                }
+                if (OUT) {
+                    if (n >= 2) {
+                        if (!store(n - 2)) {
+                            q_too = false;
+                            ++n;
+                            break;
+                        }
+                        bulk_wait_read<0>();   // its tile (or, where y has its own, also the one before) is free
+                    }
+                    load(sQ + s * Lay::kQ, qmap, &S.q_full[s], D / 64, n, false);
+                }
             }
-            for (int f = 0; f < DV / 64; ++f) tma_prefetch_4d(&vmap, f * 64, token_of(n), h, b);
-        };
-        if (elect_leader()) {   // always the same lane: it keeps the counts
-            for (int n = 0; n < 2 && n < nch; ++n) {
-                if (OUT) load_q(n);
-                load_k(n);
-                load_v(n);
+            if (OUT) {
+                if (n == nch && q_too)
+                    for (int m = max(0, nch - 2); m < nch; ++m)
+                        if (!store(m)) break;
+                bulk_wait<0>();
             }
-            if (nch > 2) prefetch(2);
+            // what is in flight lands (after a wait that ran out; otherwise it has been used)
+            for (int m = max(0, n - 2); m < n; ++m) {
+                if (!(m == 0 && (int)blockIdx.x == p.drop_item)) drain_wait(&S.k_full[m & 1], (m >> 1) & 1, g.limit_ns);
+                drain_wait(&S.v_full[m & 1], (m >> 1) & 1, g.limit_ns);
+                if (OUT && (q_too || m < n - 1)) drain_wait(&S.q_full[m & 1], (m >> 1) & 1, g.limit_ns);
+            }
         }
         __syncwarp();
+    } else if (warp == 12) {
+        // ------------------------------------------------------------ MMAs
+        constexpr uint32_t iP = idesc_bf16(128, kTC, 0, 0), iQS = idesc_bf16(128, DV, 0, 0),
+                           iKV = idesc_bf16(128, 64, 0, 1), iPV = idesc_bf16(128, DV, 0, 1);
         bool ok = true;
         auto all = [&](bool x) { ok = ok && __all_sync(0xffffffffu, x); };
         auto kv_half = [&](int n, int half) {   // (K^T W)^T, 64 columns of d
@@ -179,36 +210,49 @@ retain_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
                     mma_ts_if(leader, tb + kColKV, tb + kColW3 + pc * 64 + ks * 8, kd + ks * 128, iKV, pc < 2 || ks > 0);
             mma_commit_if(leader, &S.kv_done[half]);
         };
-        for (int n = 0; n < nch; ++n) {
+        auto scores = [&](int n) {
             const int s = n & 1, ph = (n >> 1) & 1;
-            all(mbar_wait<1>(&S.k_full[s], ph, g, 1));
-            if (OUT) all(mbar_wait<1>(&S.q_full[s], ph, g, 2));
-            if (!ok) break;
-            if (OUT) {
-                const uint32_t leader = elect_leader();
-                tc_fence_after();
-                const uint64_t qd = desc_k(smem_u32(sQ) + s * Lay::kQ), kd = desc_k(smem_u32(sK) + s * Lay::kQ);
+            all(mbar_wait<1>(&S.k_full[s], ph, g, 3));
+            all(mbar_wait<1>(&S.q_full[s], ph, g, 4));
+            if (!ok) return;
+            const uint32_t leader = elect_leader();
+            tc_fence_after();
+            const uint64_t qd = desc_k(smem_u32(sQ) + s * Lay::kQ), kd = desc_k(smem_u32(sK) + s * Lay::kQ);
 #pragma unroll
-                for (int ks = 0; ks < D / 16; ++ks) {
-                    const uint32_t o = ((ks >> 2) * 16384 + (ks & 3) * 32) >> 4;
-                    mma_ss_if(leader, tb + kColP, qd + o, kd + o, iP, ks > 0);
-                }
-                mma_commit_if(leader, &S.qk_done);
+            for (int ks = 0; ks < D / 16; ++ks) {
+                const uint32_t o = ((ks >> 2) * 16384 + (ks & 3) * 32) >> 4;
+                mma_ss_if(leader, tb + kColP, qd + o, kd + o, iP, ks > 0);
             }
-            if (n >= 1) {   // the places of the block before the last are free
-                all(mbar_wait<1>(&S.kv_done[NH - 1], (n - 1) & 1, g, 3));
-                if (OUT) all(mbar_wait<1>(&S.pv_done, (n - 1) & 1, g, 4));
-                if (!ok) break;
-                if (n + 1 < nch && elect_leader()) {
-                    load_k(n + 1);
-                    load_v(n + 1);
-                    if (n + 2 < nch) prefetch(n + 2);
+            mma_commit_if(leader, &S.qk_done);
+        };
+        // A block with a value of v that is not finite: zero in shared memory, and where the columns' first ones are.
+        auto mend_v = [&](int n) {
+            for (int c = lane; c < DV; c += 32) {
+                uint8_t *col = sV + (n & 1) * Lay::kV + (c >> 6) * 16384 + (c & 7) * 2;
+                int f = REV ? 0 : kTC;
+                for (int t = 0; t < kTC; ++t) {
+                    uint16_t *v = reinterpret_cast<uint16_t *>(col + t * 128 + ((((c & 63) >> 3) ^ (t & 7)) << 4));
+                    if ((*v & 0x7F80) == 0x7F80) {
+                        *v = 0;
+                        f = REV ? t + 1 : min(f, t);
+                    }
                 }
-                __syncwarp();
+                S.first[n & 1][c] = (uint8_t)f;
             }
+            fence_proxy_async();
+            __syncwarp();
+        };
+        if (OUT) scores(0);
+        for (int n = 0; n < nch && ok; ++n) {
+            const int s = n & 1;
+            if (!OUT) all(mbar_wait<1>(&S.k_full[s], (n >> 1) & 1, g, 3));
+            all(mbar_wait<1>(&S.w_ready, n & 1, g, 5));
+            if (!ok) break;
+            if (OUT && *(volatile int *)&S.v_bad[s] == n + 1) mend_v(n);
+            kv_half(n, 0);
             if (OUT) {
-                all(mbar_wait<1>(&S.s_ready, n & 1, g, 5));
-                if (n >= 1) all(mbar_wait<1>(&S.y_free, (n - 1) & 1, g, 6));
+                all(mbar_wait<1>(&S.s_ready, n & 1, g, 6));
+                if (n >= 1) all(mbar_wait<1>(&S.y_free, (n - 1) & 1, g, 7));
                 if (!ok) break;
                 const uint32_t leader = elect_leader();
                 tc_fence_after();
@@ -219,16 +263,12 @@ retain_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
                               sd + (uint32_t)(((ks >> 2) * DV * 128 + (ks & 3) * 32) >> 4), iQS, ks > 0);
                 mma_commit_if(leader, &S.qs_done);
             }
-            all(mbar_wait<1>(&S.w_ready, n & 1, g, 7));
-            if (!ok) break;
-            kv_half(n, 0);
+            if (NH == 2) {
+                all(mbar_wait<1>(&S.kv_read, n & 1, g, 8));
+                if (!ok) break;
+                kv_half(n, 1);
+            }
             if (OUT) {
-                if (n >= 1 && n + 1 < nch) {
-                    all(mbar_wait<1>(&S.q_free, (n - 1) & 1, g, 8));
-                    if (!ok) break;
-                    if (elect_leader()) load_q(n + 1);
-                    __syncwarp();
-                }
                 all(mbar_wait<1>(&S.p_ready, n & 1, g, 9));
                 all(mbar_wait<1>(&S.y_scaled, n & 1, g, 10));
                 if (!ok) break;
@@ -238,23 +278,16 @@ retain_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
 #pragma unroll
                 for (int ks = 0; ks < kTC / 16; ++ks)
                     mma_ts_if(leader, tb + kColY, tb + kColP + ks * 8, vd + ks * 128, iPV, 1);
-                mma_commit_if(leader, &S.pv_done);
-            }
-            if (NH == 2) {
-                all(mbar_wait<1>(&S.kv_read, n & 1, g, 11));
-                if (!ok) break;
-                kv_half(n, 1);
+                mma_commit_if(leader, &S.pv_done[s]);
+                if (n + 1 < nch) scores(n + 1);
+            } else {
+                const uint32_t leader = elect_leader();
+                mma_commit_if(leader, &S.pv_done[s]);
             }
         }
         if (elect_leader()) {
             mma_commit(&S.drain);
             drain_wait(&S.drain, 0, g.limit_ns);
-            if (!ok) {   // let the copies in flight land
-                for (int n = max(0, q_issued - 2); n < q_issued; ++n) drain_wait(&S.q_full[n & 1], (n >> 1) & 1, g.limit_ns);
-                for (int n = max(0, k_issued - 2); n < k_issued; ++n)
-                    if (!(n == 0 && (int)blockIdx.x == p.drop_item)) drain_wait(&S.k_full[n & 1], (n >> 1) & 1, g.limit_ns);
-                for (int n = max(0, v_issued - 2); n < v_issued; ++n) drain_wait(&S.v_full[n & 1], (n >> 1) & 1, g.limit_ns);
-            }
         }
         __syncwarp();
     } else if (warp >= 4) {
@@ -290,27 +323,26 @@ retain_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
             }
             mbar_arrive(&S.s_ready);
         };
-        if (OUT) put_state();
-        bool failed = false;
+        bool ok = true;
         for (int n = 0; n < nch; ++n) {
             const int L = length_of(n);
-            uint8_t *tv = sV + (n & 1) * Lay::kV;
-            bool ok = mbar_wait<1>(&S.v_full[n & 1], (n >> 1) & 1, g, 20);
-            if (n >= 1) ok = ok && mbar_wait<1>(&S.kv_done[NH - 1], (n - 1) & 1, g, 21);   // W's place is free
-            ok = __all_sync(0xffffffffu, ok);
-            if (ok && live) {
+            ok = ok && mbar_wait<1>(&S.v_full[n & 1], (n >> 1) & 1, g, 20);
+            // W's place is free (where this has not been waited for below)
+            if (n >= 1 && NH == 2 && half == 0) ok = ok && mbar_wait<1>(&S.kv_done[1], (n - 1) & 1, g, 21);
+            if (!(ok = __all_sync(0xffffffffu, ok))) break;
+            if (live) {
                 tc_fence_after();
-                uint32_t z = 0;   // 0 v: anything else where v is not finite
+                const uint8_t *tv = sV + (n & 1) * Lay::kV;
+                uint32_t z0 = 0, z1 = 0;   // 0 v: anything else where v is not finite
                 const int tq = (lane & 3) * 2;
 #pragma unroll 1
                 for (int u = 0; u < 2; ++u) {   // 32 tokens
                     const int t0 = half * 64 + u * 32;
+                    // weights of tokens t0 + 8 g + tq and + 1 (behind the last token zeros, or of zeros)
+                    const float *wp = pw + (REV ? -(t0 + tq + 1) : t0 + tq + 1 - L);
                     float w[8];
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        const int j = t0 + (k >> 1) * 8 + tq + (k & 1);
-                        w[k] = S.pw[max(0, key_exp(REV, j, L))];   // behind the last token: of zeros
-                    }
+                    for (int k = 0; k < 8; ++k) w[k] = wp[(REV ? -1 : 1) * ((k >> 1) * 8 + (k & 1))];
 #pragma unroll
                     for (int hl = 0; hl < 2; ++hl) {   // 16 columns of dv
                         uint32_t x[8], hi[8], mi[8], lo[8];
@@ -321,7 +353,7 @@ retain_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
                         ldmatrix_x4_trans(at + 16 * 128, x[4], x[5], x[6], x[7]);
 #pragma unroll
                         for (int k = 0; k < 8; ++k) {   // tokens 8 (k / 2) + tq and + 1, column lane / 4 + 8 (k % 2)
-                            z = fma_bf16x2(x[k], 0u, z);
+                            (k & 1 ? z1 : z0) = fma_bf16x2(x[k], 0u, k & 1 ? z1 : z0);
                             float a, bb;
                             f2unpack(f2mul(f2pack(w[k & 6], w[(k & 6) + 1]), f2pack(bf16_lo_f(x[k]), bf16_hi_f(x[k]))), a, bb);
                             split3(a, bb, hi[k], mi[k], lo[k]);
@@ -332,33 +364,24 @@ retain_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
                         tmem_st_16x128b_x4(to + 128, lo);
                     }
                 }
-                if (OUT && (z & 0x7FFF7FFFu)) S.v_bad[n & 1] = n + 1;
+                if (OUT && ((z0 | z1) & 0x7FFF7FFFu)) S.v_bad[n & 1] = n + 1;
                 tmem_wait_st();
                 tc_fence_before();
             }
-            if ((failed = __any_sync(0xffffffffu, group_any<kBarState, kState>(!ok)) != 0)) break;
-            if (OUT && *(volatile int *)&S.v_bad[n & 1] == n + 1) {
-                if (live && half == 0) {
-                    uint8_t *col = tv + (row >> 6) * 16384 + (row & 7) * 2;
-                    int f = REV ? 0 : kTC;
-                    for (int t = 0; t < kTC; ++t) {
-                        uint16_t *v = reinterpret_cast<uint16_t *>(col + t * 128 + ((((row & 63) >> 3) ^ (t & 7)) << 4));
-                        if ((*v & 0x7F80) == 0x7F80) {
-                            *v = 0;
-                            f = REV ? t + 1 : min(f, t);
-                        }
-                    }
-                    S.first[n & 1][row] = (uint8_t)f;
-                    fence_proxy_async();
-                }
-            }
             mbar_arrive(&S.w_ready);
+            if (OUT) {
+                if (NH == 1 && n >= 1) {   // Q S of the block before has read its operand (else K^T W's end says so)
+                    ok = __all_sync(0xffffffffu, mbar_wait<1>(&S.qs_done, (n - 1) & 1, g, 22));
+                    if (!ok) break;
+                }
+                put_state();
+            }
             // ---- S' = gamma^L S + K^T W
-            ok = mbar_wait<1>(&S.kv_done[NH == 2 ? half : 0], n & 1, g, 22);
-            ok = __all_sync(0xffffffffu, ok);
-            if (ok && live) {
+            ok = __all_sync(0xffffffffu, mbar_wait<1>(&S.kv_done[NH == 2 ? half : 0], n & 1, g, 23));
+            if (!ok) break;
+            if (live) {
                 tc_fence_after();
-                const float gl = S.pw[L];
+                const float gl = pw[-L];
                 const uint64_t g2 = f2pack(gl, gl);
 #pragma unroll
                 for (int i = 0; i < SC; i += 32) {
@@ -378,15 +401,11 @@ retain_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
                 tc_fence_before();
             }
             if (NH == 2 && half == 0) mbar_arrive(&S.kv_read);
-            if (OUT && n + 1 < nch) put_state();   // Q S came before K^T W: its operand has been read
-            // a wait that ran out shows in the next block's, or at the end
-            failed = !ok;
         }
-        failed = __any_sync(0xffffffffu, group_any<kBarState, kState>(failed)) != 0;
         const bool last = seg == (REV ? 0 : p.nseg - 1);
         float *dst = OUT ? (p.S_out && last ? p.S_out + (size_t)bh * D * DV : nullptr)
                          : p.S_out + ((size_t)bh * p.nseg + seg) * D * DV;
-        if (!failed && live && dst) {
+        if (ok && live && dst) {
             if (OUT && p.trans) {
 #pragma unroll
                 for (int i = 0; i < SC; i += 4)
@@ -399,126 +418,115 @@ retain_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
     } else if (OUT) {
         // ------------------------------------------------------------ P~ and y
         const uint32_t pcol = tb + lb + kColP, col = tb + lb + kColY;
-        const bool stores = tid == 0;
         float nr[16];
         load16(S.near, nr);
         for (int n = 0; n < nch; ++n) {
-            bool ok = __all_sync(0xffffffffu, mbar_wait<1>(&S.qk_done, n & 1, g, 30));
-            if (ok) {
+            if (!__all_sync(0xffffffffu, mbar_wait<1>(&S.qk_done, n & 1, g, 30))) break;
+            {
                 tc_fence_after();
 #pragma unroll 1
-                for (int j0 = 0; j0 < kTC; j0 += 16) {   // over P itself: columns j0 / 2 .. of a row that has been read that far
-                    const int side = j0 - 32 * wq;
-                    uint32_t o[8];
-                    if (REV ? side < 0 : side >= 32) {   // warp-uniform: beyond the diagonal
+                for (int jb = 0; jb < kTC; jb += 64) {
+                    // over P itself: columns j / 2 of a row that has been read beyond column j
+                    uint32_t x[4][16];
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) o[j] = 0u;
-                    } else {
-                        uint32_t x[16];
-                        tmem_ld16(pcol + j0, x);
-                        if (side < 0 || side >= 32) {   // gamma^|i - j| = gamma^(to the block's nearest column) near[j]
-                            const float f = S.pw[REV ? j0 - row : row - j0 - 15];
+                    for (int u = 0; u < 4; ++u) {
+                        const int side = jb + 16 * u - 32 * wq;   // warp-uniform
+                        if (REV ? side >= 0 : side < 32) tmem_ld16(pcol + jb + 16 * u, x[u]);
+                    }
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) {
+                        const int j0 = jb + 16 * u, side = j0 - 32 * wq;
+                        uint32_t o[8];
+                        if (REV ? side < 0 : side >= 32) {   // beyond the diagonal
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) o[j] = 0u;
+                        } else if (side < 0 || side >= 32) {   // gamma^|i - j| = gamma^(to the nearest column) near[j]
+                            const float f = pw[REV ? row - j0 : j0 + 15 - row];
                             const uint64_t f2 = f2pack(f, f);
-                            tmem_wait_ld();
 #pragma unroll
                             for (int j = 0; j < 8; ++j) {
                                 float a, bb;
-                                f2unpack(f2mul(f2mul(f2, f2pack(nr[2 * j], nr[2 * j + 1])), f2pack(u2f(x[2 * j]), u2f(x[2 * j + 1]))), a, bb);
+                                f2unpack(f2mul(f2mul(f2, f2pack(nr[2 * j], nr[2 * j + 1])), f2pack(u2f(x[u][2 * j]), u2f(x[u][2 * j + 1]))), a, bb);
                                 o[j] = pack_bf16x2(a, bb);
                             }
                         } else {
-                            tmem_wait_ld();
 #pragma unroll
                             for (int j = 0; j < 8; ++j) {
                                 const int e0 = REV ? j0 + 2 * j - row : row - j0 - 2 * j, e1 = REV ? e0 + 1 : e0 - 1;
-                                const float a = e0 >= 0 ? S.pw[max(e0, 0)] * u2f(x[2 * j]) : 0.f;
-                                const float bb = e1 >= 0 ? S.pw[max(e1, 0)] * u2f(x[2 * j + 1]) : 0.f;
-                                o[j] = pack_bf16x2(a, bb);
+                                const float a = pw[-max(e0, 0)] * u2f(x[u][2 * j]), bb = pw[-max(e1, 0)] * u2f(x[u][2 * j + 1]);
+                                o[j] = pack_bf16x2(e0 >= 0 ? a : 0.f, e1 >= 0 ? bb : 0.f);
                             }
                         }
+                        tmem_st8(pcol + j0 / 2, o);
                     }
-                    tmem_st8(pcol + j0 / 2, o);
                 }
                 tmem_wait_st();
                 tc_fence_before();
                 mbar_arrive(&S.p_ready);
             }
-            const int L = length_of(n);
-            ok = ok && __all_sync(0xffffffffu, mbar_wait<1>(&S.qs_done, n & 1, g, 40));
-            if (ok) {
+            if (!__all_sync(0xffffffffu, mbar_wait<1>(&S.qs_done, n & 1, g, 31))) break;
+            {
                 tc_fence_after();
-                const float f = S.pw[max(0, inter_exp(REV, row, L))];   // behind the last token: of zeros
+                const float f = pw[-max(0, inter_exp(REV, row, length_of(n)))];   // behind the last token: of zeros
                 const uint64_t f2 = f2pack(f, f);
 #pragma unroll 1
-                for (int c = 0; c < DV; c += 32) {
-                    uint32_t a[16], e[16];
-                    tmem_ld16(col + c, a);
-                    tmem_ld16(col + c + 16, e);
+                for (int c = 0; c < DV; c += 64) {
+                    uint32_t a[4][16];
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) tmem_ld16(col + c + 16 * u, a[u]);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int j = 0; j < 16; j += 2) {
-                        float u, v;
-                        f2unpack(f2mul(f2, f2pack(u2f(a[j]), u2f(a[j + 1]))), u, v);
-                        a[j] = f2u(u);
-                        a[j + 1] = f2u(v);
-                        f2unpack(f2mul(f2, f2pack(u2f(e[j]), u2f(e[j + 1]))), u, v);
-                        e[j] = f2u(u);
-                        e[j + 1] = f2u(v);
+                    for (int u = 0; u < 4; ++u) {
+#pragma unroll
+                        for (int j = 0; j < 16; j += 2) {
+                            float x, y;
+                            f2unpack(f2mul(f2, f2pack(u2f(a[u][j]), u2f(a[u][j + 1]))), x, y);
+                            a[u][j] = f2u(x);
+                            a[u][j + 1] = f2u(y);
+                        }
+                        tmem_st16(col + c + 16 * u, a[u]);
                     }
-                    tmem_st16(col + c, a);
-                    tmem_st16(col + c + 16, e);
                 }
                 tmem_wait_st();
                 tc_fence_before();
                 mbar_arrive(&S.y_scaled);
-                ok = __all_sync(0xffffffffu, mbar_wait<1>(&S.pv_done, n & 1, g, 41));
             }
-            uint8_t *sY = Lay::ownY ? sm + Lay::oY : sQ + (n & 1) * Lay::kQ;   // Q has been read
-            if (Lay::ownY) {   // the last y has left its tile (its copy was waited for below)
-                if (__any_sync(0xffffffffu, group_any<kBarY, 128>(!ok))) break;
-            }
-            if (ok) {
+            if (!__all_sync(0xffffffffu, mbar_wait<1>(&S.pv_done[n & 1], (n >> 1) & 1, g, 32))) break;
+            {
+                uint8_t *sY = y_tile(n);   // where Q was: it has been read (its own place: the copy before the last from there has, before this block's Q came)
                 tc_fence_after();
                 const bool bad = *(volatile int *)&S.v_bad[n & 1] == n + 1;
 #pragma unroll 1
-                for (int c = 0; c < DV; c += 32) {
-                    uint32_t a[16], e[16], o[16];
-                    tmem_ld16(col + c, a);
-                    tmem_ld16(col + c + 16, e);
+                for (int c = 0; c < DV; c += 64) {
+                    uint32_t a[4][16];
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) tmem_ld16(col + c + 16 * u, a[u]);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        o[j] = pack_bf16x2(u2f(a[2 * j]), u2f(a[2 * j + 1]));
-                        o[8 + j] = pack_bf16x2(u2f(e[2 * j]), u2f(e[2 * j + 1]));
-                    }
-                    if (bad) {
+                    for (int u = 0; u < 4; ++u) {
+                        uint32_t o[8];
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) {
-                            const int f = S.first[n & 1][c + j];
-                            if (REV ? row < f : row >= f) o[j >> 1] |= j & 1 ? 0x7FFF0000u : 0x7FFFu;
+                        for (int j = 0; j < 8; ++j) o[j] = pack_bf16x2(u2f(a[u][2 * j]), u2f(a[u][2 * j + 1]));
+                        if (bad) {
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) {
+                                const int f = S.first[n & 1][c + 16 * u + j];
+                                if (REV ? row < f : row >= f) o[j >> 1] |= j & 1 ? 0x7FFF0000u : 0x7FFFu;
+                            }
                         }
-                    }
 #pragma unroll
-                    for (int j = 0; j < 16; j += 4)
-                        *reinterpret_cast<uint4 *>(sY + ((c + 2 * j) >> 6) * 16384 + sw128_off(row, (c + 2 * j) & 63)) =
-                            make_uint4(o[j], o[j + 1], o[j + 2], o[j + 3]);
+                        for (int j = 0; j < 8; j += 4)
+                            *reinterpret_cast<uint4 *>(sY + (c >> 6) * 16384 + sw128_off(row, 16 * u + 2 * j)) =
+                                make_uint4(o[j], o[j + 1], o[j + 2], o[j + 3]);
+                    }
                 }
                 tc_fence_before();
                 mbar_arrive(&S.y_free);
                 fence_proxy_async();
+                mbar_arrive(&S.y_written[n & 1]);
             }
-            if (__any_sync(0xffffffffu, group_any<kBarY, 128>(!ok))) break;
-            if (stores) {
-#pragma unroll
-                for (int f = 0; f < DV / 64; ++f) tma_store_4d(&ymap, sY + f * 16384, f * 64, token_of(n), h, b);
-                bulk_commit();
-                bulk_wait_read<0>();
-                mbar_arrive(&S.q_free);
-            }
-            __syncwarp();
         }
-        if (stores) bulk_wait<0>();
-        __syncwarp();
     }
     tc_fence_before();
     __syncthreads();
