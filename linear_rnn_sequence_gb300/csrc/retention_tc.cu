@@ -27,8 +27,10 @@
 // and, for the state, shared memory that is not there.
 //
 // What is not finite reaches no token before its own: masked scores are zeros, and a value of v that is not finite would
-// make 0 * inf of them.  So the warps that make W look at every v; in a block with one that is not finite, these become zero in
-// shared memory, and y NaN from the first's token on, for its column.
+// make 0 * inf of them.  It also makes its column of K^T W something not finite, which (d = 128) the warps of the state see
+// before P~ V is issued; for d = 64, where P~ V would have to wait for that (142 us became 156 at B8 H16 N8192), the warps that
+// make W look at every v.  In a block with such values these become zero in shared memory, and y NaN from the first's
+// token on, for its column.
 #include "delta_tc.cuh"
 #include "retention.cuh"
 
@@ -70,6 +72,16 @@ template <int D, int DV> struct RetainLay {
                          oSmall = oY + (ownY ? 2 * kV : 0);
     static constexpr int request = oSmall + (int)sizeof(RetainSmall) + 1024;
 };
+
+// Three pieces of a pair by truncation, as split3, at two thirds of its time: the logical operations that take a piece
+// off a value run at half the rate of a multiply-add.
+__device__ __forceinline__ void pieces3(float x0, float x1, uint32_t &h, uint32_t &m, uint32_t &l) {
+    h = __byte_perm(f2u(x0), f2u(x1), 0x7632);
+    x0 = minus_bf16_lo(x0, h);
+    x1 = minus_bf16_hi(x1, h);
+    m = __byte_perm(f2u(x0), f2u(x1), 0x7632);
+    l = __byte_perm(f2u(minus_bf16_lo(x0, m)), f2u(minus_bf16_hi(x1, m)), 0x7632);
+}
 
 enum RetainMode { kWhole, kSums };   // y from each segment's state; each segment's own sum
 
@@ -160,7 +172,9 @@ retain_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
                 if (n >= 2 && !mbar_wait<1>(&S.pv_done[s], ph ^ 1, g, 2)) break;
                 load(sK + s * Lay::kQ, kmap, &S.k_full[s], D / 64, n, n == 0 && (int)blockIdx.x == p.drop_item);
                 load(sV + s * Lay::kV, vmap, &S.v_full[s], DV / 64, n, false);
-                if (n >= 1 && n + 1 < nch) {   // the next one into L2, while its places are still taken
+                // the next one into L2, while its places are still taken (d = 128, B8 H16 N8192: 190 us with and 205 without;
+                // d = 64, whose blocks come in time anyway: 149 and 142)
+                if (D > 64 && n >= 1 && n + 1 < nch) {
                     for (int f = 0; f < D / 64; ++f) {
                         tma_prefetch_4d(&kmap, f * 64, token_of(n + 1), h, b);
                         if (OUT) tma_prefetch_4d(&qmap, f * 64, token_of(n + 1), h, b);
@@ -248,7 +262,6 @@ retain_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
             if (!OUT) all(mbar_wait<1>(&S.k_full[s], (n >> 1) & 1, g, 3));
             all(mbar_wait<1>(&S.w_ready, n & 1, g, 5));
             if (!ok) break;
-            if (OUT && *(volatile int *)&S.v_bad[s] == n + 1) mend_v(n);
             kv_half(n, 0);
             if (OUT) {
                 all(mbar_wait<1>(&S.s_ready, n & 1, g, 6));
@@ -268,6 +281,7 @@ retain_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
                 if (!ok) break;
                 kv_half(n, 1);
             }
+            if (OUT && *(volatile int *)&S.v_bad[s] == n + 1) mend_v(n);
             if (OUT) {
                 all(mbar_wait<1>(&S.p_ready, n & 1, g, 9));
                 all(mbar_wait<1>(&S.y_scaled, n & 1, g, 10));
@@ -353,10 +367,8 @@ retain_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
                         ldmatrix_x4_trans(at + 16 * 128, x[4], x[5], x[6], x[7]);
 #pragma unroll
                         for (int k = 0; k < 8; ++k) {   // tokens 8 (k / 2) + tq and + 1, column lane / 4 + 8 (k % 2)
-                            (k & 1 ? z1 : z0) = fma_bf16x2(x[k], 0u, k & 1 ? z1 : z0);
-                            float a, bb;
-                            f2unpack(f2mul(f2pack(w[k & 6], w[(k & 6) + 1]), f2pack(bf16_lo_f(x[k]), bf16_hi_f(x[k]))), a, bb);
-                            split3(a, bb, hi[k], mi[k], lo[k]);
+                            if (OUT && NH == 1) (k & 1 ? z1 : z0) = fma_bf16x2(x[k], 0u, k & 1 ? z1 : z0);
+                            pieces3(w[k & 6] * bf16_lo_f(x[k]), w[(k & 6) + 1] * bf16_hi_f(x[k]), hi[k], mi[k], lo[k]);
                         }
                         const uint32_t to = tb + lb + ((uint32_t)hl << 20) + kColW3 + t0 / 2;
                         tmem_st_16x128b_x4(to, hi);
@@ -364,7 +376,7 @@ retain_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
                         tmem_st_16x128b_x4(to + 128, lo);
                     }
                 }
-                if (OUT && ((z0 | z1) & 0x7FFF7FFFu)) S.v_bad[n & 1] = n + 1;
+                if (OUT && NH == 1 && ((z0 | z1) & 0x7FFF7FFFu)) S.v_bad[n & 1] = n + 1;
                 tmem_wait_st();
                 tc_fence_before();
             }
@@ -390,6 +402,8 @@ retain_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
                     tmem_ld16(from, a0);
                     tmem_ld16(from + 16, a1);
                     tmem_wait_ld();
+                    // a value of v that is not finite leaves nothing finite here (a value of k may, too)
+                    if (OUT && NH == 2 && i == 0 && half == 0 && !finite(u2f(a0[0]))) S.v_bad[n & 1] = n + 1;
 #pragma unroll
                     for (int j = 0; j < 16; j += 2) {
                         f2unpack(f2fma(g2, f2pack(st[i + j], st[i + j + 1]), f2pack(u2f(a0[j]), u2f(a0[j + 1]))), st[i + j],

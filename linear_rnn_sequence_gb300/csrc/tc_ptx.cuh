@@ -442,6 +442,23 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
 }
 __device__ __forceinline__ float bf16_lo_f(uint32_t p) { return __uint_as_float(p << 16); }
 __device__ __forceinline__ float bf16_hi_f(uint32_t p) { return __uint_as_float(p & 0xFFFF0000u); }
+// x minus the low (high) half of a pair of bf16 values, in one operation on both types.
+__device__ __forceinline__ float minus_bf16_lo(float x, uint32_t p) {
+    float r;
+    asm("{\n\t.reg .b16 lo, hi, n;\n\tmov.b32 {lo, hi}, %1;\n\tmov.b16 n, 0xBF80;\n\t"   // -1
+        "fma.rn.f32.bf16 %0, lo, n, %2;\n\t}"
+        : "=f"(r)
+        : "r"(p), "f"(x));
+    return r;
+}
+__device__ __forceinline__ float minus_bf16_hi(float x, uint32_t p) {
+    float r;
+    asm("{\n\t.reg .b16 lo, hi, n;\n\tmov.b32 {lo, hi}, %1;\n\tmov.b16 n, 0xBF80;\n\t"
+        "fma.rn.f32.bf16 %0, hi, n, %2;\n\t}"
+        : "=f"(r)
+        : "r"(p), "f"(x));
+    return r;
+}
 // 2^x, flushing subnormal results to zero
 __device__ __forceinline__ float ex2_ftz(float x) {
     float r;
