@@ -20,26 +20,24 @@
 namespace la {
 namespace {
 
-constexpr int kRotThreads = 256;
+constexpr int kMostVec = 4;   // values of a chunk: the row's sums and sines over twice as many lanes as with 16-byte chunks of
+                             // bf16, and half the registers of each (gradients 293 us, with chunks of 8 343; forward 189 and 197)
 // A row whose squares sum to more than kRotBig (or to no number) is summed again with its values times kRotDown.
 constexpr float kRotBig = 1e37f, kRotDown = 0x1p-70f;
 
 // VEC values of T as they lie in memory.
 template <typename T, int VEC> struct Chunk;
-template <> struct Chunk<__nv_bfloat16, 8> {
-    using Raw = uint4;
-    static __device__ __forceinline__ Raw zero() { return make_uint4(0u, 0u, 0u, 0u); }
-    static __device__ __forceinline__ void get(const Raw &r, float (&x)[8]) {
-        const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            x[2 * i] = tc::bf16_lo_f(w[i]);
-            x[2 * i + 1] = tc::bf16_hi_f(w[i]);
-        }
+template <> struct Chunk<__nv_bfloat16, 4> {
+    using Raw = uint2;
+    static __device__ __forceinline__ Raw zero() { return make_uint2(0u, 0u); }
+    static __device__ __forceinline__ void get(const Raw &r, float (&x)[4]) {
+        x[0] = tc::bf16_lo_f(r.x);
+        x[1] = tc::bf16_hi_f(r.x);
+        x[2] = tc::bf16_lo_f(r.y);
+        x[3] = tc::bf16_hi_f(r.y);
     }
-    static __device__ __forceinline__ Raw put(const float (&x)[8]) {
-        return make_uint4(tc::pack_bf16x2(x[0], x[1]), tc::pack_bf16x2(x[2], x[3]), tc::pack_bf16x2(x[4], x[5]),
-                          tc::pack_bf16x2(x[6], x[7]));
+    static __device__ __forceinline__ Raw put(const float (&x)[4]) {
+        return make_uint2(tc::pack_bf16x2(x[0], x[1]), tc::pack_bf16x2(x[2], x[3]));
     }
 };
 template <> struct Chunk<__nv_bfloat16, 2> {
@@ -138,7 +136,8 @@ template <int VEC, int CP, bool ADJ> struct Place {
     int a[CP], b[CP];          // offsets of its chunks
     bool live[CP];
     uint64_t turn[CP][VEC];    // of the pairs of both chunks
-    bool ok[CP][VEC], rot[CP][VEC];
+    unsigned rot[CP];          // which of them are rotated (ADJ = false: all or none)
+    unsigned bad[CP];          // and have no angle
     float cs[CP][VEC], sn[CP][VEC];
 
     template <int LPR> __device__ __forceinline__ void init(const RotParams &p, int gl) {
@@ -147,24 +146,26 @@ template <int VEC, int CP, bool ADJ> struct Place {
             const int c = gl + LPR * i;
             live[i] = 2 * c * VEC < p.d;
             chunk_at<VEC, ADJ>(live[i] ? c : 0, p.r, a[i], b[i]);
+            rot[i] = bad[i] = 0;
 #pragma unroll
             for (int t = 0; t < VEC; ++t) {
                 const int pair = ADJ ? a[i] / 2 + t : a[i] + t;   // ADJ: VEC/2 pairs of each chunk, in order
-                rot[i][t] = pair < p.r;
-                ok[i][t] = true;
-                turn[i][t] = rot[i][t] ? turn_fraction(p.freq[pair], ok[i][t]) : 0ull;
+                bool ok = true;
+                turn[i][t] = 0ull;
+                if (pair < p.r) {
+                    rot[i] |= 1u << t;
+                    turn[i][t] = turn_fraction(p.freq[pair], ok);
+                    if (!ok) bad[i] |= 1u << t;
+                }
             }
         }
     }
     __device__ __forceinline__ void at(long long pos) {
 #pragma unroll
         for (int i = 0; i < CP; ++i)
+            if (ADJ || rot[i])
 #pragma unroll
-            for (int t = 0; t < VEC; ++t) {
-                cs[i][t] = 1.f;
-                sn[i][t] = 0.f;
-                if (rot[i][t]) sine_of(turn[i][t], ok[i][t], pos, cs[i][t], sn[i][t]);
-            }
+                for (int t = 0; t < VEC; ++t) sine_of(turn[i][t], !(bad[i] >> t & 1), pos, cs[i][t], sn[i][t]);
     }
     // Turns the pairs of chunk pair i, backwards with sign = -1.
     __device__ __forceinline__ void rotate(int i, float (&x)[VEC], float (&y)[VEC], float sign) const {
@@ -172,9 +173,9 @@ template <int VEC, int CP, bool ADJ> struct Place {
 #pragma unroll
             for (int t = 0; t < VEC; ++t) {
                 float &u = t < VEC / 2 ? x[2 * t % VEC] : y[2 * t % VEC], &v = t < VEC / 2 ? x[(2 * t + 1) % VEC] : y[(2 * t + 1) % VEC];
-                turn_pair(u, v, i, t, sign);
+                if (rot[i] >> t & 1) turn_pair(u, v, i, t, sign);   // what is not rotated does not meet its neighbour
             }
-        } else {
+        } else if (rot[i]) {
 #pragma unroll
             for (int t = 0; t < VEC; ++t) turn_pair(x[t], y[t], i, t, sign);
         }
@@ -182,9 +183,9 @@ template <int VEC, int CP, bool ADJ> struct Place {
 
   private:
     __device__ __forceinline__ void turn_pair(float &u, float &v, int i, int t, float sign) const {
-        const float s = sign * sn[i][t], u1 = fmaf(u, cs[i][t], -v * s), v1 = fmaf(v, cs[i][t], u * s);
-        u = rot[i][t] ? u1 : u;   // what is not rotated does not meet its neighbour
-        v = rot[i][t] ? v1 : v;
+        const float s = sign * sn[i][t], u1 = fmaf(u, cs[i][t], -v * s);
+        v = fmaf(v, cs[i][t], u * s);
+        u = u1;
     }
 };
 
@@ -194,7 +195,7 @@ struct RotShape {
     int vec, cls;   // cls: d <= 64, 128, 256
 };
 inline RotShape rot_shape(const NormRotateArgs &a) {
-    const int full = a.dt == LA_DTYPE_BF16 ? 8 : 4, es = a.dt == LA_DTYPE_BF16 ? 2 : 4;
+    const int es = a.dt == LA_DTYPE_BF16 ? 2 : 4;
     auto fits = [&](int vec) {
         if (a.d % (2 * vec) || (a.pairs == LA_PAIRS_HALVES && a.r % vec)) return false;
         const HeadsView *v[6] = {&a.q, &a.k, &a.gq, &a.gk, &a.yq, &a.yk};
@@ -206,7 +207,7 @@ inline RotShape rot_shape(const NormRotateArgs &a) {
         return true;
     };
     RotShape s;
-    s.vec = fits(full) ? full : es == 2 && fits(2) ? 2 : 1;
+    s.vec = fits(kMostVec) ? kMostVec : es == 2 && fits(2) ? 2 : 1;
     s.cls = a.d <= 64 ? 0 : a.d <= 128 ? 1 : 2;
     return s;
 }
@@ -260,7 +261,7 @@ template <typename K, typename T, int VEC> cudaError_t rot_sized(const NormRotat
 template <typename K> cudaError_t rot_launch(const NormRotateArgs &a) {
     const RotShape s = rot_shape(a);
     if (a.dt == LA_DTYPE_F32) return s.vec == 4 ? rot_sized<K, float, 4>(a, s.cls) : rot_sized<K, float, 1>(a, s.cls);
-    return s.vec == 8   ? rot_sized<K, __nv_bfloat16, 8>(a, s.cls)
+    return s.vec == 4   ? rot_sized<K, __nv_bfloat16, 4>(a, s.cls)
            : s.vec == 2 ? rot_sized<K, __nv_bfloat16, 2>(a, s.cls)
                         : rot_sized<K, __nv_bfloat16, 1>(a, s.cls);
 }

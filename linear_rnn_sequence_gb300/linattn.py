@@ -818,70 +818,86 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, sums=None, workspace=Non
 
 
 # ---- norm and rotation of queries and keys ------------------------------------
-def _rotate_inputs(q, k, freq, positions, norm, q_weight, k_weight, pairs, layout):
-    """Checks what both directions share: (B, Hq, Hk, N, d, dtype code), the device's index, the arguments behind eps,
-    and the order of a tensor's strides (batch, head, token)."""
+# What follows from shapes and types alone is worked out once for each combination of them.
+def _dense(name, t, dtype, device_index):
+    """Address of ``t``, which is None or a contiguous tensor of this dtype on this device; its shape is known."""
+    if t is None:
+        return None
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
+    if t.get_device() != device_index:
+        raise ValueError(f"{name} is on {t.device}, not on cuda:{device_index}")
+    if not t.is_contiguous():
+        raise ValueError("tensors must be contiguous")
+    return t.data_ptr()
+
+
+def _shape(t):
+    return None if t is None else t.shape
+
+
+def _code_of(dtype):
+    if dtype is torch.bfloat16:
+        return LA_DTYPE_BF16
+    if dtype is torch.float32:
+        return LA_DTYPE_F32
+    raise TypeError(f"unsupported dtype {dtype}; use bfloat16 or float32")
+
+
+@functools.lru_cache(maxsize=1024)
+def _rotate_plan(qs, ks, dtype, strides, freq, positions, norm, wq, wk, pairs, layout):
+    """From the shapes, and the strides of tensors of q's shape and of k's in turn (None: contiguous, in the shape's order):
+    (B, Hq, Hk, N, d, dtype code, layout, norm), rotated, pairs, the positions' stride from one sequence to the
+    next, the strides of batch, head and token for the C call."""
     if layout not in LAYOUT or norm not in NORM or pairs not in PAIRS:
         raise ValueError(f"layout must be one of {sorted(LAYOUT)}, norm of {list(NORM)}, pairs of {sorted(PAIRS)}")
-    shape, ks, f32 = q.shape, k.shape, torch.float32
-    if len(shape) == 4:
-        order = (0, 1, 2) if layout == "bhnd" else (0, 2, 1)
-        B, d, Hq, N, Hk = shape[0], shape[3], shape[order[1]], shape[order[2]], ks[order[1]] if len(ks) == 4 else 0
-        same = len(ks) == 4 and ks[0] == B and ks[3] == d and ks[order[2]] == N
-    elif len(shape) == 3:
-        order, N = (0, 1), 1
-        B, Hq, d = shape
-        Hk = ks[1] if len(ks) == 3 else 0
-        same = len(ks) == 3 and ks[0] == B and ks[2] == d
-    else:
+    if len(qs) not in (3, 4) or len(ks) != len(qs):
         raise ValueError("q and k must have four dimensions, or three for single tokens")
-    if not same:
+    h, t = (1, None) if len(qs) == 3 else (1, 2) if layout == "bhnd" else (2, 1)
+    B, d, N = qs[0], qs[-1], 1 if t is None else qs[t]
+    if ks[0] != B or ks[-1] != d or (t is not None and ks[t] != N):
         raise ValueError("q and k must differ in their number of heads only")
-    dev = q.get_device()
     rotated = 0
     if freq is not None:
-        if freq.dim() != 1:
-            raise ValueError("freq must be float64 of one dimension")
-        rotated = freq.shape[0]
+        if len(freq) != 1:
+            raise ValueError("freq must be of one dimension")
+        rotated = freq[0]
+    for name, w in (("q_weight", wq), ("k_weight", wk)):
+        if w is not None and tuple(w) != (d,):
+            raise ValueError(f"{name} must be of shape {(d,)}, not {tuple(w)}")
     step = 0
     if positions is not None:
-        lead = (B,) if len(shape) == 3 else (B, N)
-        if positions.shape == lead:
-            step = 1 if len(shape) == 3 else N
-        elif len(shape) == 4 and positions.shape == (N,):
-            lead = (N,)
-        else:
-            raise ValueError(f"positions must be int64 of shape {lead}" + ("" if len(shape) == 3 else f" or {(N,)}"))
-    elif len(shape) == 3 and rotated:
+        own = (B,) if t is None else (B, N)
+        if tuple(positions) == own:
+            step = 1 if t is None else N
+        elif t is None or tuple(positions) != (N,):
+            raise ValueError(f"positions must be of shape {own}" + ("" if t is None else f" or {(N,)}"))
+    elif t is None and rotated:
         raise ValueError("single tokens need positions")
-    rest = (_expect("q_weight", q_weight, (d,), f32, dev), _expect("k_weight", k_weight, (d,), f32, dev),
-            _expect("freq", freq, (rotated,), torch.float64, dev), rotated, PAIRS[pairs],
-            None if positions is None else _expect("positions", positions, lead, torch.int64, dev), step)
-    return (B, Hq, Hk, N, d, _dtype_code(q)), dev, rest, order
+    flat = []
+    for i, st in enumerate(strides):
+        shape = ks if i % 2 else qs
+        if st is None:
+            st = [1] * len(shape)
+            for x in reversed(range(len(shape) - 1)):
+                st[x] = st[x + 1] * shape[x + 1]
+        elif st[-1] != 1 and d > 1:
+            raise ValueError("the last dimension must be contiguous")
+        flat += st[0], st[h], 0 if t is None else st[t]
+    return ((B, qs[h], ks[h], N, d, _code_of(dtype), LAYOUT[layout], NORM[norm]), rotated, PAIRS[pairs], step,
+            (ctypes.c_longlong * len(flat))(*flat))
 
 
 def _rows(name, t, like, device_index):
-    """Address of ``t``, of ``like``'s shape and dtype, whose rows are contiguous."""
+    """Address of ``t``, of ``like``'s shape and dtype."""
     if t.shape != like.shape or t.dtype is not like.dtype:
         raise ValueError(f"{name} must be {like.dtype} of shape {tuple(like.shape)}, not {t.dtype} of {tuple(t.shape)}")
     if t.get_device() != device_index:
         raise ValueError(f"{name} is on {t.device}, not on cuda:{device_index}")
-    if t.stride(-1) != 1 and t.shape[-1] > 1:
-        raise ValueError(f"the last dimension of {name} must be contiguous")
     return t.data_ptr()
 
 
-def _strides(order, *ts):
-    """The tensors' strides for the C call; None where all are contiguous."""
-    if all(t.is_contiguous() for t in ts):
-        return None
-    flat = []
-    for t in ts:
-        st = t.stride()
-        flat += [st[i] for i in order]
-        if len(order) == 2:
-            flat.append(0)
-    return (ctypes.c_longlong * len(flat))(*flat)
+_contiguous = torch.contiguous_format
 
 
 def norm_rotate(q, k, freq=None, positions=None, norm="rms", q_weight=None, k_weight=None, eps: float = 1e-6,
@@ -897,21 +913,30 @@ def norm_rotate(q, k, freq=None, positions=None, norm="rms", q_weight=None, k_we
     """
     if stream is not None or not q.is_cuda or q.get_device() != _current_device():
         return _elsewhere(norm_rotate, stream, q, k, freq, positions, norm, q_weight, k_weight, eps, pairs, layout, out)
-    sizes, dev, rest, order = _rotate_inputs(q, k, freq, positions, norm, q_weight, k_weight, pairs, layout)
-    if out is None:
-        out = q.new_empty(q.shape), q.new_empty(k.shape)
-    yq, yk = out
-    if k.dtype is not q.dtype:
+    dev, dt, f32 = q.get_device(), q.dtype, torch.float32
+    if k.dtype is not dt:
         raise ValueError("q and k must have the same dtype")
-    st = lib().la_norm_rotate(_rows("q", q, q, dev), _rows("k", k, k, dev), _rows("out[0]", yq, q, dev),
-                              _rows("out[1]", yk, k, dev), _strides(order, q, k, yq, yk), *sizes, LAYOUT[layout],
-                              NORM[norm], eps, *rest, _current_stream(dev))
-    _raise(st, "la_norm_rotate")
+    strides = (q.stride(), k.stride(), *((None, None) if out is None else (t.stride() for t in out)))
+    sizes, rotated, pair_code, step, st = _rotate_plan(q.shape, k.shape, dt, strides, _shape(freq), _shape(positions),
+                                                       norm, _shape(q_weight), _shape(k_weight), pairs, layout)
+    ka = _rows("k", k, k, dev)
+    if out is None:
+        yq, yk = torch.empty_like(q, memory_format=_contiguous), torch.empty_like(k, memory_format=_contiguous)
+        at = yq.data_ptr(), yk.data_ptr()
+    else:
+        yq, yk = out
+        at = _rows("out[0]", yq, q, dev), _rows("out[1]", yk, k, dev)
+    status = lib().la_norm_rotate(q.data_ptr(), ka, *at, st, *sizes, eps, _dense("q_weight", q_weight, f32, dev),
+                                  _dense("k_weight", k_weight, f32, dev), _dense("freq", freq, torch.float64, dev),
+                                  rotated, pair_code, _dense("positions", positions, torch.int64, dev), step,
+                                  _current_stream(dev))
+    if status:
+        _raise(status, "la_norm_rotate")
     return yq, yk
 
 
 @functools.lru_cache(maxsize=1024)
-def _rotate_backward_bytes(device_index, *sizes):
+def _rotate_backward_bytes(device_index, *sizes):   # as many sums as the device has CTAs
     return int(lib().la_norm_rotate_backward_workspace_bytes(*sizes))
 
 
@@ -923,31 +948,42 @@ def norm_rotate_backward(grad_q_out, grad_k_out, q, k, freq=None, positions=None
     ``sums`` says whether to compute those (default: each where its weight is given); they are None otherwise.
     ``out``: where grad_q and grad_k go; they may be q and k, or the outputs' gradients."""
     if stream is not None or not q.is_cuda or q.get_device() != _current_device():
-        if stream is not None and stream.device != q.device:
-            raise ValueError("the stream is of another device than the tensors")
-        return _elsewhere(norm_rotate_backward, stream, grad_q_out, grad_k_out, q, k, freq, positions, norm, q_weight,
-                          k_weight, eps, pairs, layout, sums, out, workspace)
-    sizes, dev, rest, order = _rotate_inputs(q, k, freq, positions, norm, q_weight, k_weight, pairs, layout)
-    if k.dtype is not q.dtype:
+        return _elsewhere(_norm_rotate_backward_of_q, stream, q, k, grad_q_out, grad_k_out, freq, positions, norm,
+                          q_weight, k_weight, eps, pairs, layout, sums, out, workspace)
+    dev, dt, f32 = q.get_device(), q.dtype, torch.float32
+    if k.dtype is not dt:
         raise ValueError("q and k must have the same dtype")
+    strides = (q.stride(), k.stride(), grad_q_out.stride(), grad_k_out.stride(),
+               *((None, None) if out is None else (t.stride() for t in out)))
+    sizes, rotated, pair_code, step, st = _rotate_plan(q.shape, k.shape, dt, strides, _shape(freq), _shape(positions),
+                                                       norm, _shape(q_weight), _shape(k_weight), pairs, layout)
+    at = [q.data_ptr(), _rows("k", k, k, dev), _rows("grad_q_out", grad_q_out, q, dev),
+          _rows("grad_k_out", grad_k_out, k, dev)]
     if out is None:
-        out = q.new_empty(q.shape), q.new_empty(k.shape)
-    yq, yk = out
+        yq, yk = torch.empty_like(q, memory_format=_contiguous), torch.empty_like(k, memory_format=_contiguous)
+        at += yq.data_ptr(), yk.data_ptr()
+    else:
+        yq, yk = out
+        at += _rows("out[0]", yq, q, dev), _rows("out[1]", yk, k, dev)
     d = sizes[4]
-    gwq = q.new_empty(d, dtype=torch.float32) if (q_weight is not None if sums is None else sums) else None
-    gwk = q.new_empty(d, dtype=torch.float32) if (k_weight is not None if sums is None else sums) else None
+    gwq = torch.empty(d, dtype=f32, device=q.device) if (q_weight is not None if sums is None else sums) else None
+    gwk = torch.empty(d, dtype=f32, device=q.device) if (k_weight is not None if sums is None else sums) else None
     wa, wbytes = None, 0
     if gwq is not None or gwk is not None:
-        workspace, wa, wbytes = _workspace(workspace, _rotate_backward_bytes(dev, *sizes), q)
-    st = lib().la_norm_rotate_backward(_rows("q", q, q, dev), _rows("k", k, k, dev),
-                                       _rows("grad_q_out", grad_q_out, q, dev),
-                                       _rows("grad_k_out", grad_k_out, k, dev), _rows("out[0]", yq, q, dev),
-                                       _rows("out[1]", yk, k, dev),
-                                       _strides(order, q, k, grad_q_out, grad_k_out, yq, yk), *sizes,
-                                       LAYOUT[layout], NORM[norm], eps, *rest, _addr(gwq), _addr(gwk), wa, wbytes,
-                                       _current_stream(dev))
-    _raise(st, "la_norm_rotate_backward")
+        workspace, wa, wbytes = _workspace(workspace, _rotate_backward_bytes(dev, *sizes[:6]), q)
+    status = lib().la_norm_rotate_backward(*at, st, *sizes, eps,
+                                           _dense("q_weight", q_weight, f32, dev),
+                                           _dense("k_weight", k_weight, f32, dev),
+                                           _dense("freq", freq, torch.float64, dev), rotated, pair_code,
+                                           _dense("positions", positions, torch.int64, dev), step, _addr(gwq),
+                                           _addr(gwk), wa, wbytes, _current_stream(dev))
+    if status:
+        _raise(status, "la_norm_rotate_backward")
     return yq, yk, gwq, gwk
+
+
+def _norm_rotate_backward_of_q(q, k, grad_q_out, grad_k_out, *args):
+    return norm_rotate_backward(grad_q_out, grad_k_out, q, k, *args)
 
 
 # ---- retention -----------------------------------------------------------------
@@ -961,19 +997,19 @@ def _retention_backward_bytes(device_index, *sizes):
     return int(lib().la_retention_backward_workspace_bytes(*sizes))
 
 
-def _retention_inputs(q, k, v, gamma, layout):
-    """Checks the inputs of a retention call: its sizes (B, H, N, d, dv, dtype code), the device's index and the
-    inputs' addresses."""
+@functools.lru_cache(maxsize=1024)
+def _retention_plan(qs, ks, vs, gs, dtype, layout):
+    """From the shapes: (B, H, N, d, dv, dtype code), the layout's code, the state's shape."""
     if layout not in LAYOUT:
         raise ValueError(f"layout must be one of {sorted(LAYOUT)}")
-    shape, vs = q.shape, v.shape
-    if len(shape) != 4 or len(vs) != 4:
+    if len(qs) != 4 or len(vs) != 4:
         raise ValueError("q, k and v must have four dimensions")
-    B, H, N, d = shape if layout == "bhnd" else (shape[0], shape[2], shape[1], shape[3])
-    dev, dt = q.get_device(), q.dtype
-    at = (_expect("q", q, shape, dt, dev), _expect("k", k, shape, dt, dev),
-          _expect("v", v, (*shape[:3], vs[3]), dt, dev), _expect("gamma", gamma, (H,), torch.float32, dev))
-    return (B, H, N, d, vs[3], _dtype_code(q)), dev, at
+    B, H, N, d = qs if layout == "bhnd" else (qs[0], qs[2], qs[1], qs[3])
+    if tuple(ks) != tuple(qs) or tuple(vs[:3]) != tuple(qs[:3]):
+        raise ValueError(f"k must be of q's shape {tuple(qs)} and v of shape {(*qs[:3], 'dv')}, not {tuple(ks)} and {tuple(vs)}")
+    if tuple(gs) != (H,):
+        raise ValueError(f"gamma must be of shape {(H,)}, not {tuple(gs)}")
+    return (B, H, N, d, vs[3], _code_of(dtype)), LAYOUT[layout], (B, H, d, vs[3])
 
 
 def forward_retention(q, k, v, gamma, S_in=None, return_state=False, out=None, S_out=None, layout="bhnd",
@@ -988,20 +1024,23 @@ def forward_retention(q, k, v, gamma, S_in=None, return_state=False, out=None, S
     if stream is not None or not q.is_cuda or q.get_device() != _current_device():
         return _elsewhere(forward_retention, stream, q, k, v, gamma, S_in, return_state, out, S_out, layout, workspace,
                           check_status)
-    sizes, dev, (qa, ka, va, ga) = _retention_inputs(q, k, v, gamma, layout)
-    B, H, N, d, dv, dt = sizes
-    state = (B, H, d, dv)
+    dev, dt, f32 = q.get_device(), q.dtype, torch.float32
+    sizes, code, state = _retention_plan(q.shape, k.shape, v.shape, gamma.shape, dt, layout)
+    at = (_dense("q", q, dt, dev), _dense("k", k, dt, dev), _dense("v", v, dt, dev))
     if out is None:
         out = torch.empty_like(v)
+        ya = out.data_ptr()
+    else:
+        ya = _expect("out", out, v.shape, dt, dev)
     if return_state and S_out is None:
         S_out = torch.empty(state, dtype=torch.float32, device=q.device)
     need = _retention_bytes(dev, *sizes)
     workspace, wa, wbytes = _workspace(workspace, need, q)
-    st = lib().la_forward_retention(qa, ka, va, _expect("out", out, v.shape, v.dtype, dev), ga, *sizes,
-                                    LAYOUT[layout], _expect("S_in", S_in, state, torch.float32, dev),
-                                    _expect("S_out", S_out, state, torch.float32, dev), wa, wbytes,
-                                    _current_stream(dev))
-    _raise(st, "la_forward_retention")
+    st = lib().la_forward_retention(*at, ya, _dense("gamma", gamma, f32, dev), *sizes, code,
+                                    _expect("S_in", S_in, state, f32, dev), _expect("S_out", S_out, state, f32, dev),
+                                    wa, wbytes, _current_stream(dev))
+    if st:
+        _raise(st, "la_forward_retention")
     if check_status:
         _check_run_time(workspace, need, "la_forward_retention")
     return (out, S_out) if return_state else out
@@ -1015,24 +1054,36 @@ def backward_retention(q, k, v, gamma, dy, S_in=None, grad_S_out=None, layout="b
     if stream is not None or not q.is_cuda or q.get_device() != _current_device():
         return _elsewhere(backward_retention, stream, q, k, v, gamma, dy, S_in, grad_S_out, layout, workspace,
                           check_status)
-    sizes, dev, (qa, ka, va, ga) = _retention_inputs(q, k, v, gamma, layout)
-    B, H, N, d, dv, dt = sizes
-    state = (B, H, d, dv)
+    dev, dt, f32 = q.get_device(), q.dtype, torch.float32
+    sizes, code, state = _retention_plan(q.shape, k.shape, v.shape, gamma.shape, dt, layout)
+    at = (_dense("q", q, dt, dev), _dense("k", k, dt, dev), _dense("v", v, dt, dev))
     gq, gk, gv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
     gS = None
     if S_in is not None or grad_S_out is not None:
         gS = torch.empty(state, dtype=torch.float32, device=q.device)
     need = _retention_backward_bytes(dev, *sizes)
     workspace, wa, wbytes = _workspace(workspace, need, q)
-    st = lib().la_backward_retention(qa, ka, va, _expect("dy", dy, v.shape, v.dtype, dev), ga, gq.data_ptr(),
-                                     gk.data_ptr(), gv.data_ptr(), *sizes, LAYOUT[layout],
-                                     _expect("S_in", S_in, state, torch.float32, dev),
-                                     _expect("grad_S_out", grad_S_out, state, torch.float32, dev), _addr(gS), wa,
-                                     wbytes, _current_stream(dev))
-    _raise(st, "la_backward_retention")
+    st = lib().la_backward_retention(*at, _expect("dy", dy, v.shape, dt, dev), _dense("gamma", gamma, f32, dev),
+                                     gq.data_ptr(), gk.data_ptr(), gv.data_ptr(), *sizes, code,
+                                     _expect("S_in", S_in, state, f32, dev),
+                                     _expect("grad_S_out", grad_S_out, state, f32, dev), _addr(gS), wa, wbytes,
+                                     _current_stream(dev))
+    if st:
+        _raise(st, "la_backward_retention")
     if check_status:
         _check_run_time(workspace, need, "la_backward_retention")
     return gq, gk, gv, gS
+
+
+@functools.lru_cache(maxsize=1024)
+def _retention_step_plan(qs, ks, vs, gs, dtype):
+    """From the shapes: (B, H, d, dv, dtype code), the state's shape."""
+    if len(qs) != 3 or len(vs) != 3:
+        raise ValueError("q, k and v must have three dimensions")
+    B, H, d = qs
+    if tuple(ks) != tuple(qs) or tuple(vs[:2]) != (B, H) or tuple(gs) != (H,):
+        raise ValueError("q and k must be [B, H, d], v [B, H, dv] and gamma [H]")
+    return (B, H, d, vs[2], _code_of(dtype)), (B, H, d, vs[2])
 
 
 def decode_step_retention(q, k, v, gamma, S, S_out=None, out=None, stream=None):
@@ -1040,18 +1091,18 @@ def decode_step_retention(q, k, v, gamma, S, S_out=None, out=None, stream=None):
     updated in place unless ``S_out`` is given.  Returns y [B,H,dv] in v's dtype."""
     if stream is not None or not q.is_cuda or q.get_device() != _current_device():
         return _elsewhere(decode_step_retention, stream, q, k, v, gamma, S, S_out, out)
-    shape, vs = q.shape, v.shape
-    if len(shape) != 3 or len(vs) != 3:
-        raise ValueError("q, k and v must have three dimensions")
-    B, H, d = shape
-    dv, dev, dt, f32 = vs[2], q.get_device(), q.dtype, torch.float32
+    dev, dt, f32 = q.get_device(), q.dtype, torch.float32
+    sizes, state = _retention_step_plan(q.shape, k.shape, v.shape, gamma.shape, dt)
+    at = (_dense("q", q, dt, dev), _dense("k", k, dt, dev), _dense("v", v, dt, dev))
     if out is None:
         out = torch.empty_like(v)
-    sa = _expect("S", S, (B, H, d, dv), f32, dev)
-    st = lib().la_decode_step_retention(_expect("q", q, shape, dt, dev), _expect("k", k, shape, dt, dev),
-                                        _expect("v", v, (B, H, dv), dt, dev), _expect("out", out, vs, dt, dev),
-                                        _expect("gamma", gamma, (H,), f32, dev), sa,
-                                        sa if S_out is None else _expect("S_out", S_out, (B, H, d, dv), f32, dev),
-                                        B, H, d, dv, _dtype_code(q), _current_stream(dev))
-    _raise(st, "la_decode_step_retention")
+        ya = out.data_ptr()
+    else:
+        ya = _expect("out", out, v.shape, dt, dev)
+    sa = _expect("S", S, state, f32, dev)
+    st = lib().la_decode_step_retention(*at, ya, _dense("gamma", gamma, f32, dev), sa,
+                                        sa if S_out is None else _expect("S_out", S_out, state, f32, dev), *sizes,
+                                        _current_stream(dev))
+    if st:
+        _raise(st, "la_decode_step_retention")
     return out
