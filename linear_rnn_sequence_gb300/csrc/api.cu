@@ -957,17 +957,13 @@ RetainArgs retain_args(const void *q, const void *k, const void *v, void *y, con
 
 bool retain_on_tensor_cores(const RetainArgs &a) { return retain_tc_supported(a); }
 
-// Of the forward or the gradients: with a final state or without, and for both shapes of the state.
-size_t retain_ws_bytes(int B, int H, int N, int d, int dv, la_dtype dt) {
+// Of the forward, with a final state or without, or of the gradients.
+size_t retain_ws_bytes(int B, int H, int N, int d, int dv, la_dtype dt, bool grads) {
     if (check_delta(B, H, H, N, d, dv, dt) != LA_OK || N == 0) return 0;
     float some;
     const RetainArgs a = retain_args(nullptr, nullptr, nullptr, nullptr, nullptr, B, H, N, d, dv, dt, LA_LAYOUT_BHND,
                                      nullptr, &some, false, false, nullptr, nullptr);
-    return sizeof(WsHeader) + (retain_on_tensor_cores(a) ? retain_tc_workspace(a) : retain_simt_workspace(a));
-}
-
-cudaError_t launch_retain(const RetainArgs &a) {
-    return retain_on_tensor_cores(a) ? launch_retain_tc(a) : launch_retain_simt(a);
+    return sizeof(WsHeader) + (retain_on_tensor_cores(a) ? retain_tc_workspace(a) : retain_simt_workspace(a, grads));
 }
 
 }  // namespace
@@ -976,7 +972,7 @@ cudaError_t launch_retain(const RetainArgs &a) {
 extern "C" {
 
 size_t la_retention_workspace_bytes(int B, int H, int N, int d, int dv, la_dtype dt) {
-    return retain_ws_bytes(B, H, N, d, dv, dt);
+    return retain_ws_bytes(B, H, N, d, dv, dt, false);
 }
 
 la_status la_forward_retention(const void *q, const void *k, const void *v, void *y, const float *gamma, int B, int H,
@@ -1001,12 +997,12 @@ la_status la_forward_retention(const void *q, const void *k, const void *v, void
     const Buf out[] = {{y, T * dv * es}, {S_out, sb}, {need ? workspace : nullptr, need}};
     if (clash(in, out)) return LA_ERR_INVALID_ARG;
     if (need && cudaMemsetAsync(workspace, 0, sizeof(WsHeader), s) != cudaSuccess) return LA_ERR_CUDA;
-    return from_cuda(launch_retain(retain_args(q, k, v, y, gamma, B, H, N, d, dv, dt, layout, S_in, S_out, false, false, need ? workspace : nullptr,
-                                               stream)));
+    const RetainArgs a = retain_args(q, k, v, y, gamma, B, H, N, d, dv, dt, layout, S_in, S_out, false, false, workspace, stream);
+    return from_cuda(retain_on_tensor_cores(a) ? launch_retain_tc(a) : launch_retain_simt(a));
 }
 
 size_t la_retention_backward_workspace_bytes(int B, int H, int N, int d, int dv, la_dtype dt) {
-    return retain_ws_bytes(B, H, N, d, dv, dt);
+    return retain_ws_bytes(B, H, N, d, dv, dt, true);
 }
 
 la_status la_backward_retention(const void *q, const void *k, const void *v, const void *dy, const float *gamma,
@@ -1033,12 +1029,14 @@ la_status la_backward_retention(const void *q, const void *k, const void *v, con
                        {need ? workspace : nullptr, need}};
     if (clash(in, out)) return LA_ERR_INVALID_ARG;
     if (need && cudaMemsetAsync(workspace, 0, sizeof(WsHeader), s) != cudaSuccess) return LA_ERR_CUDA;
-    void *ws = need ? workspace : nullptr;
-    cudaError_t e = launch_retain(retain_args(dy, v, k, grad_q, gamma, B, H, N, dv, d, dt, layout, S_in, nullptr, false, true, ws, stream));
+    const RetainArgs a = retain_args(q, k, v, nullptr, gamma, B, H, N, d, dv, dt, layout, S_in, nullptr, false, false, workspace, stream);
+    if (!retain_on_tensor_cores(a))
+        return from_cuda(launch_retain_grads_simt(a, {dy, grad_q, grad_k, grad_v, grad_S_out, grad_S_in}));
+    cudaError_t e = launch_retain_tc(retain_args(dy, v, k, grad_q, gamma, B, H, N, dv, d, dt, layout, S_in, nullptr, false, true, workspace, stream));
     if (e == cudaSuccess)
-        e = launch_retain(retain_args(v, dy, q, grad_k, gamma, B, H, N, dv, d, dt, layout, grad_S_out, nullptr, true, true, ws, stream));
+        e = launch_retain_tc(retain_args(v, dy, q, grad_k, gamma, B, H, N, dv, d, dt, layout, grad_S_out, nullptr, true, true, workspace, stream));
     if (e == cudaSuccess)
-        e = launch_retain(retain_args(k, q, dy, grad_v, gamma, B, H, N, d, dv, dt, layout, grad_S_out, grad_S_in, true, false, ws, stream));
+        e = launch_retain_tc(retain_args(k, q, dy, grad_v, gamma, B, H, N, d, dv, dt, layout, grad_S_out, grad_S_in, true, false, workspace, stream));
     return from_cuda(e);
 }
 

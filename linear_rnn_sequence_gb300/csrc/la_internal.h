@@ -129,6 +129,14 @@ struct RetainArgs {
     cudaStream_t stream;
 };
 
+// What the gradients of retention take beside the forward's inputs.
+struct RetainGrads {
+    const void *dy;
+    void *dq, *dk, *dv;
+    const float *dS_out;         // nullable (zero)
+    float *dS_in;                // nullable
+};
+
 // Rows of heads: row (b, h, t) starts at p + b sb + h sh + t st (elements).
 struct HeadsView {
     void *p;
@@ -236,8 +244,9 @@ size_t norm_rotate_partials(const NormRotateArgs &a);   // floats of `partials`;
 cudaError_t launch_norm_rotate_grad(const NormRotateArgs &a);
 
 // retention (CUDA cores, float32), and a single token of it
-size_t retain_simt_workspace(const RetainArgs &a);
-cudaError_t launch_retain_simt(const RetainArgs &a);
+size_t retain_simt_workspace(const RetainArgs &a, bool grads);
+cudaError_t launch_retain_simt(const RetainArgs &a);   // rev and trans not looked at
+cudaError_t launch_retain_grads_simt(const RetainArgs &a, const RetainGrads &g);
 cudaError_t launch_retain_step(const RetainArgs &a);
 // Sums of `blocks` blocks of `tokens` tokens a head, [head][block][d][dv], become the states before the blocks;
 // a.S_out too.

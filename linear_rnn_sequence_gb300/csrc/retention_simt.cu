@@ -4,9 +4,10 @@
 //   2. the states before the blocks, one after another over the sums (a thread for four of a state's values);
 //   3. each block's y from its state (a CTA a block): scores, their product with v, the state's part.
 // Every block of 1 and 3 runs at once, so a long sequence of few heads fills the GPU as well as many short ones
-// do.  Bound by the float32 multiplications: 4 (32 + d) dv + 64 d ... a token of a head; the states' way through memory
-// (three times 4 d dv bytes a block) is the rest.
-// It serves float32 inputs, widths of 32, and short bf16 sequences.
+// do.  The gradients take the states of both directions in one pass of 1 and 2, and all three of them in 3 (two launches if
+// d and dv differ).  Bound by the float32 multiplications, (4 d + 64) dv + 64 d of them for a token of a head, and by
+// the states' way through memory, 16 d dv bytes a block; small calls by the three launches.
+// It serves float32 inputs and widths of 32.
 #include "retention.cuh"
 
 namespace la {
@@ -17,14 +18,20 @@ constexpr int kRThr = 256;    // 16 x 16 threads
 constexpr int kScanThr = 128;
 constexpr int kPad = 4;       // floats behind a row of Q, K and P: rows four banks apart
 
-struct RetainSimt {
+// One retention, or one of its gradients; their state arrays are [head][block][d][dv], or, to a job with `trans`,
+// [head][block][dv][d].
+struct Job {
     const void *q, *k, *v;
     void *y;
-    const float *gamma, *S_in;
-    float *S_out, *states;    // states: [head][block][d][dv]
-    int H, N, layout, nblk;
-    int tokens;               // of a block of the scan
+    const float *S_in;
+    float *S_out, *states;
     bool rev, trans;
+};
+struct RetainSimt {
+    Job job[3];
+    const float *gamma;
+    int H, N, layout, nblk, heads;
+    int tokens;               // of a block of the scan
 };
 
 // Rows t0.. of a head as floats into dst (rows LD floats apart), zeros from token n on.
@@ -73,10 +80,12 @@ __global__ void __launch_bounds__(kRThr) retain_sums_kernel(const RetainSimt p) 
     extern __shared__ float sm[];
     float *K = sm, *V = K + kRC * D;
     __shared__ float w[kRC];
-    const int bh = blockIdx.x / p.nblk, blk = blockIdx.x % p.nblk, b = bh / p.H, h = bh % p.H, t0 = blk * kRC, n = min(kRC, p.N - t0);
-    if (threadIdx.x < kRC) w[threadIdx.x] = (int)threadIdx.x < n ? gamma_power(p.gamma[h], key_exp(p.rev, threadIdx.x, n)) : 0.f;
-    stage<D, D>(K, (const T *)p.k, token_rows(p.layout, b, h, p.H, p.N, D), t0, n);
-    stage<DV, DV>(V, (const T *)p.v, token_rows(p.layout, b, h, p.H, p.N, DV), t0, n);
+    const int unit = blockIdx.x % (p.heads * p.nblk), bh = unit / p.nblk, blk = unit % p.nblk, b = bh / p.H, h = bh % p.H;
+    const int t0 = blk * kRC, n = min(kRC, p.N - t0);
+    const Job &jb = p.job[blockIdx.x / (p.heads * p.nblk)];
+    if (threadIdx.x < kRC) w[threadIdx.x] = (int)threadIdx.x < n ? gamma_power(p.gamma[h], key_exp(jb.rev, threadIdx.x, n)) : 0.f;
+    stage<D, D>(K, (const T *)jb.k, token_rows(p.layout, b, h, p.H, p.N, D), t0, n);
+    stage<DV, DV>(V, (const T *)jb.v, token_rows(p.layout, b, h, p.H, p.N, DV), t0, n);
     __syncthreads();
     using CA = Cols<D>;
     using CC = Cols<DV>;
@@ -99,7 +108,7 @@ __global__ void __launch_bounds__(kRThr) retain_sums_kernel(const RetainSimt p) 
             for (int c = 0; c < CC::N; ++c) acc[a][c] = fmaf(x[a], y[c], acc[a][c]);
         }
     }
-    float *out = p.states + ((size_t)bh * p.nblk + blk) * D * DV;
+    float *out = jb.states + (size_t)unit * D * DV;
 #pragma unroll
     for (int a = 0; a < CA::N; ++a)
 #pragma unroll
@@ -109,26 +118,28 @@ __global__ void __launch_bounds__(kRThr) retain_sums_kernel(const RetainSimt p) 
 // The sums become the states before their blocks.
 __global__ void __launch_bounds__(kScanThr) retain_scan_kernel(const RetainSimt p, int D, int DV) {
     const int st = D * DV, parts = st / 4 / kScanThr;
-    const int bh = blockIdx.x / parts, at = (blockIdx.x % parts * kScanThr + threadIdx.x) * 4;
+    const int unit = blockIdx.x / parts, bh = unit % p.heads, at = (blockIdx.x % parts * kScanThr + threadIdx.x) * 4;
+    const Job &jb = p.job[unit / p.heads];
+    const bool rev = jb.rev, trans = jb.trans;
     const float g = p.gamma[bh % p.H], whole = gamma_power(g, p.tokens), last = gamma_power(g, p.N - (p.nblk - 1) * p.tokens);
-    float4 *s = reinterpret_cast<float4 *>(p.states + (size_t)bh * p.nblk * st + at);
+    float4 *s = reinterpret_cast<float4 *>(jb.states + (size_t)bh * p.nblk * st + at);
     const int step = st / 4;
     // of a state's values in their order here; a transposed state's lie DV apart
-    auto where = [&](int i) { return p.trans ? (size_t)((at + i) % DV) * D + (at + i) / DV : (size_t)at + i; };
+    auto where = [&](int i) { return trans ? (size_t)((at + i) % DV) * D + (at + i) / DV : (size_t)at + i; };
     float x[4] = {0.f, 0.f, 0.f, 0.f};
-    if (p.S_in)
+    if (jb.S_in)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = p.S_in[(size_t)bh * st + where(i)];
+        for (int i = 0; i < 4; ++i) x[i] = jb.S_in[(size_t)bh * st + where(i)];
     constexpr int U = 8;
     for (int k0 = 0; k0 < p.nblk; k0 += U) {
         float4 u[U];
 #pragma unroll
         for (int i = 0; i < U; ++i)
-            if (k0 + i < p.nblk) u[i] = s[(size_t)(p.rev ? p.nblk - 1 - k0 - i : k0 + i) * step];
+            if (k0 + i < p.nblk) u[i] = s[(size_t)(rev ? p.nblk - 1 - k0 - i : k0 + i) * step];
 #pragma unroll
         for (int i = 0; i < U; ++i)
             if (k0 + i < p.nblk) {
-                const int blk = p.rev ? p.nblk - 1 - k0 - i : k0 + i;
+                const int blk = rev ? p.nblk - 1 - k0 - i : k0 + i;
                 const float f = blk == p.nblk - 1 ? last : whole;
                 s[(size_t)blk * step] = make_float4(x[0], x[1], x[2], x[3]);
                 x[0] = fmaf(f, x[0], u[i].x);
@@ -137,9 +148,9 @@ __global__ void __launch_bounds__(kScanThr) retain_scan_kernel(const RetainSimt 
                 x[3] = fmaf(f, x[3], u[i].w);
             }
     }
-    if (p.S_out)
+    if (jb.S_out)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) p.S_out[(size_t)bh * st + where(i)] = x[i];
+        for (int i = 0; i < 4; ++i) jb.S_out[(size_t)bh * st + where(i)] = x[i];
 }
 
 // acc[4][C] += sum over 4 j of p[4][4] v[4][C]; DIAG: only where row r may see j.
@@ -177,13 +188,15 @@ __global__ void __launch_bounds__(kRThr, 2) retain_out_kernel(const RetainSimt p
     extern __shared__ float sm[];
     float *Q = sm, *K = Q + kRC * L::LQ, *V = K + L::k, *P = K, *S = P + L::LP * kRC;
     __shared__ float pw[kRC + 1];
-    const int bh = blockIdx.x / p.nblk, blk = blockIdx.x % p.nblk, b = bh / p.H, h = bh % p.H, t0 = blk * kRC, n = min(kRC, p.N - t0);
-    const bool rev = p.rev;
+    const int unit = blockIdx.x % (p.heads * p.nblk), bh = unit / p.nblk, blk = unit % p.nblk, b = bh / p.H, h = bh % p.H;
+    const int t0 = blk * kRC, n = min(kRC, p.N - t0);
+    const Job &jb = p.job[blockIdx.x / (p.heads * p.nblk)];
+    const bool rev = jb.rev, trans = jb.trans;
     if (threadIdx.x <= kRC) pw[threadIdx.x] = gamma_power(p.gamma[h], threadIdx.x);
     const TokenRows rk = token_rows(p.layout, b, h, p.H, p.N, D), rv = token_rows(p.layout, b, h, p.H, p.N, DV);
-    stage<D, L::LQ>(Q, (const T *)p.q, rk, t0, n);
-    stage<D, L::LQ>(K, (const T *)p.k, rk, t0, n);
-    stage<DV, DV>(V, (const T *)p.v, rv, t0, n);
+    stage<D, L::LQ>(Q, (const T *)jb.q, rk, t0, n);
+    stage<D, L::LQ>(K, (const T *)jb.k, rk, t0, n);
+    stage<DV, DV>(V, (const T *)jb.v, rv, t0, n);
     __syncthreads();
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;   // rows 4 ty ..; scores of columns tx + 16 c
     float s[4][4] = {};
@@ -209,8 +222,7 @@ __global__ void __launch_bounds__(kRThr, 2) retain_out_kernel(const RetainSimt p
             P[i * L::LP + j] = e >= 0 ? s[r][c] * pw[e] : 0.f;
         }
     // the state's part, rows of S staged where K was
-    const float *S0 = p.nblk > 1 || p.S_out ? p.states + ((size_t)bh * p.nblk + blk) * D * DV : p.S_in ? p.S_in + (size_t)bh * D * DV : nullptr;
-    const bool trans = p.trans && !(p.nblk > 1 || p.S_out);
+    const float *S0 = jb.states ? jb.states + (size_t)unit * D * DV : jb.S_in ? jb.S_in + (size_t)bh * D * DV : nullptr;
     float acc[4][C];
 #pragma unroll
     for (int r = 0; r < 4; ++r)
@@ -240,7 +252,7 @@ __global__ void __launch_bounds__(kRThr, 2) retain_out_kernel(const RetainSimt p
     for (int j = rev ? d0 + 4 : 0; j < (rev ? kRC : d0); j += 4) four<C, false>(acc, P + d0 * L::LP + j, L::LP, V + j * DV, DV, tx, rev);
     if (rev) four<C, true>(acc, P + d0 * L::LP + d0, L::LP, V + d0 * DV, DV, tx, true);
     else four<C, true>(acc, P + d0 * L::LP + d0, L::LP, V + d0 * DV, DV, tx, false);
-    T *y = (T *)p.y;
+    T *y = (T *)jb.y;
 #pragma unroll
     for (int r = 0; r < 4; ++r)
         if (4 * ty + r < n)
@@ -252,57 +264,100 @@ int blocks_of(int N) { return (N + kRC - 1) / kRC; }
 // One block, and no final state asked for: y comes from S_in itself.
 bool needs_states(const RetainArgs &a) { return a.N > kRC || a.S_out; }
 
-template <int D, int DV, typename T> cudaError_t launch_t(const RetainArgs &a) {
+RetainSimt simt_params(const RetainArgs &a) {
     RetainSimt p{};
-    p.q = a.q; p.k = a.k; p.v = a.v; p.y = a.y; p.gamma = a.gamma; p.S_in = a.S_in; p.S_out = a.S_out;
-    p.H = a.H; p.N = a.N; p.layout = a.layout; p.nblk = blocks_of(a.N); p.rev = a.rev; p.trans = a.trans;
-    if (a.ws) p.states = reinterpret_cast<float *>(static_cast<char *>(a.ws) + sizeof(WsHeader));
-    const unsigned BH = (unsigned)a.B * a.H, blocks = BH * p.nblk;   // fewer than tokens, which fit 31 bits
-    cudaError_t e = cudaSuccess;
-    if (needs_states(a)) {
+    p.gamma = a.gamma; p.H = a.H; p.N = a.N; p.layout = a.layout; p.nblk = blocks_of(a.N); p.heads = a.B * a.H;
+    p.tokens = kRC;
+    return p;
+}
+
+// Launches of `jobs` jobs; their units are fewer than tokens, which fit 31 bits.
+template <int D, int DV, typename T> struct Launch {
+    static cudaError_t sums(const RetainSimt &p, int jobs, cudaStream_t s) {
         constexpr int smem = 4 * kRC * (D + DV);
-        e = cudaFuncSetAttribute(retain_sums_kernel<D, DV, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        cudaError_t e = cudaFuncSetAttribute(retain_sums_kernel<D, DV, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
-        retain_sums_kernel<D, DV, T><<<blocks, kRThr, smem, a.stream>>>(p);
-        if ((e = launch_retain_scan(a, p.states, p.nblk, kRC)) != cudaSuccess) return e;
+        retain_sums_kernel<D, DV, T><<<(unsigned)jobs * p.heads * p.nblk, kRThr, smem, s>>>(p);
+        retain_scan_kernel<<<(unsigned)jobs * p.heads * (D * DV / 4 / kScanThr), kScanThr, 0, s>>>(p, D, DV);
+        return cudaGetLastError();
     }
-    constexpr int smem = OutLay<D, DV, T>::bytes;
-    e = cudaFuncSetAttribute(retain_out_kernel<D, DV, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-    retain_out_kernel<D, DV, T><<<blocks, kRThr, smem, a.stream>>>(p);
-    return cudaGetLastError();
-}
-template <int D, typename T> cudaError_t launch_d(const RetainArgs &a) {
+    static cudaError_t out(const RetainSimt &p, int jobs, cudaStream_t s) {
+        constexpr int smem = OutLay<D, DV, T>::bytes;
+        cudaError_t e = cudaFuncSetAttribute(retain_out_kernel<D, DV, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+        retain_out_kernel<D, DV, T><<<(unsigned)jobs * p.heads * p.nblk, kRThr, smem, s>>>(p);
+        return cudaGetLastError();
+    }
+};
+
+struct Forward {
+    template <int D, int DV, typename T> static cudaError_t run(const RetainArgs &a, const RetainGrads &) {
+        RetainSimt p = simt_params(a);
+        Job &jb = p.job[0];
+        jb = {a.q, a.k, a.v, a.y, a.S_in, a.S_out, nullptr, false, false};
+        if (needs_states(a)) {
+            jb.states = reinterpret_cast<float *>(static_cast<char *>(a.ws) + sizeof(WsHeader));
+            const cudaError_t e = Launch<D, DV, T>::sums(p, 1, a.stream);
+            if (e != cudaSuccess) return e;
+        }
+        return Launch<D, DV, T>::out(p, 1, a.stream);
+    }
+};
+
+// The states S (for grad_q) and, from behind, G (for grad_k and grad_v) together, then the three gradients: those whose
+// rows are d wide, and grad_v, in one launch if d = dv.
+struct Grads {
+    template <int D, int DV, typename T> static cudaError_t run(const RetainArgs &a, const RetainGrads &g) {
+        RetainSimt p = simt_params(a);
+        float *S = reinterpret_cast<float *>(static_cast<char *>(a.ws) + sizeof(WsHeader)), *G = S + (size_t)p.heads * p.nblk * D * DV;
+        p.job[0] = {nullptr, a.k, a.v, nullptr, a.S_in, nullptr, S, false, false};
+        p.job[1] = {nullptr, a.q, g.dy, nullptr, g.dS_out, g.dS_in, G, true, false};
+        cudaError_t e = Launch<D, DV, T>::sums(p, 2, a.stream);
+        if (e != cudaSuccess) return e;
+        p.job[0] = {g.dy, a.v, a.k, g.dq, nullptr, nullptr, S, false, true};
+        p.job[1] = {a.v, g.dy, a.q, g.dk, nullptr, nullptr, G, true, true};
+        p.job[2] = {a.k, a.q, g.dy, g.dv, nullptr, nullptr, G, true, false};
+        if (D == DV) return Launch<DV, D, T>::out(p, 3, a.stream);
+        if ((e = Launch<DV, D, T>::out(p, 2, a.stream)) != cudaSuccess) return e;
+        p.job[0] = p.job[2];
+        return Launch<D, DV, T>::out(p, 1, a.stream);
+    }
+};
+
+template <typename K, int D, typename T> cudaError_t by_dv(const RetainArgs &a, const RetainGrads &g) {
     switch (a.dv) {
-    case 32: return launch_t<D, 32, T>(a);
-    case 64: return launch_t<D, 64, T>(a);
-    case 128: return launch_t<D, 128, T>(a);
+    case 32: return K::template run<D, 32, T>(a, g);
+    case 64: return K::template run<D, 64, T>(a, g);
+    case 128: return K::template run<D, 128, T>(a, g);
     }
     return cudaErrorInvalidValue;
 }
-template <typename T> cudaError_t launch(const RetainArgs &a) {
+template <typename K, typename T> cudaError_t by_d(const RetainArgs &a, const RetainGrads &g) {
     switch (a.d) {
-    case 32: return launch_d<32, T>(a);
-    case 64: return launch_d<64, T>(a);
-    case 128: return launch_d<128, T>(a);
+    case 32: return by_dv<K, 32, T>(a, g);
+    case 64: return by_dv<K, 64, T>(a, g);
+    case 128: return by_dv<K, 128, T>(a, g);
     }
     return cudaErrorInvalidValue;
+}
+template <typename K> cudaError_t by_type(const RetainArgs &a, const RetainGrads &g) {
+    return a.dt == LA_DTYPE_BF16 ? by_d<K, __nv_bfloat16>(a, g) : by_d<K, float>(a, g);
 }
 
 }  // namespace
 
-size_t retain_simt_workspace(const RetainArgs &a) {
-    return needs_states(a) ? (size_t)a.B * a.H * blocks_of(a.N) * a.d * a.dv * 4 : 0;
+size_t retain_simt_workspace(const RetainArgs &a, bool grads) {
+    const size_t one = (size_t)a.B * a.H * blocks_of(a.N) * a.d * a.dv * 4;
+    return grads ? 2 * one : needs_states(a) ? one : 0;
 }
 cudaError_t launch_retain_scan(const RetainArgs &a, float *states, int blocks, int tokens) {
-    RetainSimt p{};
-    p.gamma = a.gamma; p.S_in = a.S_in; p.S_out = a.S_out; p.states = states;
-    p.H = a.H; p.N = a.N; p.nblk = blocks; p.tokens = tokens; p.rev = a.rev; p.trans = a.trans;
-    retain_scan_kernel<<<(unsigned)a.B * a.H * (a.d * a.dv / 4 / kScanThr), kScanThr, 0, a.stream>>>(p, a.d, a.dv);
+    RetainSimt p = simt_params(a);
+    p.job[0] = {nullptr, nullptr, nullptr, nullptr, a.S_in, a.S_out, states, a.rev, a.trans};
+    p.nblk = blocks; p.tokens = tokens;
+    retain_scan_kernel<<<(unsigned)p.heads * (a.d * a.dv / 4 / kScanThr), kScanThr, 0, a.stream>>>(p, a.d, a.dv);
     return cudaGetLastError();
 }
-cudaError_t launch_retain_simt(const RetainArgs &a) {
-    return a.dt == LA_DTYPE_BF16 ? launch<__nv_bfloat16>(a) : launch<float>(a);
-}
+cudaError_t launch_retain_simt(const RetainArgs &a) { return by_type<Forward>(a, RetainGrads{}); }
+cudaError_t launch_retain_grads_simt(const RetainArgs &a, const RetainGrads &g) { return by_type<Grads>(a, g); }
 
 }  // namespace la

@@ -323,6 +323,26 @@ def test_a_layer():
         assert near(a, b) <= 10 * 2.0 ** -8
 
 
+@pytest.mark.parametrize("d,dv", [(64, 64), (128, 128), (64, 128), (128, 64)])
+@pytest.mark.parametrize("N", [100, 300, 4000])
+def test_a_copy_that_never_comes(N, d, dv):
+    """A bounded wait runs out, the call says so, and the next one is right."""
+    x = R.inputs(1, 2, N, d, dv, BF16, seed=12)
+    la.set_fault(drop_load_item=1, wait_limit_ns=2_000_000)
+    try:
+        for call in (lambda: forward(x, return_state=True), lambda: backward(x)):
+            with pytest.raises(la.LinAttnError) as e:
+                call()
+            assert e.value.status == la.LA_ERR_TIMEOUT
+    finally:
+        la.set_fault()
+    if N < 4000:
+        check_forward(x)
+        check_backward(x)
+    else:
+        forward(x), backward(x)
+
+
 def test_refusals():
     x = on_gpu(R.inputs(1, 2, 8, 64, 32, BF16))
     q, k, v, g = x["q"], x["k"], x["v"], x["gamma"]
