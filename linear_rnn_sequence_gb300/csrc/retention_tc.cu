@@ -3,7 +3,7 @@
 //
 //   scores  P  = Q K^T                        (128 x 128, K = d)
 //   masked  P~ = gamma^|i-j| P                (bf16, over P in TMEM)
-//   y          = gamma^(i+1) (Q S) + P~ V     (one accumulator: scaled between the two products)
+//   y          = gamma^(i+1) (Q S) + P~ V     (dv = 128: one accumulator, scaled between the two products)
 //   state   S' = gamma^C S + K^T W,           W_j = gamma^(C-1-j) v_j
 // and the same with the exponents of retention.cuh from behind (REV).
 //
@@ -18,6 +18,10 @@
 //   warp 13      issues the copies.
 // W is the one operand without a second place in TMEM: its three pieces, the halves of K^T W and the state's update
 // between them are the chain that bounds a block.
+//
+// With dv = 64 the upper 64 TMEM lanes hold W of the block's second 64 tokens (and zeros for the first, as the lower ones do for
+// the second), so that every warp makes half as much of it; the lanes' sums stay two states that add up to S, and Q S takes
+// both (B8 H16 N8192 d64: 143 us with W in the lower lanes alone).
 //
 // Precision: the state is float32 in registers, and what is added to it is exact but for the accumulator's float32: W is
 // rounded to float32 once and enters as three bf16 pieces that add up to it (the top, middle and low 8 bits), against
@@ -66,7 +70,8 @@ struct RetainSmall {
 };
 
 template <int D, int DV> struct RetainLay {
-    static constexpr int kQ = (D / 64) * 16384, kV = (DV / 64) * 16384, kS = DV * D * 2;
+    static constexpr int kQ = (D / 64) * 16384, kV = (DV / 64) * 16384;
+    static constexpr int kHalfS = DV * D * 2, kS = (128 / DV) * kHalfS;
     static constexpr bool ownY = DV > D;      // y does not fit where Q was
     static constexpr int oQ = 0, oK = oQ + 2 * kQ, oV = oK + 2 * kQ, oS = oV + 2 * kV, oY = oS + kS,
                          oSmall = oY + (ownY ? 2 * kV : 0);
@@ -97,6 +102,7 @@ retain_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
     using Lay = RetainLay<D, DV>;
     constexpr bool OUT = MODE == kWhole;
     constexpr int NH = D / 64;   // halves of K^T W
+    constexpr bool TWIN = DV == 64;   // two states, of the tokens' halves; Q S and P~ V in accumulators of their own
     uint8_t *sm = retain_smem();
     RetainSmall &S = *reinterpret_cast<RetainSmall *>(sm + Lay::oSmall);
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
@@ -272,8 +278,10 @@ retain_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
                 const uint64_t qd = desc_k(smem_u32(sQ) + s * Lay::kQ), sd = desc_k(smem_u32(sS));
 #pragma unroll
                 for (int ks = 0; ks < D / 16; ++ks)
-                    mma_ss_if(leader, tb + kColY, qd + (uint32_t)(((ks >> 2) * 16384 + (ks & 3) * 32) >> 4),
-                              sd + (uint32_t)(((ks >> 2) * DV * 128 + (ks & 3) * 32) >> 4), iQS, ks > 0);
+#pragma unroll
+                    for (int t = 0; t < (TWIN ? 2 : 1); ++t)
+                        mma_ss_if(leader, tb + kColY, qd + (uint32_t)(((ks >> 2) * 16384 + (ks & 3) * 32) >> 4),
+                                  sd + (uint32_t)((t * Lay::kHalfS + (ks >> 2) * DV * 128 + (ks & 3) * 32) >> 4), iQS, ks + t > 0);
                 mma_commit_if(leader, &S.qs_done);
             }
             if (NH == 2) {
@@ -284,14 +292,14 @@ retain_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
             if (OUT && *(volatile int *)&S.v_bad[s] == n + 1) mend_v(n);
             if (OUT) {
                 all(mbar_wait<1>(&S.p_ready, n & 1, g, 9));
-                all(mbar_wait<1>(&S.y_scaled, n & 1, g, 10));
+                if (!TWIN) all(mbar_wait<1>(&S.y_scaled, n & 1, g, 10));
                 if (!ok) break;
                 const uint32_t leader = elect_leader();
                 tc_fence_after();
                 const uint64_t vd = smem_desc(smem_u32(sV) + s * Lay::kV, 16384, 1024, kSwizzle128B);
 #pragma unroll
                 for (int ks = 0; ks < kTC / 16; ++ks)
-                    mma_ts_if(leader, tb + kColY, tb + kColP + ks * 8, vd + ks * 128, iPV, 1);
+                    mma_ts_if(leader, tb + kColY + (TWIN ? 64 : 0), tb + kColP + ks * 8, vd + ks * 128, iPV, !TWIN || ks > 0);
                 mma_commit_if(leader, &S.pv_done[s]);
                 if (n + 1 < nch) scores(n + 1);
             } else {
@@ -308,35 +316,39 @@ retain_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
         // ------------------------------------------------------------ W and the state
         constexpr int SC = D / 2;   // state values of a thread: column `row` of dv, half * SC .. of d
         const int half = (warp - 4) >> 2;
-        const bool live = row < DV;   // warp-uniform
+        const int part = TWIN ? wq >> 1 : 0, col = TWIN ? row & 63 : row;   // part: warp-uniform
         float st[SC];
-        if (live && p.S_in) {
+        if (part == 0 && p.S_in) {
             const float *src = p.S_in + (size_t)(p.nseg > 1 ? bh * p.nseg + seg : bh) * D * DV;
             if (p.trans) {
 #pragma unroll
                 for (int i = 0; i < SC; i += 4)
-                    *reinterpret_cast<float4 *>(st + i) = *reinterpret_cast<const float4 *>(src + (size_t)row * D + half * SC + i);
+                    *reinterpret_cast<float4 *>(st + i) = *reinterpret_cast<const float4 *>(src + (size_t)col * D + half * SC + i);
             } else {
 #pragma unroll
-                for (int i = 0; i < SC; ++i) st[i] = src[(size_t)(half * SC + i) * DV + row];
+                for (int i = 0; i < SC; ++i) st[i] = src[(size_t)(half * SC + i) * DV + col];
             }
         } else {
 #pragma unroll
             for (int i = 0; i < SC; ++i) st[i] = 0.f;
         }
         auto put_state = [&] {   // S^T in bf16, rows of d
-            if (live) {
 #pragma unroll
-                for (int i = 0; i < SC; i += 8) {
-                    const int c = half * SC + i;
-                    *reinterpret_cast<uint4 *>(sS + (c >> 6) * (DV * 128) + sw128_off(row, c & 63)) =
-                        make_uint4(pack_bf16x2(st[i], st[i + 1]), pack_bf16x2(st[i + 2], st[i + 3]),
-                                   pack_bf16x2(st[i + 4], st[i + 5]), pack_bf16x2(st[i + 6], st[i + 7]));
-                }
-                fence_proxy_async();
+            for (int i = 0; i < SC; i += 8) {
+                const int c = half * SC + i;
+                *reinterpret_cast<uint4 *>(sS + part * Lay::kHalfS + (c >> 6) * (DV * 128) + sw128_off(col, c & 63)) =
+                    make_uint4(pack_bf16x2(st[i], st[i + 1]), pack_bf16x2(st[i + 2], st[i + 3]),
+                               pack_bf16x2(st[i + 4], st[i + 5]), pack_bf16x2(st[i + 6], st[i + 7]));
             }
+            fence_proxy_async();
             mbar_arrive(&S.s_ready);
         };
+        if (TWIN) {   // W of the other half's tokens: zeros
+            const uint32_t none[16] = {};
+#pragma unroll
+            for (int i = 0; i < 3; ++i)
+                tmem_st16(tb + lb + kColW3 + i * 64 + (1 - part) * 32 + half * 16, none);
+        }
         bool ok = true;
         for (int n = 0; n < nch; ++n) {
             const int L = length_of(n);
@@ -344,14 +356,14 @@ retain_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
             // W's place is free (where this has not been waited for below)
             if (n >= 1 && NH == 2 && half == 0) ok = ok && mbar_wait<1>(&S.kv_done[1], (n - 1) & 1, g, 21);
             if (!(ok = __all_sync(0xffffffffu, ok))) break;
-            if (live) {
+            {
                 tc_fence_after();
                 const uint8_t *tv = sV + (n & 1) * Lay::kV;
                 uint32_t z0 = 0, z1 = 0;   // 0 v: anything else where v is not finite
                 const int tq = (lane & 3) * 2;
 #pragma unroll 1
-                for (int u = 0; u < 2; ++u) {   // 32 tokens
-                    const int t0 = half * 64 + u * 32;
+                for (int u = 0; u < (TWIN ? 1 : 2); ++u) {   // 32 tokens
+                    const int t0 = TWIN ? part * 64 + half * 32 : half * 64 + u * 32;
                     // weights of tokens t0 + 8 g + tq and + 1 (behind the last token zeros, or of zeros)
                     const float *wp = pw + (REV ? -(t0 + tq + 1) : t0 + tq + 1 - L);
                     float w[8];
@@ -360,7 +372,7 @@ retain_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
 #pragma unroll
                     for (int hl = 0; hl < 2; ++hl) {   // 16 columns of dv
                         uint32_t x[8], hi[8], mi[8], lo[8];
-                        const int c = wq * 4 + hl * 2 + ((lane >> 3) & 1);   // 16-byte chunk of a token's row
+                        const int c = (TWIN ? wq & 1 : wq) * 4 + hl * 2 + ((lane >> 3) & 1);   // 16-byte chunk of a token's row
                         const int t = t0 + (lane >> 4) * 8 + (lane & 7);
                         const uint32_t at = smem_u32(tv) + (c >> 3) * 16384 + t * 128 + (((c & 7) ^ (t & 7)) << 4);
                         ldmatrix_x4_trans(at, x[0], x[1], x[2], x[3]);
@@ -391,7 +403,7 @@ retain_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
             // ---- S' = gamma^L S + K^T W
             ok = __all_sync(0xffffffffu, mbar_wait<1>(&S.kv_done[NH == 2 ? half : 0], n & 1, g, 23));
             if (!ok) break;
-            if (live) {
+            {
                 tc_fence_after();
                 const float gl = pw[-L];
                 const uint64_t g2 = f2pack(gl, gl);
@@ -419,70 +431,80 @@ retain_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
         const bool last = seg == (REV ? 0 : p.nseg - 1);
         float *dst = OUT ? (p.S_out && last ? p.S_out + (size_t)bh * D * DV : nullptr)
                          : p.S_out + ((size_t)bh * p.nseg + seg) * D * DV;
-        if (ok && live && dst) {
+        if (TWIN && dst) {   // the second half's state through where S was, which the last Q S has read
+            if (OUT) ok = __all_sync(0xffffffffu, ok && mbar_wait<1>(&S.qs_done, (nch - 1) & 1, g, 24));
+            float *other = reinterpret_cast<float *>(sS) + half * SC * DV + col;
+            if (ok && part == 1)
+#pragma unroll
+                for (int i = 0; i < SC; ++i) other[i * DV] = st[i];
+            named_bar(1, kState);
+            if (ok && part == 0)
+#pragma unroll
+                for (int i = 0; i < SC; ++i) st[i] += other[i * DV];
+        }
+        if (ok && part == 0 && dst) {
             if (OUT && p.trans) {
 #pragma unroll
                 for (int i = 0; i < SC; i += 4)
-                    *reinterpret_cast<float4 *>(dst + (size_t)row * D + half * SC + i) = make_float4(st[i], st[i + 1], st[i + 2], st[i + 3]);
+                    *reinterpret_cast<float4 *>(dst + (size_t)col * D + half * SC + i) = make_float4(st[i], st[i + 1], st[i + 2], st[i + 3]);
             } else {
 #pragma unroll
-                for (int i = 0; i < SC; ++i) dst[(size_t)(half * SC + i) * DV + row] = st[i];
+                for (int i = 0; i < SC; ++i) dst[(size_t)(half * SC + i) * DV + col] = st[i];
             }
         }
     } else if (OUT) {
         // ------------------------------------------------------------ P~ and y
         const uint32_t pcol = tb + lb + kColP, col = tb + lb + kColY;
-        float nr[16];
+        float nr[16], dg[32];   // gamma^(to a block's nearest column); on the diagonal gamma^|i - j|, and what is kept there
+        uint32_t keep[16];
         load16(S.near, nr);
+#pragma unroll
+        for (int j = 0; j < 32; ++j) dg[j] = (REV ? j >= lane : j <= lane) ? pw[-abs(lane - j)] : 0.f;
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+            keep[j] = ((REV ? 2 * j >= lane : 2 * j <= lane) ? 0xFFFFu : 0u) | ((REV ? 2 * j + 1 >= lane : 2 * j + 1 <= lane) ? 0xFFFF0000u : 0u);
         for (int n = 0; n < nch; ++n) {
             if (!__all_sync(0xffffffffu, mbar_wait<1>(&S.qk_done, n & 1, g, 30))) break;
             {
                 tc_fence_after();
 #pragma unroll 1
-                for (int jb = 0; jb < kTC; jb += 64) {
-                    // over P itself: columns j / 2 of a row that has been read beyond column j
-                    uint32_t x[4][16];
+                for (int jb = 0; jb < kTC; jb += 32) {   // over P itself: columns j / 2 of a row that has been read beyond column j
+                    const int side = jb - 32 * wq;       // warp-uniform
+                    uint32_t x[32], o[16];
+                    if (REV ? side < 0 : side > 0) {     // beyond the diagonal
 #pragma unroll
-                    for (int u = 0; u < 4; ++u) {
-                        const int side = jb + 16 * u - 32 * wq;   // warp-uniform
-                        if (REV ? side >= 0 : side < 32) tmem_ld16(pcol + jb + 16 * u, x[u]);
-                    }
-                    tmem_wait_ld();
+                        for (int j = 0; j < 16; ++j) o[j] = 0u;
+                    } else {
+                        tmem_ld16(pcol + jb, *reinterpret_cast<uint32_t(*)[16]>(x));
+                        tmem_ld16(pcol + jb + 16, *reinterpret_cast<uint32_t(*)[16]>(x + 16));
+                        if (side == 0) {   // bits that are not kept: a score that is not finite leaves nothing of itself
+                            tmem_wait_ld();
 #pragma unroll
-                    for (int u = 0; u < 4; ++u) {
-                        const int j0 = jb + 16 * u, side = j0 - 32 * wq;
-                        uint32_t o[8];
-                        if (REV ? side < 0 : side >= 32) {   // beyond the diagonal
+                            for (int j = 0; j < 16; ++j)
+                                o[j] = pack_bf16x2(dg[2 * j] * u2f(x[2 * j]), dg[2 * j + 1] * u2f(x[2 * j + 1])) & keep[j];
+                        } else {
+                            const float f0 = pw[REV ? row - jb : jb + 15 - row], f1 = pw[REV ? row - jb - 16 : jb + 31 - row];
+                            tmem_wait_ld();
 #pragma unroll
-                            for (int j = 0; j < 8; ++j) o[j] = 0u;
-                        } else if (side < 0 || side >= 32) {   // gamma^|i - j| = gamma^(to the nearest column) near[j]
-                            const float f = pw[REV ? row - j0 : j0 + 15 - row];
-                            const uint64_t f2 = f2pack(f, f);
-#pragma unroll
-                            for (int j = 0; j < 8; ++j) {
+                            for (int j = 0; j < 16; ++j) {
+                                const float f = j < 8 ? f0 : f1;
                                 float a, bb;
-                                f2unpack(f2mul(f2mul(f2, f2pack(nr[2 * j], nr[2 * j + 1])), f2pack(u2f(x[u][2 * j]), u2f(x[u][2 * j + 1]))), a, bb);
+                                f2unpack(f2mul(f2mul(f2pack(f, f), f2pack(nr[2 * j & 15], nr[(2 * j + 1) & 15])),
+                                               f2pack(u2f(x[2 * j]), u2f(x[2 * j + 1]))), a, bb);
                                 o[j] = pack_bf16x2(a, bb);
                             }
-                        } else {
-#pragma unroll
-                            for (int j = 0; j < 8; ++j) {
-                                const int e0 = REV ? j0 + 2 * j - row : row - j0 - 2 * j, e1 = REV ? e0 + 1 : e0 - 1;
-                                const float a = pw[-max(e0, 0)] * u2f(x[u][2 * j]), bb = pw[-max(e1, 0)] * u2f(x[u][2 * j + 1]);
-                                o[j] = pack_bf16x2(e0 >= 0 ? a : 0.f, e1 >= 0 ? bb : 0.f);
-                            }
                         }
-                        tmem_st8(pcol + j0 / 2, o);
                     }
+                    tmem_st16(pcol + jb / 2, o);
                 }
                 tmem_wait_st();
                 tc_fence_before();
                 mbar_arrive(&S.p_ready);
             }
-            if (!__all_sync(0xffffffffu, mbar_wait<1>(&S.qs_done, n & 1, g, 31))) break;
-            {
+            const float f = pw[-max(0, inter_exp(REV, row, length_of(n)))];   // behind the last token: of zeros
+            if (!TWIN) {
+                if (!__all_sync(0xffffffffu, mbar_wait<1>(&S.qs_done, n & 1, g, 31))) break;
                 tc_fence_after();
-                const float f = pw[-max(0, inter_exp(REV, row, length_of(n)))];   // behind the last token: of zeros
                 const uint64_t f2 = f2pack(f, f);
 #pragma unroll 1
                 for (int c = 0; c < DV; c += 64) {
@@ -512,26 +534,31 @@ retain_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
                 tc_fence_after();
                 const bool bad = *(volatile int *)&S.v_bad[n & 1] == n + 1;
 #pragma unroll 1
-                for (int c = 0; c < DV; c += 64) {
-                    uint32_t a[4][16];
+                for (int c = 0; c < DV; c += 32) {
+                    uint32_t a[2][16], e[2][16];
 #pragma unroll
-                    for (int u = 0; u < 4; ++u) tmem_ld16(col + c + 16 * u, a[u]);
+                    for (int u = 0; u < 2; ++u) {
+                        tmem_ld16(col + c + 16 * u, a[u]);
+                        if (TWIN) tmem_ld16(col + 64 + c + 16 * u, e[u]);
+                    }
                     tmem_wait_ld();
 #pragma unroll
-                    for (int u = 0; u < 4; ++u) {
+                    for (int u = 0; u < 2; ++u) {
                         uint32_t o[8];
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) o[j] = pack_bf16x2(u2f(a[u][2 * j]), u2f(a[u][2 * j + 1]));
+                        for (int j = 0; j < 8; ++j)
+                            o[j] = TWIN ? pack_bf16x2(fmaf(f, u2f(a[u][2 * j]), u2f(e[u][2 * j])), fmaf(f, u2f(a[u][2 * j + 1]), u2f(e[u][2 * j + 1])))
+                                        : pack_bf16x2(u2f(a[u][2 * j]), u2f(a[u][2 * j + 1]));
                         if (bad) {
 #pragma unroll
                             for (int j = 0; j < 16; ++j) {
-                                const int f = S.first[n & 1][c + 16 * u + j];
-                                if (REV ? row < f : row >= f) o[j >> 1] |= j & 1 ? 0x7FFF0000u : 0x7FFFu;
+                                const int first = S.first[n & 1][c + 16 * u + j];
+                                if (REV ? row < first : row >= first) o[j >> 1] |= j & 1 ? 0x7FFF0000u : 0x7FFFu;
                             }
                         }
 #pragma unroll
                         for (int j = 0; j < 8; j += 4)
-                            *reinterpret_cast<uint4 *>(sY + (c >> 6) * 16384 + sw128_off(row, 16 * u + 2 * j)) =
+                            *reinterpret_cast<uint4 *>(sY + (c >> 6) * 16384 + sw128_off(row, (c & 32) + 16 * u + 2 * j)) =
                                 make_uint4(o[j], o[j + 1], o[j + 2], o[j + 3]);
                     }
                 }
