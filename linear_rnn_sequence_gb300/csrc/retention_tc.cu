@@ -17,7 +17,9 @@
 //                accumulator (d = 64: there is one), P~ V, then the next block's Q K^T;
 //   warp 13      issues the copies.
 // W is the one operand without a second place in TMEM: its three pieces, the halves of K^T W and the state's update
-// between them are the chain that bounds a block.
+// between them are the chain that bounds a block, about 5,000 cycles of which the products take 3,070; at d = dv = 128 and a CTA
+// on most SMs HBM bounds it as nearly.  B8 H16 N8192 d128: 177 us, 6.1 TB/s of the 6.7 that a copy reaches (152 heads: 6.3);
+// d64: 123 us, 4.4 TB/s; B1 H32 N131072 d64, in 19 segments: 668 us.
 //
 // With dv = 64 the upper 64 TMEM lanes hold W of the block's second 64 tokens (and zeros for the first, as the lower ones do for
 // the second), so that every warp makes half as much of it; the lanes' sums stay two states that add up to S, and Q S takes
@@ -579,7 +581,8 @@ retain_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
 
 // Segments of a head.  Splitting pays where the heads leave SMs idle: the segments' own sums come first (a block of
 // them costs about 0.6 of a whole one), their ends are joined, and every segment runs from its state.  In units of a
-// block's time, about 2.3 us: a wave of CTAs takes its segments' length, the extra launches and starts about 6.
+// block's time, about 2.2 us: a wave of CTAs takes its segments' length, the extra launches and starts about 3 (gradients of
+// 24 heads of 9 blocks: 79 us split in three, 83 whole; 8 heads of 8 blocks forward: 29 and 33).
 void retain_segments(const RetainArgs &a, int &nseg, int &seg_blocks) {
     const int nblk = (a.N + kTC - 1) / kTC, sms = num_sms();
     const long long BH = (long long)a.B * a.H;
@@ -591,7 +594,7 @@ void retain_segments(const RetainArgs &a, int &nseg, int &seg_blocks) {
     for (int s = 2; s <= 64 && s <= nblk; ++s) {
         const int len = (nblk + s - 1) / s, n = (nblk + len - 1) / len;
         if (n != s) continue;
-        const double cost = 1.6 * waves(BH * s) * len + 6;
+        const double cost = 1.6 * waves(BH * s) * len + 3;
         if (cost < best) {
             best = cost;
             nseg = s;

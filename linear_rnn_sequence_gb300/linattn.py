@@ -877,6 +877,8 @@ def _rotate_plan(qs, ks, dtype, strides, freq, positions, norm, wq, wk, pairs, l
     flat = []
     for i, st in enumerate(strides):
         shape = ks if i % 2 else qs
+        if st is not None and len(st) != len(shape):
+            raise ValueError("all tensors must have as many dimensions as q")
         if st is None:
             st = [1] * len(shape)
             for x in reversed(range(len(shape) - 1)):

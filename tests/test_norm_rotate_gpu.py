@@ -272,7 +272,7 @@ def test_refusals():
     for bad in (dict(layout="hbnd"), dict(norm="max"), dict(pairs="thirds"), dict(positions=kw["positions"].int()),
                 dict(positions=kw["positions"][:1]), dict(positions=kw["positions"].cpu()), dict(freq=kw["freq"].float()),
                 dict(freq=kw["freq"][None]), dict(q_weight=kw["q_weight"][:32]), dict(k_weight=kw["k_weight"].bfloat16()),
-                dict(out=(q.float(), k)), dict(out=(q[:1], k))):
+                dict(out=(q.float(), k)), dict(out=(q[:1], k)), dict(out=(q[0], k)), dict(out=(q, k[..., None]))):
         with pytest.raises((ValueError, TypeError)):
             la.norm_rotate(q, k, **{**kw, **bad})
     for a, b in ((q, k.float()), (q, k[:, :, :4]), (q, k[:1]), (q, k[..., :32]), (q[0], k), (q[0, 0], k[0, 0]),
