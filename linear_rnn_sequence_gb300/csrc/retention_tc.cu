@@ -46,8 +46,10 @@ namespace {
 constexpr int kTC = 128;                      // tokens of a block
 constexpr int kState = 256, kRetThr = 14 * 32;   // threads: of the state's warps, all
 
-// TMEM columns: P (P~ over its first half), y, half of K^T W, three pieces of W.
+// TMEM columns: P (P~ over its first half), y, half of K^T W, three pieces of W.  For the segments' sums alone: K^T W, and W
+// twice, so that the next one is made while the products of this one run.
 constexpr uint32_t kColP = 0, kColY = 128, kColKV = 256, kColW3 = 320;
+constexpr uint32_t kColSumW = 128;   // K^T W from column 0, W from 128 and 320 on
 
 struct RetainTc {
     const float *gamma, *S_in;
@@ -62,7 +64,7 @@ struct RetainTc {
 
 struct RetainSmall {
     uint64_t q_full[2], k_full[2], v_full[2], pv_done[2], y_written[2], kv_done[2], kv_read, qk_done, p_ready, s_ready,
-        qs_done, y_scaled, y_free, w_ready, drain;
+        qs_done, y_scaled, y_free, w_ready[2], drain;   // w_ready[1], and kv_read by all: kSums
     float pg[2 * kTC + 4];        // pg[kTC - n] = gamma^n, zeros behind
     alignas(16) float near[16];   // gamma^(15 - j) (REV: gamma^j)
     int v_bad[2];                 // block index + 1 of a block with a value that is not finite
@@ -126,14 +128,15 @@ retain_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
             mbar_init(&S.y_written[i], 128);
             mbar_init(&S.kv_done[i], 1);
         }
-        mbar_init(&S.kv_read, kState / 2);
+        mbar_init(&S.kv_read, OUT ? kState / 2 : kState);
         mbar_init(&S.qk_done, 1);
         mbar_init(&S.p_ready, 128);
         mbar_init(&S.s_ready, kState);
         mbar_init(&S.qs_done, 1);
         mbar_init(&S.y_scaled, 128);
         mbar_init(&S.y_free, 128);
-        mbar_init(&S.w_ready, kState);
+        mbar_init(&S.w_ready[0], kState);
+        mbar_init(&S.w_ready[1], kState);
         mbar_init(&S.drain, 1);
         fence_mbar_init();
         prefetch_tmap(&kmap);
@@ -222,6 +225,7 @@ retain_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
         bool ok = true;
         auto all = [&](bool x) { ok = ok && __all_sync(0xffffffffu, x); };
         auto kv_half = [&](int n, int half) {   // (K^T W)^T, 64 columns of d
+            const uint32_t to = OUT ? tb + kColKV : tb + half * 64, w = tb + (OUT ? kColW3 : kColSumW + (n & 1) * 192);
             const uint32_t leader = elect_leader();
             tc_fence_after();
             const uint64_t kd = smem_desc(smem_u32(sK) + (n & 1) * Lay::kQ + half * 16384, 16384, 1024, kSwizzle128B);
@@ -229,8 +233,8 @@ retain_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
             for (int pc = 2; pc >= 0; --pc)
 #pragma unroll
                 for (int ks = 0; ks < kTC / 16; ++ks)
-                    mma_ts_if(leader, tb + kColKV, tb + kColW3 + pc * 64 + ks * 8, kd + ks * 128, iKV, pc < 2 || ks > 0);
-            mma_commit_if(leader, &S.kv_done[half]);
+                    mma_ts_if(leader, to, w + pc * 64 + ks * 8, kd + ks * 128, iKV, pc < 2 || ks > 0);
+            if (OUT || half == NH - 1) mma_commit_if(leader, &S.kv_done[OUT ? half : 0]);
         };
         auto scores = [&](int n) {
             const int s = n & 1, ph = (n >> 1) & 1;
@@ -267,8 +271,17 @@ retain_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
         if (OUT) scores(0);
         for (int n = 0; n < nch && ok; ++n) {
             const int s = n & 1;
-            if (!OUT) all(mbar_wait<1>(&S.k_full[s], (n >> 1) & 1, g, 3));
-            all(mbar_wait<1>(&S.w_ready, n & 1, g, 5));
+            if (!OUT) {
+                all(mbar_wait<1>(&S.k_full[s], (n >> 1) & 1, g, 3));
+                all(mbar_wait<1>(&S.w_ready[s], (n >> 1) & 1, g, 5));
+                if (n >= 1) all(mbar_wait<1>(&S.kv_read, (n - 1) & 1, g, 8));
+                if (!ok) break;
+                for (int half = 0; half < NH; ++half) kv_half(n, half);
+                const uint32_t leader = elect_leader();
+                mma_commit_if(leader, &S.pv_done[s]);
+                continue;
+            }
+            all(mbar_wait<1>(&S.w_ready[0], n & 1, g, 5));
             if (!ok) break;
             kv_half(n, 0);
             if (OUT) {
@@ -304,9 +317,6 @@ retain_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
                     mma_ts_if(leader, tb + kColY + (TWIN ? 64 : 0), tb + kColP + ks * 8, vd + ks * 128, iPV, !TWIN || ks > 0);
                 mma_commit_if(leader, &S.pv_done[s]);
                 if (n + 1 < nch) scores(n + 1);
-            } else {
-                const uint32_t leader = elect_leader();
-                mma_commit_if(leader, &S.pv_done[s]);
             }
         }
         if (elect_leader()) {
@@ -348,86 +358,99 @@ retain_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
         if (TWIN) {   // W of the other half's tokens: zeros
             const uint32_t none[16] = {};
 #pragma unroll
-            for (int i = 0; i < 3; ++i)
-                tmem_st16(tb + lb + kColW3 + i * 64 + (1 - part) * 32 + half * 16, none);
+            for (int i = 0; i < (OUT ? 3 : 6); ++i)
+                tmem_st16(tb + lb + (OUT ? kColW3 : kColSumW) + i * 64 + (1 - part) * 32 + half * 16, none);
         }
         bool ok = true;
-        for (int n = 0; n < nch; ++n) {
+        auto wait_v = [&](int n) { return mbar_wait<1>(&S.v_full[n & 1], (n >> 1) & 1, g, 20); };
+        auto make_w = [&](int n, uint32_t at_w) {
             const int L = length_of(n);
-            ok = ok && mbar_wait<1>(&S.v_full[n & 1], (n >> 1) & 1, g, 20);
+            tc_fence_after();
+            const uint8_t *tv = sV + (n & 1) * Lay::kV;
+            uint32_t z0 = 0, z1 = 0;   // 0 v: anything else where v is not finite
+            const int tq = (lane & 3) * 2;
+#pragma unroll 1
+            for (int u = 0; u < (TWIN ? 1 : 2); ++u) {   // 32 tokens
+                const int t0 = TWIN ? part * 64 + half * 32 : half * 64 + u * 32;
+                // weights of tokens t0 + 8 g + tq and + 1 (behind the last token zeros, or of zeros)
+                const float *wp = pw + (REV ? -(t0 + tq + 1) : t0 + tq + 1 - L);
+                float w[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) w[k] = wp[(REV ? -1 : 1) * ((k >> 1) * 8 + (k & 1))];
+#pragma unroll
+                for (int hl = 0; hl < 2; ++hl) {   // 16 columns of dv
+                    uint32_t x[8], hi[8], mi[8], lo[8];
+                    const int c = (TWIN ? wq & 1 : wq) * 4 + hl * 2 + ((lane >> 3) & 1);   // 16-byte chunk of a token's row
+                    const int t = t0 + (lane >> 4) * 8 + (lane & 7);
+                    const uint32_t at = smem_u32(tv) + (c >> 3) * 16384 + t * 128 + (((c & 7) ^ (t & 7)) << 4);
+                    ldmatrix_x4_trans(at, x[0], x[1], x[2], x[3]);
+                    ldmatrix_x4_trans(at + 16 * 128, x[4], x[5], x[6], x[7]);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {   // tokens 8 (k / 2) + tq and + 1, column lane / 4 + 8 (k % 2)
+                        if (OUT && NH == 1) (k & 1 ? z1 : z0) = fma_bf16x2(x[k], 0u, k & 1 ? z1 : z0);
+                        pieces3(w[k & 6] * bf16_lo_f(x[k]), w[(k & 6) + 1] * bf16_hi_f(x[k]), hi[k], mi[k], lo[k]);
+                    }
+                    const uint32_t to = tb + lb + ((uint32_t)hl << 20) + at_w + t0 / 2;
+                    tmem_st_16x128b_x4(to, hi);
+                    tmem_st_16x128b_x4(to + 64, mi);
+                    tmem_st_16x128b_x4(to + 128, lo);
+                }
+            }
+            if (OUT && NH == 1 && ((z0 | z1) & 0x7FFF7FFFu)) S.v_bad[n & 1] = n + 1;
+            tmem_wait_st();
+            tc_fence_before();
+        };
+        auto update = [&](int n, uint32_t at_kv) {   // S' = gamma^L S + K^T W
+            tc_fence_after();
+            const float gl = pw[-length_of(n)];
+            const uint64_t g2 = f2pack(gl, gl);
+#pragma unroll
+            for (int i = 0; i < SC; i += 32) {
+                uint32_t a0[16], a1[16];
+                const uint32_t from = tb + lb + at_kv + i;
+                tmem_ld16(from, a0);
+                tmem_ld16(from + 16, a1);
+                tmem_wait_ld();
+                // a value of v that is not finite leaves nothing finite here (a value of k may, too)
+                if (OUT && NH == 2 && i == 0 && half == 0 && !finite(u2f(a0[0]))) S.v_bad[n & 1] = n + 1;
+#pragma unroll
+                for (int j = 0; j < 16; j += 2) {
+                    f2unpack(f2fma(g2, f2pack(st[i + j], st[i + j + 1]), f2pack(u2f(a0[j]), u2f(a0[j + 1]))), st[i + j],
+                             st[i + j + 1]);
+                    f2unpack(f2fma(g2, f2pack(st[i + 16 + j], st[i + 17 + j]), f2pack(u2f(a1[j]), u2f(a1[j + 1]))),
+                             st[i + 16 + j], st[i + 17 + j]);
+                }
+            }
+            tc_fence_before();
+        };
+        if (!OUT) {   // the next W before this block's sum is waited for
+            for (int n = -1; n < nch; ++n) {
+                if (n + 1 < nch) {   // its place: the sum before the last has been waited for
+                    if (!(ok = __all_sync(0xffffffffu, wait_v(n + 1)))) break;
+                    make_w(n + 1, kColSumW + ((n + 1) & 1) * 192);
+                    mbar_arrive(&S.w_ready[(n + 1) & 1]);
+                }
+                if (n < 0) continue;
+                if (!(ok = __all_sync(0xffffffffu, mbar_wait<1>(&S.kv_done[0], n & 1, g, 23)))) break;
+                update(n, half * SC);
+                mbar_arrive(&S.kv_read);
+            }
+        }
+        for (int n = 0; OUT && n < nch; ++n) {
+            ok = wait_v(n);
             // W's place is free (where this has not been waited for below)
             if (n >= 1 && NH == 2 && half == 0) ok = ok && mbar_wait<1>(&S.kv_done[1], (n - 1) & 1, g, 21);
             if (!(ok = __all_sync(0xffffffffu, ok))) break;
-            {
-                tc_fence_after();
-                const uint8_t *tv = sV + (n & 1) * Lay::kV;
-                uint32_t z0 = 0, z1 = 0;   // 0 v: anything else where v is not finite
-                const int tq = (lane & 3) * 2;
-#pragma unroll 1
-                for (int u = 0; u < (TWIN ? 1 : 2); ++u) {   // 32 tokens
-                    const int t0 = TWIN ? part * 64 + half * 32 : half * 64 + u * 32;
-                    // weights of tokens t0 + 8 g + tq and + 1 (behind the last token zeros, or of zeros)
-                    const float *wp = pw + (REV ? -(t0 + tq + 1) : t0 + tq + 1 - L);
-                    float w[8];
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) w[k] = wp[(REV ? -1 : 1) * ((k >> 1) * 8 + (k & 1))];
-#pragma unroll
-                    for (int hl = 0; hl < 2; ++hl) {   // 16 columns of dv
-                        uint32_t x[8], hi[8], mi[8], lo[8];
-                        const int c = (TWIN ? wq & 1 : wq) * 4 + hl * 2 + ((lane >> 3) & 1);   // 16-byte chunk of a token's row
-                        const int t = t0 + (lane >> 4) * 8 + (lane & 7);
-                        const uint32_t at = smem_u32(tv) + (c >> 3) * 16384 + t * 128 + (((c & 7) ^ (t & 7)) << 4);
-                        ldmatrix_x4_trans(at, x[0], x[1], x[2], x[3]);
-                        ldmatrix_x4_trans(at + 16 * 128, x[4], x[5], x[6], x[7]);
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) {   // tokens 8 (k / 2) + tq and + 1, column lane / 4 + 8 (k % 2)
-                            if (OUT && NH == 1) (k & 1 ? z1 : z0) = fma_bf16x2(x[k], 0u, k & 1 ? z1 : z0);
-                            pieces3(w[k & 6] * bf16_lo_f(x[k]), w[(k & 6) + 1] * bf16_hi_f(x[k]), hi[k], mi[k], lo[k]);
-                        }
-                        const uint32_t to = tb + lb + ((uint32_t)hl << 20) + kColW3 + t0 / 2;
-                        tmem_st_16x128b_x4(to, hi);
-                        tmem_st_16x128b_x4(to + 64, mi);
-                        tmem_st_16x128b_x4(to + 128, lo);
-                    }
-                }
-                if (OUT && NH == 1 && ((z0 | z1) & 0x7FFF7FFFu)) S.v_bad[n & 1] = n + 1;
-                tmem_wait_st();
-                tc_fence_before();
+            make_w(n, kColW3);
+            mbar_arrive(&S.w_ready[0]);
+            if (NH == 1 && n >= 1) {   // Q S of the block before has read its operand (else K^T W's end says so)
+                ok = __all_sync(0xffffffffu, mbar_wait<1>(&S.qs_done, (n - 1) & 1, g, 22));
+                if (!ok) break;
             }
-            mbar_arrive(&S.w_ready);
-            if (OUT) {
-                if (NH == 1 && n >= 1) {   // Q S of the block before has read its operand (else K^T W's end says so)
-                    ok = __all_sync(0xffffffffu, mbar_wait<1>(&S.qs_done, (n - 1) & 1, g, 22));
-                    if (!ok) break;
-                }
-                put_state();
-            }
-            // ---- S' = gamma^L S + K^T W
+            put_state();
             ok = __all_sync(0xffffffffu, mbar_wait<1>(&S.kv_done[NH == 2 ? half : 0], n & 1, g, 23));
             if (!ok) break;
-            {
-                tc_fence_after();
-                const float gl = pw[-L];
-                const uint64_t g2 = f2pack(gl, gl);
-#pragma unroll
-                for (int i = 0; i < SC; i += 32) {
-                    uint32_t a0[16], a1[16];
-                    const uint32_t from = tb + lb + kColKV + (NH == 2 ? 0 : half * SC) + i;
-                    tmem_ld16(from, a0);
-                    tmem_ld16(from + 16, a1);
-                    tmem_wait_ld();
-                    // a value of v that is not finite leaves nothing finite here (a value of k may, too)
-                    if (OUT && NH == 2 && i == 0 && half == 0 && !finite(u2f(a0[0]))) S.v_bad[n & 1] = n + 1;
-#pragma unroll
-                    for (int j = 0; j < 16; j += 2) {
-                        f2unpack(f2fma(g2, f2pack(st[i + j], st[i + j + 1]), f2pack(u2f(a0[j]), u2f(a0[j + 1]))), st[i + j],
-                                 st[i + j + 1]);
-                        f2unpack(f2fma(g2, f2pack(st[i + 16 + j], st[i + 17 + j]), f2pack(u2f(a1[j]), u2f(a1[j + 1]))),
-                                 st[i + 16 + j], st[i + 17 + j]);
-                    }
-                }
-                tc_fence_before();
-            }
+            update(n, kColKV + (NH == 2 ? 0 : half * SC));
             if (NH == 2 && half == 0) mbar_arrive(&S.kv_read);
         }
         const bool last = seg == (REV ? 0 : p.nseg - 1);
