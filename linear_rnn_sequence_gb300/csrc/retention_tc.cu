@@ -18,8 +18,8 @@
 //   warp 13      issues the copies.
 // W is the one operand without a second place in TMEM: its three pieces, the halves of K^T W and the state's update
 // between them are the chain that bounds a block, about 5,000 cycles of which the products take 3,070; at d = dv = 128 and a CTA
-// on most SMs HBM bounds it as nearly.  B8 H16 N8192 d128: 177 us, 6.1 TB/s of the 6.7 that a copy reaches (152 heads: 6.3);
-// d64: 123 us, 4.4 TB/s; B1 H32 N131072 d64, in 19 segments: 668 us.
+// on most SMs HBM bounds it as nearly.  B8 H16 N8192 d128: 177 us, 6.1 TB/s of the 6.7 that a copy reaches (152 heads: 6.4);
+// d64: 111 us, 4.8 TB/s; B1 H32 N131072 d64, in 19 segments: 560 us.
 //
 // With dv = 64 the upper 64 TMEM lanes hold W of the block's second 64 tokens (and zeros for the first, as the lower ones do for
 // the second), so that every warp makes half as much of it; the lanes' sums stay two states that add up to S, and Q S takes
@@ -62,8 +62,9 @@ struct RetainTc {
     int drop_item;
 };
 
+constexpr int kMostStages = 4;
 struct RetainSmall {
-    uint64_t q_full[2], k_full[2], v_full[2], pv_done[2], y_written[2], kv_done[2], kv_read, qk_done, p_ready, s_ready,
+    uint64_t q_full[kMostStages], k_full[kMostStages], v_full[kMostStages], pv_done[kMostStages], y_written[kMostStages], kv_done[2], kv_read, qk_done, p_ready, s_ready,
         qs_done, y_scaled, y_free, w_ready[2], drain;   // w_ready[1], and kv_read by all: kSums
     float pg[2 * kTC + 4];        // pg[kTC - n] = gamma^n, zeros behind
     alignas(16) float near[16];   // gamma^(15 - j) (REV: gamma^j)
@@ -73,13 +74,21 @@ struct RetainSmall {
     volatile int abort_flag;
 };
 
-template <int D, int DV> struct RetainLay {
+// What a launch computes: y from each segment's state; each segment's own sum.
+enum RetainMode { kWhole, kSums };
+
+template <int D, int DV, int MODE> struct RetainLay {
+    static constexpr bool OUT = MODE == kWhole;
     static constexpr int kQ = (D / 64) * 16384, kV = (DV / 64) * 16384;
-    static constexpr int kHalfS = DV * D * 2, kS = (128 / DV) * kHalfS;
-    static constexpr bool ownY = DV > D;      // y does not fit where Q was
-    static constexpr int oQ = 0, oK = oQ + 2 * kQ, oV = oK + 2 * kQ, oS = oV + 2 * kV, oY = oS + kS,
+    static constexpr int kHalfS = DV * D * 2, kS = OUT ? (128 / DV) * kHalfS : DV * D * 4;
+    static constexpr bool ownY = OUT && DV > D;      // y does not fit where Q was
+    // blocks in flight: as many as fit, four at most (d64: 111 us with four, 124 with two; B1 H32 N131072 d64 560 and 670)
+    static constexpr int kBlock = (OUT ? 2 : 1) * kQ + kV, kFixed = kS + (ownY ? 2 * kV : 0) + 1024 + (int)sizeof(RetainSmall);
+    static constexpr int kFit = (232448 - kFixed) / kBlock, kNst = kFit < kMostStages ? kFit : kMostStages;
+    static constexpr int oQ = 0, oK = oQ + (OUT ? kNst * kQ : 0), oV = oK + kNst * kQ, oS = oV + kNst * kV, oY = oS + kS,
                          oSmall = oY + (ownY ? 2 * kV : 0);
     static constexpr int request = oSmall + (int)sizeof(RetainSmall) + 1024;
+    static_assert(kNst >= 2 && (!ownY || kNst == 2), "y of its own has two places");
 };
 
 // Three pieces of a pair by truncation, as split3, at two thirds of its time: the logical operations that take a piece
@@ -92,7 +101,6 @@ __device__ __forceinline__ void pieces3(float x0, float x1, uint32_t &h, uint32_
     l = __byte_perm(f2u(minus_bf16_lo(x0, m)), f2u(minus_bf16_hi(x1, m)), 0x7632);
 }
 
-enum RetainMode { kWhole, kSums };   // y from each segment's state; each segment's own sum
 
 __device__ __forceinline__ uint8_t *retain_smem() {
     extern __shared__ uint8_t smem_raw[];
@@ -103,8 +111,9 @@ template <int D, int DV, bool REV, int MODE>
 __global__ void __launch_bounds__(kRetThr, 1)
 retain_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                  const __grid_constant__ CUtensorMap vmap, const __grid_constant__ CUtensorMap ymap, const RetainTc p) {
-    using Lay = RetainLay<D, DV>;
+    using Lay = RetainLay<D, DV, MODE>;
     constexpr bool OUT = MODE == kWhole;
+    constexpr int NST = Lay::kNst;
     constexpr int NH = D / 64;   // halves of K^T W
     constexpr bool TWIN = DV == 64;   // two states, of the tokens' halves; Q S and P~ V in accumulators of their own
     uint8_t *sm = retain_smem();
@@ -120,14 +129,15 @@ retain_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
     if (tid == 0) {
         S.abort_flag = 0;
         S.v_bad[0] = S.v_bad[1] = 0;
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < NST; ++i) {
             mbar_init(&S.q_full[i], 1);
             mbar_init(&S.k_full[i], 1);
             mbar_init(&S.v_full[i], 1);
             mbar_init(&S.pv_done[i], 1);
             mbar_init(&S.y_written[i], 128);
-            mbar_init(&S.kv_done[i], 1);
         }
+        mbar_init(&S.kv_done[0], 1);
+        mbar_init(&S.kv_done[1], 1);
         mbar_init(&S.kv_read, OUT ? kState / 2 : kState);
         mbar_init(&S.qk_done, 1);
         mbar_init(&S.p_ready, 128);
@@ -158,7 +168,8 @@ retain_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
     const uint32_t lb = (uint32_t)(wq * 32) << 16;
     const float *pw = S.pg + kTC;   // pw[-n] = gamma^n
     uint8_t *sQ = sm + Lay::oQ, *sK = sm + Lay::oK, *sV = sm + Lay::oV, *sS = sm + Lay::oS;
-    auto y_tile = [&](int n) { return Lay::ownY ? sm + Lay::oY + (n & 1) * Lay::kV : sQ + (n & 1) * Lay::kQ; };
+    auto y_tile = [&](int n) { return Lay::ownY ? sm + Lay::oY + (n % NST) * Lay::kV : sQ + (n % NST) * Lay::kQ; };
+    auto turn = [](int n) { return (uint32_t)(n / NST) & 1u; };   // parity of block n's use of its place
 
     if (warp == 13) {
         // ------------------------------------------------------------ copies
@@ -169,7 +180,7 @@ retain_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
                 for (int f = 0; f < slabs; ++f) tma_load_4d(dst + f * 16384, &m, bar, f * 64, token_of(n), h, b);
             };
             auto store = [&](int n) {   // y of a block, when it is written
-                if (!mbar_wait<1>(&S.y_written[n & 1], (n >> 1) & 1, g, 1)) return false;
+                if (!mbar_wait<1>(&S.y_written[n % NST], turn(n), g, 1)) return false;
 #pragma unroll
                 for (int f = 0; f < DV / 64; ++f) tma_store_4d(&ymap, y_tile(n) + f * 16384, f * 64, token_of(n), h, b);
                 bulk_commit();
@@ -178,23 +189,23 @@ retain_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
             int n = 0;
             bool q_too = true;   // of block n - 1
             for (; n < nch; ++n) {
-                const int s = n & 1, ph = (n >> 1) & 1;
-                // the block before the last has been used: its last product is P~ V
-                if (n >= 2 && !mbar_wait<1>(&S.pv_done[s], ph ^ 1, g, 2)) break;
+                const int s = n % NST;
+                // the block before it there has been used: its last product is P~ V
+                if (n >= NST && !mbar_wait<1>(&S.pv_done[s], turn(n) ^ 1u, g, 2)) break;
                 load(sK + s * Lay::kQ, kmap, &S.k_full[s], D / 64, n, n == 0 && (int)blockIdx.x == p.drop_item);
                 load(sV + s * Lay::kV, vmap, &S.v_full[s], DV / 64, n, false);
-                // the next one into L2, while its places are still taken (d = 128, B8 H16 N8192: 190 us with and 205 without;
-                // d = 64, whose blocks come in time anyway: 149 and 142)
-                if (D > 64 && n >= 1 && n + 1 < nch) {
+                // the next one into L2, while its places are still taken (d = 128, B8 H16 N8192: 190 us with and 205 without; with
+                // d = 64 more blocks are in flight, and it cost 7 us of 142 when there were two)
+                if (OUT && D > 64 && n >= 1 && n + 1 < nch) {
                     for (int f = 0; f < D / 64; ++f) {
                         tma_prefetch_4d(&kmap, f * 64, token_of(n + 1), h, b);
-                        if (OUT) tma_prefetch_4d(&qmap, f * 64, token_of(n + 1), h, b);
+                        tma_prefetch_4d(&qmap, f * 64, token_of(n + 1), h, b);
                     }
                     for (int f = 0; f < DV / 64; ++f) tma_prefetch_4d(&vmap, f * 64, token_of(n + 1), h, b);
                 }
                 if (OUT) {
-                    if (n >= 2) {
-                        if (!store(n - 2)) {
+                    if (n >= NST) {
+                        if (!store(n - NST)) {
                             q_too = false;
                             ++n;
                             break;
@@ -206,15 +217,15 @@ retain_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
             }
             if (OUT) {
                 if (n == nch && q_too)
-                    for (int m = max(0, nch - 2); m < nch; ++m)
+                    for (int m = max(0, nch - NST); m < nch; ++m)
                         if (!store(m)) break;
                 bulk_wait<0>();
             }
             // what is in flight lands (after a wait that ran out; otherwise it has been used)
-            for (int m = max(0, n - 2); m < n; ++m) {
-                if (!(m == 0 && (int)blockIdx.x == p.drop_item)) drain_wait(&S.k_full[m & 1], (m >> 1) & 1, g.limit_ns);
-                drain_wait(&S.v_full[m & 1], (m >> 1) & 1, g.limit_ns);
-                if (OUT && (q_too || m < n - 1)) drain_wait(&S.q_full[m & 1], (m >> 1) & 1, g.limit_ns);
+            for (int m = max(0, n - NST); m < n; ++m) {
+                if (!(m == 0 && (int)blockIdx.x == p.drop_item)) drain_wait(&S.k_full[m % NST], turn(m), g.limit_ns);
+                drain_wait(&S.v_full[m % NST], turn(m), g.limit_ns);
+                if (OUT && (q_too || m < n - 1)) drain_wait(&S.q_full[m % NST], turn(m), g.limit_ns);
             }
         }
         __syncwarp();
@@ -228,7 +239,7 @@ retain_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
             const uint32_t to = OUT ? tb + kColKV : tb + half * 64, w = tb + (OUT ? kColW3 : kColSumW + (n & 1) * 192);
             const uint32_t leader = elect_leader();
             tc_fence_after();
-            const uint64_t kd = smem_desc(smem_u32(sK) + (n & 1) * Lay::kQ + half * 16384, 16384, 1024, kSwizzle128B);
+            const uint64_t kd = smem_desc(smem_u32(sK) + (n % NST) * Lay::kQ + half * 16384, 16384, 1024, kSwizzle128B);
 #pragma unroll 1
             for (int pc = 2; pc >= 0; --pc)
 #pragma unroll
@@ -237,9 +248,9 @@ retain_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
             if (OUT || half == NH - 1) mma_commit_if(leader, &S.kv_done[OUT ? half : 0]);
         };
         auto scores = [&](int n) {
-            const int s = n & 1, ph = (n >> 1) & 1;
-            all(mbar_wait<1>(&S.k_full[s], ph, g, 3));
-            all(mbar_wait<1>(&S.q_full[s], ph, g, 4));
+            const int s = n % NST;
+            all(mbar_wait<1>(&S.k_full[s], turn(n), g, 3));
+            all(mbar_wait<1>(&S.q_full[s], turn(n), g, 4));
             if (!ok) return;
             const uint32_t leader = elect_leader();
             tc_fence_after();
@@ -254,7 +265,7 @@ retain_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
         // A block with a value of v that is not finite: zero in shared memory, and where the columns' first ones are.
         auto mend_v = [&](int n) {
             for (int c = lane; c < DV; c += 32) {
-                uint8_t *col = sV + (n & 1) * Lay::kV + (c >> 6) * 16384 + (c & 7) * 2;
+                uint8_t *col = sV + (n % NST) * Lay::kV + (c >> 6) * 16384 + (c & 7) * 2;
                 int f = REV ? 0 : kTC;
                 for (int t = 0; t < kTC; ++t) {
                     uint16_t *v = reinterpret_cast<uint16_t *>(col + t * 128 + ((((c & 63) >> 3) ^ (t & 7)) << 4));
@@ -270,10 +281,10 @@ retain_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
         };
         if (OUT) scores(0);
         for (int n = 0; n < nch && ok; ++n) {
-            const int s = n & 1;
+            const int s = n % NST;
             if (!OUT) {
-                all(mbar_wait<1>(&S.k_full[s], (n >> 1) & 1, g, 3));
-                all(mbar_wait<1>(&S.w_ready[s], (n >> 1) & 1, g, 5));
+                all(mbar_wait<1>(&S.k_full[s], turn(n), g, 3));
+                all(mbar_wait<1>(&S.w_ready[n & 1], (n >> 1) & 1, g, 5));
                 if (n >= 1) all(mbar_wait<1>(&S.kv_read, (n - 1) & 1, g, 8));
                 if (!ok) break;
                 for (int half = 0; half < NH; ++half) kv_half(n, half);
@@ -284,10 +295,10 @@ retain_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
             all(mbar_wait<1>(&S.w_ready[0], n & 1, g, 5));
             if (!ok) break;
             kv_half(n, 0);
-            if (OUT) {
-                all(mbar_wait<1>(&S.s_ready, n & 1, g, 6));
-                if (n >= 1) all(mbar_wait<1>(&S.y_free, (n - 1) & 1, g, 7));
-                if (!ok) break;
+            all(mbar_wait<1>(&S.s_ready, n & 1, g, 6));
+            if (n >= 1) all(mbar_wait<1>(&S.y_free, (n - 1) & 1, g, 7));
+            if (!ok) break;
+            {
                 const uint32_t leader = elect_leader();
                 tc_fence_after();
                 const uint64_t qd = desc_k(smem_u32(sQ) + s * Lay::kQ), sd = desc_k(smem_u32(sS));
@@ -304,11 +315,11 @@ retain_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
                 if (!ok) break;
                 kv_half(n, 1);
             }
-            if (OUT && *(volatile int *)&S.v_bad[s] == n + 1) mend_v(n);
-            if (OUT) {
-                all(mbar_wait<1>(&S.p_ready, n & 1, g, 9));
-                if (!TWIN) all(mbar_wait<1>(&S.y_scaled, n & 1, g, 10));
-                if (!ok) break;
+            if (*(volatile int *)&S.v_bad[n & 1] == n + 1) mend_v(n);
+            all(mbar_wait<1>(&S.p_ready, n & 1, g, 9));
+            if (!TWIN) all(mbar_wait<1>(&S.y_scaled, n & 1, g, 10));
+            if (!ok) break;
+            {
                 const uint32_t leader = elect_leader();
                 tc_fence_after();
                 const uint64_t vd = smem_desc(smem_u32(sV) + s * Lay::kV, 16384, 1024, kSwizzle128B);
@@ -316,8 +327,8 @@ retain_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
                 for (int ks = 0; ks < kTC / 16; ++ks)
                     mma_ts_if(leader, tb + kColY + (TWIN ? 64 : 0), tb + kColP + ks * 8, vd + ks * 128, iPV, !TWIN || ks > 0);
                 mma_commit_if(leader, &S.pv_done[s]);
-                if (n + 1 < nch) scores(n + 1);
             }
+            if (n + 1 < nch) scores(n + 1);
         }
         if (elect_leader()) {
             mma_commit(&S.drain);
@@ -362,11 +373,11 @@ retain_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
                 tmem_st16(tb + lb + (OUT ? kColW3 : kColSumW) + i * 64 + (1 - part) * 32 + half * 16, none);
         }
         bool ok = true;
-        auto wait_v = [&](int n) { return mbar_wait<1>(&S.v_full[n & 1], (n >> 1) & 1, g, 20); };
+        auto wait_v = [&](int n) { return mbar_wait<1>(&S.v_full[n % NST], turn(n), g, 20); };
         auto make_w = [&](int n, uint32_t at_w) {
             const int L = length_of(n);
             tc_fence_after();
-            const uint8_t *tv = sV + (n & 1) * Lay::kV;
+            const uint8_t *tv = sV + (n % NST) * Lay::kV;
             uint32_t z0 = 0, z1 = 0;   // 0 v: anything else where v is not finite
             const int tq = (lane & 3) * 2;
 #pragma unroll 1
@@ -553,7 +564,7 @@ retain_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
                 tc_fence_before();
                 mbar_arrive(&S.y_scaled);
             }
-            if (!__all_sync(0xffffffffu, mbar_wait<1>(&S.pv_done[n & 1], (n >> 1) & 1, g, 32))) break;
+            if (!__all_sync(0xffffffffu, mbar_wait<1>(&S.pv_done[n % NST], turn(n), g, 32))) break;
             {
                 uint8_t *sY = y_tile(n);   // where Q was: it has been read (its own place: the copy before the last from there has, before this block's Q came)
                 tc_fence_after();
@@ -590,7 +601,7 @@ retain_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
                 tc_fence_before();
                 mbar_arrive(&S.y_free);
                 fence_proxy_async();
-                mbar_arrive(&S.y_written[n & 1]);
+                mbar_arrive(&S.y_written[n % NST]);
             }
         }
     }
@@ -633,7 +644,7 @@ template <int D, int DV, bool REV, int MODE> cudaError_t launch_mode(const Retai
                           !encode_tokens(&ym, a.y, a.layout, a.B, a.H, a.N, DV, kTC))))
         return cudaErrorInvalidValue;
     auto kern = retain_tc_kernel<D, DV, REV, MODE>;
-    constexpr int smem = RetainLay<D, DV>::request;
+    constexpr int smem = RetainLay<D, DV, MODE>::request;
     static_assert(smem <= 232448, "shared memory of a CTA");
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
