@@ -1034,9 +1034,12 @@ la_status la_backward_retention(const void *q, const void *k, const void *v, con
         return from_cuda(launch_retain_grads_simt(a, {dy, grad_q, grad_k, grad_v, grad_S_out, grad_S_in}));
     cudaError_t e = launch_retain_tc(retain_args(dy, v, k, grad_q, gamma, B, H, N, dv, d, dt, layout, S_in, nullptr, false, true, workspace, stream));
     if (e == cudaSuccess)
-        e = launch_retain_tc(retain_args(v, dy, q, grad_k, gamma, B, H, N, dv, d, dt, layout, grad_S_out, nullptr, true, true, workspace, stream));
-    if (e == cudaSuccess)
         e = launch_retain_tc(retain_args(k, q, dy, grad_v, gamma, B, H, N, d, dv, dt, layout, grad_S_out, grad_S_in, true, false, workspace, stream));
+    if (e == cudaSuccess) {   // from the transposed state that grad_v's came from
+        RetainArgs gk = retain_args(v, dy, q, grad_k, gamma, B, H, N, dv, d, dt, layout, grad_S_out, nullptr, true, true, workspace, stream);
+        gk.have_states = true;
+        e = launch_retain_tc(gk);
+    }
     return from_cuda(e);
 }
 

@@ -127,6 +127,9 @@ struct RetainArgs {
     bool rev, trans;
     void *ws;                    // starts with a status header
     cudaStream_t stream;
+    // tensor cores, split sequences: the workspace holds the segments' states, transposed to this call's, which the call
+    // before left there (of grad_v for grad_k)
+    bool have_states = false;
 };
 
 // What the gradients of retention take beside the forward's inputs.

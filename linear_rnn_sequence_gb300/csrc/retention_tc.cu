@@ -68,7 +68,8 @@ struct RetainSmall {
         qs_done, y_scaled, y_free, w_ready[2], drain;   // w_ready[1], and kv_read by all: kSums
     float pg[2 * kTC + 4];        // pg[kTC - n] = gamma^n, zeros behind
     alignas(16) float near[16];   // gamma^(15 - j) (REV: gamma^j)
-    int v_bad[2];                 // block index + 1 of a block with a value that is not finite
+    int v_bad[4];                 // block index + 1 of a block with a value that is not finite; y of a block may still be to come
+                                  // when W of the next but one is made
     uint8_t first[2][kTC];        // then, by column: how many tokens come before its first one (REV: up to its last one)
     uint32_t tmem_base;
     volatile int abort_flag;
@@ -128,7 +129,7 @@ retain_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
 
     if (tid == 0) {
         S.abort_flag = 0;
-        S.v_bad[0] = S.v_bad[1] = 0;
+        for (int i = 0; i < 4; ++i) S.v_bad[i] = 0;
         for (int i = 0; i < NST; ++i) {
             mbar_init(&S.q_full[i], 1);
             mbar_init(&S.k_full[i], 1);
@@ -315,7 +316,7 @@ retain_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
                 if (!ok) break;
                 kv_half(n, 1);
             }
-            if (*(volatile int *)&S.v_bad[n & 1] == n + 1) mend_v(n);
+            if (*(volatile int *)&S.v_bad[n & 3] == n + 1) mend_v(n);
             all(mbar_wait<1>(&S.p_ready, n & 1, g, 9));
             if (!TWIN) all(mbar_wait<1>(&S.y_scaled, n & 1, g, 10));
             if (!ok) break;
@@ -407,7 +408,7 @@ retain_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
                     tmem_st_16x128b_x4(to + 128, lo);
                 }
             }
-            if (OUT && NH == 1 && ((z0 | z1) & 0x7FFF7FFFu)) S.v_bad[n & 1] = n + 1;
+            if (OUT && NH == 1 && ((z0 | z1) & 0x7FFF7FFFu)) S.v_bad[n & 3] = n + 1;
             tmem_wait_st();
             tc_fence_before();
         };
@@ -423,7 +424,7 @@ retain_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
                 tmem_ld16(from + 16, a1);
                 tmem_wait_ld();
                 // a value of v that is not finite leaves nothing finite here (a value of k may, too)
-                if (OUT && NH == 2 && i == 0 && half == 0 && !finite(u2f(a0[0]))) S.v_bad[n & 1] = n + 1;
+                if (OUT && NH == 2 && i == 0 && half == 0 && !finite(u2f(a0[0]))) S.v_bad[n & 3] = n + 1;
 #pragma unroll
                 for (int j = 0; j < 16; j += 2) {
                     f2unpack(f2fma(g2, f2pack(st[i + j], st[i + j + 1]), f2pack(u2f(a0[j]), u2f(a0[j + 1]))), st[i + j],
@@ -568,7 +569,7 @@ retain_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
             {
                 uint8_t *sY = y_tile(n);   // where Q was: it has been read (its own place: the copy before the last from there has, before this block's Q came)
                 tc_fence_after();
-                const bool bad = *(volatile int *)&S.v_bad[n & 1] == n + 1;
+                const bool bad = *(volatile int *)&S.v_bad[n & 3] == n + 1;
 #pragma unroll 1
                 for (int c = 0; c < DV; c += 32) {
                     uint32_t a[2][16], e[2][16];
@@ -668,10 +669,11 @@ template <int D, int DV, bool REV> cudaError_t launch_tc(const RetainArgs &a) {
         s.S_out = states;
         s.segs = p.nseg - (a.S_out ? 0 : 1);
         s.seg0 = REV ? p.nseg - s.segs : 0;
-        cudaError_t e = launch_mode<D, DV, REV, kSums>(a, s);
-        if (e == cudaSuccess) e = launch_retain_scan(a, states, p.nseg, p.seg_blocks * kTC);
+        cudaError_t e = a.have_states ? cudaSuccess : launch_mode<D, DV, REV, kSums>(a, s);
+        if (e == cudaSuccess && !a.have_states) e = launch_retain_scan(a, states, p.nseg, p.seg_blocks * kTC);
         if (e != cudaSuccess) return e;
         p.S_in = states;
+        p.trans = a.have_states;
     } else {
         p.S_in = a.S_in;
         p.S_out = a.S_out;

@@ -160,6 +160,73 @@ def test_what_is_not_finite_reaches_nothing_earlier(at, where, bad, dtype):
     assert torch.equal(grads[2][0, 1, at + 1:], clean[2][0, 1, at + 1:])
 
 
+@pytest.mark.parametrize("d,dv", [(64, 64), (128, 64), (128, 128)])
+@pytest.mark.parametrize("where", ["q", "k", "v", "dy"])
+@pytest.mark.parametrize("at", [63, 64, 129, 600])
+def test_what_is_not_finite_at_other_widths(at, where, d, dv):
+    x = R.inputs(1, 2, 700, d, dv, BF16, gamma=[0.99, 0.0], seed=13)
+    clean_y, clean = forward(x), backward(x)
+    for head, bad in ((0, float("inf")), (1, float("nan"))):
+        y = {n: t if t is None else t.clone() for n, t in x.items()}
+        y[where][0, head, at, 0 if at % 2 else -1] = bad
+        got, grads = forward(y), backward(y)
+        assert torch.equal(got[0, 1 - head], clean_y[0, 1 - head]) and torch.equal(got[0, head, :at], clean_y[0, head, :at])
+        if where != "dy":
+            assert not bool(torch.isfinite(got[0, head, at]).all())
+        for g, c in zip(grads, clean):
+            assert torch.equal(g[0, 1 - head], c[0, 1 - head])
+        assert torch.equal(grads[0][0, head, :at], clean[0][0, head, :at])
+        for g, c in zip(grads[1:3], clean[1:3]):
+            assert torch.equal(g[0, head, at + 1:], c[0, head, at + 1:])
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("dv", [64, 128])
+def test_what_is_not_finite_in_many_blocks(d, dv):
+    """Whatever the other blocks hold, a block's own tokens before its first such value are as they were and those from it on
+    are not finite in its column."""
+    x = R.inputs(1, 2, 2000, d, dv, BF16, gamma=[0.9], seed=14, state=False)
+    clean = forward(x)
+    for first in (3, 300):
+        y = {n: t if t is None else t.clone() for n, t in x.items()}
+        for t in range(first, 2000, 128):
+            y["v"][0, 0, t, 7] = float("nan")
+            y["v"][0, 1, t, dv - 1] = float("inf")
+        for _ in range(5):
+            got = forward(y)
+            assert torch.equal(got[:, :, :first], clean[:, :, :first])
+            assert not bool(torch.isfinite(got[0, 0, first:, 7]).any())
+            assert not bool(torch.isfinite(got[0, 1, first:, dv - 1]).any())
+            keep = torch.arange(dv) != 7
+            assert torch.equal(got[0, 0][:, keep], clean[0, 0][:, keep])
+
+
+def test_calls_from_several_threads():
+    import threading
+    xs = [on_gpu(R.inputs(1, 3, 200 + 130 * i, 64, 64, BF16, seed=i)) for i in range(4)]
+
+    def call(x):
+        return (*la.forward_retention(x["q"], x["k"], x["v"], x["gamma"], S_in=x["S"], return_state=True),
+                *la.backward_retention(x["q"], x["k"], x["v"], x["gamma"], x["dy"], S_in=x["S"], grad_S_out=x["dS"]))
+
+    want, got = [call(x) for x in xs], [None] * 4
+    torch.cuda.synchronize()
+
+    def work(i):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for _ in range(20):
+                got[i] = call(xs[i])
+            torch.cuda.current_stream().synchronize()
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    for a, b in zip(got, want):
+        assert all(torch.equal(u, v) for u, v in zip(a, b))
+
+
 @pytest.mark.parametrize("dtype", [BF16, F32])
 def test_what_is_not_finite_in_the_upstream_gradient(dtype):
     x = R.inputs(1, 1, 270, 64, 128, dtype, gamma=[0.99], seed=5)
