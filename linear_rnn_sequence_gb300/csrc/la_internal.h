@@ -252,7 +252,7 @@ cudaError_t launch_retain_simt(const RetainArgs &a);   // rev and trans not look
 cudaError_t launch_retain_grads_simt(const RetainArgs &a, const RetainGrads &g);
 cudaError_t launch_retain_step(const RetainArgs &a);
 // Sums of `blocks` blocks of `tokens` tokens a head, [head][block][d][dv], become the states before the blocks;
-// a.S_out too.
+// a.S_out too.  It starts while the kernel before it in the stream ends, and lets the next one do so.
 cudaError_t launch_retain_scan(const RetainArgs &a, float *states, int blocks, int tokens);
 // tensor cores (bf16, d and dv in {64, 128})
 bool retain_tc_supported(const RetainArgs &a);

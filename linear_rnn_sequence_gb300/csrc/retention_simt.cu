@@ -9,9 +9,12 @@
 // the states' way through memory, 16 d dv bytes a block; small calls by the three launches.
 // It serves float32 inputs and widths of 32.
 #include "retention.cuh"
+#include "tc_common.cuh"
 
 namespace la {
 namespace {
+
+using namespace tc;
 
 constexpr int kRC = 64;       // tokens of a block
 constexpr int kRThr = 256;    // 16 x 16 threads
@@ -80,6 +83,7 @@ __global__ void __launch_bounds__(kRThr) retain_sums_kernel(const RetainSimt p) 
     extern __shared__ float sm[];
     float *K = sm, *V = K + kRC * D;
     __shared__ float w[kRC];
+    griddep_launch_dependents();   // the scan, which waits for this grid's end
     const int unit = blockIdx.x % (p.heads * p.nblk), bh = unit / p.nblk, blk = unit % p.nblk, b = bh / p.H, h = bh % p.H;
     const int t0 = blk * kRC, n = min(kRC, p.N - t0);
     const Job &jb = p.job[blockIdx.x / (p.heads * p.nblk)];
@@ -124,6 +128,8 @@ __global__ void __launch_bounds__(kScanThr) retain_scan_kernel(const RetainSimt 
     const float g = p.gamma[bh % p.H], whole = gamma_power(g, p.tokens), last = gamma_power(g, p.N - (p.nblk - 1) * p.tokens);
     float4 *s = reinterpret_cast<float4 *>(jb.states + (size_t)bh * p.nblk * st + at);
     const int step = st / 4;
+    griddep_launch_dependents();   // what takes the states: it waits for this grid's end in turn
+    griddep_wait();
     // of a state's values in their order here; a transposed state's lie DV apart
     auto where = [&](int i) { return trans ? (size_t)((at + i) % DV) * D + (at + i) / DV : (size_t)at + i; };
     float x[4] = {0.f, 0.f, 0.f, 0.f};
@@ -221,6 +227,7 @@ __global__ void __launch_bounds__(kRThr, 2) retain_out_kernel(const RetainSimt p
             const int i = 4 * ty + r, j = tx + 16 * c, e = rev ? j - i : i - j;
             P[i * L::LP + j] = e >= 0 ? s[r][c] * pw[e] : 0.f;
         }
+    griddep_wait();   // the states
     // the state's part, rows of S staged where K was
     const float *S0 = jb.states ? jb.states + (size_t)unit * D * DV : jb.S_in ? jb.S_in + (size_t)bh * D * DV : nullptr;
     float acc[4][C];
@@ -278,14 +285,17 @@ template <int D, int DV, typename T> struct Launch {
         cudaError_t e = cudaFuncSetAttribute(retain_sums_kernel<D, DV, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
         retain_sums_kernel<D, DV, T><<<(unsigned)jobs * p.heads * p.nblk, kRThr, smem, s>>>(p);
-        retain_scan_kernel<<<(unsigned)jobs * p.heads * (D * DV / 4 / kScanThr), kScanThr, 0, s>>>(p, D, DV);
-        return cudaGetLastError();
+        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        return launch_overlapped(retain_scan_kernel, dim3((unsigned)jobs * p.heads * (D * DV / 4 / kScanThr)), dim3(kScanThr), 0, s, p, D, DV);
     }
-    static cudaError_t out(const RetainSimt &p, int jobs, cudaStream_t s) {
+    // behind: launched right behind the scan, and so early
+    static cudaError_t out(const RetainSimt &p, int jobs, bool behind, cudaStream_t s) {
         constexpr int smem = OutLay<D, DV, T>::bytes;
         cudaError_t e = cudaFuncSetAttribute(retain_out_kernel<D, DV, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
-        retain_out_kernel<D, DV, T><<<(unsigned)jobs * p.heads * p.nblk, kRThr, smem, s>>>(p);
+        const dim3 grid((unsigned)jobs * p.heads * p.nblk);
+        if (behind) return launch_overlapped(retain_out_kernel<D, DV, T>, grid, dim3(kRThr), smem, s, p);
+        retain_out_kernel<D, DV, T><<<grid, kRThr, smem, s>>>(p);
         return cudaGetLastError();
     }
 };
@@ -300,7 +310,7 @@ struct Forward {
             const cudaError_t e = Launch<D, DV, T>::sums(p, 1, a.stream);
             if (e != cudaSuccess) return e;
         }
-        return Launch<D, DV, T>::out(p, 1, a.stream);
+        return Launch<D, DV, T>::out(p, 1, jb.states != nullptr, a.stream);
     }
 };
 
@@ -317,10 +327,10 @@ struct Grads {
         p.job[0] = {g.dy, a.v, a.k, g.dq, nullptr, nullptr, S, false, true};
         p.job[1] = {a.v, g.dy, a.q, g.dk, nullptr, nullptr, G, true, true};
         p.job[2] = {a.k, a.q, g.dy, g.dv, nullptr, nullptr, G, true, false};
-        if (D == DV) return Launch<DV, D, T>::out(p, 3, a.stream);
-        if ((e = Launch<DV, D, T>::out(p, 2, a.stream)) != cudaSuccess) return e;
+        if (D == DV) return Launch<DV, D, T>::out(p, 3, true, a.stream);
+        if ((e = Launch<DV, D, T>::out(p, 2, true, a.stream)) != cudaSuccess) return e;
         p.job[0] = p.job[2];
-        return Launch<D, DV, T>::out(p, 1, a.stream);
+        return Launch<D, DV, T>::out(p, 1, false, a.stream);
     }
 };
 
@@ -354,8 +364,8 @@ cudaError_t launch_retain_scan(const RetainArgs &a, float *states, int blocks, i
     RetainSimt p = simt_params(a);
     p.job[0] = {nullptr, nullptr, nullptr, nullptr, a.S_in, a.S_out, states, a.rev, a.trans};
     p.nblk = blocks; p.tokens = tokens;
-    retain_scan_kernel<<<(unsigned)p.heads * (a.d * a.dv / 4 / kScanThr), kScanThr, 0, a.stream>>>(p, a.d, a.dv);
-    return cudaGetLastError();
+    return launch_overlapped(retain_scan_kernel, dim3((unsigned)p.heads * (a.d * a.dv / 4 / kScanThr)), dim3(kScanThr), 0, a.stream, p,
+                             a.d, a.dv);
 }
 cudaError_t launch_retain_simt(const RetainArgs &a) { return by_type<Forward>(a, RetainGrads{}); }
 cudaError_t launch_retain_grads_simt(const RetainArgs &a, const RetainGrads &g) { return by_type<Grads>(a, g); }

@@ -123,6 +123,7 @@ retain_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
     const int bh = blockIdx.x / p.segs, seg = p.seg0 + blockIdx.x % p.segs, b = bh / p.H, h = bh - b * p.H;
     const int first_blk = seg * p.seg_blocks, nch = min(p.seg_blocks, p.nblk - first_blk);
     const float gamma = p.gamma[h];
+    if (!OUT) griddep_launch_dependents();   // the scan, which waits for this grid's end
     // the n-th block taken, and its tokens
     auto token_of = [&](int n) { return (first_blk + (REV ? nch - 1 - n : n)) * kTC; };
     auto length_of = [&](int n) { return min(kTC, p.N - token_of(n)); };
@@ -342,6 +343,7 @@ retain_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
         const int half = (warp - 4) >> 2;
         const int part = TWIN ? wq >> 1 : 0, col = TWIN ? row & 63 : row;   // part: warp-uniform
         float st[SC];
+        if (OUT) griddep_wait();   // segments' states: this launch may have started before the scan's end
         if (part == 0 && p.S_in) {
             const float *src = p.S_in + (size_t)(p.nseg > 1 ? bh * p.nseg + seg : bh) * D * DV;
             if (p.trans) {
@@ -616,8 +618,8 @@ retain_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
 
 // Segments of a head.  Splitting pays where the heads leave SMs idle: the segments' own sums come first (a block of
 // them costs about 0.6 of a whole one), their ends are joined, and every segment runs from its state.  In units of a
-// block's time, about 2.2 us: a wave of CTAs takes its segments' length, the extra launches and starts about 3 (gradients of
-// 24 heads of 9 blocks: 79 us split in three, 83 whole; 8 heads of 8 blocks forward: 29 and 33).
+// block's time, about 2.2 us: a wave of CTAs takes its segments' length, the extra launches and starts about 3 (before the
+// launches overlapped: gradients of 24 heads of 9 blocks 79 us split in three, 83 whole; 8 heads of 8 blocks forward 29 and 33).
 void retain_segments(const RetainArgs &a, int &nseg, int &seg_blocks) {
     const int nblk = (a.N + kTC - 1) / kTC, sms = num_sms();
     const long long BH = (long long)a.B * a.H;
@@ -638,7 +640,8 @@ void retain_segments(const RetainArgs &a, int &nseg, int &seg_blocks) {
     }
 }
 
-template <int D, int DV, bool REV, int MODE> cudaError_t launch_mode(const RetainArgs &a, const RetainTc &p) {
+// behind: right behind the scan, and so early.
+template <int D, int DV, bool REV, int MODE> cudaError_t launch_mode(const RetainArgs &a, const RetainTc &p, bool behind = false) {
     CUtensorMap qm{}, km, vm, ym{};
     if (!encode_tokens(&km, a.k, a.layout, a.B, a.H, a.N, D, kTC) || !encode_tokens(&vm, a.v, a.layout, a.B, a.H, a.N, DV, kTC) ||
         (MODE == kWhole && (!encode_tokens(&qm, a.q, a.layout, a.B, a.H, a.N, D, kTC) ||
@@ -649,6 +652,7 @@ template <int D, int DV, bool REV, int MODE> cudaError_t launch_mode(const Retai
     static_assert(smem <= 232448, "shared memory of a CTA");
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
+    if (behind) return launch_overlapped(kern, dim3(a.B * a.H * p.segs), dim3(kRetThr), smem, a.stream, qm, km, vm, ym, p);
     kern<<<a.B * a.H * p.segs, kRetThr, smem, a.stream>>>(qm, km, vm, ym, p);
     return cudaGetLastError();
 }
@@ -680,7 +684,7 @@ template <int D, int DV, bool REV> cudaError_t launch_tc(const RetainArgs &a) {
         p.trans = a.trans;
     }
     p.segs = p.nseg;
-    return launch_mode<D, DV, REV, kWhole>(a, p);
+    return launch_mode<D, DV, REV, kWhole>(a, p, p.nseg > 1 && !a.have_states);
 }
 template <int D, int DV> cudaError_t launch_way(const RetainArgs &a) {
     return a.rev ? launch_tc<D, DV, true>(a) : launch_tc<D, DV, false>(a);
