@@ -78,13 +78,13 @@ __global__ void __launch_bounds__(kRotThreads) norm_rotate_kernel(const RotParam
             eps[u] = p.eps;
         }
         if (p.c > 0.f) {
-            float most = 0.f;   // NaN counts as more than any
+            bool big = false;
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 ss[u] = group_sum<LPR>(ss[u]);
-                most = ss[u] <= most ? most : ss[u];
+                big |= !(ss[u] <= kRotBig);
             }
-            if (__any_sync(0xffffffffu, !(most <= kRotBig))) {   // squares that pass float32's range
+            if (__any_sync(0xffffffffu, big)) {   // squares that pass float32's range
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
                     const float down = ss[u] <= kRotBig ? 1.f : kRotDown;

@@ -192,6 +192,23 @@ def test_sizes_of_values(dtype, norm):
     assert bool(torch.isnan(y[0].cpu()[0, 0, 7]).any()) and bool(torch.isnan(y[0].cpu()[0, 1, 8]).any())
 
 
+@pytest.mark.parametrize("d", [6, 30, 64, 66, 128, 250])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_large_rows_beside_rows_that_are_not_numbers(d, dtype):
+    """Heads that a lane works on together: each its own row's norm, whatever the others hold."""
+    x = R.inputs(1, 9, 9, 3, d, dtype, seed=d)
+    for n in "qk":
+        x[n][:, 0::3] *= 2.0 ** 100
+        x[n][:, 1::3, :, 1] = float("nan")
+    want = {n: R.forward({**x, n: torch.nan_to_num(x[n])}, n, norm="rms") for n in "qk"}
+    got = la.norm_rotate(x["q"].cuda(), x["k"].cuda(), **args(x))
+    res = la.norm_rotate_backward(x["gq"].cuda(), x["gk"].cuda(), x["q"].cuda(), x["k"].cuda(), **args(x))
+    whole = torch.tensor([h for h in range(9) if h % 3 != 1])
+    for n, y, g in zip("qk", got, res):
+        R.near(y[:, whole.cuda()], want[n][0][:, whole], want[n][1][:, whole], R.E, n)
+        assert bool(torch.isnan(y[:, 1::3]).all()) and bool(torch.isfinite(g[:, whole.cuda()]).all())
+
+
 @pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("pairs", ["halves", "adjacent"])
 def test_infinities_without_a_norm(pairs, dtype):
