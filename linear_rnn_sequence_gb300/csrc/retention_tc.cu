@@ -182,7 +182,7 @@ retain_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
                 for (int f = 0; f < slabs; ++f) tma_load_4d(dst + f * 16384, &m, bar, f * 64, token_of(n), h, b);
             };
             auto store = [&](int n) {   // y of a block, when it is written
-                if (!mbar_wait<1>(&S.y_written[n % NST], turn(n), g, 1)) return false;
+                if (!mbar_wait<2>(&S.y_written[n % NST], turn(n), g, 1)) return false;
 #pragma unroll
                 for (int f = 0; f < DV / 64; ++f) tma_store_4d(&ymap, y_tile(n) + f * 16384, f * 64, token_of(n), h, b);
                 bulk_commit();
@@ -193,7 +193,7 @@ retain_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
             for (; n < nch; ++n) {
                 const int s = n % NST;
                 // the block before it there has been used: its last product is P~ V
-                if (n >= NST && !mbar_wait<1>(&S.pv_done[s], turn(n) ^ 1u, g, 2)) break;
+                if (n >= NST && !mbar_wait<2>(&S.pv_done[s], turn(n) ^ 1u, g, 2)) break;
                 load(sK + s * Lay::kQ, kmap, &S.k_full[s], D / 64, n, n == 0 && (int)blockIdx.x == p.drop_item);
                 load(sV + s * Lay::kV, vmap, &S.v_full[s], DV / 64, n, false);
                 // the next one into L2, while its places are still taken (d = 128, B8 H16 N8192: 190 us with and 205 without; with
@@ -242,7 +242,7 @@ retain_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
             const uint32_t leader = elect_leader();
             tc_fence_after();
             const uint64_t kd = smem_desc(smem_u32(sK) + (n % NST) * Lay::kQ + half * 16384, 16384, 1024, kSwizzle128B);
-#pragma unroll 1
+#pragma unroll   // d64 107 us; 112 with a loop over the pieces
             for (int pc = 2; pc >= 0; --pc)
 #pragma unroll
                 for (int ks = 0; ks < kTC / 16; ++ks)
@@ -251,8 +251,7 @@ retain_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
         };
         auto scores = [&](int n) {
             const int s = n % NST;
-            all(mbar_wait<1>(&S.k_full[s], turn(n), g, 3));
-            all(mbar_wait<1>(&S.q_full[s], turn(n), g, 4));
+            all(mbar_wait<2>(&S.k_full[s], turn(n), g, 3) && mbar_wait<2>(&S.q_full[s], turn(n), g, 4));
             if (!ok) return;
             const uint32_t leader = elect_leader();
             tc_fence_after();
@@ -285,20 +284,18 @@ retain_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
         for (int n = 0; n < nch && ok; ++n) {
             const int s = n % NST;
             if (!OUT) {
-                all(mbar_wait<1>(&S.k_full[s], turn(n), g, 3));
-                all(mbar_wait<1>(&S.w_ready[n & 1], (n >> 1) & 1, g, 5));
-                if (n >= 1) all(mbar_wait<1>(&S.kv_read, (n - 1) & 1, g, 8));
+                all(mbar_wait<2>(&S.k_full[s], turn(n), g, 3) && mbar_wait<2>(&S.w_ready[n & 1], (n >> 1) & 1, g, 5) &&
+                    (n == 0 || mbar_wait<2>(&S.kv_read, (n - 1) & 1, g, 8)));
                 if (!ok) break;
                 for (int half = 0; half < NH; ++half) kv_half(n, half);
                 const uint32_t leader = elect_leader();
                 mma_commit_if(leader, &S.pv_done[s]);
                 continue;
             }
-            all(mbar_wait<1>(&S.w_ready[0], n & 1, g, 5));
+            all(mbar_wait<2>(&S.w_ready[0], n & 1, g, 5));
             if (!ok) break;
             kv_half(n, 0);
-            all(mbar_wait<1>(&S.s_ready, n & 1, g, 6));
-            if (n >= 1) all(mbar_wait<1>(&S.y_free, (n - 1) & 1, g, 7));
+            all(mbar_wait<2>(&S.s_ready, n & 1, g, 6) && (n == 0 || mbar_wait<2>(&S.y_free, (n - 1) & 1, g, 7)));
             if (!ok) break;
             {
                 const uint32_t leader = elect_leader();
@@ -313,13 +310,12 @@ retain_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
                 mma_commit_if(leader, &S.qs_done);
             }
             if (NH == 2) {
-                all(mbar_wait<1>(&S.kv_read, n & 1, g, 8));
+                all(mbar_wait<2>(&S.kv_read, n & 1, g, 8));
                 if (!ok) break;
                 kv_half(n, 1);
             }
             if (*(volatile int *)&S.v_bad[n & 3] == n + 1) mend_v(n);
-            all(mbar_wait<1>(&S.p_ready, n & 1, g, 9));
-            if (!TWIN) all(mbar_wait<1>(&S.y_scaled, n & 1, g, 10));
+            all(mbar_wait<2>(&S.p_ready, n & 1, g, 9) && (TWIN || mbar_wait<2>(&S.y_scaled, n & 1, g, 10)));
             if (!ok) break;
             {
                 const uint32_t leader = elect_leader();
@@ -376,7 +372,7 @@ retain_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
                 tmem_st16(tb + lb + (OUT ? kColW3 : kColSumW) + i * 64 + (1 - part) * 32 + half * 16, none);
         }
         bool ok = true;
-        auto wait_v = [&](int n) { return mbar_wait<1>(&S.v_full[n % NST], turn(n), g, 20); };
+        auto wait_v = [&](int n) { return mbar_wait<2>(&S.v_full[n % NST], turn(n), g, 20); };
         auto make_w = [&](int n, uint32_t at_w) {
             const int L = length_of(n);
             tc_fence_after();
@@ -445,7 +441,7 @@ retain_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
                     mbar_arrive(&S.w_ready[(n + 1) & 1]);
                 }
                 if (n < 0) continue;
-                if (!(ok = __all_sync(0xffffffffu, mbar_wait<1>(&S.kv_done[0], n & 1, g, 23)))) break;
+                if (!(ok = __all_sync(0xffffffffu, mbar_wait<2>(&S.kv_done[0], n & 1, g, 23)))) break;
                 update(n, half * SC);
                 mbar_arrive(&S.kv_read);
             }
@@ -453,16 +449,16 @@ retain_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
         for (int n = 0; OUT && n < nch; ++n) {
             ok = wait_v(n);
             // W's place is free (where this has not been waited for below)
-            if (n >= 1 && NH == 2 && half == 0) ok = ok && mbar_wait<1>(&S.kv_done[1], (n - 1) & 1, g, 21);
+            if (n >= 1 && NH == 2 && half == 0) ok = ok && mbar_wait<2>(&S.kv_done[1], (n - 1) & 1, g, 21);
             if (!(ok = __all_sync(0xffffffffu, ok))) break;
             make_w(n, kColW3);
             mbar_arrive(&S.w_ready[0]);
             if (NH == 1 && n >= 1) {   // Q S of the block before has read its operand (else K^T W's end says so)
-                ok = __all_sync(0xffffffffu, mbar_wait<1>(&S.qs_done, (n - 1) & 1, g, 22));
+                ok = __all_sync(0xffffffffu, mbar_wait<2>(&S.qs_done, (n - 1) & 1, g, 22));
                 if (!ok) break;
             }
             put_state();
-            ok = __all_sync(0xffffffffu, mbar_wait<1>(&S.kv_done[NH == 2 ? half : 0], n & 1, g, 23));
+            ok = __all_sync(0xffffffffu, mbar_wait<2>(&S.kv_done[NH == 2 ? half : 0], n & 1, g, 23));
             if (!ok) break;
             update(n, kColKV + (NH == 2 ? 0 : half * SC));
             if (NH == 2 && half == 0) mbar_arrive(&S.kv_read);
@@ -471,7 +467,7 @@ retain_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
         float *dst = OUT ? (p.S_out && last ? p.S_out + (size_t)bh * D * DV : nullptr)
                          : p.S_out + ((size_t)bh * p.nseg + seg) * D * DV;
         if (TWIN && dst) {   // the second half's state through where S was, which the last Q S has read
-            if (OUT) ok = __all_sync(0xffffffffu, ok && mbar_wait<1>(&S.qs_done, (nch - 1) & 1, g, 24));
+            if (OUT) ok = __all_sync(0xffffffffu, ok && mbar_wait<2>(&S.qs_done, (nch - 1) & 1, g, 24));
             float *other = reinterpret_cast<float *>(sS) + half * SC * DV + col;
             if (ok && part == 1)
 #pragma unroll
@@ -503,7 +499,7 @@ retain_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
         for (int j = 0; j < 16; ++j)
             keep[j] = ((REV ? 2 * j >= lane : 2 * j <= lane) ? 0xFFFFu : 0u) | ((REV ? 2 * j + 1 >= lane : 2 * j + 1 <= lane) ? 0xFFFF0000u : 0u);
         for (int n = 0; n < nch; ++n) {
-            if (!__all_sync(0xffffffffu, mbar_wait<1>(&S.qk_done, n & 1, g, 30))) break;
+            if (!__all_sync(0xffffffffu, mbar_wait<2>(&S.qk_done, n & 1, g, 30))) break;
             {
                 tc_fence_after();
 #pragma unroll 1
@@ -542,7 +538,7 @@ retain_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
             }
             const float f = pw[-max(0, inter_exp(REV, row, length_of(n)))];   // behind the last token: of zeros
             if (!TWIN) {
-                if (!__all_sync(0xffffffffu, mbar_wait<1>(&S.qs_done, n & 1, g, 31))) break;
+                if (!__all_sync(0xffffffffu, mbar_wait<2>(&S.qs_done, n & 1, g, 31))) break;
                 tc_fence_after();
                 const uint64_t f2 = f2pack(f, f);
 #pragma unroll 1
@@ -567,7 +563,7 @@ retain_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
                 tc_fence_before();
                 mbar_arrive(&S.y_scaled);
             }
-            if (!__all_sync(0xffffffffu, mbar_wait<1>(&S.pv_done[n % NST], turn(n), g, 32))) break;
+            if (!__all_sync(0xffffffffu, mbar_wait<2>(&S.pv_done[n % NST], turn(n), g, 32))) break;
             {
                 uint8_t *sY = y_tile(n);   // where Q was: it has been read (its own place: the copy before the last from there has, before this block's Q came)
                 tc_fence_after();
