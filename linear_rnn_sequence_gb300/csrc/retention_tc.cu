@@ -18,12 +18,12 @@
 //   warp 13      issues the copies.
 // W is the one operand without a second place in TMEM: its three pieces, the halves of K^T W and the state's update
 // between them are the chain that bounds a block, about 5,000 cycles of which the products take 3,070; at d = dv = 128 and a CTA
-// on most SMs HBM bounds it as nearly.  B8 H16 N8192 d128: 177 us, 6.1 TB/s of the 6.7 that a copy reaches (152 heads: 6.4);
-// d64: 111 us, 4.8 TB/s; B1 H32 N131072 d64, in 19 segments: 560 us.
+// on most SMs HBM bounds it as nearly.  B8 H16 N8192 d128: 174 us, 6.2 TB/s of the 6.7 that a copy reaches (152 heads: 6.4);
+// d64: 97 us, 5.5 TB/s; B1 H32 N131072 d64, in 19 segments: 508 us.
 //
 // With dv = 64 the upper 64 TMEM lanes hold W of the block's second 64 tokens (and zeros for the first, as the lower ones do for
 // the second), so that every warp makes half as much of it; the lanes' sums stay two states that add up to S, and Q S takes
-// both (B8 H16 N8192 d64: 143 us with W in the lower lanes alone).
+// both (B8 H16 N8192 d64: 123 us; with W in the lower lanes alone and one accumulator for y 143).
 //
 // Precision: the state is float32 in registers, and what is added to it is exact but for the accumulator's float32: W is
 // rounded to float32 once and enters as three bf16 pieces that add up to it (the top, middle and low 8 bits), against
@@ -242,7 +242,7 @@ retain_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
             const uint32_t leader = elect_leader();
             tc_fence_after();
             const uint64_t kd = smem_desc(smem_u32(sK) + (n % NST) * Lay::kQ + half * 16384, 16384, 1024, kSwizzle128B);
-#pragma unroll   // d64 107 us; 112 with a loop over the pieces
+#pragma unroll   // B8 H16 N8192 d64: 107 us, with a loop over the pieces 112
             for (int pc = 2; pc >= 0; --pc)
 #pragma unroll
                 for (int ks = 0; ks < kTC / 16; ++ks)
