@@ -633,7 +633,8 @@ LA_API size_t la_retention_workspace_bytes(int B, int H, int N, int d, int dv, l
  *     S_t = gamma_h S_{t-1} + k_t v_t^T,   y_t = S_t^T q_t.
  * There is no scale; y is usually layer-normed (la_layer_norm).
  *   q, k     dtype dt, H heads of width d, [B][H][N][d] or (LA_LAYOUT_BNHD) [B][N][H][d].
- *   v, y     dtype dt, H heads of width dv, laid out alike.  y is rounded once, to dt, from float32.
+ *   v, y     dtype dt, H heads of width dv, laid out alike.  y is rounded once, to dt, from float32 sums, whose terms may be
+ *            off by 2^-14 of each (on the tensor cores two bf16 pieces stand for a score and for a value of the state).
  *   gamma    DEVICE array of H floats in [0, 1], 4-byte aligned, shared by the batch rows; its values are
  *            not checked (one outside [0, 1] gives a meaningless result, not an error).  Gamma 0 leaves
  *            each token its own key and value.

@@ -2,7 +2,7 @@
 // tokens, one CTA a head (or a segment of one).
 //
 //   scores  P  = Q K^T                        (128 x 128, K = d)
-//   masked  P~ = gamma^|i-j| P                (bf16, over P in TMEM)
+//   masked  P~ = gamma^|i-j| P                (two bf16 pieces, over P in TMEM)
 //   y          = gamma^(i+1) (Q S) + P~ V     (dv = 128: one accumulator, scaled between the two products)
 //   state   S' = gamma^C S + K^T W,           W_j = gamma^(C-1-j) v_j
 // and the same with the exponents of retention.cuh from behind (REV).
@@ -10,31 +10,32 @@
 // The products that make the state do not wait for what is made of it, and a block's scores are ready before its turn, so
 // the tensor pipe goes from one product to the next while warps work on what they need:
 //   warps 0-3    a row (token) a thread: P~ from P; the scaling of Q S; then y, through shared memory (where the
-//                block's Q was) and a tensor copy;
+//                block's V was) and a tensor copy;
 //   warps 4-11   W into TMEM as (K^T W)^T's left operand; the state, its columns (of dv) as TMEM lanes, d/2 of each in a
-//                thread's registers; S^T in bf16 to shared memory for Q S;
+//                thread's registers; S^T in two bf16 pieces to shared memory for Q S;
 //   warp 12      issues the MMAs: of a block the first half of K^T W (64 of d), Q S, the second half over the first's
 //                accumulator (d = 64: there is one), P~ V, then the next block's Q K^T;
 //   warp 13      issues the copies.
-// W is the one operand without a second place in TMEM: its three pieces, the halves of K^T W and the state's update
-// between them are the chain that bounds a block, about 5,000 cycles of which the products take 3,070; at d = dv = 128 and a CTA
-// on most SMs HBM bounds it as nearly.  B8 H16 N8192 d128: 174 us, 6.2 TB/s of the 6.7 that a copy reaches (152 heads: 6.4);
-// d64: 97 us, 5.5 TB/s; B1 H32 N131072 d64, in 19 segments: 508 us.
+// W is the one operand without a second place in TMEM: its three pieces, the halves of K^T W, the state's update between
+// them and Q S, which stands between the halves, are the chain that bounds a block.  d = dv = 128: about 6,500 cycles, of
+// which the products take 4,100 (K^T W 1,540, Q S and P~ V 1,020 each, Q K^T 510).  B8 H16 N8192 d128: 221 us, 4.9 TB/s of the
+// 6.7 that a copy reaches; B1 H32 N131072 d64, in 19 segments: 641 us.
 //
 // With dv = 64 the upper 64 TMEM lanes hold W of the block's second 64 tokens (and zeros for the first, as the lower ones do for
 // the second), so that every warp makes half as much of it; the lanes' sums stay two states that add up to S, and Q S takes
-// both (B8 H16 N8192 d64: 123 us; with W in the lower lanes alone and one accumulator for y 143).
+// both (a seventh faster at B8 H16 N8192 d64 than W in the lower lanes alone with one accumulator for y, when it came in).
 //
 // Precision: the state is float32 in registers, and what is added to it is exact but for the accumulator's float32: W is
 // rounded to float32 once and enters as three bf16 pieces that add up to it (the top, middle and low 8 bits), against
-// bf16 K, small pieces first.  y is rounded to bf16; of what only y depends on, each score and each value of
-// the state that it meets is rounded to bf16 once, to nearest.  These roundings are independent of y's own and of each
-// other: the error is sqrt(2) times that of y's rounding alone.  A second piece of either would cost an eighth more MMAs
-// and, for the state, shared memory that is not there.
+// bf16 K, small pieces first.  What only y depends on, each score and each value of the state that it meets, enters as two
+// pieces: 2^-15 of each at most is lost, as much as float32 sums of that length lose.  With one piece, 2^-8 of each, y was
+// off by sqrt(2) times its own rounding where the terms are of random signs, but by a tenth of itself where they cancel
+// (states with a common part of 64 times the rest that the queries do not see); the second pieces took the call above from 190
+// to 221 us.  y is rounded to bf16.
 //
 // What is not finite reaches no token before its own: masked scores are zeros, and a value of v that is not finite would
 // make 0 * inf of them.  It also makes its column of K^T W something not finite, which (d = 128) the warps of the state see
-// before P~ V is issued; for d = 64, where P~ V would have to wait for that (142 us became 156 at B8 H16 N8192), the warps that
+// before P~ V is issued; for d = 64, where P~ V would have to wait for that (a tenth slower), the warps that
 // make W look at every v.  In a block with such values these become zero in shared memory, and y NaN from the first's
 // token on, for its column.
 #include "delta_tc.cuh"
@@ -81,15 +82,15 @@ enum RetainMode { kWhole, kSums };
 template <int D, int DV, int MODE> struct RetainLay {
     static constexpr bool OUT = MODE == kWhole;
     static constexpr int kQ = (D / 64) * 16384, kV = (DV / 64) * 16384;
-    static constexpr int kHalfS = DV * D * 2, kS = OUT ? (128 / DV) * kHalfS : DV * D * 4;
-    static constexpr bool ownY = OUT && DV > D;      // y does not fit where Q was
-    // blocks in flight: as many as fit, four at most (d64: 111 us with four, 124 with two; B1 H32 N131072 d64 560 and 670)
-    static constexpr int kBlock = (OUT ? 2 : 1) * kQ + kV, kFixed = kS + (ownY ? 2 * kV : 0) + 1024 + (int)sizeof(RetainSmall);
-    static constexpr int kFit = (232448 - kFixed) / kBlock, kNst = kFit < kMostStages ? kFit : kMostStages;
-    static constexpr int oQ = 0, oK = oQ + (OUT ? kNst * kQ : 0), oV = oK + kNst * kQ, oS = oV + kNst * kV, oY = oS + kS,
-                         oSmall = oY + (ownY ? 2 * kV : 0);
+    // S: one piece of one state (of two if dv = 64); two pieces.  kSums: float32
+    static constexpr int kHalfS = DV * D * 2, kS = OUT ? (128 / DV) * 2 * kHalfS : DV * D * 4;
+    // blocks in flight: as many as fit, four at most; of Q one where that makes room for a second block of K and V
+    // (d = dv = 128)
+    static constexpr int kBlock = (OUT ? 2 : 1) * kQ + kV, kFree = 232448 - kS - 1024 - (int)sizeof(RetainSmall);
+    static constexpr int kFit = kFree / kBlock < kMostStages ? kFree / kBlock : kMostStages;
+    static constexpr int kNst = kFit >= 2 ? kFit : 2, kNsq = OUT ? (kFit >= 2 ? kFit : 1) : 0;
+    static constexpr int oQ = 0, oK = oQ + kNsq * kQ, oV = oK + kNst * kQ, oS = oV + kNst * kV, oSmall = oS + kS;
     static constexpr int request = oSmall + (int)sizeof(RetainSmall) + 1024;
-    static_assert(kNst >= 2 && (!ownY || kNst == 2), "y of its own has two places");
 };
 
 // Three pieces of a pair by truncation, as split3, at two thirds of its time: the logical operations that take a piece
@@ -101,7 +102,11 @@ __device__ __forceinline__ void pieces3(float x0, float x1, uint32_t &h, uint32_
     m = __byte_perm(f2u(x0), f2u(x1), 0x7632);
     l = __byte_perm(f2u(minus_bf16_lo(x0, m)), f2u(minus_bf16_hi(x1, m)), 0x7632);
 }
-
+// Two pieces: the first cut (what is finite stays so), what is left of it rounded to nearest, 2^-15 of the value at most off.
+__device__ __forceinline__ void pieces2(float x0, float x1, uint32_t &h, uint32_t &l) {
+    h = __byte_perm(f2u(x0), f2u(x1), 0x7632);
+    l = pack_bf16x2(minus_bf16_lo(x0, h), minus_bf16_hi(x1, h));
+}
 
 __device__ __forceinline__ uint8_t *retain_smem() {
     extern __shared__ uint8_t smem_raw[];
@@ -114,7 +119,7 @@ retain_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
                  const __grid_constant__ CUtensorMap vmap, const __grid_constant__ CUtensorMap ymap, const RetainTc p) {
     using Lay = RetainLay<D, DV, MODE>;
     constexpr bool OUT = MODE == kWhole;
-    constexpr int NST = Lay::kNst;
+    constexpr int NST = Lay::kNst, NSQ = Lay::kNsq > 0 ? Lay::kNsq : 1;
     constexpr int NH = D / 64;   // halves of K^T W
     constexpr bool TWIN = DV == 64;   // two states, of the tokens' halves; Q S and P~ V in accumulators of their own
     uint8_t *sm = retain_smem();
@@ -170,8 +175,9 @@ retain_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
     const uint32_t lb = (uint32_t)(wq * 32) << 16;
     const float *pw = S.pg + kTC;   // pw[-n] = gamma^n
     uint8_t *sQ = sm + Lay::oQ, *sK = sm + Lay::oK, *sV = sm + Lay::oV, *sS = sm + Lay::oS;
-    auto y_tile = [&](int n) { return Lay::ownY ? sm + Lay::oY + (n % NST) * Lay::kV : sQ + (n % NST) * Lay::kQ; };
-    auto turn = [](int n) { return (uint32_t)(n / NST) & 1u; };   // parity of block n's use of its place
+    auto y_tile = [&](int n) { return sV + (n % NST) * Lay::kV; };   // W and P~ V have read V
+    auto turn = [](int n) { return (uint32_t)(n / NST) & 1u; };      // parity of block n's use of its place
+    auto turn_q = [](int n) { return (uint32_t)(n / NSQ) & 1u; };
 
     if (warp == 13) {
         // ------------------------------------------------------------ copies
@@ -188,16 +194,26 @@ retain_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
                 bulk_commit();
                 return true;
             };
-            int n = 0;
-            bool q_too = true;   // of block n - 1
-            for (; n < nch; ++n) {
+            int nk = 0, nv = 0, nq = 0;   // copies issued
+            auto load_q = [&](int n) {
+                load(sQ + n % NSQ * Lay::kQ, qmap, &S.q_full[n % NSQ], D / 64, n, false);
+                ++nq;
+            };
+            for (int n = 0; n < nch; ++n) {
                 const int s = n % NST;
                 // the block before it there has been used: its last product is P~ V
                 if (n >= NST && !mbar_wait<2>(&S.pv_done[s], turn(n) ^ 1u, g, 2)) break;
                 load(sK + s * Lay::kQ, kmap, &S.k_full[s], D / 64, n, n == 0 && (int)blockIdx.x == p.drop_item);
+                ++nk;
+                if (OUT && NSQ == NST) load_q(n);
+                if (OUT && n >= NST) {   // y where V comes
+                    if (!store(n - NST)) break;
+                    bulk_wait_read<0>();
+                }
                 load(sV + s * Lay::kV, vmap, &S.v_full[s], DV / 64, n, false);
-                // the next one into L2, while its places are still taken (d = 128, B8 H16 N8192: 190 us with and 205 without; with
-                // d = 64 more blocks are in flight, and it cost 7 us of 142 when there were two)
+                ++nv;
+                // the next one into L2, while its places are still taken (d = 128: a twelfth faster, when it came in; with d = 64
+                // more blocks are in flight, and it cost a twentieth)
                 if (OUT && D > 64 && n >= 1 && n + 1 < nch) {
                     for (int f = 0; f < D / 64; ++f) {
                         tma_prefetch_4d(&kmap, f * 64, token_of(n + 1), h, b);
@@ -205,30 +221,22 @@ retain_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
                     }
                     for (int f = 0; f < DV / 64; ++f) tma_prefetch_4d(&vmap, f * 64, token_of(n + 1), h, b);
                 }
-                if (OUT) {
-                    if (n >= NST) {
-                        if (!store(n - NST)) {
-                            q_too = false;
-                            ++n;
-                            break;
-                        }
-                        bulk_wait_read<0>();   // its tile (or, where y has its own, also the one before) is free
-                    }
-                    load(sQ + s * Lay::kQ, qmap, &S.q_full[s], D / 64, n, false);
+                if (OUT && NSQ != NST) {   // Q's one place: the block before's last product with it is Q S
+                    if (n >= 1 && !mbar_wait<2>(&S.qs_done, (n - 1) & 1, g, 3)) break;
+                    load_q(n);
                 }
             }
             if (OUT) {
-                if (n == nch && q_too)
+                if (nv == nch)
                     for (int m = max(0, nch - NST); m < nch; ++m)
                         if (!store(m)) break;
                 bulk_wait<0>();
             }
             // what is in flight lands (after a wait that ran out; otherwise it has been used)
-            for (int m = max(0, n - NST); m < n; ++m) {
+            for (int m = max(0, nk - NST); m < nk; ++m)
                 if (!(m == 0 && (int)blockIdx.x == p.drop_item)) drain_wait(&S.k_full[m % NST], turn(m), g.limit_ns);
-                drain_wait(&S.v_full[m % NST], turn(m), g.limit_ns);
-                if (OUT && (q_too || m < n - 1)) drain_wait(&S.q_full[m % NST], turn(m), g.limit_ns);
-            }
+            for (int m = max(0, nv - NST); m < nv; ++m) drain_wait(&S.v_full[m % NST], turn(m), g.limit_ns);
+            for (int m = max(0, nq - NSQ); m < nq; ++m) drain_wait(&S.q_full[m % NSQ], turn_q(m), g.limit_ns);
         }
         __syncwarp();
     } else if (warp == 12) {
@@ -242,7 +250,7 @@ retain_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
             const uint32_t leader = elect_leader();
             tc_fence_after();
             const uint64_t kd = smem_desc(smem_u32(sK) + (n % NST) * Lay::kQ + half * 16384, 16384, 1024, kSwizzle128B);
-#pragma unroll   // B8 H16 N8192 d64: 107 us, with a loop over the pieces 112
+#pragma unroll   // a twentieth faster than a loop over the pieces at B8 H16 N8192 d64
             for (int pc = 2; pc >= 0; --pc)
 #pragma unroll
                 for (int ks = 0; ks < kTC / 16; ++ks)
@@ -251,11 +259,11 @@ retain_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
         };
         auto scores = [&](int n) {
             const int s = n % NST;
-            all(mbar_wait<2>(&S.k_full[s], turn(n), g, 3) && mbar_wait<2>(&S.q_full[s], turn(n), g, 4));
+            all(mbar_wait<2>(&S.k_full[s], turn(n), g, 3) && mbar_wait<2>(&S.q_full[n % NSQ], turn_q(n), g, 4));
             if (!ok) return;
             const uint32_t leader = elect_leader();
             tc_fence_after();
-            const uint64_t qd = desc_k(smem_u32(sQ) + s * Lay::kQ), kd = desc_k(smem_u32(sK) + s * Lay::kQ);
+            const uint64_t qd = desc_k(smem_u32(sQ) + n % NSQ * Lay::kQ), kd = desc_k(smem_u32(sK) + s * Lay::kQ);
 #pragma unroll
             for (int ks = 0; ks < D / 16; ++ks) {
                 const uint32_t o = ((ks >> 2) * 16384 + (ks & 3) * 32) >> 4;
@@ -300,13 +308,15 @@ retain_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
             {
                 const uint32_t leader = elect_leader();
                 tc_fence_after();
-                const uint64_t qd = desc_k(smem_u32(sQ) + s * Lay::kQ), sd = desc_k(smem_u32(sS));
+                const uint64_t qd = desc_k(smem_u32(sQ) + n % NSQ * Lay::kQ), sd = desc_k(smem_u32(sS));
+                constexpr int SETS = TWIN ? 4 : 2;   // small pieces first
 #pragma unroll
-                for (int ks = 0; ks < D / 16; ++ks)
+                for (int t = SETS - 1; t >= 0; --t)
 #pragma unroll
-                    for (int t = 0; t < (TWIN ? 2 : 1); ++t)
+                    for (int ks = 0; ks < D / 16; ++ks)
                         mma_ss_if(leader, tb + kColY, qd + (uint32_t)(((ks >> 2) * 16384 + (ks & 3) * 32) >> 4),
-                                  sd + (uint32_t)((t * Lay::kHalfS + (ks >> 2) * DV * 128 + (ks & 3) * 32) >> 4), iQS, ks + t > 0);
+                                  sd + (uint32_t)((t * Lay::kHalfS + (ks >> 2) * DV * 128 + (ks & 3) * 32) >> 4), iQS,
+                                  t < SETS - 1 || ks > 0);
                 mma_commit_if(leader, &S.qs_done);
             }
             if (NH == 2) {
@@ -322,8 +332,11 @@ retain_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
                 tc_fence_after();
                 const uint64_t vd = smem_desc(smem_u32(sV) + s * Lay::kV, 16384, 1024, kSwizzle128B);
 #pragma unroll
-                for (int ks = 0; ks < kTC / 16; ++ks)
-                    mma_ts_if(leader, tb + kColY + (TWIN ? 64 : 0), tb + kColP + ks * 8, vd + ks * 128, iPV, !TWIN || ks > 0);
+                for (int pc = 1; pc >= 0; --pc)   // small pieces first: 16 columns behind the others' 16
+#pragma unroll
+                    for (int ks = 0; ks < kTC / 16; ++ks)
+                        mma_ts_if(leader, tb + kColY + (TWIN ? 64 : 0), tb + kColP + (ks >> 1) * 32 + pc * 16 + (ks & 1) * 8, vd + ks * 128,
+                                  iPV, !TWIN || pc < 1 || ks > 0);
                 mma_commit_if(leader, &S.pv_done[s]);
             }
             if (n + 1 < nch) scores(n + 1);
@@ -354,13 +367,16 @@ retain_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
 #pragma unroll
             for (int i = 0; i < SC; ++i) st[i] = 0.f;
         }
-        auto put_state = [&] {   // S^T in bf16, rows of d
+        auto put_state = [&] {   // S^T in two bf16 pieces, rows of d
 #pragma unroll
             for (int i = 0; i < SC; i += 8) {
                 const int c = half * SC + i;
-                *reinterpret_cast<uint4 *>(sS + part * Lay::kHalfS + (c >> 6) * (DV * 128) + sw128_off(col, c & 63)) =
-                    make_uint4(pack_bf16x2(st[i], st[i + 1]), pack_bf16x2(st[i + 2], st[i + 3]),
-                               pack_bf16x2(st[i + 4], st[i + 5]), pack_bf16x2(st[i + 6], st[i + 7]));
+                uint8_t *at = sS + part * Lay::kHalfS + (c >> 6) * (DV * 128) + sw128_off(col, c & 63);
+                uint32_t hi[4], lo[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) pieces2(st[i + 2 * j], st[i + 2 * j + 1], hi[j], lo[j]);
+                *reinterpret_cast<uint4 *>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                *reinterpret_cast<uint4 *>(at + (TWIN ? 2 : 1) * Lay::kHalfS) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
             }
             fence_proxy_async();
             mbar_arrive(&S.s_ready);
@@ -503,20 +519,23 @@ retain_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
             {
                 tc_fence_after();
 #pragma unroll 1
-                for (int jb = 0; jb < kTC; jb += 32) {   // over P itself: columns j / 2 of a row that has been read beyond column j
+                for (int jb = 0; jb < kTC; jb += 32) {   // over P itself: of each 32 columns 16 for the first pieces, 16 for the second
                     const int side = jb - 32 * wq;       // warp-uniform
-                    uint32_t x[32], o[16];
+                    uint32_t x[32], o[16], o2[16];
                     if (REV ? side < 0 : side > 0) {     // beyond the diagonal
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) o[j] = 0u;
+                        for (int j = 0; j < 16; ++j) o[j] = o2[j] = 0u;
                     } else {
                         tmem_ld16(pcol + jb, *reinterpret_cast<uint32_t(*)[16]>(x));
                         tmem_ld16(pcol + jb + 16, *reinterpret_cast<uint32_t(*)[16]>(x + 16));
                         if (side == 0) {   // bits that are not kept: a score that is not finite leaves nothing of itself
                             tmem_wait_ld();
 #pragma unroll
-                            for (int j = 0; j < 16; ++j)
-                                o[j] = pack_bf16x2(dg[2 * j] * u2f(x[2 * j]), dg[2 * j + 1] * u2f(x[2 * j + 1])) & keep[j];
+                            for (int j = 0; j < 16; ++j) {
+                                pieces2(dg[2 * j] * u2f(x[2 * j]), dg[2 * j + 1] * u2f(x[2 * j + 1]), o[j], o2[j]);
+                                o[j] &= keep[j];
+                                o2[j] &= keep[j];
+                            }
                         } else {
                             const float f0 = pw[REV ? row - jb : jb + 15 - row], f1 = pw[REV ? row - jb - 16 : jb + 31 - row];
                             tmem_wait_ld();
@@ -526,11 +545,12 @@ retain_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
                                 float a, bb;
                                 f2unpack(f2mul(f2mul(f2pack(f, f), f2pack(nr[2 * j & 15], nr[(2 * j + 1) & 15])),
                                                f2pack(u2f(x[2 * j]), u2f(x[2 * j + 1]))), a, bb);
-                                o[j] = pack_bf16x2(a, bb);
+                                pieces2(a, bb, o[j], o2[j]);
                             }
                         }
                     }
-                    tmem_st16(pcol + jb / 2, o);
+                    tmem_st16(pcol + jb, o);
+                    tmem_st16(pcol + jb + 16, o2);
                 }
                 tmem_wait_st();
                 tc_fence_before();
@@ -565,7 +585,7 @@ retain_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
             }
             if (!__all_sync(0xffffffffu, mbar_wait<2>(&S.pv_done[n % NST], turn(n), g, 32))) break;
             {
-                uint8_t *sY = y_tile(n);   // where Q was: it has been read (its own place: the copy before the last from there has, before this block's Q came)
+                uint8_t *sY = y_tile(n);
                 tc_fence_after();
                 const bool bad = *(volatile int *)&S.v_bad[n & 3] == n + 1;
 #pragma unroll 1
