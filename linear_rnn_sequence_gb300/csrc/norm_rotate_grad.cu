@@ -137,8 +137,9 @@ __global__ void __launch_bounds__(kRotThreads, 2) norm_rotate_grad_kernel(const 
                             ta[i][t] = fmaf(ga[u][i][t], xa[u][i][t] * s, ta[i][t]);
                             tb[i][t] = fmaf(gb[u][i][t], xb[u][i][t] * s, tb[i][t]);
                         }
-                        xa[u][i][t] = so * fmaf(-along, xa[u][i][t], ga[u][i][t] * wa[i][t]);
-                        xb[u][i][t] = so * fmaf(-along, xb[u][i][t], gb[u][i][t] * wb[i][t]);
+                        const float fa = ga[u][i][t] * wa[i][t], fb = gb[u][i][t] * wb[i][t];   // without a norm x has no say
+                        xa[u][i][t] = p.c > 0.f ? so * fmaf(-along, xa[u][i][t], fa) : fa;
+                        xb[u][i][t] = p.c > 0.f ? so * fmaf(-along, xb[u][i][t], fb) : fb;
                     }
                     if (keep && pl.live[i]) {
                         *reinterpret_cast<Raw *>(here.y + (h + u) * sd.y.h + pl.a[i]) = Ch::put(xa[u][i]);
