@@ -576,8 +576,11 @@ LA_API la_status la_layer_norm_backward(const void *dy, const void *x, const flo
  *              output must not overlap each other.
  *   weights    float32 [d], each may be NULL (ones).
  *   freq       float64 [rotated], radians a position; NULL with rotated = 0.  Angles are formed as
- *              fractions of a turn in 64-bit integers: far positions lose nothing.  A frequency that
- *              is not finite, or of 2^64 and more, makes what it turns NaN.
+ *              fractions of a turn in 64-bit integers, those of positions of 2^32 and more or
+ *              frequencies of 8 and more in 128-bit ones: off by less than 2^-27 turns, about
+ *              float32's rounding of a sine, at every position for frequencies up to 2^40 (beyond
+ *              those by less than |position freq| 2^-129 turns).  A frequency that is not finite, or
+ *              of 2^64 and more, makes what it turns NaN.
  *   positions  int64, of batch row b and token t at positions[b positions_stride + t]; NULL: t.
  * 2 <= d <= 256, even (else LA_ERR_UNSUPPORTED); 0 <= 2 rotated <= d; B, Hq, Hk >= 1,
  * Hq + Hk < 65536; N >= 0; B*N < 2^31; eps finite and > 0 (not read without a norm).  Pointers to q,

@@ -53,7 +53,7 @@ __global__ void __launch_bounds__(kRotThreads) norm_rotate_kernel(const RotParam
             wa[i][t] = sd.weight ? sd.weight[pl.a[i] + t] : 1.f;
             wb[i][t] = sd.weight ? sd.weight[pl.b[i] + t] : 1.f;
         }
-    pl.at(p.positions ? p.positions[b * p.pos_batch + n] : n);
+    pl.at(p, p.positions ? p.positions[b * p.pos_batch + n] : n);
 
 #pragma unroll 1
     for (int h = h0; h < h1; h += U) {

@@ -101,27 +101,52 @@ template <int VEC, bool ADJ> __device__ __forceinline__ void chunk_at(int c, int
     }
 }
 
-// The pair's frequency as a fraction of a turn in units of 2^-64, so that position times it is the angle with whole
-// turns dropped by the overflow: 1 / (2 pi) in 66 bits, the product's top bits.  Far positions lose nothing: at
-// 2^31 an angle is off by 2^-21 of the last place of freq.  `ok` is false for what has no angle.
+// Angles are fractions of a turn in units of 2^-64: the frequency becomes such a fraction, and position times it drops
+// whole turns by the overflow.  With the frequency's bits m, m / (2 pi) is a product with 2^66 / (2 pi) cut to an integer,
+// shifted to its exponent.  An angle is off by less than |position| (2^-64 + |freq| 2^-66) turns: 2^-30 turns for positions
+// below kNear and frequencies below kSlow.
+constexpr long long kNear = 1ll << 32;
+constexpr double kSlow = 8.0;
+struct FreqBits {
+    uint64_t m;   // |freq| = m 2^(e - 63)
+    int e;
+    __device__ __forceinline__ explicit FreqBits(double freq) {
+        const uint64_t bits = (uint64_t)__double_as_longlong(freq);
+        e = (int)((bits >> 52) & 0x7FF) - 1023;
+        m = ((bits & 0xFFFFFFFFFFFFFull) | (1ull << 52)) << 11;
+    }
+    __device__ __forceinline__ bool none() const { return e <= -1023 || e >= 64; }   // zero and what is next to it; no angle
+};
+constexpr uint64_t kInv2Pi = 0xA2F9836E4E441529ull, kInv2PiLow = 0xFC2757D1F534DDC0ull;   // 2^130 / (2 pi), upper and lower half
+// `ok` is false for what has no angle: 2^64 and more, infinities, NaN.
 __device__ __forceinline__ uint64_t turn_fraction(double freq, bool &ok) {
-    const uint64_t bits = (uint64_t)__double_as_longlong(freq);
-    const int e = (int)((bits >> 52) & 0x7FF) - 1023;
-    ok = e < 64;
-    if (e <= -1023 || !ok) return 0ull;   // zero and what is next to it; 2^64 and more, infinities, NaN
-    const uint64_t m = ((bits & 0xFFFFFFFFFFFFFull) | (1ull << 52)) << 11;   // freq = m 2^(e - 63)
-    constexpr uint64_t kInv2Pi = 0xA2F9836E4E441529ull;                     // 2^66 / (2 pi)
-    const uint64_t hi = __umul64hi(m, kInv2Pi), lo = m * kInv2Pi;           // turns 2^(129 - e)
-    const int s = 65 - e;
+    const FreqBits f(freq);
+    ok = f.e < 64;
+    if (f.none()) return 0ull;
+    const uint64_t hi = __umul64hi(f.m, kInv2Pi), lo = f.m * kInv2Pi;   // turns 2^(129 - e)
+    const int s = 65 - f.e;
     uint64_t t;
     if (s >= 128) t = 0ull;
     else if (s >= 64) t = hi >> (s - 64);
     else t = (hi << (64 - s)) | (lo >> s);
-    return bits >> 63 ? 0ull - t : t;
+    return freq < 0.0 ? 0ull - t : t;
 }
-__device__ __forceinline__ void sine_of(uint64_t turn, bool ok, long long pos, float &cs, float &sn) {
-    const float half_turns = __ll2float_rn((long long)(turn * (uint64_t)pos)) * 0x1p-63f;
-    sincospif(half_turns, &sn, &cs);
+// The angle of any position and frequency that has one: the same with fractions in units of 2^-128 and 1 / (2 pi) in 130 bits, off
+// by less than |position| (2^-128 + |freq| 2^-130) turns, 2^-27 for frequencies below 2^40 and every position.  It costs the
+// forward 5% where every token takes it.
+__device__ __forceinline__ uint64_t far_angle(double freq, long long pos) {
+    const FreqBits f(freq);
+    if (f.none()) return 0ull;
+    const uint64_t p0 = f.m * kInv2PiLow, mid = f.m * kInv2Pi, p1 = mid + __umul64hi(f.m, kInv2PiLow),
+                   p2 = __umul64hi(f.m, kInv2Pi) + (p1 < mid);
+    const int s = 65 - f.e, w = s >> 6, b = s & 63;   // turns 2^(193 - e); s >= 2
+    const uint64_t x0 = w == 0 ? p0 : w == 1 ? p1 : w == 2 ? p2 : 0ull, x1 = w == 0 ? p1 : w == 1 ? p2 : 0ull, x2 = w == 0 ? p2 : 0ull;
+    const uint64_t lo = b ? (x0 >> b) | (x1 << (64 - b)) : x0, hi = b ? (x1 >> b) | (x2 << (64 - b)) : x1;
+    const uint64_t n = pos < 0 ? 0ull - (uint64_t)pos : (uint64_t)pos, at = hi * n + __umul64hi(lo, n);
+    return (pos < 0) != (freq < 0.0) ? 0ull - at : at;
+}
+__device__ __forceinline__ void sine_of(uint64_t angle, bool ok, float &cs, float &sn) {
+    sincospif(__ll2float_rn((long long)angle) * 0x1p-63f, &sn, &cs);
     if (!ok) cs = sn = __int_as_float(0x7FFFFFFF);
 }
 
@@ -138,9 +163,11 @@ template <int VEC, int CP, bool ADJ> struct Place {
     uint64_t turn[CP][VEC];    // of the pairs of both chunks
     unsigned rot[CP];          // which of them are rotated (ADJ = false: all or none)
     unsigned bad[CP];          // and have no angle
+    bool fast;                 // one of its frequencies is kSlow or more
     float cs[CP][VEC], sn[CP][VEC];
 
     template <int LPR> __device__ __forceinline__ void init(const RotParams &p, int gl) {
+        fast = false;
 #pragma unroll
         for (int i = 0; i < CP; ++i) {
             const int c = gl + LPR * i;
@@ -149,23 +176,30 @@ template <int VEC, int CP, bool ADJ> struct Place {
             rot[i] = bad[i] = 0;
 #pragma unroll
             for (int t = 0; t < VEC; ++t) {
-                const int pair = ADJ ? a[i] / 2 + t : a[i] + t;   // ADJ: VEC/2 pairs of each chunk, in order
                 bool ok = true;
                 turn[i][t] = 0ull;
-                if (pair < p.r) {
+                if (pair(i, t) < p.r) {
+                    const double f = p.freq[pair(i, t)];
                     rot[i] |= 1u << t;
-                    turn[i][t] = turn_fraction(p.freq[pair], ok);
+                    turn[i][t] = turn_fraction(f, ok);
                     if (!ok) bad[i] |= 1u << t;
+                    fast |= !(f < kSlow && f > -kSlow);
                 }
             }
         }
     }
-    __device__ __forceinline__ void at(long long pos) {
+    __device__ __forceinline__ int pair(int i, int t) const { return ADJ ? a[i] / 2 + t : a[i] + t; }   // ADJ: VEC/2 of each chunk, in order
+    __device__ __forceinline__ void at(const RotParams &p, long long pos) {
+        const bool far = fast || pos >= kNear || pos <= -kNear;
 #pragma unroll
         for (int i = 0; i < CP; ++i)
             if (ADJ || rot[i])
 #pragma unroll
-                for (int t = 0; t < VEC; ++t) sine_of(turn[i][t], !(bad[i] >> t & 1), pos, cs[i][t], sn[i][t]);
+                for (int t = 0; t < VEC; ++t) {
+                    uint64_t angle = turn[i][t] * (uint64_t)pos;
+                    if (far && (rot[i] >> t & 1)) angle = far_angle(p.freq[pair(i, t)], pos);
+                    sine_of(angle, !(bad[i] >> t & 1), cs[i][t], sn[i][t]);
+                }
     }
     // Turns the pairs of chunk pair i, backwards with sign = -1.
     __device__ __forceinline__ void rotate(int i, float (&x)[VEC], float (&y)[VEC], float sign) const {

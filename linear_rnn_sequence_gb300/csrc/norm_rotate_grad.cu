@@ -73,7 +73,7 @@ __global__ void __launch_bounds__(kRotThreads, 2) norm_rotate_grad_kernel(const 
     while (true) {
         const bool live = t0 + grp < p.tokens, more = t0 + step < p.tokens;
         const At next = more ? token(t0 + step) : here;
-        pl.at(here.pos);
+        pl.at(p, here.pos);
         float ta[CP][VEC], tb[CP][VEC];   // this token's
 #pragma unroll
         for (int i = 0; i < CP; ++i)

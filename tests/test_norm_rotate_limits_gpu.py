@@ -1,4 +1,6 @@
-"""Norm and rotation at the ends of what the calls accept: values that are not finite where no norm looks at them."""
+"""Norm and rotation at the ends of what the calls accept: far positions and large frequencies, values that are not finite
+where no norm looks at them (bounds: rotate_ref.py; the angle of a frequency below 2^40 at any position is off by less than
+2^-27 turns, 4.7e-8, of which the bounds' 64 roundings leave room for 25)."""
 import pytest
 import torch
 
@@ -12,6 +14,34 @@ BF16, F32 = torch.bfloat16, torch.float32
 
 def args(x):
     return dict(freq=x["freq"].cuda(), positions=x["positions"].cuda(), q_weight=x["wq"].cuda(), k_weight=x["wk"].cuda())
+
+
+FAR = [2 ** 46 + 3, 2 ** 50 + 12345, 2 ** 55 - 1, 2 ** 60 + 7, 2 ** 63 - 1, -2 ** 63, -2 ** 52 - 9, 2 ** 31, 2 ** 20 + 1, -1, 0]
+
+
+# on both sides of where angles go from 64-bit fractions to 128-bit ones
+BORDER = [2 ** 32 - 1, 2 ** 32, 2 ** 32 + 1, -2 ** 32 + 1, -2 ** 32, -2 ** 32 - 1, 2 ** 31 + 5, 3, 1, 0, -1]
+FREQ = [1.0, -0.5, 0.1, 1e-4, 1e-12, 3.0, 6.283185307179586, 100.0, 1e5, -1e5, 2.0 ** 40 - 1, 2.0 ** -40, 0.0, 1e9, 2.0 ** -70, 1e-19]
+SLOW = [1.0, -0.5, 0.1, 1e-4, 1e-12, 3.0, 6.283185307179586, 7.999999, 7.0, -7.9, 5.5, 2.0 ** -40, 0.0, 2.5, 2.0 ** -70, 1e-19]
+
+
+@pytest.mark.parametrize("pairs", ["halves", "adjacent"])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("positions,freq", [(FAR, FREQ), (FAR, SLOW), (BORDER, SLOW), (BORDER, FREQ), (BORDER, SLOW[:-1] + [8.0]),
+                                            (BORDER, [-8.0] + SLOW[1:])])
+def test_far_positions_and_large_frequencies(positions, freq, dtype, pairs):
+    x = R.inputs(1, 2, 2, len(positions), 32, dtype, seed=1)
+    x["positions"] = torch.tensor(positions)
+    x["freq"] = torch.tensor(freq, dtype=torch.float64)
+    q, k, gq, gk = (x[n].cuda() for n in ("q", "k", "gq", "gk"))
+    out = la.norm_rotate(q, k, pairs=pairs, **args(x))
+    res = la.norm_rotate_backward(gq, gk, q, k, pairs=pairs, **args(x))
+    for key, y, g, gw in zip("qk", out, res[:2], res[2:]):
+        want, size = R.forward(x, key, pairs=pairs)
+        R.near(y, want, size, R.E, f"{key} out")
+        dx, size, dw, wsize = R.backward(x, key, pairs=pairs)
+        R.near(g, dx, size, R.E2, f"grad_{key}")
+        R.near(gw, dw, wsize, R.E_SUM, f"grad_{key}_weight")
 
 
 @pytest.mark.parametrize("pairs", ["halves", "adjacent"])
