@@ -586,7 +586,8 @@ LA_API la_status la_layer_norm_backward(const void *dy, const void *x, const flo
  * Hq + Hk < 65536; N >= 0; B*N < 2^31; eps finite and > 0 (not read without a norm).  Pointers to q,
  * k and the outputs aligned to their element size (16 bytes, and strides and sizes to match, are
  * faster), weights to 4, freq and positions to 8 bytes.  q_out may be q and k_out may be k, with the
- * same strides; no other output may overlap an input or output.  The sums are float32.
+ * same strides; no other output may overlap an input or output (rows may lie among rows of the same
+ * strides, of other strides not).  The sums are float32.
  * A single token of each sequence: N = 1.
  */
 LA_API la_status la_norm_rotate(const void *q, const void *k, void *q_out, void *k_out,

@@ -783,14 +783,33 @@ bool rows_overlap_each_other(const Rows &r) {
     return false;
 }
 
-// May a row of a and a row of b share bytes?  Parts of one buffer, whose common strides keep them apart, do not;
-// what cannot be told counts as shared.
+// Does some row of b lie less than a row from some row of a, b's first being `at` elements behind a's?  Along the dimensions
+// o[i] .. of common strides s, the widest first, only those steps count that the narrower dimensions can make up for.
+bool rows_meet(const Rows &a, const Rows &b, const long long (&s)[3], const int (&o)[3], int i, long long at) {
+    if (i == 3) return at < a.d && -at < a.d;
+    const int x = o[i];
+    if (s[x] == 0) return rows_meet(a, b, s, o, i + 1, at);
+    long long up = a.d - 1, down = a.d - 1;   // narrower steps of a's and of b's, and a row
+    for (int j = i + 1; j < 3; ++j) {
+        up += (a.n[o[j]] - 1) * s[o[j]];
+        down += (b.n[o[j]] - 1) * s[o[j]];
+    }
+    auto floored = [&](long long v) { return v >= 0 ? v / s[x] : -((-v + s[x] - 1) / s[x]); };
+    long long first = -floored(at + down), last = floored(up - at);   // -down <= at + steps s <= up
+    if (first < 1 - a.n[x]) first = 1 - a.n[x];
+    if (last > b.n[x] - 1) last = b.n[x] - 1;
+    if (last - first > 8) return first <= last;   // strides that are not nested (inputs): not looked into
+    for (long long steps = first; steps <= last; ++steps)
+        if (rows_meet(a, b, s, o, i + 1, at + steps * s[x])) return true;
+    return false;
+}
+
+// May a row of a and a row of b share bytes?  Rows of other strides count as sharing what lies between their ends.
 bool rows_overlap(const Rows &a, const Rows &b) {
     const uintptr_t pa = reinterpret_cast<uintptr_t>(a.v.p), pb = reinterpret_cast<uintptr_t>(b.v.p);
     if (pa > pb) return rows_overlap(b, a);
     if ((uintptr_t)a.extent() * a.es <= pb - pa) return false;
     if ((pb - pa) % a.es) return true;
-    const long long apart = (long long)((pb - pa) / a.es);
     long long s[3];
     for (int i = 0; i < 3; ++i) {
         if (a.n[i] > 1 && b.n[i] > 1 && a.st(i) != b.st(i)) return true;
@@ -798,16 +817,7 @@ bool rows_overlap(const Rows &a, const Rows &b) {
     }
     int o[3];
     widest_first(s, o);
-    long long ea = a.extent(), eb = b.extent();
-    for (int i = 0; i < 3 && s[o[i]] > 0; ++i) {   // all rows of a, and of b, at the same place modulo this stride?
-        ea -= (a.n[o[i]] - 1) * a.st(o[i]);
-        eb -= (b.n[o[i]] - 1) * b.st(o[i]);
-        const long long w = s[o[i]], at = apart % w;
-        bool whole = true;
-        for (int j = 0; j < i; ++j) whole = whole && s[o[j]] % w == 0;
-        if (whole && at >= ea && at + eb <= w) return false;
-    }
-    return true;
+    return rows_meet(a, b, s, o, 0, (long long)((pb - pa) / a.es));
 }
 
 bool same_rows(const Rows &a, const Rows &b) {
