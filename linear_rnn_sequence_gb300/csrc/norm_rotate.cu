@@ -78,27 +78,27 @@ __global__ void __launch_bounds__(kRotThreads) norm_rotate_kernel(const RotParam
             eps[u] = p.eps;
         }
         if (p.c > 0.f) {
-            bool big = false;
+            bool again = false;
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 ss[u] = group_sum<LPR>(ss[u]);
-                big |= !(ss[u] <= kRotBig);
+                again |= !sum_holds(ss[u], p.least);
             }
-            if (__any_sync(0xffffffffu, big)) {   // squares that pass float32's range
+            if (__any_sync(0xffffffffu, again)) {   // squares that pass float32's range
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
-                    const float down = ss[u] <= kRotBig ? 1.f : kRotDown;
+                    const float by = rescale(ss[u], p.least);
                     ss[u] = 0.f;
 #pragma unroll
                     for (int i = 0; i < CP; ++i)
 #pragma unroll
                         for (int t = 0; t < VEC; ++t) {
-                            xa[u][i][t] *= down;
-                            xb[u][i][t] *= down;
+                            xa[u][i][t] *= by;
+                            xb[u][i][t] *= by;
                             ss[u] = fmaf(xa[u][i][t], xa[u][i][t], fmaf(xb[u][i][t], xb[u][i][t], ss[u]));
                         }
                     ss[u] = group_sum<LPR>(ss[u]);
-                    eps[u] *= down * down;
+                    eps[u] = eps[u] * by * by;
                 }
             }
         }

@@ -22,8 +22,10 @@ namespace {
 
 constexpr int kMostVec = 4;   // values of a chunk: the row's sums and sines over twice as many lanes as with 16-byte chunks of
                              // bf16, and half the registers of each (gradients 293 us, with chunks of 8 343; forward 189 and 197)
-// A row whose squares sum to more than kRotBig (or to no number) is summed again with its values times kRotDown.
-constexpr float kRotBig = 1e37f, kRotDown = 0x1p-70f;
+// A row whose squares sum to more than kRotBig (or to no number) is summed again with its values times kRotDown, one whose
+// squares sum to less than kRotSmall, if eps is below that too, with its values times kRotUp: float32 holds squares below
+// 2^-126 with fewer and fewer bits.
+constexpr float kRotBig = 1e37f, kRotDown = 0x1p-70f, kRotSmall = 0x1p-90f, kRotUp = 0x1p70f;
 
 // VEC values of T as they lie in memory.
 template <typename T, int VEC> struct Chunk;
@@ -70,6 +72,9 @@ template <> struct Chunk<float, 1> {
     static __device__ __forceinline__ Raw put(const float (&x)[1]) { return x[0]; }
 };
 
+__device__ __forceinline__ bool sum_holds(float ss, float least) { return ss <= kRotBig && ss >= least; }
+__device__ __forceinline__ float rescale(float ss, float least) { return !(ss <= kRotBig) ? kRotDown : ss >= least ? 1.f : kRotUp; }
+
 // One of q and k.
 struct RotSide {
     HeadsView x, g, y;      // input; gradient of the output (gradients only); output or the input's gradient
@@ -83,6 +88,7 @@ struct RotParams {
     int span;               // heads of a range
     int blocks;             // CTAs along the tokens
     float c, eps;           // c = 0: no norm
+    float least;            // kRotSmall, or 0 where eps makes up for what small squares lose
     const double *freq;
     const long long *positions;   // nullable (the token's index)
     long long pos_batch;          // its stride from one sequence to the next
@@ -259,6 +265,7 @@ inline RotParams rot_params(const NormRotateArgs &a) {
     p.N = a.N; p.d = a.d; p.r = a.r;
     p.c = a.norm == LA_NORM_RMS ? 1.f / a.d : a.norm == LA_NORM_L2 ? 1.f : 0.f;
     p.eps = a.eps;
+    p.least = a.eps < kRotSmall ? kRotSmall : 0.f;
     p.freq = a.freq;
     p.positions = a.positions;
     p.pos_batch = a.pos_batch;

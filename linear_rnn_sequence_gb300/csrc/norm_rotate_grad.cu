@@ -110,25 +110,25 @@ __global__ void __launch_bounds__(kRotThreads, 2) norm_rotate_grad_kernel(const 
                     ss = group_sum<LPR>(ss);
                     gx = group_sum<LPR>(gx);
                 };
-                float s = 1.f, along = 0.f, down = 1.f;
+                float s = 1.f, along = 0.f, by = 1.f;
                 if (p.c > 0.f) {
                     sums();
-                    if (__any_sync(0xffffffffu, !(ss <= kRotBig))) {   // squares that pass float32's range
-                        down = ss <= kRotBig ? 1.f : kRotDown;
+                    if (__any_sync(0xffffffffu, !sum_holds(ss, p.least))) {   // squares that pass float32's range
+                        by = rescale(ss, p.least);
 #pragma unroll
                         for (int i = 0; i < CP; ++i)
 #pragma unroll
                             for (int t = 0; t < VEC; ++t) {
-                                xa[u][i][t] *= down;
-                                xb[u][i][t] *= down;
+                                xa[u][i][t] *= by;
+                                xb[u][i][t] *= by;
                             }
                         sums();
                     }
-                    s = rsqrtf(fmaf(p.c, ss, p.eps * (down * down)));
+                    s = rsqrtf(fmaf(p.c, ss, p.eps * by * by));
                     along = p.c * s * s * gx;
                 }
                 const bool keep = live && h + u < h1;
-                const float so = s * down;
+                const float so = s * by;
 #pragma unroll
                 for (int i = 0; i < CP; ++i) {
 #pragma unroll

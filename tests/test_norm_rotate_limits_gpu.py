@@ -1,6 +1,6 @@
-"""Norm and rotation at the ends of what the calls accept: far positions and large frequencies, values that are not finite
-where no norm looks at them (bounds: rotate_ref.py; the angle of a frequency below 2^40 at any position is off by less than
-2^-27 turns, 4.7e-8, of which the bounds' 64 roundings leave room for 25)."""
+"""Norm and rotation at the ends of what the calls accept: far positions and large frequencies, rows next to nothing,
+values that are not finite where no norm looks at them (bounds: rotate_ref.py; the angle of a frequency below 2^40 at any
+position is off by less than 2^-27 turns, 4.7e-8, of which the bounds' 64 roundings leave room for 25)."""
 import pytest
 import torch
 
@@ -61,3 +61,24 @@ def test_gradients_without_a_norm_do_not_see_the_inputs(d, dtype, pairs):
         same = torch.ones(d, dtype=torch.bool)
         same[hurt] = False
         assert torch.equal(g.cpu()[same], c.cpu()[same]) and not bool(torch.isfinite(g.cpu()[hurt]).any())
+
+
+@pytest.mark.parametrize("norm", ["rms", "l2"])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("eps", [2.0 ** -149, 2.0 ** -133, 2.0 ** -100, 2.0 ** -91, 2.0 ** -90, 2.0 ** -89])
+def test_small_rows_and_a_smaller_eps(eps, dtype, norm):
+    """Rows whose squares float32 does not hold, beside others."""
+    x = R.inputs(1, 3, 2, 8, 64, dtype, seed=3)
+    for n in "qk":
+        for t, down in enumerate((0.0, 2.0 ** -74, 2.0 ** -66, 2.0 ** -52, 2.0 ** -48, 2.0 ** -45, 2.0 ** -30)):
+            x[n][:, :, t] *= down
+    q, k, gq, gk = (x[n].cuda() for n in ("q", "k", "gq", "gk"))
+    kw = dict(args(x), norm=norm, eps=eps)
+    out = la.norm_rotate(q, k, **kw)
+    res = la.norm_rotate_backward(gq, gk, q, k, **kw)
+    for key, y, g, gw in zip("qk", out, res[:2], res[2:]):
+        want, size = R.forward(x, key, norm=norm, eps=eps)
+        R.near(y, want, size, R.E, f"{key} out")
+        dx, size, dw, wsize = R.backward(x, key, norm=norm, eps=eps)
+        R.near(g, dx, size, R.E2, f"grad_{key}")
+        R.near(gw, dw, wsize, R.E_SUM, f"grad_{key}_weight")
