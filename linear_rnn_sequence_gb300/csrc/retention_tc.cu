@@ -15,11 +15,13 @@
 //                thread's registers; S^T in two bf16 pieces to shared memory for Q S;
 //   warp 12      issues the MMAs: of a block the first half of K^T W (64 of d), Q S, the second half over the first's
 //                accumulator (d = 64: there is one), P~ V, then the next block's Q K^T;
-//   warp 13      issues the copies.
+//   warp 13      issues the copies;
+//   two more     (d = 64) P~ of half the columns of the rows that see most.
 // W is the one operand without a second place in TMEM: its three pieces, the halves of K^T W, the state's update between
-// them and Q S, which stands between the halves, are the chain that bounds a block.  d = dv = 128: about 6,500 cycles, of
-// which the products take 4,100 (K^T W 1,540, Q S and P~ V 1,020 each, Q K^T 510).  B8 H16 N8192 d128: 221 us, 4.9 TB/s of the
-// 6.7 that a copy reaches; B1 H32 N131072 d64, in 19 segments: 641 us.
+// them and Q S, which stands between the halves, are the chain that bounds a block of d = 128: at dv = 128 about 5,300 cycles, of
+// which the products take 4,100 (K^T W 1,540, Q S and P~ V 1,020 each, Q K^T 510).  For d = 64 it is the one over P~, P~ V and y
+// to the next scores.  B8 H16 N8192 d128: 220 us, 4.9 TB/s of the 6.7 that a copy reaches (inputs that stay the same from call
+// to call 202); B1 H32 N131072 d64, in 19 segments: 615 us.
 //
 // With dv = 64 the upper 64 TMEM lanes hold W of the block's second 64 tokens (and zeros for the first, as the lower ones do for
 // the second), so that every warp makes half as much of it; the lanes' sums stay two states that add up to S, and Q S takes
@@ -30,8 +32,8 @@
 // bf16 K, small pieces first.  What only y depends on, each score and each value of the state that it meets, enters as two
 // pieces: 2^-15 of each at most is lost, as much as float32 sums of that length lose.  With one piece, 2^-8 of each, y was
 // off by sqrt(2) times its own rounding where the terms are of random signs, but by a tenth of itself where they cancel
-// (states with a common part of 64 times the rest that the queries do not see); the second pieces took the call above from 190
-// to 221 us.  y is rounded to bf16.
+// (states with a common part of 64 times the rest that the queries do not see); the second pieces took the calls above
+// from 190 to 220 and from 560 to 615 us.  y is rounded to bf16.
 //
 // What is not finite reaches no token before its own: masked scores are zeros, and a value of v that is not finite would
 // make 0 * inf of them.  It also makes its column of K^T W something not finite, which (d = 128) the warps of the state see
@@ -45,9 +47,9 @@ namespace la {
 namespace {
 
 constexpr int kTC = 128;                      // tokens of a block
-constexpr int kState = 256, kRetThr = 14 * 32;   // threads: of the state's warps, all
+constexpr int kState = 256;                   // threads of the state's warps
 
-// TMEM columns: P (P~ over its first half), y, half of K^T W, three pieces of W.  For the segments' sums alone: K^T W, and W
+// TMEM columns: P (P~ over it), y, half of K^T W, three pieces of W.  For the segments' sums alone: K^T W, and W
 // twice, so that the next one is made while the products of this one run.
 constexpr uint32_t kColP = 0, kColY = 128, kColKV = 256, kColW3 = 320;
 constexpr uint32_t kColSumW = 128;   // K^T W from column 0, W from 128 and 320 on
@@ -81,6 +83,10 @@ enum RetainMode { kWhole, kSums };
 
 template <int D, int DV, int MODE> struct RetainLay {
     static constexpr bool OUT = MODE == kWhole;
+    // d = 64, where the chain from a block's scores over P~, P~ V and y to the next block's is the longest: two warps more for P~
+    // (B8 H16 N8192 d64 118 us, without them 129; dv = 128 169 and 185; at d = 128 they would cost 2%)
+    static constexpr bool HELP = OUT && D == 64;
+    static constexpr int threads = HELP ? 512 : 448;
     static constexpr int kQ = (D / 64) * 16384, kV = (DV / 64) * 16384;
     // S: one piece of one state (of two if dv = 64); two pieces.  kSums: float32
     static constexpr int kHalfS = DV * D * 2, kS = OUT ? (128 / DV) * 2 * kHalfS : DV * D * 4;
@@ -114,7 +120,7 @@ __device__ __forceinline__ uint8_t *retain_smem() {
 }
 
 template <int D, int DV, bool REV, int MODE>
-__global__ void __launch_bounds__(kRetThr, 1)
+__global__ void __launch_bounds__(RetainLay<D, DV, MODE>::threads, 1)
 retain_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                  const __grid_constant__ CUtensorMap vmap, const __grid_constant__ CUtensorMap ymap, const RetainTc p) {
     using Lay = RetainLay<D, DV, MODE>;
@@ -122,6 +128,10 @@ retain_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
     constexpr int NST = Lay::kNst, NSQ = Lay::kNsq > 0 ? Lay::kNsq : 1;
     constexpr int NH = D / 64;   // halves of K^T W
     constexpr bool TWIN = DV == 64;   // two states, of the tokens' halves; Q S and P~ V in accumulators of their own
+    constexpr bool SPLIT = TWIN && NH == 2;   // Q S in two parts
+    // the warps above 11; HELP: the two quarters of the rows that see most columns have a second one (TMEM lanes go by warp % 4)
+    constexpr bool HELP = Lay::HELP;
+    constexpr int kMma = HELP && REV ? 14 : 12, kCopy = kMma + 1;
     uint8_t *sm = retain_smem();
     RetainSmall &S = *reinterpret_cast<RetainSmall *>(sm + Lay::oSmall);
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
@@ -147,7 +157,7 @@ retain_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
         mbar_init(&S.kv_done[1], 1);
         mbar_init(&S.kv_read, OUT ? kState / 2 : kState);
         mbar_init(&S.qk_done, 1);
-        mbar_init(&S.p_ready, 128);
+        mbar_init(&S.p_ready, HELP ? 192 : 128);
         mbar_init(&S.s_ready, kState);
         mbar_init(&S.qs_done, 1);
         mbar_init(&S.y_scaled, 128);
@@ -162,7 +172,7 @@ retain_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
     }
     if (tid >= 64 && tid <= 64 + 2 * kTC) S.pg[tid - 64] = tid <= 64 + kTC ? gamma_power(gamma, 64 + kTC - tid) : 0.f;
     if (tid >= 32 && tid < 48) S.near[tid - 32] = gamma_power(gamma, REV ? tid - 32 : 47 - tid);
-    if (warp == 12) {
+    if (warp == kMma) {
         tmem_alloc(&S.tmem_base, 512);
         tmem_relinquish();
     }
@@ -179,7 +189,27 @@ retain_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
     auto turn = [](int n) { return (uint32_t)(n / NST) & 1u; };      // parity of block n's use of its place
     auto turn_q = [](int n) { return (uint32_t)(n / NSQ) & 1u; };
 
-    if (warp == 13) {
+    // P~ of 32 columns off the diagonal, over P itself: of each 32 columns 16 for the first pieces, 16 for the second
+    auto fill = [&](int jb, const float (&nr)[16]) {
+        const uint32_t pcol = tb + lb + kColP + jb;
+        uint32_t x[32], o[16], o2[16];
+        tmem_ld16(pcol, *reinterpret_cast<uint32_t(*)[16]>(x));
+        tmem_ld16(pcol + 16, *reinterpret_cast<uint32_t(*)[16]>(x + 16));
+        const float f0 = pw[REV ? row - jb : jb + 15 - row], f1 = pw[REV ? row - jb - 16 : jb + 31 - row];
+        tmem_wait_ld();
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+            const float f = j < 8 ? f0 : f1;
+            float a, bb;
+            f2unpack(f2mul(f2mul(f2pack(f, f), f2pack(nr[2 * j & 15], nr[(2 * j + 1) & 15])), f2pack(u2f(x[2 * j]), u2f(x[2 * j + 1]))),
+                     a, bb);
+            pieces2(a, bb, o[j], o2[j]);
+        }
+        tmem_st16(pcol, o);
+        tmem_st16(pcol + 16, o2);
+    };
+
+    if (warp == kCopy) {
         // ------------------------------------------------------------ copies
         if (elect_leader()) {
             auto load = [&](uint8_t *dst, const CUtensorMap &m, uint64_t *bar, int slabs, int n, bool drop) {
@@ -239,7 +269,7 @@ retain_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
             for (int m = max(0, nq - NSQ); m < nq; ++m) drain_wait(&S.q_full[m % NSQ], turn_q(m), g.limit_ns);
         }
         __syncwarp();
-    } else if (warp == 12) {
+    } else if (warp == kMma) {
         // ------------------------------------------------------------ MMAs
         constexpr uint32_t iP = idesc_bf16(128, kTC, 0, 0), iQS = idesc_bf16(128, DV, 0, 0),
                            iKV = idesc_bf16(128, 64, 0, 1), iPV = idesc_bf16(128, DV, 0, 1);
@@ -270,6 +300,23 @@ retain_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
                 mma_ss_if(leader, tb + kColP, qd + o, kd + o, iP, ks > 0);
             }
             mma_commit_if(leader, &S.qk_done);
+        };
+        // Q S, small pieces of S first.  d = 128, dv = 64: their product stands between the halves of K^T W, the others' behind
+        // them, where nothing but P~ V waits for it (B8 H16 N8192 175 us, all of it between the halves 185; with dv = 128 it is scaled
+        // before P~ V)
+        constexpr int SETS = TWIN ? 4 : 2;
+        auto queries = [&](int n, int from, int to) {
+            const uint32_t leader = elect_leader();
+            tc_fence_after();
+            const uint64_t qd = desc_k(smem_u32(sQ) + n % NSQ * Lay::kQ), sd = desc_k(smem_u32(sS));
+#pragma unroll
+            for (int t = from; t >= to; --t)
+#pragma unroll
+                for (int ks = 0; ks < D / 16; ++ks)
+                    mma_ss_if(leader, tb + kColY, qd + (uint32_t)(((ks >> 2) * 16384 + (ks & 3) * 32) >> 4),
+                              sd + (uint32_t)((t * Lay::kHalfS + (ks >> 2) * DV * 128 + (ks & 3) * 32) >> 4), iQS,
+                              t < SETS - 1 || ks > 0);
+            if (to == 0) mma_commit_if(leader, &S.qs_done);
         };
         // A block with a value of v that is not finite: zero in shared memory, and where the columns' first ones are.
         auto mend_v = [&](int n) {
@@ -305,24 +352,12 @@ retain_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
             kv_half(n, 0);
             all(mbar_wait<2>(&S.s_ready, n & 1, g, 6) && (n == 0 || mbar_wait<2>(&S.y_free, (n - 1) & 1, g, 7)));
             if (!ok) break;
-            {
-                const uint32_t leader = elect_leader();
-                tc_fence_after();
-                const uint64_t qd = desc_k(smem_u32(sQ) + n % NSQ * Lay::kQ), sd = desc_k(smem_u32(sS));
-                constexpr int SETS = TWIN ? 4 : 2;   // small pieces first
-#pragma unroll
-                for (int t = SETS - 1; t >= 0; --t)
-#pragma unroll
-                    for (int ks = 0; ks < D / 16; ++ks)
-                        mma_ss_if(leader, tb + kColY, qd + (uint32_t)(((ks >> 2) * 16384 + (ks & 3) * 32) >> 4),
-                                  sd + (uint32_t)((t * Lay::kHalfS + (ks >> 2) * DV * 128 + (ks & 3) * 32) >> 4), iQS,
-                                  t < SETS - 1 || ks > 0);
-                mma_commit_if(leader, &S.qs_done);
-            }
+            queries(n, SETS - 1, SPLIT ? SETS / 2 : 0);
             if (NH == 2) {
                 all(mbar_wait<2>(&S.kv_read, n & 1, g, 8));
                 if (!ok) break;
                 kv_half(n, 1);
+                if (SPLIT) queries(n, SETS / 2 - 1, 0);
             }
             if (*(volatile int *)&S.v_bad[n & 3] == n + 1) mend_v(n);
             all(mbar_wait<2>(&S.p_ready, n & 1, g, 9) && (TWIN || mbar_wait<2>(&S.y_scaled, n & 1, g, 10)));
@@ -346,6 +381,19 @@ retain_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
             drain_wait(&S.drain, 0, g.limit_ns);
         }
         __syncwarp();
+    } else if (HELP && warp >= 12) {
+        // ------------------------------------------------------------ P~ of the half of the columns away from the diagonal
+        float nr[16];
+        load16(S.near, nr);
+        for (int n = 0; n < nch; ++n) {
+            if (!__all_sync(0xffffffffu, mbar_wait<2>(&S.qk_done, n & 1, g, 33))) break;
+            tc_fence_after();
+#pragma unroll 1
+            for (int jb = REV ? 64 : 0; jb < (REV ? kTC : 64); jb += 32) fill(jb, nr);
+            tmem_wait_st();
+            tc_fence_before();
+            mbar_arrive(&S.p_ready);
+        }
     } else if (warp >= 4) {
         // ------------------------------------------------------------ W and the state
         constexpr int SC = D / 2;   // state values of a thread: column `row` of dv, half * SC .. of d
@@ -469,7 +517,7 @@ retain_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
             if (!(ok = __all_sync(0xffffffffu, ok))) break;
             make_w(n, kColW3);
             mbar_arrive(&S.w_ready[0]);
-            if (NH == 1 && n >= 1) {   // Q S of the block before has read its operand (else K^T W's end says so)
+            if ((NH == 1 || SPLIT) && n >= 1) {   // Q S of the block before has read its operand (else K^T W's end says so)
                 ok = __all_sync(0xffffffffu, mbar_wait<2>(&S.qs_done, (n - 1) & 1, g, 22));
                 if (!ok) break;
             }
@@ -509,6 +557,9 @@ retain_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
         float nr[16], dg[32];   // gamma^(to a block's nearest column); on the diagonal gamma^|i - j|, and what is kept there
         uint32_t keep[16];
         load16(S.near, nr);
+        // columns that are its own: half of them where another warp takes the other
+        const bool helped = HELP && (REV ? wq < 2 : wq >= 2);
+        const int first = !REV && helped ? 64 : 0, count = helped ? 64 : kTC;
 #pragma unroll
         for (int j = 0; j < 32; ++j) dg[j] = (REV ? j >= lane : j <= lane) ? pw[-abs(lane - j)] : 0.f;
 #pragma unroll
@@ -519,34 +570,26 @@ retain_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
             {
                 tc_fence_after();
 #pragma unroll 1
-                for (int jb = 0; jb < kTC; jb += 32) {   // over P itself: of each 32 columns 16 for the first pieces, 16 for the second
+                for (int jb = first; jb < first + count; jb += 32) {
                     const int side = jb - 32 * wq;       // warp-uniform
-                    uint32_t x[32], o[16], o2[16];
-                    if (REV ? side < 0 : side > 0) {     // beyond the diagonal
+                    if (REV ? side > 0 : side < 0) {
+                        fill(jb, nr);
+                        continue;
+                    }
+                    uint32_t o[16], o2[16];
+                    if (side != 0) {   // beyond the diagonal
 #pragma unroll
                         for (int j = 0; j < 16; ++j) o[j] = o2[j] = 0u;
-                    } else {
+                    } else {           // bits that are not kept: a score that is not finite leaves nothing of itself
+                        uint32_t x[32];
                         tmem_ld16(pcol + jb, *reinterpret_cast<uint32_t(*)[16]>(x));
                         tmem_ld16(pcol + jb + 16, *reinterpret_cast<uint32_t(*)[16]>(x + 16));
-                        if (side == 0) {   // bits that are not kept: a score that is not finite leaves nothing of itself
-                            tmem_wait_ld();
+                        tmem_wait_ld();
 #pragma unroll
-                            for (int j = 0; j < 16; ++j) {
-                                pieces2(dg[2 * j] * u2f(x[2 * j]), dg[2 * j + 1] * u2f(x[2 * j + 1]), o[j], o2[j]);
-                                o[j] &= keep[j];
-                                o2[j] &= keep[j];
-                            }
-                        } else {
-                            const float f0 = pw[REV ? row - jb : jb + 15 - row], f1 = pw[REV ? row - jb - 16 : jb + 31 - row];
-                            tmem_wait_ld();
-#pragma unroll
-                            for (int j = 0; j < 16; ++j) {
-                                const float f = j < 8 ? f0 : f1;
-                                float a, bb;
-                                f2unpack(f2mul(f2mul(f2pack(f, f), f2pack(nr[2 * j & 15], nr[(2 * j + 1) & 15])),
-                                               f2pack(u2f(x[2 * j]), u2f(x[2 * j + 1]))), a, bb);
-                                pieces2(a, bb, o[j], o2[j]);
-                            }
+                        for (int j = 0; j < 16; ++j) {
+                            pieces2(dg[2 * j] * u2f(x[2 * j]), dg[2 * j + 1] * u2f(x[2 * j + 1]), o[j], o2[j]);
+                            o[j] &= keep[j];
+                            o2[j] &= keep[j];
                         }
                     }
                     tmem_st16(pcol + jb, o);
@@ -626,7 +669,7 @@ retain_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 12) {
+    if (warp == kMma) {
         tc_fence_after();
         tmem_dealloc(tb, 512);
     }
@@ -668,8 +711,8 @@ template <int D, int DV, bool REV, int MODE> cudaError_t launch_mode(const Retai
     static_assert(smem <= 232448, "shared memory of a CTA");
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    if (behind) return launch_overlapped(kern, dim3(a.B * a.H * p.segs), dim3(kRetThr), smem, a.stream, qm, km, vm, ym, p);
-    kern<<<a.B * a.H * p.segs, kRetThr, smem, a.stream>>>(qm, km, vm, ym, p);
+    if (behind) return launch_overlapped(kern, dim3(a.B * a.H * p.segs), dim3(RetainLay<D, DV, MODE>::threads), smem, a.stream, qm, km, vm, ym, p);
+    kern<<<a.B * a.H * p.segs, RetainLay<D, DV, MODE>::threads, smem, a.stream>>>(qm, km, vm, ym, p);
     return cudaGetLastError();
 }
 
