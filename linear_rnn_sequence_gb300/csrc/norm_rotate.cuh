@@ -110,24 +110,27 @@ template <int VEC, bool ADJ> __device__ __forceinline__ void chunk_at(int c, int
 // Angles are fractions of a turn in units of 2^-64: the frequency becomes such a fraction, and position times it drops
 // whole turns by the overflow.  With the frequency's bits m, m / (2 pi) is a product with 2^66 / (2 pi) cut to an integer,
 // shifted to its exponent.  An angle is off by less than |position| (2^-64 + |freq| 2^-66) turns: 2^-30 turns for positions
-// below kNear and frequencies below kSlow.
+// below kNear and frequencies below 2^kSlow.
 constexpr long long kNear = 1ll << 32;
-constexpr double kSlow = 8.0;
-struct FreqBits {
+constexpr int kSlow = 3;   // the exponent of 8
+struct FreqBits {   // no comparison in 64-bit floating point, which the chip is slow at (10 us became 13 for 3,093 tokens)
     uint64_t m;   // |freq| = m 2^(e - 63)
     int e;
+    bool negative;
     __device__ __forceinline__ explicit FreqBits(double freq) {
         const uint64_t bits = (uint64_t)__double_as_longlong(freq);
         e = (int)((bits >> 52) & 0x7FF) - 1023;
         m = ((bits & 0xFFFFFFFFFFFFFull) | (1ull << 52)) << 11;
+        negative = bits >> 63;
     }
     __device__ __forceinline__ bool none() const { return e <= -1023 || e >= 64; }   // zero and what is next to it; no angle
 };
 constexpr uint64_t kInv2Pi = 0xA2F9836E4E441529ull, kInv2PiLow = 0xFC2757D1F534DDC0ull;   // 2^130 / (2 pi), upper and lower half
-// `ok` is false for what has no angle: 2^64 and more, infinities, NaN.
-__device__ __forceinline__ uint64_t turn_fraction(double freq, bool &ok) {
+// `ok` is false for what has no angle: 2^64 and more, infinities, NaN; `fast` is set for 2^kSlow and more.
+__device__ __forceinline__ uint64_t turn_fraction(double freq, bool &ok, bool &fast) {
     const FreqBits f(freq);
     ok = f.e < 64;
+    fast |= f.e >= kSlow;
     if (f.none()) return 0ull;
     const uint64_t hi = __umul64hi(f.m, kInv2Pi), lo = f.m * kInv2Pi;   // turns 2^(129 - e)
     const int s = 65 - f.e;
@@ -135,7 +138,7 @@ __device__ __forceinline__ uint64_t turn_fraction(double freq, bool &ok) {
     if (s >= 128) t = 0ull;
     else if (s >= 64) t = hi >> (s - 64);
     else t = (hi << (64 - s)) | (lo >> s);
-    return freq < 0.0 ? 0ull - t : t;
+    return f.negative ? 0ull - t : t;
 }
 // The angle of any position and frequency that has one: the same with fractions in units of 2^-128 and 1 / (2 pi) in 130 bits, off
 // by less than |position| (2^-128 + |freq| 2^-130) turns, 2^-27 for frequencies below 2^40 and every position.  It costs the
@@ -149,7 +152,7 @@ __device__ __forceinline__ uint64_t far_angle(double freq, long long pos) {
     const uint64_t x0 = w == 0 ? p0 : w == 1 ? p1 : w == 2 ? p2 : 0ull, x1 = w == 0 ? p1 : w == 1 ? p2 : 0ull, x2 = w == 0 ? p2 : 0ull;
     const uint64_t lo = b ? (x0 >> b) | (x1 << (64 - b)) : x0, hi = b ? (x1 >> b) | (x2 << (64 - b)) : x1;
     const uint64_t n = pos < 0 ? 0ull - (uint64_t)pos : (uint64_t)pos, at = hi * n + __umul64hi(lo, n);
-    return (pos < 0) != (freq < 0.0) ? 0ull - at : at;
+    return (pos < 0) != f.negative ? 0ull - at : at;
 }
 __device__ __forceinline__ void sine_of(uint64_t angle, bool ok, float &cs, float &sn) {
     sincospif(__ll2float_rn((long long)angle) * 0x1p-63f, &sn, &cs);
@@ -169,7 +172,7 @@ template <int VEC, int CP, bool ADJ> struct Place {
     uint64_t turn[CP][VEC];    // of the pairs of both chunks
     unsigned rot[CP];          // which of them are rotated (ADJ = false: all or none)
     unsigned bad[CP];          // and have no angle
-    bool fast;                 // one of its frequencies is kSlow or more
+    bool fast;                 // one of its frequencies is 2^kSlow or more
     float cs[CP][VEC], sn[CP][VEC];
 
     template <int LPR> __device__ __forceinline__ void init(const RotParams &p, int gl) {
@@ -185,27 +188,32 @@ template <int VEC, int CP, bool ADJ> struct Place {
                 bool ok = true;
                 turn[i][t] = 0ull;
                 if (pair(i, t) < p.r) {
-                    const double f = p.freq[pair(i, t)];
                     rot[i] |= 1u << t;
-                    turn[i][t] = turn_fraction(f, ok);
+                    turn[i][t] = turn_fraction(p.freq[pair(i, t)], ok, fast);
                     if (!ok) bad[i] |= 1u << t;
-                    fast |= !(f < kSlow && f > -kSlow);
                 }
             }
         }
     }
     __device__ __forceinline__ int pair(int i, int t) const { return ADJ ? a[i] / 2 + t : a[i] + t; }   // ADJ: VEC/2 of each chunk, in order
     __device__ __forceinline__ void at(const RotParams &p, long long pos) {
-        const bool far = fast || pos >= kNear || pos <= -kNear;
+        uint64_t angle[CP][VEC];
+#pragma unroll
+        for (int i = 0; i < CP; ++i)
+#pragma unroll
+            for (int t = 0; t < VEC; ++t) angle[i][t] = turn[i][t] * (uint64_t)pos;
+        if (fast || pos >= kNear || pos <= -kNear) {
+#pragma unroll
+            for (int i = 0; i < CP; ++i)
+#pragma unroll
+                for (int t = 0; t < VEC; ++t)
+                    if (rot[i] >> t & 1) angle[i][t] = far_angle(p.freq[pair(i, t)], pos);
+        }
 #pragma unroll
         for (int i = 0; i < CP; ++i)
             if (ADJ || rot[i])
 #pragma unroll
-                for (int t = 0; t < VEC; ++t) {
-                    uint64_t angle = turn[i][t] * (uint64_t)pos;
-                    if (far && (rot[i] >> t & 1)) angle = far_angle(p.freq[pair(i, t)], pos);
-                    sine_of(angle, !(bad[i] >> t & 1), cs[i][t], sn[i][t]);
-                }
+                for (int t = 0; t < VEC; ++t) sine_of(angle[i][t], !(bad[i] >> t & 1), cs[i][t], sn[i][t]);
     }
     // Turns the pairs of chunk pair i, backwards with sign = -1.
     __device__ __forceinline__ void rotate(int i, float (&x)[VEC], float (&y)[VEC], float sign) const {
