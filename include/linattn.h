@@ -584,8 +584,8 @@ LA_API la_status la_layer_norm_backward(const void *dy, const void *x, const flo
  *   positions  int64, of batch row b and token t at positions[b positions_stride + t]; NULL: t.
  * 2 <= d <= 256, even (else LA_ERR_UNSUPPORTED); 0 <= 2 rotated <= d; B, Hq, Hk >= 1,
  * Hq + Hk < 65536; N >= 0; B*N < 2^31; eps finite and > 0 (not read without a norm).  Pointers to q,
- * k and the outputs aligned to their element size (16 bytes, and strides and sizes to match, are
- * faster), weights to 4, freq and positions to 8 bytes.  q_out may be q and k_out may be k, with the
+ * k and the outputs aligned to their element size (four values, 8 bytes of bf16 and 16 of float32, with
+ * strides and sizes to match, are faster), weights to 4, freq and positions to 8 bytes.  q_out may be q and k_out may be k, with the
  * same strides; no other output may overlap an input or output (rows may lie among rows of the same
  * strides, of other strides not).  The sums are float32.
  * A single token of each sequence: N = 1.

@@ -30,7 +30,7 @@
 // Precision: the state is float32 in registers, and what is added to it is exact but for the accumulator's float32: W is
 // rounded to float32 once and enters as three bf16 pieces that add up to it (the top, middle and low 8 bits), against
 // bf16 K, small pieces first.  What only y depends on, each score and each value of the state that it meets, enters as two
-// pieces: 2^-15 of each at most is lost, as much as float32 sums of that length lose.  With one piece, 2^-8 of each, y was
+// pieces: 2^-15 of each at most is lost, no more than the bound of the float32 sums.  With one piece, 2^-8 of each, y was
 // off by sqrt(2) times its own rounding where the terms are of random signs, but by a tenth of itself where they cancel
 // (states with a common part of 64 times the rest that the queries do not see); the second pieces took the calls above
 // from 190 to 220 and from 560 to 615 us.  y is rounded to bf16.
@@ -675,10 +675,12 @@ retain_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
     }
 }
 
-// Segments of a head.  Splitting pays where the heads leave SMs idle: the segments' own sums come first (a block of
-// them costs about 0.6 of a whole one), their ends are joined, and every segment runs from its state.  In units of a
-// block's time, about 2.2 us: a wave of CTAs takes its segments' length, the extra launches and starts about 3 (before the
-// launches overlapped: gradients of 24 heads of 9 blocks 79 us split in three, 83 whole; 8 heads of 8 blocks forward 29 and 33).
+// Segments of a head.  Splitting pays where the heads leave SMs idle: the segments' own sums come first, their ends are
+// joined, and every segment runs from its state.  In units of a block's time, 1.8 us (d64) to 3.2 (d128): a wave of CTAs takes its
+// segments' length, once for y and about 0.6 times for the sums (measured as 0.42 at d64: B1 H32 N131072, 216 blocks in a row,
+// sums 165 us, y 394; the rule leaves that margin), the extra launches and starts about 3 (with one piece of scores and states and
+// before the launches overlapped: gradients of 24 heads of 9 blocks 79 us split in three, 83 whole; 8 heads of 8 blocks forward
+// 29 and 33).
 void retain_segments(const RetainArgs &a, int &nseg, int &seg_blocks) {
     const int nblk = (a.N + kTC - 1) / kTC, sms = num_sms();
     const long long BH = (long long)a.B * a.H;
